@@ -28,7 +28,11 @@
  *   - The library owns a per-device workspace (split-KV partials, reduction
  *     partials, completion tickets, an error word), grown on demand with
  *     cudaMalloc on the first call that needs more (so a call that grows it
- *     synchronises the device) and kept until spec_release() or exit.
+ *     synchronises the device) and kept until spec_release() or exit.  A
+ *     buffer that was outgrown stays as well, so that graphs captured before
+ *     the growth replay soundly; a call that would grow it while its stream
+ *     is being captured returns SPEC_ERR_UNSUPPORTED (make one such call
+ *     first).  Replays of captured graphs share it like the calls do.
  *     Calls that overlap on the GPU (different streams without ordering)
  *     share it and race: order them on one stream, or serialise them.
  *   - Device-side input faults (a block_table entry outside [0, num_pages),
@@ -57,7 +61,9 @@ enum {
     SPEC_DTYPE_BF16 = 1,
     SPEC_DTYPE_F16 = 2, /* scales only */
     SPEC_DTYPE_I8 = 3,
-    SPEC_DTYPE_I32 = 4  /* tables, lengths and token ids (descriptor form) */
+    SPEC_DTYPE_I32 = 4, /* tables, lengths and token ids (descriptor form) */
+    SPEC_DTYPE_E4M3 = 5 /* 8-bit floating codes of a cache, one fp32 scale per
+                         * (page, kv-head) */
 };
 
 /* A tensor described by itself (the descriptor form of the two hot-path
@@ -133,10 +139,12 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  *   q            [batch, num_draft, num_q_heads, head_dim]   q_dtype (F32|BF16)
  *   k_cache,
  *   v_cache      [num_pages, num_kv_heads, page_size, head_dim]  kv_dtype
- *                (F32 | BF16 | I8).  With I8 the element is c * s.
+ *                (F32 | BF16 | I8 | E4M3).  With I8 and E4M3 the element
+ *                is c * s.
  *   k_scale,
- *   v_scale      [num_pages, num_kv_heads, page_size] fp16; required with
- *                I8, ignored (may be NULL) otherwise
+ *   v_scale      I8: [num_pages, num_kv_heads, page_size] fp16; E4M3:
+ *                [num_pages, num_kv_heads] fp32, finite and >= 0, 4-byte
+ *                aligned; ignored (may be NULL) otherwise
  *   block_table  [batch, max_pages_per_seq] int32 physical page ids
  *   ctx_lens     [batch] int32 cached context per sequence, EXCLUDING the
  *                drafts; ctx_b + num_draft <= max_pages_per_seq * page_size
@@ -197,7 +205,7 @@ SPEC_API int spec_accept_greedy(const void *logits, int32_t logits_dtype, const 
  *   (F32 | BF16 | I8, same type), k_scale / v_scale [NP, Hkv, P] F16 (I8
  *   cache only, else ignored), block_table [B, max_pages] I32, ctx_lens [B]
  *   I32, out [B, num_draft, Hq, D] in q's type, lse [B, num_draft, Hq] F32
- *   or NULL;
+ *   or NULL; an E4M3 cache with k_scale / v_scale [NP, Hkv] F32;
  *   logits [B, num_draft + 1, V] (F32 | BF16), draft_tokens [B, num_draft]
  *   I32, accepted_len / next_token [B] I32.
  * Errors: SPEC_ERR_INVALID for a null descriptor, a wrong rank, element
@@ -236,6 +244,30 @@ SPEC_API int spec_verify_attn_tree(const void *q, const void *k_cache, const voi
                                    int32_t page_size, int32_t num_pages,
                                    int32_t max_pages_per_seq, int32_t q_dtype, int32_t kv_dtype,
                                    float scale, void *out, float *lse, void *stream);
+
+/*
+ * Verification attention with a sliding window and attention sinks.  Same
+ * arguments and results as spec_verify_attn (tree_mask NULL) or
+ * spec_verify_attn_tree, except that of the keys these see, query i of
+ * sequence b sees key j only if
+ *   j < num_sinks   or   pos_i - j < window,
+ * where pos_i = ctx_b + i, or with a tree ctx_b + (node i's ancestors: the
+ * set bits of its mask less one), is the query's position.  The query itself
+ * counts, so window 1 leaves a query its own key and the sinks.  Keys that no
+ * query of a sequence sees are not read (whole pages of them may have left
+ * the pool: their block_table entries are not looked at).
+ * Limits: window >= 1 (>= num_draft with a tree), num_sinks >= 0; else as
+ * spec_verify_attn.
+ */
+SPEC_API int spec_verify_attn_window(const void *q, const void *k_cache, const void *v_cache,
+                                     const void *k_scale, const void *v_scale,
+                                     const int32_t *block_table, const int32_t *ctx_lens,
+                                     const uint64_t *tree_mask, int32_t batch, int32_t num_draft,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t page_size, int32_t num_pages,
+                                     int32_t max_pages_per_seq, int32_t q_dtype, int32_t kv_dtype,
+                                     float scale, int32_t window, int32_t num_sinks, void *out,
+                                     float *lse, void *stream);
 
 /*
  * Greedy acceptance over a tree of drafts.  Node i of sequence b carries
@@ -372,7 +404,9 @@ SPEC_API int spec_accept_rejection(const void *target_logits, const void *draft_
  *     (token, kv-head) row: s = fp16(max_d |x_d| / 127) into k_scale /
  *     v_scale [num_pages, num_kv_heads, page_size], c_d = clamp(rint(x_d / s),
  *     -127, 127) (c = 0 when s = 0), every step in fp32 (IEEE division,
- *     round half to even), fp16 by round-to-nearest-even.
+ *     round half to even), fp16 by round-to-nearest-even;
+ *   - E4M3 cache: spec_rope_append without a rotation (k_new, v_new and the
+ *     caches 16-byte aligned).
  * Caches, scales and tables as in spec_verify_attn; ctx_lens is not changed
  * (spec_commit moves it).  A position past the block table or a page id
  * outside [0, num_pages) writes nothing and sets SPEC_DEVERR_CTX /
@@ -384,6 +418,106 @@ SPEC_API int spec_kv_append(const void *k_new, const void *v_new, int32_t src_dt
                             const int32_t *ctx_lens, int32_t batch, int32_t num_new,
                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
                             int32_t num_pages, int32_t max_pages_per_seq, void *stream);
+
+/*
+ * Rotary positions and the append in one launch: rotates the new tokens' q
+ * rows into q_out and writes their rotated k rows and their v rows into the
+ * paged cache (the step between the target's projections and verification).
+ *
+ * Token t of sequence b stands at p = positions[b, t] (NULL: ctx_b + t; a
+ * tree's node at ctx_b + its depth) and its k / v rows go to cache position
+ * ctx_b + t.  Pair j of the first rotary_dim elements of a q or k row, (x, y)
+ * = elements (2j, 2j + 1) (interleaved != 0) or (j, j + rotary_dim / 2), with
+ * a = p * f_j:
+ *   x' = amplitude * (x cos a - y sin a),  y' = amplitude * (x sin a + y cos a)
+ * Elements from rotary_dim on are copied.  rope_table holds f_j as fractions
+ * of a turn, [rotary_dim / 2] uint64 f_j / (2 pi) * 2^64 (spec_rope_table):
+ * the angle is reduced exactly at any position.
+ *
+ *   q          [batch, num_new, num_q_heads, head_dim] src_dtype (F32|BF16);
+ *   k_new,     tokens q_stride / k_stride / v_stride elements apart (the
+ *   v_new      batch stride is num_new of them), so that q, k and v may be
+ *              slices of one projection's output.  num_q_heads may be 0 (q
+ *              and q_out NULL).
+ *   q_out      as q, tokens q_out_stride apart; may be q itself
+ *   new_lens   [batch] int32 tokens of each sequence (clamped to [0,
+ *              num_new]), or NULL: num_new.  Nothing is read or written for
+ *              a token t >= new_lens[b].
+ *   caches, scales, block_table, ctx_lens  as in spec_kv_append
+ *   - F32 / BF16 / I8 cache: as spec_kv_append, of the rotated row (fp32)
+ *   - E4M3 cache: per (page, kv-head), over the page's new rows x,
+ *       s' = max_d,t |x| / 448, and not below the page's scale s when slots
+ *       before the first new one belong to the sequence (ctx_b not at the
+ *       page's start);
+ *       new codes = e4m3(x / s') (0 when s' = 0), and if s' > s the kept
+ *       slots' codes become e4m3((c * s) / s');
+ *     every step in fp32, IEEE division, to nearest even, saturating.  A
+ *     page's scale grows with its rows (rejected drafts' too) and starts
+ *     afresh with its first slot.  A page must belong to one sequence.
+ * A position past the block table, a negative ctx_b or a page id outside
+ * [0, num_pages) writes nothing to the cache and sets SPEC_DEVERR_CTX /
+ * SPEC_DEVERR_PAGE (q_out is still written).  Inputs are finite.
+ * Limits: head_dim % 32 == 0 and <= 256; rotary_dim % 16 == 0 and in [0,
+ * head_dim] (0: no rotation, rope_table ignored); num_new >= 1; tensors, and
+ * token strides in bytes, multiples of 16.
+ */
+SPEC_API int spec_rope_append(const void *q, const void *k_new, const void *v_new, void *q_out,
+                              int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              int64_t q_out_stride, int32_t src_dtype, void *k_cache,
+                              void *v_cache, void *k_scale, void *v_scale, int32_t cache_dtype,
+                              const int32_t *block_table, const int32_t *ctx_lens,
+                              const int32_t *positions, const int32_t *new_lens,
+                              const uint64_t *rope_table, int32_t rotary_dim, int32_t interleaved,
+                              float amplitude, int32_t batch, int32_t num_new,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                              void *stream);
+
+/* How spec_rope_table scales the frequencies for long contexts. */
+enum {
+    SPEC_ROPE_PLAIN = 0,  /* f_j = theta^(-2j / rotary_dim) */
+    SPEC_ROPE_LINEAR = 1, /* f_j / factor (positions interpolated) */
+    SPEC_ROPE_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) */
+    /* by parts: pairs that turn more than fast_turns times over original_len
+     * positions keep f_j, those below slow_turns take f_j / factor, a linear
+     * ramp between; amplitude 0.1 ln(factor) + 1 */
+    SPEC_ROPE_YARN = 3
+};
+
+/*
+ * Fill a HOST table for spec_rope_append (the caller copies it to the
+ * device) and the amplitude that goes with it.  No CUDA call.  factor is
+ * ignored by SPEC_ROPE_PLAIN; original_len, fast_turns (32 as published) and
+ * slow_turns (1) are SPEC_ROPE_YARN's.
+ * Limits: rotary_dim even, 2 .. 256; theta > 1; factor >= 1.
+ */
+SPEC_API int spec_rope_table(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                             double original_len, double fast_turns, double slow_turns,
+                             uint64_t *table, float *amplitude);
+
+/*
+ * Read the paged cache back: rows of positions start_b .. start_b + len_b -
+ * 1 of each sequence as dense tensors, dequantised (code * scale in fp32) and
+ * rounded once when out_dtype is BF16.  For consumers that want the rows
+ * themselves: a drafter sharing a prefix, a cache moved to another pool or
+ * page size.
+ *
+ *   starts, lens  [batch] int32 (starts NULL: 0; lens clamped to [0, max_len])
+ *   k_out, v_out  [batch, max_len, num_kv_heads, head_dim] out_dtype (F32 |
+ *                 BF16); row t of sequence b is position start_b + t; rows
+ *                 t >= lens[b] are left as they were
+ *   caches, scales, block_table  as in spec_verify_attn
+ * A position outside the block table or a page id outside [0, num_pages)
+ * leaves its row as it was and sets SPEC_DEVERR_CTX / SPEC_DEVERR_PAGE.
+ * Limits: head_dim % 32 == 0 and <= 256; batch <= 65535; max_len *
+ * num_kv_heads * head_dim < 2^35; caches and outputs 16-byte aligned.
+ */
+SPEC_API int spec_kv_gather(const void *k_cache, const void *v_cache, const void *k_scale,
+                            const void *v_scale, int32_t cache_dtype, const int32_t *block_table,
+                            const int32_t *starts, const int32_t *lens, int32_t batch,
+                            int32_t max_len, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                            int32_t out_dtype, void *k_out, void *v_out, void *stream);
 
 /*
  * Commit a verification step on the device: ctx_lens[b] += accepted_len[b]

@@ -18,6 +18,7 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libspecverify.so")
 
 SPEC_DTYPE_F32, SPEC_DTYPE_BF16, SPEC_DTYPE_F16, SPEC_DTYPE_I8, SPEC_DTYPE_I32 = 0, 1, 2, 3, 4
+SPEC_DTYPE_E4M3 = 5
 SPEC_OK, SPEC_ERR_INVALID, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA = 0, -1, -2, -3
 SPEC_OPT_ATTN_PATH, SPEC_OPT_NUM_CTAS, SPEC_OPT_VALIDATE, SPEC_OPT_SIMT_CHUNK = 0, 1, 2, 3
 SPEC_OPT_SPLIT_WEIGHT = 4
@@ -26,18 +27,20 @@ NUM_OPTIONS = 6
 SPEC_DEVERR_PAGE, SPEC_DEVERR_CTX, SPEC_DEVERR_TIMEOUT, SPEC_DEVERR_TOKEN = 1, 2, 4, 8
 SPEC_DEVERR_TREE = 16
 SPEC_DEVERR_CODEC = 32
+SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_NTK, SPEC_ROPE_YARN = 0, 1, 2, 3
 
 # every symbol the public header declares
 EXPORTED = ["spec_version", "spec_last_error", "spec_set_option", "spec_verify_attn",
             "spec_accept_greedy", "spec_verify_attn_tensors", "spec_accept_greedy_tensors",
             "spec_accept_greedy_noalloc", "spec_accept_rejection",
             "spec_kv_append", "spec_commit", "spec_verify_attn_tree", "spec_accept_tree",
+            "spec_verify_attn_window", "spec_rope_append", "spec_rope_table", "spec_kv_gather",
             "spec_codec_encode", "spec_codec_decode", "spec_device_error", "spec_release"]
 SPEC_NOALLOC_MAX_PARTIALS, SPEC_NOALLOC_MAX_BATCH = 65536, 4096
 
 _TORCH_DT = {torch.float32: SPEC_DTYPE_F32, torch.bfloat16: SPEC_DTYPE_BF16,
              torch.float16: SPEC_DTYPE_F16, torch.int8: SPEC_DTYPE_I8,
-             torch.int32: SPEC_DTYPE_I32}
+             torch.int32: SPEC_DTYPE_I32, torch.float8_e4m3fn: SPEC_DTYPE_E4M3}
 
 
 class SpecTensor(ctypes.Structure):
@@ -109,6 +112,17 @@ def _open(path: str):
     lib.spec_verify_attn_tree.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
                                           i32, i32, i32, ctypes.c_float, P, P, P]
     lib.spec_verify_attn_tree.restype = ctypes.c_int
+    lib.spec_verify_attn_window.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
+                                            i32, i32, i32, i32, ctypes.c_float, i32, i32, P, P, P]
+    lib.spec_verify_attn_window.restype = ctypes.c_int
+    lib.spec_rope_append.argtypes = ([P] * 4 + [i64] * 4 + [i32] + [P] * 4 + [i32] + [P] * 5 +
+                                     [i32, i32, ctypes.c_float] + [i32] * 8 + [P])
+    lib.spec_rope_append.restype = ctypes.c_int
+    f64 = ctypes.c_double
+    lib.spec_rope_table.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, P]
+    lib.spec_rope_table.restype = ctypes.c_int
+    lib.spec_kv_gather.argtypes = [P, P, P, P, i32, P, P, P] + [i32] * 8 + [P, P, P]
+    lib.spec_kv_gather.restype = ctypes.c_int
     lib.spec_accept_tree.argtypes = [P, i32, P, P, i32, i32, i64, P, P, P, P]
     lib.spec_accept_tree.restype = ctypes.c_int
     T = ctypes.POINTER(SpecTensor)
@@ -153,14 +167,37 @@ def spec_set_option(option: int, value: int) -> None:
     _check(load().spec_set_option(option, int(value)))
 
 
+def _check_page_scales(k_cache, v_cache, k_scale, v_scale) -> None:
+    """The scales of a float8_e4m3fn cache: float32 [num_pages, Hkv] each (the
+    library takes a bare pointer and cannot tell)."""
+    if k_cache.dtype != torch.float8_e4m3fn:
+        return
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must share a dtype")
+    for s in (k_scale, v_scale):
+        if s is not None and (s.dtype != torch.float32
+                              or tuple(s.shape) != tuple(k_cache.shape[:2])):
+            raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor lies on the current device (kernels launch there)."""
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != cur):
+            raise ValueError("tensors must lie on the current CUDA device")
+
+
 def spec_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int, scale: float,
                      out, lse=None, k_scale=None, v_scale=None, stream=None) -> None:
     """Verification attention; writes ``out`` (and ``lse`` if given).
 
     q [B, k, Hq, D]; k_cache / v_cache [NP, Hkv, P, D]; block_table
     [B, max_pages] int32; ctx_lens [B] int32; out like q; lse [B, k, Hq] f32;
-    k_scale / v_scale [NP, Hkv, P] fp16 for an int8 cache.
+    k_scale / v_scale [NP, Hkv, P] fp16 for an int8 cache, [NP, Hkv] float32
+    for a float8_e4m3fn cache.
     """
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
     B, k, Hq, D = q.shape
     NP, Hkv, P, D2 = k_cache.shape
     if k != num_draft or D2 != D:
@@ -208,11 +245,42 @@ def spec_verify_attn_tree(q, k_cache, v_cache, block_table, ctx_lens, tree_mask,
         raise ValueError("q must be [B, num_draft, Hq, D], tree_mask [B, num_draft]")
     if tree_mask.element_size() != 8:
         raise ValueError("tree_mask must hold 64-bit words")
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
     _check(load().spec_verify_attn_tree(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
         _ptr(ctx_lens), _ptr(tree_mask), B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), _ptr(out), _ptr(lse),
         _stream(stream)))
+
+
+def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
+                            scale: float, window: int, num_sinks: int, out, lse=None,
+                            k_scale=None, v_scale=None, tree_mask=None, stream=None) -> None:
+    """spec_verify_attn (or, with ``tree_mask``, spec_verify_attn_tree) with a
+    sliding window: a query sees the first ``num_sinks`` keys and those less
+    than ``window`` positions before it (its own counts)."""
+    B, k, Hq, D = q.shape
+    NP, Hkv, P, D2 = k_cache.shape
+    if k != num_draft or D2 != D or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("shape mismatch between q, num_draft and the caches")
+    if v_cache.dtype != k_cache.dtype or out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("v_cache must have k_cache's dtype, out q's dtype and shape")
+    if block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32:
+        raise ValueError("block_table and ctx_lens must be int32")
+    if block_table.shape[0] != B or ctx_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and ctx_lens [B]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, k, Hq)):
+        raise ValueError("lse must be float32 [B, k, Hq]")
+    if tree_mask is not None and (tuple(tree_mask.shape) != (B, k)
+                                  or tree_mask.element_size() != 8):
+        raise ValueError("tree_mask must hold 64-bit words [B, num_draft]")
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _same_device(q, k_cache, v_cache, block_table, ctx_lens, tree_mask, out, lse, k_scale, v_scale)
+    _check(load().spec_verify_attn_window(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+        _ptr(ctx_lens), _ptr(tree_mask), B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
+        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), int(window), int(num_sinks),
+        _ptr(out), _ptr(lse), _stream(stream)))
 
 
 def spec_accept_tree(logits, draft_tokens, parents, num_draft: int, accepted_len, next_token,
@@ -285,10 +353,123 @@ def spec_kv_append(k_new, v_new, k_cache, v_cache, block_table, ctx_lens, k_scal
     NP, Hkv2, P, D2 = k_cache.shape
     if (Hkv2, D2) != (Hkv, D) or tuple(v_new.shape) != tuple(k_new.shape):
         raise ValueError("k_new / v_new must be [B, n, Hkv, D] matching the cache")
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
     _check(load().spec_kv_append(_ptr(k_new), _ptr(v_new), _TORCH_DT[k_new.dtype], _ptr(k_cache),
                                  _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
                                  _TORCH_DT[k_cache.dtype], _ptr(block_table), _ptr(ctx_lens), B,
                                  n, Hkv, D, P, NP, block_table.shape[1], _stream(stream)))
+
+
+_ROPE_SCALING = {"none": SPEC_ROPE_PLAIN, "linear": SPEC_ROPE_LINEAR, "ntk": SPEC_ROPE_NTK,
+                 "yarn": SPEC_ROPE_YARN}
+
+
+def spec_rope_table(rotary_dim: int, theta: float = 10000.0, scaling: str = "none",
+                    factor: float = 1.0, original_len: float = 0.0, fast_turns: float = 32.0,
+                    slow_turns: float = 1.0, device="cuda"):
+    """The frequency table of spec_rope_append (int64 [rotary_dim / 2] on
+    ``device``, the bits of uint64 fractions of a turn) and its amplitude.
+
+    ``scaling``: "none", "linear", "ntk" or "yarn" (with ``original_len``).
+    """
+    if scaling not in _ROPE_SCALING:
+        raise ValueError("scaling must be one of %s" % ", ".join(sorted(_ROPE_SCALING)))
+    table = np.zeros(max(1, int(rotary_dim) // 2), np.uint64)
+    amplitude = ctypes.c_float(0.0)
+    _check(load().spec_rope_table(int(rotary_dim), float(theta), _ROPE_SCALING[scaling],
+                                  float(factor), float(original_len), float(fast_turns),
+                                  float(slow_turns), table.ctypes.data_as(ctypes.c_void_p),
+                                  ctypes.byref(amplitude)))
+    return torch.from_numpy(table.view(np.int64)).to(device), amplitude.value
+
+
+def _token_rows(t, name: str):
+    """Pointer and token stride (elements) of [B, n, H, D] whose rows are dense
+    and whose tokens are evenly spaced (a slice of a wider projection is)."""
+    B, n, H, D = t.shape
+    sb, sn, sh, sd = t.stride()
+    if n == 1:
+        sn = sb if B > 1 else max(sn, H * D)
+    if (sd != 1 or (H > 1 and sh != D) or (B > 1 and n > 1 and sb != n * sn)):
+        raise ValueError("%s: heads must be dense and tokens evenly spaced" % name)
+    return ctypes.c_void_p(t.data_ptr()), sn
+
+
+def spec_rope_append(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_lens, rope_table,
+                     interleaved: bool = False, amplitude: float = 1.0, positions=None,
+                     new_lens=None, k_scale=None, v_scale=None, stream=None) -> None:
+    """Rotate q [B, n, Hq, D] into ``q_out`` and append the rotated k_new and
+    v_new [B, n, Hkv, D] at positions ctx_b .. of the paged caches.
+
+    ``rope_table`` (spec_rope_table) rotates the first 2 * len(table) elements
+    of a head; None rotates nothing.  q, k_new, v_new and q_out may be slices
+    of wider rows; q_out may be q; q and q_out may be None.  ``positions``
+    [B, n] int32 replaces ctx_b + t in the angles; ``new_lens`` [B] int32
+    limits each sequence's tokens.  An e4m3 cache takes float32 scales
+    [num_pages, Hkv], an int8 cache fp16 [num_pages, Hkv, P].
+    """
+    B, n, Hkv, D = k_new.shape
+    NP, Hkv2, P, D2 = k_cache.shape
+    if (Hkv2, D2) != (Hkv, D) or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("k_new / v_new must be [B, n, Hkv, D] matching the caches")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    Hq = 0
+    if q is not None:
+        Hq = q.shape[2]
+        if tuple(q.shape) != (B, n, Hq, D) or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [B, n, Hq, D]")
+        if q.dtype != k_new.dtype or q_out.dtype != q.dtype:
+            raise ValueError("q, q_out, k_new and v_new must share a dtype")
+    if v_new.dtype != k_new.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k and v must share a dtype")
+    if (block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32
+            or block_table.shape[0] != B or ctx_lens.shape != (B,)):
+        raise ValueError("block_table must be int32 [B, max_pages] and ctx_lens int32 [B]")
+    if positions is not None and (positions.dtype != torch.int32
+                                  or tuple(positions.shape) != (B, n)):
+        raise ValueError("positions must be int32 [B, n]")
+    if new_lens is not None and (new_lens.dtype != torch.int32 or new_lens.shape != (B,)):
+        raise ValueError("new_lens must be int32 [B]")
+    if rope_table is not None and (rope_table.element_size() != 8 or rope_table.dim() != 1):
+        raise ValueError("rope_table must be a row of 64-bit words")
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _same_device(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_lens, rope_table,
+                 positions, new_lens, k_scale, v_scale)
+    qp, qs = _token_rows(q, "q") if q is not None else (None, 0)
+    op, os_ = _token_rows(q_out, "q_out") if q is not None else (None, 0)
+    kp, ks = _token_rows(k_new, "k_new")
+    vp, vs = _token_rows(v_new, "v_new")
+    rot = 0 if rope_table is None else 2 * rope_table.shape[0]
+    _check(load().spec_rope_append(
+        qp, kp, vp, op, qs, ks, vs, os_, _TORCH_DT[k_new.dtype], _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), _TORCH_DT[k_cache.dtype], _ptr(block_table), _ptr(ctx_lens),
+        _ptr(positions), _ptr(new_lens), _ptr(rope_table), rot, int(bool(interleaved)),
+        float(amplitude), B, n, Hq, Hkv, D, P, NP, block_table.shape[1], _stream(stream)))
+
+
+def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=None, k_scale=None,
+                   v_scale=None, stream=None) -> None:
+    """Rows of positions starts_b .. starts_b + lens_b - 1 of the paged caches
+    into k_out / v_out [B, max_len, Hkv, D] (float32 or bfloat16); rows from
+    lens_b on are left as they were."""
+    B, n, Hkv, D = k_out.shape
+    NP, Hkv2, P, D2 = k_cache.shape
+    if (Hkv2, D2) != (Hkv, D) or v_out.shape != k_out.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("k_out / v_out must be [B, max_len, Hkv, D] matching the caches")
+    if v_out.dtype != k_out.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k and v must share a dtype")
+    if (block_table.dtype != torch.int32 or lens.dtype != torch.int32
+            or block_table.shape[0] != B or lens.shape != (B,)):
+        raise ValueError("block_table must be int32 [B, max_pages] and lens int32 [B]")
+    if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,)):
+        raise ValueError("starts must be int32 [B]")
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _same_device(k_cache, v_cache, block_table, lens, k_out, v_out, starts, k_scale, v_scale)
+    _check(load().spec_kv_gather(
+        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _TORCH_DT[k_cache.dtype],
+        _ptr(block_table), _ptr(starts), _ptr(lens), B, n, Hkv, D, P, NP, block_table.shape[1],
+        _TORCH_DT[k_out.dtype], _ptr(k_out), _ptr(v_out), _stream(stream)))
 
 
 def spec_codec_encode(codes, pairs, num_pairs, stream=None) -> None:

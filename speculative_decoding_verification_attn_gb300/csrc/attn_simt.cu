@@ -10,8 +10,12 @@
 // kv-head, query-row group, key chunk).  All k*G query rows of a kv-head
 // share every K/V row the CTA stages in shared memory, so the cache is read
 // once per (sequence, kv-head).  Chunks produce (O/l, lse) partials that the
-// combine kernel merges with log-sum-exp weights (split-KV).
+// combine kernel merges with log-sum-exp weights (split-KV).  With a sliding
+// window the chunks run over the keys that some query sees: the sinks, then
+// the keys from the first query's window on.
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -24,7 +28,8 @@ constexpr int kRowElems = 2048;        // query rows x head_dim per CTA
 constexpr int kMaxPerThread = kRowElems / kThreads;
 
 struct SeqGeom {
-    int ctx, L;  // cached context (clamped) and total keys
+    int ctx, L;       // cached context (clamped) and keys some query may see
+    WindowSpan span;  // key x of those L is cache position x, + span.skip from span.head on
 };
 
 __device__ __forceinline__ SeqGeom seq_geom(const AttnArgs& a, int b) {
@@ -34,7 +39,8 @@ __device__ __forceinline__ SeqGeom seq_geom(const AttnArgs& a, int b) {
         raise_device_error(a.dev_err, SPEC_DEVERR_CTX);
         ctx = ctx < 0 ? 0 : (int)(cap < 0 ? 0 : cap);
     }
-    return {ctx, ctx + a.k};
+    const WindowSpan w = window_span(a, ctx, 1);
+    return {ctx, ctx + a.k - w.skip, w};
 }
 
 __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int b, int kvh, int j) {
@@ -47,10 +53,12 @@ __device__ __forceinline__ int64_t cache_row(const AttnArgs& a, int b, int kvh, 
 }
 
 template <typename TKV>
-__device__ __forceinline__ float load_kv(const AttnArgs& a, const void* cache, const uint16_t* sc,
+__device__ __forceinline__ float load_kv(const AttnArgs& a, const void* cache, const void* sc,
                                          int64_t row, int d) {
     float x = Elem<TKV>::to_f32(static_cast<const TKV*>(cache)[row * a.D + d]);
-    if constexpr (sizeof(TKV) == 1) x *= __half2float(__ushort_as_half(sc[row]));
+    if constexpr (std::is_same<TKV, int8_t>::value) x *= __half2float(__ushort_as_half(static_cast<const uint16_t*>(sc)[row]));
+    if constexpr (std::is_same<TKV, __nv_fp8_e4m3>::value)
+        x *= static_cast<const float*>(sc)[row / a.P];
     return x;
 }
 
@@ -100,21 +108,34 @@ attn_simt_kernel(AttnArgs a, SimtPlan p, float* __restrict__ part_o, float* __re
             const int jj = e / D, d = e % D, j = jt + jj;
             float kx = 0.f, vx = 0.f;
             if (j < j1) {
-                const int64_t row = cache_row(a, b, kvh, j);
-                kx = load_kv<TKV>(a, a.k_cache, a.k_scale, row, d);
-                vx = load_kv<TKV>(a, a.v_cache, a.v_scale, row, d);
+                const int64_t row =
+                    cache_row(a, b, kvh, j < sg.span.head ? j : j + sg.span.skip);
+                constexpr bool paged = std::is_same<TKV, __nv_fp8_e4m3>::value;
+                const void* ksc = paged ? (const void*)a.k_page_scale : a.k_scale;
+                const void* vsc = paged ? (const void*)a.v_page_scale : a.v_scale;
+                kx = load_kv<TKV>(a, a.k_cache, ksc, row, d);
+                vx = load_kv<TKV>(a, a.v_cache, vsc, row, d);
             }
             Ks[jj * (D + 1) + d] = kx;
             Vs[jj * D + d] = vx;
         }
         __syncthreads();
         for (int e = tid; e < nr * kKeyTile; e += kThreads) {
-            const int r = e / kKeyTile, jj = e % kKeyTile, j = jt + jj;
+            const int r = e / kKeyTile, jj = e % kKeyTile;
+            const int j = jt + jj < sg.span.head ? jt + jj : jt + jj + sg.span.skip;
             const int i = (r0 + r) / G;
             float s = -INFINITY;
-            // query i sees the context and the drafts of its row's bits
-            // (causal chain: keys <= ctx + i)
-            if (j < j1 && (j < sg.ctx || ((draft_bits(a, b, i) >> (j - sg.ctx)) & 1ull))) {
+            // query i sees the context (with a window: its sinks and the keys
+            // near the query) and the drafts of its row's bits (causal chain:
+            // keys <= ctx + i)
+            bool vis = jt + jj < j1;
+            if (vis) {
+                const uint64_t bits = draft_bits(a, b, i);
+                vis = j < sg.ctx
+                          ? j < a.sinks || j >= window_low(a, sg.ctx + draft_depth(bits))
+                          : (window_bits(a, bits, i, sg.ctx) >> (j - sg.ctx)) & 1ull;
+            }
+            if (vis) {
                 float dot = 0.f;
                 for (int d = 0; d < D; ++d) dot = fmaf(Qs[r * D + d], Ks[jj * (D + 1) + d], dot);
                 s = dot * a.scale;
@@ -194,9 +215,10 @@ combine_simt_kernel(AttnArgs a, SimtPlan p, const float* __restrict__ part_o,
     for (int c = lane; c < n; c += 32) m = fmaxf(m, part_lse[base + (int64_t)c * R]);
     m = warp_max(m);
     float tot = 0.f;
-    for (int c = lane; c < n; c += 32) tot += expf(part_lse[base + (int64_t)c * R] - m);
+    if (m != -INFINITY)  // else a row that sees no key: out 0, lse -inf
+        for (int c = lane; c < n; c += 32) tot += expf(part_lse[base + (int64_t)c * R] - m);
     tot = warp_sum(tot);
-    const float lse_tot = m + logf(tot);
+    const float lse_tot = m == -INFINITY ? m : m + logf(tot);
     const int i = row / G, h = kvh * G + row % G;
     const int64_t orow = ((int64_t)b * a.k + i) * a.Hq + h;
     TQ* out = static_cast<TQ*>(a.out);
@@ -204,7 +226,7 @@ combine_simt_kernel(AttnArgs a, SimtPlan p, const float* __restrict__ part_o,
         float acc = 0.f;
         for (int c = 0; c < n; ++c) {
             const int64_t pi = base + (int64_t)c * R;
-            const float w = expf(part_lse[pi] - lse_tot);
+            const float w = lse_tot == -INFINITY ? 0.f : expf(part_lse[pi] - lse_tot);
             acc = fmaf(w, part_o[pi * D + d], acc);
         }
         out[orow * D + d] = Elem<TQ>::from_f32(acc);
@@ -243,7 +265,10 @@ SimtPlan simt_plan(const AttnArgs& a, int num_sms, int forced_chunk) {
     p.rows_per_group = kRowElems / a.D;
     if (p.rows_per_group > R) p.rows_per_group = R;
     p.row_groups = (R + p.rows_per_group - 1) / p.rows_per_group;
-    const int64_t max_L = (int64_t)a.max_pages * a.P;
+    // the keys a sequence can hold, or those that its queries' windows reach
+    int64_t max_L = (int64_t)a.max_pages * a.P;
+    if (a.window > 0 && (int64_t)a.sinks + a.window + a.k < max_L)
+        max_L = (int64_t)a.sinks + a.window + a.k;
     int64_t chunk;
     if (forced_chunk > 0) {
         chunk = forced_chunk;
@@ -287,6 +312,9 @@ cudaError_t launch_attn_simt(const AttnArgs& a, const SimtPlan& p, void* workspa
     case SPEC_DTYPE_I8:
         return q32 ? launch_typed<float, int8_t>(a, p, part_o, part_lse, stream)
                    : launch_typed<__nv_bfloat16, int8_t>(a, p, part_o, part_lse, stream);
+    case SPEC_DTYPE_E4M3:
+        return q32 ? launch_typed<float, __nv_fp8_e4m3>(a, p, part_o, part_lse, stream)
+                   : launch_typed<__nv_bfloat16, __nv_fp8_e4m3>(a, p, part_o, part_lse, stream);
     default:
         return cudaErrorInvalidValue;
     }

@@ -408,7 +408,7 @@ cudaError_t launch_sized(const AttnArgs& a, int Lcap, int csize, bool forced,
 int small_attn_max_keys(const AttnArgs& a) {
     const int R = a.k * (a.Hq / a.Hkv), RG = small_rows_per_group(R);
     const int64_t Lcap = (int64_t)a.max_pages * a.P;
-    if (Lcap < 1 || Lcap > 4096) return 0;
+    if (a.kv_dtype == SPEC_DTYPE_E4M3 || Lcap < 1 || Lcap > 4096) return 0;
     if ((int64_t)a.B * a.Hkv * ((R + RG - 1) / RG) * kMaxSmallCluster >= (1LL << 31)) return 0;
     if (small_smem_bytes((int)Lcap, a.D, RG, a.max_pages) > kSmallAttnSmem) return 0;
     return (int)Lcap;

@@ -5,6 +5,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -25,6 +26,9 @@ template <> struct Elem<__nv_bfloat16> {
 };
 template <> struct Elem<int8_t> {
     static __device__ __forceinline__ float to_f32(int8_t x) { return (float)x; }
+};
+template <> struct Elem<__nv_fp8_e4m3> {
+    static __device__ __forceinline__ float to_f32(__nv_fp8_e4m3 x) { return (float)x; }
 };
 
 // Device error word (one per device, in the library workspace).

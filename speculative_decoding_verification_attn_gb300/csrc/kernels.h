@@ -31,6 +31,13 @@ struct AttnArgs {
     // tensor-core kernels: tiles charged per segment when the tile list is
     // split over the persistent CTAs (TileSplit); < 0 = the kernel's default
     int32_t split_alpha = -1;
+    // sliding window (0 = none): a key before the drafts is visible to query i
+    // when it is one of the first `sinks` or lies less than `window` positions
+    // before the query (see row_low)
+    int32_t window = 0, sinks = 0;
+    // e4m3 cache: fp32 scales per (page, kv-head), [num_pages, Hkv]
+    const float* k_page_scale = nullptr;
+    const float* v_page_scale = nullptr;
 };
 
 // Draft bits visible to query i of sequence b: the tree row, or the causal chain.
@@ -41,6 +48,45 @@ __host__ __device__ inline uint64_t draft_bits(const AttnArgs& a, int b, int i) 
     if (a.tree_mask) return a.tree_mask[(int64_t)b * a.k + i];
 #endif
     return i >= 63 ? ~0ull : ((1ull << (i + 1)) - 1);
+}
+
+// Ancestors of a query among the drafts: its position is ctx + depth.
+__host__ __device__ inline int draft_depth(uint64_t bits) {
+#ifdef __CUDA_ARCH__
+    const int n = __popcll(bits);
+#else
+    const int n = __builtin_popcountll(bits);
+#endif
+    return n > 0 ? n - 1 : 0;
+}
+
+// First key that the window of a query at position pos reaches (0 without a window).
+__host__ __device__ inline int window_low(const AttnArgs& a, int pos) {
+    return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
+// Draft bits of query i at context ctx with the window applied to a chain (a
+// tree's window covers all its nodes: the entry point refuses a narrower one).
+__host__ __device__ inline uint64_t window_bits(const AttnArgs& a, uint64_t bits, int i, int ctx) {
+    if (a.window <= 0 || a.tree_mask || i < a.window) return bits;
+    uint64_t near = ~0ull << (i - a.window + 1);
+    if (a.sinks > ctx) near |= a.sinks - ctx >= 64 ? ~0ull : (1ull << (a.sinks - ctx)) - 1;
+    return bits & near;
+}
+
+// The keys that no query of a sequence sees, between its sinks and the first
+// query's window, are skipped in whole units (tiles of a kernel): a sequence
+// of L keys is the units [0, head) and [head + skip, ceil(L / unit)).
+struct WindowSpan {
+    int head, skip;
+};
+__host__ __device__ inline WindowSpan window_span(const AttnArgs& a, int ctx, int unit) {
+    WindowSpan w;
+    const int low = window_low(a, ctx);
+    w.head = (int)(((int64_t)(a.sinks < low ? a.sinks : low) + unit - 1) / unit);
+    w.skip = low / unit - w.head;
+    if (w.skip < 0) w.skip = 0;
+    return w;
 }
 
 // ---- SIMT kernel (CUDA cores; any supported dtype / shape) ----
@@ -130,6 +176,49 @@ cudaError_t launch_codec_encode(const void* codes, int64_t nblk, int P, int D, v
                                 int32_t* npairs, cudaStream_t stream);
 cudaError_t launch_codec_decode(const void* pairs, const int32_t* npairs, int64_t nblk, int P,
                                 int D, void* codes, int* dev_err, cudaStream_t stream);
+
+// ---- rotary positions with the append (rope_append.cu) ----
+struct RopeAppendArgs {
+    const void* q;  // null when Hq = 0
+    const void* k_new;
+    const void* v_new;
+    void* q_out;
+    int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements between tokens
+    int32_t src_dtype;
+    void* k_cache;
+    void* v_cache;
+    void* k_scale;  // fp16 per (page, kv-head, slot) for i8, fp32 per (page, kv-head) for e4m3
+    void* v_scale;
+    int32_t cache_dtype;
+    const int32_t* block_table;
+    const int32_t* ctx_lens;
+    const int32_t* positions;  // [B, n] or null: ctx + t
+    const int32_t* new_lens;   // [B] or null: n
+    const uint64_t* table;     // [rot / 2] 64-bit fractions of a turn per position
+    int32_t rot, interleaved;
+    float amplitude;
+    int32_t B, n, Hq, Hkv, D, P, num_pages, max_pages;
+    int* dev_err;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs& a, int num_sms, cudaStream_t stream);
+
+// ---- the cache read back (kv_gather.cu) ----
+struct GatherArgs {
+    const void* k_cache;
+    const void* v_cache;
+    const void* k_scale;
+    const void* v_scale;
+    int32_t cache_dtype;
+    const int32_t* block_table;
+    const int32_t* starts;  // [B] or null: 0
+    const int32_t* lens;
+    void* k_out;
+    void* v_out;
+    int32_t out_dtype;
+    int32_t B, max_len, Hkv, D, P, num_pages, max_pages;
+    int* dev_err;
+};
+cudaError_t launch_kv_gather(const GatherArgs& a, cudaStream_t stream);
 
 cudaError_t launch_commit(int32_t* ctx_lens, const int32_t* accepted_len, int B, int extra,
                           cudaStream_t stream);

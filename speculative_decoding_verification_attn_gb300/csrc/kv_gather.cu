@@ -1,0 +1,168 @@
+// Reading the paged cache back: rows of positions start_b .. start_b + len_b -
+// 1 of every sequence, as dense [B, max_len, Hkv, D] tensors of K and of V in
+// fp32 or bf16 (one rounding).
+//
+// The value of a row element is the cache's: as stored (f32, bf16), code *
+// scale of the (token, kv-head) (i8) or of the (page, kv-head) (e4m3), the
+// product in fp32.  Rows of t >= len_b are left as they were.
+//
+// A copy bound by memory: a lane takes 16 consecutive elements of a row (16
+// bytes of codes, 32 of bf16 written), the lanes of a warp cover the heads of
+// one token and of the next ones in turn, four loads in flight per lane.
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kInFlight = 4;
+
+struct Gather16 {
+    uint4 w[4];
+};
+
+template <typename TC> __device__ __forceinline__ Gather16 load16(const TC* p) {
+    Gather16 g;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(TC); ++i) g.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    return g;
+}
+
+template <typename TC> __device__ __forceinline__ void widen(const Gather16& g, float s, float (&x)[16]) {
+    if constexpr (sizeof(TC) == 4) {
+        const float* f = reinterpret_cast<const float*>(g.w);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = f[e];
+    } else if constexpr (sizeof(TC) == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t w[4] = {g.w[i].x, g.w[i].y, g.w[i].z, g.w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+                x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+        }
+    } else {
+        const uint32_t w[4] = {g.w[0].x, g.w[0].y, g.w[0].z, g.w[0].w};
+        if constexpr (std::is_same<TC, int8_t>::value) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                x[e] = (float)(int8_t)(w[e >> 2] >> (8 * (e & 3))) * s;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)(w[e >> 1] >> (16 * (e & 1))), __NV_E4M3);
+                const float2 f = __half22float2(__half2(r));
+                x[2 * e] = f.x * s;
+                x[2 * e + 1] = f.y * s;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void put16(float* p, const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<float4*>(p)[i] =
+            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+__device__ __forceinline__ void put16(__nv_bfloat16* p, const float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        reinterpret_cast<uint4*>(p)[i] =
+            make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                       pack_bf16x2(x[8 * i + 4], x[8 * i + 5]),
+                       pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+}
+
+// grid (chunks of a sequence's rows, sequence, tensor)
+template <typename TC, typename TO>
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int b = blockIdx.y;
+    const bool is_v = blockIdx.z;
+    const int len = max(0, min(a.max_len, __ldg(a.lens + b)));
+    const int64_t start = a.starts ? (int64_t)__ldg(a.starts + b) : 0;
+    const int cpr = a.D / 16, per_token = a.Hkv * cpr;  // 16-element chunks of a row, of a token
+    const uint32_t total = (uint32_t)len * per_token;  // < 2^31 (checked by the launch)
+    const TC* cache = static_cast<const TC*>(is_v ? a.v_cache : a.k_cache);
+    TO* out = static_cast<TO*>(is_v ? a.v_out : a.k_out) + (int64_t)b * a.max_len * a.Hkv * a.D;
+    const uint32_t c0 = blockIdx.x * (kThreads * kInFlight) + threadIdx.x;
+    const int64_t reach = (int64_t)a.max_pages * a.P;
+    Gather16 g[kInFlight];
+    float s[kInFlight];
+    bool ok[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+        const uint32_t c = c0 + u * kThreads;
+        ok[u] = c < total;
+        s[u] = 1.f;
+        if (!ok[u]) continue;
+        const uint32_t t = c / (uint32_t)per_token, in = c - t * per_token;
+        const uint32_t h = in / (uint32_t)cpr, e0 = (in - h * cpr) * 16;
+        const int64_t pos = start + t;
+        if (pos < 0 || pos >= reach) {
+            raise_device_error(a.dev_err, SPEC_DEVERR_CTX);
+            ok[u] = false;
+            continue;
+        }
+        const uint32_t pg = (uint32_t)pos / (uint32_t)a.P, slot = (uint32_t)pos - pg * a.P;
+        const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
+        if (page < 0 || page >= a.num_pages) {
+            raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
+            ok[u] = false;
+            continue;
+        }
+        const int64_t block = (int64_t)page * a.Hkv + h, row = block * a.P + slot;
+        g[u] = load16(cache + row * a.D + e0);
+        if constexpr (std::is_same<TC, int8_t>::value)
+            s[u] = __half2float(__ushort_as_half(
+                __ldg(static_cast<const uint16_t*>(is_v ? a.v_scale : a.k_scale) + row)));
+        else if constexpr (sizeof(TC) == 1)
+            s[u] = __ldg(static_cast<const float*>(is_v ? a.v_scale : a.k_scale) + block);
+    }
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) {
+        if (!ok[u]) continue;
+        float x[16];
+        widen<TC>(g[u], s[u], x);
+        put16(out + (int64_t)(c0 + u * kThreads) * 16, x);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_gather(const GatherArgs& a, cudaStream_t stream) {
+    const int64_t chunks = (int64_t)a.max_len * a.Hkv * (a.D / 16);
+    const int64_t x = (chunks + kThreads * kInFlight - 1) / (kThreads * kInFlight);
+    if (x == 0 || a.B == 0) return cudaSuccess;
+    if (chunks >= (1LL << 31) || a.B > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)x, (unsigned)a.B, 2);
+    auto go = [&](auto kern) {
+        return launch_dependent(kern, grid, dim3(kThreads), 0, stream, a);
+    };
+    const bool f32 = a.out_dtype == SPEC_DTYPE_F32;
+    switch (a.cache_dtype) {
+    case SPEC_DTYPE_F32:
+        return f32 ? go(kv_gather_kernel<float, float>) : go(kv_gather_kernel<float, __nv_bfloat16>);
+    case SPEC_DTYPE_BF16:
+        return f32 ? go(kv_gather_kernel<__nv_bfloat16, float>)
+                   : go(kv_gather_kernel<__nv_bfloat16, __nv_bfloat16>);
+    case SPEC_DTYPE_I8:
+        return f32 ? go(kv_gather_kernel<int8_t, float>) : go(kv_gather_kernel<int8_t, __nv_bfloat16>);
+    case SPEC_DTYPE_E4M3:
+        return f32 ? go(kv_gather_kernel<__nv_fp8_e4m3, float>)
+                   : go(kv_gather_kernel<__nv_fp8_e4m3, __nv_bfloat16>);
+    default:
+        return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace specv

@@ -47,13 +47,16 @@ struct Workspace {
     void* base = nullptr;
     size_t bytes = 0;
     int sms = 0;
+    // outgrown buffers: graphs captured before the growth still point into
+    // them, so they stay until spec_release
+    std::vector<void*> retired;
 };
 std::mutex g_ws_mu;
 std::vector<Workspace> g_ws;
 
 // Returns the current device's workspace with at least `scratch` bytes of
 // scratch space (allocating or growing it), or sets an error.
-int get_workspace(size_t scratch, Workspace** out) {
+int get_workspace(size_t scratch, cudaStream_t stream, Workspace** out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -66,20 +69,32 @@ int get_workspace(size_t scratch, Workspace** out) {
     }
     const size_t need = kHeader + ((scratch + 255) & ~size_t(255));
     if (w.bytes < need) {
-        if (w.base) {
-            e = cudaDeviceSynchronize();  // earlier calls may still use the old buffer
-            if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-            cudaFree(w.base);
-            w.base = nullptr;
-            w.bytes = 0;
-        }
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(stream, &cap) == cudaSuccess &&
+            cap != cudaStreamCaptureStatusNone)
+            return fail(SPEC_ERR_UNSUPPORTED, "the workspace would grow during a stream capture: "
+                        "make one such call before capturing");
+        (void)cudaGetLastError();
+        // at least twice the old size, so that the retired buffers together
+        // stay below the current one
         size_t grow = need < (size_t)64 << 20 ? (size_t)64 << 20 : need;
-        e = cudaMalloc(&w.base, grow);
+        if (grow < 2 * w.bytes) grow = 2 * w.bytes;
+        try {
+            w.retired.reserve(w.retired.size() + 1);
+        } catch (...) {
+            return fail(SPEC_ERR_CUDA, "out of host memory");
+        }
+        void* fresh = nullptr;
+        e = cudaMalloc(&fresh, grow);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-        e = cudaMemset(w.base, 0, kHeader);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(workspace)");
-        e = cudaDeviceSynchronize();
-        if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+        e = cudaMemset(fresh, 0, kHeader);
+        if (e == cudaSuccess) e = cudaDeviceSynchronize();
+        if (e != cudaSuccess) {
+            cudaFree(fresh);
+            return cuda_fail(e, "cudaMemset(workspace)");
+        }
+        if (w.base) w.retired.push_back(w.base);
+        w.base = fresh;
         w.bytes = grow;
     }
     *out = &w;
@@ -94,6 +109,7 @@ int dtype_size(int32_t dt) {
     case SPEC_DTYPE_BF16: return 2;
     case SPEC_DTYPE_F16: return 2;
     case SPEC_DTYPE_I8: return 1;
+    case SPEC_DTYPE_E4M3: return 1;
     default: return 0;
     }
 }
@@ -173,13 +189,27 @@ int spec_set_option(int32_t option, int64_t value) {
 
 namespace {
 
+// The words of a call's scales: i8 fp16 per (page, kv-head, slot), e4m3 fp32
+// per (page, kv-head).
+int check_scales(int32_t dtype, const void* k_scale, const void* v_scale) {
+    if (dtype == SPEC_DTYPE_I8 && (!k_scale || !v_scale))
+        return fail(SPEC_ERR_INVALID, "an I8 cache needs k_scale and v_scale");
+    if (dtype == SPEC_DTYPE_E4M3) {
+        if (!k_scale || !v_scale)
+            return fail(SPEC_ERR_INVALID, "an E4M3 cache needs k_scale and v_scale");
+        if ((reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale)) & 3)
+            return fail(SPEC_ERR_INVALID, "E4M3 scales must be 4-byte aligned");
+    }
+    return SPEC_OK;
+}
+
 int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
                      const void* v_scale, const int32_t* block_table, const int32_t* ctx_lens,
                      const uint64_t* tree_mask, int32_t batch, int32_t num_draft,
                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                      int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
-                     int32_t q_dtype, int32_t kv_dtype, float scale, void* out, float* lse,
-                     void* stream) {
+                     int32_t q_dtype, int32_t kv_dtype, float scale, int32_t window,
+                     int32_t num_sinks, void* out, float* lse, void* stream) {
     g_err.clear();
     if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
     if (num_draft < 1 || num_draft > 64) return fail(SPEC_ERR_INVALID, "num_draft must be in [1, 64]");
@@ -192,14 +222,15 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
         return fail(SPEC_ERR_INVALID, "num_pages and max_pages_per_seq must be >= 1");
     if (q_dtype != SPEC_DTYPE_F32 && q_dtype != SPEC_DTYPE_BF16)
         return fail(SPEC_ERR_INVALID, "q_dtype must be F32 or BF16");
-    if (kv_dtype != SPEC_DTYPE_F32 && kv_dtype != SPEC_DTYPE_BF16 && kv_dtype != SPEC_DTYPE_I8)
-        return fail(SPEC_ERR_INVALID, "kv_dtype must be F32, BF16 or I8");
+    if (kv_dtype != SPEC_DTYPE_F32 && kv_dtype != SPEC_DTYPE_BF16 && kv_dtype != SPEC_DTYPE_I8 &&
+        kv_dtype != SPEC_DTYPE_E4M3)
+        return fail(SPEC_ERR_INVALID, "kv_dtype must be F32, BF16, I8 or E4M3");
     if (!(scale == scale)) return fail(SPEC_ERR_INVALID, "scale is NaN");
     if (batch == 0) return SPEC_OK;
     if (!q || !k_cache || !v_cache || !block_table || !ctx_lens || !out)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
-    if (kv_dtype == SPEC_DTYPE_I8 && (!k_scale || !v_scale))
-        return fail(SPEC_ERR_INVALID, "an I8 cache needs k_scale and v_scale");
+    int rc = check_scales(kv_dtype, k_scale, v_scale);
+    if (rc) return rc;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
         return fail(SPEC_ERR_INVALID, "q, caches and out must be 16-byte aligned");
     if ((int64_t)num_pages * num_kv_heads * page_size * head_dim >= (1LL << 40))
@@ -209,8 +240,12 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
 
     specv::AttnArgs a;
     a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
-    a.k_scale = static_cast<const uint16_t*>(k_scale);
-    a.v_scale = static_cast<const uint16_t*>(v_scale);
+    const bool paged = kv_dtype == SPEC_DTYPE_E4M3;  // one fp32 scale per (page, kv-head)
+    a.k_scale = paged ? nullptr : static_cast<const uint16_t*>(k_scale);
+    a.v_scale = paged ? nullptr : static_cast<const uint16_t*>(v_scale);
+    a.k_page_scale = paged ? static_cast<const float*>(k_scale) : nullptr;
+    a.v_page_scale = paged ? static_cast<const float*>(v_scale) : nullptr;
+    a.window = window; a.sinks = num_sinks;
     a.block_table = block_table; a.ctx_lens = ctx_lens;
     a.B = batch; a.k = num_draft; a.Hq = num_q_heads; a.Hkv = num_kv_heads; a.D = head_dim;
     a.P = page_size; a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
@@ -223,7 +258,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     cudaStream_t st = static_cast<cudaStream_t>(stream);
 
     Workspace* ws = nullptr;
-    int rc = get_workspace(0, &ws);
+    rc = get_workspace(0, st, &ws);
     if (rc) return rc;
 
     // kernels: 1 SIMT (chunked), 2 tcgen05 (64-key tiles), 3 warp MMA,
@@ -236,9 +271,10 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     // the 64-key tcgen05 kernel; every other shape the single-pass SIMT
     // kernel when a whole sequence fits its shared memory, else the chunked one
     const int64_t path = g_opt_path.load();
-    const bool tc_ok = specv::tc_supported(a), mma_ok = specv::mma_supported(a);
-    const bool tc2_ok = specv::tc2_supported(a);
-    const bool small_ok = specv::small_attn_max_keys(a) > 0;
+    const bool win = window > 0;
+    const bool tc_ok = !win && specv::tc_supported(a), mma_ok = !win && specv::mma_supported(a);
+    const bool tc2_ok = !win && specv::tc2_supported(a);
+    const bool small_ok = !win && specv::small_attn_max_keys(a) > 0;
     int kernel;
     if (path == 1) kernel = 1;
     else if (path >= 2) {
@@ -265,7 +301,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     if (use_tc) {
         int ctas = (int)g_opt_ctas.load();
         if (ctas <= 0) ctas = ws->sms;
-        rc = get_workspace(specv::tc_workspace_bytes(a, ctas), &ws);
+        rc = get_workspace(specv::tc_workspace_bytes(a, ctas), st, &ws);
         if (rc) return rc;
         a.dev_err = static_cast<int*>(ws->base);
         a.seg_counters = reinterpret_cast<int*>(static_cast<char*>(ws->base) + kCountersOff);
@@ -283,7 +319,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
         const int64_t gy = (int64_t)batch * num_kv_heads * p.row_groups;
         if (gy > 65535 || R > (1 << 20))
             return fail(SPEC_ERR_UNSUPPORTED, "batch * num_kv_heads too large for the SIMT path");
-        rc = get_workspace(specv::simt_workspace_bytes(a, p), &ws);
+        rc = get_workspace(specv::simt_workspace_bytes(a, p), st, &ws);
         if (rc) return rc;
         a.dev_err = static_cast<int*>(ws->base);
         e = specv::launch_attn_simt(a, p, static_cast<char*>(ws->base) + kHeader, st);
@@ -304,8 +340,27 @@ int spec_verify_attn(const void* q, const void* k_cache, const void* v_cache, co
                      void* out, float* lse, void* stream) {
     return verify_attn_impl(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, nullptr,
                             batch, num_draft, num_q_heads, num_kv_heads, head_dim, page_size,
-                            num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale, out, lse,
-                            stream);
+                            num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale, 0, 0, out,
+                            lse, stream);
+}
+
+int spec_verify_attn_window(const void* q, const void* k_cache, const void* v_cache,
+                            const void* k_scale, const void* v_scale, const int32_t* block_table,
+                            const int32_t* ctx_lens, const uint64_t* tree_mask, int32_t batch,
+                            int32_t num_draft, int32_t num_q_heads, int32_t num_kv_heads,
+                            int32_t head_dim, int32_t page_size, int32_t num_pages,
+                            int32_t max_pages_per_seq, int32_t q_dtype, int32_t kv_dtype,
+                            float scale, int32_t window, int32_t num_sinks, void* out, float* lse,
+                            void* stream) {
+    g_err.clear();
+    if (window < 1) return fail(SPEC_ERR_INVALID, "window must be >= 1");
+    if (num_sinks < 0) return fail(SPEC_ERR_INVALID, "num_sinks must be >= 0");
+    if (tree_mask && window < num_draft)
+        return fail(SPEC_ERR_INVALID, "a tree's window must hold all its nodes: window >= num_draft");
+    return verify_attn_impl(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens,
+                            tree_mask, batch, num_draft, num_q_heads, num_kv_heads, head_dim,
+                            page_size, num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale,
+                            window, num_sinks, out, lse, stream);
 }
 
 int spec_verify_attn_tree(const void* q, const void* k_cache, const void* v_cache,
@@ -319,7 +374,7 @@ int spec_verify_attn_tree(const void* q, const void* k_cache, const void* v_cach
     return verify_attn_impl(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens,
                             tree_mask, batch, num_draft, num_q_heads, num_kv_heads, head_dim,
                             page_size, num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale,
-                            out, lse, stream);
+                            0, 0, out, lse, stream);
 }
 
 }  // extern "C"
@@ -347,7 +402,8 @@ int accept_greedy_impl(const void* logits, int32_t logits_dtype, const int32_t* 
     const int64_t blocks = (int64_t)batch * (num_draft + 1) * ((vocab + 8191) / 8192);
     if (blocks >= (1LL << 31)) return fail(SPEC_ERR_UNSUPPORTED, "logits too large");
     Workspace* ws = nullptr;
-    int rc = get_workspace(specv::accept_workspace_bytes(a), &ws);
+    int rc = get_workspace(specv::accept_workspace_bytes(a), static_cast<cudaStream_t>(stream),
+                           &ws);
     if (rc) return rc;
     a.dev_err = static_cast<int*>(ws->base);
     int32_t* tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws->base) + kTicketsOff);
@@ -397,7 +453,8 @@ int spec_accept_rejection(const void* target_logits, const void* draft_logits,
     const int64_t units = (int64_t)batch * (2 * num_draft + 1) * ((vocab + 2047) / 2048);
     if (units >= (1LL << 31)) return fail(SPEC_ERR_UNSUPPORTED, "logits too large");
     Workspace* ws = nullptr;
-    int rc = get_workspace(specv::rejection_workspace_bytes(batch, num_draft, vocab), &ws);
+    int rc = get_workspace(specv::rejection_workspace_bytes(batch, num_draft, vocab),
+                           static_cast<cudaStream_t>(stream), &ws);
     if (rc) return rc;
     int32_t* tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws->base) + kTicketsOff);
     cudaError_t e = specv::launch_accept_rejection(
@@ -425,17 +482,26 @@ int spec_kv_append(const void* k_new, const void* v_new, int32_t src_dtype, void
     if (src_dtype != SPEC_DTYPE_F32 && src_dtype != SPEC_DTYPE_BF16)
         return fail(SPEC_ERR_INVALID, "src_dtype must be F32 or BF16");
     if (cache_dtype != SPEC_DTYPE_F32 && cache_dtype != SPEC_DTYPE_BF16 &&
-        cache_dtype != SPEC_DTYPE_I8)
-        return fail(SPEC_ERR_INVALID, "cache_dtype must be F32, BF16 or I8");
+        cache_dtype != SPEC_DTYPE_I8 && cache_dtype != SPEC_DTYPE_E4M3)
+        return fail(SPEC_ERR_INVALID, "cache_dtype must be F32, BF16, I8 or E4M3");
     if (batch == 0) return SPEC_OK;
     if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !ctx_lens)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
-    if (cache_dtype == SPEC_DTYPE_I8 && (!k_scale || !v_scale))
-        return fail(SPEC_ERR_INVALID, "an I8 cache needs k_scale and v_scale");
+    int rc = check_scales(cache_dtype, k_scale, v_scale);
+    if (rc) return rc;
+    if (cache_dtype == SPEC_DTYPE_E4M3) {
+        // pages share a scale: the page form of the rotary append, nothing rotated
+        const int64_t stride = (int64_t)num_kv_heads * head_dim;
+        return spec_rope_append(nullptr, k_new, v_new, nullptr, 0, stride, stride, 0, src_dtype,
+                                k_cache, v_cache, k_scale, v_scale, cache_dtype, block_table,
+                                ctx_lens, nullptr, nullptr, nullptr, 0, 0, 1.f, batch, num_new, 0,
+                                num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
+                                stream);
+    }
     if ((int64_t)batch * num_new * num_kv_heads * 2 / 8 >= (1LL << 31))
         return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
     Workspace* ws = nullptr;
-    int rc = get_workspace(0, &ws);
+    rc = get_workspace(0, static_cast<cudaStream_t>(stream), &ws);
     if (rc) return rc;
     cudaError_t e = specv::launch_kv_append(
         k_new, v_new, src_dtype, k_cache, v_cache, static_cast<uint16_t*>(k_scale),
@@ -443,6 +509,158 @@ int spec_kv_append(const void* k_new, const void* v_new, int32_t src_dtype, void
         num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
         static_cast<int*>(ws->base), static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
+    return SPEC_OK;
+}
+
+int spec_rope_append(const void* q, const void* k_new, const void* v_new, void* q_out,
+                     int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                     int32_t src_dtype, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                     int32_t cache_dtype, const int32_t* block_table, const int32_t* ctx_lens,
+                     const int32_t* positions, const int32_t* new_lens, const uint64_t* rope_table,
+                     int32_t rotary_dim, int32_t interleaved, float amplitude, int32_t batch,
+                     int32_t num_new, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                     void* stream) {
+    g_err.clear();
+    if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
+    if (num_new < 1) return fail(SPEC_ERR_INVALID, "num_new must be >= 1");
+    if (num_kv_heads < 1) return fail(SPEC_ERR_INVALID, "num_kv_heads must be >= 1");
+    if (num_q_heads < 0) return fail(SPEC_ERR_INVALID, "num_q_heads must be >= 0");
+    if (head_dim < 32 || head_dim > 256 || head_dim % 32)
+        return fail(SPEC_ERR_INVALID, "head_dim must be a multiple of 32 in [32, 256]");
+    if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 16)
+        return fail(SPEC_ERR_INVALID, "rotary_dim must be a multiple of 16 in [0, head_dim]");
+    if (page_size < 1) return fail(SPEC_ERR_INVALID, "page_size < 1");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(SPEC_ERR_INVALID, "num_pages and max_pages_per_seq must be >= 1");
+    if (src_dtype != SPEC_DTYPE_F32 && src_dtype != SPEC_DTYPE_BF16)
+        return fail(SPEC_ERR_INVALID, "src_dtype must be F32 or BF16");
+    if (cache_dtype != SPEC_DTYPE_F32 && cache_dtype != SPEC_DTYPE_BF16 &&
+        cache_dtype != SPEC_DTYPE_I8 && cache_dtype != SPEC_DTYPE_E4M3)
+        return fail(SPEC_ERR_INVALID, "cache_dtype must be F32, BF16, I8 or E4M3");
+    if (!(amplitude > -INFINITY && amplitude < INFINITY))
+        return fail(SPEC_ERR_INVALID, "amplitude must be finite");
+    const int64_t kv_row = (int64_t)num_kv_heads * head_dim, q_row = (int64_t)num_q_heads * head_dim;
+    if (k_stride < kv_row || v_stride < kv_row || (num_q_heads && (q_stride < q_row ||
+                                                                   q_out_stride < q_row)))
+        return fail(SPEC_ERR_INVALID, "a token stride is shorter than the token's row");
+    if (batch == 0) return SPEC_OK;
+    if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !ctx_lens ||
+        (num_q_heads && (!q || !q_out)) || (rotary_dim && !rope_table))
+        return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    int rc = check_scales(cache_dtype, k_scale, v_scale);
+    if (rc) return rc;
+    const int64_t step = src_dtype == SPEC_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (num_q_heads && (!aligned16(q) || !aligned16(q_out) || q_stride % step ||
+                         q_out_stride % step)) ||
+        k_stride % step || v_stride % step)
+        return fail(SPEC_ERR_INVALID, "tensors and token strides must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(rope_table) & 7))
+        return fail(SPEC_ERR_INVALID, "rope_table must be 8-byte aligned");
+    // every launch index and in-kernel product below stays inside 31 bits
+    if ((int64_t)batch * num_new * (num_q_heads + 2 * num_kv_heads) >= (1LL << 31) ||
+        (int64_t)num_pages * num_kv_heads * page_size >= (1LL << 40))
+        return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = get_workspace(0, st, &ws);
+    if (rc) return rc;
+    specv::RopeAppendArgs a;
+    a.q = q; a.k_new = k_new; a.v_new = v_new; a.q_out = q_out;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride; a.src_dtype = src_dtype;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype; a.block_table = block_table; a.ctx_lens = ctx_lens;
+    a.positions = positions; a.new_lens = new_lens; a.table = rope_table;
+    a.rot = rotary_dim; a.interleaved = interleaved != 0; a.amplitude = amplitude;
+    a.B = batch; a.n = num_new; a.Hq = num_q_heads; a.Hkv = num_kv_heads; a.D = head_dim;
+    a.P = page_size; a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_rope_append(a, ws->sms, st);
+    if (e != cudaSuccess) return cuda_fail(e, "rope_append launch");
+    return SPEC_OK;
+}
+
+int spec_rope_table(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                    double original_len, double fast_turns, double slow_turns, uint64_t* table,
+                    float* amplitude) {
+    g_err.clear();
+    if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2)
+        return fail(SPEC_ERR_INVALID, "rotary_dim must be even and in [2, 256]");
+    if (!(theta > 1.0 && theta < INFINITY)) return fail(SPEC_ERR_INVALID, "theta must be > 1");
+    if (scaling < SPEC_ROPE_PLAIN || scaling > SPEC_ROPE_YARN)
+        return fail(SPEC_ERR_INVALID, "unknown scaling %d", scaling);
+    if (scaling != SPEC_ROPE_PLAIN && !(factor >= 1.0 && factor < INFINITY))
+        return fail(SPEC_ERR_INVALID, "factor must be >= 1");
+    if (scaling == SPEC_ROPE_NTK && rotary_dim < 4)
+        return fail(SPEC_ERR_INVALID, "SPEC_ROPE_NTK needs rotary_dim >= 4");
+    if (scaling == SPEC_ROPE_YARN &&
+        !(original_len > 0 && original_len < INFINITY && slow_turns >= 0 &&
+          fast_turns > slow_turns && fast_turns < INFINITY))
+        return fail(SPEC_ERR_INVALID, "SPEC_ROPE_YARN needs original_len > 0 and "
+                    "0 <= slow_turns < fast_turns");
+    if (!table || !amplitude) return fail(SPEC_ERR_INVALID, "null table or amplitude");
+    const double two_pi = 6.283185307179586476925286766559;
+    const double d = rotary_dim;
+    const double base = scaling == SPEC_ROPE_NTK ? theta * pow(factor, d / (d - 2)) : theta;
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        double f = pow(base, -2.0 * j / d);
+        if (scaling == SPEC_ROPE_LINEAR) f /= factor;
+        if (scaling == SPEC_ROPE_YARN) {
+            double keep = (original_len * f / two_pi - slow_turns) / (fast_turns - slow_turns);
+            keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+            f = keep * f + (1 - keep) * f / factor;
+        }
+        // f <= 1 radian per position: the fraction of a turn stays below 2^62
+        table[j] = (uint64_t)(f / two_pi * 18446744073709551616.0);
+    }
+    *amplitude = scaling == SPEC_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return SPEC_OK;
+}
+
+int spec_kv_gather(const void* k_cache, const void* v_cache, const void* k_scale,
+                   const void* v_scale, int32_t cache_dtype, const int32_t* block_table,
+                   const int32_t* starts, const int32_t* lens, int32_t batch, int32_t max_len,
+                   int32_t num_kv_heads, int32_t head_dim, int32_t page_size, int32_t num_pages,
+                   int32_t max_pages_per_seq, int32_t out_dtype, void* k_out, void* v_out,
+                   void* stream) {
+    g_err.clear();
+    if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
+    if (max_len < 0) return fail(SPEC_ERR_INVALID, "max_len < 0");
+    if (num_kv_heads < 1) return fail(SPEC_ERR_INVALID, "num_kv_heads must be >= 1");
+    if (head_dim < 32 || head_dim > 256 || head_dim % 32)
+        return fail(SPEC_ERR_INVALID, "head_dim must be a multiple of 32 in [32, 256]");
+    if (page_size < 1) return fail(SPEC_ERR_INVALID, "page_size < 1");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(SPEC_ERR_INVALID, "num_pages and max_pages_per_seq must be >= 1");
+    if (out_dtype != SPEC_DTYPE_F32 && out_dtype != SPEC_DTYPE_BF16)
+        return fail(SPEC_ERR_INVALID, "out_dtype must be F32 or BF16");
+    if (cache_dtype != SPEC_DTYPE_F32 && cache_dtype != SPEC_DTYPE_BF16 &&
+        cache_dtype != SPEC_DTYPE_I8 && cache_dtype != SPEC_DTYPE_E4M3)
+        return fail(SPEC_ERR_INVALID, "cache_dtype must be F32, BF16, I8 or E4M3");
+    if (batch == 0 || max_len == 0) return SPEC_OK;
+    if (!k_cache || !v_cache || !block_table || !lens || !k_out || !v_out)
+        return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    int rc = check_scales(cache_dtype, k_scale, v_scale);
+    if (rc) return rc;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        return fail(SPEC_ERR_INVALID, "caches and outputs must be 16-byte aligned");
+    if (batch > 65535 || (int64_t)max_len * num_kv_heads * (head_dim / 16) >= (1LL << 31))
+        return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = get_workspace(0, st, &ws);
+    if (rc) return rc;
+    specv::GatherArgs a;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype; a.block_table = block_table; a.starts = starts; a.lens = lens;
+    a.k_out = k_out; a.v_out = v_out; a.out_dtype = out_dtype;
+    a.B = batch; a.max_len = max_len; a.Hkv = num_kv_heads; a.D = head_dim; a.P = page_size;
+    a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_kv_gather(a, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_gather launch");
     return SPEC_OK;
 }
 
@@ -479,7 +697,7 @@ int spec_codec_decode(const void* pairs, const int32_t* num_pairs, int64_t num_b
     if ((reinterpret_cast<uintptr_t>(pairs) & 15) || (reinterpret_cast<uintptr_t>(codes) & 15))
         return fail(SPEC_ERR_INVALID, "pairs and codes must be 16-byte aligned");
     Workspace* ws = nullptr;
-    rc = get_workspace(0, &ws);
+    rc = get_workspace(0, static_cast<cudaStream_t>(stream), &ws);
     if (rc) return rc;
     cudaError_t e = specv::launch_codec_decode(pairs, num_pairs, num_blocks, page_size, head_dim,
                                                codes, static_cast<int*>(ws->base),
@@ -504,16 +722,24 @@ int spec_device_error(int32_t* flags) {
     g_err.clear();
     if (!flags) return fail(SPEC_ERR_INVALID, "flags is NULL");
     Workspace* ws = nullptr;
-    int rc = get_workspace(0, &ws);
+    int rc = get_workspace(0, nullptr, &ws);
     if (rc) return rc;
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    int v = 0;
-    e = cudaMemcpy(&v, ws->base, sizeof(int), cudaMemcpyDeviceToHost);
-    if (e == cudaSuccess) e = cudaMemset(ws->base, 0, sizeof(int));
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    int all = 0;
+    auto read = [&](void* base) {  // a word of a buffer, read and cleared
+        int v = 0;
+        e = cudaMemcpy(&v, base, sizeof(int), cudaMemcpyDeviceToHost);
+        if (e == cudaSuccess && v) e = cudaMemset(base, 0, sizeof(int));
+        all |= v;
+        return e == cudaSuccess;
+    };
+    std::lock_guard<std::mutex> lk(g_ws_mu);
+    bool ok = read(ws->base);
+    for (size_t i = 0; ok && i < ws->retired.size(); ++i) ok = read(ws->retired[i]);
+    if (ok) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "read device error word");
-    *flags = v;
+    *flags = all;
     return SPEC_OK;
 }
 
@@ -527,6 +753,8 @@ int spec_release(void) {
         e = cudaDeviceSynchronize();
         if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
         cudaFree(g_ws[dev].base);
+        for (void* p : g_ws[dev].retired) cudaFree(p);
+        g_ws[dev].retired.clear();
         g_ws[dev].base = nullptr;
         g_ws[dev].bytes = 0;
     }
@@ -592,16 +820,22 @@ int spec_verify_attn_tensors(const spec_tensor_t* q, const spec_tensor_t* k_cach
     int rc = check_tensor(q, "q", 4, {SPEC_DTYPE_F32, SPEC_DTYPE_BF16}, {-1, num_draft, -1, -1}, true);
     if (rc) return rc;
     const int64_t B = q->shape[0], Hq = q->shape[2], D = q->shape[3];
-    rc = check_tensor(k_cache, "k_cache", 4, {SPEC_DTYPE_F32, SPEC_DTYPE_BF16, SPEC_DTYPE_I8},
+    rc = check_tensor(k_cache, "k_cache", 4, 
+                      {SPEC_DTYPE_F32, SPEC_DTYPE_BF16, SPEC_DTYPE_I8, SPEC_DTYPE_E4M3},
                       {-1, -1, -1, D}, true);
     if (rc) return rc;
     const int64_t NP = k_cache->shape[0], Hkv = k_cache->shape[1], P = k_cache->shape[2];
     rc = check_tensor(v_cache, "v_cache", 4, {k_cache->dtype}, {NP, Hkv, P, D}, true);
     if (rc) return rc;
-    const bool i8 = k_cache->dtype == SPEC_DTYPE_I8;
+    const bool i8 = k_cache->dtype == SPEC_DTYPE_I8, e4m3 = k_cache->dtype == SPEC_DTYPE_E4M3;
     if (i8) {
         rc = check_tensor(k_scale, "k_scale", 3, {SPEC_DTYPE_F16}, {NP, Hkv, P});
         if (!rc) rc = check_tensor(v_scale, "v_scale", 3, {SPEC_DTYPE_F16}, {NP, Hkv, P});
+        if (rc) return rc;
+    }
+    if (e4m3) {
+        rc = check_tensor(k_scale, "k_scale", 2, {SPEC_DTYPE_F32}, {NP, Hkv});
+        if (!rc) rc = check_tensor(v_scale, "v_scale", 2, {SPEC_DTYPE_F32}, {NP, Hkv});
         if (rc) return rc;
     }
     rc = check_tensor(block_table, "block_table", 2, {SPEC_DTYPE_I32}, {B, -1});
@@ -613,8 +847,9 @@ int spec_verify_attn_tensors(const spec_tensor_t* q, const spec_tensor_t* k_cach
     if (!fits_i32(B) || !fits_i32(Hq) || !fits_i32(D) || !fits_i32(NP) || !fits_i32(Hkv) ||
         !fits_i32(P) || !fits_i32(MP))
         return fail(SPEC_ERR_INVALID, "a dimension does not fit int32");
-    return spec_verify_attn(q->data, k_cache->data, v_cache->data, i8 ? k_scale->data : nullptr,
-                            i8 ? v_scale->data : nullptr,
+    const bool scaled = i8 || e4m3;
+    return spec_verify_attn(q->data, k_cache->data, v_cache->data,
+                            scaled ? k_scale->data : nullptr, scaled ? v_scale->data : nullptr,
                             static_cast<const int32_t*>(block_table->data),
                             static_cast<const int32_t*>(ctx_lens->data), (int32_t)B, num_draft,
                             (int32_t)Hq, (int32_t)Hkv, (int32_t)D, (int32_t)P, (int32_t)NP,
