@@ -90,9 +90,9 @@ enum {
     /* 0 auto, 1 SIMT (CUDA cores) kernel with split-KV chunks, 2 tcgen05
      * kernel (64-key tiles), 3 warp-MMA (mma.sync) kernel for <= 16 query
      * rows per kv-head, 4 single-pass SIMT kernel (whole sequences in shared
-     * memory), 5 tcgen05 kernel with 128-key tiles (bf16 query and cache,
-     * head_dim 128, up to 128 query rows per kv-head, power-of-two pages of
-     * 16..256 keys) */
+     * memory), 5 tcgen05 kernel with 128-key tiles (bf16 query, bf16, I8 or
+     * E4M3 cache, head_dim 128, up to 128 query rows per kv-head,
+     * power-of-two pages of 16..256 keys) */
     SPEC_OPT_ATTN_PATH = 0,
     /* persistent CTAs of the tensor-core kernel; 0 = number of SMs */
     SPEC_OPT_NUM_CTAS = 1,

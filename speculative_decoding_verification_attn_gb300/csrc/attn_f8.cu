@@ -1,0 +1,1046 @@
+// Verification attention over an e4m3 paged cache (one fp32 scale per page and
+// kv-head) on the tcgen05 tensor cores, the codes fed to them as they are
+// stored.  bf16 q, head_dim 128, up to 128 query rows per kv-head; causal
+// chain, token tree, sliding window with sinks.
+//
+// Mathematics.  Key j of page g has K_j = sk_g c_j, V_j = sv_g d_j with e4m3
+// codes c, d.  For a query row q (times the softmax scale):
+//   s_j = sk_g <q, c_j>,   out = sum_j p_j sv_g d_j / sum_j p_j,  p_j = 2^(s_j - m)
+// in log2 units, m the running maximum.  Both products take 8-bit operands:
+//  * q = 2^e (hi + lo): hi is q 2^-e rounded to e4m3 and lo the rest rounded
+//    to e4m3, with 2^e chosen per row so that the largest element lies in
+//    [128, 256).  A bf16 has 8 significant bits and each part holds 4, so
+//    hi + lo is q itself down to 2^-10 of the row's largest element, and off
+//    by at most 2^-18 of that element below.  S = hi C^T + lo C^T: two MMAs of
+//    K = 32 into one fp32 accumulator, as many as a bf16 product would take.
+//  * P: in each row and block of 32 keys, w_j = p_j sv_g is scaled by the power
+//    of two that puts the block's largest in [128, 256) and split into hi + lo
+//    in the same way (8 significant bits, as a bf16 P would have).  The
+//    block-scaled MMA applies the power back per row and block, so keys far
+//    below the row's maximum keep their precision: a first key that holds
+//    most of the weight does not flush the thousands of light ones behind it,
+//    which a P in e4m3 under one scale per row would.  sv_g enters as
+//    log2(sv_g) in the exponent; the row sum takes each 16-key group's sum of w
+//    back by 1 / sv_g, in fp32.
+//
+// What bounds it: the bytes of the cache (32 KB per 128 keys and kv-head), with
+// the tensor pipe close behind: 8 + 8 MMAs of M128 N128 K32 per 128-key tile
+// issue in ~1030 cycles (measured, one CTA), the HBM share of an SM brings a
+// tile in ~1400.  So nothing may stand between the copy and the MMAs: no
+// widening pass, and the softmax below a tile's time on every SMSP.
+//
+// Layout.  Persistent grid, the tile list split as in the 128-key bf16 kernel
+// (TileSplit, partials merged by the combine kernel).
+//  * TMEM: S of set 0 [0,128), of set 1 [128,256), O of set 0 [256,384), of set
+//    1 [384,512).  P hi / lo go over S columns [64,96) / [96,128), the scale
+//    bytes of P and of V (all one) over [0,4) / [4,8).
+//  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
+//    and 6 TMA of K and of V (5 also brings the page scales); 7 P V issue;
+//    12-15 turn the q rows of the next piece into hi / lo.  16 warps share the
+//    block's 64K registers (setmaxnreg: 160, 96, 160, 96).
+//  * Rows: R = k * G query rows are the M side of one MMA.  R <= 64 (REP 2) and
+//    R <= 32 (REP 4): the rows stand REP times and copy c takes the 32-key
+//    blocks of its own, with P zero elsewhere, so that every softmax thread
+//    has work and a tile costs it 1 / REP of the exponentials; the copies'
+//    (max, sum, O) merge through shared memory once per piece.
+//  * Every wait is bounded (warp_wait); after a timeout every role skips its
+//    work, drains its copies and tensor-core operations and returns.
+#include <cuda.h>
+#include <math.h>
+
+#include "common.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int D = 128;
+constexpr int TN = 128;                // keys per tile
+constexpr int ROWS = 128;              // MMA M
+constexpr int THREADS = 16 * 32;
+constexpr int Q_PART = ROWS * D;       // 16 KB: hi or lo of one piece's rows
+constexpr int SLOT_BYTES = TN * D;     // 16 KB: one tile of K or of V
+constexpr int SLOTS = 4;               // of K and of V each
+constexpr int MAX_CHUNKS = TN / 16;    // page chunks per tile
+constexpr int LOOKAHEAD = 6;           // tiles of block-table entries prefetched
+constexpr int SCALE_AHEAD = 3;         // tiles of page scales prefetched
+constexpr int RAW_STAGES = SCALE_AHEAD + 1;
+// scale stages: tile j + SCALE_AHEAD is fetched once Q K^T of tile j - SLOTS is
+// done, which waited for the softmax of tile j - SLOTS - 3 or later
+constexpr int SCALE_STAGES = 16;
+static_assert(SCALE_STAGES > SCALE_AHEAD + SLOTS + 3, "a stage would be overwritten unread");
+// row exponents: the q rows of piece j are written when Q K^T of piece j - 2
+// is done; a softmax set may then still be at piece j - 4
+constexpr int EXP_STAGES = 8;
+constexpr int MAX_BATCH = 1024;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_O = 256;
+constexpr uint32_t P_HI = 64, P_LO = 96, SF_P = 0, SF_V = 4;  // inside an S buffer
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr int kSplitAlpha = 3;             // tiles charged per segment in the split
+
+struct Smem {
+    static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
+    static constexpr int KS = Q + 4 * Q_PART;
+    static constexpr int VS = KS + SLOTS * SLOT_BYTES;
+    static constexpr int RED = VS + SLOTS * SLOT_BYTES;  // [set][quad][32 rows][16] fp32
+    static constexpr int SFP = RED + 2 * 4 * 32 * 16 * 4;  // scale bytes of P, per set
+    static constexpr int SFV = SFP + 2 * 512;              // scale bytes of V: all 1.0
+    static constexpr int BARS = SFV + 512;
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + SLOTS, B_VFULL = B_KEMPTY + SLOTS,
+                         B_VEMPTY = B_VFULL + SLOTS, B_QFULL = B_VEMPTY + SLOTS,
+                         B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + 2,
+                         B_SFREE = B_PREADY + 2, B_EPI = B_SFREE + 2, B_DRAIN = B_EPI + 1,
+                         B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
+                         NUM_BARS = B_SCALE + SCALE_STAGES;
+    static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
+    static constexpr int STAT = MISC + 32;            // (m, l) of [set][lane]
+    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;  // [2 producers][LOOKAHEAD+1][8] int
+    static constexpr int RAW = PIDS + 2 * (LOOKAHEAD + 1) * MAX_CHUNKS * 4;  // [stage][k, v][8]
+    static constexpr int EXPS = RAW + RAW_STAGES * 2 * MAX_CHUNKS * 4;       // [stage][row] int8
+    static constexpr int SCALE = EXPS + EXP_STAGES * ROWS;  // [stage][8] {sk, log2 sv, 1/sv, on}
+    static constexpr int CTX = SCALE + SCALE_STAGES * MAX_CHUNKS * 16;
+    static constexpr int PRE = CTX + MAX_BATCH * 4;
+    static constexpr int END = PRE + (MAX_BATCH + 1) * 4;
+};
+static_assert(Smem::MISC % 16 == 0 && Smem::SCALE % 16 == 0 && Smem::SFP % 16 == 0, "alignment");
+constexpr size_t SMEM_BYTES = Smem::END + 1024;  // + alignment slack
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+struct F8Params {
+    AttnArgs a;
+    float* part_o;    // [2*C][ROWS][D]
+    float* part_lse;  // [2*C][ROWS]
+    int4* seg_rec;    // [C][2]
+    int* seg_pre;     // [B+1]
+};
+
+// Keys [k0, k0 + 32) that a query row sees: the context (with a window: the
+// sinks and the keys from `low` on), then the drafts of the row's bits, up to
+// key `end`.
+template <bool WIN>
+__device__ __forceinline__ uint32_t visible32(int k0, int end, int ctx, uint64_t mrow, int low,
+                                              int sinks) {
+    auto below = [](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1; };
+    const int nctx = ctx - k0;
+    uint32_t c = below(nctx);
+    if (WIN) c &= below(sinks - k0) | ~below(low - k0);
+    const uint32_t d = nctx >= 32    ? 0u
+                       : nctx >= 0   ? (uint32_t)(mrow << nctx)
+                       : nctx > -64  ? (uint32_t)(mrow >> -nctx)
+                                     : 0u;
+    return (c | d) & below(end - k0);
+}
+
+// Two values as e4m3 hi + lo (8 significant bits together): the rest after hi is exact in fp16, which holds the values with 11 bits.
+__device__ __forceinline__ void split_e4m3x2(float a, float b, uint16_t& hi, uint16_t& lo) {
+    uint32_t h, back, rest;
+    h = pack_f16x2(a, b);
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(h), "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
+}
+
+// One 16-key group of a row: its page's {sk, log2 sv, 1 / sv, on}
+struct Group {
+    float top;  // largest visible score (log2 units), -inf if none
+    float wtop; // top + log2 sv
+};
+
+// Largest visible score of a 16-key group (raw accumulators, mult > 0 to log2
+// units; bits: its visible keys).
+__device__ __forceinline__ Group group_max(const uint32_t* r, uint32_t bits, float mult,
+                                           const float4& sc) {
+    float m0 = -INFINITY, m1 = -INFINITY;
+    if ((bits & 0xffffu) == 0xffffu) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+            m0 = fmax3(m0, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+            m1 = fmax3(m1, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if ((bits >> c) & 1u) m0 = fmaxf(m0, __uint_as_float(r[c]));
+    }
+    const float m = fmaxf(m0, m1);
+    Group g;
+    g.top = m == -INFINITY ? m : m * mult;
+    g.wtop = m == -INFINITY ? m : g.top + sc.y;
+    return g;
+}
+
+// w = 2^(raw mult + bias) of a 16-key group to hi / lo words (4 codes each);
+// returns the sum of w.
+__device__ __forceinline__ float group_weights(const uint32_t* r, uint32_t bits, float mult,
+                                               float bias, bool on, uint32_t* hi, uint32_t* lo) {
+    const uint64_t mm = f2(mult, mult), bb = f2(bias, bias);
+    uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+    const bool all = (bits & 0xffffu) == 0xffffu;
+#pragma unroll
+    for (int c = 0; c < 16; c += 4) {
+        uint16_t h[2], l[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float x0, x1;
+            f2_split(f2_fma(f2(__uint_as_float(r[c + 2 * e]), __uint_as_float(r[c + 2 * e + 1])),
+                            mm, bb),
+                     x0, x1);
+            if (!all) {
+                x0 = (bits >> (c + 2 * e)) & 1u ? x0 : -INFINITY;
+                x1 = (bits >> (c + 2 * e + 1)) & 1u ? x1 : -INFINITY;
+            }
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+            sum[e] = f2_add(sum[e], f2(x0, x1));
+            split_e4m3x2(x0, x1, h[e], l[e]);
+        }
+        hi[c / 4] = on ? (uint32_t)h[0] | ((uint32_t)h[1] << 16) : 0u;
+        lo[c / 4] = on ? (uint32_t)l[0] | ((uint32_t)l[1] << 16) : 0u;
+    }
+    float a0, a1, b0, b1;
+    f2_split(sum[0], a0, a1);
+    f2_split(sum[1], b0, b1);
+    return (a0 + b0) + (a1 + b1);
+}
+
+// Power of two of a 32-key block: floor(log2) of its largest w against the
+// reference, in the exponent byte's range with room for the split's 2^7.
+__device__ __forceinline__ float block_power(float wtop, float m) {
+    return wtop == -INFINITY ? 0.f : fminf(fmaxf(floorf(wtop - m), -110.f), 110.f);
+}
+
+// One 32-key block of a row: hi / lo words, the scale byte and its part of the
+// row sum (two 16-key groups with scales s0, s1).
+__device__ __forceinline__ float block_weights(const uint32_t* r, uint32_t vis, float qm,
+                                               const float4& s0, const float4& s1, float wtop,
+                                               float m, uint32_t* hi, uint32_t* lo,
+                                               uint32_t& sf) {
+    const float n = block_power(wtop, m);
+    sf = (uint32_t)(120 + (int)n);  // exponent byte of 2^(n - 7)
+    const float base = 7.f - n - m;
+    const float w0 = group_weights(r, vis, qm * s0.x, base + s0.y, s0.w != 0.f, hi, lo);
+    const float w1 = group_weights(r + 16, vis >> 16, qm * s1.x, base + s1.y, s1.w != 0.f, hi + 4,
+                                   lo + 4);
+    const float sum = (w0 > 0.f ? w0 * s0.z : 0.f) + (w1 > 0.f ? w1 * s1.z : 0.f);
+    return sum * __uint_as_float(sf << 23);
+}
+
+template <int REP, bool WIN>
+__global__ void __launch_bounds__(THREADS, 1)
+attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+               const F8Params prm) {
+    using Cursor = SegCursor<TN, WIN>;
+    constexpr int NBLK = 4 / REP;        // 32-key blocks of a softmax thread
+    constexpr int COPY = ROWS / REP;     // lanes of one copy of the rows
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const AttnArgs& a = prm.a;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::BARS);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Smem::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Smem::MISC + 4);
+    int64_t* s_rng = reinterpret_cast<int64_t*>(sm + Smem::MISC + 16);
+    int* s_ctx = reinterpret_cast<int*>(sm + Smem::CTX);
+    int* s_pre = reinterpret_cast<int*>(sm + Smem::PRE);
+    float4* s_scale = reinterpret_cast<float4*>(sm + Smem::SCALE);
+    int8_t* s_exp = reinterpret_cast<int8_t*>(sm + Smem::EXPS);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int B = a.B, k = a.k, Hkv = a.Hkv, G = a.Hq / a.Hkv, R = k * G, P = a.P;
+    const int CH = P < TN ? P : TN;      // keys per page chunk (a power of two)
+
+    if (tid == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&bars[Smem::B_KFULL + s], 1);
+            mbar_init(&bars[Smem::B_KEMPTY + s], 1);
+            mbar_init(&bars[Smem::B_VFULL + s], 1);
+            mbar_init(&bars[Smem::B_VEMPTY + s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars[Smem::B_QFULL + s], 4);   // the 4 converting warps
+            mbar_init(&bars[Smem::B_QFREE + s], 1);
+            mbar_init(&bars[Smem::B_SFULL + s], 1);
+            mbar_init(&bars[Smem::B_PREADY + s], 4);  // the 4 warps of the set
+            mbar_init(&bars[Smem::B_SFREE + s], 1);
+            mbar_init(&bars[Smem::B_DRAIN + s], 1);
+        }
+        for (int s = 0; s < EXP_STAGES; ++s) mbar_init(&bars[Smem::B_EXP + s], 4);
+        for (int s = 0; s < SCALE_STAGES; ++s) mbar_init(&bars[Smem::B_SCALE + s], 1);
+        mbar_init(&bars[Smem::B_EPI], 8);  // every softmax warp, once per piece
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    {
+        // q rows that no piece writes stay zero; the scale bytes of V are 1.0
+        uint4* q4 = reinterpret_cast<uint4*>(sm + Smem::Q);
+        for (int e = tid; e < 4 * Q_PART / 16; e += THREADS)
+            if ((e % (Q_PART / 16)) / 8 % COPY >= R) q4[e] = make_uint4(0, 0, 0, 0);
+        if (tid < 128) reinterpret_cast<uint32_t*>(sm + Smem::SFV)[tid] = 0x7f7f7f7fu;
+        fence_proxy_async_smem();
+    }
+    // the grids before this one have finished with every buffer this call
+    // touches (and with the tensor memory of this SM)
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    if (warp == 4) {
+        tmem_alloc(tmem_slot, TMEM_COLS);
+        tmem_relinquish();
+    }
+    if (warp == 5) {
+        const int per = (B + 31) / 32, lo = min(B, lane * per), hi = min(B, lo + per);
+        int sum = 0;
+        for (int b = lo; b < hi; ++b) {
+            int c = a.ctx_lens[b];
+            const int64_t cap = (int64_t)a.max_pages * P - k;
+            if (c < 0 || (int64_t)c > cap) {
+                raise_device_error(a.dev_err, SPEC_DEVERR_CTX);
+                c = c < 0 ? 0 : (int)(cap < 0 ? 0 : cap);
+            }
+            s_ctx[b] = c;
+            sum += Cursor::tiles(a, c);
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int run = incl - sum;
+        for (int b = lo; b < hi; ++b) {
+            s_pre[b] = run;
+            run += Cursor::tiles(a, s_ctx[b]);
+        }
+        if (lane == 31) s_pre[B] = incl;
+        __syncwarp();  // the prefix above, written by this warp's lanes
+        if (lane < 2) {
+            TileSplit split;
+            split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
+            s_rng[lane] = split.begin(blockIdx.x + lane);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int64_t T = (int64_t)s_pre[B] * Hkv;
+    const int64_t t_begin = ld_shared_s64(s_rng);
+    const int n_tiles = (int)(ld_shared_s64(s_rng + 1) - t_begin);
+    if (tid == 0) {
+        // the segment holding tile t_begin and t_begin itself, for the combine
+        int4 r0 = make_int4(0, 0, -1, 0);
+        if (t_begin < T) {
+            Cursor c0;
+            c0.init(t_begin, s_pre, s_ctx, a);
+            r0 = make_int4(c0.b, c0.kvh, c0.lt, c0.nb);
+        }
+        prm.seg_rec[2 * blockIdx.x] = r0;
+        prm.seg_rec[2 * blockIdx.x + 1] =
+            make_int4((int)(t_begin & 0xffffffff), (int)(t_begin >> 32), 0, 0);
+    }
+    if (blockIdx.x == 0)
+        for (int b = tid; b <= B; b += THREADS) prm.seg_pre[b] = s_pre[b];
+
+    // the page chunk `l` of a tile holds a key that some query sees
+    auto chunk_used = [&](const Cursor& c, int l) {
+        const int k0 = c.key0() + l * CH, end = s_ctx[c.b] + k;
+        if (l * CH >= TN || k0 >= end) return false;
+        return !WIN || k0 < a.sinks || k0 + CH > window_low(a, s_ctx[c.b]);
+    };
+
+    if (warp >= 4 && warp < 8) {
+    regs_dec<96>();
+    if (warp == 5 || warp == 6) {
+        // ================= TMA producers: warp 5 K and scales, warp 6 V =================
+        // Tile it goes to slot it % SLOTS of its ring; each page chunk (CH
+        // keys of 128 bytes, swizzled by the copy) is one copy.  Block-table
+        // entries are prefetched LOOKAHEAD tiles ahead, and the K warp brings
+        // the chunks' scales SCALE_AHEAD tiles ahead and hands them to the
+        // softmax as {sk, log2 sv, 1 / sv, sv != 0}.
+        const bool is_v = warp == 6;
+        int* pids = reinterpret_cast<int*>(sm + Smem::PIDS) +
+                    (is_v ? 1 : 0) * (LOOKAHEAD + 1) * MAX_CHUNKS;
+        float* raw = reinterpret_cast<float*>(sm + Smem::RAW);
+        uint64_t* full = &bars[is_v ? Smem::B_VFULL : Smem::B_KFULL];
+        uint64_t* empty = &bars[is_v ? Smem::B_VEMPTY : Smem::B_KEMPTY];
+        uint8_t* ring = sm + (is_v ? Smem::VS : Smem::KS);
+        const CUtensorMap* map = is_v ? &vmap : &kmap;
+        Cursor cur, mid, ahead;
+        if (n_tiles > 0) {
+            cur.init(t_begin, s_pre, s_ctx, a);
+            mid = ahead = cur;
+        }
+        const uint64_t pol = l2_policy_evict_first();
+        if (lane == 0) prefetch_tmap(map);
+        auto fetch_pids = [&](int slot, const Cursor& c) {
+            if (lane < MAX_CHUNKS && chunk_used(c, lane))
+                cp_async_4(&pids[slot * MAX_CHUNKS + lane],
+                           &a.block_table[(int64_t)c.b * a.max_pages + (c.key0() + lane * CH) / P]);
+        };
+        // lanes 0-7: K scales, lanes 8-15: V scales of tile t (cursor c)
+        auto fetch_scales = [&](int t, const Cursor& c) {
+            const int l = lane & 7;
+            if (is_v || lane >= 2 * MAX_CHUNKS) return;
+            float* dst = raw + (t % RAW_STAGES) * 2 * MAX_CHUNKS + lane;
+            if (!chunk_used(c, l)) {
+                *dst = 1.f;
+                return;
+            }
+            int page = pids[(t % (LOOKAHEAD + 1)) * MAX_CHUNKS + l];
+            if (page < 0 || page >= a.num_pages) page = 0;  // flagged with its copy
+            cp_async_4(dst, (lane < MAX_CHUNKS ? a.k_page_scale : a.v_page_scale) +
+                                (int64_t)page * Hkv + c.kvh);
+        };
+        for (int la = 0; la < LOOKAHEAD; ++la)
+            if (la < n_tiles) {
+                fetch_pids(la, ahead);
+                if (la + 1 < n_tiles) ahead.next(s_ctx, a);
+            }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+        for (int t = 0; t < SCALE_AHEAD; ++t) {
+            if (t < n_tiles) {
+                fetch_scales(t, mid);
+                if (t + 1 < n_tiles) mid.next(s_ctx, a);
+            }
+            cp_async_commit();
+        }
+        int n_issued = 0;
+        bool ok = true;
+        for (int it = 0; it < n_tiles && ok; ++it) {
+            if (it + LOOKAHEAD < n_tiles) {
+                fetch_pids((it + LOOKAHEAD) % (LOOKAHEAD + 1), ahead);
+                if (it + LOOKAHEAD + 1 < n_tiles) ahead.next(s_ctx, a);
+            }
+            // one group per iteration: the scales of tile it were committed
+            // SCALE_AHEAD groups ago, and with them every block-table entry up
+            // to tile it + SCALE_AHEAD
+            cp_async_wait<SCALE_AHEAD - 1>();
+            __syncwarp();
+            const int* pid = pids + (it % (LOOKAHEAD + 1)) * MAX_CHUNKS;
+            const int s = it % SLOTS;
+            const bool used = lane < MAX_CHUNKS && chunk_used(cur, lane);
+            const int nck = __popc(__ballot_sync(0xffffffffu, used));
+            if (it >= SLOTS)
+                ok = warp_wait(&empty[s], ((it / SLOTS) - 1) & 1, abort_flag, a.dev_err);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(nck * CH * D));
+            __syncwarp();
+            if (!ok) break;
+            if (used) {
+                int page = pid[lane];
+                if (page < 0 || page >= a.num_pages) {
+                    raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
+                    page = 0;
+                }
+                const int key = cur.key0() + lane * CH;
+                tma_load_2d(ring + s * SLOT_BYTES + lane * CH * D, map, &full[s], 0,
+                            (page * Hkv + cur.kvh) * P + key % P, pol);
+            }
+            n_issued = it + 1;
+            if (!is_v) {
+                if (lane < MAX_CHUNKS) {
+                    const float* r = raw + (it % RAW_STAGES) * 2 * MAX_CHUNKS;
+                    const float sv = r[MAX_CHUNKS + lane];
+                    const bool on = sv > 0.f;
+                    s_scale[(it % SCALE_STAGES) * MAX_CHUNKS + lane] =
+                        make_float4(r[lane], on ? __log2f(sv) : 0.f, on ? 1.f / sv : 1.f,
+                                    on ? 1.f : 0.f);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[Smem::B_SCALE + it % SCALE_STAGES]);
+            }
+            __syncwarp();
+            if (it + SCALE_AHEAD < n_tiles) {
+                fetch_scales(it + SCALE_AHEAD, mid);
+                if (it + SCALE_AHEAD + 1 < n_tiles) mid.next(s_ctx, a);
+            }
+            cp_async_commit();
+            if (it + 1 < n_tiles) cur.next(s_ctx, a);
+        }
+        cp_async_wait<0>();
+        if (!ok && lane == 0) {
+            // the latest copy into each slot lands before the CTA exits
+            for (int j = max(0, n_issued - SLOTS); j < n_issued; ++j)
+                mbar_drain(&full[j % SLOTS], (j / SLOTS) & 1);
+        }
+    } else if (warp == 4) {
+        // ================= Q K^T issue =================
+        if (n_tiles > 0) {
+            Cursor cur;
+            cur.init(t_begin, s_pre, s_ctx, a);
+            int pc = -1;  // piece of the current tile
+            bool ok = true;
+            const uint64_t qdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::Q), 16, 1024);
+            const uint64_t kdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::KS), 16, 1024);
+            for (int it = 0; it < n_tiles && ok; ++it) {
+                const bool first = (it == 0) || (cur.lt == 0);
+                const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
+                const int s = it & 1, slot = it % SLOTS;
+                if (first) {
+                    ++pc;
+                    ok = warp_wait(&bars[Smem::B_QFULL + (pc & 1)], (pc >> 1) & 1, abort_flag,
+                                   a.dev_err);
+                    if (!ok) break;
+                }
+                // K of tile it landed; S buffer s free (P V of tile it - 2 done)
+                ok = warp_wait(&bars[Smem::B_KFULL + slot], (it / SLOTS) & 1, abort_flag,
+                               a.dev_err);
+                if (ok && it >= 2)
+                    ok = warp_wait(&bars[Smem::B_SFREE + s], ((it >> 1) - 1) & 1, abort_flag,
+                                   a.dev_err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t qd = qdesc0 + ((uint32_t)((pc & 1) * 2 * Q_PART) >> 4);
+                const uint64_t kd = kdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // hi, then lo, in 32-byte steps
+                    umma_f8_ss_w(tmem + s * TN, qd + (kk >> 2) * (Q_PART >> 4) + (kk & 3) * 2,
+                                 kd + (kk & 3) * 2, umma_idesc_e4m3(ROWS, TN), kk ? 1u : 0u);
+                umma_commit_w(&bars[Smem::B_SFULL + s]);
+                umma_commit_w(&bars[Smem::B_KEMPTY + slot]);
+                if (last) umma_commit_w(&bars[Smem::B_QFREE + (pc & 1)]);
+                if (it + 1 < n_tiles) cur.next(s_ctx, a);
+            }
+            // every tensor-core op of this warp finishes before TMEM is released
+            __syncwarp();
+            umma_commit_w(&bars[Smem::B_DRAIN]);
+            if (lane == 0) mbar_drain(&bars[Smem::B_DRAIN], 0);
+            __syncwarp();
+        }
+    } else {
+        // ================= P V issue (warp 7) =================
+        if (n_tiles > 0) {
+            Cursor cur;
+            cur.init(t_begin, s_pre, s_ctx, a);
+            int pc = -1;
+            bool ok = true;
+            bool has0 = false, has1 = false;  // set 0 / 1 issued a P V in this piece
+            // V of 32 keys: MN-major, 8-key groups 1 KB apart
+            const uint64_t vdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::VS), 1024, 1024);
+            const uint64_t sfp0 = umma_sdesc_plain(smem_u32(sm + Smem::SFP), 128);
+            const uint64_t sfv = umma_sdesc_plain(smem_u32(sm + Smem::SFV), 128);
+            for (int it = 0; it < n_tiles && ok; ++it) {
+                const bool first = (it == 0) || (cur.lt == 0);
+                const int s = it & 1, slot = it % SLOTS;
+                const int ctx = s_ctx[cur.b], key0 = cur.key0();
+                const int nvalid = min(TN, ctx + k - key0), nkb = (nvalid + 31) / 32;
+                if (first) {
+                    ++pc;
+                    has0 = has1 = false;
+                    // the previous piece's epilogue has read both O before the
+                    // first P V of this piece overwrites them
+                    if (pc >= 1)
+                        ok = warp_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
+                    if (!ok) break;
+                }
+                ok = warp_wait(&bars[Smem::B_VFULL + slot], (it / SLOTS) & 1, abort_flag,
+                               a.dev_err);
+                if (!ok) break;
+                // rows that no query sees and a P V reads: zero, so that 0 * (stale,
+                // canary or a NaN code) never reaches O
+                auto clear = [&](int r0, int r1) {
+                    uint4* v4 = reinterpret_cast<uint4*>(sm + Smem::VS + slot * SLOT_BYTES);
+                    for (int e = r0 * 8 + lane; e < r1 * 8; e += 32) v4[e] = make_uint4(0, 0, 0, 0);
+                };
+                bool cleared = nvalid % 32 != 0;
+                if (cleared) clear(nvalid, nkb * 32);
+                if (WIN) {
+                    const int low = window_low(a, ctx);
+                    const int g0 = max(0, a.sinks >= low ? nvalid : a.sinks - key0);
+                    const int g1 = min(nvalid, low - key0);
+                    if (g0 < g1) {
+                        clear(g0, g1);
+                        cleared = true;
+                    }
+                }
+                if (cleared) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                ok = warp_wait(&bars[Smem::B_PREADY + s], (it >> 1) & 1, abort_flag, a.dev_err);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = vdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
+                const bool hs = s ? has1 : has0;
+                const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O + s * D;
+                tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
+                tmem_cp_scales_w(sbuf + SF_V, sfv);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < nkb) {
+                        const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
+                        umma_mx_ts_w(od, sbuf + P_HI + 8 * j, vj, umma_idesc_mx_e4m3(ROWS, D, j),
+                                     sbuf + SF_P, sbuf + SF_V, (hs || j > 0) ? 1u : 0u);
+                        umma_mx_ts_w(od, sbuf + P_LO + 8 * j, vj, umma_idesc_mx_e4m3(ROWS, D, j),
+                                     sbuf + SF_P, sbuf + SF_V, 1u);
+                    }
+                umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
+                umma_commit_w(&bars[Smem::B_SFREE + s]);
+                if (s) has1 = true;
+                else has0 = true;
+                if (it + 1 < n_tiles) cur.next(s_ctx, a);
+            }
+            __syncwarp();
+            umma_commit_w(&bars[Smem::B_DRAIN + 1]);
+            if (lane == 0) mbar_drain(&bars[Smem::B_DRAIN + 1], 0);
+            __syncwarp();
+        }
+    }
+    } else if (warp >= 12) {
+        regs_dec<96>();
+        // ================= q rows to hi / lo (warps 12-15) =================
+        // Piece j into buffer j & 1 (free once the last Q K^T of piece j - 2 is
+        // done), its row exponents into stage j % 8.  16 lanes per row, 8
+        // elements each; a negative softmax scale is folded into q's sign.
+        const int w = warp - 12, half = lane >> 4, c16 = lane & 15;
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        Cursor cur;
+        bool more = n_tiles > 0;
+        if (more) cur.init(t_begin, s_pre, s_ctx, a);
+        for (int j = 0; more; ++j) {
+            if (j >= 2 && !warp_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
+                                     abort_flag, a.dev_err))
+                break;
+            uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
+            for (int r0 = w * 2; r0 < R; r0 += 8) {
+                const int r = r0 + half;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < R)
+                    v = __ldg(reinterpret_cast<const uint4*>(
+                                  q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) *
+                                          D) +
+                              c16);
+                float x[8];
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                float top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(u[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // 2^-ex takes the row's largest element into [128, 256)
+                const int ex = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
+                const float mul = sign * __uint_as_float((uint32_t)(127 - ex) << 23);
+                uint32_t hw[2], lw[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y0 = x[2 * e] * mul, y1 = x[2 * e + 1] * mul;
+                    uint16_t h, l;
+                    split_e4m3x2(y0, y1, h, l);
+                    if (e & 1) {
+                        hw[e >> 1] |= (uint32_t)h << 16;
+                        lw[e >> 1] |= (uint32_t)l << 16;
+                    } else {
+                        hw[e >> 1] = h;
+                        lw[e >> 1] = l;
+                    }
+                }
+                if (r < R) {
+                    if (c16 == 0) s_exp[(j % EXP_STAGES) * ROWS + r] = (int8_t)ex;
+#pragma unroll
+                    for (int c = 0; c < REP; ++c) {
+                        const int row = r + c * COPY;
+                        const int off = row * D + (((c16 >> 1) ^ (row & 7)) << 4) + (c16 & 1) * 8;
+                        *reinterpret_cast<uint2*>(buf + off) = make_uint2(hw[0], hw[1]);
+                        *reinterpret_cast<uint2*>(buf + Q_PART + off) = make_uint2(lw[0], lw[1]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[Smem::B_EXP + j % EXP_STAGES]);
+                mbar_arrive(&bars[Smem::B_QFULL + (j & 1)]);
+            }
+            more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
+            if (more) cur.next_segment(s_ctx, a);
+        }
+    } else {
+        regs_inc<160>();
+        // ================= softmax sets (0: warps 0-3, even tiles; 1: 8-11, odd) =================
+        const int set = warp >= 8 ? 1 : 0;
+        const int quad = warp & 3;            // TMEM lane quadrant
+        const int ln = quad * 32 + lane;      // TMEM lane of this thread
+        const int copy = ln / COPY, r = ln % COPY;
+        const bool row_valid = r < R;
+        const bool quad_active = (quad * 32) % COPY < R;
+        const int i_row = row_valid ? r / G : k - 1;
+        const int blk0 = copy * NBLK;         // the first 32-key block of this thread
+        const float sl2 = fabsf(a.scale) * kLog2e;
+        const int csh = 31 - __clz(CH);       // log2 of the keys of a chunk
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t s_mine = lane_base + set * TN;
+        const uint32_t o_mine = TM_O + set * D, o_other = TM_O + (1 - set) * D;
+        float* s_stat_m = reinterpret_cast<float*>(sm + Smem::STAT);
+        float* s_stat_l = s_stat_m + 2 * ROWS;
+        float* red = reinterpret_cast<float*>(sm + Smem::RED) + set * 4 * 32 * 16;
+        float m_ref = -INFINITY, l = 0.f;
+        float qm = 0.f;         // accumulator units to log2 units, before the page's scale
+        bool has = false;       // this set took a tile of the current piece
+        int own = 0;            // tiles this set has taken
+        int low = 0;            // first key of this row's window
+        uint64_t mrow = 0;
+        Cursor cur;
+        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, a);
+        bool ok = true;
+        int pc = -1;
+        for (int it = 0; it < n_tiles; ++it) {
+            const bool first = (it == 0) || (cur.lt == 0);
+            const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
+            const bool mine = (it & 1) == set;
+            const int ctx = s_ctx[cur.b], key0 = cur.key0();
+            if (first) {
+                ++pc;
+                m_ref = -INFINITY;
+                l = 0.f;
+                has = false;
+                const uint64_t bits = draft_bits(a, cur.b, i_row);
+                mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
+                if (WIN) low = window_low(a, ctx + draft_depth(bits));
+                if (ok)
+                    ok = warp_wait(&bars[Smem::B_EXP + pc % EXP_STAGES], (pc / EXP_STAGES) & 1,
+                                   abort_flag, a.dev_err);
+                if (ok && row_valid)
+                    qm = ldexpf(sl2, (int)s_exp[(pc % EXP_STAGES) * ROWS + r]);
+            }
+            if (mine) {
+                if (ok)
+                    ok = warp_wait(&bars[Smem::B_SCALE + it % SCALE_STAGES],
+                                   (it / SCALE_STAGES) & 1, abort_flag, a.dev_err);
+                if (ok)
+                    ok = warp_wait(&bars[Smem::B_SFULL + set], own & 1, abort_flag, a.dev_err);
+                if (ok && quad_active) {
+                    tc_fence_after();
+                    const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
+                    auto scale_of = [&](int blk, int g) { return sc[(blk * 32 + g * 16) >> csh]; };
+                    auto vis_of = [&](int blk) {
+                        return visible32<WIN>(key0 + blk * 32, ctx + k, ctx, mrow, low, a.sinks);
+                    };
+                    // largest score of the row's blocks, and of each block with
+                    // its V scales
+                    uint32_t v[REP == 1 ? 1 : NBLK][32];
+                    float wtop[NBLK];
+                    float m_new = m_ref;
+#pragma unroll
+                    for (int n = 0; n < NBLK; ++n) {
+                        const int blk = blk0 + n;
+                        uint32_t(&raw)[32] = v[REP == 1 ? 0 : n];
+                        tmem_ld32(s_mine + blk * 32, raw);
+                        tmem_wait_ld();
+                        const uint32_t vis = vis_of(blk);
+                        const float4 s0 = scale_of(blk, 0), s1 = scale_of(blk, 1);
+                        const Group g0 = group_max(raw, vis, qm * s0.x, s0);
+                        const Group g1 = group_max(raw + 16, vis >> 16, qm * s1.x, s1);
+                        m_new = fmax3(m_new, g0.top, g1.top);
+                        wtop[n] = fmaxf(g0.wtop, g1.wtop);
+                    }
+                    float alpha = 1.f;
+                    const bool move = m_new > m_ref + kRescaleThreshold;  // also -inf -> finite
+                    if (move) {
+                        alpha = (m_ref == -INFINITY) ? 0.f : fast_exp2(m_ref - m_new);
+                        m_ref = m_new;
+                        l *= alpha;
+                    }
+                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                    uint32_t sfw = 0x7f7f7f7fu;
+                    if constexpr (REP == 1) {
+                        // blocks 3 and 2 first: P hi / lo lie over their columns
+                        uint32_t hi[4][8], lo[4][8];
+                        sfw = 0;
+#pragma unroll
+                        for (int b = 3; b >= 0; --b) {
+                            tmem_ld32(s_mine + b * 32, v[0]);
+                            tmem_wait_ld();
+                            uint32_t sf;
+                            l += block_weights(v[0], vis_of(b), qm, scale_of(b, 0), scale_of(b, 1),
+                                               wtop[b], m_use, hi[b], lo[b], sf);
+                            sfw |= sf << (8 * b);
+                            if (b == 2) {
+                                tmem_st8(s_mine + P_HI + 24, hi[3]);
+                                tmem_st8(s_mine + P_LO + 24, lo[3]);
+                            }
+                            if (b <= 2) {
+                                tmem_st8(s_mine + P_HI + 8 * b, hi[b]);
+                                tmem_st8(s_mine + P_LO + 8 * b, lo[b]);
+                            }
+                        }
+                    } else {
+                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                        for (int n = 0; n < NBLK; ++n) {
+                            const int blk = blk0 + n;
+                            uint32_t hi[8], lo[8], sf;
+                            l += block_weights(v[n], vis_of(blk), qm, scale_of(blk, 0),
+                                               scale_of(blk, 1), wtop[n], m_use, hi, lo, sf);
+                            tmem_st8(s_mine + P_HI + 8 * blk, hi);
+                            tmem_st8(s_mine + P_LO + 8 * blk, lo);
+                            sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                        }
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+                            if (b / NBLK != copy) {  // the other copies' blocks
+                                tmem_st8(s_mine + P_HI + 8 * b, zero);
+                                tmem_st8(s_mine + P_LO + 8 * b, zero);
+                            }
+                    }
+                    *reinterpret_cast<uint32_t*>(sm + Smem::SFP + set * 512 + lane * 16 +
+                                                 quad * 4) = sfw;
+                    fence_proxy_async_smem();
+                    tmem_wait_st();
+                    if (has && __any_sync(0xffffffffu, move)) {
+                        // O holds every earlier P V of this set (the S buffer of
+                        // this tile was free only after the previous one read it)
+#pragma unroll
+                        for (int c4 = 0; c4 < D / 32; ++c4) {
+                            uint32_t ov[32];
+                            tmem_ld32(lane_base + o_mine + c4 * 32, ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            tmem_st32(lane_base + o_mine + c4 * 32, ov);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                // P of this tile stored (every warp of the set arrives, active or not)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[Smem::B_PREADY + set]);
+                has = true;
+                ++own;
+            }
+            if (last) {
+                // ---- epilogue of the piece that ends at this tile: merge the two
+                // sets' (and the copies') (max, sum, O); each set writes half of
+                // the output columns
+                if (ok && has)  // this set's last P V (tile own - 1) is done
+                    ok = warp_wait(&bars[Smem::B_SFREE + set], (own - 1) & 1, abort_flag,
+                                   a.dev_err);
+                tc_fence_after();
+                const int64_t tb = ld_shared_s64(s_rng), te = ld_shared_s64(s_rng + 1);
+                const bool complete = cur.seg_start >= tb && cur.seg_start + cur.nb <= te;
+                const int slot = 2 * blockIdx.x + (cur.seg_start < tb ? 0 : 1);
+                s_stat_m[set * ROWS + ln] = has ? m_ref : -INFINITY;
+                s_stat_l[set * ROWS + ln] = has ? l : 0.f;
+                tc_fence_before();
+                if (REP == 1)
+                    named_bar_sync(2 + quad, 64);  // the two sets' warps of this quadrant
+                else
+                    named_bar_sync(2, 256);
+                tc_fence_after();
+                float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2 * REP; ++c)
+                    mt = fmaxf(mt, s_stat_m[(c & 1) * ROWS + (c >> 1) * COPY + r]);
+                const float mt_use = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+                for (int c = 0; c < 2 * REP; ++c)
+                    lt += fast_exp2(s_stat_m[(c & 1) * ROWS + (c >> 1) * COPY + r] - mt_use) *
+                          s_stat_l[(c & 1) * ROWS + (c >> 1) * COPY + r];
+                const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
+                const float lse = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
+                const float wm =
+                    has ? fast_exp2(m_ref - mt_use) * inv_l : 0.f;
+                const float wo = fast_exp2(s_stat_m[(1 - set) * ROWS + ln] - mt_use) * inv_l;
+                // this lane's 16 columns from c0 on, both sets weighted
+                auto merged = [&](int c0, float (&o)[16]) {
+                    uint32_t ov[16], ow[16];
+                    tmem_ld16(lane_base + o_mine + c0, ov);
+                    tmem_ld16(lane_base + o_other + c0, ow);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        // a set without a tile of this piece holds stale O: weight 0
+                        const float a0 = wm > 0.f ? __uint_as_float(ov[e]) * wm : 0.f;
+                        const float a1 = wo > 0.f ? __uint_as_float(ow[e]) * wo : 0.f;
+                        o[e] = a0 + a1;
+                    }
+                };
+                auto row_of = [&](int rr) {
+                    return ((int64_t)cur.b * k + rr / G) * a.Hq + cur.kvh * G + rr % G;
+                };
+                if (REP == 1) {
+                    if (ok && quad_active) {
+#pragma unroll
+                        for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
+                            float o[16];
+                            merged(c0, o);
+                            if (!row_valid) continue;
+                            if (complete) {
+                                uint4* dst = reinterpret_cast<uint4*>(
+                                    static_cast<__nv_bfloat16*>(a.out) + row_of(r) * D + c0);
+#pragma unroll
+                                for (int v4 = 0; v4 < 2; ++v4)
+                                    dst[v4] = make_uint4(pack_bf16x2(o[8 * v4 + 0], o[8 * v4 + 1]),
+                                                         pack_bf16x2(o[8 * v4 + 2], o[8 * v4 + 3]),
+                                                         pack_bf16x2(o[8 * v4 + 4], o[8 * v4 + 5]),
+                                                         pack_bf16x2(o[8 * v4 + 6], o[8 * v4 + 7]));
+                            } else {
+                                float4* dst = reinterpret_cast<float4*>(
+                                    prm.part_o + ((int64_t)slot * ROWS + r) * D + c0);
+#pragma unroll
+                                for (int v4 = 0; v4 < 4; ++v4)
+                                    dst[v4] = make_float4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2],
+                                                          o[4 * v4 + 3]);
+                            }
+                        }
+                    }
+                } else {
+                    // 16 columns at a time: every copy's share to shared memory,
+                    // then the set's threads sum the copies (row t / 4 of each
+                    // 32-row group, 4 columns); 4-column groups are swizzled by
+                    // the row
+                    const int t = quad * 32 + lane, rr = t >> 2, cg = t & 3;
+                    for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
+                        if (ok && quad_active) {
+                            float o[16];
+                            merged(c0, o);
+                            float4* dst = reinterpret_cast<float4*>(red + (quad * 32 + lane) * 16);
+#pragma unroll
+                            for (int v4 = 0; v4 < 4; ++v4)
+                                dst[v4 ^ ((lane >> 1) & 3)] = make_float4(
+                                    o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+                        }
+                        named_bar_sync(3 + set, 128);
+#pragma unroll
+                        for (int rb = 0; rb < COPY / 32; ++rb) {
+                            const int row = rb * 32 + rr;
+                            if (!ok || row >= R) continue;
+                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                            for (int c = 0; c < REP; ++c) {
+                                const int qd = c * (COPY / 32) + rb;
+                                const float4 x = reinterpret_cast<const float4*>(
+                                    red + (qd * 32 + rr) * 16)[cg ^ ((rr >> 1) & 3)];
+                                acc.x += x.x;
+                                acc.y += x.y;
+                                acc.z += x.z;
+                                acc.w += x.w;
+                            }
+                            if (complete)
+                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                          row_of(row) * D + c0 + cg * 4) =
+                                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                            else
+                                *reinterpret_cast<float4*>(prm.part_o +
+                                                           ((int64_t)slot * ROWS + row) * D + c0 +
+                                                           cg * 4) = acc;
+                        }
+                        named_bar_sync(3 + set, 128);
+                    }
+                }
+                if (ok && row_valid && set == 0 && copy == 0) {
+                    if (complete) {
+                        if (a.lse) a.lse[row_of(r)] = lse;
+                    } else {
+                        prm.part_lse[(int64_t)slot * ROWS + r] = lse;
+                    }
+                }
+                // every softmax warp has read O: the next piece's P V may overwrite
+                // it, and its statistics these
+                tc_fence_before();
+                if (REP == 1)
+                    named_bar_sync(2 + quad, 64);
+                else
+                    named_bar_sync(2, 256);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[Smem::B_EPI]);
+            }
+            if (it + 1 < n_tiles) cur.next(s_ctx, a);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 4) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    }
+    return fn;
+}
+
+template <int REP, bool WIN>
+cudaError_t launch_typed(const CUtensorMap& kmap, const CUtensorMap& vmap, const F8Params& prm,
+                         int num_ctas, cudaStream_t stream) {
+    auto kern = attn_f8_kernel<REP, WIN>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(num_ctas), dim3(THREADS), SMEM_BYTES, stream, kmap, vmap,
+                            prm);
+}
+
+}  // namespace
+
+bool f8_supported(const AttnArgs& a) {
+    const int G = a.Hq / a.Hkv;
+    const bool pow2 = (a.P & (a.P - 1)) == 0;
+    return a.q_dtype == SPEC_DTYPE_BF16 && a.kv_dtype == SPEC_DTYPE_E4M3 && a.D == D &&
+           a.k * G <= ROWS && pow2 && a.P >= 16 && a.P <= 256 && a.B <= MAX_BATCH &&
+           (int64_t)a.num_pages * a.Hkv * a.P < (1LL << 31);
+}
+
+cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream) {
+    if (a.B == 0) return cudaSuccess;
+    EncodeTiledFn encode = get_encode_fn();
+    if (!encode) return cudaErrorNotSupported;
+    const int R = a.k * (a.Hq / a.Hkv);
+    // K / V as rows of 128 bytes; a box is CH = min(P, 128) rows of one page
+    CUtensorMap kmap, vmap;
+    for (int t = 0; t < 2; ++t) {
+        cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)a.num_pages * a.Hkv * a.P};
+        cuuint64_t strides[1] = {(cuuint64_t)D};
+        cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)(a.P < TN ? a.P : TN)};
+        cuuint32_t es[2] = {1, 1};
+        if (encode(t == 0 ? &kmap : &vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                   const_cast<void*>(t == 0 ? a.k_cache : a.v_cache), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    F8Params prm;
+    prm.a = a;
+    prm.part_o = static_cast<float*>(workspace);
+    prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
+    prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
+    prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
+    const int rep = R <= 32 ? 4 : R <= 64 ? 2 : 1;
+    const bool win = a.window > 0;
+    const cudaError_t e =
+        rep == 4   ? (win ? launch_typed<4, true>(kmap, vmap, prm, num_ctas, stream)
+                          : launch_typed<4, false>(kmap, vmap, prm, num_ctas, stream))
+        : rep == 2 ? (win ? launch_typed<2, true>(kmap, vmap, prm, num_ctas, stream)
+                          : launch_typed<2, false>(kmap, vmap, prm, num_ctas, stream))
+                   : (win ? launch_typed<1, true>(kmap, vmap, prm, num_ctas, stream)
+                          : launch_typed<1, false>(kmap, vmap, prm, num_ctas, stream));
+    if (e != cudaSuccess) return e;
+    return launch_combine_stream_k(a, num_ctas, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha,
+                                   prm.part_o, prm.part_lse, prm.seg_rec, prm.seg_pre, stream);
+}
+
+}  // namespace specv

@@ -210,6 +210,40 @@ __device__ __forceinline__ void tmem_cp_128x256b_w(uint32_t taddr, uint64_t sdes
         : "memory");
 }
 
+// 8-bit floating operands (K = 32 per instruction).  umma_f8_ss_w: A and B from
+// shared memory, unscaled.  umma_mx_ts_w: A from TMEM (4 elements per column)
+// with a power-of-two scale for each row and 32 elements of K: scale bytes
+// (exponent + 127) in TMEM, row r at lane r % 32, column sf_a + r / 32, the
+// byte that the instruction descriptor selects; the same for B's columns.
+__device__ __forceinline__ void umma_f8_ss_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_mx_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t sf_a, uint32_t sf_b,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "[%0], [%1], %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(sf_a), "r"(sf_b), "r"(accumulate)
+        : "memory");
+}
+// 32 rows x 16 bytes (512 contiguous bytes of shared memory) to 4 columns of
+// TMEM lanes 0..31, repeated in the other three lane quadrants: scale factors
+__device__ __forceinline__ void tmem_cp_scales_w(uint32_t taddr, uint64_t sdesc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc)
+        : "memory");
+}
+
 // 32 lanes x 32 consecutive 32-bit columns (one row per thread of the warp).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
@@ -317,6 +351,28 @@ __device__ __forceinline__ uint64_t umma_sdesc_sw128(uint32_t start, uint32_t lb
     d |= (uint64_t)1 << 46;   // descriptor version (sm_100 family)
     d |= (uint64_t)2 << 61;   // layout: 128-byte swizzle
     return d;
+}
+
+// Shared-memory matrix descriptor without a swizzle: 8-row groups of 16-byte
+// rows, `sbo` bytes apart.
+__device__ __forceinline__ uint64_t umma_sdesc_plain(uint32_t start, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((start >> 4) & 0x3FFF);
+    d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 16;
+    d |= (uint64_t)((sbo >> 4) & 0x3FFF) << 32;
+    d |= (uint64_t)1 << 46;
+    return d;
+}
+
+// Instruction descriptors of e4m3 A and B with an fp32 D: unscaled (A, B
+// K-major), and with block scales (exponent bytes; B MN-major; scale byte
+// `sf` of A's columns).
+__host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t umma_idesc_mx_e4m3(int M, int N, uint32_t sf) {
+    return (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+           (sf << 29);
 }
 
 // Register budget of the calling warpgroup (all four warps execute it): the
@@ -440,6 +496,57 @@ struct CursorT {
     }
 };
 
+// The same walk for calls that may have a sliding window (WIN): a segment's
+// tiles are those of its sinks, then those from the first query's window on
+// (window_span); lt counts them and key0() is the first key of tile lt.
+template <int TILE_KEYS, bool WIN>
+struct SegCursor {
+    int b, kvh, lt, nb;
+    int64_t seg_start;  // global index of the segment's first tile
+    WindowSpan span;
+
+    static __device__ int tiles(const AttnArgs& a, int ctx) {
+        const int all = (ctx + a.k + TILE_KEYS - 1) / TILE_KEYS;
+        return WIN ? all - window_span(a, ctx, TILE_KEYS).skip : all;
+    }
+    __device__ void enter(const AttnArgs& a, int ctx) {
+        nb = (ctx + a.k + TILE_KEYS - 1) / TILE_KEYS;
+        if (WIN) {
+            span = window_span(a, ctx, TILE_KEYS);
+            nb -= span.skip;
+        }
+    }
+    __device__ void init(int64_t t, const int* pre, const int* ctx, const AttnArgs& a) {
+        int lo = 0, hi = a.B - 1;  // largest b with pre[b]*Hkv <= t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((int64_t)pre[mid] * a.Hkv <= t) lo = mid; else hi = mid - 1;
+        }
+        b = lo;
+        enter(a, ctx[b]);
+        const int64_t off = t - (int64_t)pre[b] * a.Hkv;
+        kvh = (int)(off / nb);
+        lt = (int)(off % nb);
+        seg_start = (int64_t)pre[b] * a.Hkv + (int64_t)kvh * nb;
+    }
+    // the first tile of the next segment
+    __device__ void next_segment(const int* ctx, const AttnArgs& a) {
+        lt = 0;
+        seg_start += nb;
+        if (++kvh == a.Hkv) {
+            kvh = 0;
+            ++b;
+            enter(a, ctx[b]);
+        }
+    }
+    __device__ void next(const int* ctx, const AttnArgs& a) {
+        if (++lt == nb) next_segment(ctx, a);
+    }
+    __device__ int key0() const {
+        return (WIN && lt >= span.head ? lt + span.skip : lt) * TILE_KEYS;
+    }
+};
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -463,6 +570,11 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

@@ -131,6 +131,11 @@ cudaError_t launch_combine_stream_k(const AttnArgs& a, int num_ctas, int alpha,
 bool tc2_supported(const AttnArgs& a);
 cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);
 
+// ---- tensor-core kernel over an e4m3 cache (codes fed to the MMAs as stored;
+// same shapes as the 128-key bf16 kernel); workspace as tc_workspace_bytes ----
+bool f8_supported(const AttnArgs& a);
+cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);
+
 // ---- warp-MMA kernel for k*G <= 16 query rows (mma.sync m16n8k16, TMA pages) ----
 bool mma_supported(const AttnArgs& a);
 cudaError_t launch_attn_mma(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);

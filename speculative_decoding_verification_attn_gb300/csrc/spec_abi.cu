@@ -262,7 +262,8 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     if (rc) return rc;
 
     // kernels: 1 SIMT (chunked), 2 tcgen05 (64-key tiles), 3 warp MMA,
-    // 4 single-pass SIMT, 5 tcgen05 (128-key tiles).  Automatic: a bf16
+    // 4 single-pass SIMT, 5 tcgen05 (128-key tiles; an e4m3 cache has a kernel
+    // of its own there and takes it wherever the shape fits).  Automatic: a bf16
     // cache with head_dim 128 takes the 128-key tcgen05 kernel, except that
     // with <= 16 query rows per kv-head the warp-MMA kernel (whose pieces of
     // a split segment cost less) keeps the calls with more segments than SMs
@@ -273,7 +274,8 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     const int64_t path = g_opt_path.load();
     const bool win = window > 0;
     const bool tc_ok = !win && specv::tc_supported(a), mma_ok = !win && specv::mma_supported(a);
-    const bool tc2_ok = !win && specv::tc2_supported(a);
+    const bool f8_ok = specv::f8_supported(a);
+    const bool tc2_ok = f8_ok || (!win && specv::tc2_supported(a));
     const bool small_ok = !win && specv::small_attn_max_keys(a) > 0;
     int kernel;
     if (path == 1) kernel = 1;
@@ -286,7 +288,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     } else {
         const bool many_short = (int64_t)batch * num_kv_heads > ws->sms &&
                                 (int64_t)max_pages_per_seq * page_size < 3072;
-        const bool tc2_auto = tc2_ok && kv_dtype == SPEC_DTYPE_BF16;
+        const bool tc2_auto = tc2_ok && kv_dtype != SPEC_DTYPE_I8;
         kernel = mma_ok && (many_short || !tc2_auto) ? 3 : tc2_auto ? 5 : tc_ok ? 2 : small_ok ? 4 : 1;
     }
     if (kernel == 3 && (int64_t)batch * num_kv_heads > kMaxCounters)
@@ -307,6 +309,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
         a.seg_counters = reinterpret_cast<int*>(static_cast<char*>(ws->base) + kCountersOff);
         void* wsp = static_cast<char*>(ws->base) + kHeader;
         e = kernel == 3   ? specv::launch_attn_mma(a, ctas, wsp, st)
+            : f8_ok       ? specv::launch_attn_f8(a, ctas, wsp, st)
             : kernel == 5 ? specv::launch_attn_tc2(a, ctas, wsp, st)
                           : specv::launch_attn_tc(a, ctas, wsp, st);
         if (e != cudaSuccess) return cuda_fail(e, "verify_attn (tensor-core) launch");

@@ -75,8 +75,9 @@ def visible(ctx, k, i, mask_row, window, sinks):
 
 
 def attn64(q, kc, vc, ks, vs, table, ctx, scale, mask=None, window=0, sinks=0):
-    """out, lse, and what the tolerances need: A = sum p |v| / l per output and
-    the largest sum_d |k_d| |value| a row of queries meets."""
+    """out, lse, and what the tolerances need: A = sum p |v| / l per output (over
+    an e4m3 cache with the step of its P, see attn_bounds) and the largest
+    sum_d |k_d| a row of queries meets."""
     B, k, Hq, D = q.shape
     Hkv = kc.shape[1]
     G = Hq // Hkv
@@ -113,6 +114,9 @@ def attn64(q, kc, vc, ks, vs, table, ctx, scale, mask=None, window=0, sinks=0):
             lse[b, i] = torch.logsumexp(z, -1).reshape(Hq)
             out[b, i] = torch.einsum("hgj,jhd->hgd", p, V[at]).reshape(Hq, D)
             mag[b, i] = torch.einsum("hgj,jhd->hgd", p, V[at].abs()).reshape(Hq, D)
+            if kc.dtype == E4M3:
+                top = p.amax(-1)[..., None] * V[at].abs().sum(0)[:, None]
+                mag[b, i] += 2.0 ** -9 * top.reshape(Hq, D)
             knorm[b, i] = K[at].abs().sum(-1).amax(0).repeat_interleave(G)
     return out, lse, mag, knorm
 
@@ -121,7 +125,14 @@ def attn_bounds(q, out, mag, knorm, scale, f32=False):
     """Largest errors (out, lse) of a kernel that keeps scores, maxima, sums and
     accumulators in fp32, holds a bf16 q to 2^-18 of its row's largest element
     or better, rounds P to 8 significant bits (half a step: 2^-8) and the
-    output once.  f32: fp32 throughout (128 products of 2^-24 and expf)."""
+    output once.  f32: fp32 throughout (128 products of 2^-24 and expf).
+
+    Over an e4m3 cache P is a sum of two e4m3 values under a power of two per
+    32 keys that puts the largest of them in [128, 256).  Half of e4m3's
+    smallest step, 2^-10, is then at most 2^-17 of the block's largest p, and so
+    of the row's: each key adds up to 2^-17 max(p) |v| beside its half step of
+    2^-8 p |v|.  attn64 counts that into A as 2^-9 max(p) sum |v|, of which a
+    half step is 2^-17."""
     top = q.double().abs().amax(-1)
     z = (2.0 ** -18 * top + 256 * 2.0 ** -24 * top) * knorm * abs(scale)
     if f32:
