@@ -86,7 +86,6 @@ template <bool KV8>
 __host__ __device__ constexpr uint32_t idesc_pv() {  // B (V) MN-major
     return KV8 ? umma_idesc_f16(ROWS, D, 0, 1) : umma_idesc_bf16(ROWS, D, 0, 1);
 }
-using Cursor = CursorT<TN>;
 
 // Tiles charged per segment in the split over the CTAs: a piece boundary
 // drains the tensor-core pipeline (the next piece's queries, the merge of the
@@ -234,9 +233,10 @@ __device__ __forceinline__ void store_cols(uint32_t taddr, const uint32_t* v) {
 // O accumulator in TMEM, so that one set's barrier, TMEM and MUFU latencies
 // hide behind the other's work.  The two states of a row are merged by
 // log-sum-exp weights once per piece; each set writes half of the columns.
-template <int REP, bool KV8, bool PP>
+template <int REP, bool KV8, bool PP, bool WIN>
 __device__ void softmax_role(const Cta& x) {
     using Smem = SmemT<KV8>;
+    using Cursor = SegCursor<TN, WIN>;
     constexpr int RQ = REP == 4 ? 32 : REP == 2 ? 64 : ROWS;
     constexpr int CW = TN / REP;  // key columns of a tile owned by one thread
     const AttnArgs& a = *x.a;
@@ -271,21 +271,24 @@ __device__ void softmax_role(const Cta& x) {
     float m_ref = -INFINITY, l = 0.f;
     bool has = false;  // this set has taken a tile of the current piece
     uint64_t mrow = 0;  // draft bits of this thread's query row, per piece
+    int low = 0;        // first key of its window
     Cursor cur;
-    if (x.n_tiles > 0) cur.init(ld_shared_s64(x.rng), x.s_pre, x.s_ctx, a.B, a.Hkv, k);
+    if (x.n_tiles > 0) cur.init(ld_shared_s64(x.rng), x.s_pre, x.s_ctx, a);
     bool ok = true;
     for (int it = 0; it < x.n_tiles; ++it) {
         const bool first = (it == 0) || (cur.lt == 0);
         const bool last = (it == x.n_tiles - 1) || (cur.lt == cur.nb - 1);
         const int sb = it & 1, sq = it % NSB;  // P buffer / P V barrier, S buffer
         const bool mine = !PP || sb == set;
-        const int ctx = x.s_ctx[cur.b], L = ctx + k, key0 = cur.lt * TN;
+        const int ctx = x.s_ctx[cur.b], L = ctx + k, key0 = cur.key0();
         const int nvalid = min(TN, L - key0);
         if (first) {
             m_ref = -INFINITY;
             l = 0.f;
             has = false;
-            mrow = draft_bits(a, cur.b, i_row);
+            const uint64_t bits = draft_bits(a, cur.b, i_row);
+            mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
+            if (WIN) low = window_low(a, ctx + draft_depth(bits));
         }
         if (mine) {
             if (ok)
@@ -307,9 +310,12 @@ __device__ void softmax_role(const Cta& x) {
                 uint32_t vlo, vhi;
                 {
                     const int kc0 = key0 + cbase, nv = nvalid - cbase, nctx = ctx - kc0;
-                    const uint64_t valid = nv >= 64 ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1;
-                    const uint64_t cbits =
-                        nctx >= 64 ? ~0ull : nctx <= 0 ? 0ull : (1ull << nctx) - 1;
+                    auto below = [](int n) {
+                        return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+                    };
+                    const uint64_t valid = below(nv);
+                    uint64_t cbits = below(nctx);
+                    if (WIN) cbits &= below(a.sinks - kc0) | ~below(low - kc0);
                     const uint64_t dbits = nctx >= 64   ? 0ull
                                            : nctx >= 0  ? mrow << nctx
                                            : nctx > -64 ? mrow >> -nctx
@@ -683,7 +689,7 @@ __device__ void softmax_role(const Cta& x) {
                 }
             }
         }
-        if (it + 1 < x.n_tiles) cur.next(x.s_ctx, a.Hkv, k);
+        if (it + 1 < x.n_tiles) cur.next(x.s_ctx, a);
     }
     // every P V issued from here must finish before TMEM is released
     if (ltid < 32 && x.n_tiles > 0) {
@@ -694,11 +700,12 @@ __device__ void softmax_role(const Cta& x) {
     __syncwarp();
 }
 
-template <bool KV8>
+template <bool KV8, bool WIN>
 __global__ void __launch_bounds__(threads<KV8>(), 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, const TcParams prm) {
     using Smem = SmemT<KV8>;
+    using Cursor = SegCursor<TN, WIN>;
     constexpr int NL = Smem::NL, NM = Smem::NM;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -771,7 +778,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 c = c < 0 ? 0 : (int)(cap < 0 ? 0 : cap);
             }
             s_ctx[b] = c;
-            sum += (c + k + TN - 1) / TN;
+            sum += Cursor::tiles(a, c);
         }
         int incl = sum;
 #pragma unroll
@@ -782,7 +789,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         int run = incl - sum;
         for (int b = lo; b < hi; ++b) {
             s_pre[b] = run;
-            run += (s_ctx[b] + k + TN - 1) / TN;
+            run += Cursor::tiles(a, s_ctx[b]);
         }
         if (lane == 31) s_pre[B] = incl;
         // the CTA's tile range [t_begin, t_end), kept in shared memory so that
@@ -810,7 +817,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         int4 r0 = make_int4(0, 0, -1, 0);
         if (t_begin < T) {
             Cursor c0;
-            c0.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            c0.init(t_begin, s_pre, s_ctx, a);
             r0 = make_int4(c0.b, c0.kvh, c0.lt, c0.nb);
         }
         prm.seg_rec[2 * blockIdx.x] = r0;
@@ -834,23 +841,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const int n_own = n_tiles > pw ? (n_tiles - 1 - pw) / Smem::NPROD + 1 : 0;
         Cursor cur, ahead;
         if (n_own > 0) {
-            cur.init(t_begin + pw, s_pre, s_ctx, B, Hkv, k);
+            cur.init(t_begin + pw, s_pre, s_ctx, a);
             ahead = cur;
         }
         // from tile `from` to this warp's next one
         auto advance = [&](Cursor& c, int from) {
             for (int j = 1; j <= Smem::NPROD; ++j)
-                if (from + j < n_tiles) c.next(s_ctx, Hkv, k);
+                if (from + j < n_tiles) c.next(s_ctx, a);
         };
         const uint64_t pol = l2_policy_evict_first();
         if (lane == 0 && pw == 0) {
             prefetch_tmap(&kmap);
             prefetch_tmap(&vmap);
         }
+        // with a window: box `bx` of a tile holds a key that some query sees
+        // (page 0 is read in the place of the others; their scales become 0)
+        auto box_used = [&](const Cursor& c, int bx) {
+            const int k0 = c.key0() + bx * BH;
+            return !WIN || k0 < a.sinks || k0 + BH > window_low(a, s_ctx[c.b]);
+        };
         auto fetch_pids = [&](int slot, const Cursor& c) {
-            const int key0 = c.lt * TN;
+            const int key0 = c.key0();
             const int nvalid = min(TN, s_ctx[c.b] + k - key0);
-            if (lane * BH < nvalid)
+            if (lane * BH < nvalid && box_used(c, lane))
                 cp_async_4(&pids[slot * MAX_BOX + lane],
                            &a.block_table[(int64_t)c.b * a.max_pages + (key0 + lane * BH) / P]);
         };
@@ -873,10 +886,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
             cp_async_wait<Smem::LOOKAHEAD>();  // entries of tile `it`
             __syncwarp();
             const int* pid = pids + (q % (Smem::LOOKAHEAD + 1)) * MAX_BOX;
-            const int key0 = cur.lt * TN;
+            const int key0 = cur.key0();
             const int nvalid = min(TN, s_ctx[cur.b] + k - key0);
             const int nbox = (nvalid + BH - 1) / BH;
             auto page_of = [&](int bx) {
+                if (!box_used(cur, bx)) return 0;
                 int page = pid[bx];
                 if (page < 0 || page >= a.num_pages) {
                     raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
@@ -970,16 +984,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         // Q K^T reads (8-key groups 2 KB apart), V in the box order of P V
         // (16-key boxes 4 KB apart), both as fp16 with the 128-byte swizzle;
         // the per-key scales become fp32 rows (k pre-multiplied by
-        // scale*log2(e)), zero past the sequence end.  Whole 16-key boxes are
+        // scale*log2(e)), zero past the sequence end and between the sinks and
+        // the first query's window.  Whole 16-key boxes are
         // widened; keys past the end hold finite values that P = 0 cancels.
         const int ct = tid - 8 * 32;  // 0..127
         const float sl2 = a.scale * kLog2e;
         Cursor cur;
-        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, a);
         bool ok = true;
         for (int it = 0; it < n_tiles && ok; ++it) {
             const int s = it % NL, m = it % NM;
-            const int nvalid = min(TN, s_ctx[cur.b] + k - cur.lt * TN);
+            const int nvalid = min(TN, s_ctx[cur.b] + k - cur.key0());
             const int nbox = (nvalid + BOX_ROWS - 1) / BOX_ROWS;
             ok = warp_wait(&bars[Smem::B_KVFULL + s], (it / NL) & 1, abort_flag, a.dev_err);
             // the operand stage is free once P V of tile it - NM has finished
@@ -1027,7 +1042,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 const int j = ct & (TN - 1), which = ct >> 6;  // 0: k scales, 1: v scales
                 const __half hs =
                     reinterpret_cast<const __half*>(raw + 2 * RAW8_KV + which * TN * 2)[j];
-                const float f = j < nvalid ? __half2float(hs) * (which ? 1.f : sl2) : 0.f;
+                bool seen = j < nvalid;
+                if (WIN) {
+                    const int key = cur.key0() + j;
+                    seen = seen && (key < a.sinks || key >= window_low(a, s_ctx[cur.b]));
+                }
+                const float f = seen ? __half2float(hs) * (which ? 1.f : sl2) : 0.f;
                 reinterpret_cast<float*>(sm + Smem::SCALES + m * 2 * TN * 4)[which * TN + j] = f;
             }
             fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
@@ -1036,7 +1056,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                 mbar_arrive(&bars[Smem::B_RAWFREE + s]);
                 mbar_arrive(&bars[Smem::B_KREADY + m]);
             }
-            if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+            if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
     } else if (warp == 4) {
         // ================= Q K^T issue (warp 4) =================
@@ -1047,7 +1067,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         // piece's Q has been copied out of it into TMEM.
         if (n_tiles > 0) {
             Cursor cur;
-            cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            cur.init(t_begin, s_pre, s_ctx, a);
             int pc = -1;
             int q_issued = 0;  // pieces whose Q load has gone out
             bool ok = true;
@@ -1147,7 +1167,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                         if (lane == 0 && mbar_try_wait(&bars[Smem::B_QFREE], pc & 1)) {
                             Cursor nx = cur;
                             nx.lt = nx.nb - 1;
-                            nx.next(s_ctx, Hkv, k);
+                            nx.next(s_ctx, a);
                             issue_q(nx);
                             go = true;
                         }
@@ -1155,7 +1175,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
                     }
                     __syncwarp();
                 }
-                if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+                if (it + 1 < n_tiles) cur.next(s_ctx, a);
             }
             // an abort leaves no Q copy in flight (Q loads complete in order,
             // each issued after the previous one was waited for)
@@ -1186,20 +1206,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__
         const bool second = warp >= 8;
         if (REP == 4) {
             if (KV8) {
-                if (!second) softmax_role<4, true, false>(x);
+                if (!second) softmax_role<4, true, false, WIN>(x);
             } else {
-                softmax_role<4, false, true>(x);
+                softmax_role<4, false, true, WIN>(x);
             }
         } else if (REP == 2) {
             if (KV8) {
-                if (!second) softmax_role<2, true, false>(x);
+                if (!second) softmax_role<2, true, false, WIN>(x);
             } else {
-                softmax_role<2, false, true>(x);
+                softmax_role<2, false, true, WIN>(x);
             }
         } else if (KV8) {
-            softmax_role<1, true, false>(x);
+            softmax_role<1, true, false, WIN>(x);
         } else {
-            softmax_role<1, false, true>(x);
+            softmax_role<1, false, true, WIN>(x);
         }
     }
 
@@ -1374,13 +1394,28 @@ EncodeTiledFn get_encode_fn() {
 
 }  // namespace
 
+namespace {
+
+template <bool KV8, bool WIN>
+cudaError_t launch_typed(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         const TcParams& prm, int num_ctas, cudaStream_t stream) {
+    auto kern = attn_tc_kernel<KV8, WIN>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem_bytes<KV8>());
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(num_ctas), dim3(threads<KV8>()), smem_bytes<KV8>(), stream,
+                            qmap, kmap, vmap, prm);
+}
+
+}  // namespace
+
 bool tc_supported(const AttnArgs& a) {
     const int G = a.Hq / a.Hkv;
     const bool pow2 = (a.P & (a.P - 1)) == 0;
     // INT8 cache: the scales are fetched 16 keys (32 bytes) at a time with
     // bulk copies, which need 16-byte aligned sources
     const bool kv_ok =
-        a.kv_dtype == SPEC_DTYPE_BF16 ||
+        (a.kv_dtype == SPEC_DTYPE_BF16 && a.window <= 0) ||
         (a.kv_dtype == SPEC_DTYPE_I8 && a.k_scale && a.v_scale &&
          (reinterpret_cast<uintptr_t>(a.k_scale) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(a.v_scale) & 15) == 0);
@@ -1447,21 +1482,10 @@ cudaError_t launch_attn_tc(const AttnArgs& a, int num_ctas, void* workspace, cud
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
-    cudaError_t e;
-    if (kv8) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<true>());
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(attn_tc_kernel<true>, dim3(num_ctas), dim3(threads<true>()),
-                             smem_bytes<true>(), stream, qmap, kmap, vmap, prm);
-    } else {
-        e = cudaFuncSetAttribute(attn_tc_kernel<false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem_bytes<false>());
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(attn_tc_kernel<false>, dim3(num_ctas), dim3(threads<false>()),
-                             smem_bytes<false>(), stream, qmap, kmap, vmap, prm);
-    }
+    const cudaError_t e =
+        !kv8           ? launch_typed<false, false>(qmap, kmap, vmap, prm, num_ctas, stream)
+        : a.window > 0 ? launch_typed<true, true>(qmap, kmap, vmap, prm, num_ctas, stream)
+                       : launch_typed<true, false>(qmap, kmap, vmap, prm, num_ctas, stream);
     if (e != cudaSuccess) return e;
     return launch_combine_stream_k(a, num_ctas, split_alpha(a), prm.part_o, prm.part_lse,
                                    prm.seg_rec, prm.seg_pre, stream);

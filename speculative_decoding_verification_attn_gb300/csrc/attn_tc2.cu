@@ -38,6 +38,10 @@
 //    share a type.
 //    The 16 warps share the 64K registers of the block unevenly
 //    (setmaxnreg): softmax 160 each, issue / copy 80, dequantization 112.
+//  * A sliding window (WIN) takes the tiles of the sinks and of the keys from
+//    the first query's window on; inside them, page chunks that no query sees
+//    are not copied and their V rows are zeroed (the P V of a masked key adds
+//    0 * V).
 //  * Every mbarrier wait is bounded (1 s); a timeout sets the device error
 //    word and an abort flag, after which every role skips its remaining work
 //    (the softmax sets still pass their pairwise barriers), drains its copies
@@ -81,7 +85,7 @@ constexpr uint32_t idesc_pv() {  // B (V) MN-major
 template <bool KV8>
 constexpr int threads() { return KV8 ? 16 * 32 : 12 * 32; }
 
-using Cursor = CursorT<TN>;
+
 
 // INT8: the raw int8 tile (128 keys x 128 B = 16 KB) lands in the upper half
 // of its 32 KB operand slot and is dequantized in place
@@ -171,12 +175,16 @@ __device__ __forceinline__ float exp_pack64(const uint32_t (&v)[64], float m, ui
 }
 
 // Visible columns [c0, c0 + 64) of a 128-key tile for a query row: the
-// context keys, then the drafts of the row's bits, limited to the tile's keys.
+// context keys (with a window: the sinks and the keys from `low` on), then the
+// drafts of the row's bits, limited to the tile's keys.
+template <bool WIN>
 __device__ __forceinline__ uint64_t visible64(int key0, int c0, int nvalid, int ctx,
-                                              uint64_t mrow) {
+                                              uint64_t mrow, int low, int sinks) {
     const int kc0 = key0 + c0, nv = nvalid - c0, nctx = ctx - kc0;
-    const uint64_t valid = nv >= 64 ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1;
-    const uint64_t cbits = nctx >= 64 ? ~0ull : nctx <= 0 ? 0ull : (1ull << nctx) - 1;
+    auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+    const uint64_t valid = below(nv);
+    uint64_t cbits = below(nctx);
+    if (WIN) cbits &= below(sinks - kc0) | ~below(low - kc0);
     const uint64_t dbits = nctx >= 64    ? 0ull
                            : nctx >= 0   ? mrow << nctx
                            : nctx > -64  ? mrow >> -nctx
@@ -184,10 +192,11 @@ __device__ __forceinline__ uint64_t visible64(int key0, int c0, int nvalid, int 
     return (cbits | dbits) & valid;
 }
 
-template <bool KV8>
+template <bool KV8, bool WIN>
 __global__ void __launch_bounds__(threads<KV8>(), 1)
 attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const Tc2Params prm) {
+    using Cursor = SegCursor<TN, WIN>;
     constexpr int NT = threads<KV8>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -252,7 +261,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 c = c < 0 ? 0 : (int)(cap < 0 ? 0 : cap);
             }
             s_ctx[b] = c;
-            sum += (c + k + TN - 1) / TN;
+            sum += Cursor::tiles(a, c);
         }
         int incl = sum;
 #pragma unroll
@@ -263,7 +272,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         int run = incl - sum;
         for (int b = lo; b < hi; ++b) {
             s_pre[b] = run;
-            run += (s_ctx[b] + k + TN - 1) / TN;
+            run += Cursor::tiles(a, s_ctx[b]);
         }
         if (lane == 31) s_pre[B] = incl;
         __syncwarp();  // the prefix above, written by this warp's lanes
@@ -285,7 +294,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         int4 r0 = make_int4(0, 0, -1, 0);
         if (t_begin < T) {
             Cursor c0;
-            c0.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            c0.init(t_begin, s_pre, s_ctx, a);
             r0 = make_int4(c0.b, c0.kvh, c0.lt, c0.nb);
         }
         prm.seg_rec[2 * blockIdx.x] = r0;
@@ -298,6 +307,11 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
     // does a piece follow the one of cursor c in this CTA's range
     auto has_next_piece = [&](const Cursor& c) {
         return c.seg_start + c.nb < ld_shared_s64(s_rng + 1);
+    };
+    // with a window: page chunk `l` of a tile holds a key that some query sees
+    auto chunk_used = [&](const Cursor& c, int l) {
+        const int k0 = c.key0() + l * CH;
+        return !WIN || k0 < a.sinks || k0 + CH > window_low(a, s_ctx[c.b]);
     };
     // INT8 (16 warps on 64K registers): the softmax warpgroups take 160 each,
     // the issue / copy warpgroup gives its registers down to 80 and the
@@ -327,22 +341,22 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const int gshift = is_v ? 4 : 3;  // log2 of the rows of a group
         Cursor cur, ahead;
         if (n_tiles > 0) {
-            cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            cur.init(t_begin, s_pre, s_ctx, a);
             ahead = cur;
         }
         const uint64_t pol = l2_policy_evict_first();
         if (lane == 0) prefetch_tmap(map);
         auto fetch_pids = [&](int slot, const Cursor& c) {
-            const int key0 = c.lt * TN;
+            const int key0 = c.key0();
             const int nvalid = min(TN, s_ctx[c.b] + k - key0);
-            if (lane < NCH && lane * CH < nvalid)
+            if (lane < NCH && lane * CH < nvalid && chunk_used(c, lane))
                 cp_async_4(&pids[slot * NVB + lane],
                            &a.block_table[(int64_t)c.b * a.max_pages + (key0 + lane * CH) / P]);
         };
         for (int la = 0; la < LOOKAHEAD; ++la) {
             if (la < n_tiles) {
                 fetch_pids(la % (LOOKAHEAD + 1), ahead);
-                if (la + 1 < n_tiles) ahead.next(s_ctx, Hkv, k);
+                if (la + 1 < n_tiles) ahead.next(s_ctx, a);
             }
             cp_async_commit();
         }
@@ -351,22 +365,25 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         for (int it = 0; it < n_tiles && ok; ++it) {
             if (it + LOOKAHEAD < n_tiles) {
                 fetch_pids((it + LOOKAHEAD) % (LOOKAHEAD + 1), ahead);
-                if (it + LOOKAHEAD + 1 < n_tiles) ahead.next(s_ctx, Hkv, k);
+                if (it + LOOKAHEAD + 1 < n_tiles) ahead.next(s_ctx, a);
             }
             cp_async_commit();
             cp_async_wait<LOOKAHEAD>();  // entries of tile `it`
             __syncwarp();
             const int* pid = pids + (it % (LOOKAHEAD + 1)) * NVB;
-            const int key0 = cur.lt * TN;
+            const int key0 = cur.key0();
             const int nvalid = min(TN, s_ctx[cur.b] + k - key0);
-            const int nck = (nvalid + CH - 1) / CH;  // chunks holding keys of the tile
+            // chunks holding keys of the tile (with a window: keys some query sees)
+            const bool used = lane < (nvalid + CH - 1) / CH && chunk_used(cur, lane);
+            const int nck =
+                WIN ? __popc(__ballot_sync(0xffffffffu, used)) : (nvalid + CH - 1) / CH;
             const int s = it & 1;
             if (it >= 2) ok = warp_wait(&empty[s], ((it >> 1) - 1) & 1, abort_flag, a.dev_err);
             const uint32_t bytes = (uint32_t)(nck * CH) * (KV8 ? 128u + 2u : 256u);
             if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], bytes);
             __syncwarp();
             if (!ok) break;
-            if (lane < nck) {
+            if (used) {
                 int page = pid[lane];
                 if (page < 0 || page >= a.num_pages) {
                     raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
@@ -385,7 +402,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             }
             n_issued = it + 1;
             __syncwarp();
-            if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+            if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
         cp_async_wait<0>();
         if (!ok && lane == 0) {
@@ -399,7 +416,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         // ================= Q loads and Q K^T issue =================
         if (n_tiles > 0) {
             Cursor cur;
-            cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            cur.init(t_begin, s_pre, s_ctx, a);
             int pc = -1;                  // piece of the current tile
             int q_issued = 0;             // pieces whose Q load went out
             bool ok = true;
@@ -475,7 +492,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     umma_commit_w(&bars[Smem::B_KEMPTY + s]);
                     if (last) umma_commit_w(&bars[Smem::B_QFREE + (pc & 1)]);
                 }
-                if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+                if (it + 1 < n_tiles) cur.next(s_ctx, a);
             }
             // Q loads in flight land before the CTA exits (loads of one buffer
             // complete in order)
@@ -492,7 +509,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         // ================= P V issue =================
         if (n_tiles > 0) {
             Cursor cur;
-            cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+            cur.init(t_begin, s_pre, s_ctx, a);
             int pc = -1;
             bool ok = true;
             bool has0 = false, has1 = false;  // set 0 / 1 issued a P V in this piece
@@ -502,7 +519,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             for (int it = 0; it < n_tiles && ok; ++it) {
                 const bool first = (it == 0) || (cur.lt == 0);
                 const int s = it & 1;
-                const int nvalid = min(TN, s_ctx[cur.b] + k - cur.lt * TN);
+                const int nvalid = min(TN, s_ctx[cur.b] + k - cur.key0());
                 if (first) {
                     ++pc;
                     has0 = has1 = false;
@@ -521,18 +538,25 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 if (!ok) break;
                 const int nvb = (nvalid + 15) / 16;
                 // (INT8: the widened rows past the sequence end are finite)
-                if (!KV8 && nvalid % 16 != 0) {
-                    // keys past the sequence end that the last P V reads: zero
-                    // their V rows so that 0 * (stale or canary) never reaches O
+                // zero the V rows [r0, r1), so that 0 * (stale or canary) never reaches O
+                auto clear = [&](int r0, int r1) {
                     uint8_t* vst = sm + Smem::VS + s * SLOT_BYTES;
-                    for (int e = lane; e < (nvb * 16 - nvalid) * 16; e += 32) {
-                        const int t = nvalid + e / 16, h = (e / 8) & 1, c16 = e % 8;
+                    for (int e = lane; e < (r1 - r0) * 16; e += 32) {
+                        const int t = r0 + e / 16, h = (e / 8) & 1, c16 = e % 8;
                         *reinterpret_cast<uint4*>(vst + (t / 16) * 4096 + h * 2048 +
                                                   (t % 16) * 128 + c16 * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
+                };
+                // keys past the sequence end that the last P V reads
+                if (!KV8 && nvalid % 16 != 0) clear(nvalid, nvb * 16);
+                if (WIN) {  // keys between the sinks and the first query's window
+                    const int low = window_low(a, s_ctx[cur.b]), key0 = cur.key0();
+                    const int g0 = max(0, a.sinks >= low ? nvalid : a.sinks - key0);
+                    const int g1 = min(nvalid, low - key0);
+                    if (g0 < g1) clear(g0, g1);
                 }
                 tc_fence_after();
                 {
@@ -554,7 +578,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 }
                 if (s) has1 = true;
                 else has0 = true;
-                if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+                if (it + 1 < n_tiles) cur.next(s_ctx, a);
             }
             __syncwarp();
             umma_commit_w(&bars[Smem::B_DRAIN + 1]);
@@ -578,11 +602,11 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         const bool is_v = warp >= 14;
         const int ct = tid - (is_v ? 14 : 12) * 32;  // 0..63
         Cursor c;
-        if (n_tiles > 0) c.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+        if (n_tiles > 0) c.init(t_begin, s_pre, s_ctx, a);
         bool ok = true;
         for (int it = 0; it < n_tiles; ++it) {
             const int s = it & 1;
-            const int nvalid = min(TN, s_ctx[c.b] + k - c.lt * TN);
+            const int nvalid = min(TN, s_ctx[c.b] + k - c.key0());
             const int nch = (nvalid + CH - 1) / CH * CH * 8;  // raw 16-byte chunks loaded
             if (ok)
                 ok = warp_wait(&bars[(is_v ? Smem::B_VFULL : Smem::B_KFULL) + s], (it >> 1) & 1,
@@ -635,7 +659,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
             fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[(is_v ? Smem::B_VREADY : Smem::B_KREADY) + s]);
-            if (it + 1 < n_tiles) c.next(s_ctx, Hkv, k);
+            if (it + 1 < n_tiles) c.next(s_ctx, a);
         }
     } else {
         if constexpr (KV8) regs_inc<160>();
@@ -656,22 +680,25 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         bool has = false;       // this set took a tile of the current piece
         int own = 0;            // tiles this set has taken (its S / P V phase count)
         uint64_t mrow = 0;
+        int low = 0;            // first key of this row's window
         Cursor cur;
-        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, B, Hkv, k);
+        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, a);
         bool ok = true;
         int pc = -1;
         for (int it = 0; it < n_tiles; ++it) {
             const bool first = (it == 0) || (cur.lt == 0);
             const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
             const bool mine = (it & 1) == set;
-            const int ctx = s_ctx[cur.b], key0 = cur.lt * TN;
+            const int ctx = s_ctx[cur.b], key0 = cur.key0();
             const int nvalid = min(TN, ctx + k - key0);
             if (first) {
                 ++pc;
                 m_ref = -INFINITY;
                 l = 0.f;
                 has = false;
-                mrow = draft_bits(a, cur.b, i_row);
+                const uint64_t bits = draft_bits(a, cur.b, i_row);
+                mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
+                if (WIN) low = window_low(a, ctx + draft_depth(bits));
             }
             if (mine) {
                 if (ok)
@@ -679,12 +706,12 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 if (ok && quad_active) {
                     tc_fence_after();
                     uint32_t v[64];
-                    const uint64_t vis0 = visible64(key0, 0, nvalid, ctx, mrow);
+                    const uint64_t vis0 = visible64<WIN>(key0, 0, nvalid, ctx, mrow, low, a.sinks);
                     // row maximum over both halves; the second half stays in v
                     load64(s_mine, v);
                     const float mx0 = scale_mask64(v, sl2, vis0);
                     load64(s_mine + 64, v);
-                    const float mx1 = scale_mask64(v, sl2, visible64(key0, 64, nvalid, ctx, mrow));
+                    const float mx1 = scale_mask64(v, sl2, visible64<WIN>(key0, 64, nvalid, ctx, mrow, low, a.sinks));
                     const float m_new = fmaxf(m_ref, fmaxf(mx0, mx1));
                     float alpha = 1.f;
                     const bool move = m_new > m_ref + kRescaleThreshold;  // also -inf -> finite
@@ -804,7 +831,7 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[Smem::B_EPI]);
             }
-            if (it + 1 < n_tiles) cur.next(s_ctx, Hkv, k);
+            if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
     }
 
@@ -832,6 +859,17 @@ EncodeTiledFn get_encode_fn() {
     return fn;
 }
 
+template <bool KV8, bool WIN>
+cudaError_t launch_typed(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                         const Tc2Params& prm, int num_ctas, cudaStream_t stream) {
+    auto kern = attn_tc2_kernel<KV8, WIN>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(num_ctas), dim3(threads<KV8>()), SMEM_BYTES, stream, qmap,
+                            kmap, vmap, prm);
+}
+
 }  // namespace
 
 bool tc2_supported(const AttnArgs& a) {
@@ -841,7 +879,7 @@ bool tc2_supported(const AttnArgs& a) {
     // with bulk copies, which need 16-byte aligned sources
     const bool kv_ok =
         a.kv_dtype == SPEC_DTYPE_BF16 ||
-        (a.kv_dtype == SPEC_DTYPE_I8 && a.k_scale && a.v_scale &&
+        (a.kv_dtype == SPEC_DTYPE_I8 && a.window <= 0 && a.k_scale && a.v_scale &&
          (reinterpret_cast<uintptr_t>(a.k_scale) & 15) == 0 &&
          (reinterpret_cast<uintptr_t>(a.v_scale) & 15) == 0);
     return a.q_dtype == SPEC_DTYPE_BF16 && kv_ok && a.D == D &&
@@ -908,20 +946,10 @@ cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cu
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
-    cudaError_t e;
-    if (kv8) {
-        e = cudaFuncSetAttribute(attn_tc2_kernel<true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(attn_tc2_kernel<true>, dim3(num_ctas), dim3(threads<true>()),
-                             SMEM_BYTES, stream, qmap, kmap, vmap, prm);
-    } else {
-        e = cudaFuncSetAttribute(attn_tc2_kernel<false>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
-        if (e != cudaSuccess) return e;
-        e = launch_dependent(attn_tc2_kernel<false>, dim3(num_ctas), dim3(threads<false>()),
-                             SMEM_BYTES, stream, qmap, kmap, vmap, prm);
-    }
+    const cudaError_t e =
+        kv8            ? launch_typed<true, false>(qmap, kmap, vmap, prm, num_ctas, stream)
+        : a.window > 0 ? launch_typed<false, true>(qmap, kmap, vmap, prm, num_ctas, stream)
+                       : launch_typed<false, false>(qmap, kmap, vmap, prm, num_ctas, stream);
     if (e != cudaSuccess) return e;
     return launch_combine_stream_k(a, num_ctas, tc2_split_alpha(a), prm.part_o, prm.part_lse,
                                    prm.seg_rec, prm.seg_pre, stream);

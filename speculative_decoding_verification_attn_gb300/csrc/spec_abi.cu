@@ -273,9 +273,9 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     // kernel when a whole sequence fits its shared memory, else the chunked one
     const int64_t path = g_opt_path.load();
     const bool win = window > 0;
-    const bool tc_ok = !win && specv::tc_supported(a), mma_ok = !win && specv::mma_supported(a);
+    const bool tc_ok = specv::tc_supported(a), mma_ok = !win && specv::mma_supported(a);
     const bool f8_ok = specv::f8_supported(a);
-    const bool tc2_ok = f8_ok || (!win && specv::tc2_supported(a));
+    const bool tc2_ok = f8_ok || specv::tc2_supported(a);
     const bool small_ok = !win && specv::small_attn_max_keys(a) > 0;
     int kernel;
     if (path == 1) kernel = 1;

@@ -117,6 +117,8 @@ def attn64(q, kc, vc, ks, vs, table, ctx, scale, mask=None, window=0, sinks=0):
             if kc.dtype == E4M3:
                 top = p.amax(-1)[..., None] * V[at].abs().sum(0)[:, None]
                 mag[b, i] += 2.0 ** -9 * top.reshape(Hq, D)
+            if kc.dtype == torch.int8:
+                mag[b, i] += 2.0 ** -17 * rows(vc, None)[at].abs().sum(0).repeat_interleave(G, 0)
             knorm[b, i] = K[at].abs().sum(-1).amax(0).repeat_interleave(G)
     return out, lse, mag, knorm
 
@@ -132,7 +134,10 @@ def attn_bounds(q, out, mag, knorm, scale, f32=False):
     smallest step, 2^-10, is then at most 2^-17 of the block's largest p, and so
     of the row's: each key adds up to 2^-17 max(p) |v| beside its half step of
     2^-8 p |v|.  attn64 counts that into A as 2^-9 max(p) sum |v|, of which a
-    half step is 2^-17."""
+    half step is 2^-17.  Over an i8 cache P is p times the key's scale in fp16,
+    half of whose smallest step is 2^-25: each key adds up to 2^-25 |code| / l,
+    with l >= 1 (a term of the row's maximum is at least 1); attn64 counts
+    2^-17 sum |code| into A."""
     top = q.double().abs().amax(-1)
     z = (2.0 ** -18 * top + 256 * 2.0 ** -24 * top) * knorm * abs(scale)
     if f32:
