@@ -6,7 +6,7 @@
 // Mathematics.  Key j of page g has K_j = sk_g c_j, V_j = sv_g d_j with e4m3
 // codes c, d.  For a query row q (times the softmax scale):
 //   s_j = sk_g <q, c_j>,   out = sum_j p_j sv_g d_j / sum_j p_j,  p_j = 2^(s_j - m)
-// in log2 units, m the running maximum.  Both products take 8-bit operands:
+// in log2 units, for any reference m.  Both products take 8-bit operands:
 //  * q = 2^e (hi + lo): hi is q 2^-e rounded to e4m3 and lo the rest rounded
 //    to e4m3, with 2^e chosen per row so that the largest element lies in
 //    [128, 256).  A bf16 has 8 significant bits and each part holds 4, so
@@ -21,7 +21,10 @@
 //    most of the weight does not flush the thousands of light ones behind it,
 //    which a P in e4m3 under one scale per row would.  sv_g enters as
 //    log2(sv_g) in the exponent; the row sum takes each 16-key group's sum of w
-//    back by 1 / sv_g, in fp32.
+//    back by 1 / sv_g, in fp32.  And since the block scales carry the distance
+//    to the reference, m need not be the running maximum: it is a whole number
+//    near the first block's, moved only when a block exceeds it by 2^40, so one
+//    pass over a tile's scores does (its blocks' maxima come with their load).
 //
 // What bounds it: the bytes of the cache (32 KB per 128 keys and kv-head), with
 // the tensor pipe close behind: 8 + 8 MMAs of M128 N128 K32 per 128-key tile
@@ -32,8 +35,8 @@
 // Layout.  Persistent grid, the tile list split as in the 128-key bf16 kernel
 // (TileSplit, partials merged by the combine kernel).
 //  * TMEM: S of set 0 [0,128), of set 1 [128,256), O of set 0 [256,384), of set
-//    1 [384,512).  P hi / lo go over S columns [64,96) / [96,128), the scale
-//    bytes of P and of V (all one) over [0,4) / [4,8).
+//    1 [384,512).  P goes over S columns [64,128) (p_col), the scale bytes of P
+//    and of V (all one) over [0,4) / [4,8).
 //  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
 //    and 6 TMA of K and of V (5 also brings the page scales); 7 P V issue;
 //    12-15 turn the q rows of the next piece into hi / lo.  16 warps share the
@@ -74,10 +77,12 @@ constexpr int EXP_STAGES = 8;
 constexpr int MAX_BATCH = 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_O = 256;
-constexpr uint32_t P_HI = 64, P_LO = 96, SF_P = 0, SF_V = 4;  // inside an S buffer
+constexpr uint32_t SF_P = 0, SF_V = 4;  // columns of the scale bytes inside an S buffer
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// the reference moves when a block's largest w exceeds it by more than this
+// (log2 units): the block scales carry any distance below, fp32 sums this one
+constexpr float kMoveThreshold = 40.f;
 constexpr int kSplitAlpha = 3;             // tiles charged per segment in the split
 
 struct Smem {
@@ -143,42 +148,12 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint16_t& hi, uin
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(rest));
 }
 
-// One 16-key group of a row: its page's {sk, log2 sv, 1 / sv, on}
-struct Group {
-    float top;  // largest visible score (log2 units), -inf if none
-    float wtop; // top + log2 sv
-};
-
-// Largest visible score of a 16-key group (raw accumulators, mult > 0 to log2
-// units; bits: its visible keys).
-__device__ __forceinline__ Group group_max(const uint32_t* r, uint32_t bits, float mult,
-                                           const float4& sc) {
-    float m0 = -INFINITY, m1 = -INFINITY;
-    if ((bits & 0xffffu) == 0xffffu) {
-#pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-            m0 = fmax3(m0, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-            m1 = fmax3(m1, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-            if ((bits >> c) & 1u) m0 = fmaxf(m0, __uint_as_float(r[c]));
-    }
-    const float m = fmaxf(m0, m1);
-    Group g;
-    g.top = m == -INFINITY ? m : m * mult;
-    g.wtop = m == -INFINITY ? m : g.top + sc.y;
-    return g;
-}
-
-// w = 2^(raw mult + bias) of a 16-key group to hi / lo words (4 codes each);
+// w = 2^(raw mult + bias) of a 16-key group as hi / lo words (4 codes each);
 // returns the sum of w.
-__device__ __forceinline__ float group_weights(const uint32_t* r, uint32_t bits, float mult,
-                                               float bias, bool on, uint32_t* hi, uint32_t* lo) {
+__device__ __forceinline__ float group_weights(const uint32_t (&r)[16], float mult, float bias,
+                                               bool on, uint32_t* hi, uint32_t* lo) {
     const uint64_t mm = f2(mult, mult), bb = f2(bias, bias);
     uint64_t sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-    const bool all = (bits & 0xffffu) == 0xffffu;
 #pragma unroll
     for (int c = 0; c < 16; c += 4) {
         uint16_t h[2], l[2];
@@ -188,17 +163,17 @@ __device__ __forceinline__ float group_weights(const uint32_t* r, uint32_t bits,
             f2_split(f2_fma(f2(__uint_as_float(r[c + 2 * e]), __uint_as_float(r[c + 2 * e + 1])),
                             mm, bb),
                      x0, x1);
-            if (!all) {
-                x0 = (bits >> (c + 2 * e)) & 1u ? x0 : -INFINITY;
-                x1 = (bits >> (c + 2 * e + 1)) & 1u ? x1 : -INFINITY;
-            }
             x0 = fast_exp2(x0);
             x1 = fast_exp2(x1);
             sum[e] = f2_add(sum[e], f2(x0, x1));
             split_e4m3x2(x0, x1, h[e], l[e]);
         }
-        hi[c / 4] = on ? (uint32_t)h[0] | ((uint32_t)h[1] << 16) : 0u;
-        lo[c / 4] = on ? (uint32_t)l[0] | ((uint32_t)l[1] << 16) : 0u;
+        hi[c / 4] = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
+        lo[c / 4] = (uint32_t)l[0] | ((uint32_t)l[1] << 16);
+    }
+    if (!on) {  // a page of zero scale: its keys count, its values do not
+#pragma unroll
+        for (int c = 0; c < 4; ++c) hi[c] = lo[c] = 0;
     }
     float a0, a1, b0, b1;
     f2_split(sum[0], a0, a1);
@@ -206,27 +181,14 @@ __device__ __forceinline__ float group_weights(const uint32_t* r, uint32_t bits,
     return (a0 + b0) + (a1 + b1);
 }
 
-// Power of two of a 32-key block: floor(log2) of its largest w against the
-// reference, in the exponent byte's range with room for the split's 2^7.
-__device__ __forceinline__ float block_power(float wtop, float m) {
-    return wtop == -INFINITY ? 0.f : fminf(fmaxf(floorf(wtop - m), -110.f), 110.f);
+// 2^-d for a whole d >= 0 (0 from 2^-127 on).
+__device__ __forceinline__ float pow2_neg(int d) {
+    return d > 126 ? 0.f : __uint_as_float((uint32_t)(127 - d) << 23);
 }
 
-// One 32-key block of a row: hi / lo words, the scale byte and its part of the
-// row sum (two 16-key groups with scales s0, s1).
-__device__ __forceinline__ float block_weights(const uint32_t* r, uint32_t vis, float qm,
-                                               const float4& s0, const float4& s1, float wtop,
-                                               float m, uint32_t* hi, uint32_t* lo,
-                                               uint32_t& sf) {
-    const float n = block_power(wtop, m);
-    sf = (uint32_t)(120 + (int)n);  // exponent byte of 2^(n - 7)
-    const float base = 7.f - n - m;
-    const float w0 = group_weights(r, vis, qm * s0.x, base + s0.y, s0.w != 0.f, hi, lo);
-    const float w1 = group_weights(r + 16, vis >> 16, qm * s1.x, base + s1.y, s1.w != 0.f, hi + 4,
-                                   lo + 4);
-    const float sum = (w0 > 0.f ? w0 * s0.z : 0.f) + (w1 > 0.f ? w1 * s1.z : 0.f);
-    return sum * __uint_as_float(sf << 23);
-}
+// P of 32-key block b (16 columns: hi, lo) inside the S buffer: over the raw
+// scores of a block that comes before it (blocks are taken from 3 down to 0).
+__device__ __forceinline__ uint32_t p_col(int b) { return 64 + (b >> 1) * 32 + (b & 1 ? 0 : 16); }
 
 template <int REP, bool WIN>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -444,7 +406,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (lane < MAX_CHUNKS) {
                     const float* r = raw + (it % RAW_STAGES) * 2 * MAX_CHUNKS;
                     const float sv = r[MAX_CHUNKS + lane];
-                    const bool on = sv > 0.f;
+                    const bool on = sv > 1e-30f;
                     s_scale[(it % SCALE_STAGES) * MAX_CHUNKS + lane] =
                         make_float4(r[lane], on ? __log2f(sv) : 0.f, on ? 1.f / sv : 1.f,
                                     on ? 1.f : 0.f);
@@ -572,9 +534,9 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 for (int j = 0; j < 4; ++j)
                     if (j < nkb) {
                         const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
-                        umma_mx_ts_w(od, sbuf + P_HI + 8 * j, vj, umma_idesc_mx_e4m3(ROWS, D, j),
+                        umma_mx_ts_w(od, sbuf + p_col(j), vj, umma_idesc_mx_e4m3(ROWS, D, j),
                                      sbuf + SF_P, sbuf + SF_V, (hs || j > 0) ? 1u : 0u);
-                        umma_mx_ts_w(od, sbuf + P_LO + 8 * j, vj, umma_idesc_mx_e4m3(ROWS, D, j),
+                        umma_mx_ts_w(od, sbuf + p_col(j) + 8, vj, umma_idesc_mx_e4m3(ROWS, D, j),
                                      sbuf + SF_P, sbuf + SF_V, 1u);
                     }
                 umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
@@ -682,7 +644,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         float* s_stat_m = reinterpret_cast<float*>(sm + Smem::STAT);
         float* s_stat_l = s_stat_m + 2 * ROWS;
         float* red = reinterpret_cast<float*>(sm + Smem::RED) + set * 4 * 32 * 16;
-        float m_ref = -INFINITY, l = 0.f;
+        float m_ref = -INFINITY, l = 0.f;  // reference (whole), row sum against it
         float qm = 0.f;         // accumulator units to log2 units, before the page's scale
         bool has = false;       // this set took a tile of the current piece
         int own = 0;            // tiles this set has taken
@@ -720,76 +682,68 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (ok && quad_active) {
                     tc_fence_after();
                     const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
-                    auto scale_of = [&](int blk, int g) { return sc[(blk * 32 + g * 16) >> csh]; };
-                    auto vis_of = [&](int blk) {
-                        return visible32<WIN>(key0 + blk * 32, ctx + k, ctx, mrow, low, a.sinks);
-                    };
-                    // largest score of the row's blocks, and of each block with
-                    // its V scales
-                    uint32_t v[REP == 1 ? 1 : NBLK][32];
-                    float wtop[NBLK];
-                    float m_new = m_ref;
-#pragma unroll
-                    for (int n = 0; n < NBLK; ++n) {
-                        const int blk = blk0 + n;
-                        uint32_t(&raw)[32] = v[REP == 1 ? 0 : n];
-                        tmem_ld32(s_mine + blk * 32, raw);
-                        tmem_wait_ld();
-                        const uint32_t vis = vis_of(blk);
-                        const float4 s0 = scale_of(blk, 0), s1 = scale_of(blk, 1);
-                        const Group g0 = group_max(raw, vis, qm * s0.x, s0);
-                        const Group g1 = group_max(raw + 16, vis >> 16, qm * s1.x, s1);
-                        m_new = fmax3(m_new, g0.top, g1.top);
-                        wtop[n] = fmaxf(g0.wtop, g1.wtop);
-                    }
-                    float alpha = 1.f;
-                    const bool move = m_new > m_ref + kRescaleThreshold;  // also -inf -> finite
-                    if (move) {
-                        alpha = (m_ref == -INFINITY) ? 0.f : fast_exp2(m_ref - m_new);
-                        m_ref = m_new;
-                        l *= alpha;
-                    }
-                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                    uint32_t sfw = 0x7f7f7f7fu;
-                    if constexpr (REP == 1) {
-                        // blocks 3 and 2 first: P hi / lo lie over their columns
-                        uint32_t hi[4][8], lo[4][8];
-                        sfw = 0;
-#pragma unroll
-                        for (int b = 3; b >= 0; --b) {
-                            tmem_ld32(s_mine + b * 32, v[0]);
+                    // a tile's edge: invisible keys' scores become -inf where they are
+                    const bool full = key0 + TN <= ctx &&
+                                      (!WIN || key0 >= low || key0 + TN <= a.sinks);
+                    if (__any_sync(0xffffffffu, !full)) {
+#pragma unroll 1
+                        for (int blk = blk0; blk < blk0 + NBLK; ++blk) {
+                            uint32_t raw[32];
+                            tmem_ld32(s_mine + blk * 32, raw);
+                            const uint32_t vis = visible32<WIN>(key0 + blk * 32, ctx + k, ctx,
+                                                                mrow, low, a.sinks);
                             tmem_wait_ld();
-                            uint32_t sf;
-                            l += block_weights(v[0], vis_of(b), qm, scale_of(b, 0), scale_of(b, 1),
-                                               wtop[b], m_use, hi[b], lo[b], sf);
-                            sfw |= sf << (8 * b);
-                            if (b == 2) {
-                                tmem_st8(s_mine + P_HI + 24, hi[3]);
-                                tmem_st8(s_mine + P_LO + 24, lo[3]);
-                            }
-                            if (b <= 2) {
-                                tmem_st8(s_mine + P_HI + 8 * b, hi[b]);
-                                tmem_st8(s_mine + P_LO + 8 * b, lo[b]);
-                            }
-                        }
-                    } else {
-                        const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                        for (int n = 0; n < NBLK; ++n) {
-                            const int blk = blk0 + n;
-                            uint32_t hi[8], lo[8], sf;
-                            l += block_weights(v[n], vis_of(blk), qm, scale_of(blk, 0),
-                                               scale_of(blk, 1), wtop[n], m_use, hi, lo, sf);
-                            tmem_st8(s_mine + P_HI + 8 * blk, hi);
-                            tmem_st8(s_mine + P_LO + 8 * blk, lo);
-                            sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                            for (int c = 0; c < 32; ++c)
+                                if (!((vis >> c) & 1u)) raw[c] = __float_as_uint(-INFINITY);
+                            tmem_st32(s_mine + blk * 32, raw);
                         }
+                        tmem_wait_st();
+                    }
+                    uint32_t sfw = 0x7f7f7f7fu;  // scale bytes of this lane's blocks
+                    float alpha = 1.f;           // what a moved reference takes off O
+                    bool move = false;
+#pragma unroll 1
+                    for (int blk = blk0 + NBLK - 1; blk >= blk0; --blk) {
+                        uint32_t r0[16], r1[16], pw[16];
+                        float x0, x1;
+                        tmem_ld16_max(s_mine + blk * 32, r0, x0);
+                        tmem_ld16_max(s_mine + blk * 32 + 16, r1, x1);
+                        const float4 s0 = sc[(blk * 32) >> csh], s1 = sc[(blk * 32 + 16) >> csh];
+                        // to log2 units; not 0, so that -inf stays -inf
+                        const float mu0 = fmaxf(qm * s0.x, 1.2e-38f);
+                        const float mu1 = fmaxf(qm * s1.x, 1.2e-38f);
+                        tmem_wait_ld();
+                        // whole power of two of the block's largest w (-inf: no key)
+                        const float top =
+                            floorf(fmaxf(fmaf(x0, mu0, s0.y), fmaf(x1, mu1, s1.y)));
+                        if (top > m_ref + kMoveThreshold) {  // also -inf -> finite
+                            const int d = (int)fminf(top - m_ref, 255.f);
+                            move = true;
+                            alpha *= pow2_neg(d);
+                            l *= pow2_neg(d);
+                            m_ref = top;
 #pragma unroll
+                            for (int b = 0; b < 32; b += 8)  // blocks of this tile so far
+                                sfw = (sfw & ~(0xffu << b)) |
+                                      (uint32_t)max((int)((sfw >> b) & 0xffu) - d, 0) << b;
+                        }
+                        const float n = fmaxf(top - m_ref, -110.f);  // (NaN without a key: -110)
+                        const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
+                        const float base = top == -INFINITY ? 0.f : 7.f - (m_ref + n);
+                        const float w0 =
+                            group_weights(r0, mu0, base + s0.y, s0.w != 0.f, pw, pw + 8);
+                        const float w1 =
+                            group_weights(r1, mu1, base + s1.y, s1.w != 0.f, pw + 4, pw + 12);
+                        l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
+                        sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                        tmem_st16(s_mine + p_col(blk), pw);
+                    }
+                    if (REP > 1) {  // the blocks of the other copies
+                        const uint32_t zero[16] = {};
+#pragma unroll 1
                         for (int b = 0; b < 4; ++b)
-                            if (b / NBLK != copy) {  // the other copies' blocks
-                                tmem_st8(s_mine + P_HI + 8 * b, zero);
-                                tmem_st8(s_mine + P_LO + 8 * b, zero);
-                            }
+                            if (b / NBLK != copy) tmem_st16(s_mine + p_col(b), zero);
                     }
                     *reinterpret_cast<uint32_t*>(sm + Smem::SFP + set * 512 + lane * 16 +
                                                  quad * 4) = sfw;
@@ -798,7 +752,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (has && __any_sync(0xffffffffu, move)) {
                         // O holds every earlier P V of this set (the S buffer of
                         // this tile was free only after the previous one read it)
-#pragma unroll
+#pragma unroll 1
                         for (int c4 = 0; c4 < D / 32; ++c4) {
                             uint32_t ov[32];
                             tmem_ld32(lane_base + o_mine + c4 * 32, ov);
@@ -870,7 +824,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 };
                 if (REP == 1) {
                     if (ok && quad_active) {
-#pragma unroll
+#pragma unroll 1
                         for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
                             float o[16];
                             merged(c0, o);
@@ -900,6 +854,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     // 32-row group, 4 columns); 4-column groups are swizzled by
                     // the row
                     const int t = quad * 32 + lane, rr = t >> 2, cg = t & 3;
+#pragma unroll 1
                     for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
                         if (ok && quad_active) {
                             float o[16];
