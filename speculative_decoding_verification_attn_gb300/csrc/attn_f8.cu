@@ -38,9 +38,9 @@
 //    1 [384,512).  P goes over S columns [64,128) (p_col), the scale bytes of P
 //    and of V (all one) over [0,4) / [4,8).
 //  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
-//    and 6 TMA of K and of V (5 also brings the page scales); 7 P V issue;
-//    12-15 turn the q rows of the next piece into hi / lo.  16 warps share the
-//    block's 64K registers (setmaxnreg: 160, 96, 160, 96).
+//    and 6 TMA of K and of V; 7 P V issue; 12-14 turn the q rows of the next
+//    piece into hi / lo; 15 brings the page scales.  16 warps share the block's
+//    64K registers (setmaxnreg: 160, 96, 160, 96).
 //  * Rows: R = k * G query rows are the M side of one MMA.  R <= 64 (REP 2) and
 //    R <= 32 (REP 4): the rows stand REP times and copy c takes the 32-key
 //    blocks of its own, with P zero elsewhere, so that every softmax thread
@@ -64,13 +64,13 @@ constexpr int Q_PART = ROWS * D;       // 16 KB: hi or lo of one piece's rows
 constexpr int SLOT_BYTES = TN * D;     // 16 KB: one tile of K or of V
 constexpr int SLOTS = 4;               // of K and of V each
 constexpr int MAX_CHUNKS = TN / 16;    // page chunks per tile
-constexpr int LOOKAHEAD = 6;           // tiles of block-table entries prefetched
-constexpr int SCALE_AHEAD = 3;         // tiles of page scales prefetched
-constexpr int RAW_STAGES = SCALE_AHEAD + 1;
-// scale stages: tile j + SCALE_AHEAD is fetched once Q K^T of tile j - SLOTS is
-// done, which waited for the softmax of tile j - SLOTS - 3 or later
-constexpr int SCALE_STAGES = 16;
-static_assert(SCALE_STAGES > SCALE_AHEAD + SLOTS + 3, "a stage would be overwritten unread");
+constexpr int LOOKAHEAD = 7;           // tiles of block-table entries prefetched
+constexpr int PID_STAGES = LOOKAHEAD + 1;
+// the scale warp takes two tiles at a time (16 lanes each): its block-table
+// entries come SCALE_PAIRS + 2 pairs ahead, the scales SCALE_PAIRS ahead
+constexpr int SCALE_PAIRS = 2;
+constexpr int RAW_STAGES = 4;          // pairs of tiles
+constexpr int SCALE_STAGES = 16;       // tiles
 // row exponents: the q rows of piece j are written when Q K^T of piece j - 2
 // is done; a softmax set may then still be at piece j - 4
 constexpr int EXP_STAGES = 8;
@@ -98,12 +98,15 @@ struct Smem {
                          B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + 2,
                          B_SFREE = B_PREADY + 2, B_EPI = B_SFREE + 2, B_DRAIN = B_EPI + 1,
                          B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
-                         NUM_BARS = B_SCALE + SCALE_STAGES;
+                         B_SCFREE = B_SCALE + SCALE_STAGES, NUM_BARS = B_SCFREE + SCALE_STAGES;
     static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
-    static constexpr int STAT = MISC + 32;            // (m, l) of [set][lane]
-    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;  // [2 producers][LOOKAHEAD+1][8] int
-    static constexpr int RAW = PIDS + 2 * (LOOKAHEAD + 1) * MAX_CHUNKS * 4;  // [stage][k, v][8]
-    static constexpr int EXPS = RAW + RAW_STAGES * 2 * MAX_CHUNKS * 4;       // [stage][row] int8
+    static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
+    static constexpr int STAT = FIRST + 48;           // (m, l) of [set][lane]
+    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;  // [2 producers][PID_STAGES][8] int
+    // scale warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8] scales
+    static constexpr int SPIDS = PIDS + 2 * PID_STAGES * MAX_CHUNKS * 4;
+    static constexpr int RAW = SPIDS + RAW_STAGES * 2 * MAX_CHUNKS * 4;
+    static constexpr int EXPS = RAW + RAW_STAGES * 4 * MAX_CHUNKS * 4;  // [stage][row] int8
     static constexpr int SCALE = EXPS + EXP_STAGES * ROWS;  // [stage][8] {sk, log2 sv, 1/sv, on}
     static constexpr int CTX = SCALE + SCALE_STAGES * MAX_CHUNKS * 16;
     static constexpr int PRE = CTX + MAX_BATCH * 4;
@@ -120,6 +123,27 @@ struct F8Params {
     int4* seg_rec;    // [C][2]
     int* seg_pre;     // [B+1]
 };
+
+// warp_wait in fewer instructions.  Five roles of different code share each
+// SM's instruction caches, so what the hot loops hold counts: the same softmax
+// beside 8 KB more code in other roles ran up to 15 % slower.
+__device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity,
+                                          volatile int* abort_flag, int* dev_err) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = globaltimer_ns();
+    bool late;
+    do {
+        if (__all_sync(kAll, mbar_try_wait(bar, parity))) return true;
+        late = globaltimer_ns() - t0 > kWaitLimitNs;
+    } while (!__any_sync(kAll, late || *abort_flag != 0));
+    if (late) {
+        *abort_flag = 1;
+        raise_device_error(dev_err, SPEC_DEVERR_TIMEOUT);
+    }
+    __syncwarp();
+    return false;
+}
 
 // Keys [k0, k0 + 32) that a query row sees: the context (with a window: the
 // sinks and the keys from `low` on), then the drafts of the row's bits, up to
@@ -195,6 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const F8Params prm) {
     using Cursor = SegCursor<TN, WIN>;
+    static_assert(sizeof(Cursor) <= 48, "the first cursor's place");
     constexpr int NBLK = 4 / REP;        // 32-key blocks of a softmax thread
     constexpr int COPY = ROWS / REP;     // lanes of one copy of the rows
     extern __shared__ uint8_t smem_raw[];
@@ -207,12 +232,14 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     int64_t* s_rng = reinterpret_cast<int64_t*>(sm + Smem::MISC + 16);
     int* s_ctx = reinterpret_cast<int*>(sm + Smem::CTX);
     int* s_pre = reinterpret_cast<int*>(sm + Smem::PRE);
+    Cursor* s_first = reinterpret_cast<Cursor*>(sm + Smem::FIRST);  // of tile t_begin
     float4* s_scale = reinterpret_cast<float4*>(sm + Smem::SCALE);
     int8_t* s_exp = reinterpret_cast<int8_t*>(sm + Smem::EXPS);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.B, k = a.k, Hkv = a.Hkv, G = a.Hq / a.Hkv, R = k * G, P = a.P;
-    const int CH = P < TN ? P : TN;      // keys per page chunk (a power of two)
+    const int CH = P < TN ? P : TN;      // keys per page chunk
+    const int lgP = 31 - __clz(P), lgCH = 31 - __clz(CH);  // both powers of two
 
     if (tid == 0) {
         for (int s = 0; s < SLOTS; ++s) {
@@ -222,15 +249,18 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             mbar_init(&bars[Smem::B_VEMPTY + s], 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&bars[Smem::B_QFULL + s], 4);   // the 4 converting warps
+            mbar_init(&bars[Smem::B_QFULL + s], 3);   // the 3 converting warps
             mbar_init(&bars[Smem::B_QFREE + s], 1);
             mbar_init(&bars[Smem::B_SFULL + s], 1);
             mbar_init(&bars[Smem::B_PREADY + s], 4);  // the 4 warps of the set
             mbar_init(&bars[Smem::B_SFREE + s], 1);
             mbar_init(&bars[Smem::B_DRAIN + s], 1);
         }
-        for (int s = 0; s < EXP_STAGES; ++s) mbar_init(&bars[Smem::B_EXP + s], 4);
-        for (int s = 0; s < SCALE_STAGES; ++s) mbar_init(&bars[Smem::B_SCALE + s], 1);
+        for (int s = 0; s < EXP_STAGES; ++s) mbar_init(&bars[Smem::B_EXP + s], 3);
+        for (int s = 0; s < SCALE_STAGES; ++s) {
+            mbar_init(&bars[Smem::B_SCALE + s], 1);
+            mbar_init(&bars[Smem::B_SCFREE + s], 4);  // the 4 warps of a set
+        }
         mbar_init(&bars[Smem::B_EPI], 8);  // every softmax warp, once per piece
         *abort_flag = 0;
         fence_mbar_init();
@@ -280,7 +310,9 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (lane < 2) {
             TileSplit split;
             split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
-            s_rng[lane] = split.begin(blockIdx.x + lane);
+            const int64_t t = split.begin(blockIdx.x + lane);
+            s_rng[lane] = t;
+            if (lane == 0 && t < (int64_t)s_pre[B] * Hkv) s_first->init(t, s_pre, s_ctx, a);
         }
     }
     tc_fence_before();
@@ -293,11 +325,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (tid == 0) {
         // the segment holding tile t_begin and t_begin itself, for the combine
         int4 r0 = make_int4(0, 0, -1, 0);
-        if (t_begin < T) {
-            Cursor c0;
-            c0.init(t_begin, s_pre, s_ctx, a);
-            r0 = make_int4(c0.b, c0.kvh, c0.lt, c0.nb);
-        }
+        if (t_begin < T) r0 = make_int4(s_first->b, s_first->kvh, s_first->lt, s_first->nb);
         prm.seg_rec[2 * blockIdx.x] = r0;
         prm.seg_rec[2 * blockIdx.x + 1] =
             make_int4((int)(t_begin & 0xffffffff), (int)(t_begin >> 32), 0, 0);
@@ -305,68 +333,45 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (blockIdx.x == 0)
         for (int b = tid; b <= B; b += THREADS) prm.seg_pre[b] = s_pre[b];
 
+    auto start_at = [&](Cursor& c) { c = *s_first; };
     // the page chunk `l` of a tile holds a key that some query sees
     auto chunk_used = [&](const Cursor& c, int l) {
-        const int k0 = c.key0() + l * CH, end = s_ctx[c.b] + k;
-        if (l * CH >= TN || k0 >= end) return false;
+        const int k0 = c.key0() + (l << lgCH), end = s_ctx[c.b] + k;
+        if ((l << lgCH) >= TN || k0 >= end) return false;
         return !WIN || k0 < a.sinks || k0 + CH > window_low(a, s_ctx[c.b]);
     };
 
     if (warp >= 4 && warp < 8) {
     regs_dec<96>();
     if (warp == 5 || warp == 6) {
-        // ================= TMA producers: warp 5 K and scales, warp 6 V =================
+        // ================= TMA producers: warp 5 K, warp 6 V =================
         // Tile it goes to slot it % SLOTS of its ring; each page chunk (CH
         // keys of 128 bytes, swizzled by the copy) is one copy.  Block-table
-        // entries are prefetched LOOKAHEAD tiles ahead, and the K warp brings
-        // the chunks' scales SCALE_AHEAD tiles ahead and hands them to the
-        // softmax as {sk, log2 sv, 1 / sv, sv != 0}.
+        // entries are prefetched LOOKAHEAD tiles ahead.  One warp's latency per
+        // iteration is what a tile can cost here, so the loop does no more.
         const bool is_v = warp == 6;
-        int* pids = reinterpret_cast<int*>(sm + Smem::PIDS) +
-                    (is_v ? 1 : 0) * (LOOKAHEAD + 1) * MAX_CHUNKS;
-        float* raw = reinterpret_cast<float*>(sm + Smem::RAW);
+        int* pids = reinterpret_cast<int*>(sm + Smem::PIDS) + (is_v ? PID_STAGES * MAX_CHUNKS : 0);
         uint64_t* full = &bars[is_v ? Smem::B_VFULL : Smem::B_KFULL];
         uint64_t* empty = &bars[is_v ? Smem::B_VEMPTY : Smem::B_KEMPTY];
-        uint8_t* ring = sm + (is_v ? Smem::VS : Smem::KS);
+        uint8_t* ring = sm + (is_v ? Smem::VS : Smem::KS) + ((lane << lgCH) * D);
         const CUtensorMap* map = is_v ? &vmap : &kmap;
-        Cursor cur, mid, ahead;
+        Cursor cur, ahead;
         if (n_tiles > 0) {
-            cur.init(t_begin, s_pre, s_ctx, a);
-            mid = ahead = cur;
+            start_at(cur);
+            ahead = cur;
         }
         const uint64_t pol = l2_policy_evict_first();
         if (lane == 0) prefetch_tmap(map);
-        auto fetch_pids = [&](int slot, const Cursor& c) {
+        auto fetch_pids = [&](int t, const Cursor& c) {
             if (lane < MAX_CHUNKS && chunk_used(c, lane))
-                cp_async_4(&pids[slot * MAX_CHUNKS + lane],
-                           &a.block_table[(int64_t)c.b * a.max_pages + (c.key0() + lane * CH) / P]);
+                cp_async_4(&pids[(t % PID_STAGES) * MAX_CHUNKS + lane],
+                           &a.block_table[(int64_t)c.b * a.max_pages +
+                                          ((c.key0() + (lane << lgCH)) >> lgP)]);
         };
-        // lanes 0-7: K scales, lanes 8-15: V scales of tile t (cursor c)
-        auto fetch_scales = [&](int t, const Cursor& c) {
-            const int l = lane & 7;
-            if (is_v || lane >= 2 * MAX_CHUNKS) return;
-            float* dst = raw + (t % RAW_STAGES) * 2 * MAX_CHUNKS + lane;
-            if (!chunk_used(c, l)) {
-                *dst = 1.f;
-                return;
-            }
-            int page = pids[(t % (LOOKAHEAD + 1)) * MAX_CHUNKS + l];
-            if (page < 0 || page >= a.num_pages) page = 0;  // flagged with its copy
-            cp_async_4(dst, (lane < MAX_CHUNKS ? a.k_page_scale : a.v_page_scale) +
-                                (int64_t)page * Hkv + c.kvh);
-        };
-        for (int la = 0; la < LOOKAHEAD; ++la)
+        for (int la = 0; la < LOOKAHEAD; ++la) {
             if (la < n_tiles) {
                 fetch_pids(la, ahead);
                 if (la + 1 < n_tiles) ahead.next(s_ctx, a);
-            }
-        cp_async_commit();
-        cp_async_wait<0>();
-        __syncwarp();
-        for (int t = 0; t < SCALE_AHEAD; ++t) {
-            if (t < n_tiles) {
-                fetch_scales(t, mid);
-                if (t + 1 < n_tiles) mid.next(s_ctx, a);
             }
             cp_async_commit();
         }
@@ -374,52 +379,32 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         bool ok = true;
         for (int it = 0; it < n_tiles && ok; ++it) {
             if (it + LOOKAHEAD < n_tiles) {
-                fetch_pids((it + LOOKAHEAD) % (LOOKAHEAD + 1), ahead);
+                fetch_pids(it + LOOKAHEAD, ahead);
                 if (it + LOOKAHEAD + 1 < n_tiles) ahead.next(s_ctx, a);
             }
-            // one group per iteration: the scales of tile it were committed
-            // SCALE_AHEAD groups ago, and with them every block-table entry up
-            // to tile it + SCALE_AHEAD
-            cp_async_wait<SCALE_AHEAD - 1>();
-            __syncwarp();
-            const int* pid = pids + (it % (LOOKAHEAD + 1)) * MAX_CHUNKS;
+            cp_async_commit();
+            cp_async_wait<LOOKAHEAD>();  // entries of tile `it` (each lane its own)
             const int s = it % SLOTS;
             const bool used = lane < MAX_CHUNKS && chunk_used(cur, lane);
             const int nck = __popc(__ballot_sync(0xffffffffu, used));
             if (it >= SLOTS)
-                ok = warp_wait(&empty[s], ((it / SLOTS) - 1) & 1, abort_flag, a.dev_err);
-            if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(nck * CH * D));
+                ok = role_wait(&empty[s], ((it / SLOTS) - 1) & 1, abort_flag, a.dev_err);
+            if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)((nck << lgCH) * D));
             __syncwarp();
             if (!ok) break;
             if (used) {
-                int page = pid[lane];
+                int page = pids[(it % PID_STAGES) * MAX_CHUNKS + lane];
                 if (page < 0 || page >= a.num_pages) {
                     raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
                     page = 0;
                 }
-                const int key = cur.key0() + lane * CH;
-                tma_load_2d(ring + s * SLOT_BYTES + lane * CH * D, map, &full[s], 0,
-                            (page * Hkv + cur.kvh) * P + key % P, pol);
+                tma_load_2d(ring + s * SLOT_BYTES, map, &full[s], 0,
+                            ((page * Hkv + cur.kvh) << lgP) +
+                                ((cur.key0() + (lane << lgCH)) & (P - 1)),
+                            pol);
             }
             n_issued = it + 1;
-            if (!is_v) {
-                if (lane < MAX_CHUNKS) {
-                    const float* r = raw + (it % RAW_STAGES) * 2 * MAX_CHUNKS;
-                    const float sv = r[MAX_CHUNKS + lane];
-                    const bool on = sv > 1e-30f;
-                    s_scale[(it % SCALE_STAGES) * MAX_CHUNKS + lane] =
-                        make_float4(r[lane], on ? __log2f(sv) : 0.f, on ? 1.f / sv : 1.f,
-                                    on ? 1.f : 0.f);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[Smem::B_SCALE + it % SCALE_STAGES]);
-            }
             __syncwarp();
-            if (it + SCALE_AHEAD < n_tiles) {
-                fetch_scales(it + SCALE_AHEAD, mid);
-                if (it + SCALE_AHEAD + 1 < n_tiles) mid.next(s_ctx, a);
-            }
-            cp_async_commit();
             if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
         cp_async_wait<0>();
@@ -432,7 +417,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         // ================= Q K^T issue =================
         if (n_tiles > 0) {
             Cursor cur;
-            cur.init(t_begin, s_pre, s_ctx, a);
+            start_at(cur);
             int pc = -1;  // piece of the current tile
             bool ok = true;
             const uint64_t qdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::Q), 16, 1024);
@@ -443,21 +428,21 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const int s = it & 1, slot = it % SLOTS;
                 if (first) {
                     ++pc;
-                    ok = warp_wait(&bars[Smem::B_QFULL + (pc & 1)], (pc >> 1) & 1, abort_flag,
+                    ok = role_wait(&bars[Smem::B_QFULL + (pc & 1)], (pc >> 1) & 1, abort_flag,
                                    a.dev_err);
                     if (!ok) break;
                 }
                 // K of tile it landed; S buffer s free (P V of tile it - 2 done)
-                ok = warp_wait(&bars[Smem::B_KFULL + slot], (it / SLOTS) & 1, abort_flag,
+                ok = role_wait(&bars[Smem::B_KFULL + slot], (it / SLOTS) & 1, abort_flag,
                                a.dev_err);
                 if (ok && it >= 2)
-                    ok = warp_wait(&bars[Smem::B_SFREE + s], ((it >> 1) - 1) & 1, abort_flag,
+                    ok = role_wait(&bars[Smem::B_SFREE + s], ((it >> 1) - 1) & 1, abort_flag,
                                    a.dev_err);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t qd = qdesc0 + ((uint32_t)((pc & 1) * 2 * Q_PART) >> 4);
                 const uint64_t kd = kdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < 8; ++kk)  // hi, then lo, in 32-byte steps
                     umma_f8_ss_w(tmem + s * TN, qd + (kk >> 2) * (Q_PART >> 4) + (kk & 3) * 2,
                                  kd + (kk & 3) * 2, umma_idesc_e4m3(ROWS, TN), kk ? 1u : 0u);
@@ -476,7 +461,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         // ================= P V issue (warp 7) =================
         if (n_tiles > 0) {
             Cursor cur;
-            cur.init(t_begin, s_pre, s_ctx, a);
+            start_at(cur);
             int pc = -1;
             bool ok = true;
             bool has0 = false, has1 = false;  // set 0 / 1 issued a P V in this piece
@@ -495,10 +480,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     // the previous piece's epilogue has read both O before the
                     // first P V of this piece overwrites them
                     if (pc >= 1)
-                        ok = warp_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
+                        ok = role_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
                     if (!ok) break;
                 }
-                ok = warp_wait(&bars[Smem::B_VFULL + slot], (it / SLOTS) & 1, abort_flag,
+                ok = role_wait(&bars[Smem::B_VFULL + slot], (it / SLOTS) & 1, abort_flag,
                                a.dev_err);
                 if (!ok) break;
                 // rows that no query sees and a P V reads: zero, so that 0 * (stale,
@@ -522,7 +507,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = warp_wait(&bars[Smem::B_PREADY + s], (it >> 1) & 1, abort_flag, a.dev_err);
+                ok = role_wait(&bars[Smem::B_PREADY + s], (it >> 1) & 1, abort_flag, a.dev_err);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = vdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
@@ -530,15 +515,14 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O + s * D;
                 tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
                 tmem_cp_scales_w(sbuf + SF_V, sfv);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < nkb) {
-                        const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
-                        umma_mx_ts_w(od, sbuf + p_col(j), vj, umma_idesc_mx_e4m3(ROWS, D, j),
-                                     sbuf + SF_P, sbuf + SF_V, (hs || j > 0) ? 1u : 0u);
-                        umma_mx_ts_w(od, sbuf + p_col(j) + 8, vj, umma_idesc_mx_e4m3(ROWS, D, j),
-                                     sbuf + SF_P, sbuf + SF_V, 1u);
-                    }
+#pragma unroll 1
+                for (int j = 0; j < nkb; ++j) {
+                    const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
+                    const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, j);
+                    umma_mx_ts_w(od, sbuf + p_col(j), vj, id, sbuf + SF_P, sbuf + SF_V,
+                                 (hs || j > 0) ? 1u : 0u);
+                    umma_mx_ts_w(od, sbuf + p_col(j) + 8, vj, id, sbuf + SF_P, sbuf + SF_V, 1u);
+                }
                 umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
                 umma_commit_w(&bars[Smem::B_SFREE + s]);
                 if (s) has1 = true;
@@ -552,8 +536,90 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
     }
     } else if (warp >= 12) {
-        regs_dec<96>();
-        // ================= q rows to hi / lo (warps 12-15) =================
+    regs_dec<96>();
+    if (warp == 15) {
+        // ================= page scales =================
+        // Two tiles per iteration, 16 lanes each (8 chunks of K, 8 of V):
+        // {sk, log2 sv, 1 / sv, on} of tile it into stage it % SCALE_STAGES,
+        // free once its softmax set has taken it.
+        int* pids = reinterpret_cast<int*>(sm + Smem::SPIDS);
+        float* raw = reinterpret_cast<float*>(sm + Smem::RAW);
+        const int half = lane >> 4, l = lane & 7;
+        const bool is_v = lane & 8;
+        const float* src = is_v ? a.v_page_scale : a.k_page_scale;
+        const int pairs = (n_tiles + 1) / 2;
+        Cursor c_pid, c_sc;  // of this half's tile, as the two loads advance
+        int t_pid = half, t_sc = half;
+        if (half < n_tiles) {
+            start_at(c_pid);
+            if (half) c_pid.next(s_ctx, a);
+            c_sc = c_pid;
+        }
+        auto advance = [&](Cursor& c, int& t) {
+            for (int e = 0; e < 2; ++e)
+                if (++t < n_tiles) c.next(s_ctx, a);
+        };
+        auto fetch_pids = [&](int p) {  // pair p
+            if (t_pid < n_tiles && !is_v && chunk_used(c_pid, l))
+                cp_async_4(&pids[((p % RAW_STAGES) * 2 + half) * MAX_CHUNKS + l],
+                           &a.block_table[(int64_t)c_pid.b * a.max_pages +
+                                          ((c_pid.key0() + (l << lgCH)) >> lgP)]);
+            advance(c_pid, t_pid);
+        };
+        auto fetch_scales = [&](int p) {
+            if (t_sc < n_tiles) {
+                float* dst = raw + (p % RAW_STAGES) * 32 + lane;
+                if (chunk_used(c_sc, l)) {
+                    int page = pids[((p % RAW_STAGES) * 2 + half) * MAX_CHUNKS + l];
+                    if (page < 0 || page >= a.num_pages) page = 0;  // flagged with its copy
+                    cp_async_4(dst, src + (int64_t)page * Hkv + c_sc.kvh);
+                } else {
+                    *dst = 1.f;
+                }
+            }
+            advance(c_sc, t_sc);
+        };
+        // groups: the entries of pairs 0 and 1, then scales p with entries p + 2
+        fetch_pids(0);
+        if (pairs > 1) fetch_pids(1);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+        for (int p = 0; p < SCALE_PAIRS; ++p) {
+            if (p < pairs) fetch_scales(p);
+            if (p + 2 < pairs) fetch_pids(p + 2);
+            cp_async_commit();
+        }
+        bool ok = true;
+        for (int p = 0; p < pairs && ok; ++p) {
+            cp_async_wait<SCALE_PAIRS - 1>();  // scales p, entries p + 2
+            __syncwarp();
+            for (int e = 0; e < 2 && ok; ++e) {
+                const int t = 2 * p + e;
+                if (t < n_tiles && t >= SCALE_STAGES)
+                    ok = role_wait(&bars[Smem::B_SCFREE + t % SCALE_STAGES],
+                                   (t / SCALE_STAGES - 1) & 1, abort_flag, a.dev_err);
+            }
+            if (!ok) break;
+            const int t = 2 * p + half;
+            if (!is_v && t < n_tiles) {
+                const float* r = raw + (p % RAW_STAGES) * 32 + lane;
+                const float sv = r[8];
+                const bool on = sv > 1e-30f;
+                s_scale[(t % SCALE_STAGES) * MAX_CHUNKS + l] =
+                    make_float4(r[0], on ? __log2f(sv) : 0.f, on ? __fdividef(1.f, sv) : 1.f,
+                                on ? 1.f : 0.f);
+            }
+            __syncwarp();
+            if ((lane & 15) == 0 && t < n_tiles)
+                mbar_arrive(&bars[Smem::B_SCALE + t % SCALE_STAGES]);
+            if (p + SCALE_PAIRS < pairs) fetch_scales(p + SCALE_PAIRS);
+            if (p + SCALE_PAIRS + 2 < pairs) fetch_pids(p + SCALE_PAIRS + 2);
+            cp_async_commit();
+        }
+        cp_async_wait<0>();
+    } else {
+        // ================= q rows to hi / lo (warps 12-14) =================
         // Piece j into buffer j & 1 (free once the last Q K^T of piece j - 2 is
         // done), its row exponents into stage j % 8.  16 lanes per row, 8
         // elements each; a negative softmax scale is folded into q's sign.
@@ -562,27 +628,37 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
         Cursor cur;
         bool more = n_tiles > 0;
-        if (more) cur.init(t_begin, s_pre, s_ctx, a);
+        if (more) start_at(cur);
         for (int j = 0; more; ++j) {
-            if (j >= 2 && !warp_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
+            if (j >= 2 && !role_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
                                      abort_flag, a.dev_err))
                 break;
             uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
-            for (int r0 = w * 2; r0 < R; r0 += 8) {
-                const int r = r0 + half;
-                uint4 v = make_uint4(0, 0, 0, 0);
+            constexpr int U = 1;  // rows in flight per lane
+            for (int base = w * 2 + half; base - half < R; base += 6 * U) {
+            uint4 in[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = base + 6 * u;
+                in[u] = make_uint4(0, 0, 0, 0);
                 if (r < R)
-                    v = __ldg(reinterpret_cast<const uint4*>(
-                                  q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) *
-                                          D) +
-                              c16);
+                    in[u] = __ldg(
+                        reinterpret_cast<const uint4*>(
+                            q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) * D) +
+                        c16);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = base + 6 * u;
+                const uint4 v = in[u];
+                if (r - half >= R) continue;  // uniform over the warp
                 float x[8];
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
                 float top = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(u[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                    x[2 * e] = __uint_as_float(pair[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(pair[e] & 0xffff0000u);
                     top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
                 }
 #pragma unroll
@@ -616,6 +692,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     }
                 }
             }
+            }
             fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
             __syncwarp();
             if (lane == 0) {
@@ -625,6 +702,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
             if (more) cur.next_segment(s_ctx, a);
         }
+    }
     } else {
         regs_inc<160>();
         // ================= softmax sets (0: warps 0-3, even tiles; 1: 8-11, odd) =================
@@ -637,7 +715,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int i_row = row_valid ? r / G : k - 1;
         const int blk0 = copy * NBLK;         // the first 32-key block of this thread
         const float sl2 = fabsf(a.scale) * kLog2e;
-        const int csh = 31 - __clz(CH);       // log2 of the keys of a chunk
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t s_mine = lane_base + set * TN;
         const uint32_t o_mine = TM_O + set * D, o_other = TM_O + (1 - set) * D;
@@ -651,7 +728,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         int low = 0;            // first key of this row's window
         uint64_t mrow = 0;
         Cursor cur;
-        if (n_tiles > 0) cur.init(t_begin, s_pre, s_ctx, a);
+        if (n_tiles > 0) start_at(cur);
         bool ok = true;
         int pc = -1;
         for (int it = 0; it < n_tiles; ++it) {
@@ -668,17 +745,17 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
                 if (WIN) low = window_low(a, ctx + draft_depth(bits));
                 if (ok)
-                    ok = warp_wait(&bars[Smem::B_EXP + pc % EXP_STAGES], (pc / EXP_STAGES) & 1,
+                    ok = role_wait(&bars[Smem::B_EXP + pc % EXP_STAGES], (pc / EXP_STAGES) & 1,
                                    abort_flag, a.dev_err);
                 if (ok && row_valid)
                     qm = ldexpf(sl2, (int)s_exp[(pc % EXP_STAGES) * ROWS + r]);
             }
             if (mine) {
                 if (ok)
-                    ok = warp_wait(&bars[Smem::B_SCALE + it % SCALE_STAGES],
+                    ok = role_wait(&bars[Smem::B_SCALE + it % SCALE_STAGES],
                                    (it / SCALE_STAGES) & 1, abort_flag, a.dev_err);
                 if (ok)
-                    ok = warp_wait(&bars[Smem::B_SFULL + set], own & 1, abort_flag, a.dev_err);
+                    ok = role_wait(&bars[Smem::B_SFULL + set], own & 1, abort_flag, a.dev_err);
                 if (ok && quad_active) {
                     tc_fence_after();
                     const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
@@ -703,41 +780,52 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     uint32_t sfw = 0x7f7f7f7fu;  // scale bytes of this lane's blocks
                     float alpha = 1.f;           // what a moved reference takes off O
                     bool move = false;
+                    // STEP blocks at a time, their loads together
+                    constexpr int STEP = 1;
 #pragma unroll 1
-                    for (int blk = blk0 + NBLK - 1; blk >= blk0; --blk) {
-                        uint32_t r0[16], r1[16], pw[16];
-                        float x0, x1;
-                        tmem_ld16_max(s_mine + blk * 32, r0, x0);
-                        tmem_ld16_max(s_mine + blk * 32 + 16, r1, x1);
-                        const float4 s0 = sc[(blk * 32) >> csh], s1 = sc[(blk * 32 + 16) >> csh];
-                        // to log2 units; not 0, so that -inf stays -inf
-                        const float mu0 = fmaxf(qm * s0.x, 1.2e-38f);
-                        const float mu1 = fmaxf(qm * s1.x, 1.2e-38f);
-                        tmem_wait_ld();
-                        // whole power of two of the block's largest w (-inf: no key)
-                        const float top =
-                            floorf(fmaxf(fmaf(x0, mu0, s0.y), fmaf(x1, mu1, s1.y)));
-                        if (top > m_ref + kMoveThreshold) {  // also -inf -> finite
-                            const int d = (int)fminf(top - m_ref, 255.f);
-                            move = true;
-                            alpha *= pow2_neg(d);
-                            l *= pow2_neg(d);
-                            m_ref = top;
+                    for (int b0 = blk0 + NBLK - STEP; b0 >= blk0; b0 -= STEP) {
+                        uint32_t r[2 * STEP][16], pw[16];
+                        float x[2 * STEP];
 #pragma unroll
-                            for (int b = 0; b < 32; b += 8)  // blocks of this tile so far
-                                sfw = (sfw & ~(0xffu << b)) |
-                                      (uint32_t)max((int)((sfw >> b) & 0xffu) - d, 0) << b;
+                        for (int g = 2 * STEP - 1; g >= 0; --g)
+                            tmem_ld16_max(s_mine + b0 * 32 + g * 16, r[g], x[g]);
+                        float4 gs[2 * STEP];
+#pragma unroll
+                        for (int g = 0; g < 2 * STEP; ++g)
+                            gs[g] = sc[(b0 * 32 + g * 16) >> lgCH];
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = STEP - 1; e >= 0; --e) {
+                            const int blk = b0 + e;
+                            const float4 s0 = gs[2 * e], s1 = gs[2 * e + 1];
+                            // to log2 units; not 0, so that -inf stays -inf
+                            const float mu0 = fmaxf(qm * s0.x, 1.2e-38f);
+                            const float mu1 = fmaxf(qm * s1.x, 1.2e-38f);
+                            // whole power of two of the block's largest w (-inf: no key)
+                            const float top = floorf(
+                                fmaxf(fmaf(x[2 * e], mu0, s0.y), fmaf(x[2 * e + 1], mu1, s1.y)));
+                            if (top > m_ref + kMoveThreshold) {  // also -inf -> finite
+                                const int d = (int)fminf(top - m_ref, 255.f);
+                                move = true;
+                                alpha *= pow2_neg(d);
+                                l *= pow2_neg(d);
+                                m_ref = top;
+#pragma unroll
+                                for (int b = 0; b < 32; b += 8)  // blocks of this tile so far
+                                    sfw = (sfw & ~(0xffu << b)) |
+                                          (uint32_t)max((int)((sfw >> b) & 0xffu) - d, 0) << b;
+                            }
+                            const float n = fmaxf(top - m_ref, -110.f);  // (NaN: -110)
+                            const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
+                            const float base = top == -INFINITY ? 0.f : 7.f - (m_ref + n);
+                            const float w0 = group_weights(r[2 * e], mu0, base + s0.y,
+                                                           s0.w != 0.f, pw, pw + 8);
+                            const float w1 = group_weights(r[2 * e + 1], mu1, base + s1.y,
+                                                           s1.w != 0.f, pw + 4, pw + 12);
+                            l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
+                            sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                            tmem_st16(s_mine + p_col(blk), pw);
                         }
-                        const float n = fmaxf(top - m_ref, -110.f);  // (NaN without a key: -110)
-                        const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
-                        const float base = top == -INFINITY ? 0.f : 7.f - (m_ref + n);
-                        const float w0 =
-                            group_weights(r0, mu0, base + s0.y, s0.w != 0.f, pw, pw + 8);
-                        const float w1 =
-                            group_weights(r1, mu1, base + s1.y, s1.w != 0.f, pw + 4, pw + 12);
-                        l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
-                        sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
-                        tmem_st16(s_mine + p_col(blk), pw);
                     }
                     if (REP > 1) {  // the blocks of the other copies
                         const uint32_t zero[16] = {};
@@ -768,7 +856,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 // P of this tile stored (every warp of the set arrives, active or not)
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[Smem::B_PREADY + set]);
+                if (lane == 0) {
+                    mbar_arrive(&bars[Smem::B_PREADY + set]);
+                    mbar_arrive(&bars[Smem::B_SCFREE + it % SCALE_STAGES]);
+                }
                 has = true;
                 ++own;
             }
@@ -777,7 +868,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 // sets' (and the copies') (max, sum, O); each set writes half of
                 // the output columns
                 if (ok && has)  // this set's last P V (tile own - 1) is done
-                    ok = warp_wait(&bars[Smem::B_SFREE + set], (own - 1) & 1, abort_flag,
+                    ok = role_wait(&bars[Smem::B_SFREE + set], (own - 1) & 1, abort_flag,
                                    a.dev_err);
                 tc_fence_after();
                 const int64_t tb = ld_shared_s64(s_rng), te = ld_shared_s64(s_rng + 1);
