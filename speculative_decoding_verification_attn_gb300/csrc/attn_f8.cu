@@ -34,9 +34,12 @@
 //
 // Layout.  Persistent grid, the tile list split as in the 128-key bf16 kernel
 // (TileSplit, partials merged by the combine kernel).
-//  * TMEM: S of set 0 [0,128), of set 1 [128,256), O of set 0 [256,384), of set
-//    1 [384,512).  P goes over S columns [64,128) (p_col), the scale bytes of P
-//    and of V (all one) over [0,4) / [4,8).
+//  * TMEM: three S buffers [0,384), one O [384,512).  P goes over S columns
+//    [64,128) of its tile (p_col), the scale bytes of P and of V (all one) over
+//    [0,4) / [4,8).  Three tiles are in flight: the chain of one tile (Q K^T,
+//    softmax, P V, ~3800 cycles at 32 rows) is longer than two tiles' share of
+//    HBM.  That both softmax sets add into one O is what frees the third buffer;
+//    they share each lane's reference, handed on from tile to tile.
 //  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
 //    and 6 TMA of K and of V; 7 P V issue; 12-14 turn the q rows of the next
 //    piece into hi / lo; 15 brings the page scales.  16 warps share the block's
@@ -72,11 +75,12 @@ constexpr int SCALE_PAIRS = 2;
 constexpr int RAW_STAGES = 4;          // pairs of tiles
 constexpr int SCALE_STAGES = 16;       // tiles
 // row exponents: the q rows of piece j are written when Q K^T of piece j - 2
-// is done; a softmax set may then still be at piece j - 4
+// is done; the softmax may then still be NS tiles behind it, at piece j - 5
 constexpr int EXP_STAGES = 8;
 constexpr int MAX_BATCH = 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TM_O = 256;
+constexpr int NS = 3;                   // S buffers
+constexpr uint32_t TM_O = NS * TN;
 constexpr uint32_t SF_P = 0, SF_V = 4;  // columns of the scale bytes inside an S buffer
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -90,18 +94,20 @@ struct Smem {
     static constexpr int KS = Q + 4 * Q_PART;
     static constexpr int VS = KS + SLOTS * SLOT_BYTES;
     static constexpr int RED = VS + SLOTS * SLOT_BYTES;  // [set][quad][32 rows][16] fp32
-    static constexpr int SFP = RED + 2 * 4 * 32 * 16 * 4;  // scale bytes of P, per set
-    static constexpr int SFV = SFP + 2 * 512;              // scale bytes of V: all 1.0
+    static constexpr int SFP = RED + 2 * 4 * 32 * 16 * 4;  // scale bytes of P, per S buffer
+    static constexpr int SFV = SFP + NS * 512;             // scale bytes of V: all 1.0
     static constexpr int BARS = SFV + 512;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + SLOTS, B_VFULL = B_KEMPTY + SLOTS,
                          B_VEMPTY = B_VFULL + SLOTS, B_QFULL = B_VEMPTY + SLOTS,
-                         B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + 2,
-                         B_SFREE = B_PREADY + 2, B_EPI = B_SFREE + 2, B_DRAIN = B_EPI + 1,
+                         B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + NS,
+                         B_SFREE = B_PREADY + NS, B_REF = B_SFREE + NS, B_EPI = B_REF + 4,
+                         B_DRAIN = B_EPI + 1,
                          B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
                          B_SCFREE = B_SCALE + SCALE_STAGES, NUM_BARS = B_SCFREE + SCALE_STAGES;
     static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
     static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
-    static constexpr int STAT = FIRST + 48;           // (m, l) of [set][lane]
+    static constexpr int REF = FIRST + 48;            // reference of each lane
+    static constexpr int STAT = REF + ROWS * 4;       // (m, l) of [set][lane]
     static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;  // [2 producers][PID_STAGES][8] int
     // scale warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8] scales
     static constexpr int SPIDS = PIDS + 2 * PID_STAGES * MAX_CHUNKS * 4;
@@ -251,11 +257,14 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[Smem::B_QFULL + s], 3);   // the 3 converting warps
             mbar_init(&bars[Smem::B_QFREE + s], 1);
+            mbar_init(&bars[Smem::B_DRAIN + s], 1);
+        }
+        for (int s = 0; s < NS; ++s) {
             mbar_init(&bars[Smem::B_SFULL + s], 1);
             mbar_init(&bars[Smem::B_PREADY + s], 4);  // the 4 warps of the set
             mbar_init(&bars[Smem::B_SFREE + s], 1);
-            mbar_init(&bars[Smem::B_DRAIN + s], 1);
         }
+        for (int s = 0; s < 4; ++s) mbar_init(&bars[Smem::B_REF + s], 1);  // per lane quadrant
         for (int s = 0; s < EXP_STAGES; ++s) mbar_init(&bars[Smem::B_EXP + s], 3);
         for (int s = 0; s < SCALE_STAGES; ++s) {
             mbar_init(&bars[Smem::B_SCALE + s], 1);
@@ -341,6 +350,89 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         return !WIN || k0 < a.sinks || k0 + CH > window_low(a, s_ctx[c.b]);
     };
 
+    if (warp >= 12) regs_dec<96>();
+    if (warp < 4 || (warp >= 8 && warp < 15)) {
+        // ================= q rows to hi / lo =================
+        // Piece j into buffer j & 1 (free once the last Q K^T of piece j - 2 is
+        // done), its row exponents into stage j % 8.  16 lanes per row, 8
+        // elements each; a negative softmax scale is folded into q's sign.  The
+        // first piece, which everything waits for, by the softmax warps too;
+        // the others by warps 12-14.
+        const int half = lane >> 4, c16 = lane & 15;
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        Cursor cur;
+        bool more = n_tiles > 0;
+        if (more) start_at(cur);
+        for (int j = 0; more; ++j) {
+            if (j >= 2 && !role_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
+                                     abort_flag, a.dev_err))
+                break;
+            uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
+            const int w = j > 0 ? warp - 12 : warp < 4 ? warp : warp - 4;  // of 3, or of 11
+#pragma unroll 1
+            for (int r0 = w * 2; r0 < R; r0 += j > 0 ? 6 : 22) {
+                const int r = r0 + half;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < R)
+                    v = __ldg(reinterpret_cast<const uint4*>(
+                                  q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) *
+                                          D) +
+                              c16);
+                float x[8];
+                const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
+                float top = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(pair[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(pair[e] & 0xffff0000u);
+                    top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                // 2^-ex takes the row's largest element into [128, 256)
+                const int ex = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
+                const float mul = sign * __uint_as_float((uint32_t)(127 - ex) << 23);
+                uint32_t hw[2], lw[2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    uint16_t h, l;
+                    split_e4m3x2(x[2 * e] * mul, x[2 * e + 1] * mul, h, l);
+                    if (e & 1) {
+                        hw[e >> 1] |= (uint32_t)h << 16;
+                        lw[e >> 1] |= (uint32_t)l << 16;
+                    } else {
+                        hw[e >> 1] = h;
+                        lw[e >> 1] = l;
+                    }
+                }
+                if (r < R) {
+                    if (c16 == 0) s_exp[(j % EXP_STAGES) * ROWS + r] = (int8_t)ex;
+#pragma unroll
+                    for (int c = 0; c < REP; ++c) {
+                        const int row = r + c * COPY;
+                        const int off = row * D + (((c16 >> 1) ^ (row & 7)) << 4) + (c16 & 1) * 8;
+                        *reinterpret_cast<uint2*>(buf + off) = make_uint2(hw[0], hw[1]);
+                        *reinterpret_cast<uint2*>(buf + Q_PART + off) = make_uint2(lw[0], lw[1]);
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
+            if (j == 0)
+                named_bar_sync(1, 11 * 32);
+            else
+                __syncwarp();
+            if (warp < 12) break;
+            if (lane == 0) {
+                mbar_arrive(&bars[Smem::B_EXP + j % EXP_STAGES]);
+                mbar_arrive(&bars[Smem::B_QFULL + (j & 1)]);
+            }
+            more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
+            if (more) cur.next_segment(s_ctx, a);
+        }
+    }
+
     if (warp >= 4 && warp < 8) {
     regs_dec<96>();
     if (warp == 5 || warp == 6) {
@@ -425,18 +517,18 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             for (int it = 0; it < n_tiles && ok; ++it) {
                 const bool first = (it == 0) || (cur.lt == 0);
                 const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
-                const int s = it & 1, slot = it % SLOTS;
+                const int s = it % NS, slot = it % SLOTS;
                 if (first) {
                     ++pc;
                     ok = role_wait(&bars[Smem::B_QFULL + (pc & 1)], (pc >> 1) & 1, abort_flag,
                                    a.dev_err);
                     if (!ok) break;
                 }
-                // K of tile it landed; S buffer s free (P V of tile it - 2 done)
+                // K of tile it landed; S buffer s free (P V of tile it - NS done)
                 ok = role_wait(&bars[Smem::B_KFULL + slot], (it / SLOTS) & 1, abort_flag,
                                a.dev_err);
-                if (ok && it >= 2)
-                    ok = role_wait(&bars[Smem::B_SFREE + s], ((it >> 1) - 1) & 1, abort_flag,
+                if (ok && it >= NS)
+                    ok = role_wait(&bars[Smem::B_SFREE + s], (it / NS - 1) & 1, abort_flag,
                                    a.dev_err);
                 if (!ok) break;
                 tc_fence_after();
@@ -464,21 +556,19 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             start_at(cur);
             int pc = -1;
             bool ok = true;
-            bool has0 = false, has1 = false;  // set 0 / 1 issued a P V in this piece
             // V of 32 keys: MN-major, 8-key groups 1 KB apart
             const uint64_t vdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::VS), 1024, 1024);
             const uint64_t sfp0 = umma_sdesc_plain(smem_u32(sm + Smem::SFP), 128);
             const uint64_t sfv = umma_sdesc_plain(smem_u32(sm + Smem::SFV), 128);
             for (int it = 0; it < n_tiles && ok; ++it) {
                 const bool first = (it == 0) || (cur.lt == 0);
-                const int s = it & 1, slot = it % SLOTS;
+                const int s = it % NS, slot = it % SLOTS;
                 const int ctx = s_ctx[cur.b], key0 = cur.key0();
                 const int nvalid = min(TN, ctx + k - key0), nkb = (nvalid + 31) / 32;
                 if (first) {
                     ++pc;
-                    has0 = has1 = false;
-                    // the previous piece's epilogue has read both O before the
-                    // first P V of this piece overwrites them
+                    // the previous piece's epilogue has read O before the first
+                    // P V of this piece overwrites it
                     if (pc >= 1)
                         ok = role_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
                     if (!ok) break;
@@ -507,12 +597,11 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                ok = role_wait(&bars[Smem::B_PREADY + s], (it >> 1) & 1, abort_flag, a.dev_err);
+                ok = role_wait(&bars[Smem::B_PREADY + s], (it / NS) & 1, abort_flag, a.dev_err);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = vdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
-                const bool hs = s ? has1 : has0;
-                const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O + s * D;
+                const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O;
                 tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
                 tmem_cp_scales_w(sbuf + SF_V, sfv);
 #pragma unroll 1
@@ -520,13 +609,11 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
                     const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, j);
                     umma_mx_ts_w(od, sbuf + p_col(j), vj, id, sbuf + SF_P, sbuf + SF_V,
-                                 (hs || j > 0) ? 1u : 0u);
+                                 (!first || j > 0) ? 1u : 0u);
                     umma_mx_ts_w(od, sbuf + p_col(j) + 8, vj, id, sbuf + SF_P, sbuf + SF_V, 1u);
                 }
                 umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
                 umma_commit_w(&bars[Smem::B_SFREE + s]);
-                if (s) has1 = true;
-                else has0 = true;
                 if (it + 1 < n_tiles) cur.next(s_ctx, a);
             }
             __syncwarp();
@@ -536,7 +623,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
     }
     } else if (warp >= 12) {
-    regs_dec<96>();
     if (warp == 15) {
         // ================= page scales =================
         // Two tiles per iteration, 16 lanes each (8 chunks of K, 8 of V):
@@ -618,90 +704,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             cp_async_commit();
         }
         cp_async_wait<0>();
-    } else {
-        // ================= q rows to hi / lo (warps 12-14) =================
-        // Piece j into buffer j & 1 (free once the last Q K^T of piece j - 2 is
-        // done), its row exponents into stage j % 8.  16 lanes per row, 8
-        // elements each; a negative softmax scale is folded into q's sign.
-        const int w = warp - 12, half = lane >> 4, c16 = lane & 15;
-        const float sign = a.scale < 0.f ? -1.f : 1.f;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-        Cursor cur;
-        bool more = n_tiles > 0;
-        if (more) start_at(cur);
-        for (int j = 0; more; ++j) {
-            if (j >= 2 && !role_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
-                                     abort_flag, a.dev_err))
-                break;
-            uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
-            constexpr int U = 1;  // rows in flight per lane
-            for (int base = w * 2 + half; base - half < R; base += 6 * U) {
-            uint4 in[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = base + 6 * u;
-                in[u] = make_uint4(0, 0, 0, 0);
-                if (r < R)
-                    in[u] = __ldg(
-                        reinterpret_cast<const uint4*>(
-                            q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) * D) +
-                        c16);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int r = base + 6 * u;
-                const uint4 v = in[u];
-                if (r - half >= R) continue;  // uniform over the warp
-                float x[8];
-                const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
-                float top = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(pair[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(pair[e] & 0xffff0000u);
-                    top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // 2^-ex takes the row's largest element into [128, 256)
-                const int ex = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
-                const float mul = sign * __uint_as_float((uint32_t)(127 - ex) << 23);
-                uint32_t hw[2], lw[2];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y0 = x[2 * e] * mul, y1 = x[2 * e + 1] * mul;
-                    uint16_t h, l;
-                    split_e4m3x2(y0, y1, h, l);
-                    if (e & 1) {
-                        hw[e >> 1] |= (uint32_t)h << 16;
-                        lw[e >> 1] |= (uint32_t)l << 16;
-                    } else {
-                        hw[e >> 1] = h;
-                        lw[e >> 1] = l;
-                    }
-                }
-                if (r < R) {
-                    if (c16 == 0) s_exp[(j % EXP_STAGES) * ROWS + r] = (int8_t)ex;
-#pragma unroll
-                    for (int c = 0; c < REP; ++c) {
-                        const int row = r + c * COPY;
-                        const int off = row * D + (((c16 >> 1) ^ (row & 7)) << 4) + (c16 & 1) * 8;
-                        *reinterpret_cast<uint2*>(buf + off) = make_uint2(hw[0], hw[1]);
-                        *reinterpret_cast<uint2*>(buf + Q_PART + off) = make_uint2(lw[0], lw[1]);
-                    }
-                }
-            }
-            }
-            fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars[Smem::B_EXP + j % EXP_STAGES]);
-                mbar_arrive(&bars[Smem::B_QFULL + (j & 1)]);
-            }
-            more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
-            if (more) cur.next_segment(s_ctx, a);
-        }
     }
     } else {
         regs_inc<160>();
@@ -716,15 +718,12 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int blk0 = copy * NBLK;         // the first 32-key block of this thread
         const float sl2 = fabsf(a.scale) * kLog2e;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        const uint32_t s_mine = lane_base + set * TN;
-        const uint32_t o_mine = TM_O + set * D, o_other = TM_O + (1 - set) * D;
         float* s_stat_m = reinterpret_cast<float*>(sm + Smem::STAT);
         float* s_stat_l = s_stat_m + 2 * ROWS;
+        float* s_ref = reinterpret_cast<float*>(sm + Smem::REF);
         float* red = reinterpret_cast<float*>(sm + Smem::RED) + set * 4 * 32 * 16;
-        float m_ref = -INFINITY, l = 0.f;  // reference (whole), row sum against it
+        float m = -INFINITY, l = 0.f;  // reference that the row sum l of this set stands to
         float qm = 0.f;         // accumulator units to log2 units, before the page's scale
-        bool has = false;       // this set took a tile of the current piece
-        int own = 0;            // tiles this set has taken
         int low = 0;            // first key of this row's window
         uint64_t mrow = 0;
         Cursor cur;
@@ -735,12 +734,12 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const bool first = (it == 0) || (cur.lt == 0);
             const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
             const bool mine = (it & 1) == set;
+            const int sb = it % NS;
             const int ctx = s_ctx[cur.b], key0 = cur.key0();
             if (first) {
                 ++pc;
-                m_ref = -INFINITY;
+                m = -INFINITY;
                 l = 0.f;
-                has = false;
                 const uint64_t bits = draft_bits(a, cur.b, i_row);
                 mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
                 if (WIN) low = window_low(a, ctx + draft_depth(bits));
@@ -755,9 +754,11 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     ok = role_wait(&bars[Smem::B_SCALE + it % SCALE_STAGES],
                                    (it / SCALE_STAGES) & 1, abort_flag, a.dev_err);
                 if (ok)
-                    ok = role_wait(&bars[Smem::B_SFULL + set], own & 1, abort_flag, a.dev_err);
+                    ok = role_wait(&bars[Smem::B_SFULL + sb], (it / NS) & 1, abort_flag,
+                                   a.dev_err);
                 if (ok && quad_active) {
                     tc_fence_after();
+                    const uint32_t s_mine = lane_base + sb * TN;
                     const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
                     // a tile's edge: invisible keys' scores become -inf where they are
                     const bool full = key0 + TN <= ctx &&
@@ -777,55 +778,77 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                         tmem_wait_st();
                     }
-                    uint32_t sfw = 0x7f7f7f7fu;  // scale bytes of this lane's blocks
-                    float alpha = 1.f;           // what a moved reference takes off O
-                    bool move = false;
-                    // STEP blocks at a time, their loads together
-                    constexpr int STEP = 1;
-#pragma unroll 1
-                    for (int b0 = blk0 + NBLK - STEP; b0 >= blk0; b0 -= STEP) {
-                        uint32_t r[2 * STEP][16], pw[16];
-                        float x[2 * STEP];
-#pragma unroll
-                        for (int g = 2 * STEP - 1; g >= 0; --g)
-                            tmem_ld16_max(s_mine + b0 * 32 + g * 16, r[g], x[g]);
-                        float4 gs[2 * STEP];
-#pragma unroll
-                        for (int g = 0; g < 2 * STEP; ++g)
-                            gs[g] = sc[(b0 * 32 + g * 16) >> lgCH];
+                    // scores of a block with the whole power of two of its largest w
+                    // (-inf: no visible key); mult is not 0, so that -inf stays -inf
+                    uint32_t r0[16], r1[16];
+                    auto load_block = [&](int blk, float4& s0, float4& s1) {
+                        float x0, x1;
+                        tmem_ld16_max(s_mine + blk * 32, r0, x0);
+                        tmem_ld16_max(s_mine + blk * 32 + 16, r1, x1);
+                        s0 = sc[(blk * 32) >> lgCH];
+                        s1 = sc[(blk * 32 + 16) >> lgCH];
+                        s0.x = fmaxf(qm * s0.x, 1.2e-38f);
+                        s1.x = fmaxf(qm * s1.x, 1.2e-38f);
                         tmem_wait_ld();
+                        return floorf(fmaxf(fmaf(x0, s0.x, s0.y), fmaf(x1, s1.x, s1.y)));
+                    };
+                    float4 s0, s1;
+                    float top = load_block(blk0 + NBLK - 1, s0, s1), most = top;
+                    if (NBLK > 1) {
+#pragma unroll 1
+                        for (int blk = blk0; blk < blk0 + NBLK - 1; ++blk)
+                            most = fmaxf(most, load_block(blk, s0, s1));
+                    }
+                    // the lane's reference, handed from tile to tile through shared
+                    // memory (its two softmax warps alternate)
+                    if (it > 0)
+                        ok = role_wait(&bars[Smem::B_REF + quad], (it - 1) & 1, abort_flag,
+                                       a.dev_err);
+                    const float ref = first ? -INFINITY : s_ref[ln];
+                    const bool move = most > ref + kMoveThreshold;  // also -inf -> finite
+                    const float next = move ? most : ref;
+                    if (first || move) s_ref[ln] = next;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[Smem::B_REF + quad]);
+                    if (next > m) l *= m == -INFINITY ? 0.f : pow2_neg((int)fminf(next - m, 255.f));
+                    m = next;
+                    if (!first && __any_sync(0xffffffffu, move)) {
+                        // a moved reference: O (all of the piece so far, once P V of
+                        // the tile before is done) shrinks with it
+                        if (ok)
+                            ok = role_wait(&bars[Smem::B_SFREE + (it - 1) % NS],
+                                           ((it - 1) / NS) & 1, abort_flag, a.dev_err);
+                        tc_fence_after();
+                        const float alpha =
+                            !move                ? 1.f
+                            : ref == -INFINITY ? 0.f
+                                                 : pow2_neg((int)fminf(next - ref, 255.f));
+#pragma unroll 1
+                        for (int c4 = 0; c4 < D / 16; ++c4) {
+                            uint32_t ov[16];
+                            tmem_ld16(lane_base + TM_O + c4 * 16, ov);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = STEP - 1; e >= 0; --e) {
-                            const int blk = b0 + e;
-                            const float4 s0 = gs[2 * e], s1 = gs[2 * e + 1];
-                            // to log2 units; not 0, so that -inf stays -inf
-                            const float mu0 = fmaxf(qm * s0.x, 1.2e-38f);
-                            const float mu1 = fmaxf(qm * s1.x, 1.2e-38f);
-                            // whole power of two of the block's largest w (-inf: no key)
-                            const float top = floorf(
-                                fmaxf(fmaf(x[2 * e], mu0, s0.y), fmaf(x[2 * e + 1], mu1, s1.y)));
-                            if (top > m_ref + kMoveThreshold) {  // also -inf -> finite
-                                const int d = (int)fminf(top - m_ref, 255.f);
-                                move = true;
-                                alpha *= pow2_neg(d);
-                                l *= pow2_neg(d);
-                                m_ref = top;
-#pragma unroll
-                                for (int b = 0; b < 32; b += 8)  // blocks of this tile so far
-                                    sfw = (sfw & ~(0xffu << b)) |
-                                          (uint32_t)max((int)((sfw >> b) & 0xffu) - d, 0) << b;
-                            }
-                            const float n = fmaxf(top - m_ref, -110.f);  // (NaN: -110)
-                            const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
-                            const float base = top == -INFINITY ? 0.f : 7.f - (m_ref + n);
-                            const float w0 = group_weights(r[2 * e], mu0, base + s0.y,
-                                                           s0.w != 0.f, pw, pw + 8);
-                            const float w1 = group_weights(r[2 * e + 1], mu1, base + s1.y,
-                                                           s1.w != 0.f, pw + 4, pw + 12);
-                            l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
-                            sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
-                            tmem_st16(s_mine + p_col(blk), pw);
+                            for (int e = 0; e < 16; ++e)
+                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                            tmem_st16(lane_base + TM_O + c4 * 16, ov);
                         }
+                    }
+                    uint32_t sfw = 0x7f7f7f7fu;  // scale bytes of this lane's blocks
+#pragma unroll 1
+                    for (int blk = blk0 + NBLK - 1; blk >= blk0; --blk) {
+                        uint32_t pw[16];
+                        if (NBLK > 1) top = load_block(blk, s0, s1);
+                        const float n = fmaxf(top - m, -110.f);  // (NaN without a key: -110)
+                        const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
+                        const float base = top == -INFINITY ? 0.f : 7.f - (m + n);
+                        const float w0 =
+                            group_weights(r0, s0.x, base + s0.y, s0.w != 0.f, pw, pw + 8);
+                        const float w1 =
+                            group_weights(r1, s1.x, base + s1.y, s1.w != 0.f, pw + 4, pw + 12);
+                        l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
+                        sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                        tmem_st16(s_mine + p_col(blk), pw);
                     }
                     if (REP > 1) {  // the blocks of the other copies
                         const uint32_t zero[16] = {};
@@ -833,49 +856,31 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         for (int b = 0; b < 4; ++b)
                             if (b / NBLK != copy) tmem_st16(s_mine + p_col(b), zero);
                     }
-                    *reinterpret_cast<uint32_t*>(sm + Smem::SFP + set * 512 + lane * 16 +
+                    *reinterpret_cast<uint32_t*>(sm + Smem::SFP + sb * 512 + lane * 16 +
                                                  quad * 4) = sfw;
                     fence_proxy_async_smem();
                     tmem_wait_st();
-                    if (has && __any_sync(0xffffffffu, move)) {
-                        // O holds every earlier P V of this set (the S buffer of
-                        // this tile was free only after the previous one read it)
-#pragma unroll 1
-                        for (int c4 = 0; c4 < D / 32; ++c4) {
-                            uint32_t ov[32];
-                            tmem_ld32(lane_base + o_mine + c4 * 32, ov);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                            tmem_st32(lane_base + o_mine + c4 * 32, ov);
-                        }
-                        tmem_wait_st();
-                    }
                 }
                 // P of this tile stored (every warp of the set arrives, active or not)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&bars[Smem::B_PREADY + set]);
+                    mbar_arrive(&bars[Smem::B_PREADY + sb]);
                     mbar_arrive(&bars[Smem::B_SCFREE + it % SCALE_STAGES]);
                 }
-                has = true;
-                ++own;
             }
             if (last) {
-                // ---- epilogue of the piece that ends at this tile: merge the two
-                // sets' (and the copies') (max, sum, O); each set writes half of
-                // the output columns
-                if (ok && has)  // this set's last P V (tile own - 1) is done
-                    ok = role_wait(&bars[Smem::B_SFREE + set], (own - 1) & 1, abort_flag,
+                // ---- epilogue of the piece that ends at this tile: both sets' row
+                // sums and the copies' (reference, O) merge; each set writes half
+                // of the output columns
+                if (ok)  // the piece's last P V is done
+                    ok = role_wait(&bars[Smem::B_SFREE + sb], (it / NS) & 1, abort_flag,
                                    a.dev_err);
-                tc_fence_after();
                 const int64_t tb = ld_shared_s64(s_rng), te = ld_shared_s64(s_rng + 1);
                 const bool complete = cur.seg_start >= tb && cur.seg_start + cur.nb <= te;
                 const int slot = 2 * blockIdx.x + (cur.seg_start < tb ? 0 : 1);
-                s_stat_m[set * ROWS + ln] = has ? m_ref : -INFINITY;
-                s_stat_l[set * ROWS + ln] = has ? l : 0.f;
+                s_stat_m[set * ROWS + ln] = m;
+                s_stat_l[set * ROWS + ln] = l;
                 tc_fence_before();
                 if (REP == 1)
                     named_bar_sync(2 + quad, 64);  // the two sets' warps of this quadrant
@@ -884,31 +889,21 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 tc_fence_after();
                 float mt = -INFINITY, lt = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2 * REP; ++c)
-                    mt = fmaxf(mt, s_stat_m[(c & 1) * ROWS + (c >> 1) * COPY + r]);
+                for (int c = 0; c < REP; ++c) mt = fmaxf(mt, s_ref[c * COPY + r]);
                 const float mt_use = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
                 for (int c = 0; c < 2 * REP; ++c)
                     lt += fast_exp2(s_stat_m[(c & 1) * ROWS + (c >> 1) * COPY + r] - mt_use) *
                           s_stat_l[(c & 1) * ROWS + (c >> 1) * COPY + r];
-                const float inv_l = lt > 0.f ? 1.f / lt : 0.f;
                 const float lse = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
-                const float wm =
-                    has ? fast_exp2(m_ref - mt_use) * inv_l : 0.f;
-                const float wo = fast_exp2(s_stat_m[(1 - set) * ROWS + ln] - mt_use) * inv_l;
-                // this lane's 16 columns from c0 on, both sets weighted
-                auto merged = [&](int c0, float (&o)[16]) {
-                    uint32_t ov[16], ow[16];
-                    tmem_ld16(lane_base + o_mine + c0, ov);
-                    tmem_ld16(lane_base + o_other + c0, ow);
+                // a lane that saw no key has reference -inf: weight 0
+                const float wgt = lt > 0.f ? fast_exp2(s_ref[ln] - mt_use) / lt : 0.f;
+                auto merged = [&](int c0, float (&o)[16]) {  // this lane's share of 16 columns
+                    uint32_t ov[16];
+                    tmem_ld16(lane_base + TM_O + c0, ov);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        // a set without a tile of this piece holds stale O: weight 0
-                        const float a0 = wm > 0.f ? __uint_as_float(ov[e]) * wm : 0.f;
-                        const float a1 = wo > 0.f ? __uint_as_float(ow[e]) * wo : 0.f;
-                        o[e] = a0 + a1;
-                    }
+                    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(ov[e]) * wgt;
                 };
                 auto row_of = [&](int rr) {
                     return ((int64_t)cur.b * k + rr / G) * a.Hq + cur.kvh * G + rr % G;
@@ -992,7 +987,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     }
                 }
                 // every softmax warp has read O: the next piece's P V may overwrite
-                // it, and its statistics these
+                // it, and its references and row sums these
                 tc_fence_before();
                 if (REP == 1)
                     named_bar_sync(2 + quad, 64);
