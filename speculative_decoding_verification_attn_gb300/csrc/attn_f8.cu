@@ -42,7 +42,7 @@
 //    they share each lane's reference, handed on from tile to tile.
 //  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
 //    and 6 TMA of K and of V; 7 P V issue; 12-14 turn the q rows of the next
-//    piece into hi / lo; 15 brings the page scales.  16 warps share the block's
+//    piece into hi / lo; 15 looks up pages and their scales.  16 warps share the block's
 //    64K registers (setmaxnreg: 160, 96, 160, 96).
 //  * Rows: R = k * G query rows are the M side of one MMA.  R <= 64 (REP 2) and
 //    R <= 32 (REP 4): the rows stand REP times and copy c takes the 32-key
@@ -65,18 +65,18 @@ constexpr int ROWS = 128;              // MMA M
 constexpr int THREADS = 16 * 32;
 constexpr int Q_PART = ROWS * D;       // 16 KB: hi or lo of one piece's rows
 constexpr int SLOT_BYTES = TN * D;     // 16 KB: one tile of K or of V
-constexpr int SLOTS = 4;               // of K and of V each
+constexpr int KSLOTS = 5, VSLOTS = 4;  // a K slot is refilled one P V earlier than V's
 constexpr int MAX_CHUNKS = TN / 16;    // page chunks per tile
-constexpr int LOOKAHEAD = 7;           // tiles of block-table entries prefetched
-constexpr int PID_STAGES = LOOKAHEAD + 1;
-// the scale warp takes two tiles at a time (16 lanes each): its block-table
-// entries come SCALE_PAIRS + 2 pairs ahead, the scales SCALE_PAIRS ahead
-constexpr int SCALE_PAIRS = 2;
+// The page warp takes two tiles at a time (16 lanes each): block-table entries
+// PAGE_PAIRS + 2 pairs ahead, scales PAGE_PAIRS ahead; the copies' first rows go
+// to the producers with the latter.
+constexpr int PAGE_PAIRS = 2;
 constexpr int RAW_STAGES = 4;          // pairs of tiles
+constexpr int ROW_STAGES = 16;         // pairs of tiles
 constexpr int SCALE_STAGES = 16;       // tiles
-// row exponents: the q rows of piece j are written when Q K^T of piece j - 2
-// is done; the softmax may then still be NS tiles behind it, at piece j - 5
-constexpr int EXP_STAGES = 8;
+// row exponents: the q rows of piece j are written after the epilogue of piece
+// j - 2, so no stage before j - 1's is still to be read
+constexpr int EXP_STAGES = 4;
 constexpr int MAX_BATCH = 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NS = 3;                   // S buffers
@@ -92,26 +92,28 @@ constexpr int kSplitAlpha = 3;             // tiles charged per segment in the s
 struct Smem {
     static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
     static constexpr int KS = Q + 4 * Q_PART;
-    static constexpr int VS = KS + SLOTS * SLOT_BYTES;
-    static constexpr int RED = VS + SLOTS * SLOT_BYTES;  // [set][quad][32 rows][16] fp32
-    static constexpr int SFP = RED + 2 * 4 * 32 * 16 * 4;  // scale bytes of P, per S buffer
+    static constexpr int VS = KS + KSLOTS * SLOT_BYTES;
+    static constexpr int SFP = VS + VSLOTS * SLOT_BYTES;   // scale bytes of P, per S buffer
     static constexpr int SFV = SFP + NS * 512;             // scale bytes of V: all 1.0
     static constexpr int BARS = SFV + 512;
-    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + SLOTS, B_VFULL = B_KEMPTY + SLOTS,
-                         B_VEMPTY = B_VFULL + SLOTS, B_QFULL = B_VEMPTY + SLOTS,
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KSLOTS,
+                         B_VFULL = B_KEMPTY + KSLOTS, B_VEMPTY = B_VFULL + VSLOTS,
+                         B_QFULL = B_VEMPTY + VSLOTS,
                          B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + NS,
                          B_SFREE = B_PREADY + NS, B_REF = B_SFREE + NS, B_EPI = B_REF + 4,
                          B_DRAIN = B_EPI + 1,
                          B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
-                         B_SCFREE = B_SCALE + SCALE_STAGES, NUM_BARS = B_SCFREE + SCALE_STAGES;
+                         B_SCFREE = B_SCALE + SCALE_STAGES, B_ROWS = B_SCFREE + SCALE_STAGES,
+                         NUM_BARS = B_ROWS + ROW_STAGES;
     static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
     static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
     static constexpr int REF = FIRST + 48;            // reference of each lane
     static constexpr int STAT = REF + ROWS * 4;       // (m, l) of [set][lane]
-    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;  // [2 producers][PID_STAGES][8] int
-    // scale warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8] scales
-    static constexpr int SPIDS = PIDS + 2 * PID_STAGES * MAX_CHUNKS * 4;
-    static constexpr int RAW = SPIDS + RAW_STAGES * 2 * MAX_CHUNKS * 4;
+    // page warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8]
+    // scales, and for the producers [stage][2 tiles][8] cache rows (-1: no copy)
+    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;
+    static constexpr int TROWS = PIDS + RAW_STAGES * 2 * MAX_CHUNKS * 4;
+    static constexpr int RAW = TROWS + ROW_STAGES * 2 * MAX_CHUNKS * 4;
     static constexpr int EXPS = RAW + RAW_STAGES * 4 * MAX_CHUNKS * 4;  // [stage][row] int8
     static constexpr int SCALE = EXPS + EXP_STAGES * ROWS;  // [stage][8] {sk, log2 sv, 1/sv, on}
     static constexpr int CTX = SCALE + SCALE_STAGES * MAX_CHUNKS * 16;
@@ -248,15 +250,18 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     const int lgP = 31 - __clz(P), lgCH = 31 - __clz(CH);  // both powers of two
 
     if (tid == 0) {
-        for (int s = 0; s < SLOTS; ++s) {
+        for (int s = 0; s < KSLOTS; ++s) {
             mbar_init(&bars[Smem::B_KFULL + s], 1);
             mbar_init(&bars[Smem::B_KEMPTY + s], 1);
+        }
+        for (int s = 0; s < VSLOTS; ++s) {
             mbar_init(&bars[Smem::B_VFULL + s], 1);
             mbar_init(&bars[Smem::B_VEMPTY + s], 1);
         }
+        for (int s = 0; s < ROW_STAGES; ++s) mbar_init(&bars[Smem::B_ROWS + s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[Smem::B_QFULL + s], 3);   // the 3 converting warps
-            mbar_init(&bars[Smem::B_QFREE + s], 1);
+            mbar_init(&bars[Smem::B_QFREE + s], 8);   // every softmax warp, after the piece
             mbar_init(&bars[Smem::B_DRAIN + s], 1);
         }
         for (int s = 0; s < NS; ++s) {
@@ -353,8 +358,8 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (warp >= 12) regs_dec<96>();
     if (warp < 4 || (warp >= 8 && warp < 15)) {
         // ================= q rows to hi / lo =================
-        // Piece j into buffer j & 1 (free once the last Q K^T of piece j - 2 is
-        // done), its row exponents into stage j % 8.  16 lanes per row, 8
+        // Piece j into buffer j & 1 (free after the epilogue of piece j - 2, which
+        // merges the copies there), its row exponents into stage j % 4.  16 lanes per row, 8
         // elements each; a negative softmax scale is folded into q's sign.  The
         // first piece, which everything waits for, by the softmax warps too;
         // the others by warps 12-14.
@@ -438,72 +443,45 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     if (warp == 5 || warp == 6) {
         // ================= TMA producers: warp 5 K, warp 6 V =================
         // Tile it goes to slot it % SLOTS of its ring; each page chunk (CH
-        // keys of 128 bytes, swizzled by the copy) is one copy.  Block-table
-        // entries are prefetched LOOKAHEAD tiles ahead.  One warp's latency per
-        // iteration is what a tile can cost here, so the loop does no more.
+        // keys of 128 bytes, swizzled by the copy) is one copy, its first row
+        // of the cache from the page warp.  One warp's latency per iteration is
+        // what a tile can cost here (the copies alone ~50 cycles each), so the
+        // loop does no more.
         const bool is_v = warp == 6;
-        int* pids = reinterpret_cast<int*>(sm + Smem::PIDS) + (is_v ? PID_STAGES * MAX_CHUNKS : 0);
+        const int* rows = reinterpret_cast<const int*>(sm + Smem::TROWS) + (lane & 7);
+        const int slots = is_v ? VSLOTS : KSLOTS;
         uint64_t* full = &bars[is_v ? Smem::B_VFULL : Smem::B_KFULL];
         uint64_t* empty = &bars[is_v ? Smem::B_VEMPTY : Smem::B_KEMPTY];
         uint8_t* ring = sm + (is_v ? Smem::VS : Smem::KS) + ((lane << lgCH) * D);
         const CUtensorMap* map = is_v ? &vmap : &kmap;
-        Cursor cur, ahead;
-        if (n_tiles > 0) {
-            start_at(cur);
-            ahead = cur;
-        }
         const uint64_t pol = l2_policy_evict_first();
         if (lane == 0) prefetch_tmap(map);
-        auto fetch_pids = [&](int t, const Cursor& c) {
-            if (lane < MAX_CHUNKS && chunk_used(c, lane))
-                cp_async_4(&pids[(t % PID_STAGES) * MAX_CHUNKS + lane],
-                           &a.block_table[(int64_t)c.b * a.max_pages +
-                                          ((c.key0() + (lane << lgCH)) >> lgP)]);
-        };
-        for (int la = 0; la < LOOKAHEAD; ++la) {
-            if (la < n_tiles) {
-                fetch_pids(la, ahead);
-                if (la + 1 < n_tiles) ahead.next(s_ctx, a);
-            }
-            cp_async_commit();
-        }
-        int n_issued = 0;
+        int n_issued = 0, s = 0, round = 0;
         bool ok = true;
         for (int it = 0; it < n_tiles && ok; ++it) {
-            if (it + LOOKAHEAD < n_tiles) {
-                fetch_pids(it + LOOKAHEAD, ahead);
-                if (it + LOOKAHEAD + 1 < n_tiles) ahead.next(s_ctx, a);
-            }
-            cp_async_commit();
-            cp_async_wait<LOOKAHEAD>();  // entries of tile `it` (each lane its own)
-            const int s = it % SLOTS;
-            const bool used = lane < MAX_CHUNKS && chunk_used(cur, lane);
-            const int nck = __popc(__ballot_sync(0xffffffffu, used));
-            if (it >= SLOTS)
-                ok = role_wait(&empty[s], ((it / SLOTS) - 1) & 1, abort_flag, a.dev_err);
+            const int p = it >> 1, stage = p % ROW_STAGES;
+            if (!(it & 1))
+                ok = role_wait(&bars[Smem::B_ROWS + stage], (p / ROW_STAGES) & 1, abort_flag,
+                               a.dev_err);
+            const int row = lane < MAX_CHUNKS ? rows[(2 * stage + (it & 1)) * MAX_CHUNKS] : -1;
+            const int nck = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (ok && round > 0)
+                ok = role_wait(&empty[s], (round - 1) & 1, abort_flag, a.dev_err);
             if (ok && lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)((nck << lgCH) * D));
             __syncwarp();
             if (!ok) break;
-            if (used) {
-                int page = pids[(it % PID_STAGES) * MAX_CHUNKS + lane];
-                if (page < 0 || page >= a.num_pages) {
-                    raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
-                    page = 0;
-                }
-                tma_load_2d(ring + s * SLOT_BYTES, map, &full[s], 0,
-                            ((page * Hkv + cur.kvh) << lgP) +
-                                ((cur.key0() + (lane << lgCH)) & (P - 1)),
-                            pol);
-            }
+            if (row >= 0) tma_load_2d(ring + s * SLOT_BYTES, map, &full[s], 0, row, pol);
             n_issued = it + 1;
+            if (++s == slots) {
+                s = 0;
+                ++round;
+            }
             __syncwarp();
-            if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
-        cp_async_wait<0>();
         if (!ok && lane == 0) {
             // the latest copy into each slot lands before the CTA exits
-            for (int j = max(0, n_issued - SLOTS); j < n_issued; ++j)
-                mbar_drain(&full[j % SLOTS], (j / SLOTS) & 1);
+            for (int j = max(0, n_issued - slots); j < n_issued; ++j)
+                mbar_drain(&full[j % slots], (j / slots) & 1);
         }
     } else if (warp == 4) {
         // ================= Q K^T issue =================
@@ -516,8 +494,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const uint64_t kdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::KS), 16, 1024);
             for (int it = 0; it < n_tiles && ok; ++it) {
                 const bool first = (it == 0) || (cur.lt == 0);
-                const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
-                const int s = it % NS, slot = it % SLOTS;
+                const int s = it % NS, slot = it % KSLOTS;
                 if (first) {
                     ++pc;
                     ok = role_wait(&bars[Smem::B_QFULL + (pc & 1)], (pc >> 1) & 1, abort_flag,
@@ -525,7 +502,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     if (!ok) break;
                 }
                 // K of tile it landed; S buffer s free (P V of tile it - NS done)
-                ok = role_wait(&bars[Smem::B_KFULL + slot], (it / SLOTS) & 1, abort_flag,
+                ok = role_wait(&bars[Smem::B_KFULL + slot], (it / KSLOTS) & 1, abort_flag,
                                a.dev_err);
                 if (ok && it >= NS)
                     ok = role_wait(&bars[Smem::B_SFREE + s], (it / NS - 1) & 1, abort_flag,
@@ -540,7 +517,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                                  kd + (kk & 3) * 2, umma_idesc_e4m3(ROWS, TN), kk ? 1u : 0u);
                 umma_commit_w(&bars[Smem::B_SFULL + s]);
                 umma_commit_w(&bars[Smem::B_KEMPTY + slot]);
-                if (last) umma_commit_w(&bars[Smem::B_QFREE + (pc & 1)]);
                 if (it + 1 < n_tiles) cur.next(s_ctx, a);
             }
             // every tensor-core op of this warp finishes before TMEM is released
@@ -562,7 +538,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             const uint64_t sfv = umma_sdesc_plain(smem_u32(sm + Smem::SFV), 128);
             for (int it = 0; it < n_tiles && ok; ++it) {
                 const bool first = (it == 0) || (cur.lt == 0);
-                const int s = it % NS, slot = it % SLOTS;
+                const int s = it % NS, slot = it % VSLOTS;
                 const int ctx = s_ctx[cur.b], key0 = cur.key0();
                 const int nvalid = min(TN, ctx + k - key0), nkb = (nvalid + 31) / 32;
                 if (first) {
@@ -573,7 +549,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         ok = role_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
                     if (!ok) break;
                 }
-                ok = role_wait(&bars[Smem::B_VFULL + slot], (it / SLOTS) & 1, abort_flag,
+                ok = role_wait(&bars[Smem::B_VFULL + slot], (it / VSLOTS) & 1, abort_flag,
                                a.dev_err);
                 if (!ok) break;
                 // rows that no query sees and a P V reads: zero, so that 0 * (stale,
@@ -624,11 +600,13 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     }
     } else if (warp >= 12) {
     if (warp == 15) {
-        // ================= page scales =================
-        // Two tiles per iteration, 16 lanes each (8 chunks of K, 8 of V):
-        // {sk, log2 sv, 1 / sv, on} of tile it into stage it % SCALE_STAGES,
-        // free once its softmax set has taken it.
-        int* pids = reinterpret_cast<int*>(sm + Smem::SPIDS);
+        // ================= pages: rows of the copies, scales =================
+        // Two tiles per iteration, 16 lanes each (8 chunks of K, 8 of V).  Rows
+        // of pair p to stage p % ROW_STAGES, {sk, log2 sv, 1 / sv, on} of tile
+        // it to stage it % SCALE_STAGES once its softmax set has freed that;
+        // by then the producers are past the rows ROW_STAGES pairs back.
+        int* pids = reinterpret_cast<int*>(sm + Smem::PIDS);
+        int* rows = reinterpret_cast<int*>(sm + Smem::TROWS);
         float* raw = reinterpret_cast<float*>(sm + Smem::RAW);
         const int half = lane >> 4, l = lane & 7;
         const bool is_v = lane & 8;
@@ -646,40 +624,54 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 if (++t < n_tiles) c.next(s_ctx, a);
         };
         auto fetch_pids = [&](int p) {  // pair p
+            if (p >= pairs) return;
             if (t_pid < n_tiles && !is_v && chunk_used(c_pid, l))
                 cp_async_4(&pids[((p % RAW_STAGES) * 2 + half) * MAX_CHUNKS + l],
                            &a.block_table[(int64_t)c_pid.b * a.max_pages +
                                           ((c_pid.key0() + (l << lgCH)) >> lgP)]);
             advance(c_pid, t_pid);
         };
-        auto fetch_scales = [&](int p) {
+        auto fetch_scales = [&](int p) {  // and the rows (entries of pair p landed)
+            if (p >= pairs) return;
+            int row = -1;
             if (t_sc < n_tiles) {
                 float* dst = raw + (p % RAW_STAGES) * 32 + lane;
                 if (chunk_used(c_sc, l)) {
                     int page = pids[((p % RAW_STAGES) * 2 + half) * MAX_CHUNKS + l];
-                    if (page < 0 || page >= a.num_pages) page = 0;  // flagged with its copy
-                    cp_async_4(dst, src + (int64_t)page * Hkv + c_sc.kvh);
+                    if (page < 0 || page >= a.num_pages) {
+                        raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
+                        page = 0;
+                    }
+                    row = page * Hkv + c_sc.kvh;
+                    cp_async_4(dst, src + row);
+                    row = (row << lgP) + ((c_sc.key0() + (l << lgCH)) & (P - 1));
                 } else {
                     *dst = 1.f;
                 }
             }
+            if (!is_v) rows[((p % ROW_STAGES) * 2 + half) * MAX_CHUNKS + l] = row;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[Smem::B_ROWS + p % ROW_STAGES]);
             advance(c_sc, t_sc);
         };
         // groups: the entries of pairs 0 and 1, then scales p with entries p + 2
         fetch_pids(0);
-        if (pairs > 1) fetch_pids(1);
+        fetch_pids(1);
         cp_async_commit();
         cp_async_wait<0>();
         __syncwarp();
-        for (int p = 0; p < SCALE_PAIRS; ++p) {
-            if (p < pairs) fetch_scales(p);
-            if (p + 2 < pairs) fetch_pids(p + 2);
+        for (int p = 0; p < PAGE_PAIRS; ++p) {
+            fetch_scales(p);
+            fetch_pids(p + 2);
             cp_async_commit();
         }
         bool ok = true;
         for (int p = 0; p < pairs && ok; ++p) {
-            cp_async_wait<SCALE_PAIRS - 1>();  // scales p, entries p + 2
+            cp_async_wait<PAGE_PAIRS - 1>();  // scales p, entries p + 2
             __syncwarp();
+            fetch_scales(p + PAGE_PAIRS);
+            fetch_pids(p + PAGE_PAIRS + 2);
+            cp_async_commit();
             for (int e = 0; e < 2 && ok; ++e) {
                 const int t = 2 * p + e;
                 if (t < n_tiles && t >= SCALE_STAGES)
@@ -699,9 +691,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             __syncwarp();
             if ((lane & 15) == 0 && t < n_tiles)
                 mbar_arrive(&bars[Smem::B_SCALE + t % SCALE_STAGES]);
-            if (p + SCALE_PAIRS < pairs) fetch_scales(p + SCALE_PAIRS);
-            if (p + SCALE_PAIRS + 2 < pairs) fetch_pids(p + SCALE_PAIRS + 2);
-            cp_async_commit();
         }
         cp_async_wait<0>();
     }
@@ -721,7 +710,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         float* s_stat_m = reinterpret_cast<float*>(sm + Smem::STAT);
         float* s_stat_l = s_stat_m + 2 * ROWS;
         float* s_ref = reinterpret_cast<float*>(sm + Smem::REF);
-        float* red = reinterpret_cast<float*>(sm + Smem::RED) + set * 4 * 32 * 16;
         float m = -INFINITY, l = 0.f;  // reference that the row sum l of this set stands to
         float qm = 0.f;         // accumulator units to log2 units, before the page's scale
         int low = 0;            // first key of this row's window
@@ -935,33 +923,35 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                         }
                     }
                 } else {
-                    // 16 columns at a time: every copy's share to shared memory,
-                    // then the set's threads sum the copies (row t / 4 of each
-                    // 32-row group, 4 columns); 4-column groups are swizzled by
-                    // the row
-                    const int t = quad * 32 + lane, rr = t >> 2, cg = t & 3;
+                    // 32 columns at a time: every copy's share to the piece's q
+                    // buffer (its Q K^T are done), then the set's threads sum the
+                    // copies (row t / 8 of each 16-row group, 4 columns); 4-column
+                    // groups are swizzled by the row
+                    float* red = reinterpret_cast<float*>(sm + Smem::Q + (pc & 1) * 2 * Q_PART) +
+                                 set * ROWS * 32;
+                    const int t = quad * 32 + lane, rr = t >> 3, cg = t & 7;
 #pragma unroll 1
-                    for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
+                    for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 32) {
                         if (ok && quad_active) {
-                            float o[16];
-                            merged(c0, o);
-                            float4* dst = reinterpret_cast<float4*>(red + (quad * 32 + lane) * 16);
+                            float4* dst = reinterpret_cast<float4*>(red + t * 32);
 #pragma unroll
-                            for (int v4 = 0; v4 < 4; ++v4)
-                                dst[v4 ^ ((lane >> 1) & 3)] = make_float4(
-                                    o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+                            for (int h = 0; h < 2; ++h) {
+                                float o[16];
+                                merged(c0 + 16 * h, o);
+#pragma unroll
+                                for (int v4 = 0; v4 < 4; ++v4)
+                                    dst[(4 * h + v4) ^ (lane & 7)] = make_float4(
+                                        o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
+                            }
                         }
                         named_bar_sync(3 + set, 128);
-#pragma unroll
-                        for (int rb = 0; rb < COPY / 32; ++rb) {
-                            const int row = rb * 32 + rr;
-                            if (!ok || row >= R) continue;
+#pragma unroll 1
+                        for (int row = rr; row < (ok ? R : 0); row += 16) {
                             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                             for (int c = 0; c < REP; ++c) {
-                                const int qd = c * (COPY / 32) + rb;
                                 const float4 x = reinterpret_cast<const float4*>(
-                                    red + (qd * 32 + rr) * 16)[cg ^ ((rr >> 1) & 3)];
+                                    red + (c * COPY + row) * 32)[cg ^ (row & 7)];
                                 acc.x += x.x;
                                 acc.y += x.y;
                                 acc.z += x.z;
@@ -994,7 +984,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 else
                     named_bar_sync(2, 256);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[Smem::B_EPI]);
+                if (lane == 0) {
+                    mbar_arrive(&bars[Smem::B_EPI]);
+                    mbar_arrive(&bars[Smem::B_QFREE + (pc & 1)]);
+                }
             }
             if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
