@@ -87,7 +87,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the reference moves when a block's largest w exceeds it by more than this
 // (log2 units): the block scales carry any distance below, fp32 sums this one
 constexpr float kMoveThreshold = 40.f;
-constexpr int kSplitAlpha = 3;             // tiles charged per segment in the split
+// tiles charged per segment in the split (ragged 8B step: 83, 71.2, 69.7, 67.2,
+// 67.0 us at 0, 2, 3, 4, 6; a piece end costs 3.7 us, a tile 0.9)
+constexpr int kSplitAlpha = 4;
 
 struct Smem {
     static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
@@ -244,7 +246,9 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     float4* s_scale = reinterpret_cast<float4*>(sm + Smem::SCALE);
     int8_t* s_exp = reinterpret_cast<int8_t*>(sm + Smem::EXPS);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // (shuffled: the roles' branches and operands stay in uniform registers)
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int B = a.B, k = a.k, Hkv = a.Hkv, G = a.Hq / a.Hkv, R = k * G, P = a.P;
     const int CH = P < TN ? P : TN;      // keys per page chunk
     const int lgP = 31 - __clz(P), lgCH = 31 - __clz(CH);  // both powers of two
@@ -332,7 +336,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int64_t T = (int64_t)s_pre[B] * Hkv;
     const int64_t t_begin = ld_shared_s64(s_rng);
     const int n_tiles = (int)(ld_shared_s64(s_rng + 1) - t_begin);
@@ -511,10 +515,13 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 tc_fence_after();
                 const uint64_t qd = qdesc0 + ((uint32_t)((pc & 1) * 2 * Q_PART) >> 4);
                 const uint64_t kd = kdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
-#pragma unroll 1
-                for (int kk = 0; kk < 8; ++kk)  // hi, then lo, in 32-byte steps
-                    umma_f8_ss_w(tmem + s * TN, qd + (kk >> 2) * (Q_PART >> 4) + (kk & 3) * 2,
-                                 kd + (kk & 3) * 2, umma_idesc_e4m3(ROWS, TN), kk ? 1u : 0u);
+                if (elect_lane()) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)  // hi, then lo, in 32-byte steps
+                        umma_f8_ss(tmem + s * TN, qd + (kk >> 2) * (Q_PART >> 4) + (kk & 3) * 2,
+                                   kd + (kk & 3) * 2, umma_idesc_e4m3(ROWS, TN), kk ? 1u : 0u);
+                }
+                __syncwarp();
                 umma_commit_w(&bars[Smem::B_SFULL + s]);
                 umma_commit_w(&bars[Smem::B_KEMPTY + slot]);
                 if (it + 1 < n_tiles) cur.next(s_ctx, a);
@@ -580,14 +587,17 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O;
                 tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
                 tmem_cp_scales_w(sbuf + SF_V, sfv);
+                if (elect_lane()) {
 #pragma unroll 1
-                for (int j = 0; j < nkb; ++j) {
-                    const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
-                    const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, j);
-                    umma_mx_ts_w(od, sbuf + p_col(j), vj, id, sbuf + SF_P, sbuf + SF_V,
-                                 (!first || j > 0) ? 1u : 0u);
-                    umma_mx_ts_w(od, sbuf + p_col(j) + 8, vj, id, sbuf + SF_P, sbuf + SF_V, 1u);
+                    for (int j = 0; j < nkb; ++j) {
+                        const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
+                        const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, j);
+                        umma_mx_ts(od, sbuf + p_col(j), vj, id, sbuf + SF_P, sbuf + SF_V,
+                                   (!first || j > 0) ? 1u : 0u);
+                        umma_mx_ts(od, sbuf + p_col(j) + 8, vj, id, sbuf + SF_P, sbuf + SF_V, 1u);
+                    }
                 }
+                __syncwarp();
                 umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
                 umma_commit_w(&bars[Smem::B_SFREE + s]);
                 if (it + 1 < n_tiles) cur.next(s_ctx, a);

@@ -210,27 +210,37 @@ __device__ __forceinline__ void tmem_cp_128x256b_w(uint32_t taddr, uint64_t sdes
         : "memory");
 }
 
-// 8-bit floating operands (K = 32 per instruction).  umma_f8_ss_w: A and B from
-// shared memory, unscaled.  umma_mx_ts_w: A from TMEM (4 elements per column)
-// with a power-of-two scale for each row and 32 elements of K: scale bytes
-// (exponent + 127) in TMEM, row r at lane r % 32, column sf_a + r / 32, the
-// byte that the instruction descriptor selects; the same for B's columns.
-__device__ __forceinline__ void umma_f8_ss_w(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// One lane of a converged warp (the compiler keeps the branch uniform), for a
+// batch of issue instructions: eight MMAs behind one election issue in ~120
+// cycles, with one election each in ~210 to ~290.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t r;
     asm volatile(
-        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// 8-bit floating operands (K = 32 per instruction), by the elected lane.
+// umma_f8_ss: A and B from shared memory, unscaled.  umma_mx_ts: A from TMEM (4
+// elements per column) with a power-of-two scale for each row and 32 elements
+// of K: scale bytes (exponent + 127) in TMEM, row r at lane r % 32, column sf_a
+// + r / 32, the byte that the instruction descriptor selects; the same for B's
+// columns.
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void umma_mx_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                             uint32_t idesc, uint32_t sf_a, uint32_t sf_b,
-                                             uint32_t accumulate) {
+__device__ __forceinline__ void umma_mx_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t sf_a, uint32_t sf_b,
+                                           uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred e, p;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X "
         "[%0], [%1], %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(sf_a), "r"(sf_b), "r"(accumulate)
         : "memory");

@@ -185,6 +185,33 @@ def test_e4m3_one_key_outweighs_the_rest(binding):
     assert out.float().min() > 1e-3  # 2048 keys of e^-14.1: the light keys' share
 
 
+@pytest.mark.parametrize("qscale", [1e-30, 0.02, 20.0, 200.0])
+@pytest.mark.parametrize("k,Hq,Hkv", [(4, 8, 2), (8, 16, 2), (16, 28, 4)])
+def test_e4m3_score_ranges(binding, k, Hq, Hkv, qscale):
+    """Scores that lie hundreds apart from tile to tile (every reference moves,
+    both up and past the block scales' range) and scores that hardly differ."""
+    check_attn(binding, attn_case(61, "e4m3", torch.bfloat16, 2, k, Hq, Hkv, 128, 16,
+                                  [1500, 333], qscale=qscale))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("k,Hq,Hkv", [(2, 8, 2), (8, 16, 2), (16, 28, 4)])
+def test_e4m3_rising_and_falling_scores(binding, k, Hq, Hkv, order):
+    """Keys whose scores climb (or fall) by 30 in the exponent every 100 keys."""
+    c = attn_case(62, "e4m3", torch.bfloat16, 1, k, Hq, Hkv, 128, 32, [1300])
+    q = 0.3 * c["q"]
+    q[..., 0] = 8.0
+    c["q"] = q
+    x = c["kc"].float() / 448.0
+    for j in range(1300 + k):
+        at = j if order > 0 else 1300 - j
+        x[int(c["table"][0, j // 32]), :, j % 32, 0] = float(at // 100) * 40.0
+    x = torch.nan_to_num(x)
+    c["ks"] = x.abs().amax((2, 3)).clamp(min=0.01) / 448.0
+    c["kc"] = (x / c["ks"][:, :, None, None]).to(E4M3)
+    check_attn(binding, c)
+
+
 def test_e4m3_descriptor_form(binding):
     c = attn_case(2, "e4m3", torch.bfloat16, 2, 4, 8, 2, 128, 16, [60, 200])
     out, lse = check_attn(binding, c)
