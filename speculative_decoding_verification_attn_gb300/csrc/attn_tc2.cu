@@ -482,12 +482,15 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     // in every 8-key group), 32-byte step kk%4
                     const uint64_t qd = qdesc0 + ((uint32_t)((pc & 1) * Q_BYTES) >> 4);
                     const uint64_t kd = kdesc0 + ((uint32_t)(s * SLOT_BYTES) >> 4);
+                    if (elect_lane()) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_ss_w(tmem + TM_S + s * TN,
-                                  qd + (kk >> 2) * (Q_HALF >> 4) + (kk & 3) * 2,
-                                  kd + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, idesc_qk<KV8>(),
-                                  kk ? 1u : 0u);
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_ss(tmem + TM_S + s * TN,
+                                    qd + (kk >> 2) * (Q_HALF >> 4) + (kk & 3) * 2,
+                                    kd + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, idesc_qk<KV8>(),
+                                    kk ? 1u : 0u);
+                    }
+                    __syncwarp();
                     umma_commit_w(&bars[Smem::B_SFULL + s]);
                     umma_commit_w(&bars[Smem::B_KEMPTY + s]);
                     if (last) umma_commit_w(&bars[Smem::B_QFREE + (pc & 1)]);
@@ -567,12 +570,15 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
                     const bool hs = s ? has1 : has0;
                     const uint32_t sbuf = tmem + TM_S + s * TN;
                     const uint32_t od = tmem + TM_O + s * D;
+                    if (elect_lane()) {
 #pragma unroll
-                    for (int j = 0; j < NVB; ++j)
-                        if (j < nvb)
-                            umma_ts_w(od, sbuf + (j < 4 ? 8 * j : 64 + 8 * (j - 4)),
-                                      vd + ((uint32_t)(j * 4096) >> 4), idesc_pv<KV8>(),
-                                      (hs || j > 0) ? 1u : 0u);
+                        for (int j = 0; j < NVB; ++j)
+                            if (j < nvb)
+                                umma_ts(od, sbuf + (j < 4 ? 8 * j : 64 + 8 * (j - 4)),
+                                        vd + ((uint32_t)(j * 4096) >> 4), idesc_pv<KV8>(),
+                                        (hs || j > 0) ? 1u : 0u);
+                    }
+                    __syncwarp();
                     umma_commit_w(&bars[Smem::B_VEMPTY + s]);
                     umma_commit_w(&bars[Smem::B_SFREE + s]);
                 }
