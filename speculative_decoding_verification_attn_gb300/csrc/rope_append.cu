@@ -9,7 +9,8 @@
 // The table holds f_j / 2 pi as a 64-bit binary fraction of a turn, so that
 // p * table[j] modulo 2^64 is the angle reduced exactly, however far the
 // position: one integer product instead of a 64-bit floating reduction.  Its
-// upper 32 bits go to sincospif (angle error below 2^-24 turns of rounding).
+// upper 32 bits go to sincospif, and what their rounding to fp32 leaves out (up
+// to 2^-25 turns) back by the first-order terms of the angle sum.
 //
 // The cache rows: f32 / bf16 as they are (bf16 rounded once, to nearest
 // even); i8 as in kv_append.cu; e4m3 with one scale per (page, kv-head):
@@ -27,11 +28,11 @@
 //  * row CTAs: a warp takes one token and a run of its heads (q, and k / v of
 //    the caches whose rows are independent), the token's cosines and sines in
 //    registers for all of them;
-//  * page CTAs (e4m3): a warp takes one (page, kv-head) of k or of v, whose
-//    rows share a scale; the CTA's warps share the cosines and sines of its
-//    16 tokens in shared memory.  Up to 16 rows stay in registers between the
-//    maximum and the codes; a longer page is read twice (the second time from
-//    L1 / L2).
+//  * page CTAs (e4m3): two warps take one (page, kv-head) of k or of v, whose
+//    rows share a scale, half of the rows each; the CTA's warps share the
+//    cosines and sines of its 16 tokens in shared memory.  Up to 16 rows stay in
+//    registers between the maximum and the codes; a longer page is read twice
+//    (the second time from L1 / L2).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -41,7 +42,9 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kRowBlock = 16;  // tokens of a page CTA's table (at most)
+constexpr int kPageHeads = kWarps / 2;  // heads of a page CTA
 constexpr int kMaxPairs = 128;
+enum { kF32, kBf16, kI8, kPages };
 
 struct RopeParams {
     RopeAppendArgs a;
@@ -132,27 +135,31 @@ __device__ __forceinline__ void e4m3x8_to_f32(uint2 w, float (&x)[8]) {
     }
 }
 
-// (cos, sin) of pair j at position p, times the amplitude
-__device__ __forceinline__ float2 turn(const RopeAppendArgs& a, int64_t p, int j) {
-    const uint64_t t = (uint64_t)p * (uint64_t)__ldg(a.table + j);
+// (cos, sin) of the angle p * freq (64-bit fraction of a turn), times amplitude
+__device__ __forceinline__ float2 turn(int64_t p, uint64_t freq, float amplitude) {
+    const int32_t t = (int32_t)(((uint64_t)p * freq) >> 32);
+    const float x = __int2float_rz(t);  // at most 2^31 - 128: back to an int exactly
+    const float rest = (float)(t - (int32_t)x) * (0x1p-31f * 3.14159265358979f);
     float s, c;
-    sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c * a.amplitude, s * a.amplitude);
+    sincospif(x * 0x1p-31f, &s, &c);
+    return make_float2((c - s * rest) * amplitude, (s + c * rest) * amplitude);
 }
 
 // The first pair of the 8 elements from e0 on, in the layout's order (halves:
 // 8 pairs, interleaved: 4), or -1 when they are not rotated
-__device__ __forceinline__ int first_pair(const RopeAppendArgs& a, int e0) {
+template <bool INTER> __device__ __forceinline__ int first_pair(const RopeAppendArgs& a, int e0) {
     if (e0 >= a.rot) return -1;
-    return a.interleaved ? e0 / 2 : e0 % (a.rot / 2);
+    return INTER ? e0 / 2 : e0 < a.rot / 2 ? e0 : e0 - a.rot / 2;
 }
 
 // Rotates a lane's 8 elements (from e0 on) in place.  `other` holds the
-// partner's 8 elements (halves); cs the pairs' (cos, sin).
+// partner's 8 elements (halves); cs the pairs' (cos, sin), in the lower half
+// of a half layout (cos, -sin).
+template <bool INTER, int N>
 __device__ __forceinline__ void rotate8(const RopeAppendArgs& a, int e0, float (&x)[8],
-                                        const float (&other)[8], const float2 (&cs)[8]) {
+                                        const float (&other)[8], const float2 (&cs)[N]) {
     if (e0 >= a.rot) return;
-    if (a.interleaved) {
+    if constexpr (INTER) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float u = x[2 * e], v = x[2 * e + 1];
@@ -160,15 +167,14 @@ __device__ __forceinline__ void rotate8(const RopeAppendArgs& a, int e0, float (
             x[2 * e + 1] = u * cs[e].y + v * cs[e].x;
         }
     } else {
-        const float sign = e0 < a.rot / 2 ? -1.f : 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[e].x + sign * other[e] * cs[e].y;
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * cs[e].x + other[e] * cs[e].y;
     }
 }
 
-// lane offset (in 8-element chunks) of the partner of a half-layout chunk
+// lane that holds the partner of a half-layout chunk (8 elements per lane)
 __device__ __forceinline__ int partner_lane(const RopeAppendArgs& a, int lane, int e0) {
-    if (a.interleaved || e0 >= a.rot) return lane;
+    if (e0 >= a.rot) return lane;
     return e0 < a.rot / 2 ? lane + a.rot / 16 : lane - a.rot / 16;
 }
 
@@ -194,80 +200,46 @@ __device__ __forceinline__ int new_len(const RopeAppendArgs& a, int b) {
 }
 
 // ---------------------------------------------------------------- row CTAs
-template <typename T>
-__device__ __forceinline__ void row_cta(const RopeParams& p) {
-    const RopeAppendArgs& a = p.a;
+// The rows of one kind (q, k or v) of a token's heads [h0, h1): U of a lane's
+// rows in flight, rotated, and stored `head_stride` elements apart.
+template <typename T, typename TD, bool INTER, bool I8, int N>
+__device__ __forceinline__ void token_rows(const RopeAppendArgs& a, int lr_log2, const T* src,
+                                           TD* dst, int64_t head_stride, uint16_t* scale, int h0,
+                                           int h1, bool spin, const float2 (&cs)[N]) {
     const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t token = item / p.groups;
-    const int group = (int)(item % p.groups);
-    if (token >= (int64_t)a.B * a.n) return;
-    const int b = (int)(token / a.n), t = (int)(token % a.n);
-    if (t >= new_len(a, b)) return;
-    const int lr = 1 << p.lr_log2, rows = 32 >> p.lr_log2;  // lanes of a row, rows at a time
+    const int lr = 1 << lr_log2, rows = 32 >> lr_log2;  // lanes of a row, rows at a time
     const int e0 = (lane & (lr - 1)) * 8;
     const bool in_row = e0 < a.D;
-    const int h_begin = group * p.heads_per_warp;
-    const int h_end = min(p.heads, h_begin + p.heads_per_warp);
-    const int64_t pos = (int64_t)__ldg(a.ctx_lens + b) + t;
-    // the cache row of a warp that holds k or v heads
-    int page = -1;
-    if (h_end > a.Hq) page = find_page(a, b, pos, lane == 0);
-    float2 cs[8];
-    const int j0 = in_row ? first_pair(a, e0) : -1;
-    if (j0 >= 0 && h_begin < a.Hq + a.Hkv) {
-        const int64_t at = a.positions ? (int64_t)__ldg(a.positions + token) : pos;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < 4 || !a.interleaved) cs[e] = turn(a, at, j0 + e);
-    }
-    constexpr int U = 4;  // rows in flight per lane
-    for (int h0 = h_begin; h0 < h_end; h0 += rows * U) {
+    const int from = in_row ? partner_lane(a, lane, e0) : lane;
+    constexpr int U = 4;
+    for (int hb = h0; hb < h1; hb += rows * U) {
         Chunk<T> c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * rows + (lane >> p.lr_log2);
+            const int h = hb + u * rows + (lane >> lr_log2);
             c[u].zero();
-            if (h < h_end && in_row) {
-                const T* src =
-                    h < a.Hq ? static_cast<const T*>(a.q) + token * a.q_stride + (int64_t)h * a.D
-                    : h < a.Hq + a.Hkv
-                        ? static_cast<const T*>(a.k_new) + token * a.k_stride +
-                              (int64_t)(h - a.Hq) * a.D
-                        : static_cast<const T*>(a.v_new) + token * a.v_stride +
-                              (int64_t)(h - a.Hq - a.Hkv) * a.D;
-                c[u].load(src + e0);
-            }
+            if (h < h1 && in_row) c[u].load(src + h * a.D + e0);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (h0 + u * rows >= h_end) continue;  // uniform over the warp
-            const int h = h0 + u * rows + (lane >> p.lr_log2);
-            const bool mine = h < h_end && in_row;
-            float x[8], o[8];
+            if (hb + u * rows >= h1) break;  // uniform over the warp
+            const int h = hb + u * rows + (lane >> lr_log2);
+            const bool mine = h < h1 && in_row;
+            float x[8];
             c[u].get(x);
-            if (!a.interleaved && a.rot > 0)
-                c[u].from_lane(in_row ? partner_lane(a, lane, e0) : lane).get(o);
-            if (mine && h < a.Hq + a.Hkv) rotate8(a, e0, x, o, cs);
-            if (mine && h < a.Hq)
-                store8(static_cast<T*>(a.q_out) + token * a.q_out_stride + (int64_t)h * a.D + e0, x);
-            if (h0 + (u + 1) * rows <= a.Hq || p.heads == a.Hq) continue;  // q alone; uniform
-            // k / v rows (q rows may stand beside them in the warp)
-            const bool is_v = h >= a.Hq + a.Hkv;
-            const int g = is_v ? h - a.Hq - a.Hkv : h - a.Hq;
-            const bool put = mine && h >= a.Hq && page >= 0;
-            const int64_t row = ((int64_t)page * a.Hkv + g) * a.P + pos % a.P;
-            void* cache = is_v ? a.v_cache : a.k_cache;
-            if (a.cache_dtype == SPEC_DTYPE_BF16) {
-                if (put) store8(static_cast<__nv_bfloat16*>(cache) + row * a.D + e0, x);
-            } else if (a.cache_dtype == SPEC_DTYPE_F32) {
-                if (put) store8(static_cast<float*>(cache) + row * a.D + e0, x);
+            if (spin) {
+                float o[8];
+                if constexpr (!INTER) c[u].from_lane(from).get(o);
+                rotate8<INTER>(a, e0, x, o, cs);
+            }
+            if constexpr (!I8) {
+                if (mine) store8(dst + h * head_stride + e0, x);
             } else {
-                // i8: one scale per (token, kv-head) row
+                // one scale per (token, kv-head) row
                 float amax = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-                if (!mine) amax = 0.f;
+                if (!in_row) amax = 0.f;
                 for (int off = lr / 2; off > 0; off >>= 1)
                     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
                 const __half s16 = __float2half_rn(__fdiv_rn(amax, 127.0f));
@@ -279,24 +251,113 @@ __device__ __forceinline__ void row_cta(const RopeParams& p) {
                     if (s > 0.f) v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -127.f), 127.f);
                     w[e >> 2] |= (uint32_t)(uint8_t)(int8_t)v << (8 * (e & 3));
                 }
-                if (put) {
-                    *reinterpret_cast<uint2*>(static_cast<int8_t*>(cache) + row * a.D + e0) =
-                        make_uint2(w[0], w[1]);
-                    if (e0 == 0)
-                        static_cast<uint16_t*>(is_v ? a.v_scale : a.k_scale)[row] =
-                            __half_as_ushort(s16);
+                if (mine) {
+                    *reinterpret_cast<uint2*>(dst + h * head_stride + e0) = make_uint2(w[0], w[1]);
+                    if (e0 == 0) scale[(int64_t)h * a.P] = __half_as_ushort(s16);
                 }
             }
         }
     }
 }
 
+template <typename T, bool INTER, int MODE>
+__device__ __forceinline__ void row_cta(const RopeParams& p, int64_t block) {
+    const RopeAppendArgs& a = p.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t item = block * kWarps + (threadIdx.x >> 5);
+    const int64_t token = item / p.groups;
+    const int group = (int)(item % p.groups);
+    if (token >= (int64_t)a.B * a.n) return;
+    const int b = (int)(token / a.n), t = (int)(token % a.n);
+    const int64_t pos = (int64_t)__ldg(a.ctx_lens + b) + t;
+    if (t >= new_len(a, b)) return;
+    const int e0 = (lane & ((1 << p.lr_log2) - 1)) * 8;
+    const int h_begin = group * p.heads_per_warp;
+    const int h_end = min(p.heads, h_begin + p.heads_per_warp);
+    // the cache row of a warp that holds k or v heads
+    int page = -1;
+    if (MODE != kPages && h_end > a.Hq) page = find_page(a, b, pos, lane == 0);
+    constexpr int N = INTER ? 4 : 8;
+    float2 cs[N];
+    const int j0 = e0 < a.D ? first_pair<INTER>(a, e0) : -1;
+    const bool spin = a.rot > 0 && h_begin < a.Hq + a.Hkv;
+    if (spin && j0 >= 0) {
+        const int64_t at = a.positions ? (int64_t)__ldg(a.positions + token) : pos;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            cs[e] = turn(at, __ldg(a.table + j0 + e), a.amplitude);
+            if (!INTER && e0 < a.rot / 2) cs[e].y = -cs[e].y;
+        }
+    }
+    if (h_begin < a.Hq)
+        token_rows<T, T, INTER, false>(
+            a, p.lr_log2, static_cast<const T*>(a.q) + token * a.q_stride,
+            static_cast<T*>(a.q_out) + token * a.q_out_stride, a.D, nullptr, h_begin,
+            min(h_end, a.Hq), spin, cs);
+    if (MODE == kPages || page < 0) return;
+    const int64_t row = (int64_t)page * a.Hkv * a.P + pos % a.P;
+#pragma unroll 1
+    for (int is_v = 0; is_v < 2; ++is_v) {
+        const int first = a.Hq + is_v * a.Hkv;
+        const int h0 = max(0, h_begin - first), h1 = min(h_end - first, a.Hkv);
+        if (h0 >= h1) continue;
+        const T* src = is_v ? static_cast<const T*>(a.v_new) + token * a.v_stride
+                            : static_cast<const T*>(a.k_new) + token * a.k_stride;
+        void* cache = is_v ? a.v_cache : a.k_cache;
+        const int64_t hs = (int64_t)a.P * a.D;
+        if constexpr (MODE == kI8)
+            token_rows<T, int8_t, INTER, true>(
+                a, p.lr_log2, src, static_cast<int8_t*>(cache) + row * a.D, hs,
+                static_cast<uint16_t*>(is_v ? a.v_scale : a.k_scale) + row, h0, h1,
+                spin && !is_v, cs);
+        else if constexpr (MODE == kBf16)
+            token_rows<T, __nv_bfloat16, INTER, false>(
+                a, p.lr_log2, src, static_cast<__nv_bfloat16*>(cache) + row * a.D, hs, nullptr, h0,
+                h1, spin && !is_v, cs);
+        else
+            token_rows<T, float, INTER, false>(a, p.lr_log2, src,
+                                               static_cast<float*>(cache) + row * a.D, hs, nullptr,
+                                               h0, h1, spin && !is_v, cs);
+    }
+}
+
 // ---------------------------------------------------------------- page CTAs (e4m3)
-template <typename T>
-__device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMaxPairs]) {
+// x / s for a fixed positive s, to nearest: with r = 1 / s rounded to nearest,
+// q = x r and the exact remainder x - q s, q + r (x - q s) is the correctly
+// rounded quotient (Markstein's theorem), three instructions per element where
+// a division takes three times as many.  Outside the range where no step
+// underflows the division itself.
+struct Divide {
+    float s, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divide(float by) : s(by) {
+        plain = !(by > 0x1p-96f && by < 0x1p96f);
+        r = plain ? 0.f : __frcp_rn(by);
+    }
+    __device__ __forceinline__ void operator()(float (&x)[8]) const {
+        if (plain) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {  // (rotated: no dynamic index)
+                const float q = s > 0.f ? __fdiv_rn(x[0], s) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 7; ++k) x[k] = x[k + 1];
+                x[7] = q;
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = x[e] * r;
+            x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
+        }
+    }
+};
+
+template <typename T, bool INTER>
+__device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMaxPairs],
+                                         float* s_max, int64_t item) {
     const RopeAppendArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t item = (int64_t)blockIdx.x - p.row_blocks;
     const int hg = (int)(item % p.head_groups);
     item /= p.head_groups;
     const bool is_v = item & 1;
@@ -304,6 +365,12 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
     const int pg = (int)(item % p.pages), b = (int)(item / p.pages);
     const int64_t ctx = __ldg(a.ctx_lens + b);
     const int count = new_len(a, b);
+    const bool spin = !is_v && a.rot > 0;
+    const int pairs = a.rot / 2;
+    // this thread's frequency of every row of the table when the pairs divide
+    // the CTA (loaded beside the context length, not after it)
+    const bool even = spin && (kWarps * 32) % pairs == 0;
+    const uint64_t freq = even ? __ldg(a.table + threadIdx.x % pairs) : 0;
     if (ctx < 0) {
         if (threadIdx.x == 0) raise_device_error(a.dev_err, SPEC_DEVERR_CTX);
         return;
@@ -314,36 +381,34 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
     const int last = (int)min((int64_t)a.P, ctx + count - page_start);
     if (first >= last) return;
     const int t0 = (int)(page_start + first - ctx), nr = last - first;
-    const int page = find_page(a, b, page_start, threadIdx.x == 0);
-    if (page < 0) return;
-    const int g = hg * kWarps + warp;
-    const bool active = g < a.Hkv;
-    const bool spin = !is_v && a.rot > 0;
+    // two warps per head, each half of the rows of a block
+    const int g = hg * kPageHeads + (warp >> 1), part = warp & 1;
     const int lr = 1 << p.lr_log2, rows = 32 >> p.lr_log2;
     const int e0 = (lane & (lr - 1)) * 8, sub = lane >> p.lr_log2;
-    const bool in_row = e0 < a.D;
-    const int j0 = in_row ? first_pair(a, e0) : -1;
-    const int pairs = a.rot / 2;
-    const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) +
-                   ((int64_t)b * a.n + t0) * (is_v ? a.v_stride : a.k_stride) + (int64_t)g * a.D + e0;
+    const bool in_row = e0 < a.D, active = g < a.Hkv && in_row;
+    const int j0 = in_row ? first_pair<INTER>(a, e0) : -1;
+    const int from = in_row ? partner_lane(a, lane, e0) : lane;
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
-    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-                     ((int64_t)page * a.Hkv + g) * a.P * a.D + e0;
-    float* scale = static_cast<float*>(is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.Hkv + g;
-
-    constexpr int U = 8;                     // rows in flight per lane
-    const int rb = min(kRowBlock, U * rows);  // rows of a block: one table, the registers
-    const bool keep = nr <= rb;
+    const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) +
+                   ((int64_t)b * a.n + t0) * stride + (int64_t)g * a.D + e0;
+    const float sign = e0 < a.rot / 2 ? -1.f : 1.f;    // of the sine (halves)
+    constexpr int N = INTER ? 4 : 8;                   // pairs of a lane's 8 elements
+    constexpr int U = 4;                               // rows in flight per lane
+    const int half = min(kRowBlock / 2, U * rows);     // rows of a block per warp
+    const int rb = 2 * half;                           // rows of a block: one table
+    // row of the block (its first row `base`) that this lane holds at u, or -1
+    auto row_of = [&](int base, int u) {
+        const int in = u * rows + sub, r = part * half + in;
+        return in < half && base + r < nr ? r : -1;
+    };
     Chunk<T> c[U];
-    float amax = 0.f, s = 0.f;
-    // rows [base, base + rb) of the append: load them
+    float x[U][8];
     auto load_rows = [&](int base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = base + u * rows + sub;
+            const int r = row_of(base, u);
             c[u].zero();
-            if (u * rows + sub < rb && r < nr && active && in_row)
-                c[u].load(src + r * stride);
+            if (r >= 0 && active) c[u].load(src + (base + r) * stride);
         }
     };
     auto fill_table = [&](int base) {
@@ -354,96 +419,124 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
                 const int64_t at = a.positions
                                        ? (int64_t)__ldg(a.positions + (int64_t)b * a.n + t0 + r)
                                        : page_start + first + r;
-                tab[e / pairs][e % pairs] = turn(a, at, e % pairs);
+                const int j = e % pairs;
+                // pair j beside the pairs that its warp's lanes read with it
+                tab[e / pairs][(j % N) * (pairs / N) + j / N] =
+                    turn(at, even ? freq : __ldg(a.table + j), a.amplitude);
             }
         __syncthreads();
     };
-    auto value = [&](int base, int u, float (&x)[8]) {
-        c[u].get(x);
-        if (!spin) return;
-        float o[8];
-        float2 cs[8];
-        if (!a.interleaved) c[u].from_lane(in_row ? partner_lane(a, lane, e0) : lane).get(o);
-        const int r = u * rows + sub;
-        if (j0 >= 0 && base + r < nr && r < rb) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < 4 || !a.interleaved) cs[e] = tab[r][j0 + e];
-            rotate8(a, e0, x, o, cs);
-        }
-    };
-    auto maximum = [&](int base) {
+    auto rotate_rows = [&](int base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (u * rows >= rb || base + u * rows >= nr) continue;  // uniform
-            float x[8];
-            value(base, u, x);  // rows past the last are zero
+            c[u].get(x[u]);
+            if (!spin) continue;
+            float o[8];
+            float2 cs[N];
+            if constexpr (!INTER) c[u].from_lane(from).get(o);
+            const int r = row_of(base, u);
+            if (j0 >= 0 && r >= 0) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-        }
-    };
-    auto store = [&](int base) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (u * rows >= rb || base + u * rows >= nr) continue;  // uniform
-            float x[8];
-            value(base, u, x);
-            const int r = base + u * rows + sub;
-            if (u * rows + sub < rb && r < nr && active && in_row) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = s > 0.f ? __fdiv_rn(x[e], s) : 0.f;
-                *reinterpret_cast<uint2*>(codes + (int64_t)(first + r) * a.D) = e4m3x8(x);
+                for (int e = 0; e < N; ++e) {
+                    cs[e] = tab[r][e * (pairs / N) + j0 / N];
+                    if (!INTER) cs[e].y *= sign;
+                }
+                rotate8<INTER>(a, e0, x[u], o, cs);
             }
         }
     };
+    // the first rows are on their way while the page is looked up, the page's
+    // scale while they are rotated
+    load_rows(0);
+    const int page = find_page(a, b, page_start, threadIdx.x == 0);
+    if (page < 0) return;
+    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+                     ((int64_t)page * a.Hkv + g) * a.P * a.D + e0;
+    float* scale = static_cast<float*>(is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.Hkv + g;
+    const float old = g < a.Hkv && first > 0 ? *scale : 0.f;
+    float amax = 0.f;
     for (int base = 0; base < nr; base += rb) {
-        load_rows(base);
+        if (base > 0) load_rows(base);
         fill_table(base);
-        maximum(base);
+        rotate_rows(base);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[u][e]));  // (no row: zeros)
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    s = __fdiv_rn(amax, 448.0f);
-    if (active && first > 0) {
-        const float old = *scale;
-        if (old >= s) {
-            s = old;
-        } else {
-            // the kept rows' codes in the new scale
-            for (int r = sub; r < first; r += rows) {
-                if (!in_row) continue;
-                uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)r * a.D);
-                float x[8];
-                e4m3x8_to_f32(*at, x);
+    if (lane == 0) s_max[warp] = amax;
+    __syncthreads();  // (both warps have read the old scale, too)
+    float s = __fdiv_rn(fmaxf(amax, s_max[warp ^ 1]), 448.0f);
+    if (first > 0 && old >= s) s = old;
+    const Divide by(s);
+    if (g < a.Hkv && part == 0 && lane == 0) *scale = s;
+    if (first > 0 && s > old) {
+        // the kept rows' codes in the new scale
+        for (int r = part * rows + sub; r < first; r += 2 * rows) {
+            if (!active) continue;
+            uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)r * a.D);
+            float v[8];
+            e4m3x8_to_f32(*at, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(__fmul_rn(x[e], old), s);
-                *at = e4m3x8(x);
-            }
+            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], old);
+            by(v);
+            *at = e4m3x8(v);
         }
     }
-    __syncwarp();  // every lane has read the old scale
-    if (active && lane == 0) *scale = s;
-    if (keep) {
-        store(0);
-        return;
-    }
     for (int base = 0; base < nr; base += rb) {
-        load_rows(base);
-        fill_table(base);
-        store(base);
+        if (nr > rb) {  // more rows than the registers held
+            load_rows(base);
+            fill_table(base);
+            rotate_rows(base);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = row_of(base, u);
+            if (r < 0 || !active) continue;
+            by(x[u]);
+            *reinterpret_cast<uint2*>(codes + (int64_t)(first + base + r) * a.D) = e4m3x8(x[u]);
+        }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeParams p) {
-    __shared__ float2 tab[kRowBlock][kMaxPairs];
+// MODE: what the row CTAs write besides q (f32, bf16 or i8 cache rows), or the
+// page CTAs of an e4m3 cache beside them.  Measured: 12.3K prompt tokens of 32 + 8
+// heads into bf16 53.8 us (0.86 of the copy rate), 16.4K into e4m3 91 us (0.60: the
+// page CTAs' arithmetic and barriers), 32 x 4 drafts into e4m3 5.3 us.
+template <typename T, bool INTER, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeParams p) {
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if (blockIdx.x < p.row_blocks)
-        row_cta<T>(p);
-    else
-        page_cta<T>(p, tab);
+    if constexpr (MODE != kPages) {
+        row_cta<T, INTER, MODE>(p, blockIdx.x);
+    } else {
+        // the page CTAs, whose chain of loads is longer, start first
+        const int64_t pages = gridDim.x - p.row_blocks;
+        if (blockIdx.x >= pages) {
+            row_cta<T, INTER, MODE>(p, blockIdx.x - pages);
+        } else {
+            __shared__ float2 tab[kRowBlock][kMaxPairs];
+            __shared__ float s_max[kWarps];
+            page_cta<T, INTER>(p, tab, s_max, blockIdx.x);
+        }
+    }
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_typed(const RopeParams& p, unsigned blocks, cudaStream_t stream) {
+    auto go = [&](auto kern) {
+        return launch_dependent(kern, dim3(blocks), dim3(kWarps * 32), 0, stream, p);
+    };
+    switch (p.a.cache_dtype) {
+    case SPEC_DTYPE_F32: return go(rope_append_kernel<T, INTER, kF32>);
+    case SPEC_DTYPE_BF16: return go(rope_append_kernel<T, INTER, kBf16>);
+    case SPEC_DTYPE_I8: return go(rope_append_kernel<T, INTER, kI8>);
+    case SPEC_DTYPE_E4M3: return go(rope_append_kernel<T, INTER, kPages>);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
@@ -467,13 +560,16 @@ cudaError_t launch_rope_append(const RopeAppendArgs& a, int num_sms, cudaStream_
     p.groups = p.heads > 0 ? (p.heads + p.heads_per_warp - 1) / p.heads_per_warp : 0;
     p.row_blocks = (tokens * p.groups + kWarps - 1) / kWarps;
     p.pages = paged ? (int)(((int64_t)a.n + a.P - 2) / a.P + 1) : 0;
-    p.head_groups = (a.Hkv + kWarps - 1) / kWarps;
+    p.head_groups = (a.Hkv + kPageHeads - 1) / kPageHeads;
     const int64_t blocks = p.row_blocks + (int64_t)a.B * p.pages * 2 * p.head_groups;
     if (blocks == 0) return cudaSuccess;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-    auto kern = a.src_dtype == SPEC_DTYPE_F32 ? rope_append_kernel<float>
-                                              : rope_append_kernel<__nv_bfloat16>;
-    return launch_dependent(kern, dim3((unsigned)blocks), dim3(kWarps * 32), 0, stream, p);
+    const unsigned n = (unsigned)blocks;
+    if (a.src_dtype == SPEC_DTYPE_F32)
+        return a.interleaved ? launch_typed<float, true>(p, n, stream)
+                             : launch_typed<float, false>(p, n, stream);
+    return a.interleaved ? launch_typed<__nv_bfloat16, true>(p, n, stream)
+                         : launch_typed<__nv_bfloat16, false>(p, n, stream);
 }
 
 }  // namespace specv
