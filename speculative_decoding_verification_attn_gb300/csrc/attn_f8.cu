@@ -379,15 +379,22 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 break;
             uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
             const int w = j > 0 ? warp - 12 : warp < 4 ? warp : warp - 4;  // of 3, or of 11
-#pragma unroll 1
-            for (int r0 = w * 2; r0 < R; r0 += j > 0 ? 6 : 22) {
-                const int r = r0 + half;
+            const int step = j > 0 ? 6 : 22;
+            auto q_chunk = [&](int r) {  // this lane's 16 bytes of row r
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (r < R)
                     v = __ldg(reinterpret_cast<const uint4*>(
                                   q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) *
                                           D) +
                               c16);
+                return v;
+            };
+            uint4 ahead = q_chunk(w * 2 + half);
+#pragma unroll 1
+            for (int r0 = w * 2; r0 < R; r0 += step) {
+                const int r = r0 + half;
+                const uint4 v = ahead;
+                ahead = q_chunk(r + step);
                 float x[8];
                 const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
                 float top = 0.f;
@@ -880,10 +887,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 s_stat_m[set * ROWS + ln] = m;
                 s_stat_l[set * ROWS + ln] = l;
                 tc_fence_before();
-                if (REP == 1)
-                    named_bar_sync(2 + quad, 64);  // the two sets' warps of this quadrant
-                else
-                    named_bar_sync(2, 256);
+                named_bar_sync(2, 256);
                 tc_fence_after();
                 float mt = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -906,37 +910,13 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 auto row_of = [&](int rr) {
                     return ((int64_t)cur.b * k + rr / G) * a.Hq + cur.kvh * G + rr % G;
                 };
-                if (REP == 1) {
-                    if (ok && quad_active) {
-#pragma unroll 1
-                        for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 16) {
-                            float o[16];
-                            merged(c0, o);
-                            if (!row_valid) continue;
-                            if (complete) {
-                                uint4* dst = reinterpret_cast<uint4*>(
-                                    static_cast<__nv_bfloat16*>(a.out) + row_of(r) * D + c0);
-#pragma unroll
-                                for (int v4 = 0; v4 < 2; ++v4)
-                                    dst[v4] = make_uint4(pack_bf16x2(o[8 * v4 + 0], o[8 * v4 + 1]),
-                                                         pack_bf16x2(o[8 * v4 + 2], o[8 * v4 + 3]),
-                                                         pack_bf16x2(o[8 * v4 + 4], o[8 * v4 + 5]),
-                                                         pack_bf16x2(o[8 * v4 + 6], o[8 * v4 + 7]));
-                            } else {
-                                float4* dst = reinterpret_cast<float4*>(
-                                    prm.part_o + ((int64_t)slot * ROWS + r) * D + c0);
-#pragma unroll
-                                for (int v4 = 0; v4 < 4; ++v4)
-                                    dst[v4] = make_float4(o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2],
-                                                          o[4 * v4 + 3]);
-                            }
-                        }
-                    }
-                } else {
-                    // 32 columns at a time: every copy's share to the piece's q
+                {
+                    // 32 columns at a time: every lane's share to the piece's q
                     // buffer (its Q K^T are done), then the set's threads sum the
-                    // copies (row t / 8 of each 16-row group, 4 columns); 4-column
-                    // groups are swizzled by the row
+                    // copies (row t / 8 of each 16-row group, 4 columns) and write
+                    // 128 contiguous bytes per row; 4-column groups are swizzled by
+                    // the row.  (Straight from the lanes, a row each, the stores
+                    // cost a piece of 112 rows 2 us more.)
                     float* red = reinterpret_cast<float*>(sm + Smem::Q + (pc & 1) * 2 * Q_PART) +
                                  set * ROWS * 32;
                     const int t = quad * 32 + lane, rr = t >> 3, cg = t & 7;
@@ -989,10 +969,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 // every softmax warp has read O: the next piece's P V may overwrite
                 // it, and its references and row sums these
                 tc_fence_before();
-                if (REP == 1)
-                    named_bar_sync(2 + quad, 64);
-                else
-                    named_bar_sync(2, 256);
+                named_bar_sync(2, 256);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars[Smem::B_EPI]);
