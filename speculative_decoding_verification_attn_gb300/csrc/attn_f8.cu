@@ -100,29 +100,31 @@ struct Smem {
     static constexpr int BARS = SFV + 512;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KSLOTS,
                          B_VFULL = B_KEMPTY + KSLOTS, B_VEMPTY = B_VFULL + VSLOTS,
-                         B_QFULL = B_VEMPTY + VSLOTS,
-                         B_QFREE = B_QFULL + 2, B_SFULL = B_QFREE + 2, B_PREADY = B_SFULL + NS,
-                         B_SFREE = B_PREADY + NS, B_REF = B_SFREE + NS, B_EPI = B_REF + 4,
-                         B_DRAIN = B_EPI + 1,
+                         B_QFULL = B_VEMPTY + VSLOTS, B_SFULL = B_QFULL + 2,
+                         B_PREADY = B_SFULL + NS, B_SFREE = B_PREADY + NS, B_REF = B_SFREE + NS,
+                         B_STAT = B_REF + 4, B_STFREE = B_STAT + 2, B_DRAIN = B_STFREE + 2,
                          B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
                          B_SCFREE = B_SCALE + SCALE_STAGES, B_ROWS = B_SCFREE + SCALE_STAGES,
                          NUM_BARS = B_ROWS + ROW_STAGES;
     static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
     static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
     static constexpr int REF = FIRST + 48;            // reference of each lane
-    static constexpr int STAT = REF + ROWS * 4;       // (m, l) of [set][lane]
     // page warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8]
     // scales, and for the producers [stage][2 tiles][8] cache rows (-1: no copy)
-    static constexpr int PIDS = STAT + 2 * 2 * ROWS * 4;
+    static constexpr int PIDS = REF + ROWS * 4;
     static constexpr int TROWS = PIDS + RAW_STAGES * 2 * MAX_CHUNKS * 4;
     static constexpr int RAW = TROWS + ROW_STAGES * 2 * MAX_CHUNKS * 4;
     static constexpr int EXPS = RAW + RAW_STAGES * 4 * MAX_CHUNKS * 4;  // [stage][row] int8
     static constexpr int SCALE = EXPS + EXP_STAGES * ROWS;  // [stage][8] {sk, log2 sv, 1/sv, on}
     static constexpr int CTX = SCALE + SCALE_STAGES * MAX_CHUNKS * 16;
     static constexpr int PRE = CTX + MAX_BATCH * 4;
+    // (m, l) of [piece & 1][set][lane]: over the tile prefix, which only the start reads
+    static constexpr int STAT = PRE;
     static constexpr int END = PRE + (MAX_BATCH + 1) * 4;
+    static_assert(2 * 2 * ROWS * 8 <= END - PRE, "the statistics' place");
 };
-static_assert(Smem::MISC % 16 == 0 && Smem::SCALE % 16 == 0 && Smem::SFP % 16 == 0, "alignment");
+static_assert(Smem::MISC % 16 == 0 && Smem::SCALE % 16 == 0 && Smem::SFP % 16 == 0 &&
+              Smem::STAT % 8 == 0, "alignment");
 constexpr size_t SMEM_BYTES = Smem::END + 1024;  // + alignment slack
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
@@ -245,6 +247,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     Cursor* s_first = reinterpret_cast<Cursor*>(sm + Smem::FIRST);  // of tile t_begin
     float4* s_scale = reinterpret_cast<float4*>(sm + Smem::SCALE);
     int8_t* s_exp = reinterpret_cast<int8_t*>(sm + Smem::EXPS);
+    float2* s_stat = reinterpret_cast<float2*>(sm + Smem::STAT);
 
     // (shuffled: the roles' branches and operands stay in uniform registers)
     const int tid = threadIdx.x, lane = tid & 31;
@@ -265,7 +268,8 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         for (int s = 0; s < ROW_STAGES; ++s) mbar_init(&bars[Smem::B_ROWS + s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars[Smem::B_QFULL + s], 3);   // the 3 converting warps
-            mbar_init(&bars[Smem::B_QFREE + s], 8);   // every softmax warp, after the piece
+            mbar_init(&bars[Smem::B_STAT + s], 8);    // every softmax warp, at a piece's end
+            mbar_init(&bars[Smem::B_STFREE + s], 4);  // the epilogue's warps
             mbar_init(&bars[Smem::B_DRAIN + s], 1);
         }
         for (int s = 0; s < NS; ++s) {
@@ -279,7 +283,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             mbar_init(&bars[Smem::B_SCALE + s], 1);
             mbar_init(&bars[Smem::B_SCFREE + s], 4);  // the 4 warps of a set
         }
-        mbar_init(&bars[Smem::B_EPI], 8);  // every softmax warp, once per piece
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -348,8 +351,8 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         prm.seg_rec[2 * blockIdx.x + 1] =
             make_int4((int)(t_begin & 0xffffffff), (int)(t_begin >> 32), 0, 0);
     }
-    if (blockIdx.x == 0)
-        for (int b = tid; b <= B; b += THREADS) prm.seg_pre[b] = s_pre[b];
+    if (blockIdx.x == 0 && warp < 4)  // (before the first statistics, barrier 1 between)
+        for (int b = tid; b <= B; b += 128) prm.seg_pre[b] = s_pre[b];
 
     auto start_at = [&](Cursor& c) { c = *s_first; };
     // the page chunk `l` of a tile holds a key that some query sees
@@ -359,97 +362,74 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         return !WIN || k0 < a.sinks || k0 + CH > window_low(a, s_ctx[c.b]);
     };
 
-    if (warp >= 12) regs_dec<96>();
-    if (warp < 4 || (warp >= 8 && warp < 15)) {
-        // ================= q rows to hi / lo =================
-        // Piece j into buffer j & 1 (free after the epilogue of piece j - 2, which
-        // merges the copies there), its row exponents into stage j % 4.  16 lanes per row, 8
-        // elements each; a negative softmax scale is folded into q's sign.  The
-        // first piece, which everything waits for, by the softmax warps too;
-        // the others by warps 12-14.
+    // ================= q rows to hi / lo =================
+    // The q rows of piece j (cursor c), two rows per warp and step, from row
+    // 2 w on: 16 lanes per row, 8 elements each, into buffer j & 1, the rows'
+    // exponents into stage j % 4; a negative softmax scale is folded into q's
+    // sign.  The first piece, which everything waits for, by the softmax warps
+    // too; the others by warps 12-14.
+    auto convert = [&](const Cursor& c, int j, int w, int step) {
         const int half = lane >> 4, c16 = lane & 15;
         const float sign = a.scale < 0.f ? -1.f : 1.f;
         const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-        Cursor cur;
-        bool more = n_tiles > 0;
-        if (more) start_at(cur);
-        for (int j = 0; more; ++j) {
-            if (j >= 2 && !role_wait(&bars[Smem::B_QFREE + (j & 1)], ((j >> 1) - 1) & 1,
-                                     abort_flag, a.dev_err))
-                break;
-            uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
-            const int w = j > 0 ? warp - 12 : warp < 4 ? warp : warp - 4;  // of 3, or of 11
-            const int step = j > 0 ? 6 : 22;
-            auto q_chunk = [&](int r) {  // this lane's 16 bytes of row r
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < R)
-                    v = __ldg(reinterpret_cast<const uint4*>(
-                                  q + (((int64_t)cur.b * k + r / G) * a.Hq + cur.kvh * G + r % G) *
-                                          D) +
-                              c16);
-                return v;
-            };
-            uint4 ahead = q_chunk(w * 2 + half);
+        uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
+        auto q_chunk = [&](int r) {  // this lane's 16 bytes of row r
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < R)
+                v = __ldg(reinterpret_cast<const uint4*>(
+                              q + (((int64_t)c.b * k + r / G) * a.Hq + c.kvh * G + r % G) * D) +
+                          c16);
+            return v;
+        };
+        uint4 ahead = q_chunk(w * 2 + half);
 #pragma unroll 1
-            for (int r0 = w * 2; r0 < R; r0 += step) {
-                const int r = r0 + half;
-                const uint4 v = ahead;
-                ahead = q_chunk(r + step);
-                float x[8];
-                const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
-                float top = 0.f;
+        for (int r0 = w * 2; r0 < R; r0 += step) {
+            const int r = r0 + half;
+            const uint4 v = ahead;
+            ahead = q_chunk(r + step);
+            float x[8];
+            const uint32_t pair[4] = {v.x, v.y, v.z, v.w};
+            float top = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(pair[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(pair[e] & 0xffff0000u);
-                    top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-                }
+            for (int e = 0; e < 4; ++e) {
+                x[2 * e] = __uint_as_float(pair[e] << 16);
+                x[2 * e + 1] = __uint_as_float(pair[e] & 0xffff0000u);
+                top = fmaxf(top, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+            }
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                // 2^-ex takes the row's largest element into [128, 256)
-                const int ex = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
-                const float mul = sign * __uint_as_float((uint32_t)(127 - ex) << 23);
-                uint32_t hw[2], lw[2];
+            for (int o = 8; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^-ex takes the row's largest element into [128, 256)
+            const int ex = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
+            const float mul = sign * __uint_as_float((uint32_t)(127 - ex) << 23);
+            uint32_t hw[2], lw[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint16_t h, l;
-                    split_e4m3x2(x[2 * e] * mul, x[2 * e + 1] * mul, h, l);
-                    if (e & 1) {
-                        hw[e >> 1] |= (uint32_t)h << 16;
-                        lw[e >> 1] |= (uint32_t)l << 16;
-                    } else {
-                        hw[e >> 1] = h;
-                        lw[e >> 1] = l;
-                    }
-                }
-                if (r < R) {
-                    if (c16 == 0) s_exp[(j % EXP_STAGES) * ROWS + r] = (int8_t)ex;
-#pragma unroll
-                    for (int c = 0; c < REP; ++c) {
-                        const int row = r + c * COPY;
-                        const int off = row * D + (((c16 >> 1) ^ (row & 7)) << 4) + (c16 & 1) * 8;
-                        *reinterpret_cast<uint2*>(buf + off) = make_uint2(hw[0], hw[1]);
-                        *reinterpret_cast<uint2*>(buf + Q_PART + off) = make_uint2(lw[0], lw[1]);
-                    }
+            for (int e = 0; e < 4; ++e) {
+                uint16_t h, l;
+                split_e4m3x2(x[2 * e] * mul, x[2 * e + 1] * mul, h, l);
+                if (e & 1) {
+                    hw[e >> 1] |= (uint32_t)h << 16;
+                    lw[e >> 1] |= (uint32_t)l << 16;
+                } else {
+                    hw[e >> 1] = h;
+                    lw[e >> 1] = l;
                 }
             }
-            fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
-            if (j == 0)
-                named_bar_sync(1, 11 * 32);
-            else
-                __syncwarp();
-            if (warp < 12) break;
-            if (lane == 0) {
-                mbar_arrive(&bars[Smem::B_EXP + j % EXP_STAGES]);
-                mbar_arrive(&bars[Smem::B_QFULL + (j & 1)]);
+            if (r < R) {
+                if (c16 == 0) s_exp[(j % EXP_STAGES) * ROWS + r] = (int8_t)ex;
+#pragma unroll
+                for (int cp = 0; cp < REP; ++cp) {
+                    const int row = r + cp * COPY;
+                    const int off = row * D + (((c16 >> 1) ^ (row & 7)) << 4) + (c16 & 1) * 8;
+                    *reinterpret_cast<uint2*>(buf + off) = make_uint2(hw[0], hw[1]);
+                    *reinterpret_cast<uint2*>(buf + Q_PART + off) = make_uint2(lw[0], lw[1]);
+                }
             }
-            more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
-            if (more) cur.next_segment(s_ctx, a);
         }
-    }
+        fence_proxy_async_smem();  // generic-proxy writes -> tensor-core reads
+    };
 
-    if (warp >= 4 && warp < 8) {
+    if (warp & 4) {
     regs_dec<96>();
     if (warp == 5 || warp == 6) {
         // ================= TMA producers: warp 5 K, warp 6 V =================
@@ -539,84 +519,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             if (lane == 0) mbar_drain(&bars[Smem::B_DRAIN], 0);
             __syncwarp();
         }
-    } else {
-        // ================= P V issue (warp 7) =================
-        if (n_tiles > 0) {
-            Cursor cur;
-            start_at(cur);
-            int pc = -1;
-            bool ok = true;
-            // V of 32 keys: MN-major, 8-key groups 1 KB apart
-            const uint64_t vdesc0 = umma_sdesc_sw128(smem_u32(sm + Smem::VS), 1024, 1024);
-            const uint64_t sfp0 = umma_sdesc_plain(smem_u32(sm + Smem::SFP), 128);
-            const uint64_t sfv = umma_sdesc_plain(smem_u32(sm + Smem::SFV), 128);
-            for (int it = 0; it < n_tiles && ok; ++it) {
-                const bool first = (it == 0) || (cur.lt == 0);
-                const int s = it % NS, slot = it % VSLOTS;
-                const int ctx = s_ctx[cur.b], key0 = cur.key0();
-                const int nvalid = min(TN, ctx + k - key0), nkb = (nvalid + 31) / 32;
-                if (first) {
-                    ++pc;
-                    // the previous piece's epilogue has read O before the first
-                    // P V of this piece overwrites it
-                    if (pc >= 1)
-                        ok = role_wait(&bars[Smem::B_EPI], (pc - 1) & 1, abort_flag, a.dev_err);
-                    if (!ok) break;
-                }
-                ok = role_wait(&bars[Smem::B_VFULL + slot], (it / VSLOTS) & 1, abort_flag,
-                               a.dev_err);
-                if (!ok) break;
-                // rows that no query sees and a P V reads: zero, so that 0 * (stale,
-                // canary or a NaN code) never reaches O
-                auto clear = [&](int r0, int r1) {
-                    uint4* v4 = reinterpret_cast<uint4*>(sm + Smem::VS + slot * SLOT_BYTES);
-                    for (int e = r0 * 8 + lane; e < r1 * 8; e += 32) v4[e] = make_uint4(0, 0, 0, 0);
-                };
-                bool cleared = nvalid % 32 != 0;
-                if (cleared) clear(nvalid, nkb * 32);
-                if (WIN) {
-                    const int low = window_low(a, ctx);
-                    const int g0 = max(0, a.sinks >= low ? nvalid : a.sinks - key0);
-                    const int g1 = min(nvalid, low - key0);
-                    if (g0 < g1) {
-                        clear(g0, g1);
-                        cleared = true;
-                    }
-                }
-                if (cleared) {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                ok = role_wait(&bars[Smem::B_PREADY + s], (it / NS) & 1, abort_flag, a.dev_err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = vdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
-                const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O;
-                tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
-                tmem_cp_scales_w(sbuf + SF_V, sfv);
-                if (elect_lane()) {
-#pragma unroll 1
-                    for (int j = 0; j < nkb; ++j) {
-                        const uint64_t vj = vd + ((uint32_t)(j * 4096) >> 4);
-                        const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, j);
-                        umma_mx_ts(od, sbuf + p_col(j), vj, id, sbuf + SF_P, sbuf + SF_V,
-                                   (!first || j > 0) ? 1u : 0u);
-                        umma_mx_ts(od, sbuf + p_col(j) + 8, vj, id, sbuf + SF_P, sbuf + SF_V, 1u);
-                    }
-                }
-                __syncwarp();
-                umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
-                umma_commit_w(&bars[Smem::B_SFREE + s]);
-                if (it + 1 < n_tiles) cur.next(s_ctx, a);
-            }
-            __syncwarp();
-            umma_commit_w(&bars[Smem::B_DRAIN + 1]);
-            if (lane == 0) mbar_drain(&bars[Smem::B_DRAIN + 1], 0);
-            __syncwarp();
-        }
-    }
-    } else if (warp >= 12) {
-    if (warp == 15) {
+    } else if (warp == 15) {
         // ================= pages: rows of the copies, scales =================
         // Two tiles per iteration, 16 lanes each (8 chunks of K, 8 of V).  Rows
         // of pair p to stage p % ROW_STAGES, {sk, log2 sv, 1 / sv, on} of tile
@@ -710,8 +613,212 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 mbar_arrive(&bars[Smem::B_SCALE + t % SCALE_STAGES]);
         }
         cp_async_wait<0>();
+    } else {
+        // ================= P V issue (warp 7) and epilogue (7, 12-14) =================
+        // Piece by piece: warps 12-14 convert the q rows of piece j (the buffer
+        // is the one that piece j - 2 was written out from) while warp 7 issues
+        // the P V of piece j - 1, then the four, one per TMEM lane quadrant,
+        // write piece j - 1 out; the softmax warps are at the next one by then.
+        const bool pv = warp == 7;
+        Cursor cur, prev;     // of pieces j and j - 1
+        bool more = n_tiles > 0, ok = true;
+        int it0 = 0;          // first tile of piece j - 1
+        if (more) start_at(cur);
+        for (int j = 0;; ++j) {
+            if (more && !pv) {
+                convert(cur, j, j > 0 ? warp - 12 : warp - 4, j > 0 ? 6 : 22);
+                if (j == 0)
+                    named_bar_sync(1, 11 * 32);
+                else
+                    __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[Smem::B_EXP + j % EXP_STAGES]);
+                    mbar_arrive(&bars[Smem::B_QFULL + (j & 1)]);
+                }
+            }
+            if (j > 0) {
+                const int nt = min(prev.nb - prev.lt, n_tiles - it0);
+                if (pv) {
+                    // V of 32 keys: MN-major, 8-key groups 1 KB apart
+                    const uint64_t vdesc0 =
+                        umma_sdesc_sw128(smem_u32(sm + Smem::VS), 1024, 1024);
+                    const uint64_t sfp0 = umma_sdesc_plain(smem_u32(sm + Smem::SFP), 128);
+                    const uint64_t sfv = umma_sdesc_plain(smem_u32(sm + Smem::SFV), 128);
+                    const int ctx = s_ctx[prev.b];
+                    for (int it = it0; it < it0 + nt && ok; ++it, ++prev.lt) {
+                        const int s = it % NS, slot = it % VSLOTS;
+                        const int key0 = prev.key0();
+                        const int nvalid = min(TN, ctx + k - key0), nkb = (nvalid + 31) / 32;
+                        ok = role_wait(&bars[Smem::B_VFULL + slot], (it / VSLOTS) & 1, abort_flag,
+                                       a.dev_err);
+                        if (!ok) break;
+                        // rows that no query sees and a P V reads: zero, so that
+                        // 0 * (stale or a NaN code) never reaches O
+                        auto clear = [&](int r0, int r1) {
+                            uint4* v4 =
+                                reinterpret_cast<uint4*>(sm + Smem::VS + slot * SLOT_BYTES);
+                            for (int e = r0 * 8 + lane; e < r1 * 8; e += 32)
+                                v4[e] = make_uint4(0, 0, 0, 0);
+                        };
+                        bool cleared = nvalid % 32 != 0;
+                        if (cleared) clear(nvalid, nkb * 32);
+                        if (WIN) {
+                            const int low = window_low(a, ctx);
+                            const int g0 = max(0, a.sinks >= low ? nvalid : a.sinks - key0);
+                            const int g1 = min(nvalid, low - key0);
+                            if (g0 < g1) {
+                                clear(g0, g1);
+                                cleared = true;
+                            }
+                        }
+                        if (cleared) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        ok = role_wait(&bars[Smem::B_PREADY + s], (it / NS) & 1, abort_flag,
+                                       a.dev_err);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = vdesc0 + ((uint32_t)(slot * SLOT_BYTES) >> 4);
+                        const uint32_t sbuf = tmem + s * TN, od = tmem + TM_O;
+                        tmem_cp_scales_w(sbuf + SF_P, sfp0 + ((uint32_t)(s * 512) >> 4));
+                        tmem_cp_scales_w(sbuf + SF_V, sfv);
+                        if (elect_lane()) {
+#pragma unroll 1
+                            for (int kb = 0; kb < nkb; ++kb) {
+                                const uint64_t vk = vd + ((uint32_t)(kb * 4096) >> 4);
+                                const uint32_t id = umma_idesc_mx_e4m3(ROWS, D, kb);
+                                umma_mx_ts(od, sbuf + p_col(kb), vk, id, sbuf + SF_P, sbuf + SF_V,
+                                           (it > it0 || kb > 0) ? 1u : 0u);
+                                umma_mx_ts(od, sbuf + p_col(kb) + 8, vk, id, sbuf + SF_P,
+                                           sbuf + SF_V, 1u);
+                            }
+                        }
+                        __syncwarp();
+                        umma_commit_w(&bars[Smem::B_VEMPTY + slot]);
+                        umma_commit_w(&bars[Smem::B_SFREE + s]);
+                    }
+                }
+                // ---- epilogue: both sets' row sums and the copies' (reference, O)
+                // merge.  64 columns at a time: every lane's share to the piece's
+                // q buffer (its Q K^T are done), 4-column groups swizzled by the
+                // row; then 16 threads sum the copies of a row and write 128
+                // contiguous bytes.  Once the second half is in shared memory
+                // warp 7 goes on to the next piece's P V, which overwrites O.
+                const int jp = (j - 1) & 1, end = it0 + nt - 1;
+                if (ok)
+                    ok = role_wait(&bars[Smem::B_STAT + jp], ((j - 1) >> 1) & 1, abort_flag,
+                                   a.dev_err);
+                if (ok)  // the piece's last P V is done
+                    ok = role_wait(&bars[Smem::B_SFREE + end % NS], (end / NS) & 1, abort_flag,
+                                   a.dev_err);
+                tc_fence_after();
+                const int64_t tb = ld_shared_s64(s_rng), te = ld_shared_s64(s_rng + 1);
+                const bool complete = prev.seg_start >= tb && prev.seg_start + prev.nb <= te;
+                const int slot = 2 * blockIdx.x + (prev.seg_start < tb ? 0 : 1);
+                const int ln = (warp & 3) * 32 + lane, r = ln % COPY;
+                const float2* stat = s_stat + jp * 2 * ROWS;
+                float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2 * REP; ++c)
+                    mt = fmaxf(mt, stat[(c & 1) * ROWS + (c >> 1) * COPY + r].x);
+                const float mt_use = mt == -INFINITY ? 0.f : mt;
+#pragma unroll
+                for (int c = 0; c < 2 * REP; ++c) {
+                    const float2 x = stat[(c & 1) * ROWS + (c >> 1) * COPY + r];
+                    lt += fast_exp2(x.x - mt_use) * x.y;
+                }
+                // the lane's O stands to the larger of its sets' references (-inf
+                // where it saw no key: weight 0)
+                const float wgt =
+                    lt > 0.f ? fast_exp2(fmaxf(stat[ln].x, stat[ROWS + ln].x) - mt_use) / lt : 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[Smem::B_STFREE + jp]);
+                auto row_of = [&](int rr) {
+                    return ((int64_t)prev.b * k + rr / G) * a.Hq + prev.kvh * G + rr % G;
+                };
+                if (ok && ln < R && ln < COPY) {
+                    const float lse = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
+                    if (!complete)
+                        prm.part_lse[(int64_t)slot * ROWS + r] = lse;
+                    else if (a.lse)
+                        a.lse[row_of(r)] = lse;
+                }
+                float* red = reinterpret_cast<float*>(sm + Smem::Q + jp * 2 * Q_PART);
+                const int t = (pv ? 96 : (warp - 12) * 32) + lane, cg = lane & 15;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    if (ok && ((warp & 3) * 32) % COPY < R) {
+                        float4* dst = reinterpret_cast<float4*>(red + ln * 64);
+#pragma unroll 1
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t ov[16];
+                            tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + TM_O + c0 +
+                                          16 * h,
+                                      ov);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int v4 = 0; v4 < 4; ++v4)
+                                dst[(4 * h + v4) ^ (lane & 7)] =
+                                    make_float4(__uint_as_float(ov[4 * v4]) * wgt,
+                                                __uint_as_float(ov[4 * v4 + 1]) * wgt,
+                                                __uint_as_float(ov[4 * v4 + 2]) * wgt,
+                                                __uint_as_float(ov[4 * v4 + 3]) * wgt);
+                        }
+                    }
+                    tc_fence_before();
+                    named_bar_sync(2, 128);
+                    tc_fence_after();
+                    if (pv && c0) break;
+#pragma unroll 1
+                    for (int row = t >> 4; row < (ok ? R : 0); row += c0 ? 6 : 8) {
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int c = 0; c < REP; ++c) {
+                            const float4 x = reinterpret_cast<const float4*>(
+                                red + (c * COPY + row) * 64)[cg ^ (row & 7)];
+                            acc.x += x.x;
+                            acc.y += x.y;
+                            acc.z += x.z;
+                            acc.w += x.w;
+                        }
+                        if (complete)
+                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                      row_of(row) * D + c0 + cg * 4) =
+                                make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                        else
+                            *reinterpret_cast<float4*>(prm.part_o +
+                                                       ((int64_t)slot * ROWS + row) * D + c0 +
+                                                       cg * 4) = acc;
+                    }
+                    // the shares are read: the second half's may follow, the next
+                    // but one piece's q rows after those
+                    if (c0)
+                        named_bar_sync(4, 96);
+                    else
+                        named_bar_sync(3, 128);
+                }
+                it0 += nt;
+            }
+            if (!more) break;
+            prev = cur;
+            more = cur.seg_start + cur.nb < ld_shared_s64(s_rng + 1);
+            if (more) cur.next_segment(s_ctx, a);
+        }
+        if (pv && n_tiles > 0) {
+            __syncwarp();
+            umma_commit_w(&bars[Smem::B_DRAIN + 1]);
+            if (lane == 0) mbar_drain(&bars[Smem::B_DRAIN + 1], 0);
+            __syncwarp();
+        }
     }
     } else {
+        if (n_tiles > 0) {
+            Cursor first_piece;
+            start_at(first_piece);
+            convert(first_piece, 0, warp < 4 ? warp : warp - 4, 22);
+            named_bar_sync(1, 11 * 32);
+        }
         regs_inc<160>();
         // ================= softmax sets (0: warps 0-3, even tiles; 1: 8-11, odd) =================
         const int set = warp >= 8 ? 1 : 0;
@@ -724,8 +831,6 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const int blk0 = copy * NBLK;         // the first 32-key block of this thread
         const float sl2 = fabsf(a.scale) * kLog2e;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        float* s_stat_m = reinterpret_cast<float*>(sm + Smem::STAT);
-        float* s_stat_l = s_stat_m + 2 * ROWS;
         float* s_ref = reinterpret_cast<float*>(sm + Smem::REF);
         float m = -INFINITY, l = 0.f;  // reference that the row sum l of this set stands to
         float qm = 0.f;         // accumulator units to log2 units, before the page's scale
@@ -875,106 +980,14 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 }
             }
             if (last) {
-                // ---- epilogue of the piece that ends at this tile: both sets' row
-                // sums and the copies' (reference, O) merge; each set writes half
-                // of the output columns
-                if (ok)  // the piece's last P V is done
-                    ok = role_wait(&bars[Smem::B_SFREE + sb], (it / NS) & 1, abort_flag,
-                                   a.dev_err);
-                const int64_t tb = ld_shared_s64(s_rng), te = ld_shared_s64(s_rng + 1);
-                const bool complete = cur.seg_start >= tb && cur.seg_start + cur.nb <= te;
-                const int slot = 2 * blockIdx.x + (cur.seg_start < tb ? 0 : 1);
-                s_stat_m[set * ROWS + ln] = m;
-                s_stat_l[set * ROWS + ln] = l;
-                tc_fence_before();
-                named_bar_sync(2, 256);
-                tc_fence_after();
-                float mt = -INFINITY, lt = 0.f;
-#pragma unroll
-                for (int c = 0; c < REP; ++c) mt = fmaxf(mt, s_ref[c * COPY + r]);
-                const float mt_use = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-                for (int c = 0; c < 2 * REP; ++c)
-                    lt += fast_exp2(s_stat_m[(c & 1) * ROWS + (c >> 1) * COPY + r] - mt_use) *
-                          s_stat_l[(c & 1) * ROWS + (c >> 1) * COPY + r];
-                const float lse = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
-                // a lane that saw no key has reference -inf: weight 0
-                const float wgt = lt > 0.f ? fast_exp2(s_ref[ln] - mt_use) / lt : 0.f;
-                auto merged = [&](int c0, float (&o)[16]) {  // this lane's share of 16 columns
-                    uint32_t ov[16];
-                    tmem_ld16(lane_base + TM_O + c0, ov);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(ov[e]) * wgt;
-                };
-                auto row_of = [&](int rr) {
-                    return ((int64_t)cur.b * k + rr / G) * a.Hq + cur.kvh * G + rr % G;
-                };
-                {
-                    // 32 columns at a time: every lane's share to the piece's q
-                    // buffer (its Q K^T are done), then the set's threads sum the
-                    // copies (row t / 8 of each 16-row group, 4 columns) and write
-                    // 128 contiguous bytes per row; 4-column groups are swizzled by
-                    // the row.  (Straight from the lanes, a row each, the stores
-                    // cost a piece of 112 rows 2 us more.)
-                    float* red = reinterpret_cast<float*>(sm + Smem::Q + (pc & 1) * 2 * Q_PART) +
-                                 set * ROWS * 32;
-                    const int t = quad * 32 + lane, rr = t >> 3, cg = t & 7;
-#pragma unroll 1
-                    for (int c0 = set * 64; c0 < set * 64 + 64; c0 += 32) {
-                        if (ok && quad_active) {
-                            float4* dst = reinterpret_cast<float4*>(red + t * 32);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float o[16];
-                                merged(c0 + 16 * h, o);
-#pragma unroll
-                                for (int v4 = 0; v4 < 4; ++v4)
-                                    dst[(4 * h + v4) ^ (lane & 7)] = make_float4(
-                                        o[4 * v4], o[4 * v4 + 1], o[4 * v4 + 2], o[4 * v4 + 3]);
-                            }
-                        }
-                        named_bar_sync(3 + set, 128);
-#pragma unroll 1
-                        for (int row = rr; row < (ok ? R : 0); row += 16) {
-                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                            for (int c = 0; c < REP; ++c) {
-                                const float4 x = reinterpret_cast<const float4*>(
-                                    red + (c * COPY + row) * 32)[cg ^ (row & 7)];
-                                acc.x += x.x;
-                                acc.y += x.y;
-                                acc.z += x.z;
-                                acc.w += x.w;
-                            }
-                            if (complete)
-                                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                          row_of(row) * D + c0 + cg * 4) =
-                                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-                            else
-                                *reinterpret_cast<float4*>(prm.part_o +
-                                                           ((int64_t)slot * ROWS + row) * D + c0 +
-                                                           cg * 4) = acc;
-                        }
-                        named_bar_sync(3 + set, 128);
-                    }
-                }
-                if (ok && row_valid && set == 0 && copy == 0) {
-                    if (complete) {
-                        if (a.lse) a.lse[row_of(r)] = lse;
-                    } else {
-                        prm.part_lse[(int64_t)slot * ROWS + r] = lse;
-                    }
-                }
-                // every softmax warp has read O: the next piece's P V may overwrite
-                // it, and its references and row sums these
-                tc_fence_before();
-                named_bar_sync(2, 256);
+                // this set's reference and row sum to the epilogue (which has
+                // read those of the piece before the last)
+                if (ok && pc >= 2)
+                    ok = role_wait(&bars[Smem::B_STFREE + (pc & 1)], ((pc >> 1) - 1) & 1,
+                                   abort_flag, a.dev_err);
+                s_stat[((pc & 1) * 2 + set) * ROWS + ln] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[Smem::B_EPI]);
-                    mbar_arrive(&bars[Smem::B_QFREE + (pc & 1)]);
-                }
+                if (lane == 0) mbar_arrive(&bars[Smem::B_STAT + (pc & 1)]);
             }
             if (it + 1 < n_tiles) cur.next(s_ctx, a);
         }
