@@ -101,17 +101,18 @@ struct Smem {
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + KSLOTS,
                          B_VFULL = B_KEMPTY + KSLOTS, B_VEMPTY = B_VFULL + VSLOTS,
                          B_QFULL = B_VEMPTY + VSLOTS, B_SFULL = B_QFULL + 2,
-                         B_PREADY = B_SFULL + NS, B_SFREE = B_PREADY + NS, B_REF = B_SFREE + NS,
-                         B_STAT = B_REF + 4, B_STFREE = B_STAT + 2, B_DRAIN = B_STFREE + 2,
+                         B_PREADY = B_SFULL + NS, B_SFREE = B_PREADY + NS, B_STAT = B_SFREE + NS,
+                         B_STFREE = B_STAT + 2, B_DRAIN = B_STFREE + 2,
                          B_EXP = B_DRAIN + 2, B_SCALE = B_EXP + EXP_STAGES,
-                         B_SCFREE = B_SCALE + SCALE_STAGES, B_ROWS = B_SCFREE + SCALE_STAGES,
+                         B_SCFREE = B_SCALE + SCALE_STAGES / 2,
+                         B_ROWS = B_SCFREE + SCALE_STAGES / 2,
                          NUM_BARS = B_ROWS + ROW_STAGES;
     static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
     static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
-    static constexpr int REF = FIRST + 48;            // reference of each lane
+    static constexpr int MOST = FIRST + 48;           // largest w of [tile & 1][set][lane]
     // page warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8]
     // scales, and for the producers [stage][2 tiles][8] cache rows (-1: no copy)
-    static constexpr int PIDS = REF + ROWS * 4;
+    static constexpr int PIDS = MOST + 2 * 2 * ROWS * 4;
     static constexpr int TROWS = PIDS + RAW_STAGES * 2 * MAX_CHUNKS * 4;
     static constexpr int RAW = TROWS + ROW_STAGES * 2 * MAX_CHUNKS * 4;
     static constexpr int EXPS = RAW + RAW_STAGES * 4 * MAX_CHUNKS * 4;  // [stage][row] int8
@@ -232,7 +233,8 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                const F8Params prm) {
     using Cursor = SegCursor<TN, WIN>;
     static_assert(sizeof(Cursor) <= 48, "the first cursor's place");
-    constexpr int NBLK = 4 / REP;        // 32-key blocks of a softmax thread
+    constexpr int NBLK = REP == 1 ? 2 : 1;   // 32-key blocks of a softmax thread
+    constexpr int GROUPS = REP == 4 ? 1 : 2;  // 16-key groups of a block that it takes
     constexpr int COPY = ROWS / REP;     // lanes of one copy of the rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(
@@ -274,24 +276,25 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         }
         for (int s = 0; s < NS; ++s) {
             mbar_init(&bars[Smem::B_SFULL + s], 1);
-            mbar_init(&bars[Smem::B_PREADY + s], 4);  // the 4 warps of the set
+            mbar_init(&bars[Smem::B_PREADY + s], 8);  // every softmax warp
             mbar_init(&bars[Smem::B_SFREE + s], 1);
         }
-        for (int s = 0; s < 4; ++s) mbar_init(&bars[Smem::B_REF + s], 1);  // per lane quadrant
         for (int s = 0; s < EXP_STAGES; ++s) mbar_init(&bars[Smem::B_EXP + s], 3);
-        for (int s = 0; s < SCALE_STAGES; ++s) {
+        for (int s = 0; s < SCALE_STAGES / 2; ++s) {  // per pair of tiles
             mbar_init(&bars[Smem::B_SCALE + s], 1);
-            mbar_init(&bars[Smem::B_SCFREE + s], 4);  // the 4 warps of a set
+            mbar_init(&bars[Smem::B_SCFREE + s], 8);  // every softmax warp
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
     {
-        // q rows that no piece writes stay zero; the scale bytes of V are 1.0
+        // q rows that no piece writes stay zero; the scale bytes of V, and of
+        // P blocks that no lane of a row writes, are 1.0
         uint4* q4 = reinterpret_cast<uint4*>(sm + Smem::Q);
         for (int e = tid; e < 4 * Q_PART / 16; e += THREADS)
             if ((e % (Q_PART / 16)) / 8 % COPY >= R) q4[e] = make_uint4(0, 0, 0, 0);
-        if (tid < 128) reinterpret_cast<uint32_t*>(sm + Smem::SFV)[tid] = 0x7f7f7f7fu;
+        static_assert(NS * 128 + 128 <= THREADS && Smem::SFV == Smem::SFP + NS * 512, "one pass");
+        if (tid < NS * 128 + 128) reinterpret_cast<uint32_t*>(sm + Smem::SFP)[tid] = 0x7f7f7f7fu;
         fence_proxy_async_smem();
     }
     // the grids before this one have finished with every buffer this call
@@ -355,6 +358,11 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         for (int b = tid; b <= B; b += 128) prm.seg_pre[b] = s_pre[b];
 
     auto start_at = [&](Cursor& c) { c = *s_first; };
+    // query row r of a (sequence, kv-head) in q and out, from its row 0 on: row
+    // r % G of draft r / G (exact: r + 1/2 over G is 1 / 256 at least from a
+    // whole number, and a division costs what a row's whole sum does)
+    const float inv_g = 1.f / (float)G;
+    auto row_at = [&](int r) { return (int)(((float)r + 0.5f) * inv_g) * (a.Hq - G) + r; };
     // the page chunk `l` of a tile holds a key that some query sees
     auto chunk_used = [&](const Cursor& c, int l) {
         const int k0 = c.key0() + (l << lgCH), end = s_ctx[c.b] + k;
@@ -371,14 +379,13 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
     auto convert = [&](const Cursor& c, int j, int w, int step) {
         const int half = lane >> 4, c16 = lane & 15;
         const float sign = a.scale < 0.f ? -1.f : 1.f;
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                                 ((int64_t)c.b * k * a.Hq + c.kvh * G) * D;
         uint8_t* buf = sm + Smem::Q + (j & 1) * 2 * Q_PART;
         auto q_chunk = [&](int r) {  // this lane's 16 bytes of row r
             uint4 v = make_uint4(0, 0, 0, 0);
             if (r < R)
-                v = __ldg(reinterpret_cast<const uint4*>(
-                              q + (((int64_t)c.b * k + r / G) * a.Hq + c.kvh * G + r % G) * D) +
-                          c16);
+                v = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)row_at(r) * D) + c16);
             return v;
         };
         uint4 ahead = q_chunk(w * 2 + half);
@@ -592,12 +599,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             fetch_scales(p + PAGE_PAIRS);
             fetch_pids(p + PAGE_PAIRS + 2);
             cp_async_commit();
-            for (int e = 0; e < 2 && ok; ++e) {
-                const int t = 2 * p + e;
-                if (t < n_tiles && t >= SCALE_STAGES)
-                    ok = role_wait(&bars[Smem::B_SCFREE + t % SCALE_STAGES],
-                                   (t / SCALE_STAGES - 1) & 1, abort_flag, a.dev_err);
-            }
+            constexpr int PAIRS = SCALE_STAGES / 2;
+            if (p >= PAIRS)
+                ok = role_wait(&bars[Smem::B_SCFREE + p % PAIRS], (p / PAIRS - 1) & 1, abort_flag,
+                               a.dev_err);
             if (!ok) break;
             const int t = 2 * p + half;
             if (!is_v && t < n_tiles) {
@@ -609,8 +614,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                                 on ? 1.f : 0.f);
             }
             __syncwarp();
-            if ((lane & 15) == 0 && t < n_tiles)
-                mbar_arrive(&bars[Smem::B_SCALE + t % SCALE_STAGES]);
+            if (lane == 0) mbar_arrive(&bars[Smem::B_SCALE + p % PAIRS]);
         }
         cp_async_wait<0>();
     } else {
@@ -720,37 +724,34 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                 const float2* stat = s_stat + jp * 2 * ROWS;
                 float mt = -INFINITY, lt = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2 * REP; ++c)
-                    mt = fmaxf(mt, stat[(c & 1) * ROWS + (c >> 1) * COPY + r].x);
+                for (int c = 0; c < REP; ++c) mt = fmaxf(mt, stat[c * COPY + r].x);
                 const float mt_use = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-                for (int c = 0; c < 2 * REP; ++c) {
-                    const float2 x = stat[(c & 1) * ROWS + (c >> 1) * COPY + r];
-                    lt += fast_exp2(x.x - mt_use) * x.y;
+                for (int c = 0; c < REP; ++c) {
+                    const float2 x = stat[c * COPY + r];
+                    lt += fast_exp2(x.x - mt_use) * (x.y + stat[ROWS + c * COPY + r].y);
                 }
-                // the lane's O stands to the larger of its sets' references (-inf
-                // where it saw no key: weight 0)
-                const float wgt =
-                    lt > 0.f ? fast_exp2(fmaxf(stat[ln].x, stat[ROWS + ln].x) - mt_use) / lt : 0.f;
+                // (a lane that saw no key has reference -inf: weight 0)
+                const float wgt = lt > 0.f ? fast_exp2(stat[ln].x - mt_use) / lt : 0.f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[Smem::B_STFREE + jp]);
-                auto row_of = [&](int rr) {
-                    return ((int64_t)prev.b * k + rr / G) * a.Hq + prev.kvh * G + rr % G;
-                };
+                const int64_t row0 = (int64_t)prev.b * k * a.Hq + prev.kvh * G;
                 if (ok && ln < R && ln < COPY) {
                     const float lse = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
                     if (!complete)
                         prm.part_lse[(int64_t)slot * ROWS + r] = lse;
                     else if (a.lse)
-                        a.lse[row_of(r)] = lse;
+                        a.lse[row0 + row_at(r)] = lse;
                 }
                 float* red = reinterpret_cast<float*>(sm + Smem::Q + jp * 2 * Q_PART);
                 const int t = (pv ? 96 : (warp - 12) * 32) + lane, cg = lane & 15;
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row0 * D + cg * 4;
+                float* part = prm.part_o + (int64_t)slot * ROWS * D + cg * 4;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 64) {
                     if (ok && ((warp & 3) * 32) % COPY < R) {
                         float4* dst = reinterpret_cast<float4*>(red + ln * 64);
-#pragma unroll 1
+#pragma unroll 2
                         for (int h = 0; h < 4; ++h) {
                             uint32_t ov[16];
                             tmem_ld16(tmem + ((uint32_t)((warp & 3) * 32) << 16) + TM_O + c0 +
@@ -770,7 +771,7 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                     named_bar_sync(2, 128);
                     tc_fence_after();
                     if (pv && c0) break;
-#pragma unroll 1
+#pragma unroll 2
                     for (int row = t >> 4; row < (ok ? R : 0); row += c0 ? 6 : 8) {
                         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -783,13 +784,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             acc.w += x.w;
                         }
                         if (complete)
-                            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) +
-                                                      row_of(row) * D + c0 + cg * 4) =
+                            *reinterpret_cast<uint2*>(out + (int64_t)row_at(row) * D + c0) =
                                 make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
                         else
-                            *reinterpret_cast<float4*>(prm.part_o +
-                                                       ((int64_t)slot * ROWS + row) * D + c0 +
-                                                       cg * 4) = acc;
+                            *reinterpret_cast<float4*>(part + row * D + c0) = acc;
                     }
                     // the shares are read: the second half's may follow, the next
                     // but one piece's q rows after those
@@ -820,7 +818,12 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
             named_bar_sync(1, 11 * 32);
         }
         regs_inc<160>();
-        // ================= softmax sets (0: warps 0-3, even tiles; 1: 8-11, odd) =================
+        // ================= softmax sets (0: warps 0-3; 1: 8-11) =================
+        // Both take every tile, and of a lane's blocks half each: blocks set and
+        // set + 2 (REP 1), block 2 copy + set (REP 2), 16 keys of block copy
+        // (REP 4).  The two warps of a lane quadrant meet once per tile, where
+        // they agree on the reference; every raw score that is not in registers by
+        // then lies in columns [0, 64), and P goes to [64, 128).
         const int set = warp >= 8 ? 1 : 0;
         const int quad = warp & 3;            // TMEM lane quadrant
         const int ln = quad * 32 + lane;      // TMEM lane of this thread
@@ -828,113 +831,111 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         const bool row_valid = r < R;
         const bool quad_active = (quad * 32) % COPY < R;
         const int i_row = row_valid ? r / G : k - 1;
-        const int blk0 = copy * NBLK;         // the first 32-key block of this thread
+        const int blk0 = REP == 1 ? set : REP == 2 ? 2 * copy + set : copy;
+        const int col0 = REP == 4 ? 16 * set : 0;  // this thread's first key of a block
         const float sl2 = fabsf(a.scale) * kLog2e;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-        float* s_ref = reinterpret_cast<float*>(sm + Smem::REF);
-        float m = -INFINITY, l = 0.f;  // reference that the row sum l of this set stands to
-        float qm = 0.f;         // accumulator units to log2 units, before the page's scale
-        int low = 0;            // first key of this row's window
-        uint64_t mrow = 0;
+        float* s_most = reinterpret_cast<float*>(sm + Smem::MOST);
+        float m = -INFINITY, l = 0.f;  // reference of the lane, and the row sum to it
         Cursor cur;
         if (n_tiles > 0) start_at(cur);
         bool ok = true;
-        int pc = -1;
-        for (int it = 0; it < n_tiles; ++it) {
-            const bool first = (it == 0) || (cur.lt == 0);
-            const bool last = (it == n_tiles - 1) || (cur.lt == cur.nb - 1);
-            const bool mine = (it & 1) == set;
-            const int sb = it % NS;
-            const int ctx = s_ctx[cur.b], key0 = cur.key0();
-            if (first) {
-                ++pc;
-                m = -INFINITY;
-                l = 0.f;
-                const uint64_t bits = draft_bits(a, cur.b, i_row);
-                mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
-                if (WIN) low = window_low(a, ctx + draft_depth(bits));
-                if (ok)
-                    ok = role_wait(&bars[Smem::B_EXP + pc % EXP_STAGES], (pc / EXP_STAGES) & 1,
-                                   abort_flag, a.dev_err);
-                if (ok && row_valid)
-                    qm = ldexpf(sl2, (int)s_exp[(pc % EXP_STAGES) * ROWS + r]);
-            }
-            if (mine) {
-                if (ok)
-                    ok = role_wait(&bars[Smem::B_SCALE + it % SCALE_STAGES],
-                                   (it / SCALE_STAGES) & 1, abort_flag, a.dev_err);
-                if (ok)
-                    ok = role_wait(&bars[Smem::B_SFULL + sb], (it / NS) & 1, abort_flag,
-                                   a.dev_err);
-                if (ok && quad_active) {
-                    tc_fence_after();
-                    const uint32_t s_mine = lane_base + sb * TN;
-                    const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
-                    // a tile's edge: invisible keys' scores become -inf where they are
-                    const bool full = key0 + TN <= ctx &&
-                                      (!WIN || key0 >= low || key0 + TN <= a.sinks);
-                    if (__any_sync(0xffffffffu, !full)) {
+        int it = 0, sb = 0, phase = 0;  // tile, its S buffer, that buffer's phase
+        for (int pc = 0; it < n_tiles; ++pc) {
+        // ---- a piece
+        const int ctx = s_ctx[cur.b], it0 = it;
+        const int it1 = min(n_tiles, it + cur.nb - cur.lt);
+        m = -INFINITY;
+        l = 0.f;
+        const uint64_t bits = draft_bits(a, cur.b, i_row);
+        const uint64_t mrow = WIN ? window_bits(a, bits, i_row, ctx) : bits;
+        // first key of this row's window
+        const int low = WIN ? window_low(a, ctx + draft_depth(bits)) : 0;
+        if (ok)
+            ok = role_wait(&bars[Smem::B_EXP + pc % EXP_STAGES], (pc / EXP_STAGES) & 1,
+                           abort_flag, a.dev_err);
+        // accumulator units to log2 units, before the page's scale
+        const float qm =
+            ok && row_valid ? ldexpf(sl2, (int)s_exp[(pc % EXP_STAGES) * ROWS + r]) : 0.f;
 #pragma unroll 1
-                        for (int blk = blk0; blk < blk0 + NBLK; ++blk) {
-                            uint32_t raw[32];
-                            tmem_ld32(s_mine + blk * 32, raw);
-                            const uint32_t vis = visible32<WIN>(key0 + blk * 32, ctx + k, ctx,
-                                                                mrow, low, a.sinks);
+        for (; it < it1; ++it, ++cur.lt) {
+            const int key0 = cur.key0();
+            if (ok && !(it & 1))
+                ok = role_wait(&bars[Smem::B_SCALE + (it % SCALE_STAGES) / 2],
+                               (it / SCALE_STAGES) & 1, abort_flag, a.dev_err);
+            if (ok) ok = role_wait(&bars[Smem::B_SFULL + sb], phase, abort_flag, a.dev_err);
+            if (quad_active) {  // (after an abort: of no consequence, but the barrier is met)
+                tc_fence_after();
+                const uint32_t s_mine = lane_base + sb * TN;
+                const float4* sc = s_scale + (it % SCALE_STAGES) * MAX_CHUNKS;
+                // a tile's edge: invisible keys' scores become -inf where they are
+                const bool full = key0 + TN <= ctx &&
+                                  (!WIN || key0 >= low || key0 + TN <= a.sinks);
+                if (__any_sync(0xffffffffu, !full)) {
+#pragma unroll 1
+                    for (int blk = blk0; blk < blk0 + 2 * NBLK; blk += 2) {
+                        const uint32_t vis = visible32<WIN>(key0 + blk * 32, ctx + k, ctx, mrow,
+                                                            low, a.sinks) >> col0;
+#pragma unroll 1
+                        for (int g = 0; g < GROUPS; ++g) {
+                            uint32_t raw[16];
+                            tmem_ld16(s_mine + blk * 32 + col0 + 16 * g, raw);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (!((vis >> c) & 1u)) raw[c] = __float_as_uint(-INFINITY);
-                            tmem_st32(s_mine + blk * 32, raw);
+                            for (int c = 0; c < 16; ++c)
+                                if (!((vis >> (16 * g + c)) & 1u))
+                                    raw[c] = __float_as_uint(-INFINITY);
+                            tmem_st16(s_mine + blk * 32 + col0 + 16 * g, raw);
                         }
-                        tmem_wait_st();
                     }
-                    // scores of a block with the whole power of two of its largest w
-                    // (-inf: no visible key); mult is not 0, so that -inf stays -inf
-                    uint32_t r0[16], r1[16];
-                    auto load_block = [&](int blk, float4& s0, float4& s1) {
-                        float x0, x1;
-                        tmem_ld16_max(s_mine + blk * 32, r0, x0);
-                        tmem_ld16_max(s_mine + blk * 32 + 16, r1, x1);
-                        s0 = sc[(blk * 32) >> lgCH];
-                        s1 = sc[(blk * 32 + 16) >> lgCH];
-                        s0.x = fmaxf(qm * s0.x, 1.2e-38f);
-                        s1.x = fmaxf(qm * s1.x, 1.2e-38f);
-                        tmem_wait_ld();
-                        return floorf(fmaxf(fmaf(x0, s0.x, s0.y), fmaf(x1, s1.x, s1.y)));
-                    };
-                    float4 s0, s1;
-                    float top = load_block(blk0 + NBLK - 1, s0, s1), most = top;
-                    if (NBLK > 1) {
-#pragma unroll 1
-                        for (int blk = blk0; blk < blk0 + NBLK - 1; ++blk)
-                            most = fmaxf(most, load_block(blk, s0, s1));
+                    tmem_wait_st();
+                }
+                // scores of a block with the whole power of two of its largest w
+                // (-inf: no visible key); mult is not 0, so that -inf stays -inf
+                uint32_t raw[GROUPS][16];
+                float4 s[GROUPS];
+                auto load_block = [&](int blk) {
+                    float x[GROUPS], top = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) {
+                        tmem_ld16_max(s_mine + blk * 32 + col0 + 16 * g, raw[g], x[g]);
+                        s[g] = sc[(blk * 32 + col0 + 16 * g) >> lgCH];
+                        s[g].x = fmaxf(qm * s[g].x, 1.2e-38f);
                     }
-                    // the lane's reference, handed from tile to tile through shared
-                    // memory (its two softmax warps alternate)
-                    if (it > 0)
-                        ok = role_wait(&bars[Smem::B_REF + quad], (it - 1) & 1, abort_flag,
-                                       a.dev_err);
-                    const float ref = first ? -INFINITY : s_ref[ln];
-                    const bool move = most > ref + kMoveThreshold;  // also -inf -> finite
-                    const float next = move ? most : ref;
-                    if (first || move) s_ref[ln] = next;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars[Smem::B_REF + quad]);
-                    if (next > m) l *= m == -INFINITY ? 0.f : pow2_neg((int)fminf(next - m, 255.f));
-                    m = next;
-                    if (!first && __any_sync(0xffffffffu, move)) {
-                        // a moved reference: O (all of the piece so far, once P V of
-                        // the tile before is done) shrinks with it
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) top = fmaxf(top, fmaf(x[g], s[g].x, s[g].y));
+                    return floorf(top);
+                };
+                float most = -INFINITY;
+                if (NBLK > 1) most = load_block(blk0);
+                float top = load_block(blk0 + 2 * (NBLK - 1));
+                most = fmaxf(most, top);
+                // both warps' largest w; the reference follows when that exceeds it
+                // by far (also -inf -> finite)
+                float* mine = s_most + (it & 1) * 2 * ROWS + set * ROWS + ln;
+                *mine = most;
+                tc_fence_before();
+                named_bar_sync(5 + quad, 64);
+                tc_fence_after();
+                most = fmaxf(most, mine[set ? -ROWS : ROWS]);
+                if (REP == 4) top = most;  // one block, half of it each
+                const bool move = most > m + kMoveThreshold;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float alpha = !move             ? 1.f
+                                        : m == -INFINITY ? 0.f
+                                                          : pow2_neg((int)fminf(most - m, 255.f));
+                    l *= alpha;
+                    if (move) m = most;
+                    if (it > it0) {
+                        // O (all of the piece so far, once P V of the tile before
+                        // is done) shrinks with it
                         if (ok)
                             ok = role_wait(&bars[Smem::B_SFREE + (it - 1) % NS],
                                            ((it - 1) / NS) & 1, abort_flag, a.dev_err);
                         tc_fence_after();
-                        const float alpha =
-                            !move                ? 1.f
-                            : ref == -INFINITY ? 0.f
-                                                 : pow2_neg((int)fminf(next - ref, 255.f));
 #pragma unroll 1
-                        for (int c4 = 0; c4 < D / 16; ++c4) {
+                        for (int c4 = set * 4; c4 < set * 4 + 4; ++c4) {
                             uint32_t ov[16];
                             tmem_ld16(lane_base + TM_O + c4 * 16, ov);
                             tmem_wait_ld();
@@ -944,52 +945,62 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
                             tmem_st16(lane_base + TM_O + c4 * 16, ov);
                         }
                     }
-                    uint32_t sfw = 0x7f7f7f7fu;  // scale bytes of this lane's blocks
+                }
+                uint8_t* sfp = sm + Smem::SFP + sb * 512 + lane * 16 + quad * 4;
 #pragma unroll 1
-                    for (int blk = blk0 + NBLK - 1; blk >= blk0; --blk) {
-                        uint32_t pw[16];
-                        if (NBLK > 1) top = load_block(blk, s0, s1);
-                        const float n = fmaxf(top - m, -110.f);  // (NaN without a key: -110)
-                        const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
-                        const float base = top == -INFINITY ? 0.f : 7.f - (m + n);
-                        const float w0 =
-                            group_weights(r0, s0.x, base + s0.y, s0.w != 0.f, pw, pw + 8);
-                        const float w1 =
-                            group_weights(r1, s1.x, base + s1.y, s1.w != 0.f, pw + 4, pw + 12);
-                        l += (w0 * s0.z + w1 * s1.z) * __uint_as_float(sf << 23);
-                        sfw = (sfw & ~(0xffu << (8 * blk))) | (sf << (8 * blk));
+                for (int blk = blk0 + 2 * (NBLK - 1); blk >= blk0; blk -= 2) {
+                    uint32_t pw[GROUPS * 8];
+                    if (NBLK > 1 && blk == blk0) top = load_block(blk);
+                    const float n = fmaxf(top - m, -110.f);  // (NaN without a key: -110)
+                    const uint32_t sf = (uint32_t)(120 + (int)n);  // byte of 2^(n - 7)
+                    const float base = top == -INFINITY ? 0.f : 7.f - (m + n);
+                    float w = 0.f;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        w += group_weights(raw[g], s[g].x, base + s[g].y, s[g].w != 0.f,
+                                           pw + 4 * g, pw + 4 * (GROUPS + g)) *
+                             s[g].z;
+                    l += w * __uint_as_float(sf << 23);
+                    if (REP < 4 || set == 0) sfp[blk] = (uint8_t)sf;
+                    if constexpr (REP < 4) {
                         tmem_st16(s_mine + p_col(blk), pw);
+                    } else {
+                        tmem_st4(s_mine + p_col(blk) + 4 * set, pw);
+                        tmem_st4(s_mine + p_col(blk) + 8 + 4 * set, pw + 4);
                     }
-                    if (REP > 1) {  // the blocks of the other copies
-                        const uint32_t zero[16] = {};
+                }
+                if (REP > 1) {  // the blocks of the other copies
+                    const uint32_t zero[16] = {};
+                    if (REP == 2) tmem_st16(s_mine + p_col(blk0 ^ 2), zero);
+                    if (REP == 4)
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b)
-                            if (b / NBLK != copy) tmem_st16(s_mine + p_col(b), zero);
-                    }
-                    *reinterpret_cast<uint32_t*>(sm + Smem::SFP + sb * 512 + lane * 16 +
-                                                 quad * 4) = sfw;
-                    fence_proxy_async_smem();
-                    tmem_wait_st();
+                        for (int e = 1; e < 4; ++e)
+                            tmem_st8(s_mine + p_col((copy + e) & 3) + 8 * set, zero);
                 }
-                // P of this tile stored (every warp of the set arrives, active or not)
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[Smem::B_PREADY + sb]);
-                    mbar_arrive(&bars[Smem::B_SCFREE + it % SCALE_STAGES]);
-                }
+                fence_proxy_async_smem();
+                tmem_wait_st();
             }
-            if (last) {
-                // this set's reference and row sum to the epilogue (which has
-                // read those of the piece before the last)
-                if (ok && pc >= 2)
-                    ok = role_wait(&bars[Smem::B_STFREE + (pc & 1)], ((pc >> 1) - 1) & 1,
-                                   abort_flag, a.dev_err);
-                s_stat[((pc & 1) * 2 + set) * ROWS + ln] = make_float2(m, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[Smem::B_STAT + (pc & 1)]);
+            // P of this tile stored (every warp arrives, active or not)
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[Smem::B_PREADY + sb]);
+                if (it & 1) mbar_arrive(&bars[Smem::B_SCFREE + (it % SCALE_STAGES) / 2]);
             }
-            if (it + 1 < n_tiles) cur.next(s_ctx, a);
+            if (++sb == NS) {
+                sb = 0;
+                phase ^= 1;
+            }
+        }
+        // this set's reference and row sum to the epilogue (which has read
+        // those of the piece before the last)
+        if (ok && pc >= 2)
+            ok = role_wait(&bars[Smem::B_STFREE + (pc & 1)], ((pc >> 1) - 1) & 1, abort_flag,
+                           a.dev_err);
+        s_stat[((pc & 1) * 2 + set) * ROWS + ln] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Smem::B_STAT + (pc & 1)]);
+        if (it < n_tiles) cur.next_segment(s_ctx, a);
         }
     }
 
