@@ -187,6 +187,15 @@ def _check_page_scales(k_cache, v_cache, k_scale, v_scale) -> None:
             raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
 
 
+def _check_scales(k_cache, v_cache, k_scale, v_scale) -> None:
+    """_check_page_scales, and an int8 cache's scales: float16 [num_pages, Hkv, P]."""
+    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    if k_cache.dtype == torch.int8:
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float16 or s.shape != k_cache.shape[:3]):
+                raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
+
+
 def _same_device(first, *tensors) -> None:
     """Every tensor lies on the current device (kernels launch there)."""
     dev = first.get_device()  # -1: not on a GPU
@@ -282,7 +291,7 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draf
         raise ValueError("lse must be float32 [B, k, Hq]")
     if tree_mask is not None and (tree_mask.shape != (B, k) or tree_mask.element_size() != 8):
         raise ValueError("tree_mask must hold 64-bit words [B, num_draft]")
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
     _same_device(q, k_cache, v_cache, block_table, ctx_lens, tree_mask, out, lse, k_scale, v_scale)
     _check(load().spec_verify_attn_window(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
@@ -442,7 +451,7 @@ def spec_rope_append(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_
         raise ValueError("new_lens must be int32 [B]")
     if rope_table is not None and (rope_table.element_size() != 8 or rope_table.dim() != 1):
         raise ValueError("rope_table must be a row of 64-bit words")
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
     _same_device(k_new, v_new, q, q_out, k_cache, v_cache, block_table, ctx_lens, rope_table,
                  positions, new_lens, k_scale, v_scale)
     qp, qs = _token_rows(q, "q", B, n, Hq, D) if q is not None else (None, 0)
@@ -473,7 +482,7 @@ def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=Non
         raise ValueError("block_table must be int32 [B, max_pages] and lens int32 [B]")
     if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,)):
         raise ValueError("starts must be int32 [B]")
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
     _same_device(k_cache, v_cache, block_table, lens, k_out, v_out, starts, k_scale, v_scale)
     _check(load().spec_kv_gather(
         _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _TORCH_DT[k_cache.dtype],

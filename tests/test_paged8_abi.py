@@ -229,3 +229,25 @@ def test_plain_window_closed_forms():
     assert torch.equal(a[0], b[0])
     assert paged8.visible(10, 3, 1, None, 4, 2) == [0, 1, 8, 9, 10, 11]
     assert paged8.visible(10, 3, 2, 0b101, 4, 0) == [8, 9, 10, 12]
+
+
+def test_binding_checks_int8_scales(binding):
+    """The windowed attention, the rotary append and the gather take an int8
+    cache's scales as float16 [num_pages, Hkv, P] and nothing else (the library
+    sees a bare pointer)."""
+    B, k, Hq, Hkv, D, P, NP = 2, 4, 8, 2, 64, 16, 4
+    q = torch.zeros(B, k, Hq, D, dtype=torch.bfloat16)
+    kn = torch.zeros(B, k, Hkv, D, dtype=torch.bfloat16)
+    c8 = torch.zeros(NP, Hkv, P, D, dtype=torch.int8)
+    good = torch.zeros(NP, Hkv, P, dtype=torch.float16)
+    bt = torch.zeros(B, 2, dtype=torch.int32)
+    ctx = torch.zeros(B, dtype=torch.int32)
+    for bad in (good.float(), good[:3], good[:, :, 0]):
+        for pair in ((bad, good), (good, bad)):
+            kw = dict(k_scale=pair[0], v_scale=pair[1])
+            with pytest.raises(ValueError, match="int8 cache"):
+                binding.spec_verify_attn_window(q, c8, c8, bt, ctx, k, 0.1, 8, 0, q, **kw)
+            with pytest.raises(ValueError, match="int8 cache"):
+                binding.spec_rope_append(q, kn, kn, q, c8, c8, bt, ctx, None, **kw)
+            with pytest.raises(ValueError, match="int8 cache"):
+                binding.spec_kv_gather(c8, c8, bt, ctx, kn, kn.clone(), **kw)
