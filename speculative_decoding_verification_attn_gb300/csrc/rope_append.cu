@@ -62,7 +62,7 @@ template <typename T> struct Chunk;
 template <> struct Chunk<__nv_bfloat16> {
     uint4 r;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        r = __ldg(reinterpret_cast<const uint4*>(p));
+        r = *reinterpret_cast<const uint4*>(p);  // (q_out may be q: no read-only path)
     }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
@@ -85,8 +85,8 @@ template <> struct Chunk<__nv_bfloat16> {
 template <> struct Chunk<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
