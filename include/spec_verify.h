@@ -157,10 +157,17 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  * 16-byte aligned.  A bf16 query over a bf16 cache with head_dim 128, a
  * power-of-two page_size in [16, 256] and batch <= 1024 runs on a
  * tensor-core kernel: the warp-MMA kernel when num_draft * (num_q_heads /
- * num_kv_heads) <= 16, the tcgen05 kernel up to 128.  Every other accepted
+ * num_kv_heads) <= 16, the tcgen05 kernel up to 128.  An E4M3 cache runs on a
+ * tcgen05 kernel of its own at the same shapes (up to 128 rows, num_pages *
+ * num_kv_heads * page_size < 2^31).  Every other accepted
  * shape runs on the CUDA cores: in one launch when every sequence's keys
  * (max_pages_per_seq * page_size of them) fit the single-pass kernel's
- * shared memory, else on the chunked split-KV kernel and its combine.
+ * shared memory (not an E4M3 cache's), else on the chunked split-KV kernel
+ * and its combine.
+ * K and V are finite at every key below ctx_b + num_draft, seen or not: a
+ * weight of zero does not stop an infinity.  On the E4M3 tensor-core kernel
+ * page scales of V up to 1e-30 count as zero, and those of one sequence should
+ * lie within 2^80 of each other.
  */
 SPEC_API int spec_verify_attn(const void *q, const void *k_cache, const void *v_cache,
                      const void *k_scale, const void *v_scale,

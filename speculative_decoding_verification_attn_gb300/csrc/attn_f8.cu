@@ -23,8 +23,8 @@
 //    log2(sv_g) in the exponent; the row sum takes each 16-key group's sum of w
 //    back by 1 / sv_g, in fp32.  And since the block scales carry the distance
 //    to the reference, m need not be the running maximum: it is a whole number
-//    near the first block's, moved only when a block exceeds it by 2^40, so one
-//    pass over a tile's scores does (its blocks' maxima come with their load).
+//    near the first tile's largest, moved only when a tile exceeds it by 2^40
+//    (the blocks' maxima come with the load of their scores).
 //
 // What bounds it: the bytes of the cache (32 KB per 128 keys and kv-head), with
 // the tensor pipe close behind: 8 + 8 MMAs of M128 N128 K32 per 128-key tile
@@ -32,24 +32,42 @@
 // tile in ~1400.  So nothing may stand between the copy and the MMAs: no
 // widening pass, and the softmax below a tile's time on every SMSP.
 //
+// Measured (one call among others, combine included; the bytes' floor at 6768
+// GB/s): 32 sequences of 1 to 8K keys, 32/8 heads, 4 drafts 62.7 us (4.87 TB/s,
+// floor 45.1); 32 x 2048 keys, 64/8 heads, 8 drafts 45 us (21.2); 4 x 32K keys,
+// 28/4 heads, 16-node trees 50 us (20.0).  A tile takes ~1500, ~1700 and ~2600
+// cycles there (16, 64 and 112 rows): the softmax of the rows is what is left
+// above the HBM share, of which half is its arithmetic (the exponentials and
+// the conversions to e4m3 share one pipe, 4 cycles per warp instruction each:
+// 16 per pair of weights) and the rest its waits, loads and hand-overs.
+// The combine costs 5 us of a call, a piece's end ~1.
+//
 // Layout.  Persistent grid, the tile list split as in the 128-key bf16 kernel
 // (TileSplit, partials merged by the combine kernel).
 //  * TMEM: three S buffers [0,384), one O [384,512).  P goes over S columns
 //    [64,128) of its tile (p_col), the scale bytes of P and of V (all one) over
 //    [0,4) / [4,8).  Three tiles are in flight: the chain of one tile (Q K^T,
-//    softmax, P V, ~3800 cycles at 32 rows) is longer than two tiles' share of
-//    HBM.  That both softmax sets add into one O is what frees the third buffer;
-//    they share each lane's reference, handed on from tile to tile.
-//  * Warps: 0-3 and 8-11 two softmax sets on alternate tiles; 4 Q K^T issue; 5
-//    and 6 TMA of K and of V; 7 P V issue; 12-14 turn the q rows of the next
-//    piece into hi / lo; 15 looks up pages and their scales.  16 warps share the block's
-//    64K registers (setmaxnreg: 160, 96, 160, 96).
+//    softmax, P V, ~3100 cycles) is longer than two tiles' share of HBM.  That
+//    both softmax sets add into one O is what frees the third buffer.
+//  * Warps: 0-3 and 8-11 two softmax sets; 4 Q K^T issue; 5 and 6 TMA of K and of
+//    V; 7 P V issue; 12-14 turn the q rows of the next piece into hi / lo; 7 and
+//    12-14, one per TMEM lane quadrant, write a finished piece out while the
+//    softmax is at the next one (by the softmax warps themselves a piece's end
+//    cost 3.7 us, and the 16-row step above 3.9 us more); 15 looks up pages and
+//    their scales.  16 warps share the block's 64K registers (setmaxnreg: 160,
+//    96, 160, 96).
+//  * Softmax: both sets take every tile, half of a lane's keys each, and meet once
+//    per tile to agree on the reference.  Alternate tiles instead (the
+//    reference handed on from set to set) left each tile twice as long in the
+//    softmax, and three tiles in flight did not cover that: 49.4, 53.0 us at 64
+//    and 112 rows against 45.2, 50.4 (at 16 rows, where a set's work per tile
+//    is small against its waits, 60.8 against 63.3).
 //  * Rows: R = k * G query rows are the M side of one MMA.  R <= 64 (REP 2) and
 //    R <= 32 (REP 4): the rows stand REP times and copy c takes the 32-key
 //    blocks of its own, with P zero elsewhere, so that every softmax thread
 //    has work and a tile costs it 1 / REP of the exponentials; the copies'
 //    (max, sum, O) merge through shared memory once per piece.
-//  * Every wait is bounded (warp_wait); after a timeout every role skips its
+//  * Every wait is bounded (role_wait); after a timeout every role skips its
 //    work, drains its copies and tensor-core operations and returns.
 #include <cuda.h>
 #include <math.h>
@@ -74,8 +92,8 @@ constexpr int PAGE_PAIRS = 2;
 constexpr int RAW_STAGES = 4;          // pairs of tiles
 constexpr int ROW_STAGES = 16;         // pairs of tiles
 constexpr int SCALE_STAGES = 16;       // tiles
-// row exponents: the q rows of piece j are written after the epilogue of piece
-// j - 2, so no stage before j - 1's is still to be read
+// row exponents: the q rows of piece j are converted after piece j - 2 is written
+// out, so no stage before j - 1's is still to be read
 constexpr int EXP_STAGES = 4;
 constexpr int MAX_BATCH = 1024;
 constexpr uint32_t TMEM_COLS = 512;
@@ -87,9 +105,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the reference moves when a block's largest w exceeds it by more than this
 // (log2 units): the block scales carry any distance below, fp32 sums this one
 constexpr float kMoveThreshold = 40.f;
-// tiles charged per segment in the split (ragged 8B step: 83, 71.2, 69.7, 67.2,
-// 67.0 us at 0, 2, 3, 4, 6; a piece end costs 3.7 us, a tile 0.9)
-constexpr int kSplitAlpha = 4;
+// tiles charged per segment in the split (1, 2, 3 and 4: 63.9, 63.3, 64.1, 64.5 us
+// on the ragged 16-row step, 44.8, 44.8, 44.5, 45.3 at 64 rows, 37.8, 37.7, 37.3,
+// 37.3 with a 1024-key window)
+constexpr int kSplitAlpha = 3;
 
 struct Smem {
     static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
@@ -107,7 +126,8 @@ struct Smem {
                          B_SCFREE = B_SCALE + SCALE_STAGES / 2,
                          B_ROWS = B_SCFREE + SCALE_STAGES / 2,
                          NUM_BARS = B_ROWS + ROW_STAGES;
-    static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;  // tmem base, abort flag, range at +16
+    // tmem base, abort flag, the CTA's tile range at +16
+    static constexpr int MISC = BARS + (NUM_BARS + 1) / 2 * 16;
     static constexpr int FIRST = MISC + 32;           // the CTA's first cursor
     static constexpr int MOST = FIRST + 48;           // largest w of [tile & 1][set][lane]
     // page warp: [stage][2 tiles][8] block-table entries, [stage][2 tiles][k, v][8]
@@ -137,9 +157,9 @@ struct F8Params {
     int* seg_pre;     // [B+1]
 };
 
-// warp_wait in fewer instructions.  Five roles of different code share each
-// SM's instruction caches, so what the hot loops hold counts: the same softmax
-// beside 8 KB more code in other roles ran up to 15 % slower.
+// warp_wait in fewer instructions.  Roles of different code share each SM's
+// instruction caches, so what the hot loops hold counts: the same softmax beside
+// 8 KB more code in other roles ran up to 15 % slower.
 __device__ __forceinline__ bool role_wait(uint64_t* bar, uint32_t parity,
                                           volatile int* abort_flag, int* dev_err) {
     constexpr uint32_t kAll = 0xffffffffu;
@@ -175,7 +195,8 @@ __device__ __forceinline__ uint32_t visible32(int k0, int end, int ctx, uint64_t
     return (c | d) & below(end - k0);
 }
 
-// Two values as e4m3 hi + lo (8 significant bits together): the rest after hi is exact in fp16, which holds the values with 11 bits.
+// Two values as e4m3 hi + lo (8 significant bits together): the rest after hi is
+// exact in fp16, which holds the values with 11 bits.
 __device__ __forceinline__ void split_e4m3x2(float a, float b, uint16_t& hi, uint16_t& lo) {
     uint32_t h, back, rest;
     h = pack_f16x2(a, b);

@@ -174,9 +174,10 @@ __device__ __forceinline__ void tc_fence_after() {
 // warp-uniform operands; elect.sync picks the one lane (the lowest) that
 // issues.  Issued that way the operands stay in the uniform datapath; from a
 // one-lane branch with operands computed at run time each instruction costs
-// several times more issue cycles.  ts: A from TMEM; commit: arrive on `bar` once every tcgen05 op this thread issued
-// is done (it must come from the warp that issued them); cp: a 128-row x
-// 256-bit matrix (a shared-memory descriptor) into TMEM lanes 0..127.
+// several times more issue cycles.  ts: A from TMEM; commit: arrive on `bar`
+// once every tcgen05 op this thread issued is done (it must come from the warp
+// that issued them); cp: a 128-row x 256-bit matrix (a shared-memory
+// descriptor) into TMEM lanes 0..127.
 __device__ __forceinline__ void umma_ts_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
     asm volatile(
