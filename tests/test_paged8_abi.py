@@ -231,10 +231,11 @@ def test_plain_window_closed_forms():
     assert paged8.visible(10, 3, 2, 0b101, 4, 0) == [8, 9, 10, 12]
 
 
-def test_binding_checks_int8_scales(binding):
+def test_binding_checks_int8_scales(lib):
     """The windowed attention, the rotary append and the gather take an int8
     cache's scales as float16 [num_pages, Hkv, P] and nothing else (the library
     sees a bare pointer)."""
+    from speculative_decoding_verification_attn_gb300 import binding
     B, k, Hq, Hkv, D, P, NP = 2, 4, 8, 2, 64, 16, 4
     q = torch.zeros(B, k, Hq, D, dtype=torch.bfloat16)
     kn = torch.zeros(B, k, Hkv, D, dtype=torch.bfloat16)
