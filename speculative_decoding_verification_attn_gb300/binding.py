@@ -179,31 +179,54 @@ def _check_page_scales(k_cache, v_cache, k_scale, v_scale) -> None:
     library takes a bare pointer and cannot tell)."""
     if k_cache.dtype != torch.float8_e4m3fn:
         return
-    if v_cache.dtype != k_cache.dtype:
+    if v_cache.dtype != torch.float8_e4m3fn:
         raise ValueError("k_cache and v_cache must share a dtype")
     want = k_cache.shape[:2]
-    for s in (k_scale, v_scale):
-        if s is not None and (s.dtype != torch.float32 or s.shape != want):
-            raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
+    if (k_scale is not None and (k_scale.dtype != torch.float32 or k_scale.shape != want)
+            or v_scale is not None and (v_scale.dtype != torch.float32 or v_scale.shape != want)):
+        raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
 
 
 def _check_scales(k_cache, v_cache, k_scale, v_scale) -> None:
     """_check_page_scales, and an int8 cache's scales: float16 [num_pages, Hkv, P]."""
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
-    if k_cache.dtype == torch.int8:
-        for s in (k_scale, v_scale):
-            if s is not None and (s.dtype != torch.float16 or s.shape != k_cache.shape[:3]):
-                raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
+    if k_cache.dtype != torch.int8:
+        return _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    for s in (k_scale, v_scale):
+        if s is not None and (s.dtype != torch.float16 or s.shape != k_cache.shape[:3]):
+            raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
 
 
-def _same_device(first, *tensors) -> None:
-    """Every tensor lies on the current device (kernels launch there)."""
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _device_of(first) -> int:
+    """The current device, on which ``first`` has to lie (kernels launch there)."""
     dev = first.get_device()  # -1: not on a GPU
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _get_device():
         raise ValueError("tensors must lie on the current CUDA device")
+    return dev
+
+
+def _ptrs(dev: int, *tensors):
+    """Pointers of dense tensors of device ``dev`` (None stays None), in one
+    pass: a call's checks cost the host as much as its launch."""
+    out = []
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
             raise ValueError("tensors must lie on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _stream_on(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def spec_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int, scale: float,
@@ -292,12 +315,13 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draf
     if tree_mask is not None and (tree_mask.shape != (B, k) or tree_mask.element_size() != 8):
         raise ValueError("tree_mask must hold 64-bit words [B, num_draft]")
     _check_scales(k_cache, v_cache, k_scale, v_scale)
-    _same_device(q, k_cache, v_cache, block_table, ctx_lens, tree_mask, out, lse, k_scale, v_scale)
+    dev = _device_of(q)
+    qp, kp, vp, ksp, vsp, tp, cp, mp, op, lp = _ptrs(
+        dev, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, tree_mask, out, lse)
     _check(load().spec_verify_attn_window(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-        _ptr(ctx_lens), _ptr(tree_mask), B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
+        qp, kp, vp, ksp, vsp, tp, cp, mp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), int(window), int(num_sinks),
-        _ptr(out), _ptr(lse), _stream(stream)))
+        op, lp, _stream_on(stream, dev)))
 
 
 def spec_accept_tree(logits, draft_tokens, parents, num_draft: int, accepted_len, next_token,
@@ -400,9 +424,13 @@ def spec_rope_table(rotary_dim: int, theta: float = 10000.0, scaling: str = "non
     return torch.from_numpy(table.view(np.int64)).to(device), amplitude.value
 
 
-def _token_rows(t, name: str, B: int, n: int, H: int, D: int):
+def _token_rows(t, dev: int, name: str, B: int, n: int, H: int, D: int):
     """Pointer and token stride (elements) of [B, n, H, D] whose rows are dense
     and whose tokens are evenly spaced (a slice of a wider projection is)."""
+    if t.get_device() != dev:
+        raise ValueError("tensors must lie on the current CUDA device")
+    if t.is_contiguous():
+        return t.data_ptr(), H * D
     sb, sn, sh, sd = t.stride()
     if n == 1:
         sn = sb
@@ -426,20 +454,21 @@ def spec_rope_append(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_
     limits each sequence's tokens.  An e4m3 cache takes float32 scales
     [num_pages, Hkv], an int8 cache fp16 [num_pages, Hkv, P].
     """
-    B, n, Hkv, D = k_new.shape
-    NP, Hkv2, P, D2 = k_cache.shape
-    if (Hkv2, D2) != (Hkv, D) or v_new.shape != k_new.shape or v_cache.shape != k_cache.shape:
+    B, n, Hkv, D = rows = k_new.shape
+    NP, Hkv2, P, D2 = pool = k_cache.shape
+    src, kind = k_new.dtype, k_cache.dtype
+    if (Hkv2, D2) != (Hkv, D) or v_new.shape != rows or v_cache.shape != pool:
         raise ValueError("k_new / v_new must be [B, n, Hkv, D] matching the caches")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     Hq = 0
     if q is not None:
-        Hq = q.shape[2]
-        if q.shape != (B, n, Hq, D) or q_out.shape != q.shape:
+        Bq, nq, Hq, Dq = heads = q.shape
+        if (Bq, nq, Dq) != (B, n, D) or q_out.shape != heads:
             raise ValueError("q and q_out must be [B, n, Hq, D]")
-        if q.dtype != k_new.dtype or q_out.dtype != q.dtype:
+        if q.dtype != src or q_out.dtype != src:
             raise ValueError("q, q_out, k_new and v_new must share a dtype")
-    if v_new.dtype != k_new.dtype or v_cache.dtype != k_cache.dtype:
+    if v_new.dtype != src or v_cache.dtype != kind:
         raise ValueError("k and v must share a dtype")
     if (block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32
             or block_table.shape[0] != B or ctx_lens.shape != (B,)):
@@ -452,18 +481,21 @@ def spec_rope_append(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_
     if rope_table is not None and (rope_table.element_size() != 8 or rope_table.dim() != 1):
         raise ValueError("rope_table must be a row of 64-bit words")
     _check_scales(k_cache, v_cache, k_scale, v_scale)
-    _same_device(k_new, v_new, q, q_out, k_cache, v_cache, block_table, ctx_lens, rope_table,
-                 positions, new_lens, k_scale, v_scale)
-    qp, qs = _token_rows(q, "q", B, n, Hq, D) if q is not None else (None, 0)
-    op, os_ = _token_rows(q_out, "q_out", B, n, Hq, D) if q is not None else (None, 0)
-    kp, ks = _token_rows(k_new, "k_new", B, n, Hkv, D)
-    vp, vs = _token_rows(v_new, "v_new", B, n, Hkv, D)
-    rot = 0 if rope_table is None else 2 * rope_table.shape[0]
+    dev = k_new.get_device()  # (a CPU tensor's layout is still checked first)
+    qp, qs, op, os_ = None, 0, None, 0
+    if q is not None:
+        qp, qs = _token_rows(q, dev, "q", B, n, Hq, D)
+        op, os_ = _token_rows(q_out, dev, "q_out", B, n, Hq, D)
+    kp, ks = _token_rows(k_new, dev, "k_new", B, n, Hkv, D)
+    vp, vs = _token_rows(v_new, dev, "v_new", B, n, Hkv, D)
+    _device_of(k_new)
+    kcp, vcp, ksp, vsp, tp, cp, pp, lp, rp = _ptrs(
+        dev, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, positions, new_lens,
+        rope_table)
     _check(load().spec_rope_append(
-        qp, kp, vp, op, qs, ks, vs, os_, _TORCH_DT[k_new.dtype], _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), _TORCH_DT[k_cache.dtype], _ptr(block_table), _ptr(ctx_lens),
-        _ptr(positions), _ptr(new_lens), _ptr(rope_table), rot, int(bool(interleaved)),
-        float(amplitude), B, n, Hq, Hkv, D, P, NP, block_table.shape[1], _stream(stream)))
+        qp, kp, vp, op, qs, ks, vs, os_, _TORCH_DT[src], kcp, vcp, ksp, vsp, _TORCH_DT[kind], tp,
+        cp, pp, lp, rp, 0 if rope_table is None else 2 * rope_table.shape[0], bool(interleaved),
+        float(amplitude), B, n, Hq, Hkv, D, P, NP, block_table.shape[1], _stream_on(stream, dev)))
 
 
 def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=None, k_scale=None,
@@ -483,11 +515,12 @@ def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=Non
     if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,)):
         raise ValueError("starts must be int32 [B]")
     _check_scales(k_cache, v_cache, k_scale, v_scale)
-    _same_device(k_cache, v_cache, block_table, lens, k_out, v_out, starts, k_scale, v_scale)
+    dev = _device_of(k_cache)
+    kp, vp, ksp, vsp, tp, sp, lp, kop, vop = _ptrs(
+        dev, k_cache, v_cache, k_scale, v_scale, block_table, starts, lens, k_out, v_out)
     _check(load().spec_kv_gather(
-        _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _TORCH_DT[k_cache.dtype],
-        _ptr(block_table), _ptr(starts), _ptr(lens), B, n, Hkv, D, P, NP, block_table.shape[1],
-        _TORCH_DT[k_out.dtype], _ptr(k_out), _ptr(v_out), _stream(stream)))
+        kp, vp, ksp, vsp, _TORCH_DT[k_cache.dtype], tp, sp, lp, B, n, Hkv, D, P, NP,
+        block_table.shape[1], _TORCH_DT[k_out.dtype], kop, vop, _stream_on(stream, dev)))
 
 
 def spec_codec_encode(codes, pairs, num_pairs, stream=None) -> None:
