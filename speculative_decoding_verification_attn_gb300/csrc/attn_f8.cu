@@ -1104,7 +1104,8 @@ cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cud
                           : launch_typed<2, false>(kmap, vmap, prm, num_ctas, stream))
                    : (win ? launch_typed<1, true>(kmap, vmap, prm, num_ctas, stream)
                           : launch_typed<1, false>(kmap, vmap, prm, num_ctas, stream));
-    if (e != cudaSuccess) return e;
+    // no segment is longer than a tile: none is cut
+    if (e != cudaSuccess || (int64_t)a.max_pages * a.P <= TN) return e;
     return launch_combine_stream_k(a, num_ctas, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha,
                                    prm.part_o, prm.part_lse, prm.seg_rec, prm.seg_pre, stream);
 }

@@ -956,7 +956,8 @@ cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cu
         kv8            ? launch_typed<true, false>(qmap, kmap, vmap, prm, num_ctas, stream)
         : a.window > 0 ? launch_typed<false, true>(qmap, kmap, vmap, prm, num_ctas, stream)
                        : launch_typed<false, false>(qmap, kmap, vmap, prm, num_ctas, stream);
-    if (e != cudaSuccess) return e;
+    // no segment is longer than a tile: none is cut
+    if (e != cudaSuccess || (int64_t)a.max_pages * a.P <= TN) return e;
     return launch_combine_stream_k(a, num_ctas, tc2_split_alpha(a), prm.part_o, prm.part_lse,
                                    prm.seg_rec, prm.seg_pre, stream);
 }
