@@ -110,6 +110,12 @@ constexpr float kMoveThreshold = 40.f;
 // 37.3 with a 1024-key window)
 constexpr int kSplitAlpha = 3;
 
+// Tiles' time that cutting a segment costs (whole_segments).  Whole against cut, us:
+// 8 segments of 2, 4, 6, 8, 12 tiles 7.5 / 10.9, 8.9 / 11.7, 10.3 / 12.6, 11.8 / 13.3,
+// 14.6 / 14.0; 64 segments 8.4 / 12.7, 9.8 / 14.1, 11.3 / 14.8, 12.8 / 15.5, 15.8 / 17.5;
+// 152 segments of 12 18.3 / 19.8
+constexpr int kCutTiles = 8;
+
 struct Smem {
     static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
     static constexpr int KS = Q + 4 * Q_PART;
@@ -155,6 +161,7 @@ struct F8Params {
     float* part_lse;  // [2*C][ROWS]
     int4* seg_rec;    // [C][2]
     int* seg_pre;     // [B+1]
+    int whole;        // CTA x takes segment x: none is cut
 };
 
 // warp_wait in fewer instructions.  Roles of different code share each SM's
@@ -355,7 +362,8 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (lane < 2) {
             TileSplit split;
             split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
-            const int64_t t = split.begin(blockIdx.x + lane);
+            const int64_t t = prm.whole ? segment_begin(s_pre, B, Hkv, blockIdx.x + lane)
+                                        : split.begin(blockIdx.x + lane);
             s_rng[lane] = t;
             if (lane == 0 && t < (int64_t)s_pre[B] * Hkv) s_first->init(t, s_pre, s_ctx, a);
         }
@@ -1095,6 +1103,8 @@ cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cud
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
+    prm.whole = whole_segments(a, num_ctas, TN, kCutTiles);
+    if (prm.whole) num_ctas = a.B * a.Hkv;
     const int rep = R <= 32 ? 4 : R <= 64 ? 2 : 1;
     const bool win = a.window > 0;
     const cudaError_t e =
@@ -1104,8 +1114,7 @@ cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cud
                           : launch_typed<2, false>(kmap, vmap, prm, num_ctas, stream))
                    : (win ? launch_typed<1, true>(kmap, vmap, prm, num_ctas, stream)
                           : launch_typed<1, false>(kmap, vmap, prm, num_ctas, stream));
-    // no segment is longer than a tile: none is cut
-    if (e != cudaSuccess || (int64_t)a.max_pages * a.P <= TN) return e;
+    if (e != cudaSuccess || prm.whole || max_units(a, TN) <= 1) return e;  // none is cut
     return launch_combine_stream_k(a, num_ctas, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha,
                                    prm.part_o, prm.part_lse, prm.seg_rec, prm.seg_pre, stream);
 }

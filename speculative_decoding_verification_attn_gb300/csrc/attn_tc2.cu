@@ -71,6 +71,11 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // tiles charged per segment in the split over the CTAs (a piece boundary
 // drains the pipeline: the next piece's Q, the merge of the two sets)
 constexpr int kSplitAlpha = 3;
+// Tiles' time that cutting a segment costs (whole_segments; calls with a window).
+// Whole against cut, us, windows of 128, 256, 512, 768, 1280 keys (3 .. 12 tiles): 8
+// segments 11.7 / 13.4, 12.8 / 13.8, 15.2 / 14.6, 17.5 / 15.3, 22.2 / 16.3; 64 segments
+// 12.6 / 17.7, 13.7 / 17.8, 16.6 / 19.2, 19.2 / 21.7, 24.2 / 25.0
+constexpr int kCutTiles = 5;
 
 // A / B operand formats of tcgen05.mma kind::f16: bf16 cache: bf16; INT8
 // cache widened to fp16, so q and P are fp16 there too
@@ -117,6 +122,7 @@ struct Tc2Params {
     float* part_lse;  // [2*C][ROWS]
     int4* seg_rec;    // [C][2]
     int* seg_pre;     // [B+1]
+    int whole;        // with a window: CTA x takes segment x, none is cut
 };
 
 // 64 consecutive fp32 TMEM columns of this thread's lane.
@@ -279,7 +285,8 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (lane < 2) {
             TileSplit split;
             split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
-            s_rng[lane] = split.begin(blockIdx.x + lane);
+            s_rng[lane] = WIN && prm.whole ? segment_begin(s_pre, B, Hkv, blockIdx.x + lane)
+                                           : split.begin(blockIdx.x + lane);
         }
     }
     tc_fence_before();
@@ -952,12 +959,13 @@ cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cu
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
+    prm.whole = a.window > 0 && whole_segments(a, num_ctas, TN, kCutTiles);
+    if (prm.whole) num_ctas = a.B * a.Hkv;
     const cudaError_t e =
         kv8            ? launch_typed<true, false>(qmap, kmap, vmap, prm, num_ctas, stream)
         : a.window > 0 ? launch_typed<false, true>(qmap, kmap, vmap, prm, num_ctas, stream)
                        : launch_typed<false, false>(qmap, kmap, vmap, prm, num_ctas, stream);
-    // no segment is longer than a tile: none is cut
-    if (e != cudaSuccess || (int64_t)a.max_pages * a.P <= TN) return e;
+    if (e != cudaSuccess || prm.whole || max_units(a, TN) <= 1) return e;  // none is cut
     return launch_combine_stream_k(a, num_ctas, tc2_split_alpha(a), prm.part_o, prm.part_lse,
                                    prm.seg_rec, prm.seg_pre, stream);
 }

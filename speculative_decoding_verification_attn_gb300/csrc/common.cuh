@@ -488,6 +488,13 @@ struct TileSplit {
     __device__ int cta_of_cost(int64_t x) const { return (int)(((x + 1) * C - 1) / W); }
 };
 
+// First tile of segment s in the order of the tile list (s = B * Hkv: its end).
+__device__ __forceinline__ int64_t segment_begin(const int* pre, int B, int Hkv, int s) {
+    const int b = s / Hkv;
+    if (b >= B) return (int64_t)pre[B] * Hkv;
+    return (int64_t)pre[b] * Hkv + (int64_t)(s - b * Hkv) * (pre[b + 1] - pre[b]);
+}
+
 // A 64-bit value in shared memory, read afresh at every use: the persistent
 // kernels keep their CTA range there so that it occupies no register through
 // their main loops.

@@ -131,6 +131,25 @@ cudaError_t launch_combine_stream_k(const AttnArgs& a, int num_ctas, int alpha,
 bool tc2_supported(const AttnArgs& a);
 cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);
 
+// Most units that a segment's keys can fill, by the block table and the window.
+inline int64_t max_units(const AttnArgs& a, int unit) {
+    const int64_t all = ((int64_t)a.max_pages * a.P + unit - 1) / unit;
+    if (a.window <= 0) return all;
+    const int64_t seen = ((int64_t)a.sinks + unit - 1) / unit +
+                         ((int64_t)a.window + a.k + unit - 2) / unit + 1;
+    return all < seen ? all : seen;
+}
+
+// Whether a call of short segments gives each a CTA of its own.  Cutting them
+// costs the combine launch and a piece's end, `worth` tiles' time together; not
+// cutting them leaves a segment's tiles to one CTA while the others idle, so
+// that a segment of t tiles takes t (1 - segments / CTAs) tiles' time longer.
+// Past 12 tiles unequal lengths outweigh it.
+inline bool whole_segments(const AttnArgs& a, int num_ctas, int unit, int worth) {
+    const int64_t segs = (int64_t)a.B * a.Hkv, t = max_units(a, unit);
+    return segs <= num_ctas && t <= 12 && t * (num_ctas - segs) <= (int64_t)worth * num_ctas;
+}
+
 // ---- tensor-core kernel over an e4m3 cache (codes fed to the MMAs as stored;
 // same shapes as the 128-key bf16 kernel); workspace as tc_workspace_bytes ----
 bool f8_supported(const AttnArgs& a);

@@ -156,6 +156,16 @@ def test_e4m3_forced_splits(binding, ctas):
     check_attn(binding, attn_case(5, "e4m3", torch.bfloat16, 3, 4, 16, 4, 128, 16, [900, 3, 517]))
 
 
+@pytest.mark.parametrize("ctas", [0, 1, 3, 40, 400])
+@pytest.mark.parametrize("k,Hq,Hkv", [(4, 8, 2), (8, 16, 2), (16, 28, 4)])
+def test_e4m3_cut_segments(binding, k, Hq, Hkv, ctas):
+    """Tables too long for a CTA per segment: segments cut at every place, CTAs
+    without a tile among the pieces, 16 to 112 rows."""
+    binding.spec_set_option(binding.SPEC_OPT_NUM_CTAS, ctas)
+    check_attn(binding, attn_case(6, "e4m3", torch.bfloat16, 3, k, Hq, Hkv, 128, 16,
+                                  [2100, 3, 1300]))
+
+
 def test_e4m3_scales(binding):
     """A page whose scale is zero counts as zero rows; a very large and a very
     small scale keep their rows' weight."""
@@ -280,6 +290,15 @@ def test_window_forced_splits(binding, kind, ctas):
     binding.spec_set_option(binding.SPEC_OPT_NUM_CTAS, ctas)
     check_attn(binding, attn_case(26, kind, torch.bfloat16, 4, 3, 8, 2, 128, 16,
                                   [1300, 5, 900, 260], 400, 140))
+
+
+@pytest.mark.parametrize("ctas", [0, 7, 400])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_window_cut_segments(binding, kind, ctas):
+    """As above with a window of more tiles than a CTA takes whole."""
+    binding.spec_set_option(binding.SPEC_OPT_NUM_CTAS, ctas)
+    check_attn(binding, attn_case(29, kind, torch.bfloat16, 4, 3, 8, 2, 128, 16,
+                                  [3100, 5, 2200, 260], 1600, 140))
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
