@@ -29,7 +29,8 @@
 //    the caches whose rows are independent), the token's cosines and sines in
 //    registers for all of them;
 //  * page CTAs (e4m3): two warps take one (page, kv-head) of k or of v, whose
-//    rows share a scale, half of the rows each; the CTA's warps share the
+//    rows share a scale, half of the rows each, four heads at a time and, in calls
+//    of many pages, several such groups in turn; the CTA's warps share the
 //    cosines and sines of its 16 tokens in shared memory.  Up to 16 rows stay in
 //    registers between the maximum and the codes; a longer page is read twice
 //    (the second time from L1 / L2).
@@ -44,7 +45,8 @@ constexpr int kWarps = 8;
 constexpr int kRowBlock = 16;  // tokens of a page CTA's table (at most)
 constexpr int kPageHeads = kWarps / 2;  // heads of a page CTA
 constexpr int kMaxPairs = 128;
-enum { kF32, kBf16, kI8, kPages };
+// what the row CTAs write besides q; e4m3: page CTAs of one group of heads, of many
+enum { kF32, kBf16, kI8, kPages, kPagesMany };
 
 struct RopeParams {
     RopeAppendArgs a;
@@ -54,7 +56,7 @@ struct RopeParams {
     int groups;         // row items of a token
     int64_t row_blocks; // CTAs of the row kind
     int pages;          // pages a sequence's append can touch
-    int head_groups;    // page CTAs per (sequence, page, tensor)
+    int head_parts;     // page CTAs per (sequence, page, tensor)
 };
 
 // 8 consecutive source elements as fp32
@@ -81,6 +83,10 @@ template <> struct Chunk<__nv_bfloat16> {
         o.r.w = __shfl_sync(0xffffffffu, r.w, src);
         return o;
     }
+    __device__ __forceinline__ void flip(bool neg) {  // the signs when neg
+        const uint32_t m = neg ? 0x80008000u : 0u;
+        r.x ^= m; r.y ^= m; r.z ^= m; r.w ^= m;
+    }
 };
 template <> struct Chunk<float> {
     float4 a, b;
@@ -101,6 +107,11 @@ template <> struct Chunk<float> {
         o.b.x = __shfl_sync(kAll, b.x, src); o.b.y = __shfl_sync(kAll, b.y, src);
         o.b.z = __shfl_sync(kAll, b.z, src); o.b.w = __shfl_sync(kAll, b.w, src);
         return o;
+    }
+    __device__ __forceinline__ void flip(bool neg) {
+        const float m = neg ? -1.f : 1.f;
+        a.x *= m; a.y *= m; a.z *= m; a.w *= m;
+        b.x *= m; b.y *= m; b.z *= m; b.w *= m;
     }
 };
 
@@ -199,6 +210,37 @@ __device__ __forceinline__ int new_len(const RopeAppendArgs& a, int b) {
     return max(0, min(a.n, __ldg(a.new_lens + b)));
 }
 
+// x / s for a fixed positive s, to nearest: with r = 1 / s rounded to nearest,
+// q = x r and the exact remainder x - q s, q + r (x - q s) is the correctly
+// rounded quotient (Markstein's theorem), three instructions per element where
+// a division takes three times as many.  Outside the range where no step
+// underflows the division itself.
+struct Divide {
+    float s, r;
+    bool plain;
+    __device__ __forceinline__ explicit Divide(float by) : s(by) {
+        plain = !(by > 0x1p-96f && by < 0x1p96f);
+        r = plain ? 0.f : __frcp_rn(by);
+    }
+    __device__ __forceinline__ void operator()(float (&x)[8]) const {
+        if (plain) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {  // (rotated: no dynamic index)
+                const float q = s > 0.f ? __fdiv_rn(x[0], s) : 0.f;
+#pragma unroll
+                for (int k = 0; k < 7; ++k) x[k] = x[k + 1];
+                x[7] = q;
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float q = x[e] * r;
+            x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
+        }
+    }
+};
+
 // ---------------------------------------------------------------- row CTAs
 // The rows of one kind (q, k or v) of a token's heads [h0, h1): U of a lane's
 // rows in flight, rotated, and stored `head_stride` elements apart.
@@ -244,11 +286,12 @@ __device__ __forceinline__ void token_rows(const RopeAppendArgs& a, int lr_log2,
                     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
                 const __half s16 = __float2half_rn(__fdiv_rn(amax, 127.0f));
                 const float s = __half2float(s16);
+                const Divide by(s);
+                by(x);
                 uint32_t w[2] = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float v = 0.f;
-                    if (s > 0.f) v = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -127.f), 127.f);
+                    const float v = fminf(fmaxf(rintf(x[e]), -127.f), 127.f);
                     w[e >> 2] |= (uint32_t)(uint8_t)(int8_t)v << (8 * (e & 3));
                 }
                 if (mine) {
@@ -322,44 +365,13 @@ __device__ __forceinline__ void row_cta(const RopeParams& p, int64_t block) {
 }
 
 // ---------------------------------------------------------------- page CTAs (e4m3)
-// x / s for a fixed positive s, to nearest: with r = 1 / s rounded to nearest,
-// q = x r and the exact remainder x - q s, q + r (x - q s) is the correctly
-// rounded quotient (Markstein's theorem), three instructions per element where
-// a division takes three times as many.  Outside the range where no step
-// underflows the division itself.
-struct Divide {
-    float s, r;
-    bool plain;
-    __device__ __forceinline__ explicit Divide(float by) : s(by) {
-        plain = !(by > 0x1p-96f && by < 0x1p96f);
-        r = plain ? 0.f : __frcp_rn(by);
-    }
-    __device__ __forceinline__ void operator()(float (&x)[8]) const {
-        if (plain) {
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e) {  // (rotated: no dynamic index)
-                const float q = s > 0.f ? __fdiv_rn(x[0], s) : 0.f;
-#pragma unroll
-                for (int k = 0; k < 7; ++k) x[k] = x[k + 1];
-                x[7] = q;
-            }
-            return;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float q = x[e] * r;
-            x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
-        }
-    }
-};
-
-template <typename T, bool INTER>
+template <typename T, bool INTER, bool MANY>
 __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMaxPairs],
-                                         float* s_max, int64_t item) {
+                                         float (*s_max)[kWarps], int64_t item) {
     const RopeAppendArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int hg = (int)(item % p.head_groups);
-    item /= p.head_groups;
+    const int part0 = (int)(item % p.head_parts);
+    item /= p.head_parts;
     const bool is_v = item & 1;
     item >>= 1;
     const int pg = (int)(item % p.pages), b = (int)(item / p.pages);
@@ -367,8 +379,8 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
     const int count = new_len(a, b);
     const bool spin = !is_v && a.rot > 0;
     const int pairs = a.rot / 2;
-    // this thread's frequency of every row of the table when the pairs divide
-    // the CTA (loaded beside the context length, not after it)
+    // When the pairs divide the CTA a thread computes one pair of every few rows
+    // (its frequency loaded beside the context length, not after it).
     const bool even = spin && (kWarps * 32) % pairs == 0;
     const uint64_t freq = even ? __ldg(a.table + threadIdx.x % pairs) : 0;
     if (ctx < 0) {
@@ -381,17 +393,17 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
     const int last = (int)min((int64_t)a.P, ctx + count - page_start);
     if (first >= last) return;
     const int t0 = (int)(page_start + first - ctx), nr = last - first;
-    // two warps per head, each half of the rows of a block
-    const int g = hg * kPageHeads + (warp >> 1), part = warp & 1;
+    // two warps per head, each half of the rows of a block; the CTA's heads in
+    // groups of kPageHeads, every head_parts-th its own
+    const int pair = warp >> 1, part = warp & 1;
     const int lr = 1 << p.lr_log2, rows = 32 >> p.lr_log2;
     const int e0 = (lane & (lr - 1)) * 8, sub = lane >> p.lr_log2;
-    const bool in_row = e0 < a.D, active = g < a.Hkv && in_row;
+    const bool in_row = e0 < a.D;
     const int j0 = in_row ? first_pair<INTER>(a, e0) : -1;
     const int from = in_row ? partner_lane(a, lane, e0) : lane;
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
-    const T* src = static_cast<const T*>(is_v ? a.v_new : a.k_new) +
-                   ((int64_t)b * a.n + t0) * stride + (int64_t)g * a.D + e0;
-    const float sign = e0 < a.rot / 2 ? -1.f : 1.f;    // of the sine (halves)
+    const T* src0 = static_cast<const T*>(is_v ? a.v_new : a.k_new) +
+                    ((int64_t)b * a.n + t0) * stride + e0;
     constexpr int N = INTER ? 4 : 8;                   // pairs of a lane's 8 elements
     constexpr int U = 4;                               // rows in flight per lane
     const int half = min(kRowBlock / 2, U * rows);     // rows of a block per warp
@@ -403,27 +415,38 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
     };
     Chunk<T> c[U];
     float x[U][8];
-    auto load_rows = [&](int base) {
+    auto load_rows = [&](int g, int base) {
+        const T* src = src0 + (int64_t)g * a.D;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = row_of(base, u);
             c[u].zero();
-            if (r >= 0 && active) c[u].load(src + (base + r) * stride);
+            if (r >= 0 && in_row && g < a.Hkv) c[u].load(src + (base + r) * stride);
         }
     };
+    // The table of a block: pair j of a row in the order that its readers take,
+    // two pairs of a lane side by side (j / N of the lanes, j % N in it).
+    auto slot_of = [&](int j) {
+        const int e = j % N;
+        return ((e >> 1) * (pairs / N) + j / N) * 2 + (e & 1);
+    };
+    auto put_angle = [&](int base, int r, int j, uint64_t f) {
+        const int64_t at = a.positions
+                               ? (int64_t)__ldg(a.positions + (int64_t)b * a.n + t0 + base + r)
+                               : page_start + first + base + r;
+        tab[r][slot_of(j)] = turn(at, f, a.amplitude);
+    };
     auto fill_table = [&](int base) {
+        if (!spin) return;
         __syncthreads();  // the table's readers are done
-        if (spin)
-            for (int e = threadIdx.x; e < min(rb, nr - base) * pairs; e += kWarps * 32) {
-                const int r = base + e / pairs;
-                const int64_t at = a.positions
-                                       ? (int64_t)__ldg(a.positions + (int64_t)b * a.n + t0 + r)
-                                       : page_start + first + r;
-                const int j = e % pairs;
-                // pair j beside the pairs that its warp's lanes read with it
-                tab[e / pairs][(j % N) * (pairs / N) + j / N] =
-                    turn(at, even ? freq : __ldg(a.table + j), a.amplitude);
-            }
+        const int n = min(rb, nr - base);
+        if (even) {
+            const int j = threadIdx.x % pairs, step = kWarps * 32 / pairs;
+            for (int r = threadIdx.x / pairs; r < n; r += step) put_angle(base, r, j, freq);
+        } else {
+            for (int e = threadIdx.x; e < n * pairs; e += kWarps * 32)
+                put_angle(base, e / pairs, e % pairs, __ldg(a.table + e % pairs));
+        }
         __syncthreads();
     };
     auto rotate_rows = [&](int base) {
@@ -433,94 +456,135 @@ __device__ __forceinline__ void page_cta(const RopeParams& p, float2 (*tab)[kMax
             if (!spin) continue;
             float o[8];
             float2 cs[N];
-            if constexpr (!INTER) c[u].from_lane(from).get(o);
+            if constexpr (!INTER) {
+                Chunk<T> other = c[u].from_lane(from);
+                other.flip(e0 < a.rot / 2);  // x cos - y sin in the lower half
+                other.get(o);
+            }
             const int r = row_of(base, u);
             if (j0 >= 0 && r >= 0) {
+                const float4* row = reinterpret_cast<const float4*>(tab[r]) + j0 / N;
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    cs[e] = tab[r][e * (pairs / N) + j0 / N];
-                    if (!INTER) cs[e].y *= sign;
+                for (int e = 0; e < N; e += 2) {
+                    const float4 two = row[(e >> 1) * (pairs / N)];
+                    cs[e] = make_float2(two.x, two.y);
+                    cs[e + 1] = make_float2(two.z, two.w);
                 }
                 rotate8<INTER>(a, e0, x[u], o, cs);
             }
         }
     };
-    // the first rows are on their way while the page is looked up, the page's
-    // scale while they are rotated
-    load_rows(0);
-    const int page = find_page(a, b, page_start, threadIdx.x == 0);
-    if (page < 0) return;
-    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
-                     ((int64_t)page * a.Hkv + g) * a.P * a.D + e0;
-    float* scale = static_cast<float*>(is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.Hkv + g;
-    const float old = g < a.Hkv && first > 0 ? *scale : 0.f;
-    float amax = 0.f;
-    for (int base = 0; base < nr; base += rb) {
-        if (base > 0) load_rows(base);
-        fill_table(base);
-        rotate_rows(base);
+    auto largest = [&](float amax) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[u][e]));  // (no row: zeros)
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    if (lane == 0) s_max[warp] = amax;
-    __syncthreads();  // (both warps have read the old scale, too)
-    float s = __fdiv_rn(fmaxf(amax, s_max[warp ^ 1]), 448.0f);
-    if (first > 0 && old >= s) s = old;
-    const Divide by(s);
-    if (g < a.Hkv && part == 0 && lane == 0) *scale = s;
-    if (first > 0 && s > old) {
-        // the kept rows' codes in the new scale
-        for (int r = part * rows + sub; r < first; r += 2 * rows) {
-            if (!active) continue;
-            uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)r * a.D);
-            float v[8];
-            e4m3x8_to_f32(*at, v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], old);
-            by(v);
-            *at = e4m3x8(v);
+        return amax;
+    };
+    // the first rows are on their way while the page is looked up, its scale while
+    // the angles are computed
+    int g = part0 * kPageHeads + pair;
+    load_rows(g, 0);
+    const int page = find_page(a, b, page_start, threadIdx.x == 0);
+    if (page < 0) return;
+    float* scales = static_cast<float*>(is_v ? a.v_scale : a.k_scale) + (int64_t)page * a.Hkv;
+    float old = g < a.Hkv && first > 0 ? scales[g] : 0.f;
+    fill_table(0);
+    const bool one_block = nr <= rb;
+#pragma unroll 1
+    for (int it = 0;; ++it) {
+        const int next = g + p.head_parts * kPageHeads;
+        const bool active = g < a.Hkv && in_row;
+        uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) +
+                         ((int64_t)page * a.Hkv + g) * a.P * a.D + e0;
+        float amax = 0.f;
+        if (one_block) {
+            // the rows stay in registers (the next group's are loaded after them: read
+            // ahead they spill, 78 -> 84 us on 16.4K prompt tokens)
+            rotate_rows(0);
+            amax = largest(0.f);
+        } else {
+#pragma unroll 1
+            for (int base = 0; base < nr; base += rb) {
+                load_rows(g, base);
+                fill_table(base);
+                rotate_rows(base);
+                amax = largest(amax);
+            }
         }
-    }
-    for (int base = 0; base < nr; base += rb) {
-        if (nr > rb) {  // more rows than the registers held
-            load_rows(base);
-            fill_table(base);
-            rotate_rows(base);
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = row_of(base, u);
-            if (r < 0 || !active) continue;
-            by(x[u]);
-            *reinterpret_cast<uint2*>(codes + (int64_t)(first + base + r) * a.D) = e4m3x8(x[u]);
+        for (int off = 16; off > 0; off >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        float* mx = s_max[it & 1];
+        if (lane == 0) mx[warp] = amax;
+        named_bar_sync(1 + pair, 64);  // (both warps have read the old scale, too)
+        float s = __fdiv_rn(fmaxf(amax, mx[warp ^ 1]), 448.0f);
+        if (first > 0 && old >= s) s = old;
+        const Divide by(s);
+        if (g < a.Hkv && part == 0 && lane == 0) scales[g] = s;
+        if (first > 0 && s > old) {
+            // the kept rows' codes in the new scale
+            for (int r = part * rows + sub; r < first; r += 2 * rows) {
+                if (!active) continue;
+                uint2* at = reinterpret_cast<uint2*>(codes + (int64_t)r * a.D);
+                float v[8];
+                e4m3x8_to_f32(*at, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], old);
+                by(v);
+                *at = e4m3x8(v);
+            }
         }
+#pragma unroll 1
+        for (int base = 0; base < nr; base += rb) {
+            if (!one_block) {  // more rows than the registers held
+                load_rows(g, base);
+                fill_table(base);
+                rotate_rows(base);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int r = row_of(base, u);
+                if (r < 0 || !active) continue;
+                by(x[u]);
+                *reinterpret_cast<uint2*>(codes + (int64_t)(first + base + r) * a.D) =
+                    e4m3x8(x[u]);
+            }
+        }
+        if (!MANY || next - pair >= a.Hkv) break;  // (next - pair: the CTA's group)
+        g = next;
+        load_rows(g, 0);
+        old = g < a.Hkv && first > 0 ? scales[g] : 0.f;
     }
 }
 
-// MODE: what the row CTAs write besides q (f32, bf16 or i8 cache rows), or the
-// page CTAs of an e4m3 cache beside them.  Measured: 12.3K prompt tokens of 32 + 8
-// heads into bf16 53.8 us (0.86 of the copy rate), 16.4K into e4m3 91 us (0.60: the
-// page CTAs' arithmetic and barriers), 32 x 4 drafts into e4m3 5.3 us.
+// CTAs per SM.  Row kernels whose registers allow a fourth gain by it (12.3K prompt
+// tokens in pairs side by side 53.8 -> 52.0 us, 16.4K in halves into i8 82.5 -> 78.5);
+// halves into bf16 spill (71.7 -> 74.3).
+template <typename T, bool INTER, int MODE> constexpr int resident() {
+    return sizeof(T) == 2 && MODE < kPages && (INTER || MODE == kI8) ? 4 : 3;
+}
+
+// Measured: 12.3K prompt tokens of 32 + 8 heads into bf16 52.0 us (0.89 of the copy
+// rate), 16.4K into e4m3 78 us (0.70:
+// the page CTAs' arithmetic; 89 with a CTA, and its own angles, per group of
+// heads), 32 x 4 drafts into e4m3 4.9 us.
 template <typename T, bool INTER, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, 3) rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, (resident<T, INTER, MODE>()))
+rope_append_kernel(const RopeParams p) {
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if constexpr (MODE != kPages) {
+    if constexpr (MODE < kPages) {
         row_cta<T, INTER, MODE>(p, blockIdx.x);
     } else {
         // the page CTAs, whose chain of loads is longer, start first
         const int64_t pages = gridDim.x - p.row_blocks;
         if (blockIdx.x >= pages) {
-            row_cta<T, INTER, MODE>(p, blockIdx.x - pages);
+            row_cta<T, INTER, kPages>(p, blockIdx.x - pages);
         } else {
-            __shared__ float2 tab[kRowBlock][kMaxPairs];
-            __shared__ float s_max[kWarps];
-            page_cta<T, INTER>(p, tab, s_max, blockIdx.x);
+            __shared__ __align__(16) float2 tab[kRowBlock][kMaxPairs];
+            __shared__ float s_max[2][kWarps];
+            page_cta<T, INTER, MODE == kPagesMany>(p, tab, s_max, blockIdx.x);
         }
     }
 }
@@ -534,7 +598,9 @@ cudaError_t launch_typed(const RopeParams& p, unsigned blocks, cudaStream_t stre
     case SPEC_DTYPE_F32: return go(rope_append_kernel<T, INTER, kF32>);
     case SPEC_DTYPE_BF16: return go(rope_append_kernel<T, INTER, kBf16>);
     case SPEC_DTYPE_I8: return go(rope_append_kernel<T, INTER, kI8>);
-    case SPEC_DTYPE_E4M3: return go(rope_append_kernel<T, INTER, kPages>);
+    case SPEC_DTYPE_E4M3:
+        return p.head_parts * kPageHeads < p.a.Hkv ? go(rope_append_kernel<T, INTER, kPagesMany>)
+                                                   : go(rope_append_kernel<T, INTER, kPages>);
     default: return cudaErrorInvalidValue;
     }
 }
@@ -560,8 +626,13 @@ cudaError_t launch_rope_append(const RopeAppendArgs& a, int num_sms, cudaStream_
     p.groups = p.heads > 0 ? (p.heads + p.heads_per_warp - 1) / p.heads_per_warp : 0;
     p.row_blocks = (tokens * p.groups + kWarps - 1) / kWarps;
     p.pages = paged ? (int)(((int64_t)a.n + a.P - 2) / a.P + 1) : 0;
-    p.head_groups = (a.Hkv + kPageHeads - 1) / kPageHeads;
-    const int64_t blocks = p.row_blocks + (int64_t)a.B * p.pages * 2 * p.head_groups;
+    // page CTAs take several groups of heads (the angles are theirs in common)
+    // while that leaves enough of them to fill the SMs a few times
+    p.head_parts = (a.Hkv + kPageHeads - 1) / kPageHeads;
+    const int64_t page_ctas = (int64_t)a.B * p.pages * 2;
+    while (p.head_parts > 1 && page_ctas * ((p.head_parts + 1) / 2) >= (int64_t)num_sms * 12)
+        p.head_parts = (p.head_parts + 1) / 2;
+    const int64_t blocks = p.row_blocks + page_ctas * p.head_parts;
     if (blocks == 0) return cudaSuccess;
     if (blocks >= (1LL << 31)) return cudaErrorInvalidConfiguration;
     const unsigned n = (unsigned)blocks;

@@ -487,6 +487,40 @@ def test_rope_append_padded_batch(binding, kind):
     check_rope(binding, c, kind, 128, True)
 
 
+@pytest.mark.parametrize("P,n,inter,src", [
+    (16, 1024, False, torch.bfloat16), (16, 1024, True, torch.float32),
+    (64, 4096, False, torch.float32), (64, 4096, True, torch.bfloat16)])
+def test_rope_append_many_pages(binding, P, n, inter, src):
+    """A call of so many pages that a block takes several groups of heads writes
+    what one call per sequence writes, bit for bit (partly filled pages, ragged
+    lengths, a last group of its own)."""
+    B, Hq, Hkv, D, rot = 8, 2, 12, 32, 32
+    gen = torch.Generator(device="cuda").manual_seed(P)
+    q, k, v = (torch.randn(B, n, H, D, device="cuda", generator=gen).to(src)
+               for H in (Hq, Hkv, Hkv))
+    k *= torch.rand(B, n, 1, 1, device="cuda", generator=gen).add(0.1).to(src)
+    mp = (n + 2 * P - 1) // P + 1
+    table = torch.randperm(B * mp, device="cuda", generator=gen).int().view(B, mp)
+    ctx = torch.tensor([0, 1, P - 1, 5, P, 7, 3, 2], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n, n - 1, n // 2, 0, 1, n, n - 17, 33], dtype=torch.int32, device="cuda")
+    kc, vc = (torch.randint(0, 0x78, (B * mp, Hkv, P, D), device="cuda", generator=gen)
+              .to(torch.uint8).view(paged8.E4M3) for _ in range(2))
+    ks, vs = (torch.rand(B * mp, Hkv, device="cuda", generator=gen) * 0.02 for _ in range(2))
+    rope, amp = binding.spec_rope_table(rot)
+    one = [t.clone() for t in (kc, vc, ks, vs)]
+    qo, qone = torch.zeros_like(q), torch.zeros_like(q)
+    binding.spec_rope_append(q, k, v, qo, kc, vc, table, ctx, rope, inter, amp, new_lens=lens,
+                             k_scale=ks, v_scale=vs)
+    for b in range(B):
+        s = slice(b, b + 1)
+        binding.spec_rope_append(q[s], k[s], v[s], qone[s], one[0], one[1], table[s], ctx[s], rope,
+                                 inter, amp, new_lens=lens[s], k_scale=one[2], v_scale=one[3])
+    assert torch.equal(qo, qone)
+    for got, want in zip((kc, vc), one[:2]):
+        assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    assert torch.equal(ks, one[2]) and torch.equal(vs, one[3])
+
+
 def test_rope_append_in_place(binding):
     c = rope_case(36, "e4m3", torch.bfloat16, 2, 6, 8, 2, 128, 16, [9, 64])
     check_rope(binding, c, "e4m3", 128, False, in_place=True)
