@@ -304,7 +304,7 @@ __device__ __forceinline__ void token_rows(const RopeAppendArgs& a, int lr_log2,
 }
 
 template <typename T, bool INTER, int MODE>
-__device__ __forceinline__ void row_cta(const RopeParams& p, int64_t block) {
+__device__ __forceinline__ void row_cta(const RopeParams& p, float2* turns, int64_t block) {
     const RopeAppendArgs& a = p.a;
     const int lane = threadIdx.x & 31;
     const int64_t item = block * kWarps + (threadIdx.x >> 5);
@@ -324,12 +324,28 @@ __device__ __forceinline__ void row_cta(const RopeParams& p, int64_t block) {
     float2 cs[N];
     const int j0 = e0 < a.D ? first_pair<INTER>(a, e0) : -1;
     const bool spin = a.rot > 0 && h_begin < a.Hq + a.Hkv;
-    if (spin && j0 >= 0) {
+    if (spin) {
         const int64_t at = a.positions ? (int64_t)__ldg(a.positions + token) : pos;
+        if constexpr (INTER) {
+            if (j0 >= 0)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            cs[e] = turn(at, __ldg(a.table + j0 + e), a.amplitude);
-            if (!INTER && e0 < a.rot / 2) cs[e].y = -cs[e].y;
+                for (int e = 0; e < N; ++e) cs[e] = turn(at, __ldg(a.table + j0 + e), a.amplitude);
+        } else {
+            // the warp computes each angle once and shares it: a lane needs eight, the
+            // same ones as the lane of the other half (32 x 64 tokens 16.0 -> 14.7 us;
+            // pairs side by side take four, and lost by it: 52.0 -> 53.4 on prompts)
+            turns += (threadIdx.x >> 5) * kMaxPairs;
+            for (int j = lane; j < a.rot / 2; j += 32)
+                turns[j] = turn(at, __ldg(a.table + j), a.amplitude);
+            __syncwarp();
+            if (j0 >= 0)
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    const float4 two = *reinterpret_cast<const float4*>(turns + j0 + e);
+                    const float sign = e0 < a.rot / 2 ? -1.f : 1.f;
+                    cs[e] = make_float2(two.x, two.y * sign);
+                    cs[e + 1] = make_float2(two.z, two.w * sign);
+                }
         }
     }
     if (h_begin < a.Hq)
@@ -566,23 +582,24 @@ template <typename T, bool INTER, int MODE> constexpr int resident() {
 }
 
 // Measured: 12.3K prompt tokens of 32 + 8 heads into bf16 52.0 us (0.89 of the copy
-// rate), 16.4K into e4m3 78 us (0.70:
+// rate), 16.4K into e4m3 76 us (0.72:
 // the page CTAs' arithmetic; 89 with a CTA, and its own angles, per group of
-// heads), 32 x 4 drafts into e4m3 4.9 us.
+// heads), 32 x 4 drafts into e4m3 4.8 us.
 template <typename T, bool INTER, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, (resident<T, INTER, MODE>()))
 rope_append_kernel(const RopeParams p) {
     grid_dep_launch_dependents();
     grid_dep_wait();
+    // of a page CTA's rows, or of each warp's token
+    __shared__ __align__(16) float2 tab[MODE < kPages ? kWarps : kRowBlock][kMaxPairs];
     if constexpr (MODE < kPages) {
-        row_cta<T, INTER, MODE>(p, blockIdx.x);
+        row_cta<T, INTER, MODE>(p, tab[0], blockIdx.x);
     } else {
         // the page CTAs, whose chain of loads is longer, start first
         const int64_t pages = gridDim.x - p.row_blocks;
         if (blockIdx.x >= pages) {
-            row_cta<T, INTER, kPages>(p, blockIdx.x - pages);
+            row_cta<T, INTER, kPages>(p, tab[0], blockIdx.x - pages);
         } else {
-            __shared__ __align__(16) float2 tab[kRowBlock][kMaxPairs];
             __shared__ float s_max[2][kWarps];
             page_cta<T, INTER, MODE == kPagesMany>(p, tab, s_max, blockIdx.x);
         }
