@@ -41,7 +41,9 @@
 //  * A sliding window (WIN) takes the tiles of the sinks and of the keys from
 //    the first query's window on; inside them, page chunks that no query sees
 //    are not copied and their V rows are zeroed (the P V of a masked key adds
-//    0 * V).
+//    0 * V).  2048 keys and 4 sinks of 32 sequences of 1 to 8K keys, 32/8 heads, 4
+//    drafts: 66 us (3.97 TB/s), against 102 without a window (5.9 TB/s over all
+//    keys): 2.7 pieces per CTA of ~18 tiles each, whose ends the tiles do not hide.
 //  * Every mbarrier wait is bounded (1 s); a timeout sets the device error
 //    word and an abort flag, after which every role skips its remaining work
 //    (the softmax sets still pass their pairwise barriers), drains its copies
