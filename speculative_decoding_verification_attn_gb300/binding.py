@@ -152,12 +152,13 @@ def _ptr(t: Optional[torch.Tensor]):
 # The current stream's handle without building a Stream object (0.1 us against
 # 2.9 of a call that takes 4 to 9 in the library).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_get_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -174,29 +175,30 @@ def spec_set_option(option: int, value: int) -> None:
     _check(load().spec_set_option(option, int(value)))
 
 
+_E4M3, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+
+
 def _check_page_scales(k_cache, v_cache, k_scale, v_scale) -> None:
     """The scales of a float8_e4m3fn cache: float32 [num_pages, Hkv] each (the
     library takes a bare pointer and cannot tell)."""
-    if k_cache.dtype != torch.float8_e4m3fn:
+    if k_cache.dtype is not _E4M3:
         return
-    if v_cache.dtype != torch.float8_e4m3fn:
-        raise ValueError("k_cache and v_cache must share a dtype")
-    want = k_cache.shape[:2]
-    if (k_scale is not None and (k_scale.dtype != torch.float32 or k_scale.shape != want)
-            or v_scale is not None and (v_scale.dtype != torch.float32 or v_scale.shape != want)):
+    pool = k_cache.shape
+    if v_cache.dtype is not _E4M3 or v_cache.shape != pool:
+        raise ValueError("k_cache and v_cache must share a dtype and a shape")
+    want = (pool[0], pool[1])
+    if (k_scale is not None and (k_scale.dtype is not _F32 or k_scale.shape != want)
+            or v_scale is not None and (v_scale.dtype is not _F32 or v_scale.shape != want)):
         raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
 
 
 def _check_scales(k_cache, v_cache, k_scale, v_scale) -> None:
     """_check_page_scales, and an int8 cache's scales: float16 [num_pages, Hkv, P]."""
-    if k_cache.dtype != torch.int8:
+    if k_cache.dtype is not torch.int8:
         return _check_page_scales(k_cache, v_cache, k_scale, v_scale)
     for s in (k_scale, v_scale):
-        if s is not None and (s.dtype != torch.float16 or s.shape != k_cache.shape[:3]):
+        if s is not None and (s.dtype is not torch.float16 or s.shape != k_cache.shape[:3]):
             raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
-
-
-_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device_of(first) -> int:
@@ -210,17 +212,10 @@ def _device_of(first) -> int:
 def _ptrs(dev: int, *tensors):
     """Pointers of dense tensors of device ``dev`` (None stays None), in one
     pass: a call's checks cost the host as much as its launch."""
-    out = []
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if t.get_device() != dev:
-            raise ValueError("tensors must lie on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-        out.append(t.data_ptr())
-    return out
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous and lie on the current CUDA device")
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _stream_on(stream, dev: int) -> int:
@@ -243,12 +238,16 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
     NP, Hkv, P, D2 = k_cache.shape
     if k != num_draft or D2 != D:
         raise ValueError("shape mismatch between q, num_draft and the cache")
-    if block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32:
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
         raise ValueError("block_table and ctx_lens must be int32")
+    tensors = (q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse)
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    qp, kp, vp, ksp, vsp, tp, cp, op, lp = [None if t is None else t.data_ptr() for t in tensors]
     _check(load().spec_verify_attn(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-        _ptr(ctx_lens), B, k, Hq, Hkv, D, P, NP, block_table.shape[1], _TORCH_DT[q.dtype],
-        _TORCH_DT[k_cache.dtype], float(scale), _ptr(out), _ptr(lse), _stream(stream)))
+        qp, kp, vp, ksp, vsp, tp, cp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
+        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
 
 
 def _ref(d):
@@ -306,11 +305,11 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draf
         raise ValueError("shape mismatch between q, num_draft and the caches")
     if v_cache.dtype != k_cache.dtype or out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("v_cache must have k_cache's dtype, out q's dtype and shape")
-    if block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32:
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
         raise ValueError("block_table and ctx_lens must be int32")
     if block_table.shape[0] != B or ctx_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_pages] and ctx_lens [B]")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, k, Hq)):
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, k, Hq)):
         raise ValueError("lse must be float32 [B, k, Hq]")
     if tree_mask is not None and (tree_mask.shape != (B, k) or tree_mask.element_size() != 8):
         raise ValueError("tree_mask must hold 64-bit words [B, num_draft]")
@@ -470,13 +469,13 @@ def spec_rope_append(q, k_new, v_new, q_out, k_cache, v_cache, block_table, ctx_
             raise ValueError("q, q_out, k_new and v_new must share a dtype")
     if v_new.dtype != src or v_cache.dtype != kind:
         raise ValueError("k and v must share a dtype")
-    if (block_table.dtype != torch.int32 or ctx_lens.dtype != torch.int32
+    if (block_table.dtype is not _I32 or ctx_lens.dtype is not _I32
             or block_table.shape[0] != B or ctx_lens.shape != (B,)):
         raise ValueError("block_table must be int32 [B, max_pages] and ctx_lens int32 [B]")
-    if positions is not None and (positions.dtype != torch.int32
+    if positions is not None and (positions.dtype is not _I32
                                   or positions.shape != (B, n)):
         raise ValueError("positions must be int32 [B, n]")
-    if new_lens is not None and (new_lens.dtype != torch.int32 or new_lens.shape != (B,)):
+    if new_lens is not None and (new_lens.dtype is not _I32 or new_lens.shape != (B,)):
         raise ValueError("new_lens must be int32 [B]")
     if rope_table is not None and (rope_table.element_size() != 8 or rope_table.dim() != 1):
         raise ValueError("rope_table must be a row of 64-bit words")
@@ -509,10 +508,10 @@ def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=Non
         raise ValueError("k_out / v_out must be [B, max_len, Hkv, D] matching the caches")
     if v_out.dtype != k_out.dtype or v_cache.dtype != k_cache.dtype:
         raise ValueError("k and v must share a dtype")
-    if (block_table.dtype != torch.int32 or lens.dtype != torch.int32
+    if (block_table.dtype is not _I32 or lens.dtype is not _I32
             or block_table.shape[0] != B or lens.shape != (B,)):
         raise ValueError("block_table must be int32 [B, max_pages] and lens int32 [B]")
-    if starts is not None and (starts.dtype != torch.int32 or starts.shape != (B,)):
+    if starts is not None and (starts.dtype is not _I32 or starts.shape != (B,)):
         raise ValueError("starts must be int32 [B]")
     _check_scales(k_cache, v_cache, k_scale, v_scale)
     dev = _device_of(k_cache)
