@@ -33,6 +33,10 @@
 //    max only moves when it grows by more than 2^8, so O is rarely rescaled
 //    (exact in real arithmetic: O and l share the reference max), and a tile's
 //    P is released without waiting for the previous tile's P V.
+//  * A sliding window (WIN, INT8 cache) takes only the tiles that some query
+//    sees, copies the boxes inside them that hold such keys, and gives the other
+//    keys the scale 0 (32 x 8K keys, 64/8 heads, 8 drafts: 316 us, 130 with a
+//    window of 2048).
 //  * Every mbarrier wait is bounded (1 s); a timeout sets the device error
 //    word and an abort flag after which every role skips its remaining work
 //    (still passing every CTA barrier) and returns.
