@@ -115,6 +115,11 @@ constexpr int kSplitAlpha = 3;
 // 14.6 / 14.0; 64 segments 8.4 / 12.7, 9.8 / 14.1, 11.3 / 14.8, 12.8 / 15.5, 15.8 / 17.5;
 // 152 segments of 12 18.3 / 19.8
 constexpr int kCutTiles = 8;
+// With more segments than CTAs, ranges that end with segments against cut ones, us:
+// 192 segments of 3, 4, 6, 10 tiles 16.1 / 17.5, 17.8 / 18.3, 21.1 / 21.1, 27.2 / 25.3; 512
+// of 3, 6, 7, 10 25.7 / 27.9, 35.3 / 36.8, 39.4 / 40.1, 47.8 / 46.9; 1280 of 4, 7, 11, 15,
+// 19 56.2 / 60.4, 75.8 / 83.3, 103.5 / 109.3, 126.5 / 127.8, 160.5 / 157.2
+constexpr int kRoundedBase = 3, kRoundedMore = 5;
 
 struct Smem {
     static constexpr int Q = 0;                          // 2 buffers of [hi | lo]
@@ -161,7 +166,7 @@ struct F8Params {
     float* part_lse;  // [2*C][ROWS]
     int4* seg_rec;    // [C][2]
     int* seg_pre;     // [B+1]
-    int whole;        // CTA x takes segment x: none is cut
+    int whole;        // whole_segments: kCut, or how none is cut
 };
 
 // warp_wait in fewer instructions.  Roles of different code share each SM's
@@ -362,8 +367,10 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         if (lane < 2) {
             TileSplit split;
             split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
-            const int64_t t = prm.whole ? segment_begin(s_pre, B, Hkv, blockIdx.x + lane)
-                                        : split.begin(blockIdx.x + lane);
+            const int c = blockIdx.x + lane;
+            const int64_t t = prm.whole
+                                  ? whole_begin<Cursor>(prm.whole, split, s_pre, s_ctx, a, c)
+                                  : split.begin(c);
             s_rng[lane] = t;
             if (lane == 0 && t < (int64_t)s_pre[B] * Hkv) s_first->init(t, s_pre, s_ctx, a);
         }
@@ -1103,8 +1110,8 @@ cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cud
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
-    prm.whole = whole_segments(a, num_ctas, TN, kCutTiles);
-    if (prm.whole) num_ctas = a.B * a.Hkv;
+    prm.whole = whole_segments(a, num_ctas, TN, kCutTiles, kRoundedBase, kRoundedMore);
+    if (prm.whole == kOwnCta) num_ctas = a.B * a.Hkv;
     const int rep = R <= 32 ? 4 : R <= 64 ? 2 : 1;
     const bool win = a.window > 0;
     const cudaError_t e =

@@ -78,6 +78,11 @@ constexpr int kSplitAlpha = 3;
 // segments 11.7 / 13.4, 12.8 / 13.8, 15.2 / 14.6, 17.5 / 15.3, 22.2 / 16.3; 64 segments
 // 12.6 / 17.7, 13.7 / 17.8, 16.6 / 19.2, 19.2 / 21.7, 24.2 / 25.0
 constexpr int kCutTiles = 5;
+// With more segments than CTAs, ranges that end with segments against cut ones, us:
+// 192 segments of 3, 4, 6, 10 tiles 22.7 / 24.0, 24.8 / 26.5, 30.0 / 31.7, 41.4 / 39.9; 768
+// of 6, 9, 15, 19 72.2 / 82.7, 91.7 / 104.9, 143.6 / 145.3, 177.9 / 171.1; 1280 of 6, 9, 15,
+// 19 107.1 / 131.3, 139.8 / 168.4, 218.7 / 236.2, 272.1 / 278.2
+constexpr int kRoundedBase = 4, kRoundedMore = 9;
 
 // A / B operand formats of tcgen05.mma kind::f16: bf16 cache: bf16; INT8
 // cache widened to fp16, so q and P are fp16 there too
@@ -124,7 +129,7 @@ struct Tc2Params {
     float* part_lse;  // [2*C][ROWS]
     int4* seg_rec;    // [C][2]
     int* seg_pre;     // [B+1]
-    int whole;        // with a window: CTA x takes segment x, none is cut
+    int whole;        // with a window, whole_segments: kCut, or how none is cut
 };
 
 // 64 consecutive fp32 TMEM columns of this thread's lane.
@@ -287,8 +292,10 @@ attn_tc2_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant_
         if (lane < 2) {
             TileSplit split;
             split.init(s_pre, B, Hkv, a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha, gridDim.x);
-            s_rng[lane] = WIN && prm.whole ? segment_begin(s_pre, B, Hkv, blockIdx.x + lane)
-                                           : split.begin(blockIdx.x + lane);
+            const int c = blockIdx.x + lane;
+            s_rng[lane] = WIN && prm.whole
+                              ? whole_begin<Cursor>(prm.whole, split, s_pre, s_ctx, a, c)
+                              : split.begin(c);
         }
     }
     tc_fence_before();
@@ -961,8 +968,10 @@ cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cu
     prm.part_lse = prm.part_o + (size_t)2 * num_ctas * ROWS * D;
     prm.seg_rec = reinterpret_cast<int4*>(prm.part_lse + (size_t)2 * num_ctas * ROWS);
     prm.seg_pre = reinterpret_cast<int*>(prm.seg_rec + 2 * (size_t)num_ctas);
-    prm.whole = a.window > 0 && whole_segments(a, num_ctas, TN, kCutTiles);
-    if (prm.whole) num_ctas = a.B * a.Hkv;
+    prm.whole = kCut;
+    if (a.window > 0)
+        prm.whole = whole_segments(a, num_ctas, TN, kCutTiles, kRoundedBase, kRoundedMore);
+    if (prm.whole == kOwnCta) num_ctas = a.B * a.Hkv;
     const cudaError_t e =
         kv8            ? launch_typed<true, false>(qmap, kmap, vmap, prm, num_ctas, stream)
         : a.window > 0 ? launch_typed<false, true>(qmap, kmap, vmap, prm, num_ctas, stream)

@@ -495,6 +495,18 @@ __device__ __forceinline__ int64_t segment_begin(const int* pre, int B, int Hkv,
     return (int64_t)pre[b] * Hkv + (int64_t)(s - b * Hkv) * (pre[b + 1] - pre[b]);
 }
 
+// First tile of CTA c's range when no segment is cut (whole_segments).
+template <typename Cursor>
+__device__ __forceinline__ int64_t whole_begin(int whole, const TileSplit& split, const int* pre,
+                                               const int* ctx, const AttnArgs& a, int c) {
+    if (whole == kOwnCta) return segment_begin(pre, a.B, a.Hkv, c);
+    const int64_t t = split.begin(c);
+    if (t >= (int64_t)pre[a.B] * a.Hkv) return t;
+    Cursor s;
+    s.init(t, pre, ctx, a);
+    return s.seg_start + (2 * s.lt < s.nb ? 0 : s.nb);
+}
+
 // A 64-bit value in shared memory, read afresh at every use: the persistent
 // kernels keep their CTA range there so that it occupies no register through
 // their main loops.

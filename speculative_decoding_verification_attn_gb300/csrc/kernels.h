@@ -140,14 +140,22 @@ inline int64_t max_units(const AttnArgs& a, int unit) {
     return all < seen ? all : seen;
 }
 
-// Whether a call of short segments gives each a CTA of its own.  Cutting them
-// costs the combine launch and a piece's end, `worth` tiles' time together; not
-// cutting them leaves a segment's tiles to one CTA while the others idle, so
-// that a segment of t tiles takes t (1 - segments / CTAs) tiles' time longer.
-// Past 12 tiles unequal lengths outweigh it.
-inline bool whole_segments(const AttnArgs& a, int num_ctas, int unit, int worth) {
+// How a call of short segments goes without cutting any (and so without the
+// combine): cutting costs a launch, the partials and a piece's end, `worth` tiles'
+// time together.
+//  * kOwnCta: as many segments as CTAs or fewer, a CTA each.  A segment of t tiles
+//    then takes t (1 - segments / CTAs) tiles' time longer than its share.  Past 12
+//    tiles unequal lengths outweigh it.
+//  * kRounded: more segments; the CTAs' ranges end at the segment's end nearest to
+//    an even split, up to a segment away from it at both ends together.  Worth it up
+//    to `base` tiles per segment and `more` / 4 for every segment that a CTA takes.
+enum { kCut, kOwnCta, kRounded };
+inline int whole_segments(const AttnArgs& a, int num_ctas, int unit, int worth, int base,
+                          int more) {
     const int64_t segs = (int64_t)a.B * a.Hkv, t = max_units(a, unit);
-    return segs <= num_ctas && t <= 12 && t * (num_ctas - segs) <= (int64_t)worth * num_ctas;
+    if (segs > num_ctas)
+        return (t - base) * 4 * num_ctas <= (int64_t)more * segs ? kRounded : kCut;
+    return t <= 12 && t * (num_ctas - segs) <= (int64_t)worth * num_ctas ? kOwnCta : kCut;
 }
 
 // ---- tensor-core kernel over an e4m3 cache (codes fed to the MMAs as stored;

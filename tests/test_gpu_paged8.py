@@ -301,6 +301,17 @@ def test_window_cut_segments(binding, kind, ctas):
                                   [3100, 5, 2200, 260], 1600, 140))
 
 
+@pytest.mark.parametrize("ctas", [1, 2, 5, 11, 23])
+@pytest.mark.parametrize("kind,window", [("bf16", 200), ("e4m3", 200), ("e4m3", 0)])
+def test_ranges_that_end_with_segments(binding, kind, window, ctas):
+    """More short segments than CTAs, of very unequal lengths: no segment is cut,
+    some CTAs take many and some none."""
+    binding.spec_set_option(binding.SPEC_OPT_NUM_CTAS, ctas)
+    ctx = [1300, 5, 900, 260, 0, 64] if window else [370, 5, 130, 260, 0, 64]
+    check_attn(binding, attn_case(30, kind, torch.bfloat16, 6, 3, 16, 4, 128, 16, ctx, window,
+                                  9 if window else 0))
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_window_that_covers_all_equals_none(binding, kind):
     c = attn_case(27, kind, torch.bfloat16, 2, 4, 8, 2, 128, 16, [90, 300])
