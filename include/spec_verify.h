@@ -153,8 +153,9 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  *   lse          [batch, num_draft, num_q_heads] fp32 natural log, or NULL
  *
  * Limits: 1 <= num_draft <= 64; num_q_heads % num_kv_heads == 0;
- * head_dim % 32 == 0 and head_dim <= 256; page_size >= 1; q, caches and out
- * 16-byte aligned.  A bf16 query over a bf16 cache with head_dim 128, a
+ * head_dim % 32 == 0 and head_dim <= 256; page_size >= 1;
+ * max_pages_per_seq * page_size >= num_draft (the drafts' keys have a place);
+ * q, caches and out 16-byte aligned.  A bf16 query over a bf16 cache with head_dim 128, a
  * power-of-two page_size in [16, 256] and batch <= 1024 runs on a
  * tensor-core kernel: the warp-MMA kernel when num_draft * (num_q_heads /
  * num_kv_heads) <= 16, the tcgen05 kernel up to 128.  An E4M3 cache runs on a

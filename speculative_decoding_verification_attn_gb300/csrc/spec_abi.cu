@@ -227,6 +227,10 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
         return fail(SPEC_ERR_INVALID, "kv_dtype must be F32, BF16, I8 or E4M3");
     if (!(scale == scale)) return fail(SPEC_ERR_INVALID, "scale is NaN");
     if (batch == 0) return SPEC_OK;
+    // the kernels walk keys 0 .. num_draft - 1 at least, whatever ctx_lens says
+    if ((int64_t)max_pages_per_seq * page_size < num_draft)
+        return fail(SPEC_ERR_INVALID, "the block table's %d pages of %d do not hold num_draft = %d "
+                    "keys", max_pages_per_seq, page_size, num_draft);
     if (!q || !k_cache || !v_cache || !block_table || !ctx_lens || !out)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
     int rc = check_scales(kv_dtype, k_scale, v_scale);

@@ -1,0 +1,51 @@
+"""Refusals and host logic at the edges of the paged calls.  Runs without a GPU:
+every argument check precedes the first CUDA call."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_attn_gb300 import binding, build
+    build.build()
+    return binding.load()
+
+
+def vp(x):
+    return ctypes.c_void_p(x) if x else None
+
+
+def attn_args(**kw):
+    a = dict(q=16, kc=16, vc=16, ks=None, vs=None, bt=16, ctx=16, mask=None, B=1, k=4, Hq=8, Hkv=2,
+             D=128, P=16, NP=8, MP=4, qdt=1, kvdt=1, scale=0.088, window=64, sinks=4, out=16)
+    a.update(kw)
+    return a
+
+
+def attend(lib, form, **kw):
+    """The status of an attention call of the given form."""
+    a = attn_args(**kw)
+    head = [vp(a[n]) for n in ("q", "kc", "vc", "ks", "vs", "bt", "ctx")]
+    if form != "chain":
+        head.append(vp(a["mask"]))
+    tail = [a[n] for n in ("B", "k", "Hq", "Hkv", "D", "P", "NP", "MP", "qdt", "kvdt", "scale")]
+    if form == "window":
+        tail += [a["window"], a["sinks"]]
+    name = {"chain": "", "tree": "_tree", "window": "_window"}[form]
+    return getattr(lib, "spec_verify_attn" + name)(*head, *tail, vp(a["out"]), None, None)
+
+
+@pytest.mark.parametrize("form,mask", [("chain", None), ("tree", 16), ("window", None),
+                                       ("window", 16)])
+@pytest.mark.parametrize("kvdt", [1, 5])
+@pytest.mark.parametrize("k,P,MP", [(64, 16, 1), (2, 1, 1), (33, 16, 2)])
+def test_tables_too_short_for_the_drafts(lib, form, mask, kvdt, k, P, MP):
+    """A block table that cannot hold the drafts' keys is refused: the kernels read
+    an entry for each of them."""
+    kw = dict(k=k, P=P, MP=MP, mask=mask, kvdt=kvdt, window=64, ks=16, vs=16)
+    assert attend(lib, form, **kw) == -1
+    assert "block table" in lib.spec_last_error().decode()
+    assert attend(lib, form, **dict(kw, B=0)) == 0
