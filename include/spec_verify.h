@@ -242,7 +242,8 @@ SPEC_API int spec_accept_greedy_tensors(const spec_tensor_t *logits,
  * cached context and the draft keys t (position ctx_b + t) whose bit t is
  * set in tree_mask[b, i] (uint64 [batch, num_draft], device memory) -- for a
  * tree, node i's ancestors and itself.  The causal chain is the mask with
- * bits 0..i.  Runs on the same kernels as spec_verify_attn.
+ * bits 0..i; bits from num_draft on are ignored.  Runs on the same kernels as
+ * spec_verify_attn.
  */
 SPEC_API int spec_verify_attn_tree(const void *q, const void *k_cache, const void *v_cache,
                                    const void *k_scale, const void *v_scale,
@@ -260,7 +261,7 @@ SPEC_API int spec_verify_attn_tree(const void *q, const void *k_cache, const voi
  * sequence b sees key j only if
  *   j < num_sinks   or   pos_i - j < window,
  * where pos_i = ctx_b + i, or with a tree ctx_b + (node i's ancestors: the
- * set bits of its mask less one), is the query's position.  The query itself
+ * set bits of its mask below num_draft, less one), is the query's position.  The query itself
  * counts, so window 1 leaves a query its own key and the sinks.  Keys that no
  * query of a sequence sees are not read (whole pages of them may have left
  * the pool: their block_table entries are not looked at).
