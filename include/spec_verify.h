@@ -97,7 +97,8 @@ enum {
     /* persistent CTAs of the tensor-core kernel; 0 = number of SMs */
     SPEC_OPT_NUM_CTAS = 1,
     /* 1: copy block_table and ctx_lens to the host and check them before
-     * launching (synchronises the stream); 0: no host check */
+     * launching (synchronises the stream); with a window, entries of pages
+     * that no query sees are not checked.  0: no host check */
     SPEC_OPT_VALIDATE = 2,
     /* key chunk of the SIMT kernel's split-KV; 0 = automatic */
     SPEC_OPT_SIMT_CHUNK = 3,

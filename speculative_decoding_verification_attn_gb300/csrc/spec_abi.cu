@@ -114,9 +114,17 @@ int dtype_size(int32_t dt) {
     }
 }
 
-// Host-side check of block_table / ctx_lens (SPEC_OPT_VALIDATE).
+// Host-side check of block_table / ctx_lens (SPEC_OPT_VALIDATE): of the entries
+// that a kernel looks at, which with a window are those of pages that hold a
+// sink or a key of the first query's window (or later).
 int validate_tables(const specv::AttnArgs& a, cudaStream_t stream) {
-    std::vector<int32_t> ctx(a.B), bt((size_t)a.B * a.max_pages);
+    std::vector<int32_t> ctx, bt;
+    try {
+        ctx.resize(a.B);
+        bt.resize((size_t)a.B * a.max_pages);
+    } catch (...) {
+        return fail(SPEC_ERR_CUDA, "validate: out of host memory");
+    }
     cudaError_t e = cudaMemcpyAsync(ctx.data(), a.ctx_lens, sizeof(int32_t) * a.B,
                                     cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess)
@@ -129,8 +137,9 @@ int validate_tables(const specv::AttnArgs& a, cudaStream_t stream) {
         if (ctx[b] < 0 || L > (int64_t)a.max_pages * a.P)
             return fail(SPEC_ERR_INVALID, "ctx_lens[%d]=%d: ctx + num_draft exceeds the %d pages "
                         "of the block table", b, ctx[b], a.max_pages);
-        const int64_t n = (L + a.P - 1) / a.P;
+        const int64_t n = (L + a.P - 1) / a.P, low = specv::window_low(a, ctx[b]);
         for (int64_t p = 0; p < n; ++p) {
+            if (p * a.P >= a.sinks && (p + 1) * a.P <= low) continue;  // no query sees it
             const int32_t id = bt[(size_t)b * a.max_pages + p];
             if (id < 0 || id >= a.num_pages)
                 return fail(SPEC_ERR_INVALID, "block_table[%d][%lld]=%d outside [0, %d)", b,

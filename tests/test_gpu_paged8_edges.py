@@ -34,3 +34,32 @@ def test_window_tree_bits_past_the_drafts(binding, kind, qdt, D, path, k, window
     high = np.int64(-1) << k
     got = window_call(binding, c, window, 2, c["mask"] | int(high))
     assert torch.equal(got[0], want) and torch.equal(got[1], lse)
+
+
+# ---------------------------------------------------------------- host checks
+@pytest.mark.parametrize("kind,D", [("bf16", 128), ("e4m3", 128), ("f32", 64)])
+def test_validation_knows_the_window(binding, kind, D):
+    """SPEC_OPT_VALIDATE looks at the entries of pages that some query sees and at
+    no others (pages behind the window may have left the pool)."""
+    m = binding
+    qdt = torch.float32 if kind == "f32" else torch.bfloat16
+    c = attn_case(72, kind, qdt, 2, 4, 4, 2, D, 16, [300, 11], 64, 20)
+    assert int(c["table"][0, 2]) == -1  # freed
+    m.spec_set_option(m.SPEC_OPT_VALIDATE, 1)
+    try:
+        check_attn(m, c)
+        first = (300 - 64 + 1) // 16  # page of the first key in the window
+        for page in (0, 1, first, 18):  # sinks, window, drafts
+            table = c["table"].clone()
+            assert int(table[0, page]) >= 0
+            table[0, page] = 10 ** 6
+            with pytest.raises(m.SpecError) as err:
+                window_call(m, dict(c, table=table), 64, 20)
+            assert err.value.code == m.SPEC_ERR_INVALID
+        assert int(c["table"][0, first - 1]) == -1
+        full = c["table"].clamp(min=0)
+        with pytest.raises(m.SpecError):  # without a window every page counts
+            window_call(m, c, 400, 0)
+        window_call(m, dict(c, table=full), 400, 0)
+    finally:
+        m.spec_set_option(m.SPEC_OPT_VALIDATE, 0)
