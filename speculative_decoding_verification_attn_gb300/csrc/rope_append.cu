@@ -312,14 +312,15 @@ __device__ __forceinline__ void row_cta(const RopeParams& p, float2* turns, int6
     const int group = (int)(item % p.groups);
     if (token >= (int64_t)a.B * a.n) return;
     const int b = (int)(token / a.n), t = (int)(token % a.n);
-    const int64_t pos = (int64_t)__ldg(a.ctx_lens + b) + t;
+    const int64_t ctx = __ldg(a.ctx_lens + b), pos = ctx + t;
     if (t >= new_len(a, b)) return;
     const int e0 = (lane & ((1 << p.lr_log2) - 1)) * 8;
     const int h_begin = group * p.heads_per_warp;
     const int h_end = min(p.heads, h_begin + p.heads_per_warp);
-    // the cache row of a warp that holds k or v heads
+    // the cache row of a warp that holds k or v heads (none of a sequence whose
+    // context is negative, also where ctx + t is a position again)
     int page = -1;
-    if (MODE != kPages && h_end > a.Hq) page = find_page(a, b, pos, lane == 0);
+    if (MODE != kPages && h_end > a.Hq) page = find_page(a, b, ctx < 0 ? ctx : pos, lane == 0);
     constexpr int N = INTER ? 4 : 8;
     float2 cs[N];
     const int j0 = e0 < a.D ? first_pair<INTER>(a, e0) : -1;

@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_paged8 import attn_case, binding, check_attn, cuda  # noqa: F401
+from paged8 import E4M3
+from test_gpu_paged8 import attn_case, binding, check_attn, cuda, rope_case, run_rope  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +64,27 @@ def test_validation_knows_the_window(binding, kind, D):
         window_call(m, dict(c, table=full), 400, 0)
     finally:
         m.spec_set_option(m.SPEC_OPT_VALIDATE, 0)
+
+
+# ---------------------------------------------------------------- append
+@pytest.mark.parametrize("kind", ["f32", "bf16", "i8", "e4m3"])
+def test_rope_append_negative_context(binding, kind):
+    """A sequence whose context is negative writes nothing, also where ctx + t is
+    a position again; the others go on."""
+    c = rope_case(74, kind, torch.bfloat16, 2, 6, 4, 2, 128, 16, [14, 40])
+    bad = dict(c, ctx=torch.tensor([-2, 40]).int())
+    table, _ = binding.spec_rope_table(128)
+    good = run_rope(binding, c, 128, False, 1.0, table)
+    assert binding.spec_device_error() == 0
+    got = run_rope(binding, bad, 128, False, 1.0, table)
+    assert binding.spec_device_error() == binding.SPEC_DEVERR_CTX
+    assert (got["q"] != -7.0).any(-1).all()  # q is rotated all the same
+    mine = torch.zeros(c["kc"].shape[0], dtype=torch.bool)
+    mine[c["table"][1].clamp(min=0).long()] = c["table"][1] >= 0
+    for n in ("kc", "vc", "ks", "vs"):
+        if got[n] is None:
+            continue
+        a, b, g = ((t.view(torch.uint8) if t.dtype == E4M3 else t)
+                   for t in (got[n], c[n], good[n]))
+        assert torch.equal(a[~mine], b[~mine])
+        assert torch.equal(a[mine], g[mine])
