@@ -213,7 +213,9 @@ __device__ __forceinline__ int new_len(const RopeAppendArgs& a, int b) {
 // x / s for a fixed positive s, to nearest: with r = 1 / s rounded to nearest,
 // q = x r and the exact remainder x - q s, q + r (x - q s) is the correctly
 // rounded quotient (Markstein's theorem), three instructions per element where
-// a division takes three times as many.  Outside the range where no step
+// a division takes three times as many.  The remainder, exact, is rounded down:
+// a zero one is then -0, which leaves the sign of a zero q as it is (+0 would turn
+// -0 / s, a code of its own in e4m3, into +0).  Outside the range where no step
 // underflows the division itself.
 struct Divide {
     float s, r;
@@ -236,7 +238,7 @@ struct Divide {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float q = x[e] * r;
-            x[e] = fmaf(fmaf(-q, s, x[e]), r, q);
+            x[e] = fmaf(__fmaf_rd(-q, s, x[e]), r, q);
         }
     }
 };

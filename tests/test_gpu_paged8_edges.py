@@ -88,3 +88,53 @@ def test_rope_append_negative_context(binding, kind):
                    for t in (got[n], c[n], good[n]))
         assert torch.equal(a[~mine], b[~mine])
         assert torch.equal(a[mine], g[mine])
+
+
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("P,D,kept", [(16, 128, 5), (32, 64, 0), (64, 256, 40)])
+def test_e4m3_append_bit_for_bit(binding, src, P, D, kept):
+    """Unrotated rows: scales, new codes and the kept rows' codes are the formula's
+    in fp32, bit for bit, signed zeros and subnormal codes among them."""
+    B, n, Hkv = 4, 20, 3
+    gen = torch.Generator().manual_seed(75)
+    x = torch.randn(2, B, n, Hkv, D, generator=gen)
+    x *= torch.exp(3 * torch.randn(2, B, 1, Hkv, 1, generator=gen))
+    x *= torch.rand(x.shape, generator=gen) ** 6  # down to the subnormal codes
+    zero = torch.rand(x.shape, generator=gen) < 0.2
+    x[zero] = torch.copysign(torch.zeros(()), torch.randn(x.shape, generator=gen)[zero])
+    x[0, 3] = torch.copysign(torch.zeros(()), x[0, 3])  # a page of zeros
+    x = x.to(src)
+    mp = (kept + n + P - 1) // P
+    table = torch.randperm(B * mp, generator=gen).int().view(B, mp)
+    codes = torch.randint(0, 256, (2, B * mp, Hkv, P, D), generator=gen).to(torch.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0x80  # no NaN
+    scale = torch.rand(2, B * mp, Hkv, generator=gen) * 0.05
+    old_codes, old_scale = codes.clone(), scale.clone()
+    got = [codes[w].view(E4M3).cuda() for w in range(2)]
+    gs = [scale[w].cuda() for w in range(2)]
+    binding.spec_kv_append(x[0].cuda(), x[1].cuda(), *got, table.cuda(),
+                           torch.full((B,), kept).int().cuda(), *gs)
+    for w in range(2):
+        for b in range(B):
+            for g in range(mp):
+                page = int(table[b, g])
+                lo, hi = max(kept, g * P), min(kept + n, (g + 1) * P)
+                if lo >= hi:
+                    continue
+                rows = x[w, b, lo - kept:hi - kept].float().transpose(0, 1)  # [Hkv, r, D]
+                first = lo - g * P
+                s = rows.abs().amax((1, 2)) / 448.0
+                before = old_scale[w, page].clone()
+                if first:
+                    s = torch.maximum(s, before)
+                old_scale[w, page] = s
+                wide = s[:, None, None]
+                new = torch.where(wide > 0, rows / wide, torch.zeros(())).to(E4M3)
+                old_codes[w, page, :, first:first + hi - lo] = new.view(torch.uint8)
+                for h in range(Hkv):
+                    if first and s[h] > before[h]:
+                        row = old_codes[w, page, h, :first].view(E4M3).float() * before[h]
+                        old_codes[w, page, h, :first] = (row / s[h]).to(E4M3).view(torch.uint8)
+        assert torch.equal(gs[w].cpu(), old_scale[w])
+        off = (got[w].cpu().view(torch.uint8) != old_codes[w]).sum().item()
+        assert off == 0, "%d codes differ" % off
