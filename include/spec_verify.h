@@ -28,9 +28,10 @@
  *   - The library owns a per-device workspace (split-KV partials, reduction
  *     partials, completion tickets, an error word), grown on demand with
  *     cudaMalloc on the first call that needs more (so a call that grows it
- *     synchronises the device) and kept until spec_release() or exit.  A
- *     buffer that was outgrown stays as well, so that graphs captured before
- *     the growth replay soundly; a call that would grow it while its stream
+ *     synchronises the device) and kept until spec_release() or exit.  It
+ *     grows to twice its size, or where that cannot be had to what the call
+ *     needs.  A buffer that was outgrown stays as well, so that graphs captured
+ *     before the growth replay soundly; a call that would grow it while its stream
  *     is being captured returns SPEC_ERR_UNSUPPORTED (make one such call
  *     first).  Replays of captured graphs share it like the calls do.
  *     Calls that overlap on the GPU (different streams without ordering)

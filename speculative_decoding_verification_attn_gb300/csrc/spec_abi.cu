@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "kernels.h"
+#include "workspace.h"
 
 namespace {
 
@@ -75,18 +76,18 @@ int get_workspace(size_t scratch, cudaStream_t stream, Workspace** out) {
             return fail(SPEC_ERR_UNSUPPORTED, "the workspace would grow during a stream capture: "
                         "make one such call before capturing");
         (void)cudaGetLastError();
-        // at least twice the old size, so that the retired buffers together
-        // stay below the current one
-        size_t grow = need < (size_t)64 << 20 ? (size_t)64 << 20 : need;
-        if (grow < 2 * w.bytes) grow = 2 * w.bytes;
         try {
             w.retired.reserve(w.retired.size() + 1);
         } catch (...) {
             return fail(SPEC_ERR_CUDA, "out of host memory");
         }
         void* fresh = nullptr;
-        e = cudaMalloc(&fresh, grow);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
+        const size_t grow = specv::grow_buffer(need, w.bytes, [&](size_t bytes) {
+            e = cudaMalloc(&fresh, bytes);
+            if (e != cudaSuccess) (void)cudaGetLastError();  // not the next launch's
+            return e == cudaSuccess;
+        });
+        if (!grow) return cuda_fail(e, "cudaMalloc(workspace)");
         e = cudaMemset(fresh, 0, kHeader);
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
         if (e != cudaSuccess) {
