@@ -178,27 +178,19 @@ def spec_set_option(option: int, value: int) -> None:
 _E4M3, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
 
 
-def _check_page_scales(k_cache, v_cache, k_scale, v_scale) -> None:
-    """The scales of a float8_e4m3fn cache: float32 [num_pages, Hkv] each (the
-    library takes a bare pointer and cannot tell)."""
-    if k_cache.dtype is not _E4M3:
-        return
-    pool = k_cache.shape
-    if v_cache.dtype is not _E4M3 or v_cache.shape != pool:
-        raise ValueError("k_cache and v_cache must share a dtype and a shape")
-    want = (pool[0], pool[1])
-    if (k_scale is not None and (k_scale.dtype is not _F32 or k_scale.shape != want)
-            or v_scale is not None and (v_scale.dtype is not _F32 or v_scale.shape != want)):
-        raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
-
-
 def _check_scales(k_cache, v_cache, k_scale, v_scale) -> None:
-    """_check_page_scales, and an int8 cache's scales: float16 [num_pages, Hkv, P]."""
-    if k_cache.dtype is not torch.int8:
-        return _check_page_scales(k_cache, v_cache, k_scale, v_scale)
-    for s in (k_scale, v_scale):
-        if s is not None and (s.dtype is not torch.float16 or s.shape != k_cache.shape[:3]):
-            raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
+    """The scales of an int8 cache (float16 [num_pages, Hkv, P]) or a float8_e4m3fn
+    one (float32 [num_pages, Hkv]): the library takes a bare pointer and cannot
+    tell."""
+    kind, pool = k_cache.dtype, k_cache.shape
+    if kind is torch.int8:
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype is not torch.float16 or s.shape != pool[:3]):
+                raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
+    elif kind is _E4M3:
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype is not _F32 or s.shape != pool[:2]):
+                raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
 
 
 def _device_of(first) -> int:
@@ -218,6 +210,33 @@ def _ptrs(dev: int, *tensors):
     return [None if t is None else t.data_ptr() for t in tensors]
 
 
+def _reach(*tensors):
+    """Pointers of dense tensors that the current device reaches: its own memory or
+    the host's, but no other GPU's (None stays None)."""
+    dev = _get_device()
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+        if t.get_device() not in (dev, -1):  # (-1: host memory)
+            raise ValueError("tensors must not lie on another GPU than the current CUDA device")
+    return [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale) -> None:
+    """What the library cannot see behind the pointers of an attention call."""
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share a dtype and a shape")
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
+        raise ValueError("block_table and ctx_lens must be int32")
+    if out.dtype is not q.dtype or out.numel() < q.numel():
+        raise ValueError("out must have q's dtype and size")
+    if lse is not None and lse.dtype is not _F32:
+        raise ValueError("lse must be float32")
+
+
 def _stream_on(stream, dev: int) -> int:
     if stream is None and _raw_stream is not None:
         return _raw_stream(dev)
@@ -233,18 +252,13 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
     k_scale / v_scale [NP, Hkv, P] fp16 for an int8 cache, [NP, Hkv] float32
     for a float8_e4m3fn cache.
     """
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
     B, k, Hq, D = q.shape
     NP, Hkv, P, D2 = k_cache.shape
     if k != num_draft or D2 != D:
         raise ValueError("shape mismatch between q, num_draft and the cache")
-    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
-        raise ValueError("block_table and ctx_lens must be int32")
-    tensors = (q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse)
-    for t in tensors:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
-    qp, kp, vp, ksp, vsp, tp, cp, op, lp = [None if t is None else t.data_ptr() for t in tensors]
+    _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale)
+    qp, kp, vp, ksp, vsp, tp, cp, op, lp = _reach(q, k_cache, v_cache, k_scale, v_scale,
+                                                  block_table, ctx_lens, out, lse)
     _check(load().spec_verify_attn(
         qp, kp, vp, ksp, vsp, tp, cp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
@@ -285,12 +299,12 @@ def spec_verify_attn_tree(q, k_cache, v_cache, block_table, ctx_lens, tree_mask,
         raise ValueError("q must be [B, num_draft, Hq, D], tree_mask [B, num_draft]")
     if tree_mask.element_size() != 8:
         raise ValueError("tree_mask must hold 64-bit words")
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
+    _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale)
+    qp, kp, vp, ksp, vsp, tp, cp, mp, op, lp = _reach(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, tree_mask, out, lse)
     _check(load().spec_verify_attn_tree(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-        _ptr(ctx_lens), _ptr(tree_mask), B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
-        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), _ptr(out), _ptr(lse),
-        _stream(stream)))
+        qp, kp, vp, ksp, vsp, tp, cp, mp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
+        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
 
 
 def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
@@ -391,13 +405,20 @@ def spec_kv_append(k_new, v_new, k_cache, v_cache, block_table, ctx_lens, k_scal
     the paged caches (INT8 caches are quantised into k_scale / v_scale)."""
     B, n, Hkv, D = k_new.shape
     NP, Hkv2, P, D2 = k_cache.shape
-    if (Hkv2, D2) != (Hkv, D) or tuple(v_new.shape) != tuple(k_new.shape):
+    if (Hkv2, D2) != (Hkv, D) or v_new.shape != k_new.shape:
         raise ValueError("k_new / v_new must be [B, n, Hkv, D] matching the cache")
-    _check_page_scales(k_cache, v_cache, k_scale, v_scale)
-    _check(load().spec_kv_append(_ptr(k_new), _ptr(v_new), _TORCH_DT[k_new.dtype], _ptr(k_cache),
-                                 _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                 _TORCH_DT[k_cache.dtype], _ptr(block_table), _ptr(ctx_lens), B,
-                                 n, Hkv, D, P, NP, block_table.shape[1], _stream(stream)))
+    if v_new.dtype is not k_new.dtype:
+        raise ValueError("k_new and v_new must share a dtype")
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share a dtype and a shape")
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
+        raise ValueError("block_table and ctx_lens must be int32")
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
+    kp, vp, kcp, vcp, ksp, vsp, tp, cp = _reach(k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                                block_table, ctx_lens)
+    _check(load().spec_kv_append(kp, vp, _TORCH_DT[k_new.dtype], kcp, vcp, ksp, vsp,
+                                 _TORCH_DT[k_cache.dtype], tp, cp, B, n, Hkv, D, P, NP,
+                                 block_table.shape[1], _stream(stream)))
 
 
 _ROPE_SCALING = {"none": SPEC_ROPE_PLAIN, "linear": SPEC_ROPE_LINEAR, "ntk": SPEC_ROPE_NTK,

@@ -6,6 +6,7 @@ import ctypes
 import subprocess
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -91,3 +92,90 @@ def test_workspace_growth(growth):
     assert growth(1000, 0, 5000) == (1000, 2)
     assert growth(GB + GB // 10, GB, GB) == (0, 2)
     assert growth(3 * GB, GB, GB) == (0, 1)  # the same size is not asked for twice
+
+
+def paged_tensors(kind):
+    """Tensors of a small call on the CPU: q, rows, cache, scale, table, context."""
+    B, k, Hq, Hkv, D, P, NP = 2, 4, 8, 2, 64, 16, 4
+    cache = torch.zeros(NP, Hkv, P, D, dtype=torch.uint8)
+    cache = cache.view(torch.int8 if kind == "i8" else torch.float8_e4m3fn) if kind != "bf16" \
+        else cache.bfloat16()
+    scale = {"bf16": None, "i8": torch.zeros(NP, Hkv, P, dtype=torch.float16),
+             "e4m3": torch.zeros(NP, Hkv)}[kind]
+    return dict(q=torch.zeros(B, k, Hq, D, dtype=torch.bfloat16),
+                rows=torch.zeros(B, k, Hkv, D, dtype=torch.bfloat16), cache=cache, scale=scale,
+                table=torch.zeros(B, 2, dtype=torch.int32), ctx=torch.zeros(B, dtype=torch.int32),
+                mask=torch.zeros(B, k, dtype=torch.int64))
+
+
+def paged_call(binding, call, t, **kw):
+    """spec_verify_attn, _tree or spec_kv_append over the tensors t, some replaced."""
+    a = dict(v_cache=t["cache"], out=t["q"], lse=None, k_scale=t["scale"], v_scale=t["scale"],
+             v_new=t["rows"], table=t["table"], ctx=t["ctx"])
+    a.update(kw)
+    scales = dict(k_scale=a["k_scale"], v_scale=a["v_scale"])
+    if call == "append":
+        return binding.spec_kv_append(t["rows"], a["v_new"], t["cache"], a["v_cache"], a["table"],
+                                      a["ctx"], **scales)
+    args = (t["q"], t["cache"], a["v_cache"], a["table"], a["ctx"])
+    if call == "tree":
+        args += (t["mask"],)
+        return binding.spec_verify_attn_tree(*args, 4, 0.1, a["out"], a["lse"], **scales)
+    return binding.spec_verify_attn(*args, 4, 0.1, a["out"], a["lse"], **scales)
+
+
+@pytest.mark.parametrize("call", ["chain", "tree", "append"])
+def test_binding_checks_what_the_library_cannot_see(lib, call):
+    """Scales, tables, caches and outputs of another type or size than the pointers
+    are taken for are refused by the older calls as well."""
+    from speculative_decoding_verification_attn_gb300 import binding
+    for kind in ("i8", "e4m3"):
+        t = paged_tensors(kind)
+        other = t["scale"].float() if kind == "i8" else t["scale"].half()
+        for bad in (other, t["scale"][:3], t["scale"][..., 0]):
+            for name in ("k_scale", "v_scale"):
+                with pytest.raises(ValueError, match="scales of an"):
+                    paged_call(binding, call, t, **{name: bad})
+    t = paged_tensors("bf16")
+    for name in ("table", "ctx"):
+        for dt in (torch.int64, torch.int16):
+            with pytest.raises(ValueError, match="int32"):
+                paged_call(binding, call, t, **{name: t[name].to(dt)})
+    for bad in (t["cache"].float(), t["cache"][:3]):
+        with pytest.raises(ValueError, match="k_cache and v_cache"):
+            paged_call(binding, call, t, v_cache=bad)
+    if call == "append":
+        with pytest.raises(ValueError, match="k_new and v_new"):
+            paged_call(binding, call, t, v_new=t["rows"].float())
+    else:
+        for bad in (t["q"].float(), t["q"][:1]):
+            with pytest.raises(ValueError, match="out must"):
+                paged_call(binding, call, t, out=bad)
+        with pytest.raises(ValueError, match="lse must"):
+            paged_call(binding, call, t, lse=torch.zeros(2, 4, 8, dtype=torch.float64))
+
+
+class Elsewhere:
+    """A tensor that says it lies on another GPU."""
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return 1
+
+
+@pytest.mark.parametrize("call", ["chain", "tree", "append"])
+def test_binding_refuses_memory_of_another_device(lib, call, monkeypatch):
+    """Kernels launch on the current device: a tensor of another one is refused
+    before its pointer reaches them."""
+    from speculative_decoding_verification_attn_gb300 import binding
+    monkeypatch.setattr(binding, "_get_device", lambda: 0)
+    t = paged_tensors("bf16")
+    for name in ("table", "ctx", "v_new" if call == "append" else "out"):
+        where = t["rows"] if name == "v_new" else t["q"] if name == "out" else t[name]
+        with pytest.raises(ValueError, match="current CUDA device"):
+            paged_call(binding, call, t, **{name: Elsewhere(where)})
