@@ -307,6 +307,12 @@ def spec_verify_attn_tree(q, k_cache, v_cache, block_table, ctx_lens, tree_mask,
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
 
 
+def _span(n) -> int:
+    """A number of positions as int32: one past its range stands for as many as
+    there are (ctypes would drop its upper bits)."""
+    return max(-1, min(int(n), 2 ** 31 - 1))
+
+
 def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
                             scale: float, window: int, num_sinks: int, out, lse=None,
                             k_scale=None, v_scale=None, tree_mask=None, stream=None) -> None:
@@ -333,7 +339,7 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draf
         dev, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, tree_mask, out, lse)
     _check(load().spec_verify_attn_window(
         qp, kp, vp, ksp, vsp, tp, cp, mp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
-        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), int(window), int(num_sinks),
+        _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), _span(window), _span(num_sinks),
         op, lp, _stream_on(stream, dev)))
 
 

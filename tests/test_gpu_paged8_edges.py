@@ -66,6 +66,21 @@ def test_validation_knows_the_window(binding, kind, D):
         m.spec_set_option(m.SPEC_OPT_VALIDATE, 0)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31, 0), (2 ** 32 + 5, 3), (2 ** 40, 2 ** 33),
+                                          (7, 2 ** 32 + 1)])
+def test_windows_past_32_bits(binding, kind, window, sinks):
+    """A window (or a number of sinks) longer than any context sees all of it."""
+    c = attn_case(73, kind, torch.bfloat16, 2, 4, 8, 2, 128, 16, [90, 300])
+    want = window_call(binding, c, 2 ** 31 - 1, 0)
+    got = window_call(binding, c, window, sinks)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(binding.SpecError):
+        window_call(binding, c, -2 ** 32 + 5, 0)
+    with pytest.raises(binding.SpecError):
+        window_call(binding, c, 5, -2 ** 32 + 5)
+
+
 # ---------------------------------------------------------------- append
 @pytest.mark.parametrize("kind", ["f32", "bf16", "i8", "e4m3"])
 def test_rope_append_negative_context(binding, kind):
