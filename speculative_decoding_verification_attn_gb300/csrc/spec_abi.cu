@@ -104,6 +104,16 @@ int get_workspace(size_t scratch, cudaStream_t stream, Workspace** out) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether the product of sizes >= 1 reaches `limit`; no step of it overflows.
+bool reaches(int64_t limit, std::initializer_list<int64_t> sizes) {
+    int64_t p = 1;
+    for (const int64_t s : sizes) {
+        if (p >= (limit + s - 1) / s) return true;
+        p *= s;
+    }
+    return false;
+}
+
 int dtype_size(int32_t dt) {
     switch (dt) {
     case SPEC_DTYPE_F32: return 4;
@@ -247,7 +257,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     if (rc) return rc;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
         return fail(SPEC_ERR_INVALID, "q, caches and out must be 16-byte aligned");
-    if ((int64_t)num_pages * num_kv_heads * page_size * head_dim >= (1LL << 40))
+    if (reaches(1LL << 40, {num_pages, num_kv_heads, page_size, head_dim}))
         return fail(SPEC_ERR_INVALID, "cache too large");
     const int64_t R = (int64_t)num_draft * (num_q_heads / num_kv_heads);
     (void)dtype_size;
@@ -515,7 +525,7 @@ int spec_kv_append(const void* k_new, const void* v_new, int32_t src_dtype, void
                                 num_kv_heads, head_dim, page_size, num_pages, max_pages_per_seq,
                                 stream);
     }
-    if ((int64_t)batch * num_new * num_kv_heads * 2 / 8 >= (1LL << 31))
+    if (reaches(1LL << 33, {batch, num_new, num_kv_heads}))
         return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
     Workspace* ws = nullptr;
     rc = get_workspace(0, static_cast<cudaStream_t>(stream), &ws);
@@ -576,8 +586,8 @@ int spec_rope_append(const void* q, const void* k_new, const void* v_new, void* 
     if ((reinterpret_cast<uintptr_t>(rope_table) & 7))
         return fail(SPEC_ERR_INVALID, "rope_table must be 8-byte aligned");
     // every launch index and in-kernel product below stays inside 31 bits
-    if ((int64_t)batch * num_new * (num_q_heads + 2 * num_kv_heads) >= (1LL << 31) ||
-        (int64_t)num_pages * num_kv_heads * page_size >= (1LL << 40))
+    if (reaches(1LL << 31, {batch, num_new, num_q_heads + 2 * (int64_t)num_kv_heads}) ||
+        reaches(1LL << 40, {num_pages, num_kv_heads, page_size}))
         return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
     Workspace* ws = nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -663,7 +673,7 @@ int spec_kv_gather(const void* k_cache, const void* v_cache, const void* k_scale
     if (rc) return rc;
     if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
         return fail(SPEC_ERR_INVALID, "caches and outputs must be 16-byte aligned");
-    if (batch > 65535 || (int64_t)max_len * num_kv_heads * (head_dim / 16) >= (1LL << 31))
+    if (batch > 65535 || reaches(1LL << 31, {max_len, num_kv_heads, head_dim / 16}))
         return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
     Workspace* ws = nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

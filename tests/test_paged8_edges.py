@@ -179,3 +179,35 @@ def test_binding_refuses_memory_of_another_device(lib, call, monkeypatch):
         where = t["rows"] if name == "v_new" else t["q"] if name == "out" else t[name]
         with pytest.raises(ValueError, match="current CUDA device"):
             paged_call(binding, call, t, **{name: Elsewhere(where)})
+
+
+@pytest.mark.parametrize("B,n,Hq,Hkv", [
+    (1, 1, 8, 1 << 30),                # 2 * Hkv is 2^31
+    (1 << 16, 1 << 16, 1 << 31 >> 1, 1 << 30),
+    (1, 1, (1 << 31) - 1, (1 << 31) - 1), (1 << 30, 1, 0, 1), (1, 1 << 30, 0, 1)])
+def test_append_limits_do_not_overflow(lib, B, n, Hq, Hkv):
+    """Rows past 2^31 are refused however their number is made up."""
+    row = 32 * max(Hq, Hkv)
+    q = vp(16 if Hq else 0)
+    rc = lib.spec_rope_append(q, vp(16), vp(16), q, row, row, row, row, 1, vp(16), vp(16), vp(16),
+                              vp(16), 5, vp(16), vp(16), None, None, vp(16), 0, 0, 1.0, B, n, Hq,
+                              Hkv, 32, 16, 8, 4, None)
+    assert rc == -2 and "too many" in lib.spec_last_error().decode()
+
+
+@pytest.mark.parametrize("n,Hkv,D", [(1 << 30, 1 << 30, 256), ((1 << 31) - 1, (1 << 31) - 1, 64),
+                                     (1 << 27, 1, 256), (1 << 28, 1, 128)])
+def test_gather_limits_do_not_overflow(lib, n, Hkv, D):
+    rc = lib.spec_kv_gather(vp(16), vp(16), vp(16), vp(16), 5, vp(16), None, vp(16), 1, n, Hkv, D,
+                            16, 8, 4, 1, vp(16), vp(16), None)
+    assert rc == -2 and "too many" in lib.spec_last_error().decode()
+
+
+def test_attention_limits_do_not_overflow(lib):
+    big = (1 << 31) - 1
+    for NP, Hkv, P in ((big, 1 << 22, big), (1 << 30, 1 << 13, 1 << 30), (1 << 13, 1, 1 << 20)):
+        assert attend(lib, "chain", NP=NP, Hkv=Hkv, Hq=Hkv, P=P) == -1
+        assert "cache too large" in lib.spec_last_error().decode()
+    assert lib.spec_kv_append(vp(16), vp(16), 1, vp(16), vp(16), None, None, 1, vp(16), vp(16),
+                              1 << 21, 1 << 21, 1 << 21, 32, 16, 8, 4, None) == -2
+    assert "too many" in lib.spec_last_error().decode()
