@@ -490,9 +490,17 @@ enum {
     SPEC_ROPE_LINEAR = 1, /* f_j / factor (positions interpolated) */
     SPEC_ROPE_NTK = 2,    /* theta * factor^(rotary_dim / (rotary_dim - 2)) */
     /* by parts: pairs that turn more than fast_turns times over original_len
-     * positions keep f_j, those below slow_turns take f_j / factor, a linear
-     * ramp between; amplitude 0.1 ln(factor) + 1 */
-    SPEC_ROPE_YARN = 3
+     * positions keep f_j, those below slow_turns take f_j / factor, between
+     * them a ramp linear in the number of turns (the method's equation);
+     * amplitude 0.1 ln(factor) + 1 */
+    SPEC_ROPE_YARN = 3,
+    /* or-ed to SPEC_ROPE_YARN: the ramp is linear in the pair's index instead,
+     * from floor(j(fast_turns)) to ceil(j(slow_turns)), where a pair of index
+     * j(t) = rotary_dim / 2 * ln(original_len / (2 pi t)) / ln(theta) turns t
+     * times (the borders kept in [0, rotary_dim - 1]).  Checkpoints extended
+     * with the method's published code were trained with this one; the two
+     * differ by tens of percent in some frequencies. */
+    SPEC_ROPE_RAMP_BY_INDEX = 16
 };
 
 /*

@@ -28,6 +28,7 @@ SPEC_DEVERR_PAGE, SPEC_DEVERR_CTX, SPEC_DEVERR_TIMEOUT, SPEC_DEVERR_TOKEN = 1, 2
 SPEC_DEVERR_TREE = 16
 SPEC_DEVERR_CODEC = 32
 SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_NTK, SPEC_ROPE_YARN = 0, 1, 2, 3
+SPEC_ROPE_RAMP_BY_INDEX = 16
 
 # every symbol the public header declares
 EXPORTED = ["spec_version", "spec_last_error", "spec_set_option", "spec_verify_attn",
@@ -428,7 +429,7 @@ def spec_kv_append(k_new, v_new, k_cache, v_cache, block_table, ctx_lens, k_scal
 
 
 _ROPE_SCALING = {"none": SPEC_ROPE_PLAIN, "linear": SPEC_ROPE_LINEAR, "ntk": SPEC_ROPE_NTK,
-                 "yarn": SPEC_ROPE_YARN}
+                 "yarn": SPEC_ROPE_YARN, "yarn-index": SPEC_ROPE_YARN | SPEC_ROPE_RAMP_BY_INDEX}
 
 
 def spec_rope_table(rotary_dim: int, theta: float = 10000.0, scaling: str = "none",
@@ -437,7 +438,10 @@ def spec_rope_table(rotary_dim: int, theta: float = 10000.0, scaling: str = "non
     """The frequency table of spec_rope_append (int64 [rotary_dim / 2] on
     ``device``, the bits of uint64 fractions of a turn) and its amplitude.
 
-    ``scaling``: "none", "linear", "ntk" or "yarn" (with ``original_len``).
+    ``scaling``: "none", "linear", "ntk", or with ``original_len`` "yarn" (its ramp
+    linear in a pair's number of turns, as the method is written down) or
+    "yarn-index" (linear in the pair's index, as checkpoints that were extended
+    with its published code have it).
     """
     if scaling not in _ROPE_SCALING:
         raise ValueError("scaling must be one of %s" % ", ".join(sorted(_ROPE_SCALING)))

@@ -616,6 +616,8 @@ int spec_rope_table(int32_t rotary_dim, double theta, int32_t scaling, double fa
     if (rotary_dim < 2 || rotary_dim > 256 || rotary_dim % 2)
         return fail(SPEC_ERR_INVALID, "rotary_dim must be even and in [2, 256]");
     if (!(theta > 1.0 && theta < INFINITY)) return fail(SPEC_ERR_INVALID, "theta must be > 1");
+    const bool by_index = scaling == (SPEC_ROPE_YARN | SPEC_ROPE_RAMP_BY_INDEX);
+    if (by_index) scaling = SPEC_ROPE_YARN;
     if (scaling < SPEC_ROPE_PLAIN || scaling > SPEC_ROPE_YARN)
         return fail(SPEC_ERR_INVALID, "unknown scaling %d", scaling);
     if (scaling != SPEC_ROPE_PLAIN && !(factor >= 1.0 && factor < INFINITY))
@@ -631,11 +633,23 @@ int spec_rope_table(int32_t rotary_dim, double theta, int32_t scaling, double fa
     const double two_pi = 6.283185307179586476925286766559;
     const double d = rotary_dim;
     const double base = scaling == SPEC_ROPE_NTK ? theta * pow(factor, d / (d - 2)) : theta;
+    // the ramp over the index: from pair `first` (kept) to pair `last` (all scaled)
+    double first = 0, last = 0;
+    if (by_index) {
+        auto border = [&](double turns) {  // slow_turns may be 0: no pair turns so little
+            return turns > 0 ? d / 2 * log(original_len / (two_pi * turns)) / log(theta) : d;
+        };
+        first = fmin(fmax(floor(border(fast_turns)), 0.0), d - 1);
+        last = fmin(fmax(ceil(border(slow_turns)), 0.0), d - 1);
+        if (last <= first) last = first + 0.001;  // a step
+    }
     for (int j = 0; j < rotary_dim / 2; ++j) {
         double f = pow(base, -2.0 * j / d);
         if (scaling == SPEC_ROPE_LINEAR) f /= factor;
         if (scaling == SPEC_ROPE_YARN) {
-            double keep = (original_len * f / two_pi - slow_turns) / (fast_turns - slow_turns);
+            double keep =
+                by_index ? 1 - (j - first) / (last - first)
+                         : (original_len * f / two_pi - slow_turns) / (fast_turns - slow_turns);
             keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
             f = keep * f + (1 - keep) * f / factor;
         }

@@ -3,6 +3,7 @@ every argument check precedes the first CUDA call."""
 from __future__ import annotations
 
 import ctypes
+import math
 import subprocess
 
 import pytest
@@ -211,3 +212,48 @@ def test_attention_limits_do_not_overflow(lib):
     assert lib.spec_kv_append(vp(16), vp(16), 1, vp(16), vp(16), None, None, 1, vp(16), vp(16),
                               1 << 21, 1 << 21, 1 << 21, 32, 16, 8, 4, None) == -2
     assert "too many" in lib.spec_last_error().decode()
+
+
+@pytest.mark.parametrize("rot,theta,factor,original", [
+    (128, 10000.0, 16.0, 4096), (128, 500000.0, 4.0, 8192), (64, 1e6, 8.0, 32768), (32, 1e4, 2.0, 50)])
+def test_rope_table_ramp_by_index(lib, rot, theta, factor, original):
+    """The ramp over the pair's index: the table is the formula's in 64 bits (pow, the
+    ramp, the sum and the division by 2 pi are off by less than 2^-49 together)."""
+    from speculative_decoding_verification_attn_gb300 import binding
+    table, amp = binding.spec_rope_table(rot, theta, "yarn-index", factor, original, device="cpu")
+    assert abs(amp - (0.1 * math.log(factor) + 1)) <= 2.0 ** -24 * amp
+
+    def border(turns):
+        return rot / 2 * math.log(original / (2 * math.pi * turns)) / math.log(theta)
+    first = max(0, math.floor(border(32.0)))
+    last = max(first + 0.001, min(rot - 1, math.ceil(border(1.0))))
+    for j in range(rot // 2):
+        f = theta ** (-2 * j / rot)
+        keep = 1 - min(1.0, max(0.0, (j - first) / (last - first)))
+        want = (keep * f + (1 - keep) * f / factor) / (2 * math.pi) * 2.0 ** 64
+        assert abs(int(table[j]) - want) <= 2.0 ** -49 * want + 1
+
+
+def test_rope_table_ramp_by_index_borders(lib):
+    """rot 128, theta 10000, 4096 positions: 64 ln(4096 / 64 pi) / ln 10000 = 20.9 and
+    64 ln(4096 / 2 pi) / ln 10000 = 45.03, so pairs up to 20 are kept, pairs from 46 on
+    scaled whole and pair 33 half; the other ramp has its own values between."""
+    from speculative_decoding_verification_attn_gb300 import binding
+    plain, _ = binding.spec_rope_table(128, 10000.0, device="cpu")
+    by = {s: binding.spec_rope_table(128, 10000.0, s, 4.0, 4096, device="cpu")[0].double() /
+          plain.double() for s in ("yarn", "yarn-index")}
+    got = by["yarn-index"]
+    assert (got[:21] - 1).abs().max() < 1e-12 and got[21] < 1
+    assert (got[46:] - 0.25).abs().max() < 1e-12 and got[45] > 0.25
+    assert abs(got[33] - 0.625) < 1e-12
+    assert (by["yarn"] / got - 1).abs().max() > 0.2
+
+
+def test_rope_table_ramp_flag_needs_yarn(lib):
+    buf, amp = (ctypes.c_uint64 * 64)(), ctypes.c_float()
+    for how in (16, 17, 18, 20, 35):
+        assert lib.spec_rope_table(64, 1e4, how, 2.0, 4096.0, 32.0, 1.0, buf,
+                                   ctypes.byref(amp)) == -1
+        assert "scaling" in lib.spec_last_error().decode()
+    assert lib.spec_rope_table(64, 1e4, 19, 2.0, 4096.0, 32.0, 0.0, buf, ctypes.byref(amp)) == 0
+    assert lib.spec_rope_table(64, 1e4, 19, 2.0, 0.0, 32.0, 1.0, buf, ctypes.byref(amp)) == -1
