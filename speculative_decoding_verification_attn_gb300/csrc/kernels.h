@@ -43,11 +43,10 @@ struct AttnArgs {
 // Draft bits visible to query i of sequence b: the tree row's first k (further
 // bits name no draft: they must not count into its depth), or the causal chain.
 __host__ __device__ inline uint64_t draft_bits(const AttnArgs& a, int b, int i) {
-    const uint64_t drafts = a.k >= 64 ? ~0ull : (1ull << a.k) - 1;
 #ifdef __CUDA_ARCH__
-    if (a.tree_mask) return __ldg(a.tree_mask + (int64_t)b * a.k + i) & drafts;
+    if (a.tree_mask) return __ldg(a.tree_mask + (int64_t)b * a.k + i) & (~0ull >> (64 - a.k));
 #else
-    if (a.tree_mask) return a.tree_mask[(int64_t)b * a.k + i] & drafts;
+    if (a.tree_mask) return a.tree_mask[(int64_t)b * a.k + i] & (~0ull >> (64 - a.k));
 #endif
     return i >= 63 ? ~0ull : ((1ull << (i + 1)) - 1);
 }
