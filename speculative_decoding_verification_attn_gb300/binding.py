@@ -176,22 +176,24 @@ def spec_set_option(option: int, value: int) -> None:
     _check(load().spec_set_option(option, int(value)))
 
 
-_E4M3, _F32, _I32 = torch.float8_e4m3fn, torch.float32, torch.int32
+_E4M3, _F32, _F16 = torch.float8_e4m3fn, torch.float32, torch.float16
+_I32, _I8 = torch.int32, torch.int8
 
 
 def _check_scales(k_cache, v_cache, k_scale, v_scale) -> None:
     """The scales of an int8 cache (float16 [num_pages, Hkv, P]) or a float8_e4m3fn
     one (float32 [num_pages, Hkv]): the library takes a bare pointer and cannot
     tell."""
-    kind, pool = k_cache.dtype, k_cache.shape
-    if kind is torch.int8:
-        for s in (k_scale, v_scale):
-            if s is not None and (s.dtype is not torch.float16 or s.shape != pool[:3]):
-                raise ValueError("scales of an int8 cache must be float16 [num_pages, Hkv, P]")
-    elif kind is _E4M3:
-        for s in (k_scale, v_scale):
-            if s is not None and (s.dtype is not _F32 or s.shape != pool[:2]):
-                raise ValueError("scales of an e4m3 cache must be float32 [num_pages, Hkv]")
+    kind = k_cache.dtype
+    if kind is _E4M3:
+        dt, want, what = _F32, k_cache.shape[:2], "an e4m3 cache must be float32 [num_pages, Hkv]"
+    elif kind is _I8:
+        dt, want, what = _F16, k_cache.shape[:3], "an int8 cache must be float16 [num_pages, Hkv, P]"
+    else:
+        return
+    if (k_scale is not None and (k_scale.dtype is not dt or k_scale.shape != want)
+            or v_scale is not None and (v_scale.dtype is not dt or v_scale.shape != want)):
+        raise ValueError("scales of " + what)
 
 
 def _device_of(first) -> int:
@@ -211,28 +213,36 @@ def _ptrs(dev: int, *tensors):
     return [None if t is None else t.data_ptr() for t in tensors]
 
 
-def _reach(*tensors):
+_gpus = 0  # of this process, once known
+
+
+def _reach(tensors):
     """Pointers of dense tensors that the current device reaches: its own memory or
-    the host's, but no other GPU's (None stays None)."""
-    dev = _get_device()
+    the host's, but no other GPU's (None stays None).  With one GPU there is no
+    other, and a call's nine tensors are not asked (0.6 us of a call of 7)."""
+    global _gpus
+    if _gpus != 1:
+        _gpus = _gpus or torch.cuda.device_count()
+        here = (_get_device(), -1)  # (-1: host memory)
+        for t in tensors:
+            if t is not None and t.get_device() not in here:
+                raise ValueError("tensors must not lie on another GPU than the current device")
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_contiguous():
+        if t is not None and not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        if t.get_device() not in (dev, -1):  # (-1: host memory)
-            raise ValueError("tensors must not lie on another GPU than the current CUDA device")
     return [None if t is None else t.data_ptr() for t in tensors]
 
 
-def _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale) -> None:
+def _check_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse) -> None:
     """What the library cannot see behind the pointers of an attention call."""
-    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+    kind, dt = k_cache.dtype, q.dtype
+    if v_cache.dtype is not kind or v_cache.numel() != k_cache.numel():
         raise ValueError("k_cache and v_cache must share a dtype and a shape")
-    _check_scales(k_cache, v_cache, k_scale, v_scale)
+    if kind is not dt:  # (scales come with a cache of codes)
+        _check_scales(k_cache, v_cache, k_scale, v_scale)
     if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
         raise ValueError("block_table and ctx_lens must be int32")
-    if out.dtype is not q.dtype or out.numel() < q.numel():
+    if out.dtype is not dt or out.numel() < q.numel():
         raise ValueError("out must have q's dtype and size")
     if lse is not None and lse.dtype is not _F32:
         raise ValueError("lse must be float32")
@@ -257,9 +267,9 @@ def spec_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, num_draft: int,
     NP, Hkv, P, D2 = k_cache.shape
     if k != num_draft or D2 != D:
         raise ValueError("shape mismatch between q, num_draft and the cache")
-    _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale)
-    qp, kp, vp, ksp, vsp, tp, cp, op, lp = _reach(q, k_cache, v_cache, k_scale, v_scale,
-                                                  block_table, ctx_lens, out, lse)
+    tensors = (q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse)
+    _check_attn(*tensors)
+    qp, kp, vp, ksp, vsp, tp, cp, op, lp = _reach(tensors)
     _check(load().spec_verify_attn(
         qp, kp, vp, ksp, vsp, tp, cp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
@@ -296,13 +306,13 @@ def spec_verify_attn_tree(q, k_cache, v_cache, block_table, ctx_lens, tree_mask,
     bit t of row i: query i sees draft t; int64 or uint64 tensor)."""
     B, k, Hq, D = q.shape
     NP, Hkv, P, D2 = k_cache.shape
-    if k != num_draft or D2 != D or tuple(tree_mask.shape) != (B, k):
+    if k != num_draft or D2 != D or tree_mask.shape != (B, k):
         raise ValueError("q must be [B, num_draft, Hq, D], tree_mask [B, num_draft]")
     if tree_mask.element_size() != 8:
         raise ValueError("tree_mask must hold 64-bit words")
-    _check_attn(q, k_cache, v_cache, block_table, ctx_lens, out, lse, k_scale, v_scale)
-    qp, kp, vp, ksp, vsp, tp, cp, mp, op, lp = _reach(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, tree_mask, out, lse)
+    tensors = (q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse)
+    _check_attn(*tensors)
+    qp, kp, vp, ksp, vsp, tp, cp, op, lp, mp = _reach(tensors + (tree_mask,))
     _check(load().spec_verify_attn_tree(
         qp, kp, vp, ksp, vsp, tp, cp, mp, B, k, Hq, Hkv, D, P, NP, block_table.shape[1],
         _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp, _stream(stream)))
@@ -416,13 +426,13 @@ def spec_kv_append(k_new, v_new, k_cache, v_cache, block_table, ctx_lens, k_scal
         raise ValueError("k_new / v_new must be [B, n, Hkv, D] matching the cache")
     if v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new must share a dtype")
-    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+    if v_cache.dtype is not k_cache.dtype or v_cache.numel() != k_cache.numel():
         raise ValueError("k_cache and v_cache must share a dtype and a shape")
     if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
         raise ValueError("block_table and ctx_lens must be int32")
     _check_scales(k_cache, v_cache, k_scale, v_scale)
-    kp, vp, kcp, vcp, ksp, vsp, tp, cp = _reach(k_new, v_new, k_cache, v_cache, k_scale, v_scale,
-                                                block_table, ctx_lens)
+    kp, vp, kcp, vcp, ksp, vsp, tp, cp = _reach(
+        (k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens))
     _check(load().spec_kv_append(kp, vp, _TORCH_DT[k_new.dtype], kcp, vcp, ksp, vsp,
                                  _TORCH_DT[k_cache.dtype], tp, cp, B, n, Hkv, D, P, NP,
                                  block_table.shape[1], _stream(stream)))

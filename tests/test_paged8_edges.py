@@ -175,10 +175,12 @@ def test_binding_refuses_memory_of_another_device(lib, call, monkeypatch):
     before its pointer reaches them."""
     from speculative_decoding_verification_attn_gb300 import binding
     monkeypatch.setattr(binding, "_get_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(binding, "_gpus", 0)
     t = paged_tensors("bf16")
     for name in ("table", "ctx", "v_new" if call == "append" else "out"):
         where = t["rows"] if name == "v_new" else t["q"] if name == "out" else t[name]
-        with pytest.raises(ValueError, match="current CUDA device"):
+        with pytest.raises(ValueError, match="current device"):
             paged_call(binding, call, t, **{name: Elsewhere(where)})
 
 
