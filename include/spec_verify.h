@@ -167,10 +167,15 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  * (max_pages_per_seq * page_size of them) fit the single-pass kernel's
  * shared memory (not an E4M3 cache's), else on the chunked split-KV kernel
  * and its combine.
- * K and V are finite at every key below ctx_b + num_draft, seen or not: a
- * weight of zero does not stop an infinity.  On the E4M3 tensor-core kernel
- * page scales of V up to 1e-30 count as zero, and those of one sequence should
- * lie within 2^80 of each other.
+ * q is finite (on the E4M3 tensor-core kernel an infinity would count as a
+ * large number), and K and V are at every key below ctx_b + num_draft, seen or
+ * not: a weight of zero does not stop an infinity.
+ * The tensor-core kernels hold scores, sums and outputs in fp32 and a weight p
+ * in 8 significant bits.  The E4M3 one also takes q to 2^-18 of its row's
+ * largest element (exact above 2^-10 of it) and fewer than 8 bits of a weight
+ * below 2^-10 of the largest among its 32 keys; page scales of V up to 1e-30
+ * count as zero there, and those of one sequence should lie within 2^80 of each
+ * other.  SPEC_OPT_ATTN_PATH 1 computes in fp32 throughout.
  */
 SPEC_API int spec_verify_attn(const void *q, const void *k_cache, const void *v_cache,
                      const void *k_scale, const void *v_scale,

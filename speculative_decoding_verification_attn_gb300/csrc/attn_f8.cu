@@ -321,8 +321,11 @@ attn_f8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__
         fence_mbar_init();
     }
     {
-        // q rows that no piece writes stay zero; the scale bytes of V, and of
-        // P blocks that no lane of a row writes, are 1.0
+        // q rows that no piece writes are zero at first; the scale bytes of V, and
+        // of P blocks that no lane of a row writes, are 1.0.  (The epilogue's
+        // scratch lies over the q rows, so from a CTA's third piece on rows >= R
+        // hold any bytes.  A row of the MMAs reads no other, the softmax takes
+        // such a lane's scores times 2^-126, and nothing of it is stored.)
         uint4* q4 = reinterpret_cast<uint4*>(sm + Smem::Q);
         for (int e = tid; e < 4 * Q_PART / 16; e += THREADS)
             if ((e % (Q_PART / 16)) / 8 % COPY >= R) q4[e] = make_uint4(0, 0, 0, 0);

@@ -33,7 +33,7 @@ struct AttnArgs {
     int32_t split_alpha = -1;
     // sliding window (0 = none): a key before the drafts is visible to query i
     // when it is one of the first `sinks` or lies less than `window` positions
-    // before the query (see row_low)
+    // before the query (see window_low)
     int32_t window = 0, sinks = 0;
     // e4m3 cache: fp32 scales per (page, kv-head), [num_pages, Hkv]
     const float* k_page_scale = nullptr;
@@ -132,7 +132,9 @@ cudaError_t launch_combine_stream_k(const AttnArgs& a, int num_ctas, int alpha,
 bool tc2_supported(const AttnArgs& a);
 cudaError_t launch_attn_tc2(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);
 
-// Most units that a segment's keys can fill, by the block table and the window.
+// Most units that a segment's keys can fill, by the block table's width and the
+// window: the host does not know the lengths, so a call without a window of short
+// sequences in a wide table counts as one of long segments.
 inline int64_t max_units(const AttnArgs& a, int unit) {
     const int64_t all = ((int64_t)a.max_pages * a.P + unit - 1) / unit;
     if (a.window <= 0) return all;
