@@ -33,9 +33,9 @@
 // widening pass, and the softmax below a tile's time on every SMSP.
 //
 // Measured (one call among others, combine included; the bytes' floor at 6768
-// GB/s): 32 sequences of 1 to 8K keys, 32/8 heads, 4 drafts 62.7 us (4.87 TB/s,
-// floor 45.1); 32 x 2048 keys, 64/8 heads, 8 drafts 45 us (21.2); 4 x 32K keys,
-// 28/4 heads, 16-node trees 50 us (20.0).  A tile takes ~1500, ~1700 and ~2600
+// GB/s): 32 sequences of 1 to 8K keys, 32/8 heads, 4 drafts 63 to 65 us (4.85 to
+// 4.69 TB/s, floor 45.1); 32 x 2048 keys, 64/8 heads, 8 drafts 45 us (21.2); 4 x 32K
+// keys, 28/4 heads, 16-node trees 51 us (20.0).  A tile takes ~1500, ~1700 and ~2600
 // cycles there (16, 64 and 112 rows): the softmax of the rows is what is left
 // above the HBM share, of which half is its arithmetic (the exponentials and
 // the conversions to e4m3 share one pipe, 4 cycles per warp instruction each:
