@@ -157,8 +157,8 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  * Limits: 1 <= num_draft <= 64; num_q_heads % num_kv_heads == 0;
  * head_dim % 32 == 0 and head_dim <= 256; page_size >= 1;
  * max_pages_per_seq * page_size >= num_draft (the drafts' keys have a place);
- * q, caches and out 16-byte aligned.  A bf16 query over a bf16 cache with head_dim 128, a
- * power-of-two page_size in [16, 256] and batch <= 1024 runs on a
+ * q, caches and out 16-byte aligned.
+ * A bf16 query over a bf16 cache with head_dim 128, a power-of-two page_size in [16, 256] and batch <= 1024 runs on a
  * tensor-core kernel: the warp-MMA kernel when num_draft * (num_q_heads /
  * num_kv_heads) <= 16, the tcgen05 kernel up to 128.  An E4M3 cache runs on a
  * tcgen05 kernel of its own at the same shapes (up to 128 rows, num_pages *
@@ -171,7 +171,7 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  * large number), and K and V are at every key below ctx_b + num_draft, seen or
  * not: a weight of zero does not stop an infinity.
  * The tensor-core kernels hold scores, sums and outputs in fp32 and a weight p
- * in 8 significant bits.  The E4M3 one also takes q to 2^-18 of its row's
+ * in 8 significant bits (over an I8 cache in fp16).  The E4M3 one also takes q to 2^-18 of its row's
  * largest element (exact above 2^-10 of it) and fewer than 8 bits of a weight
  * below 2^-10 of the largest among its 32 keys; page scales of V up to 1e-30
  * count as zero there, and those of one sequence should lie within 2^80 of each
@@ -268,9 +268,9 @@ SPEC_API int spec_verify_attn_tree(const void *q, const void *k_cache, const voi
  * sequence b sees key j only if
  *   j < num_sinks   or   pos_i - j < window,
  * where pos_i = ctx_b + i, or with a tree ctx_b + (node i's ancestors: the
- * set bits of its mask below num_draft, less one), is the query's position.  The query itself
- * counts, so window 1 leaves a query its own key and the sinks.  Keys that no
- * query of a sequence sees are not read (whole pages of them may have left
+ * set bits of its mask below num_draft, less one), is the query's position.
+ * The query itself counts, so window 1 leaves a query its own key and the
+ * sinks.  Keys that no query of a sequence sees are not read (whole pages of them may have left
  * the pool: their block_table entries are not looked at).
  * Limits: window >= 1 (>= num_draft with a tree), num_sinks >= 0; else as
  * spec_verify_attn.
