@@ -158,24 +158,25 @@ SPEC_API int spec_set_option(int32_t option, int64_t value);
  * head_dim % 32 == 0 and head_dim <= 256; page_size >= 1;
  * max_pages_per_seq * page_size >= num_draft (the drafts' keys have a place);
  * q, caches and out 16-byte aligned.
- * A bf16 query over a bf16 cache with head_dim 128, a power-of-two page_size in [16, 256] and batch <= 1024 runs on a
- * tensor-core kernel: the warp-MMA kernel when num_draft * (num_q_heads /
- * num_kv_heads) <= 16, the tcgen05 kernel up to 128.  An E4M3 cache runs on a
- * tcgen05 kernel of its own at the same shapes (up to 128 rows, num_pages *
- * num_kv_heads * page_size < 2^31).  Every other accepted
- * shape runs on the CUDA cores: in one launch when every sequence's keys
- * (max_pages_per_seq * page_size of them) fit the single-pass kernel's
- * shared memory (not an E4M3 cache's), else on the chunked split-KV kernel
- * and its combine.
+ * A bf16 query over a bf16 cache with head_dim 128, a power-of-two page_size
+ * in [16, 256] and batch <= 1024 runs on a tensor-core kernel: the warp-MMA
+ * kernel when num_draft * (num_q_heads / num_kv_heads) <= 16, the tcgen05
+ * kernel up to 128.  An E4M3 cache runs on a tcgen05 kernel of its own at the
+ * same shapes (up to 128 rows, num_pages * num_kv_heads * page_size < 2^31).
+ * Every other accepted shape runs on the CUDA cores: in one launch when every
+ * sequence's keys (max_pages_per_seq * page_size of them) fit the single-pass
+ * kernel's shared memory (not an E4M3 cache's), else on the chunked split-KV
+ * kernel and its combine.
  * q is finite (on the E4M3 tensor-core kernel an infinity would count as a
  * large number), and K and V are at every key below ctx_b + num_draft, seen or
  * not: a weight of zero does not stop an infinity.
- * The tensor-core kernels hold scores, sums and outputs in fp32 and a weight p
- * in 8 significant bits (over an I8 cache in fp16).  The E4M3 one also takes q to 2^-18 of its row's
- * largest element (exact above 2^-10 of it) and fewer than 8 bits of a weight
- * below 2^-10 of the largest among its 32 keys; page scales of V up to 1e-30
- * count as zero there, and those of one sequence should lie within 2^80 of each
- * other.  SPEC_OPT_ATTN_PATH 1 computes in fp32 throughout.
+ * The tensor-core kernels hold scores, sums and outputs in fp32 and a weight
+ * p in 8 significant bits (over an I8 cache in fp16).  The E4M3 one also
+ * takes q to 2^-18 of its row's largest element (exact above 2^-10 of it) and
+ * fewer than 8 bits of a weight below 2^-10 of the largest among its 32 keys;
+ * page scales of V up to 1e-30 count as zero there, and those of one sequence
+ * should lie within 2^80 of each other.  SPEC_OPT_ATTN_PATH 1 computes in
+ * fp32 throughout.
  */
 SPEC_API int spec_verify_attn(const void *q, const void *k_cache, const void *v_cache,
                      const void *k_scale, const void *v_scale,
@@ -270,8 +271,8 @@ SPEC_API int spec_verify_attn_tree(const void *q, const void *k_cache, const voi
  * where pos_i = ctx_b + i, or with a tree ctx_b + (node i's ancestors: the
  * set bits of its mask below num_draft, less one), is the query's position.
  * The query itself counts, so window 1 leaves a query its own key and the
- * sinks.  Keys that no query of a sequence sees are not read (whole pages of them may have left
- * the pool: their block_table entries are not looked at).
+ * sinks.  Keys that no query of a sequence sees are not read (whole pages of
+ * them may have left the pool: their block_table entries are not looked at).
  * Limits: window >= 1 (>= num_draft with a tree), num_sinks >= 0; else as
  * spec_verify_attn.
  */
