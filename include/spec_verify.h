@@ -287,6 +287,42 @@ SPEC_API int spec_verify_attn_window(const void *q, const void *k_cache, const v
                                      float *lse, void *stream);
 
 /*
+ * Verification attention of sequences that share prefixes (several
+ * continuations of one prompt, verified side by side).  Same arguments and
+ * results as spec_verify_attn (tree_mask NULL) or spec_verify_attn_tree; the
+ * groups say which pages several sequences hold, and a prefix is read and
+ * multiplied once for all of its group's queries.
+ *
+ *   group_starts [num_groups + 1] int32, ascending: group g is the sequences
+ *                group_starts[g] .. group_starts[g + 1] - 1 (sequences outside
+ *                [group_starts[0], group_starts[num_groups]) share nothing)
+ *   shared_lens  [num_groups] int32: keys 0 .. shared_lens[g] - 1 of all the
+ *                group's sequences lie in the same pages: their block_table
+ *                rows agree in the entries that hold them, and any one of the
+ *                rows may be read for them
+ * Groups are a promise about the tables, not a mask: every query sees what it
+ * sees in spec_verify_attn.  A start outside [the one before it, batch] (the
+ * group is taken as empty) sets SPEC_DEVERR_GROUP; so does a shared length below 0
+ * or above the shortest context of the group, and it is clamped.  A part of a
+ * shared length that does not fill a page is read sequence by sequence.
+ * Limits: num_groups >= 0; else as spec_verify_attn.  A BF16 query with head_dim
+ * 128 and a BF16, I8 or E4M3 cache of power-of-two pages in [16, 256], up to 128
+ * query rows per kv-head and about 1000 sequences and blocks of 256 query rows
+ * runs on a tensor-core kernel of its own, which rounds as the BF16 one of
+ * spec_verify_attn does (codes are exact in its MMAs, scales fp32); every other
+ * accepted shape runs as spec_verify_attn.
+ */
+SPEC_API int spec_verify_attn_shared(const void *q, const void *k_cache, const void *v_cache,
+                                     const void *k_scale, const void *v_scale,
+                                     const int32_t *block_table, const int32_t *ctx_lens,
+                                     const uint64_t *tree_mask, const int32_t *group_starts,
+                                     const int32_t *shared_lens, int32_t num_groups, int32_t batch,
+                                     int32_t num_draft, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t page_size, int32_t num_pages,
+                                     int32_t max_pages_per_seq, int32_t q_dtype, int32_t kv_dtype,
+                                     float scale, void *out, float *lse, void *stream);
+
+/*
  * Greedy acceptance over a tree of drafts.  Node i of sequence b carries
  * draft_tokens[b, i] and parents[b, i] in [-1, i) (-1: a child of the last
  * committed token); logits row 0 is the target's prediction at the root and
@@ -555,6 +591,115 @@ SPEC_API int spec_kv_gather(const void *k_cache, const void *v_cache, const void
 SPEC_API int spec_commit(int32_t *ctx_lens, const int32_t *accepted_len, int32_t batch,
                          int32_t extra, void *stream);
 
+/*
+ * Keep the accepted path of a token tree: the row of node path[b, i] (cache
+ * position ctx_b + path[b, i]) moves to position ctx_b + i for i <
+ * accepted_len[b], in K and V, for every kv-head.  spec_commit alone is right
+ * for a chain; after a tree's acceptance this call comes before it (rotary
+ * positions already are those of the depth).
+ *
+ *   path          [batch, num_draft] int32, spec_accept_tree's: i <= path[b, i]
+ *                 < num_draft for i < accepted_len[b]; else the row stays as it
+ *                 was and SPEC_DEVERR_TREE is set
+ *   accepted_len  [batch] int32 (clamped to [0, num_draft])
+ *   - F32 / BF16 cache: the row's bits; I8: its codes and its scale;
+ *   - E4M3 cache: the code where the row stays in its page, otherwise (in fp32,
+ *     IEEE division, to nearest even, saturating) e4m3((c * s_from) / s'), with
+ *     s' = max(s, |c * s_from| / 448 of the rows that come into the page), and
+ *     where s' > s every row of the page below ctx_b + num_draft becomes
+ *     e4m3((c * s) / s').
+ * A position outside the block table or a page id outside [0, num_pages) moves
+ * nothing and sets SPEC_DEVERR_CTX / SPEC_DEVERR_PAGE.  The pages that hold
+ * drafts belong to one sequence.  Caches, scales and tables as in
+ * spec_kv_append; ctx_lens is not changed.
+ * Limits: 1 <= num_draft <= 64; head_dim % 32 == 0 and <= 256; batch <= 65535;
+ * caches 16-byte aligned.
+ */
+SPEC_API int spec_kv_compact(void *k_cache, void *v_cache, void *k_scale, void *v_scale,
+                             int32_t cache_dtype, const int32_t *block_table,
+                             const int32_t *ctx_lens, const int32_t *path,
+                             const int32_t *accepted_len, int32_t batch, int32_t num_draft,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                             int32_t num_pages, int32_t max_pages_per_seq, void *stream);
+
+/*
+ * Pages that several rows of a block table hold.  A row lists its pages, then
+ * negative entries; page_refs [num_pages] int32 counts the rows that hold a
+ * page, 0 for a free one.  Both, and ctx_lens [num_rows], live on the device, so
+ * that a captured step may fork and release.
+ *
+ * spec_kv_fork: for pair j, row children[j] becomes a continuation of row
+ * parents[j] with pages for ctx + room tokens (ctx the parent's context):
+ *   - whole pages of the context are shared: page_refs + 1;
+ *   - a page in use (ctx % page_size rows) is copied to a fresh page, those
+ *     rows and their scales only (the page's, for E4M3); other slots stay as they were;
+ *   - pages up to ceil((ctx + room) / page_size) are fresh;
+ *   - entries behind them become -1 and ctx_lens[child] = ctx.
+ * With children[j] == parents[j] the row itself gets the room: it keeps the
+ * pages behind its whole ones that no other row holds and gets fresh ones for those it
+ * lacks or shares (page_refs - 1 of these; the page in use is copied first).
+ * A fresh page is a page that was free before the call, the lowest ids first,
+ * pair by pair in order, place by place; page_refs = 1.
+ * A pair is skipped, its child as it was:
+ *   - SPEC_DEVERR_POOL: a row outside [0, num_rows); a child that holds pages
+ *     (release it first), is the child of an earlier pair or the parent of
+ *     another one (unless it is its own parent); or fewer free pages than this
+ *     pair and those before it need;
+ *   - SPEC_DEVERR_CTX: ctx < 0 or ctx + room beyond the block table;
+ *   - SPEC_DEVERR_PAGE: a page id outside [0, num_pages) among the parent's.
+ *
+ * spec_kv_release: row rows[j] keeps its first keep_lens[j] tokens (NULL: 0):
+ * ctx_lens = min(ctx_lens, keep), and of every page behind ceil(keep /
+ * page_size) the entry becomes -1 and page_refs falls by 1.  A row may be listed
+ * more than once.  A row outside [0, num_rows), or a page that nobody held, sets
+ * SPEC_DEVERR_POOL; a page id >= num_pages SPEC_DEVERR_PAGE.
+ *
+ * Limits: num_pairs, num >= 0; room >= 0; num_rows >= 1; else as spec_kv_append,
+ * caches 16-byte aligned; num_pairs < 2^24.
+ */
+SPEC_API int spec_kv_fork(void *k_cache, void *v_cache, void *k_scale, void *v_scale,
+                          int32_t cache_dtype, int32_t *block_table, int32_t *ctx_lens,
+                          int32_t *page_refs, const int32_t *parents, const int32_t *children,
+                          int32_t num_pairs, int32_t room, int32_t num_rows, int32_t num_kv_heads,
+                          int32_t head_dim, int32_t page_size, int32_t num_pages,
+                          int32_t max_pages_per_seq, void *stream);
+SPEC_API int spec_kv_release(int32_t *block_table, int32_t *ctx_lens, int32_t *page_refs,
+                             const int32_t *rows, const int32_t *keep_lens, int32_t num,
+                             int32_t num_rows, int32_t page_size, int32_t num_pages,
+                             int32_t max_pages_per_seq, void *stream);
+
+/*
+ * Log probabilities of given tokens, with the entropy of their rows and the top
+ * alternatives (what a serving API reports of its tokens, and what ranks
+ * several continuations).  With z = logits / temperature and lse = ln sum exp z
+ * of a row:
+ *   logprob  = z[token] - lse,   entropy = -sum p ln p,  p = exp(z - lse),
+ *   top_ids / top_logprobs = the num_top tokens of largest logit, largest
+ *   first, the lower id first among equals (values compare as stored, -0 == +0).
+ *
+ *   logits        [batch, num_rows, vocab]  logits_dtype (F32 | BF16), finite or
+ *                 -inf (a masked token: p = 0, never an alternative).  A row with a NaN
+ *                 or +inf gives NaN and undefined alternatives; a row of -inf
+ *                 alone gives logprob -inf and entropy 0
+ *   tokens        [batch, num_rows] int32; one outside [0, vocab) gives -inf and
+ *                 sets SPEC_DEVERR_TOKEN
+ *   lens          [batch] int32 rows of each sequence (accepted_len + 1, say; any
+ *                 value counts as within [0, num_rows]), or NULL: num_rows; other
+ *                 rows are not read and their results stay as they were
+ *   logprob       [batch, num_rows] fp32
+ *   entropy       [batch, num_rows] fp32, or NULL
+ *   top_ids       [batch, num_rows, num_top] int32, or NULL
+ *   top_logprobs  [batch, num_rows, num_top] fp32, or NULL; where a row has fewer
+ *                 unmasked tokens, -1 and -inf follow
+ * Limits: num_rows >= 1; 1 <= vocab < 2^31 - 2^16; 0 <= num_top <= 32; temperature
+ * > 0 and finite, and not below 1e-30; logits 16-byte aligned; batch * num_rows < 2^26.
+ */
+SPEC_API int spec_token_logprobs(const void *logits, int32_t logits_dtype, const int32_t *tokens,
+                                 const int32_t *lens, int32_t batch, int32_t num_rows,
+                                 int64_t vocab, float temperature, int32_t num_top, float *logprob,
+                                 float *entropy, int32_t *top_ids, float *top_logprobs,
+                                 void *stream);
+
 /* Read and clear the device error word of the current device (synchronises
  * the device).  0 = no fault seen; otherwise a bitwise OR of SPEC_DEVERR_*. */
 SPEC_API int spec_device_error(int32_t *flags);
@@ -565,7 +710,9 @@ enum {
     SPEC_DEVERR_TIMEOUT = 4, /* a bounded on-chip wait gave up; results invalid */
     SPEC_DEVERR_TOKEN = 8,   /* a draft token outside [0, vocab) (treated as rejected) */
     SPEC_DEVERR_TREE = 16,   /* a tree parent outside [-1, i) (the node is never taken) */
-    SPEC_DEVERR_CODEC = 32   /* a malformed coded block (decoded as zeros) */
+    SPEC_DEVERR_CODEC = 32,  /* a malformed coded block (decoded as zeros) */
+    SPEC_DEVERR_POOL = 64,   /* a row that cannot be forked or released (skipped), or no free pages */
+    SPEC_DEVERR_GROUP = 128  /* a group's start or shared length out of range (clamped) */
 };
 
 /* Free the current device's workspace (synchronises the device). */

@@ -27,6 +27,8 @@ NUM_OPTIONS = 6
 SPEC_DEVERR_PAGE, SPEC_DEVERR_CTX, SPEC_DEVERR_TIMEOUT, SPEC_DEVERR_TOKEN = 1, 2, 4, 8
 SPEC_DEVERR_TREE = 16
 SPEC_DEVERR_CODEC = 32
+SPEC_DEVERR_POOL = 64
+SPEC_DEVERR_GROUP = 128
 SPEC_ROPE_PLAIN, SPEC_ROPE_LINEAR, SPEC_ROPE_NTK, SPEC_ROPE_YARN = 0, 1, 2, 3
 SPEC_ROPE_RAMP_BY_INDEX = 16
 
@@ -36,6 +38,8 @@ EXPORTED = ["spec_version", "spec_last_error", "spec_set_option", "spec_verify_a
             "spec_accept_greedy_noalloc", "spec_accept_rejection",
             "spec_kv_append", "spec_commit", "spec_verify_attn_tree", "spec_accept_tree",
             "spec_verify_attn_window", "spec_rope_append", "spec_rope_table", "spec_kv_gather",
+            "spec_verify_attn_shared", "spec_kv_fork", "spec_kv_release", "spec_kv_compact",
+            "spec_token_logprobs",
             "spec_codec_encode", "spec_codec_decode", "spec_device_error", "spec_release"]
 SPEC_NOALLOC_MAX_PARTIALS, SPEC_NOALLOC_MAX_BATCH = 65536, 4096
 
@@ -124,6 +128,17 @@ def _open(path: str):
     lib.spec_rope_table.restype = ctypes.c_int
     lib.spec_kv_gather.argtypes = [P, P, P, P, i32, P, P, P] + [i32] * 8 + [P, P, P]
     lib.spec_kv_gather.restype = ctypes.c_int
+    lib.spec_verify_attn_shared.argtypes = [P] * 10 + [i32] * 11 + [ctypes.c_float, P, P, P]
+    lib.spec_verify_attn_shared.restype = ctypes.c_int
+    lib.spec_kv_fork.argtypes = [P] * 4 + [i32] + [P] * 5 + [i32] * 8 + [P]
+    lib.spec_kv_fork.restype = ctypes.c_int
+    lib.spec_kv_release.argtypes = [P] * 5 + [i32] * 5 + [P]
+    lib.spec_kv_release.restype = ctypes.c_int
+    lib.spec_kv_compact.argtypes = [P] * 4 + [i32] + [P] * 4 + [i32] * 7 + [P]
+    lib.spec_kv_compact.restype = ctypes.c_int
+    lib.spec_token_logprobs.argtypes = [P, i32, P, P, i32, i32, i64, ctypes.c_float, i32, P, P, P,
+                                        P, P]
+    lib.spec_token_logprobs.restype = ctypes.c_int
     lib.spec_accept_tree.argtypes = [P, i32, P, P, i32, i32, i64, P, P, P, P]
     lib.spec_accept_tree.restype = ctypes.c_int
     T = ctypes.POINTER(SpecTensor)
@@ -354,6 +369,45 @@ def spec_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, num_draf
         op, lp, _stream_on(stream, dev)))
 
 
+def spec_verify_attn_shared(q, k_cache, v_cache, block_table, ctx_lens, group_starts, shared_lens,
+                            num_draft: int, scale: float, out, lse=None, k_scale=None, v_scale=None,
+                            tree_mask=None, stream=None) -> None:
+    """spec_verify_attn (or, with ``tree_mask``, spec_verify_attn_tree) for groups of
+    sequences that share a prefix, read and multiplied once for the group.
+
+    Group g is sequences group_starts[g] .. group_starts[g + 1] - 1 (int32
+    [groups + 1]), whose first shared_lens[g] keys (int32 [groups]) lie in the
+    same pages: their rows of ``block_table`` agree there.
+    """
+    B, k, Hq, D = q.shape
+    NP, Hkv, P, D2 = k_cache.shape
+    if k != num_draft or D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between q, num_draft and the caches")
+    if v_cache.dtype != k_cache.dtype or out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("v_cache must have k_cache's dtype, out q's dtype and shape")
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
+        raise ValueError("block_table and ctx_lens must be int32")
+    if block_table.shape[0] != B or ctx_lens.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and ctx_lens [B]")
+    groups = shared_lens.shape[0]
+    if (group_starts.dtype is not _I32 or shared_lens.dtype is not _I32
+            or group_starts.shape != (groups + 1,) or shared_lens.shape != (groups,)):
+        raise ValueError("group_starts must be int32 [groups + 1], shared_lens int32 [groups]")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (B, k, Hq)):
+        raise ValueError("lse must be float32 [B, k, Hq]")
+    if tree_mask is not None and (tree_mask.shape != (B, k) or tree_mask.element_size() != 8):
+        raise ValueError("tree_mask must hold 64-bit words [B, num_draft]")
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
+    dev = _device_of(q)
+    qp, kp, vp, ksp, vsp, tp, cp, mp, gp, sp, op, lp = _ptrs(
+        dev, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, tree_mask, group_starts,
+        shared_lens, out, lse)
+    _check(load().spec_verify_attn_shared(
+        qp, kp, vp, ksp, vsp, tp, cp, mp, gp, sp, groups, B, k, Hq, Hkv, D, P, NP,
+        block_table.shape[1], _TORCH_DT[q.dtype], _TORCH_DT[k_cache.dtype], float(scale), op, lp,
+        _stream_on(stream, dev)))
+
+
 def spec_accept_tree(logits, draft_tokens, parents, num_draft: int, accepted_len, next_token,
                      path=None, stream=None) -> None:
     """Greedy acceptance over a tree of drafts (parents int32 [B, k] in [-1, i))."""
@@ -561,6 +615,112 @@ def spec_kv_gather(k_cache, v_cache, block_table, lens, k_out, v_out, starts=Non
     _check(load().spec_kv_gather(
         kp, vp, ksp, vsp, _TORCH_DT[k_cache.dtype], tp, sp, lp, B, n, Hkv, D, P, NP,
         block_table.shape[1], _TORCH_DT[k_out.dtype], kop, vop, _stream_on(stream, dev)))
+
+
+def _check_pool(k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens) -> None:
+    """Caches, scales and tables of a call that moves cached rows."""
+    if v_cache.dtype is not k_cache.dtype or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share a dtype and a shape")
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32:
+        raise ValueError("block_table and ctx_lens must be int32")
+    if block_table.dim() != 2 or ctx_lens.shape != (block_table.shape[0],):
+        raise ValueError("block_table must be [rows, max_pages] and ctx_lens [rows]")
+    _check_scales(k_cache, v_cache, k_scale, v_scale)
+
+
+def spec_kv_compact(k_cache, v_cache, block_table, ctx_lens, path, accepted_len, k_scale=None,
+                    v_scale=None, stream=None) -> None:
+    """Move the cached rows of a tree's accepted nodes to the front: position ctx_b
+    + path[b, i] to ctx_b + i for i < accepted_len[b] (``path`` int32 [B, k] as
+    spec_accept_tree writes it)."""
+    NP, Hkv, P, D = k_cache.shape
+    _check_pool(k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens)
+    B = block_table.shape[0]
+    if path.dtype is not _I32 or path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be int32 [B, num_draft]")
+    if accepted_len.dtype is not _I32 or accepted_len.shape != (B,):
+        raise ValueError("accepted_len must be int32 [B]")
+    dev = _device_of(k_cache)
+    kp, vp, ksp, vsp, tp, cp, pp, ap = _ptrs(dev, k_cache, v_cache, k_scale, v_scale, block_table,
+                                             ctx_lens, path, accepted_len)
+    _check(load().spec_kv_compact(kp, vp, ksp, vsp, _TORCH_DT[k_cache.dtype], tp, cp, pp, ap, B,
+                                  path.shape[1], Hkv, D, P, NP, block_table.shape[1],
+                                  _stream_on(stream, dev)))
+
+
+def spec_kv_fork(k_cache, v_cache, block_table, ctx_lens, page_refs, parents, children, room: int = 0,
+                 k_scale=None, v_scale=None, stream=None) -> None:
+    """Make row children[j] of ``block_table`` [rows, max_pages] a continuation of
+    row parents[j]: whole pages shared, the page in use copied, fresh pages for
+    ``room`` more tokens.  A child that is its own parent gets the room and sole
+    pages to write in.  ``page_refs`` int32 [num_pages] counts holders."""
+    NP, Hkv, P, D = k_cache.shape
+    _check_pool(k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens)
+    if page_refs.dtype is not _I32 or page_refs.shape != (NP,):
+        raise ValueError("page_refs must be int32 [num_pages]")
+    if (parents.dtype is not _I32 or children.dtype is not _I32 or parents.dim() != 1
+            or children.shape != parents.shape):
+        raise ValueError("parents and children must be int32 [pairs]")
+    dev = _device_of(k_cache)
+    kp, vp, ksp, vsp, tp, cp, rp, pp, chp = _ptrs(dev, k_cache, v_cache, k_scale, v_scale,
+                                                  block_table, ctx_lens, page_refs, parents,
+                                                  children)
+    _check(load().spec_kv_fork(kp, vp, ksp, vsp, _TORCH_DT[k_cache.dtype], tp, cp, rp, pp, chp,
+                               parents.shape[0], _span(room), block_table.shape[0], Hkv, D, P, NP,
+                               block_table.shape[1], _stream_on(stream, dev)))
+
+
+def spec_kv_release(block_table, ctx_lens, page_refs, rows, page_size: int, keep_lens=None,
+                    stream=None) -> None:
+    """Let ``rows`` (int32) of ``block_table`` drop their pages behind the first
+    keep_lens[j] tokens (None: all of them)."""
+    if block_table.dtype is not _I32 or ctx_lens.dtype is not _I32 or page_refs.dtype is not _I32:
+        raise ValueError("block_table, ctx_lens and page_refs must be int32")
+    if (block_table.dim() != 2 or ctx_lens.shape != (block_table.shape[0],)
+            or page_refs.dim() != 1):
+        raise ValueError("block_table must be [rows, max_pages], ctx_lens [rows], page_refs "
+                         "[num_pages]")
+    if rows.dtype is not _I32 or rows.dim() != 1:
+        raise ValueError("rows must be a row of int32")
+    if keep_lens is not None and (keep_lens.dtype is not _I32 or keep_lens.shape != rows.shape):
+        raise ValueError("keep_lens must be int32, one for each row")
+    dev = _device_of(block_table)
+    tp, cp, rp, wp, lp = _ptrs(dev, block_table, ctx_lens, page_refs, rows, keep_lens)
+    _check(load().spec_kv_release(tp, cp, rp, wp, lp, rows.shape[0], block_table.shape[0],
+                                  int(page_size), page_refs.shape[0], block_table.shape[1],
+                                  _stream_on(stream, dev)))
+
+
+def spec_token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None,
+                        lens=None, temperature: float = 1.0, stream=None) -> None:
+    """Log probabilities of ``tokens`` int32 [B, n] under softmax(logits /
+    temperature), logits [B, n, V] (float32 or bfloat16), into ``logprob``
+    [B, n]; the rows' ``entropy`` [B, n] and the alternatives of largest logit
+    into ``top_ids`` (int32) / ``top_logprobs`` [B, n, K], if given.  ``lens``
+    int32 [B] limits each sequence's rows (accepted_len + 1, say)."""
+    B, n, V = logits.shape
+    if tokens.dtype is not _I32 or tokens.shape != (B, n):
+        raise ValueError("tokens must be int32 [B, n]")
+    if logprob.dtype is not _F32 or logprob.shape != (B, n):
+        raise ValueError("logprob must be float32 [B, n]")
+    if entropy is not None and (entropy.dtype is not _F32 or entropy.shape != (B, n)):
+        raise ValueError("entropy must be float32 [B, n]")
+    if lens is not None and (lens.dtype is not _I32 or lens.shape != (B,)):
+        raise ValueError("lens must be int32 [B]")
+    K = 0
+    for t, dt in ((top_ids, _I32), (top_logprobs, _F32)):
+        if t is not None:
+            if t.dtype is not dt or t.dim() != 3 or t.shape[:2] != (B, n):
+                raise ValueError("top_ids must be int32, top_logprobs float32, [B, n, K]")
+            K = t.shape[2]
+    if top_ids is not None and top_logprobs is not None and top_ids.shape != top_logprobs.shape:
+        raise ValueError("top_ids and top_logprobs must share a shape")
+    dev = _device_of(logits)
+    xp, tp, lp, op, ep, ip, vp = _ptrs(dev, logits, tokens, lens, logprob, entropy, top_ids,
+                                       top_logprobs)
+    _check(load().spec_token_logprobs(xp, _TORCH_DT[logits.dtype], tp, lp, B, n, V,
+                                      float(temperature), K, op, ep, ip, vp,
+                                      _stream_on(stream, dev)))
 
 
 def spec_codec_encode(codes, pairs, num_pairs, stream=None) -> None:

@@ -255,6 +255,81 @@ struct GatherArgs {
 };
 cudaError_t launch_kv_gather(const GatherArgs& a, cudaStream_t stream);
 
+// ---- log probabilities, entropy, top alternatives (logprobs.cu) ----
+struct LogprobArgs {
+    const void* logits;
+    int32_t dtype;
+    const int32_t* tokens;
+    const int32_t* lens;  // [B] or null: n
+    int32_t B, n;
+    int64_t V;
+    double temperature;
+    float c;  // log2(e) / temperature
+    int32_t K;
+    float* logprob;
+    float* entropy;       // or null
+    int32_t* top_ids;     // [B, n, K] or null
+    float* top_logprobs;  // [B, n, K] or null
+    int32_t parts = 1;    // CTAs of a row (logprob_parts)
+    int32_t* tickets;     // [B * n] zeroed when parts > 1 (self-resetting)
+    float* part_stats;    // workspace
+    float* part_v;
+    int32_t* part_i;
+    int* dev_err;
+};
+int logprob_parts(const LogprobArgs& a, int num_sms, int max_tickets);
+size_t logprob_workspace_bytes(const LogprobArgs& a);
+cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream);
+
+// ---- pages held by several rows, and the accepted path of a tree (kv_pages.cu) ----
+struct ForkArgs {
+    void* k_cache;
+    void* v_cache;
+    void* k_scale;
+    void* v_scale;
+    int32_t cache_dtype, elem;  // bytes of an element
+    int32_t* block_table;
+    int32_t* ctx_lens;
+    int32_t* page_refs;
+    const int32_t* parents;
+    const int32_t* children;
+    int32_t n, room, rows, Hkv, D, P, num_pages, max_pages;
+    uint32_t* free_bits;  // workspace
+    uint32_t* one_bits;
+    int32_t* free_count;
+    int32_t* need;
+    int32_t* src;
+    int* dev_err;
+};
+size_t fork_workspace_bytes(int num_pages, int n);
+cudaError_t launch_kv_fork(ForkArgs a, void* workspace, cudaStream_t stream);
+
+struct ReleaseArgs {
+    int32_t* block_table;
+    int32_t* ctx_lens;
+    int32_t* page_refs;
+    const int32_t* rows;
+    const int32_t* keep_lens;  // [n] or null: 0
+    int32_t n, batch, P, num_pages, max_pages;
+    int* dev_err;
+};
+cudaError_t launch_kv_release(const ReleaseArgs& a, cudaStream_t stream);
+
+struct CompactArgs {
+    void* k_cache;
+    void* v_cache;
+    void* k_scale;
+    void* v_scale;
+    int32_t cache_dtype, elem;
+    const int32_t* block_table;
+    const int32_t* ctx_lens;
+    const int32_t* path;
+    const int32_t* accepted;
+    int32_t B, k, Hkv, D, P, num_pages, max_pages;
+    int* dev_err;
+};
+cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream);
+
 cudaError_t launch_commit(int32_t* ctx_lens, const int32_t* accepted_len, int B, int extra,
                           cudaStream_t stream);
 

@@ -390,6 +390,25 @@ int spec_verify_attn_window(const void* q, const void* k_cache, const void* v_ca
                             window, num_sinks, out, lse, stream);
 }
 
+int spec_verify_attn_shared(const void* q, const void* k_cache, const void* v_cache,
+                            const void* k_scale, const void* v_scale, const int32_t* block_table,
+                            const int32_t* ctx_lens, const uint64_t* tree_mask,
+                            const int32_t* group_starts, const int32_t* shared_lens,
+                            int32_t num_groups, int32_t batch, int32_t num_draft,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
+                            int32_t q_dtype, int32_t kv_dtype, float scale, void* out, float* lse,
+                            void* stream) {
+    g_err.clear();
+    if (num_groups < 0) return fail(SPEC_ERR_INVALID, "num_groups < 0");
+    if (num_groups > 0 && batch > 0 && (!group_starts || !shared_lens))
+        return fail(SPEC_ERR_INVALID, "group_starts or shared_lens is NULL");
+    return verify_attn_impl(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens,
+                            tree_mask, batch, num_draft, num_q_heads, num_kv_heads, head_dim,
+                            page_size, num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale, 0,
+                            0, out, lse, stream);
+}
+
 int spec_verify_attn_tree(const void* q, const void* k_cache, const void* v_cache,
                           const void* k_scale, const void* v_scale, const int32_t* block_table,
                           const int32_t* ctx_lens, const uint64_t* tree_mask, int32_t batch,
@@ -702,6 +721,162 @@ int spec_kv_gather(const void* k_cache, const void* v_cache, const void* k_scale
     a.dev_err = static_cast<int*>(ws->base);
     cudaError_t e = specv::launch_kv_gather(a, st);
     if (e != cudaSuccess) return cuda_fail(e, "kv_gather launch");
+    return SPEC_OK;
+}
+
+// Sizes, types and pointers of a paged cache that a call writes.
+static int check_cache(const void* k_cache, const void* v_cache, const void* k_scale,
+                       const void* v_scale, int32_t cache_dtype, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t page_size, int32_t num_pages,
+                       int32_t max_pages_per_seq, bool empty) {
+    if (num_kv_heads < 1) return fail(SPEC_ERR_INVALID, "num_kv_heads must be >= 1");
+    if (head_dim < 32 || head_dim > 256 || head_dim % 32)
+        return fail(SPEC_ERR_INVALID, "head_dim must be a multiple of 32 in [32, 256]");
+    if (page_size < 1) return fail(SPEC_ERR_INVALID, "page_size < 1");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(SPEC_ERR_INVALID, "num_pages and max_pages_per_seq must be >= 1");
+    if (cache_dtype != SPEC_DTYPE_F32 && cache_dtype != SPEC_DTYPE_BF16 &&
+        cache_dtype != SPEC_DTYPE_I8 && cache_dtype != SPEC_DTYPE_E4M3)
+        return fail(SPEC_ERR_INVALID, "cache_dtype must be F32, BF16, I8 or E4M3");
+    if (empty) return SPEC_OK;
+    if (!k_cache || !v_cache) return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    const int rc = check_scales(cache_dtype, k_scale, v_scale);
+    if (rc) return rc;
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(SPEC_ERR_INVALID, "caches must be 16-byte aligned");
+    if (reaches(1LL << 40, {num_pages, num_kv_heads, page_size, head_dim}))
+        return fail(SPEC_ERR_INVALID, "cache too large");
+    // (indexes inside a page are 32-bit)
+    if (reaches(1LL << 30, {num_kv_heads, page_size, head_dim}))
+        return fail(SPEC_ERR_UNSUPPORTED, "page too large");
+    return SPEC_OK;
+}
+
+int spec_kv_compact(void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                    int32_t cache_dtype, const int32_t* block_table, const int32_t* ctx_lens,
+                    const int32_t* path, const int32_t* accepted_len, int32_t batch,
+                    int32_t num_draft, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                    int32_t num_pages, int32_t max_pages_per_seq, void* stream) {
+    g_err.clear();
+    if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
+    if (num_draft < 1 || num_draft > 64) return fail(SPEC_ERR_INVALID, "num_draft must be in [1, 64]");
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, cache_dtype, num_kv_heads, head_dim,
+                         page_size, num_pages, max_pages_per_seq, batch == 0);
+    if (rc || batch == 0) return rc;
+    if (!block_table || !ctx_lens || !path || !accepted_len)
+        return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    if (batch > 65535) return fail(SPEC_ERR_UNSUPPORTED, "batch > 65535");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = get_workspace(0, st, &ws);
+    if (rc) return rc;
+    specv::CompactArgs a;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype; a.elem = dtype_size(cache_dtype);
+    a.block_table = block_table; a.ctx_lens = ctx_lens; a.path = path; a.accepted = accepted_len;
+    a.B = batch; a.k = num_draft; a.Hkv = num_kv_heads; a.D = head_dim; a.P = page_size;
+    a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_kv_compact(a, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_compact launch");
+    return SPEC_OK;
+}
+
+int spec_kv_fork(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int32_t cache_dtype,
+                 int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs,
+                 const int32_t* parents, const int32_t* children, int32_t num_pairs, int32_t room,
+                 int32_t num_rows, int32_t num_kv_heads, int32_t head_dim, int32_t page_size,
+                 int32_t num_pages, int32_t max_pages_per_seq, void* stream) {
+    g_err.clear();
+    if (num_pairs < 0) return fail(SPEC_ERR_INVALID, "num_pairs < 0");
+    if (room < 0) return fail(SPEC_ERR_INVALID, "room < 0");
+    if (num_rows < 1) return fail(SPEC_ERR_INVALID, "num_rows must be >= 1");
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, cache_dtype, num_kv_heads, head_dim,
+                         page_size, num_pages, max_pages_per_seq, num_pairs == 0);
+    if (rc || num_pairs == 0) return rc;
+    if (!block_table || !ctx_lens || !page_refs || !parents || !children)
+        return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    if (num_pairs >= 1 << 24) return fail(SPEC_ERR_UNSUPPORTED, "num_pairs must be < 2^24");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = get_workspace(specv::fork_workspace_bytes(num_pages, num_pairs), st, &ws);
+    if (rc) return rc;
+    specv::ForkArgs a;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale; a.v_scale = v_scale;
+    a.cache_dtype = cache_dtype; a.elem = dtype_size(cache_dtype);
+    a.block_table = block_table; a.ctx_lens = ctx_lens; a.page_refs = page_refs;
+    a.parents = parents; a.children = children; a.n = num_pairs; a.room = room; a.rows = num_rows;
+    a.Hkv = num_kv_heads; a.D = head_dim; a.P = page_size; a.num_pages = num_pages;
+    a.max_pages = max_pages_per_seq;
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_kv_fork(a, static_cast<char*>(ws->base) + kHeader, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_fork launch");
+    return SPEC_OK;
+}
+
+int spec_kv_release(int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs,
+                    const int32_t* rows, const int32_t* keep_lens, int32_t num, int32_t num_rows,
+                    int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq, void* stream) {
+    g_err.clear();
+    if (num < 0) return fail(SPEC_ERR_INVALID, "num < 0");
+    if (num_rows < 1) return fail(SPEC_ERR_INVALID, "num_rows must be >= 1");
+    if (page_size < 1) return fail(SPEC_ERR_INVALID, "page_size < 1");
+    if (num_pages < 1 || max_pages_per_seq < 1)
+        return fail(SPEC_ERR_INVALID, "num_pages and max_pages_per_seq must be >= 1");
+    if (num == 0) return SPEC_OK;
+    if (!block_table || !ctx_lens || !page_refs || !rows)
+        return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc = get_workspace(0, st, &ws);
+    if (rc) return rc;
+    specv::ReleaseArgs a;
+    a.block_table = block_table; a.ctx_lens = ctx_lens; a.page_refs = page_refs; a.rows = rows;
+    a.keep_lens = keep_lens; a.n = num; a.batch = num_rows; a.P = page_size;
+    a.num_pages = num_pages; a.max_pages = max_pages_per_seq;
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_kv_release(a, st);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_release launch");
+    return SPEC_OK;
+}
+
+int spec_token_logprobs(const void* logits, int32_t logits_dtype, const int32_t* tokens,
+                        const int32_t* lens, int32_t batch, int32_t num_rows, int64_t vocab,
+                        float temperature, int32_t num_top, float* logprob, float* entropy,
+                        int32_t* top_ids, float* top_logprobs, void* stream) {
+    g_err.clear();
+    if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
+    if (num_rows < 1) return fail(SPEC_ERR_INVALID, "num_rows must be >= 1");
+    if (vocab < 1 || vocab >= (1LL << 31) - (1 << 16))
+        return fail(SPEC_ERR_INVALID, "vocab must be in [1, 2^31 - 2^16)");
+    if (logits_dtype != SPEC_DTYPE_F32 && logits_dtype != SPEC_DTYPE_BF16)
+        return fail(SPEC_ERR_INVALID, "logits_dtype must be F32 or BF16");
+    if (!(temperature >= 1e-30f) || !(temperature < INFINITY))
+        return fail(SPEC_ERR_INVALID, "temperature must be positive (1e-30 at least) and finite");
+    if (num_top < 0 || num_top > 32) return fail(SPEC_ERR_INVALID, "num_top must be in [0, 32]");
+    if (batch == 0) return SPEC_OK;
+    if (!logits || !tokens || !logprob) return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    if (num_top && !top_ids && !top_logprobs)
+        return fail(SPEC_ERR_INVALID, "num_top > 0 needs top_ids or top_logprobs");
+    if (!aligned16(logits)) return fail(SPEC_ERR_INVALID, "logits must be 16-byte aligned");
+    if (reaches(1LL << 26, {batch, num_rows})) return fail(SPEC_ERR_UNSUPPORTED, "too many rows");
+    Workspace* ws = nullptr;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int rc = get_workspace(0, st, &ws);
+    if (rc) return rc;
+    specv::LogprobArgs a;
+    a.logits = logits; a.dtype = logits_dtype; a.tokens = tokens; a.lens = lens;
+    a.B = batch; a.n = num_rows; a.V = vocab; a.temperature = temperature;
+    a.c = (float)(1.4426950408889634074 / (double)temperature);
+    a.K = num_top; a.logprob = logprob; a.entropy = entropy; a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.parts = specv::logprob_parts(a, ws->sms, kMaxTickets);
+    rc = get_workspace(specv::logprob_workspace_bytes(a), st, &ws);
+    if (rc) return rc;
+    a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws->base) + kTicketsOff);
+    a.dev_err = static_cast<int*>(ws->base);
+    cudaError_t e = specv::launch_logprobs(a, static_cast<char*>(ws->base) + kHeader, st);
+    if (e != cudaSuccess) return cuda_fail(e, "token_logprobs launch");
     return SPEC_OK;
 }
 
