@@ -166,6 +166,14 @@ inline int whole_segments(const AttnArgs& a, int num_ctas, int unit, int worth, 
 bool f8_supported(const AttnArgs& a);
 cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);
 
+// ---- tensor-core kernel for groups of sequences that share a prefix (bf16, i8
+// or e4m3 cache), and the launch that joins its pieces ----
+bool shared_supported(const AttnArgs& a, int groups);
+size_t shared_workspace_bytes(const AttnArgs& a, int num_ctas);
+cudaError_t launch_attn_shared(const AttnArgs& a, const int32_t* group_starts,
+                               const int32_t* shared_lens, int groups, int num_ctas, void* workspace,
+                               cudaStream_t stream);
+
 // ---- warp-MMA kernel for k*G <= 16 query rows (mma.sync m16n8k16, TMA pages) ----
 bool mma_supported(const AttnArgs& a);
 cudaError_t launch_attn_mma(const AttnArgs& a, int num_ctas, void* workspace, cudaStream_t stream);

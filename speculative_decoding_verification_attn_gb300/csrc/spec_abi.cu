@@ -229,7 +229,9 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                      int32_t page_size, int32_t num_pages, int32_t max_pages_per_seq,
                      int32_t q_dtype, int32_t kv_dtype, float scale, int32_t window,
-                     int32_t num_sinks, void* out, float* lse, void* stream) {
+                     int32_t num_sinks, void* out, float* lse, void* stream,
+                     const int32_t* group_starts = nullptr, const int32_t* shared_lens = nullptr,
+                     int32_t num_groups = 0) {
     g_err.clear();
     if (batch < 0) return fail(SPEC_ERR_INVALID, "batch < 0");
     if (num_draft < 1 || num_draft > 64) return fail(SPEC_ERR_INVALID, "num_draft must be in [1, 64]");
@@ -301,8 +303,11 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     const bool f8_ok = specv::f8_supported(a);
     const bool tc2_ok = f8_ok || specv::tc2_supported(a);
     const bool small_ok = !win && specv::small_attn_max_keys(a) > 0;
+    // groups with shared prefixes: a tensor-core kernel of its own (any other
+    // forced kernel reads each sequence by itself)
+    const bool groups = (path == 0 || path == 5) && specv::shared_supported(a, num_groups);
     int kernel;
-    if (path == 1) kernel = 1;
+    if (path == 1 || groups) kernel = 1;
     else if (path >= 2) {
         if ((path == 2 && !tc_ok) || (path == 3 && !mma_ok) || (path == 4 && !small_ok) ||
             (path == 5 && !tc2_ok))
@@ -324,6 +329,17 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
         if (rc) return rc;
     }
     cudaError_t e;
+    if (groups) {
+        int ctas = (int)g_opt_ctas.load();
+        if (ctas <= 0) ctas = ws->sms;
+        rc = get_workspace(specv::shared_workspace_bytes(a, ctas), st, &ws);
+        if (rc) return rc;
+        a.dev_err = static_cast<int*>(ws->base);
+        e = specv::launch_attn_shared(a, group_starts, shared_lens, num_groups, ctas,
+                                      static_cast<char*>(ws->base) + kHeader, st);
+        if (e != cudaSuccess) return cuda_fail(e, "verify_attn (shared prefixes) launch");
+        return SPEC_OK;
+    }
     if (use_tc) {
         int ctas = (int)g_opt_ctas.load();
         if (ctas <= 0) ctas = ws->sms;
@@ -406,7 +422,7 @@ int spec_verify_attn_shared(const void* q, const void* k_cache, const void* v_ca
     return verify_attn_impl(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens,
                             tree_mask, batch, num_draft, num_q_heads, num_kv_heads, head_dim,
                             page_size, num_pages, max_pages_per_seq, q_dtype, kv_dtype, scale, 0,
-                            0, out, lse, stream);
+                            0, out, lse, stream, group_starts, shared_lens, num_groups);
 }
 
 int spec_verify_attn_tree(const void* q, const void* k_cache, const void* v_cache,
