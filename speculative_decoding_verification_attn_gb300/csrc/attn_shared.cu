@@ -30,12 +30,13 @@
 //  * TMEM (512 columns): S of the streams [0,128), [128,256), their O [256,384),
 //    [384,512); P (bf16) over the S columns it came from.
 //  * Warps: 0-7 and 8-15 softmax (two for the 32 rows of a TMEM quadrant, half of the keys
-//    each); 16 and 19 MMAs; 17 and 18 producers; with codes, 20-21 and 22-23 widen
+//    each); 16 and 19 MMAs; 17 and 18 producers; with codes, 20-23 and 24-27 widen
 //    what lands in slot 0 and slot 1.
-//  * INT8 and e4m3 codes become bf16 exactly, in place (raw bytes land in the
-//    upper half of their operand slot); scales are fp32 and enter the scores
-//    and, before its rounding to bf16, P.  So the MMAs see the stored values and
-//    the only roundings are P's (8 bits) and the output's.
+//  * INT8 and e4m3 codes become bf16 exactly: a sequence's own keys in place (raw bytes
+//    land in the upper half of their operand slot), and so a prefix that one block
+//    reads; prefixes of several blocks by a launch before this one, once (widen_kernel).
+//    Scales enter the scores and, before its rounding to bf16, P, in fp32.  So the MMAs
+//    see the stored values and the only roundings are P's (8 bits) and the output's.
 //  * Every mbarrier wait is bounded (1 s); a timeout sets the device error word
 //    and an abort flag, after which every role skips its remaining work, drains
 //    its copies and tensor-core operations, and returns.
@@ -71,9 +72,11 @@ constexpr int kSplitAlpha = 3;  // narrow tiles' time that a piece's fixed work 
 constexpr int kWideCost = 2;    // narrow tiles' time that a wide tile takes
 // Keys below which a prefix is read sequence by sequence: one tile
 constexpr int kMinShared = TN;
+// Rows of K (and of V) that widened prefixes may take: 1 GiB together
+constexpr int64_t kMaxPrefixRows = (int64_t)1 << 21;
 
 enum { KV_BF16, KV_I8, KV_E4M3 };
-template <int KV> constexpr int threads() { return KV == KV_BF16 ? 20 * 32 : 24 * 32; }
+template <int KV> constexpr int threads() { return KV == KV_BF16 ? 20 * 32 : 28 * 32; }
 
 constexpr uint32_t IDESC_QK = umma_idesc_bf16(ROWS, TN, 0, 0);
 constexpr uint32_t IDESC_PV = umma_idesc_bf16(ROWS, D, 0, 1);  // B (V) MN-major
@@ -92,10 +95,11 @@ struct Smem {
     static constexpr int PIDS = STAT + 3 * 2 * 2 * ROWS * 4;  // [2 producers][LOOKAHEAD+1][8] int
     // scales of a slot's use u at stage u % 2 of the slot, K then V.  Two stages: a
     // tile's softmax may still read its scales when its K slot is refilled.
-    // e4m3: fp32, one per 16 keys; INT8: the fp16 words as they are stored, and the least
-    // and largest of K's for every 16 keys
+    // e4m3: fp32 for every 16 keys, K's (with the softmax scale), V's and V's logarithm;
+    // INT8: the fp16 words as they are stored, and the least and largest of K's for
+    // every 16 keys
     static constexpr int SCALE = (PIDS + 2 * (LOOKAHEAD + 1) * NVB * 4 + 15) / 16 * 16;
-    static constexpr int SCRAW = SCALE + 4 * 16 * 4;
+    static constexpr int SCRAW = SCALE + 4 * 24 * 4;
     static constexpr int SEG = SCRAW + 4 * 2 * TN * 2;    // int4 [MAX_SEGS]
     static constexpr int TPRE = SEG + MAX_SEGS * 16;
     static constexpr int CPRE = TPRE + (MAX_SEGS + 4) * 4;
@@ -110,10 +114,16 @@ struct Params {
     const int32_t* group_starts;
     const int32_t* shared_lens;
     int groups;
-    float* slot_o;     // [8 C][128][D]: pieces of cut segments (slot_of)
-    float* slot_lse;   // [8 C][128]
-    float* home_o;     // [2][B k Hq][D]: own keys, prefix
-    float* home_lse;   // [2][B k Hq]
+    // codes: [groups][max_pages][Hkv][P][D] bf16 values of the prefixes' codes, K and V,
+    // or null (they are widened tile by tile)
+    __nv_bfloat16* k_prefix;
+    __nv_bfloat16* v_prefix;
+    // rows [8 C][128] of pieces of cut segments (slot_row), then [2][B k Hq] rows of whole
+    // ones (own keys, prefix): values and log2-sums
+    float* slot_o;
+    float* slot_lse;
+    int slots;         // 8 C * 128
+    int G, NT;         // query heads of a kv-head, tokens that fill a Q tile
     int4* seq_block;   // [B] the group's wide blocks (first, count), its narrow one, its
                        // first token (-1: nothing shared)
     int* n_begin;      // [2 C + 1] first tile of each stream's narrow range
@@ -127,9 +137,11 @@ __device__ __forceinline__ int slot_row(bool wide, int c, int s, bool tail) {
     return (8 * c + (wide ? 4 + (tail ? 0 : 2) : 2 * s + (tail ? 0 : 1))) * ROWS;
 }
 
-// A segment: rows of tokens tok0 .. tok0 + ntok - 1, keys [key0, key1).
+// A segment: rows of tokens tok0 .. tok0 + ntok - 1, keys [key0, key1); a block's group.
 struct Seg {
-    int tok0, ntok, key0, key1;
+    int tok0;
+    int16_t ntok, group;
+    int key0, key1;
 };
 
 // V segments: the sequences' own keys, then narrow blocks, then wide ones.
@@ -152,6 +164,7 @@ struct Cursor {
     int start;  // global index of the segment's first tile
     __device__ void init(int t, const List& L) {
         int lo = 0, hi = L.V - 1;  // largest v with tpre[v] * Hkv <= t
+#pragma unroll 1
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (L.tpre[mid] * L.Hkv <= t) lo = mid; else hi = mid - 1;
@@ -176,6 +189,7 @@ struct Cursor {
         if (++lt == nt) next_segment(L);
     }
     __device__ void skip(int n, const List& L) {
+#pragma unroll 1
         for (lt += n; lt >= nt;) {
             const int over = lt - nt;
             next_segment(L);
@@ -198,6 +212,7 @@ __device__ __forceinline__ int range_begin(const List& L, const int* cpre, int a
     const int x = (int)(c * each_c + c * (W - each_c * C) / C);  // c W / C; C < 2^16
     if (x >= (int)W) return L.tpre[L.V] * L.Hkv;
     int lo = 0, hi = L.V - 1;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (cpre[mid] * L.Hkv <= x) lo = mid; else hi = mid - 1;
@@ -214,6 +229,7 @@ template <bool MAX>
 __device__ __forceinline__ void warp_scan(int* s, int n) {
     const int lane = threadIdx.x & 31, per = (n + 31) / 32, lo = lane * per, hi = min(n, lo + per);
     int run = 0;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) run = MAX ? max(run, s[i]) : run + s[i];
     int incl = run;
 #pragma unroll
@@ -223,6 +239,7 @@ __device__ __forceinline__ void warp_scan(int* s, int n) {
     }
     run = __shfl_up_sync(0xffffffffu, incl, 1);
     if (lane == 0) run = 0;
+#pragma unroll 1
     for (int i = lo; i < hi; ++i) {
         run = MAX ? max(run, s[i]) : run + s[i];
         s[i] = run;
@@ -242,12 +259,14 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
     int* starts = tpre;  // scratch until the prefixes are taken
     int* blocks = cpre;  // first each group's shared length, then its blocks
     bool bad = false;
+#pragma unroll 1
     for (int g = tid; g <= groups; g += NTHREADS) {
         const int s = __ldg(prm.group_starts + g), n = g < groups ? __ldg(prm.shared_lens + g) : 0;
         bad |= s < 0 || s > a.B;
         starts[g] = s < 0 ? 0 : s > a.B ? a.B : s;
         blocks[g] = n;
     }
+#pragma unroll 1
     for (int b = tid; b < a.B; b += NTHREADS) {
         int c = __ldg(a.ctx_lens + b);
         const int64_t cap = (int64_t)a.max_pages * a.P - k;
@@ -255,10 +274,11 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
             raise_device_error(a.dev_err, SPEC_DEVERR_CTX);
             c = c < 0 ? 0 : (int)(cap < 0 ? 0 : cap);
         }
-        seg[b] = Seg{b * k, k, 0, c + k};
+        seg[b] = Seg{b * k, (int16_t)k, -1, 0, c + k};
         if (one) prm.seq_block[b] = make_int4(0, 0, 0, -1);
     }
     __syncthreads();
+#pragma unroll 1
     for (int g = tid; g < groups; g += NTHREADS) bad |= starts[g + 1] < starts[g];
     if (__syncthreads_or(bad)) {
         if (bad) raise_device_error(a.dev_err, SPEC_DEVERR_GROUP);
@@ -266,9 +286,11 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
         __syncthreads();
     }
     // how many blocks each group's prefix takes, and where each sequence's own keys begin
+#pragma unroll 1
     for (int g = warp; g < groups; g += NTHREADS / 32) {
         const int lo = starts[g], hi = starts[g + 1];
         int least = INT32_MAX;
+#pragma unroll 1
         for (int b = lo + lane; b < hi; b += 32) least = min(least, seg[b].key1 - k);
         least = __reduce_min_sync(0xffffffffu, least);
         int s = blocks[g], n = 0;
@@ -283,6 +305,7 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
         }
         __syncwarp();
         if (lane == 0) blocks[g] = n;
+#pragma unroll 1
         for (int b = lo + lane; b < hi; b += 32) seg[b].key0 = s;
     }
     __syncthreads();
@@ -291,15 +314,19 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
         __syncthreads();
     }
     const int all = blocks[groups - 1], narrow = a.B + (all >> 16), V = narrow + (all & 0xffff);
+#pragma unroll 1
     for (int g = warp; g < groups; g += NTHREADS / 32) {
         const int before = g ? blocks[g - 1] : 0, mine = blocks[g] - before;
         if (mine == 0) continue;
         const int w0 = narrow + (before & 0xffff), nw = mine & 0xffff, n0 = a.B + (before >> 16);
         const int lo = starts[g], hi = starts[g + 1], s = seg[lo].key0, tok = (hi - lo) * k;
+#pragma unroll 1
         for (int i = lane; i < nw; i += 32)
-            seg[w0 + i] = Seg{lo * k + i * 2 * NT, min(tok - i * 2 * NT, 2 * NT), 0, s};
-        if (lane == 0 && mine >> 16) seg[n0] = Seg{lo * k + nw * 2 * NT, tok - nw * 2 * NT, 0, s};
+            seg[w0 + i] = Seg{lo * k + i * 2 * NT, (int16_t)min(tok - i * 2 * NT, 2 * NT), (int16_t)g, 0, s};
+        if (lane == 0 && mine >> 16)
+            seg[n0] = Seg{lo * k + nw * 2 * NT, (int16_t)(tok - nw * 2 * NT), (int16_t)g, 0, s};
         if (one)
+#pragma unroll 1
             for (int b = lo + lane; b < hi; b += 32) prm.seq_block[b] = make_int4(w0, nw, n0, lo * k);
     }
     if (tid == 0) *s_narrow = narrow;
@@ -314,6 +341,7 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
             return warp ? alpha + nt * (q.ntok > NT ? kWideCost : 1) : nt;
         };
         int sum = 0;
+#pragma unroll 1
         for (int v = lo; v < hi; ++v) sum += cost(v);
         int incl = sum;
 #pragma unroll
@@ -323,6 +351,7 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
         }
         int run = incl - sum;
         if (lane == 0) pre[0] = 0;
+#pragma unroll 1
         for (int v = lo; v < hi; ++v) {
             run += cost(v);
             pre[v + 1] = run;
@@ -332,7 +361,7 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
     return V;
 }
 
-// Widens 16 codes to bf16, exactly.
+// Codes to bf16, exactly.
 // INT8: the low seven bits under the exponent of 128, less 128 (or 256 for a
 // negative code, whose low seven bits are its value + 128).
 __device__ __forceinline__ uint32_t i8x2_to_bf16(uint32_t t) {  // bytes 0 and 2
@@ -349,44 +378,47 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint32_t t) {  // bytes 1 and
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(0x7b807b80u));
     return r;
 }
+template <int KV> __device__ __forceinline__ uint2 widen4(uint32_t w) {
+    if (KV == KV_I8)
+        return make_uint2(i8x2_to_bf16(__byte_perm(w, 0, 0x4140)),
+                          i8x2_to_bf16(__byte_perm(w, 0, 0x4342)));
+    return make_uint2(e4m3x2_to_bf16(__byte_perm(w, 0, 0x1404)),
+                      e4m3x2_to_bf16(__byte_perm(w, 0, 0x3424)));
+}
+template <int KV> __device__ __forceinline__ uint4 widen8(const uint2 r) {
+    const uint2 a = widen4<KV>(r.x), b = widen4<KV>(r.y);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
 template <int KV>
 __device__ __forceinline__ void widen16(const uint4 r, uint4& lo, uint4& hi) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (KV == KV_I8) {
-            o[2 * i] = i8x2_to_bf16(__byte_perm(w[i], 0, 0x4140));
-            o[2 * i + 1] = i8x2_to_bf16(__byte_perm(w[i], 0, 0x4342));
-        } else {
-            o[2 * i] = e4m3x2_to_bf16(__byte_perm(w[i], 0, 0x1404));
-            o[2 * i + 1] = e4m3x2_to_bf16(__byte_perm(w[i], 0, 0x3424));
-        }
-    }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
+    lo = widen8<KV>(make_uint2(r.x, r.y));
+    hi = widen8<KV>(make_uint2(r.z, r.w));
 }
 
 // The keys' scales of a tile as its softmax reads them.
 template <int KV> struct Scales {
-    const float* e4m3;    // K, and 8 words on V: one per 16 keys
+    const float* e4m3;    // of 16 keys: K's; 8 words on V's; 16 words on log2 of V's
     const __half* i8;     // K, and 128 on V
 };
 
-// Exponents of 32 columns from c0 on (raw fp32 scores, rewritten in place): score times
-// the softmax scale in log2 units (for codes: and the keys' scales), less m.
-template <int KV>
-__device__ __forceinline__ void exponents32(uint32_t (&r)[32], float sl2, const Scales<KV>& sc, int c0,
-                                            float m) {
-    const uint64_t neg = f2(-m, -m);
-    uint64_t s = f2(sl2, sl2);
+// Exponents of N columns from c0 on (raw fp32 scores, rewritten in place): score times
+// the softmax scale in log2 units (for codes: and the keys' scales), less m.  LOGV (e4m3):
+// plus the logarithm of V's scale.
+template <int KV, bool LOGV, int N>
+__device__ __forceinline__ void exponents(uint32_t (&r)[N], float sl2, const Scales<KV>& sc, int c0,
+                                          float m) {
+    uint64_t neg = f2(-m, -m), s = f2(sl2, sl2);
 #pragma unroll
-    for (int c = 0; c < 32; c += 8) {
+    for (int c = 0; c < N; c += 8) {
         uint4 h;
         if (KV == KV_I8) h = *reinterpret_cast<const uint4*>(sc.i8 + c0 + c);
         if (KV == KV_E4M3 && c % 16 == 0) {
             const float x = sc.e4m3[(c0 + c) / 16];
             s = f2(x, x);
+            if (LOGV) {
+                const float y = sc.e4m3[16 + (c0 + c) / 16] - m;
+                neg = f2(y, y);
+            }
         }
         const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
@@ -404,24 +436,24 @@ __device__ __forceinline__ void exponents32(uint32_t (&r)[32], float sl2, const 
     }
 }
 
-__device__ __forceinline__ void hide32(uint32_t (&r)[32], uint32_t vis) {
-    if (vis != ~0u) {
+// p = 2^v of N columns from c0 on, for codes times the keys' scales of V (LOGV: they are in
+// v), packed to bf16 pairs; adds the sum of p to l.
+template <int KV, bool LOGV, int N>
+__device__ __forceinline__ void weights(const uint32_t (&v)[N], const Scales<KV>& sc, int c0, float& l,
+                                        uint32_t (&pk)[N / 2]) {
+    uint64_t s = 0, ps[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+    auto total = [&]() {
+        float a0, a1, b0, b1;
+        f2_split(ps[0], a0, a1);
+        f2_split(ps[1], b0, b1);
+        ps[0] = ps[1] = f2(0.f, 0.f);
+        return (a0 + b0) + (a1 + b1);
+    };
 #pragma unroll
-        for (int c = 0; c < 32; ++c) r[c] = ((vis >> c) & 1u) ? r[c] : __float_as_uint(-INFINITY);
-    }
-}
-
-// p = 2^v of 32 columns from c0 on, for codes times the keys' scales of V, packed to
-// bf16 pairs; adds the sum of p to ps.
-template <int KV>
-__device__ __forceinline__ void weights32(const uint32_t (&v)[32], const Scales<KV>& sc, int c0,
-                                          uint64_t (&ps)[2], uint32_t (&pk)[16]) {
-    uint64_t s = 0;
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) {
+    for (int c = 0; c < N; c += 8) {
         uint4 h;
         if (KV == KV_I8) h = *reinterpret_cast<const uint4*>(sc.i8 + TN + c0 + c);
-        if (KV == KV_E4M3 && c % 16 == 0) {
+        if (KV == KV_E4M3 && !LOGV && c % 16 == 0) {
             const float x = sc.e4m3[8 + (c0 + c) / 16];
             s = f2(x, x);
         }
@@ -436,10 +468,13 @@ __device__ __forceinline__ void weights32(const uint32_t (&v)[32], const Scales<
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[u]));
                 s = f2(x.x, x.y);
             }
-            if (KV != KV_BF16) f2_split(f2_mul(e, s), e0, e1);
+            if (KV != KV_BF16 && !LOGV) f2_split(f2_mul(e, s), e0, e1);
             pk[c / 2 + u] = pack_bf16x2(e0, e1);
         }
+        // (the sums of 16 keys that share a scale, without it)
+        if (LOGV && c % 16 == 8) l = fmaf(total(), __frcp_rn(sc.e4m3[8 + (c0 + c) / 16]), l);
     }
+    if (!LOGV) l += total();
 }
 
 template <int KV>
@@ -447,7 +482,9 @@ __global__ void __launch_bounds__(threads<KV>(), 1)
 attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of k tokens
                    const __grid_constant__ CUtensorMap block_map,  // q: boxes of NT tokens
                    const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const Params prm) {
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap kwide,  // codes: prefixes as bf16
+                   const __grid_constant__ CUtensorMap vwide, const Params prm) {
     constexpr int NTH = threads<KV>();
     constexpr bool CODES = KV != KV_BF16;
     extern __shared__ uint8_t smem_raw[];
@@ -463,11 +500,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     Seg* s_seg = reinterpret_cast<Seg*>(sm + Smem::SEG);
     int* s_tpre = reinterpret_cast<int*>(sm + Smem::TPRE);
     int* s_cpre = reinterpret_cast<int*>(sm + Smem::CPRE);
-    float* s_scale = reinterpret_cast<float*>(sm + Smem::SCALE);  // [slot][stage][16]
+    float* s_scale = reinterpret_cast<float*>(sm + Smem::SCALE);  // [slot][stage][24]
     __half* s_half = reinterpret_cast<__half*>(sm + Smem::SCRAW);  // [slot][stage][2][TN]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int k = a.k, Hkv = a.Hkv, G = a.Hq / a.Hkv, P = a.P, NT = ROWS / G;
+    const int k = a.k, Hkv = a.Hkv, G = prm.G, P = a.P, NT = prm.NT;
 
     if (tid < 2) {
         mbar_init(&bars[Smem::B_KFULL + tid], 1);
@@ -480,8 +517,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
         mbar_init(&bars[Smem::B_SFREE + tid], 1);
         mbar_init(&bars[Smem::B_EPI + tid], 8);
         mbar_init(&bars[Smem::B_DRAIN + tid], 1);
-        mbar_init(&bars[Smem::B_KREADY + tid], 2);  // the 2 warps that widen the slot
-        mbar_init(&bars[Smem::B_VREADY + tid], 2);
+        mbar_init(&bars[Smem::B_KREADY + tid], 4);  // the 4 warps that widen the slot
+        mbar_init(&bars[Smem::B_VREADY + tid], 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -528,7 +565,16 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     tc_fence_after();
     const uint32_t tmem = uniform(*tmem_slot);
     if (blockIdx.x == 0)
+#pragma unroll 1
         for (int v = tid; v <= V; v += NTH) prm.tile_pre[v] = s_tpre[v];
+
+    // a range without a tile can lie inside a segment: its slot counts as a piece of weight 0
+    if (tid < 2 * ROWS) {
+        const Range g = *s_rng;
+        const int s = tid >> 7, r = tid & (ROWS - 1);
+        if (g.n[s] == g.n[s + 1]) prm.slot_lse[slot_row(false, blockIdx.x, s, true) + r] = -INFINITY;
+        if (g.w[0] == g.w[1]) prm.slot_lse[slot_row(true, blockIdx.x, 0, true) + tid] = -INFINITY;
+    }
 
     // Stream s: narrow tiles, then the wide ones of the CTA.  Slot s holds tile i of
     // the stream's narrow ones as its use i, and wide tile 2 i + s as its use
@@ -536,11 +582,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     const int n_wide = uniform(s_rng->w[1] - s_rng->w[0]);
     auto narrow_tiles = [&](int s) { return uniform(s_rng->n[s + 1] - s_rng->n[s]); };
 
-    // Registers (a thread, per warpgroup; the launch gives 96, with codes 80): softmax
-    // 104 / 88, MMAs and copies 64 / 64, widening 64 (4 x 104 + 64 = 5 x 96, 4 x 88 + 2 x 64 =
-    // 6 x 80)
+    // Registers (a thread, per warpgroup; the launch gives 96, with codes 72): softmax
+    // 104 / 80, MMAs and copies 64 / 56, widening 64 (4 x 104 + 64 = 5 x 96, 4 x 80 + 56 +
+    // 2 x 64 = 7 x 72)
     if (warp >= 16 && warp < 20) {
-        regs_dec<64>();
+        regs_dec<CODES ? 56 : 64>();
         if (warp == 17 || warp == 18) {
             // ================= producers: slot s of K and of V =================
             // A tile is chunks of CH = min(P, 128) keys, each inside one page and one TMA
@@ -616,16 +662,24 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 cp_async_wait<LOOKAHEAD - 1>();  // entries of tiles i and i + 1
                 __syncwarp();
                 const int nck = (cur.valid(L) + CH - 1) / CH;
-                int row = 0;
-                if (lane < nck)
-                    row = (page_of(i, lane) * Hkv + cur.kvh) * P + ((cur.key0(L) + lane * CH) & (P - 1));
+                const bool wide = CODES && prm.k_prefix && cur.v >= L.B;  // values, not codes
+                int row = 0, row16 = 0;
+                if (lane < nck) {
+                    const int key = cur.key0(L) + lane * CH;
+                    row = row16 = (page_of(i, lane) * Hkv + cur.kvh) * P + (key & (P - 1));
+                    if (wide)
+                        row16 = ((L.seg[cur.v].group * a.max_pages + (key >> shift)) * Hkv + cur.kvh) * P +
+                                (key & (P - 1));
+                }
                 const uint64_t pol = cur.v < L.B ? once : again;
                 if (i > 0) ok = warp_wait(&bars[Smem::B_KEMPTY + s], (i - 1) & 1, abort_flag, a.dev_err);
                 if (!ok) break;
-                uint32_t bytes = (uint32_t)(nck * CH) * (CODES ? 128u : 256u);
-                if (KV == KV_E4M3 && lane < 16)
-                    s_scale[(2 * s + (i & 1)) * 16 + lane] =
-                        lane < 8 ? scale * a.scale * kLog2e : scale;
+                const uint32_t bytes = (uint32_t)(nck * CH) * (CODES && !wide ? 128u : 256u);
+                if (KV == KV_E4M3 && lane < 16) {
+                    float* to = s_scale + (2 * s + (i & 1)) * 24 + lane;
+                    to[0] = lane < 8 ? scale * a.scale * kLog2e : scale;
+                    if (lane >= 8) to[8] = log2f(scale);
+                }
                 __syncwarp();
                 uint64_t* full = &bars[Smem::B_KFULL + s];
                 if (lane == 0)
@@ -633,7 +687,10 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 __syncwarp();
                 if (lane < nck) {
                     if constexpr (CODES) {
-                        tma_load_2d(kslot + RAW_OFF + lane * CH * 128, &kmap, full, 0, row, pol);
+                        if (wide)
+                            tma_load_4d_hint(kslot + lane * CH * 256, &kwide, full, 0, 0, 0, row16 >> 3, pol);
+                        else
+                            tma_load_2d(kslot + RAW_OFF + lane * CH * 128, &kmap, full, 0, row, pol);
                         if (KV == KV_I8) {
                             __half* raw = s_half + (2 * s + (i & 1)) * 2 * TN + lane * CH;
                             bulk_load(raw, a.k_scale + row, CH * 2, full);
@@ -651,10 +708,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
                 if (lane < nck) {
-                    if constexpr (CODES)
+                    if (CODES && !wide)
                         tma_load_2d(vslot + RAW_OFF + lane * CH * 128, &vmap, full, 0, row, pol);
                     else
-                        tma_load_4d_hint(vslot + lane * CH * 256, &vmap, full, 0, 0, 0, row >> 4, pol);
+                        tma_load_4d_hint(vslot + lane * CH * 256, CODES ? &vwide : &vmap, full, 0, 0, 0,
+                                         row16 >> 4, pol);
                 }
                 v_loads = i + 1;
                 __syncwarp();
@@ -714,6 +772,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 }
                 const int len = uniform(min(cur.nt - cur.lt, (wide ? total : n) - t0));
                 const int keys = uniform(L.seg[cur.v].key1 - cur.key0(L));  // from its first tile on
+                const bool values = CODES && prm.k_prefix && uniform(cur.v >= L.B);
                 ok = warp_wait(&bars[Smem::B_QFULL + s], (q_loads - 1) & 1, abort_flag, a.dev_err);
 #pragma unroll 1
                 for (int j = 0; j < len && ok; ++j) {
@@ -742,10 +801,11 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     ok = warp_wait(&bars[(CODES ? Smem::B_VREADY : Smem::B_VFULL) + slot], use & 1,
                                    abort_flag, a.dev_err);
                     if (!ok) break;
-                    if (!CODES && nvalid % 16 != 0) {
+                    if (nvalid % 16 != 0 && (!CODES || values)) {
                         // keys past the end that the last P V reads: 0 * (stale or canary) never
                         // reaches O (both streams may write the zeros of a wide tile)
                         uint8_t* vst = sm + Smem::VS + slot * SLOT_BYTES;
+#pragma unroll 1
                         for (int e = lane; e < (nvb * 16 - nvalid) * 16; e += 32) {
                             const int key = nvalid + e / 16, h = (e / 8) & 1, c16 = e % 8;
                             *reinterpret_cast<uint4*>(vst + (key / 16) * 4096 + h * 2048 +
@@ -800,14 +860,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     } else if (CODES && warp >= 20) {
         if constexpr (CODES) {
             regs_dec<64>();
-            // ================= widening of slot s (warps 20-21, 22-23) =================
+            // ================= widening of slot s (warps 20-23, 24-27) =================
             // Each code exactly to bf16, in place, in the layout the MMAs read.  The raw tile
             // sits in the upper half of its slot, row r at 16 KB + 128 r; its bf16 row
             // takes the 256 bytes from 256 r on (in groups of 8 or 16 rows), so
             // ascending rows never land on unread ones.  Rows past the end
             // become zeros.  Every warp runs every tile and every barrier,
             // also after an abort.
-            const int s = warp >= 22, ct = tid - (20 + 2 * s) * 32;  // 0..63
+            const int s = warp >= 24, ct = tid - (20 + 4 * s) * 32;  // 0..127
             const int n = narrow_tiles(s), total = n + (n_wide - s + 1) / 2;
             Cursor c = s_cur[n > 0 ? s : 2];
             if (n == 0 && s && n_wide > 1) c.next(L);
@@ -815,6 +875,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
 #pragma unroll 1
             for (int i = 0; i < total; ++i) {
                 const int nvalid = c.valid(L);
+                const bool values = prm.k_prefix && c.v >= L.B;  // nothing to widen
 #pragma unroll 1
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     if (ok)
@@ -825,47 +886,45 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                         // bounds of K's scales over 16 keys, and no V scale past the end (a
                         // weight of 0 times whatever is stored there)
                         __half* raw = s_half + (2 * s + (i & 1)) * 2 * TN;
-                        float* to = s_scale + (2 * s + (i & 1)) * 16;
+                        float* to = s_scale + (2 * s + (i & 1)) * 24;
+                        const int j = ct;
+                        const float x = __half2float(raw[j]);
+                        float lo = j < nvalid ? x : INFINITY, hi = j < nvalid ? x : 0.f;
 #pragma unroll
-                        for (int j = ct; j < TN; j += 64) {
-                            const float x = __half2float(raw[j]);
-                            float lo = j < nvalid ? x : INFINITY, hi = j < nvalid ? x : 0.f;
-#pragma unroll
-                            for (int o = 8; o > 0; o >>= 1) {
-                                lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                            }
-                            if (j % 16 == 0) {
-                                to[j / 16] = lo;
-                                to[8 + j / 16] = hi;
-                            }
-                            if (j >= nvalid) raw[TN + j] = __float2half(0.f);
+                        for (int o = 8; o > 0; o >>= 1) {
+                            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+                            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
                         }
+                        if (j % 16 == 0) {
+                            to[j / 16] = lo;
+                            to[8 + j / 16] = hi;
+                        }
+                        if (j >= nvalid) raw[TN + j] = __float2half(0.f);
                     }
                     // piece id: key id / 8, head dims 16 (id % 8) ..; 32 rows at a time; rows
-                    // from 64 on land over raw rows that both warps have read by then
+                    // from 64 on land over raw rows that all four warps have read by then
                     const int c16 = ct & 7, h = c16 >> 2, cc = (c16 & 3) * 2, j0 = ct >> 3;
-                    // chunks cc, cc + 1 of half h, swizzled by the row (j0 % 8: a piece's
-                    // rows are 8 apart); lanes of half 1 store their odd chunk
-                    // first so that 8 consecutive lanes hit 8 bank groups
-                    const int o0 = ((cc + h) ^ j0) << 4, o1 = ((cc + 1 - h) ^ j0) << 4;
-                    uint8_t* to = slot + h * (is_v ? 2048 : 1024) + j0 * 128;
+                    // chunks cc, cc + 1 of half h, swizzled by the row; lanes of half 1
+                    // store their odd chunk first so that 8 consecutive lanes hit 8
+                    // bank groups
+                    const int o0 = ((cc + h) ^ (j0 & 7)) << 4, o1 = ((cc + 1 - h) ^ (j0 & 7)) << 4;
+                    // row 32 pass + 16 u + j0: K groups of 8 rows 2 KB apart, V of 16 4 KB
+                    uint8_t* to = slot + (is_v ? h * 2048 + j0 * 128
+                                               : h * 1024 + (j0 >> 3) * 2048 + (j0 & 7) * 128);
                     const uint8_t* from = slot + RAW_OFF + ct * 16;
 #pragma unroll 1
-                    for (int pass = 0; pass < 4; ++pass) {
-                        uint4 raw[4];
+                    for (int pass = values ? 4 : 0; pass < 4; ++pass) {
+                        uint4 raw[2];
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            raw[u] = *reinterpret_cast<const uint4*>(from + pass * 4096 + u * 1024);
-                        if (pass >= 2) named_bar_sync(10 + s, 64);
+                        for (int u = 0; u < 2; ++u)
+                            raw[u] = *reinterpret_cast<const uint4*>(from + pass * 4096 + u * 2048);
+                        if (pass >= 2) named_bar_sync(10 + s, 128);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
+                        for (int u = 0; u < 2; ++u) {
                             uint4 lo, hi;
                             widen16<KV>(raw[u], lo, hi);
-                            if (pass * 32 + u * 8 + j0 >= nvalid) lo = hi = make_uint4(0, 0, 0, 0);
-                            // row 32 pass + 8 u + j0: K groups of 8 rows 2 KB apart, V of 16 4 KB
-                            uint8_t* row = to + pass * 8192 +
-                                           (is_v ? (u >> 1) * 4096 + (u & 1) * 1024 : u * 2048);
+                            if (pass * 32 + u * 16 + j0 >= nvalid) lo = hi = make_uint4(0, 0, 0, 0);
+                            uint8_t* row = to + pass * 8192 + u * 4096;
                             *reinterpret_cast<uint4*>(row + o0) = h ? hi : lo;
                             *reinterpret_cast<uint4*>(row + o1) = h ? lo : hi;
                         }
@@ -885,7 +944,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
             }
         }
     } else {
-        regs_inc<CODES ? 88 : 104>();
+        regs_inc<CODES ? 80 : 104>();
         // ================= softmax of stream s =================
         // Two warps for the 32 rows of a TMEM quadrant, each on 64 of the tile's keys and
         // 64 of O's columns; they meet at the row's maximum.
@@ -923,15 +982,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 const int use = wide ? (slot == s ? n : other) + ((t - n) >> 1) : t;
                 const int stage = 2 * slot + (use & 1);
                 // scales of this half: e4m3 (and INT8's bounds) 4 of 8, INT8 64 of 128
-                const Scales<KV> sc = {s_scale + stage * 16 + half * 4,
+                const Scales<KV> sc = {s_scale + stage * 24 + half * 4,
                                        s_half + stage * 2 * TN + half * 64};
                 const uint64_t vis =
                     visible64<false>(cur.key0(L), half * 64, cur.valid(L), ctx, mrow, 0, 0);
                 // the row's maximum: with the loads where all keys are visible (INT8: within
                 // the bounds that the scales of 16 keys give, when those lie close enough)
                 float mx = -INFINITY;
-                bool exact = vis != ~0ull || a.scale < 0.f;
-                if (!__any_sync(0xffffffffu, exact)) {
+                bool slow = vis != ~0ull || a.scale < 0.f;
+                if (!__any_sync(0xffffffffu, slow && r < rows)) {
                     float least = -INFINITY;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
@@ -948,27 +1007,39 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                                 least = fmaxf(least, x[j] * sl2 * (x[j] > 0.f ? lo : hi));
                             } else {
                                 mx = fmaxf(mx, x[j] * (KV == KV_E4M3 ? sc.e4m3[h * 2 + j] : sl2));
+                                // a scale of V whose logarithm would cost weights
+                                if (KV == KV_E4M3) slow |= !(sc.e4m3[8 + h * 2 + j] > 1e-18f);
                             }
                         }
                     }
-                    exact = KV == KV_I8 && !(mx - fmaxf(least, m_ref) <= kRescaleThreshold);
+                    if (KV == KV_I8) slow = !(mx - fmaxf(least, m_ref) <= kRescaleThreshold);
                 }
-                if (__any_sync(0xffffffffu, exact)) {
+                // (rows past the piece's hold anything: they decide nothing)
+                slow = __any_sync(0xffffffffu, slow && r < rows);
+                // 16 columns less m (the slow way: hidden keys to -inf, small code)
+                auto some = [&](int c, float m, uint32_t (&v)[16]) {
+                    tmem_ld16(s_mine + c, v);
+                    tmem_wait_ld();
+                    exponents<KV, false, 16>(v, sl2, sc, c, m);
+                    const uint32_t bits = (uint32_t)(vis >> c);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        v[e] = ((bits >> e) & 1u) ? v[e] : __float_as_uint(-INFINITY);
+                };
+                if (slow) {
                     mx = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(s_mine + c * 32, v);
-                        tmem_wait_ld();
-                        exponents32<KV>(v, sl2, sc, c * 32, 0.f);
-                        hide32(v, (uint32_t)(vis >> (c * 32)));
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t v[16];
+                        some(c, 0.f, v);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2)
+                        for (int e = 0; e < 16; e += 2)
                             mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                     }
                 }
                 {
                     float* mine = stat + (t & 1) * 4 * ROWS;
+                    if (r >= rows) mx = 0.f;
                     mine[half * ROWS] = mx;
                     named_bar_sync(meet, 64);
                     mx = fmaxf(mx, mine[(1 - half) * ROWS]);
@@ -983,35 +1054,40 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     l *= al;
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // keeps -inf - m finite
-                uint64_t ps[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-                // P over the first 32 of this half's S columns, read by then
+                // P over the first 32 of this half's S columns, read by then.  (A branch on
+                // hidden keys inside the loop cost a third of the kernel's time: the
+                // compiler no longer runs the exponents under the products.)
+                constexpr bool LOGV = KV == KV_E4M3;
+                if (!slow) {
+#pragma unroll(KV == KV_I8 ? 2 : 1)
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(s_mine + c, v);
+                        tmem_wait_ld();
+                        exponents<KV, LOGV, 32>(v, sl2, sc, c, m_use);
+                        weights<KV, LOGV, 32>(v, sc, c, l, pk);
+                        tmem_st16(s_mine + c / 2, pk);
+                    }
+                } else {
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t v[32], pk[16];
-                    tmem_ld32(s_mine + c * 32, v);
-                    tmem_wait_ld();
-                    exponents32<KV>(v, sl2, sc, c * 32, m_use);
-                    hide32(v, (uint32_t)(vis >> (c * 32)));
-                    weights32<KV>(v, sc, c * 32, ps, pk);
-                    tmem_st16(s_mine + c * 16, pk);
-                }
-                {
-                    float a0, a1, b0, b1;
-                    f2_split(ps[0], a0, a1);
-                    f2_split(ps[1], b0, b1);
-                    l += (a0 + b0) + (a1 + b1);
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t v[16], pk[8];
+                        some(c, m_use, v);
+                        weights<KV, false, 16>(v, sc, c, l, pk);
+                        tmem_st8(s_mine + c / 2, pk);
+                    }
                 }
                 if (!first && __any_sync(0xffffffffu, move)) {
                     // O holds every earlier P V of the piece (S of this tile came after them)
 #pragma unroll 1
-                    for (int c4 = 0; c4 < 2; ++c4) {
-                        uint32_t ov[32];
-                        tmem_ld32(o_mine + c4 * 32, ov);
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_mine + c, ov);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             ov[e] = __float_as_uint(__uint_as_float(ov[e]) * al);
-                        tmem_st32(o_mine + c4 * 32, ov);
+                        tmem_st16(o_mine + c, ov);
                     }
                 }
                 tmem_wait_st();
@@ -1038,48 +1114,44 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     const bool complete = cur.start >= tb && cur.start + cur.nt <= te;
                     const bool final = complete && cur.v < L.B && q.key0 == 0;
                     const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+                    const float lse = l > 0.f ? m_ref + log2f(l) : -INFINITY;
                     // this row's place: out, the arrays of whole segments, or a slot
                     const int64_t orow =
                         (int64_t)(q.tok0 + (wide && s ? NT : 0) + r / G) * a.Hq + cur.kvh * G + r % G;
                     const int64_t at =
-                        complete ? (cur.v < L.B ? 0 : (int64_t)a.B * k * a.Hq) + orow
+                        complete ? prm.slots + (cur.v < L.B ? 0 : (int64_t)a.B * k * a.Hq) + orow
                                  : (int64_t)(slot_row(wide, blockIdx.x, s, cur.start < tb) +
                                              (wide && s ? ROWS : 0) + r);
-                    float* po = (complete ? prm.home_o : prm.slot_o) + at * D + half * 64;
+                    float* po = prm.slot_o + at * D + half * 64;
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + orow * D + half * 64;
 #pragma unroll 1
-                    for (int c4 = 0; c4 < 2; ++c4) {
-                        uint32_t ov[32];
-                        tmem_ld32(o_mine + c4 * 32, ov);
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t ov[16];
+                        tmem_ld16(o_mine + c, ov);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
                         if (r >= rows) {
                         } else if (final) {
-                            uint4* dst = reinterpret_cast<uint4*>(out + c4 * 32);
+                            uint32_t w[8];
 #pragma unroll
-                            for (int v4 = 0; v4 < 4; ++v4) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    w[u] = pack_bf16x2(__uint_as_float(ov[8 * v4 + 2 * u]),
-                                                       __uint_as_float(ov[8 * v4 + 2 * u + 1]));
-                                dst[v4] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int u = 0; u < 8; ++u)
+                                w[u] = pack_bf16x2(__uint_as_float(ov[2 * u]), __uint_as_float(ov[2 * u + 1]));
+                            uint4* dst = reinterpret_cast<uint4*>(out + c);
+                            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         } else {
-                            uint4* dst = reinterpret_cast<uint4*>(po + c4 * 32);
+                            uint4* dst = reinterpret_cast<uint4*>(po + c);
 #pragma unroll
-                            for (int v4 = 0; v4 < 8; ++v4)
-                                dst[v4] = make_uint4(ov[4 * v4], ov[4 * v4 + 1], ov[4 * v4 + 2],
-                                                     ov[4 * v4 + 3]);
+                            for (int u = 0; u < 4; ++u)
+                                dst[u] = make_uint4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
                         }
                         __syncwarp();
                     }
                     if (r < rows && half == 0) {
-                        if (!final) (complete ? prm.home_lse : prm.slot_lse)[at] = lse;
-                        else if (a.lse) a.lse[orow] = lse;
+                        if (!final) prm.slot_lse[at] = lse;
+                        else if (a.lse) a.lse[orow] = lse * kLn2;
                     }
                 }
                 tc_fence_before();
@@ -1104,123 +1176,206 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
 
 constexpr int kJoinWarps = 8;
 
-// The last of n ranges (first tiles in `begin`) that starts at or before tile t; a warp.
-__device__ __forceinline__ int range_of(const int* begin, int n, int t) {
-    const int lane = threadIdx.x & 31;
-    int count = 0;
-    for (int c = lane; c < n; c += 32) count += __ldg(begin + c) <= t;
-    return (int)__reduce_add_sync(0xffffffffu, (unsigned)count) - 1;
+// A segment's pieces for one kv-head: ranges first .. first + count - 1; one alone is
+// whole.  (Ranges without a tile among them have left sums of -inf.)
+struct Pieces {
+    int first, count, wide;
+};
+
+// Of n ranges with these first tiles, the last that starts at or before tile t0, and the
+// number of them up to tile t1's; a warp.
+__device__ __forceinline__ void find_ranges(const int* begin, int n, int t0, int t1, Pieces& p) {
+    int c0 = 0, c1 = 0;
+#pragma unroll 5
+    for (int c = threadIdx.x & 31; c < n; c += 32) {
+        const int t = __ldg(begin + c);
+        c0 += t <= t0;
+        c1 += t <= t1;
+    }
+    p.first = (int)__reduce_add_sync(0xffffffffu, (unsigned)c0) - 1;
+    p.count = (int)__reduce_add_sync(0xffffffffu, (unsigned)c1) - 1 - p.first + 1;
 }
 
-// A warp per query row.
+// x / y for 0 <= x < 2^20, given 1 / y
+__device__ __forceinline__ int quotient(int x, float inverse) { return (int)((x + 0.5f) * inverse); }
+
+// A block per (sequence, kv-head): its own keys' pieces and those of the (up to two)
+// blocks that hold its tokens are looked up once, by a warp each; then a warp per query
+// row, its pieces' sums and values in one round trip.  The launch runs once through its
+// code: short code counts more here than few instructions.
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm, int C) {
+    __shared__ Pieces s_seg[3];
     grid_dep_launch_dependents();
     grid_dep_wait();
     const AttnArgs& a = prm.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.Hq / a.Hkv, NT = ROWS / G, b = blockIdx.x / a.Hkv, kvh = blockIdx.x % a.Hkv;
-    const int row = blockIdx.y * kJoinWarps + warp;
-    if (row >= a.k * G) return;
-    const int token = b * a.k + row / G;
-    const int rows = a.B * a.k * a.Hq, slots = 8 * C * ROWS;
-    const int orow = token * a.Hq + kvh * G + row % G;
+    const int G = prm.G, NT = prm.NT, kvh = blockIdx.y, b = blockIdx.x;
+    const float inv_g = 1.f / G, inv_nt = 1.f / NT;
     const int4 blk = __ldg(prm.seq_block + b);
-    // the prefix: its block, and the row there
-    const int dt = token - blk.w, nth = dt / (2 * NT), off = dt - nth * 2 * NT;
-    const bool shared = blk.w >= 0, wide = shared && nth < blk.y;
-    const int v1 = wide ? blk.x + nth : blk.z;
-    const int row1 = off / NT * ROWS + off % NT * G + row % G;
-    // pieces first .. first + count - 1 of each of the two segments; one alone is whole
-    auto find = [&](int v, bool w, int& seg0, int& first, int& count) {
-        const int p0 = __ldg(prm.tile_pre + v), nt = __ldg(prm.tile_pre + v + 1) - p0;
-        const int* begin = w ? prm.w_begin : prm.n_begin;
-        const int n = w ? C : 2 * C;
-        seg0 = p0 * a.Hkv + kvh * nt;
-        first = range_of(begin, n, seg0);
-        count = range_of(begin, n, seg0 + nt - 1) - first + 1;
-    };
-    int seg0, first0, count0, seg1 = 0, first1 = 0, count1 = 0;
-    find(b, false, seg0, first0, count0);
-    if (shared) find(v1, wide, seg1, first1, count1);
-    else if (count0 == 1) return;  // written already
-    // piece i: its row among the slots, or past them among the whole rows; -1 for none
-    auto place = [&](int i) {
-        const bool p = i >= count0;
-        if ((p ? count1 : count0) == 1) return slots + (p ? rows : 0) + orow;
-        const bool w = p && wide;
-        const int c = p ? first1 + i - count0 : first0 + i;
-        const int* begin = w ? prm.w_begin : prm.n_begin;
-        const int t = __ldg(begin + c);
-        if (t == __ldg(begin + c + 1)) return -1;
-        return slot_row(w, w ? c : c >> 1, w ? 0 : c & 1, (p ? seg1 : seg0) < t) + (p ? row1 : row);
-    };
-    auto lse_at = [&](int p) {
-        return p < 0 ? -INFINITY : p < slots ? __ldg(prm.slot_lse + p) : __ldg(prm.home_lse + (p - slots));
-    };
-    const int n = count0 + count1;
-    // up to 32 pieces: one per lane, read once
-    const int mine = lane < n ? place(lane) : -1;
-    const float z = lse_at(mine);
-    float m = z;
-    for (int i = 32 + lane; i < n; i += 32) m = fmaxf(m, lse_at(place(i)));
-    m = warp_max(m);
-    float sum = z == -INFINITY ? 0.f : expf(z - m);
-    for (int i = 32 + lane; i < n; i += 32) {
-        const float x = lse_at(place(i));
-        if (x != -INFINITY) sum += expf(x - m);
+    const bool shared = blk.w >= 0;
+    const int dt0 = b * a.k - blk.w, nth0 = shared ? quotient(dt0, 0.5f * inv_nt) : 0;
+    if (warp < 3) {
+        const int nth = nth0 + warp - 1;
+        const bool wide = warp > 0 && nth < blk.y;
+        const int v = warp == 0 ? b : wide ? blk.x + nth : blk.z;
+        Pieces p = {0, 0, wide};
+        // (where its last token lies in the first block nobody asks for the second)
+        if (warp == 0 || (shared && dt0 + a.k > 2 * NT * nth)) {
+            const int p0 = __ldg(prm.tile_pre + v), nt = __ldg(prm.tile_pre + v + 1) - p0;
+            const int t0 = p0 * a.Hkv + kvh * nt;
+            find_ranges(wide ? prm.w_begin : prm.n_begin, wide ? C : 2 * C, t0, t0 + nt - 1, p);
+        }
+        if (lane == 0) s_seg[warp] = p;
     }
-    sum = warp_sum(sum);
-    const float lse = sum > 0.f ? m + logf(sum) : -INFINITY;
-    const float w_mine = z == -INFINITY ? 0.f : expf(z - lse);
+    __syncthreads();
+    const int row = blockIdx.z * kJoinWarps + warp;
+    const Pieces own = s_seg[0];
+    if ((!shared && own.count == 1) || row >= a.k * G) return;  // written already
+    const int tok = quotient(row, inv_g), dt = dt0 + tok;
+    const int nth = shared ? quotient(dt, 0.5f * inv_nt) : 0, off = dt - nth * 2 * NT;
+    const int orow = (b * a.k + tok) * a.Hq + kvh * G + row - tok * G;
+    const Pieces pre = shared ? s_seg[1 + nth - nth0] : Pieces{0, 0, 0};
+    const int row1 = (off >= NT ? ROWS + (off - NT) * G : off * G) + row - tok * G;
+    const int rows = a.B * a.k * a.Hq, slots = 8 * C * ROWS, n = own.count + pre.count;
+    // piece i: its row among the slots, or past them among the whole rows
+    auto place = [&](int i) {
+        const bool p = i >= own.count;
+        const Pieces q = p ? pre : own;
+        if (p) i -= own.count;
+        if (q.count == 1) return slots + (p ? rows : 0) + orow;
+        const int c = q.first + i;
+        return slot_row(q.wide, q.wide ? c : c >> 1, q.wide ? 0 : c & 1, i > 0) + (p ? row1 : row);
+    };
+    // (the arrays of whole segments lie behind the slots': one base for both)
+    float m = -INFINITY, sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 4) {
-        float w[4];
-        float4 x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u;
-            int p = __shfl_sync(0xffffffffu, mine, i & 31);
-            w[u] = __shfl_sync(0xffffffffu, w_mine, i & 31);
-            if (i >= 32) {
-                p = i < n ? place(i) : -1;
-                const float y = lse_at(p);
-                w[u] = y == -INFINITY ? 0.f : expf(y - lse);
-            }
-            if (i >= n) w[u] = 0.f;
-            // a piece of weight 0 may have written nothing: its value is not read
-            if (w[u] > 0.f) {
-                const float* o = p < slots ? prm.slot_o + (int64_t)p * D
-                                           : prm.home_o + (int64_t)(p - slots) * D;
-                x[u] = __ldg(reinterpret_cast<const float4*>(o) + lane);
+    for (int i0 = 0; i0 < n; i0 += 32) {  // (one round but for very long segments)
+        int mine = -1;
+        float z = -INFINITY;
+        if (i0 + lane < n) {
+            mine = place(i0 + lane);
+            z = __ldg(prm.slot_lse + mine);
+        }
+        const float top = fmaxf(m, warp_max(z));
+        const float back = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        const float w_mine = z == -INFINITY ? 0.f : fast_exp2(z - top);
+        m = top;
+        sum = sum * back + warp_sum(w_mine);
+        acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
+        const int left = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < left; ++i) {
+            const int p = __shfl_sync(0xffffffffu, mine, i);
+            const float w = __shfl_sync(0xffffffffu, w_mine, i);
+            const float4 x =
+                __ldg(reinterpret_cast<const float4*>(prm.slot_o + (int64_t)p * D) + lane);
+            if (w > 0.f) {  // a place that nobody wrote holds anything
+                acc.x = fmaf(w, x.x, acc.x);
+                acc.y = fmaf(w, x.y, acc.y);
+                acc.z = fmaf(w, x.z, acc.z);
+                acc.w = fmaf(w, x.w, acc.w);
             }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (w[u] > 0.f) {
-                acc.x = fmaf(w[u], x[u].x, acc.x);
-                acc.y = fmaf(w[u], x[u].y, acc.y);
-                acc.z = fmaf(w[u], x[u].z, acc.z);
-                acc.w = fmaf(w[u], x[u].w, acc.w);
-            }
     }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     uint2 o;
-    o.x = pack_bf16x2(acc.x, acc.y);
-    o.y = pack_bf16x2(acc.z, acc.w);
+    o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+    o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
     reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)orow * D)[lane] = o;
-    if (lane == 0 && a.lse) a.lse[orow] = lse;
+    if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
+// ------------------------------------------------------------------ prefixes of codes
+
+// The codes of every group's prefix as bf16 values: a prefix of several blocks is read by
+// each of them.  grid (blocks, groups); a thread takes 8 codes of K and of V at a time, so
+// that a warp's loads and stores are whole lines.
 template <int KV>
-cudaError_t launch_typed(const CUtensorMap& own_map, const CUtensorMap& block_map,
-                         const CUtensorMap& kmap, const CUtensorMap& vmap, const Params& prm,
-                         int num_ctas, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) widen_kernel(const Params prm) {
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const AttnArgs& a = prm.a;
+    const int g = blockIdx.y, lane = threadIdx.x & 31;
+    // the group's whole pages, as build_list finds them (a group that is no range of
+    // sequences shares nothing there)
+    int lo = max(0, min(a.B, __ldg(prm.group_starts + g)));
+    for (int i = lane; i < g; i += 32) lo = max(lo, min(a.B, __ldg(prm.group_starts + i)));
+    lo = (int)__reduce_max_sync(0xffffffffu, lo);
+    const int hi = max(lo, min(a.B, __ldg(prm.group_starts + g + 1)));
+    if (hi - lo < 2) return;
+    int least = INT32_MAX;
+    const int64_t cap = (int64_t)a.max_pages * a.P - a.k;
+    for (int b = lo + lane; b < hi; b += 32)
+        least = min(least, (int)max((int64_t)0, min(cap, (int64_t)__ldg(a.ctx_lens + b))));
+    least = __reduce_min_sync(0xffffffffu, least);
+    const int s = min(least, __ldg(prm.shared_lens + g));
+    if (s < kMinShared) return;
+    const int shift = 31 - __clz(a.P), per = a.P * D / 8;  // pieces of a (page, kv-head)
+    const int64_t all = (int64_t)(s >> shift) * a.Hkv * per, step = (int64_t)gridDim.x * 256;
+    const uint2* kc = static_cast<const uint2*>(a.k_cache);
+    const uint2* vc = static_cast<const uint2*>(a.v_cache);
+    uint4* ko = reinterpret_cast<uint4*>(prm.k_prefix);
+    uint4* vo = reinterpret_cast<uint4*>(prm.v_prefix);
+    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < all; i0 += 2 * step) {
+        uint2 k[2], v[2];
+        int64_t to[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t i = i0 + u * step;
+            if (i >= all) continue;
+            const int piece = (int)(i & (per - 1));
+            const uint32_t block = (uint32_t)(i >> (shift + 4));  // page of the prefix, kv-head
+            const uint32_t n = block / (uint32_t)a.Hkv, h = block - n * a.Hkv;
+            int page = __ldg(a.block_table + (int64_t)lo * a.max_pages + n);
+            if (page < 0 || page >= a.num_pages) page = 0;  // flagged by the attention kernel
+            const int64_t from = ((int64_t)page * a.Hkv + h) * per + piece;
+            to[u] = (((int64_t)g * a.max_pages + n) * a.Hkv + h) * per + piece;
+            k[u] = __ldg(kc + from);
+            v[u] = __ldg(vc + from);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (i0 + u * step >= all) continue;
+            ko[to[u]] = widen8<KV>(k[u]);
+            vo[to[u]] = widen8<KV>(v[u]);
+        }
+    }
+}
+
+// Bytes of the widened prefixes, K and V, or 0 where they are widened tile by tile: with one
+// block a group (256 query rows of a kv-head) on average, or too large a table.
+size_t prefix_bytes(const AttnArgs& a, int groups) {
+    if (a.kv_dtype == SPEC_DTYPE_BF16) return 0;
+    const int64_t G = a.Hq / a.Hkv, rows = (int64_t)a.B * a.k * G;
+    const int64_t all = (int64_t)groups * a.max_pages * a.Hkv * a.P;  // rows of K
+    if (rows < 2 * 2 * ROWS * (int64_t)groups || all >= kMaxPrefixRows) return 0;
+    return (size_t)all * D * 2 * 2;
+}
+
+struct Maps {
+    CUtensorMap own, block, k, v, kwide, vwide;
+};
+
+template <int KV>
+cudaError_t launch_typed(const Maps& m, const Params& prm, int num_ctas, cudaStream_t stream) {
     auto kern = attn_shared_kernel<KV>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)SMEM_BYTES);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3(num_ctas), dim3(threads<KV>()), SMEM_BYTES, stream, own_map,
-                            block_map, kmap, vmap, prm);
+    if constexpr (KV != KV_BF16) {
+        if (prm.k_prefix) {
+            const AttnArgs& a = prm.a;
+            const int64_t pieces = (int64_t)a.max_pages * a.Hkv * a.P * D / 16 / 256 + 1;
+            const int64_t want = (num_ctas * 8 + prm.groups - 1) / prm.groups;
+            e = launch_dependent(widen_kernel<KV>,
+                                 dim3((unsigned)(pieces < want ? pieces : want), (unsigned)prm.groups),
+                                 dim3(256), 0, stream, prm);
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return launch_dependent(kern, dim3(num_ctas), dim3(threads<KV>()), SMEM_BYTES, stream, m.own,
+                            m.block, m.k, m.v, m.kwide, m.vwide, prm);
 }
 
 }  // namespace
@@ -1244,13 +1399,14 @@ bool shared_supported(const AttnArgs& a, int groups) {
     // tile and cost counts are 32-bit (a charge of up to 256 tiles a segment)
     const int64_t tiles = ((int64_t)a.max_pages * a.P + TN - 1) / TN + 1;
     return tiles < (1LL << 31) && segs * (256 + kWideCost * tiles) < (1LL << 31) / a.Hkv &&
-           (int64_t)a.num_pages * a.Hkv * a.P < (1LL << 31) && tokens * a.Hq < (1LL << 28);
+           (int64_t)a.num_pages * a.Hkv * a.P < (1LL << 31) && tokens * a.Hq < (1LL << 28) &&
+           a.Hkv < 65536;
 }
 
-size_t shared_workspace_bytes(const AttnArgs& a, int num_ctas) {
+size_t shared_workspace_bytes(const AttnArgs& a, int groups, int num_ctas) {
     const size_t rows = (size_t)a.B * a.k * a.Hq, slots = (size_t)8 * num_ctas * ROWS;
-    return (2 * rows + slots) * (D + 1) * sizeof(float) + ((size_t)3 * num_ctas + 2) * 4 +
-           (size_t)(MAX_SEGS + 4) * 4 + (size_t)a.B * 16 + 64;
+    return prefix_bytes(a, groups) + (2 * rows + slots) * (D + 1) * sizeof(float) +
+           ((size_t)3 * num_ctas + 2) * 4 + (size_t)(MAX_SEGS + 4) * 4 + (size_t)a.B * 16 + 64;
 }
 
 cudaError_t launch_attn_shared(const AttnArgs& a, const int32_t* group_starts,
@@ -1259,69 +1415,80 @@ cudaError_t launch_attn_shared(const AttnArgs& a, const int32_t* group_starts,
     EncodeTiledFn encode = get_encode_fn();
     if (!encode) return cudaErrorNotSupported;
     const int G = a.Hq / a.Hkv;
-    CUtensorMap qmap[2], kmap, vmap;
+    Params prm;
+    prm.a = a;
+    prm.group_starts = group_starts;
+    prm.shared_lens = shared_lens;
+    prm.groups = groups;
+    const size_t wide = prefix_bytes(a, groups);
+    prm.k_prefix = wide ? static_cast<__nv_bfloat16*>(workspace) : nullptr;
+    prm.v_prefix = wide ? prm.k_prefix + wide / 4 : nullptr;
+    const size_t nrows = (size_t)a.B * a.k * a.Hq, slots = (size_t)8 * num_ctas * ROWS;
+    prm.slot_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + wide);
+    prm.slot_lse = prm.slot_o + (slots + 2 * nrows) * D;
+    prm.slots = (int)slots;
+    prm.G = G;
+    prm.NT = ROWS / G;
+    // (the fp32 arrays together are a multiple of 16 bytes)
+    prm.seq_block = reinterpret_cast<int4*>(prm.slot_lse + slots + (2 * nrows + 3) / 4 * 4);
+    prm.n_begin = reinterpret_cast<int*>(prm.seq_block + a.B);
+    prm.w_begin = prm.n_begin + 2 * num_ctas + 1;
+    prm.tile_pre = prm.w_begin + num_ctas + 1;
+
+    Maps m;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
     for (int t = 0; t < 2; ++t) {
         cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.B * a.k};
         cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.Hq * D * 2};
         cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(t ? ROWS / G : a.k)};
-        cuuint32_t es[3] = {1, 1, 1};
-        if (encode(&qmap[t], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims,
-                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+        if (encode(t ? &m.block : &m.own, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q),
+                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
     // K / V rows as in the 128-key kernel: bf16 as [groups of g rows] x [2 halves]
     // x [g rows] x [64 columns], g = 8 (K) or 16 (V); codes row by row
-    const cuuint64_t rows = (cuuint64_t)a.num_pages * a.Hkv * a.P;
     const cuuint32_t ch = (cuuint32_t)(a.P < TN ? a.P : TN);
-    const bool codes = a.kv_dtype != SPEC_DTYPE_BF16;
-    for (int t = 0; t < 2; ++t) {
-        void* cache = const_cast<void*>(t == 0 ? a.k_cache : a.v_cache);
-        CUresult res;
-        if (codes) {
-            cuuint64_t dims[2] = {(cuuint64_t)D, rows};
-            cuuint64_t strides[1] = {(cuuint64_t)D};
-            cuuint32_t box[2] = {(cuuint32_t)D, ch};
-            cuuint32_t es[2] = {1, 1};
-            res = encode(t == 0 ? &kmap : &vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, cache, dims,
-                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        } else {
-            const cuuint32_t g = t == 0 ? 8 : 16;
-            cuuint64_t dims[4] = {64, g, 2, rows / g};
-            cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)g * D * 2};
-            cuuint32_t box[4] = {64, g, 2, ch / g};
-            cuuint32_t es[4] = {1, 1, 1, 1};
-            res = encode(t == 0 ? &kmap : &vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, cache, dims,
-                         strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    auto map16 = [&](CUtensorMap* map, const void* base, cuuint64_t rows, cuuint32_t g) {
+        cuuint64_t dims[4] = {64, g, 2, rows / g};
+        cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)g * D * 2};
+        cuuint32_t box[4] = {64, g, 2, ch / g};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                      box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    auto map8 = [&](CUtensorMap* map, const void* base, cuuint64_t rows) {
+        cuuint64_t dims[2] = {(cuuint64_t)D, rows};
+        cuuint64_t strides[1] = {(cuuint64_t)D};
+        cuuint32_t box[2] = {(cuuint32_t)D, ch};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                      es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t rows = (cuuint64_t)a.num_pages * a.Hkv * a.P;
+    bool ok;
+    if (a.kv_dtype == SPEC_DTYPE_BF16) {
+        ok = map16(&m.k, a.k_cache, rows, 8) && map16(&m.v, a.v_cache, rows, 16);
+        m.kwide = m.k;
+        m.vwide = m.v;
+    } else {
+        ok = map8(&m.k, a.k_cache, rows) && map8(&m.v, a.v_cache, rows);
+        m.kwide = m.k;
+        m.vwide = m.v;
+        if (ok && wide) {
+            const cuuint64_t n = (cuuint64_t)groups * a.max_pages * a.Hkv * a.P;
+            ok = map16(&m.kwide, prm.k_prefix, n, 8) && map16(&m.vwide, prm.v_prefix, n, 16);
         }
-        if (res != CUDA_SUCCESS) return cudaErrorInvalidValue;
     }
-    Params prm;
-    prm.a = a;
-    prm.group_starts = group_starts;
-    prm.shared_lens = shared_lens;
-    prm.groups = groups;
-    const size_t nrows = (size_t)a.B * a.k * a.Hq, slots = (size_t)8 * num_ctas * ROWS;
-    prm.slot_o = static_cast<float*>(workspace);
-    prm.home_o = prm.slot_o + slots * D;
-    prm.slot_lse = prm.home_o + 2 * nrows * D;
-    prm.home_lse = prm.slot_lse + slots;
-    // (the fp32 arrays together are a multiple of 16 bytes)
-    prm.seq_block = reinterpret_cast<int4*>(prm.home_lse + (2 * nrows + 3) / 4 * 4);
-    prm.n_begin = reinterpret_cast<int*>(prm.seq_block + a.B);
-    prm.w_begin = prm.n_begin + 2 * num_ctas + 1;
-    prm.tile_pre = prm.w_begin + num_ctas + 1;
-    const cudaError_t e =
-        a.kv_dtype == SPEC_DTYPE_I8
-            ? launch_typed<KV_I8>(qmap[0], qmap[1], kmap, vmap, prm, num_ctas, stream)
-        : a.kv_dtype == SPEC_DTYPE_E4M3
-            ? launch_typed<KV_E4M3>(qmap[0], qmap[1], kmap, vmap, prm, num_ctas, stream)
-            : launch_typed<KV_BF16>(qmap[0], qmap[1], kmap, vmap, prm, num_ctas, stream);
+    if (!ok) return cudaErrorInvalidValue;
+    const cudaError_t e = a.kv_dtype == SPEC_DTYPE_I8     ? launch_typed<KV_I8>(m, prm, num_ctas, stream)
+                          : a.kv_dtype == SPEC_DTYPE_E4M3 ? launch_typed<KV_E4M3>(m, prm, num_ctas, stream)
+                                                          : launch_typed<KV_BF16>(m, prm, num_ctas, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.B * a.Hkv), (unsigned)((a.k * G + kJoinWarps - 1) / kJoinWarps));
+    const dim3 grid((unsigned)a.B, (unsigned)a.Hkv, (unsigned)((a.k * G + kJoinWarps - 1) / kJoinWarps));
     return launch_dependent(join_kernel, grid, dim3(kJoinWarps * 32), 0, stream, prm, num_ctas);
 }
 

@@ -332,7 +332,7 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     if (groups) {
         int ctas = (int)g_opt_ctas.load();
         if (ctas <= 0) ctas = ws->sms;
-        rc = get_workspace(specv::shared_workspace_bytes(a, ctas), st, &ws);
+        rc = get_workspace(specv::shared_workspace_bytes(a, num_groups, ctas), st, &ws);
         if (rc) return rc;
         a.dev_err = static_cast<int*>(ws->base);
         e = specv::launch_attn_shared(a, group_starts, shared_lens, num_groups, ctas,
