@@ -271,8 +271,8 @@ struct LogprobArgs {
     const int32_t* lens;  // [B] or null: n
     int32_t B, n;
     int64_t V;
-    double temperature;
-    float c;  // log2(e) / temperature
+    float inv_t;  // 1 / temperature
+    float c;      // log2(e) / temperature
     int32_t K;
     float* logprob;
     float* entropy;       // or null

@@ -7,7 +7,7 @@
 // (the entropy as a difference of two terms of its own size, not of lse and a
 // mean of z).  x - m comes before the product, so an exponent near zero is
 // exact; l and a are held in fp32 per thread over a few hundred terms and
-// merged by their maxima, the logarithm and what is written are taken in 64 bits.
+// merged by their maxima.
 //
 // What bounds it: the logits are read once.  An element costs ~5 issue slots
 // (widen, subtract, scale, clamp, 2^y, two sums), about half of what an SM has
@@ -18,13 +18,17 @@
 // in flight.  With S > 1 the CTA that takes the row's last ticket merges the
 // parts; no CTA waits on another.
 //
-// Top alternatives, K <= 32.  In a part's first round the K-th largest of the
-// 256 threads' maxima (value, then lower index) is a bound that K elements
-// reach: only those at or above it go to a list in shared memory, at most
-// (K - 1) * 32 + 1 of them whatever the values, about K for values in no
-// order.  Later rounds append what exceeds the K-th best so far; a list past
-// 128 entries is ranked (each entry counts the better ones) and cut to K, and
-// a round that would overflow it takes a bound of its own first.
+// Top alternatives, K <= 32.  In a part's first round the K-th largest of the maxima of
+// 64 groups of threads is a bound that K elements reach: only those at or above it go to
+// a list in shared memory, about K + a few for values in no order, and later rounds append
+// what exceeds it.  Every kCheck rounds the threads meet; a list past 128 entries is
+// ranked (each entry counts the better ones) and cut to K, whose last is the bound from
+// then on.  Where the list overflowed meanwhile (many equal or rising values) the rounds
+// since are read once more, each with a bound over the 256 threads' maxima by value and
+// index, which at most (K - 1) * 32 + 1 elements of a round reach, whatever they are.
+// Meeting in every round made rows of 152064 take 1.5 times as long.
+// The rare parts are rolled loops, in line: unrolled, the kernel had 78 KB of code; as
+// function calls they made the compiler wait for the next round's loads at every call.
 #include <limits.h>
 #include <math.h>
 
@@ -37,6 +41,7 @@ constexpr int kThreads = 256;
 constexpr int kVecs = 4;          // 16-byte loads of a thread per round
 constexpr int kCap = 2048;        // list entries
 constexpr int kSoft = 128;        // list length that is cut to K
+constexpr int kCheck = 4;         // rounds between two looks at the list
 constexpr int kMaxParts = 32;
 constexpr float kFarBelow = -1000.f;  // 2^y is +0 there; keeps -inf out of products
 
@@ -90,35 +95,49 @@ template <> __device__ __forceinline__ void widen<__nv_bfloat16>(const uint4& r,
     }
 }
 
-// Vector v of a row: elements v * EPV - off .. of [0, V), -inf outside.  The
-// vectors lie on the 16-byte grid of memory; one that is not whole is read
-// element by element, so nothing outside the row is.
-template <typename T>
-__device__ __forceinline__ uint4 load_vec(const T* row, int64_t V, int off, int64_t v) {
+// Largest element of a vector.
+template <typename T> __device__ __forceinline__ float max_of(const uint4& r) {
     constexpr int EPV = per_vec<T>();
-    const int64_t e = v * EPV - off;
-    if (e >= 0 && e + EPV <= V) {
-        uint4 r;
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                     : "l"(row + e));
-        return r;
-    }
-    alignas(16) T x[EPV];
+    float e[EPV];
+    widen<T>(r, e);
+    float m = fmaxf(e[0], e[1]);
 #pragma unroll
-    for (int i = 0; i < EPV; ++i)
-        x[i] = e + i >= 0 && e + i < V ? row[e + i] : Elem<T>::from_f32(-INFINITY);
-    return *reinterpret_cast<const uint4*>(x);
+    for (int j = 2; j < EPV; j += 2) m = fmax3(m, e[j], e[j + 1]);
+    return m;
+}
+
+// Vector v of a row: elements v * EPV - off .. of [0, V), -inf outside and for v >= end.
+// The vectors lie on the 16-byte grid of memory; one that is not whole is read element by
+// element, so nothing outside the row is.
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const T* row, int V, int off, int v, int end) {
+    constexpr int EPV = per_vec<T>(), EPW = EPV / 4;
+    const int64_t e = (int64_t)v * EPV - off;
+    if (v < end && e >= 0 && e + EPV <= V) return __ldg(reinterpret_cast<const uint4*>(row + e));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int i = 0; i < EPV; ++i) {
+        const T x = v < end && e + i >= 0 && e + i < V ? row[e + i] : Elem<T>::from_f32(-INFINITY);
+        uint32_t bits;
+        if constexpr (sizeof(T) == 4) bits = __float_as_uint(x);
+        else bits = (uint32_t)__bfloat16_as_ushort(x) << (16 * (i & 1));
+        const int j = i / EPW;
+        w[0] |= j == 0 ? bits : 0;
+        w[1] |= j == 1 ? bits : 0;
+        w[2] |= j == 2 ? bits : 0;
+        w[3] |= j == 3 ? bits : 0;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct Shared {
     float v[kCap];
     int i[kCap];
-    float tv[kThreads];  // the threads' maxima
+    alignas(16) float tv[kThreads];  // maxima of the groups or threads
     int ti[kThreads];
     float best_v[32];
     int best_i[32];
-    Stats stats[kThreads / 32];
+    float4 stats[kThreads / 32];
     float bound_v;
     int bound_i;
     int count, last;
@@ -128,10 +147,12 @@ struct Shared {
 // the front (every thread calls it; the list is complete and visible).
 __device__ __forceinline__ int cut(Shared& s, int count, int K) {
     const int tid = threadIdx.x;
+#pragma unroll 1
     for (int e = tid; e < count; e += kThreads) {
         const float v = s.v[e];
         const int i = s.i[e];
         int rank = 0;
+#pragma unroll 4
         for (int o = 0; o < count; ++o) rank += better(s.v[o], s.i[o], v, i);
         if (rank < K) {
             s.best_v[rank] = v;
@@ -149,78 +170,160 @@ __device__ __forceinline__ int cut(Shared& s, int count, int K) {
     return kept;
 }
 
-// What is written for a row: stats complete, the sorted alternatives in s.
+// Appends the elements of a thread's round (vectors cur with maxima vm, elements from
+// `first` on, `stride` apart) that lie above `above` and reach the bound (bv at index bx at
+// the latest, or at any index: INT_MAX); returns the last place taken, -1 for none.  Most
+// calls find one element: a vector whose maximum is too small is not looked into.
+template <typename T>
+__device__ __forceinline__ int append(Shared& s, const uint4 (&cur)[kVecs], const float (&vm)[kVecs],
+                                      int first, float above, float bv, int bx) {
+    constexpr int EPV = per_vec<T>(), EPW = EPV / 4;  // elements of a vector, of a word
+    int place = -1;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+        if (!(vm[u] > above && vm[u] >= bv)) continue;
+        float e[EPV];
+        widen<T>(cur[u], e);
+        const int at = first + u * kThreads * EPV;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int j = 0; j < EPV; ++j)
+            bits |= (uint32_t)(e[j] > above && !better(bv, bx, e[j], at + j)) << j;
+#pragma unroll 1
+        for (; bits; bits &= bits - 1) {
+            const int j = __ffs(bits) - 1, q = j / EPW;
+            const uint32_t w = q == 0 ? cur[u].x : q == 1 ? cur[u].y : q == 2 ? cur[u].z : cur[u].w;
+            place = atomicAdd(&s.count, 1);
+            if (place < kCap) {
+                s.v[place] = __uint_as_float(EPW == 1 ? w : j & 1 ? w & 0xffff0000u : w << 16);
+                s.i[place] = at + j;
+            }
+        }
+    }
+    return place;
+}
+
+// Index of the first element of a thread's round that equals v.
+template <typename T>
+__device__ __forceinline__ int index_of(uint4 c0, uint4 c1, uint4 c2, uint4 c3, int first, float v) {
+    constexpr int EPV = per_vec<T>(), EPW = EPV / 4;
+#pragma unroll 1
+    for (int e = 0; e < kVecs * EPV; ++e) {
+        const int u = e / EPV, j = e % EPV / EPW, h = e % EPW;
+        const uint4 r = u == 0 ? c0 : u == 1 ? c1 : u == 2 ? c2 : c3;
+        const uint32_t w = j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
+        if (__uint_as_float(EPW == 1 ? w : h ? w & 0xffff0000u : w << 16) == v)
+            return first + u * kThreads * EPV + e % EPV;
+    }
+    return INT_MAX;
+}
+
+// What is written for a row: stats complete, the sorted alternatives in s.  (fp32: on this
+// GPU a 64-bit logarithm by every warp took longer than the row.)
 template <typename T>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, Shared& s, const Stats& st, int64_t row,
-                                          const T* x, int found) {
+                                          float token, int found) {
     const int tid = threadIdx.x;
+    if (tid >= 32) return;
     const bool none = st.l == 0.f;  // every logit is -inf
-    const double lnl = log((double)st.l), t = a.temperature;
-    const double lse = none ? 0.0 : (double)st.m / t + lnl;
+    const float lnl = logf(st.l);
+    // z - lse = (x - m) / T - ln l, from the difference on
+    auto lp = [&](float x) { return none ? -INFINITY : (x - st.m) * a.inv_t - lnl; };
     if (tid == 0) {
-        const int tok = a.tokens[row];
-        float lp = -INFINITY;
-        if (tok < 0 || tok >= a.V) raise_device_error(a.dev_err, SPEC_DEVERR_TOKEN);
-        else if (!none) lp = (float)((double)Elem<T>::to_f32(x[tok]) / t - lse);
-        a.logprob[row] = lp;
-        if (a.entropy)
-            a.entropy[row] = none ? 0.f : (float)(lnl - 0.69314718055994530942 * ((double)st.a / st.l));
+        a.logprob[row] = lp(token);
+        if (a.entropy) a.entropy[row] = none ? 0.f : lnl - 0.69314718055994530942f * (st.a / st.l);
     }
     if (tid < a.K) {
         const bool have = tid < found;
         if (a.top_ids) a.top_ids[row * a.K + tid] = have ? s.i[tid] : -1;
-        if (a.top_logprobs)
-            a.top_logprobs[row * a.K + tid] = have ? (float)((double)s.v[tid] / t - lse) : -INFINITY;
+        if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = have ? lp(s.v[tid]) : -INFINITY;
     }
 }
 
+// The K-th largest of the maxima of 64 groups of four threads (bm: a thread's), which K
+// elements reach; -inf if there are fewer.
+__device__ __forceinline__ float bound_of_groups(Shared& s, float bm, int K) {
+    const int tid = threadIdx.x;
+    float g = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if ((tid & 3) == 0) s.tv[tid >> 2] = g;
+    __syncthreads();
+    if (tid < 64) {
+        const float mine = s.tv[tid];
+        int rank = 0;
+#pragma unroll 4
+        for (int o = 0; o < 64; o += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(&s.tv[o]);
+            rank += (q.x > mine || (q.x == mine && o < tid)) + (q.y > mine || (q.y == mine && o + 1 < tid)) +
+                    (q.z > mine || (q.z == mine && o + 2 < tid)) +
+                    (q.w > mine || (q.w == mine && o + 3 < tid));
+        }
+        if (rank == K - 1) s.bound_v = mine;
+    }
+    __syncthreads();
+    return s.bound_v;
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(const LogprobArgs a) {
     constexpr int EPV = per_vec<T>();
     __shared__ Shared s;
     const int tid = threadIdx.x, S = a.parts, K = a.K;
-    const int64_t row = blockIdx.x / S;
-    const int part = blockIdx.x - (int)row * S;
-    if (tid == 0) s.count = 0;
+    const int row = blockIdx.x / (uint32_t)S, part = blockIdx.x - row * S;
+    if (tid == 0) {
+        s.count = 0;
+        s.bound_v = -INFINITY;
+    }
     grid_dep_launch_dependents();
     grid_dep_wait();
-    if (a.lens && (int)(row % a.n) >= a.lens[row / a.n]) return;
+    if (a.lens) {
+        const int b = (uint32_t)row / (uint32_t)a.n;
+        if (row - b * a.n >= __ldg(a.lens + b)) return;
+    }
 
-    const T* x = static_cast<const T*>(a.logits) + row * a.V;
-    const int off = (int)(((uint64_t)row * (uint64_t)a.V) % EPV);
-    const int64_t vecs = (a.V + off + EPV - 1) / EPV, per = (vecs + S - 1) / S;
-    const int64_t v0 = part * per, v1 = v0 + per < vecs ? v0 + per : vecs;
+    const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.V;
+    // vectors of 16 bytes on memory's grid (indexes inside a row are 32-bit)
+    const int V = (int)a.V, off = (int)(((uint64_t)row * (uint64_t)a.V) % EPV);
+    const int vecs = (int)(((int64_t)V + off + EPV - 1) / EPV), per = (vecs + S - 1) / S;
+    const int v0 = part * per, v1 = min(v0 + per, vecs);
     const float c = a.c;
-    Stats st;
     uint64_t l2 = f2(0.f, 0.f), a2 = l2;
     float m = -INFINITY;
-    float tau = -INFINITY;  // the K-th best of the rounds before (-inf: fewer than K)
+    // what an element has to exceed: K elements of the rounds before reach it
+    float tau = -INFINITY;
+    int checked = v0;  // first vector of the rounds since the list was looked at
 
     uint4 cur[kVecs], nxt[kVecs];
-    auto fetch = [&](uint4 (&r)[kVecs], int64_t v) {
+    // (of a round that lies whole inside the row no vector is looked at singly)
+    auto fetch = [&](uint4 (&r)[kVecs], int v) {
+        if (v + kVecs * kThreads <= v1 && (v > 0 || off == 0) && (int64_t)(v + kVecs * kThreads) * EPV - off <= V) {
+            const uint4* p = reinterpret_cast<const uint4*>(x - off) + v + tid;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int64_t at = v + u * kThreads + tid;
-            r[u] = at < v1 ? load_vec(x, a.V, off, at)
-                           : (sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
-                                             : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u));
+            for (int u = 0; u < kVecs; ++u)
+                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[u].x), "=r"(r[u].y), "=r"(r[u].z), "=r"(r[u].w)
+                             : "l"(p + u * kThreads));
+        } else {
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u)
+                r[u] = load_edge<T>(x, V, off, v + u * kThreads + tid, v1);
         }
     };
+    // the given token and, once it is known, its logit (thread 0)
+    const int tok = tid == 0 ? __ldg(a.tokens + row) : 0;
+    float token = -INFINITY;
     fetch(cur, v0);
-    for (int64_t v = v0; v < v1; v += kVecs * kThreads) {
-        fetch(nxt, v + kVecs * kThreads);
-        float bm = -INFINITY;
+#pragma unroll 1
+    for (int v = v0; v < v1; v += kVecs * kThreads) {
+        if (v + kVecs * kThreads < v1) fetch(nxt, v + kVecs * kThreads);
+        float vm[kVecs];
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            float e[EPV];
-            widen<T>(cur[u], e);
-#pragma unroll
-            for (int j = 0; j < EPV; j += 2) bm = fmax3(bm, e[j], e[j + 1]);
-        }
+        for (int u = 0; u < kVecs; ++u) vm[u] = max_of<T>(cur[u]);
+        const float bm = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
         if (bm > m) {
+            float p, q;
             Stats old;
             old.m = m;
-            float p, q;
             f2_split(l2, p, q);
             old.l = p + q;
             f2_split(a2, p, q);
@@ -249,75 +352,73 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
                 }
             }
         }
+        if (v == v0 && tid == 0) {
+            if (tok >= 0 && tok < V) token = Elem<T>::to_f32(x[tok]);
+            else if (part == 0) raise_device_error(a.dev_err, SPEC_DEVERR_TOKEN);
+        }
         if (TOP) {
-            const bool first = v == v0;
-            const int base = (int)(v * EPV - off);  // first element of the round
-            // appends this round's elements that `want` takes; the last place taken
-            auto append = [&](auto want) {
-                int place = -1;
+            constexpr int kRound = kVecs * kThreads;
+            const int at = (v + tid) * EPV - off;
+            if (v == v0) {
+                const float bv = bound_of_groups(s, bm, K);
+                if (bm >= bv) append<T>(s, cur, vm, at, -INFINITY, bv, INT_MAX);
+                tau = bv;
+            } else if (bm > tau) {
+                append<T>(s, cur, vm, at, tau, -INFINITY, INT_MAX);
+            }
+            const bool end = v + kRound >= v1;
+            if (end || v == v0 || (v - checked) >= (kCheck - 1) * kRound) {
+                __syncthreads();
+                int count = s.count;
+                if (count > kCap) {
+                    // entries from before (at most kSoft) stand in front
+                    const int before =
+                        v == v0 ? 0 : __syncthreads_count(tid < kSoft && s.i[tid] < checked * EPV - off);
+                    if (v == v0) tau = -INFINITY;
+                    __syncthreads();
+                    if (tid == 0) s.count = before;
+#pragma unroll 1
+                    for (int w = checked; w <= v; w += kRound) {
+                        fetch(cur, w);
+                        const int first = (w + tid) * EPV - off;
 #pragma unroll
-                for (int u = 0; u < kVecs; ++u) {
-                    float e[EPV];
-                    widen<T>(cur[u], e);
-                    const int at = base + (u * kThreads + tid) * EPV;
-#pragma unroll
-                    for (int j = 0; j < EPV; ++j)
-                        if (want(e[j], at + j)) {
-                            place = atomicAdd(&s.count, 1);
-                            if (place < kCap) {
-                                s.v[place] = e[j];
-                                s.i[place] = at + j;
-                            }
+                        for (int u = 0; u < kVecs; ++u) vm[u] = max_of<T>(cur[u]);
+                        const float top = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
+                        const int bi = index_of<T>(cur[0], cur[1], cur[2], cur[3], first, top);
+                        s.tv[tid] = top;
+                        s.ti[tid] = bi;
+                        if (tid == 0) {
+                            s.bound_v = -INFINITY;
+                            s.bound_i = INT_MAX;
                         }
+                        __syncthreads();
+                        int rank = 0;
+#pragma unroll 1
+                        for (int o = 0; o < kThreads; ++o) rank += better(s.tv[o], s.ti[o], top, bi);
+                        if (rank == K - 1 && top > -INFINITY) {
+                            s.bound_v = top;
+                            s.bound_i = bi;
+                        }
+                        __syncthreads();
+                        append<T>(s, cur, vm, first, tau, s.bound_v, s.bound_i);
+                        __syncthreads();
+                        count = s.count;
+                        cut(s, count, K);
+                        if (count >= K) tau = s.v[K - 1];
+                        __syncthreads();
+                    }
+                } else if (count > kSoft && !end) {
+                    cut(s, count, K);
+                    tau = s.v[K - 1];
+                    __syncthreads();  // before the next round appends
                 }
-                return place;
-            };
-            int place = -1;
-            if (!first && bm > tau) place = append([&](float e, int) { return e > tau; });
-            if (__syncthreads_or(first || place >= kSoft)) {
-                int count = first ? 0 : s.count;
-                if (first || count > kCap) {
-                    // entries of earlier rounds (fewer than kSoft) stand in front
-                    const int before = first ? 0 : __syncthreads_count(tid < kSoft && s.i[tid] < base);
-                    int bi = INT_MAX;
-#pragma unroll
-                    for (int u = kVecs - 1; u >= 0; --u) {
-                        float e[EPV];
-                        widen<T>(cur[u], e);
-#pragma unroll
-                        for (int j = EPV - 1; j >= 0; --j)
-                            if (e[j] == bm) bi = base + (u * kThreads + tid) * EPV + j;
-                    }
-                    s.tv[tid] = bm;
-                    s.ti[tid] = bi;
-                    if (tid == 0) {
-                        s.count = before;
-                        s.bound_v = -INFINITY;
-                        s.bound_i = INT_MAX;
-                    }
-                    __syncthreads();
-                    int rank = 0;
-                    for (int o = 0; o < kThreads; ++o) rank += better(s.tv[o], s.ti[o], bm, bi);
-                    if (rank == K - 1 && bm > -INFINITY) {
-                        s.bound_v = bm;
-                        s.bound_i = bi;
-                    }
-                    __syncthreads();
-                    const float bv = s.bound_v;
-                    const int bx = s.bound_i;
-                    if (bm > tau && bm >= bv)
-                        append([&](float e, int i) { return e > tau && !better(bv, bx, e, i); });
-                    __syncthreads();
-                    count = s.count;
-                }
-                cut(s, count, K);
-                tau = count >= K ? s.v[K - 1] : -INFINITY;
-                __syncthreads();  // before the next round appends
+                checked = v + kRound;
             }
         }
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) cur[u] = nxt[u];
     }
+    Stats st;
     st.m = m;
     {
         float p, q;
@@ -327,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         st.a = p + q;
     }
     // the CTA's sums
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o > 0; o >>= 1) {
         Stats other;
         other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
@@ -335,58 +436,93 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(const LogprobArgs 
         other.a = __shfl_xor_sync(0xffffffffu, st.a, o);
         st.merge(other, c);
     }
-    if ((tid & 31) == 0) s.stats[tid >> 5] = st;
+    if ((tid & 31) == 0) s.stats[tid >> 5] = make_float4(st.m, st.l, st.a, 0.f);
     __syncthreads();
-    st = s.stats[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) st.merge(s.stats[w], c);
-    int found = 0;
-    if (TOP) found = cut(s, s.count, K);
-
-    if (S == 1) {
-        write_row<T>(a, s, st, row, x, found);
-        return;
-    }
-    // ---- parts: leave this one's record; the last CTA of the row merges them
-    const int64_t rec = row * S + part;
-    float* pst = a.part_stats + rec * 4;
-    if (TOP && tid < K) {
-        a.part_v[rec * K + tid] = tid < found ? s.v[tid] : -INFINITY;
-        a.part_i[rec * K + tid] = tid < found ? s.i[tid] : -1;
-    }
-    if (tid == 0) *reinterpret_cast<float4*>(pst) = make_float4(st.m, st.l, st.a, 0.f);
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        s.last = atomicAdd(&a.tickets[row], 1) == S - 1;
-        s.count = 0;
-    }
-    __syncthreads();
-    if (!s.last) return;
-    __threadfence();
-    if (tid == 0) a.tickets[row] = 0;
-    if (TOP) {
-        for (int e = tid; e < S * K; e += kThreads) {
-            const int i = __ldcg(a.part_i + row * S * K + e);
-            if (i >= 0) {
-                const int place = atomicAdd(&s.count, 1);
-                s.v[place] = __ldcg(a.part_v + row * S * K + e);
-                s.i[place] = i;
-            }
+    // sums in `from` of n parts (a warp: all that is needed further on)
+    auto gather = [&](const float4* from, int n) {
+        Stats sum;
+        if ((tid & 31) < n) {
+            const float4 r = __ldcg(from + (tid & 31));
+            sum.m = r.x;
+            sum.l = r.y;
+            sum.a = r.z;
+        }
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) {
+            Stats other;
+            other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
+            other.l = __shfl_xor_sync(0xffffffffu, sum.l, o);
+            other.a = __shfl_xor_sync(0xffffffffu, sum.a, o);
+            sum.merge(other, c);
+        }
+        return sum;
+    };
+    if (tid < 32) {
+        const float4 r = tid < kThreads / 32 ? s.stats[tid] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        st.m = r.x;
+        st.l = r.y;
+        st.a = r.z;
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) {
+            Stats other;
+            other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+            other.l = __shfl_xor_sync(0xffffffffu, st.l, o);
+            other.a = __shfl_xor_sync(0xffffffffu, st.a, o);
+            st.merge(other, c);
         }
     }
-    st = Stats();
-    for (int p = 0; p < S; ++p) {
-        const float4 r = __ldcg(reinterpret_cast<const float4*>(a.part_stats) + row * S + p);
-        Stats o;
-        o.m = r.x;
-        o.l = r.y;
-        o.a = r.z;
-        st.merge(o, c);
-    }
-    __syncthreads();
+    int found = 0;
     if (TOP) found = cut(s, s.count, K);
-    write_row<T>(a, s, st, row, x, found);
+    if (S > 1) {
+        // ---- parts: leave this one's record; the last CTA of the row merges them
+        const int64_t rec = (int64_t)row * S + part;
+        if (TOP && tid < K) {
+            a.part_v[rec * K + tid] = tid < found ? s.v[tid] : -INFINITY;
+            a.part_i[rec * K + tid] = tid < found ? s.i[tid] : -1;
+        }
+        if (tid == 0) reinterpret_cast<float4*>(a.part_stats)[rec] = make_float4(st.m, st.l, st.a, 0.f);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            s.last = atomicAdd(&a.tickets[row], 1) == S - 1;
+            s.count = 0;
+        }
+        __syncthreads();
+        if (!s.last) return;
+        __threadfence();
+        if (tid == 0) a.tickets[row] = 0;
+        // the parts' alternatives, up to four a thread, through a bound of their own
+        constexpr int kMine = kMaxParts * 32 / kThreads;
+        float w[kMine], bm = -INFINITY;
+        int id[kMine];
+        if (TOP) {
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) {
+                const int e = u * kThreads + tid;
+                w[u] = -INFINITY;
+                if (e < S * K) {
+                    w[u] = __ldcg(a.part_v + (int64_t)row * S * K + e);
+                    id[u] = __ldcg(a.part_i + (int64_t)row * S * K + e);
+                }
+                bm = fmaxf(bm, w[u]);
+            }
+        }
+        if (tid < 32) st = gather(reinterpret_cast<const float4*>(a.part_stats) + (int64_t)row * S, S);
+        if (TOP) {
+            if (tid == 0) s.bound_v = -INFINITY;
+            const float bv = bound_of_groups(s, bm, K);
+#pragma unroll
+            for (int u = 0; u < kMine; ++u)
+                if (w[u] >= bv && w[u] > -INFINITY) {
+                    const int place = atomicAdd(&s.count, 1);
+                    s.v[place] = w[u];
+                    s.i[place] = id[u];
+                }
+            __syncthreads();
+            found = cut(s, s.count, K);
+        }
+    }
+    write_row<T>(a, s, st, row, token, found);
 }
 
 }  // namespace

@@ -882,7 +882,8 @@ int spec_token_logprobs(const void* logits, int32_t logits_dtype, const int32_t*
     if (rc) return rc;
     specv::LogprobArgs a;
     a.logits = logits; a.dtype = logits_dtype; a.tokens = tokens; a.lens = lens;
-    a.B = batch; a.n = num_rows; a.V = vocab; a.temperature = temperature;
+    a.B = batch; a.n = num_rows; a.V = vocab;
+    a.inv_t = (float)(1.0 / (double)temperature);
     a.c = (float)(1.4426950408889634074 / (double)temperature);
     a.K = num_top; a.logprob = logprob; a.entropy = entropy; a.top_ids = top_ids;
     a.top_logprobs = top_logprobs;
