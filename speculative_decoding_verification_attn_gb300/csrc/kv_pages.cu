@@ -14,10 +14,12 @@
 //    fresh page (pairs before it, then blocks of pages before it, then bits), shares
 //    the whole pages, takes the fresh ones, and copies the rows of the page in
 //    use.
-// Release, one launch: a block per row; an exchange with -1 takes each entry
-// once, however often the row is listed.
-// All of it is launch latency and a few dependent round trips: a table row of
-// 2048 entries is 8 KB, a copy at most a page.
+// Release, one launch: a block per row (the first that lists it), eight entries of a
+// thread under way together.
+// All of it is launch latency, a few dependent round trips and the atomics on the counts:
+// a table row of 2048 entries is 8 KB, a copy at most a page.  240 rows of 1024 to 2048
+// pages released and forked again: 37 us with one entry of a thread at a time and an
+// exchange for each, see the table of figures for this form.
 //
 // Compaction, one launch: a block per (sequence, kv-head, tensor).  Row path[i]
 // goes to place i <= path[i], so blocks of rows in ascending order may be read
@@ -33,6 +35,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kScan = 8192;  // pages of a planning block
 constexpr float kE4m3Max = 448.f;
+constexpr int kBatch = 8;    // entries of a thread whose loads and atomics are under way together
 
 __device__ __forceinline__ int block_sum(int v, int* s_warp) {
 #pragma unroll
@@ -99,8 +102,9 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const ForkArgs a) {
                 bad |= SPEC_DEVERR_POOL;
         if (c != p && a.block_table[(int64_t)c * a.max_pages] >= 0) bad |= SPEC_DEVERR_POOL;
         if (!(bad & SPEC_DEVERR_CTX)) {
+#pragma unroll 8
             for (int i = tid; i < span.whole + (span.part > 0); i += kThreads) {
-                const int page = from[i];
+                const int page = __ldg(from + i);
                 if (page < 0 || page >= a.num_pages) bad |= SPEC_DEVERR_PAGE;
                 if (i == span.whole) src = page;
             }
@@ -248,10 +252,17 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkArgs a) 
     if (blockIdx.y) return;
 
     if (c != p) {
-        for (int i = tid; i < span.whole; i += kThreads) {
-            const int page = from[i];
-            to[i] = page;
-            atomicAdd(&a.page_refs[page], 1);
+        for (int i0 = tid; i0 < span.whole; i0 += kThreads * kBatch) {
+            int page[kBatch];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (i0 + u * kThreads < span.whole) page[u] = __ldcg(from + i0 + u * kThreads);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (i0 + u * kThreads < span.whole) {
+                    to[i0 + u * kThreads] = page[u];
+                    atomicAdd(&a.page_refs[page[u]], 1);
+                }
         }
         for (int i = span.total + tid; i < a.max_pages; i += kThreads) to[i] = -1;
         if (tid == 0) a.ctx_lens[c] = ctx;
@@ -292,29 +303,60 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkArgs a) 
 }
 
 __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, j = blockIdx.x;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    const int r = a.rows[blockIdx.x];
+    const int r = a.rows[j];
     if (r < 0 || r >= a.batch) {
         if (tid == 0) raise_device_error(a.dev_err, SPEC_DEVERR_POOL);
         return;
     }
-    const int keep = a.keep_lens ? max(0, a.keep_lens[blockIdx.x]) : 0;
-    int32_t* row = a.block_table + (int64_t)r * a.max_pages;
-    if (tid == 0) atomicMin(&a.ctx_lens[r], keep);
-    const int64_t first = ((int64_t)keep + a.P - 1) / a.P;
-    for (int64_t i = first + tid; i < a.max_pages; i += kThreads) {
-        if (row[i] < 0) continue;
-        const int page = atomicExch(&row[i], -1);
-        if (page < 0) continue;  // the row is listed twice
-        if (page >= a.num_pages) {
-            raise_device_error(a.dev_err, SPEC_DEVERR_PAGE);
-        } else if (atomicSub(&a.page_refs[page], 1) <= 0) {  // nobody held it
-            atomicAdd(&a.page_refs[page], 1);
-            raise_device_error(a.dev_err, SPEC_DEVERR_POOL);
+    // a row that is listed several times keeps the least, and its first block drops the pages
+    int keep = a.keep_lens ? max(0, a.keep_lens[j]) : 0;
+    bool earlier = false;
+    int least = keep;
+    for (int i = tid; i < a.n; i += kThreads)
+        if (i != j && a.rows[i] == r) {
+            earlier |= i < j;
+            least = min(least, a.keep_lens ? max(0, a.keep_lens[i]) : 0);
         }
+    const int again = __syncthreads_or((earlier ? 1 : 0) | (least < keep ? 2 : 0));
+    if (again) {  // (rare) settle both with the whole block
+        if (__syncthreads_or(earlier)) return;
+        __shared__ int s_least;
+        if (tid == 0) s_least = keep;
+        __syncthreads();
+        atomicMin(&s_least, least);
+        __syncthreads();
+        keep = s_least;
     }
+    int32_t* row = a.block_table + (int64_t)r * a.max_pages;
+    if (tid == 0) a.ctx_lens[r] = min(a.ctx_lens[r], keep);
+    const int first = (int)(((int64_t)keep + a.P - 1) / a.P);
+    int bad = 0;
+    for (int i0 = first + tid; i0 < a.max_pages; i0 += kThreads * kBatch) {
+        int page[kBatch], old[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kThreads;
+            page[u] = i < a.max_pages ? row[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            old[u] = 1;
+            if (page[u] < 0) continue;
+            row[i0 + u * kThreads] = -1;
+            if (page[u] >= a.num_pages) bad |= SPEC_DEVERR_PAGE;
+            else old[u] = atomicSub(&a.page_refs[page[u]], 1);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (old[u] <= 0) {  // nobody held it
+                atomicAdd(&a.page_refs[page[u]], 1);
+                bad |= SPEC_DEVERR_POOL;
+            }
+    }
+    if (bad) raise_device_error(a.dev_err, bad);
 }
 
 // ------------------------------------------------------------------ compaction

@@ -70,14 +70,17 @@ struct Stats {
         }
         m = to;
     }
-    __device__ void merge(Stats o, float c) {
-        const float to = fmaxf(m, o.m);
-        if (m < to) rebase(to, c);
-        if (o.m < to) o.rebase(to, c);
-        l += o.l;
-        a += o.a;
-    }
 };
+
+// The sums of a warp's lanes, in every lane.
+__device__ __forceinline__ Stats warp_total(Stats v, float c) {
+    const float to = warp_max(v.m);
+    if (v.m < to) v.rebase(to, c);
+    v.m = to;
+    v.l = warp_sum(v.l);
+    v.a = warp_sum(v.a);
+    return v;
+}
 
 template <typename T> __device__ __forceinline__ void widen(const uint4& r, float (&x)[per_vec<T>()]);
 template <> __device__ __forceinline__ void widen<float>(const uint4& r, float (&x)[4]) {
@@ -265,7 +268,7 @@ __device__ __forceinline__ float bound_of_groups(Shared& s, float bm, int K) {
 }
 
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logprob_kernel(const LogprobArgs a) {
     constexpr int EPV = per_vec<T>();
     __shared__ Shared s;
     const int tid = threadIdx.x, S = a.parts, K = a.K;
@@ -428,14 +431,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(const Lo
         st.a = p + q;
     }
     // the CTA's sums
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) {
-        Stats other;
-        other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-        other.l = __shfl_xor_sync(0xffffffffu, st.l, o);
-        other.a = __shfl_xor_sync(0xffffffffu, st.a, o);
-        st.merge(other, c);
-    }
+    st = warp_total(st, c);
     if ((tid & 31) == 0) s.stats[tid >> 5] = make_float4(st.m, st.l, st.a, 0.f);
     __syncthreads();
     // sums in `from` of n parts (a warp: all that is needed further on)
@@ -447,29 +443,14 @@ __global__ void __launch_bounds__(kThreads, TOP ? 3 : 4) logprob_kernel(const Lo
             sum.l = r.y;
             sum.a = r.z;
         }
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) {
-            Stats other;
-            other.m = __shfl_xor_sync(0xffffffffu, sum.m, o);
-            other.l = __shfl_xor_sync(0xffffffffu, sum.l, o);
-            other.a = __shfl_xor_sync(0xffffffffu, sum.a, o);
-            sum.merge(other, c);
-        }
-        return sum;
+        return warp_total(sum, c);
     };
     if (tid < 32) {
         const float4 r = tid < kThreads / 32 ? s.stats[tid] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         st.m = r.x;
         st.l = r.y;
         st.a = r.z;
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1) {
-            Stats other;
-            other.m = __shfl_xor_sync(0xffffffffu, st.m, o);
-            other.l = __shfl_xor_sync(0xffffffffu, st.l, o);
-            other.a = __shfl_xor_sync(0xffffffffu, st.a, o);
-            st.merge(other, c);
-        }
+        st = warp_total(st, c);
     }
     int found = 0;
     if (TOP) found = cut(s, s.count, K);
