@@ -33,7 +33,7 @@ namespace specv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kScan = 8192;  // pages of a planning block
+constexpr int kScan = 2048;  // pages of a planning block: 8 ballots a warp
 constexpr float kE4m3Max = 448.f;
 constexpr int kBatch = 8;    // entries of a thread whose loads and atomics are under way together
 
@@ -69,20 +69,29 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const ForkArgs a) {
     grid_dep_launch_dependents();
     grid_dep_wait();
     if ((int)blockIdx.x >= a.n) {  // pages
-        const int64_t p0 = (int64_t)(blockIdx.x - a.n) * kScan + warp * 1024;
-        int free = 0;
-#pragma unroll 8
-        for (int i = 0; i < 32; ++i) {
+        constexpr int kWords = kScan / 32 / (kThreads / 32);
+        const int64_t p0 = (int64_t)(blockIdx.x - a.n) * kScan + warp * (32 * kWords);
+        int refs[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
             const int64_t p = p0 + i * 32 + lane;
-            const int refs = p < a.num_pages ? a.page_refs[p] : -1;
-            const uint32_t none = __ballot_sync(0xffffffffu, refs == 0);
-            const uint32_t one = __ballot_sync(0xffffffffu, refs == 1);
+            refs[i] = p < a.num_pages ? a.page_refs[p] : -1;
+        }
+        uint32_t none = 0, one = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            const uint32_t w0 = __ballot_sync(0xffffffffu, refs[i] == 0);
+            const uint32_t w1 = __ballot_sync(0xffffffffu, refs[i] == 1);
             if (lane == i) {
-                a.free_bits[p0 / 32 + i] = none;
-                a.one_bits[p0 / 32 + i] = one;
-                free = __popc(none);
+                none = w0;
+                one = w1;
             }
         }
+        if (lane < kWords) {
+            a.free_bits[p0 / 32 + lane] = none;
+            a.one_bits[p0 / 32 + lane] = one;
+        }
+        int free = __popc(none);
         free = block_sum(free, s_warp);
         if (tid == 0) a.free_count[blockIdx.x - a.n] = free;
         return;
@@ -452,54 +461,59 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
     return (float)v;
 }
 
-// e4m3: a place's page may have to take a larger scale.
-__global__ void __launch_bounds__(kCThreads) compact_e4m3_kernel(const CompactArgs a) {
+// e4m3: a place's page may have to take a larger scale.  The moved rows and every scale come
+// in one round trip; the rest is arithmetic between barriers.
+constexpr int kEThreads = 256;
+
+__global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactArgs a) {
     __shared__ Moves mv;
     __shared__ __align__(16) uint8_t s_row[64 * 256];
-    __shared__ float s_src[64];           // scale of a move's source page
+    __shared__ float s_src[64];             // scale of a move's source page
     __shared__ float s_old[65], s_new[65];  // scales of the pages that hold the drafts' places
     __shared__ int s_page[65];
     const int tid = threadIdx.x, lane = tid & 31, t = blockIdx.x & 1, h = blockIdx.x >> 1, b = blockIdx.y;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    find_moves(a, b, mv);
     uint8_t* cache = static_cast<uint8_t*>(t ? a.v_cache : a.k_cache);
     float* scales = static_cast<float*>(t ? a.v_scale : a.k_scale);
     const int ctx = a.ctx_lens[b];
-    if (ctx < 0) return;
-    const int64_t g0 = ctx / a.P, g1 = ((int64_t)ctx + a.k - 1) / a.P;
-    const int pages = (int)(g1 - g0) + 1;  // at most 64 drafts: 65
-    for (int g = tid; g < pages; g += kCThreads) {
+    const int64_t g0 = ctx / a.P;
+    const int pages = ctx < 0 ? 0 : (int)(((int64_t)ctx + a.k - 1) / a.P - g0) + 1;  // 65 at most
+    // (the last threads, while the first 64 find the moves)
+    for (int g = kEThreads - 1 - tid; g < pages; g += kEThreads) {
         int page = -1;
         if (g0 + g < a.max_pages) page = a.block_table[(int64_t)b * a.max_pages + g0 + g];
         if (page >= a.num_pages) page = -1;
         s_page[g] = page;
         s_old[g] = s_new[g] = page >= 0 ? scales[(int64_t)page * a.Hkv + h] : 0.f;
     }
-    __syncthreads();
+    find_moves(a, b, mv);
+    if (ctx < 0) return;
     auto at = [&](int64_t r) { return ((r / a.P * a.Hkv + h) * a.P + r % a.P) * a.D; };
-    // every moved row, and the scale its new page needs for it (a warp per row)
-    for (int i = tid >> 5; i < mv.n; i += kCThreads / 32) {
-        if (mv.dst[i] < 0) continue;
-        const int64_t from = at(mv.src[i]);
+    if (tid < mv.n && mv.dst[tid] >= 0) s_src[tid] = scales[mv.src[tid] / a.P * a.Hkv + h];
+    const int per = a.D / 16;  // 16-byte pieces of a row
+    for (int e = tid; e < mv.n * per; e += kEThreads) {
+        const int i = e / per;
+        if (mv.dst[i] >= 0)
+            *reinterpret_cast<uint4*>(s_row + e * 16) =
+                *reinterpret_cast<const uint4*>(cache + at(mv.src[i]) + (e - i * per) * 16);
+    }
+    __syncthreads();
+    // the scale that a row needs in another page (a warp per row)
+    for (int i = tid >> 5; i < mv.n; i += kEThreads / 32) {
+        if (mv.dst[i] < 0 || mv.src[i] / a.P == mv.dst[i] / a.P) continue;
         int top = 0;  // largest code without its sign: codes are ordered as their values
         for (int d = lane * 4; d < a.D; d += 128) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(cache + from + d);
-            *reinterpret_cast<uint32_t*>(s_row + i * a.D + d) = w;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + i * a.D + d);
 #pragma unroll
             for (int u = 0; u < 4; ++u) top = max(top, (int)((w >> (8 * u)) & 0x7f));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) {
-            const float s = scales[mv.src[i] / a.P * a.Hkv + h];
-            s_src[i] = s;
-            if (mv.src[i] / a.P != mv.dst[i] / a.P) {
-                const float x = __fdiv_rn(e4m3_value((uint8_t)top) * s, kE4m3Max);
-                const int g = (int)(((int64_t)ctx + i) / a.P - g0);
-                // (scales are >= 0: their bits are ordered as they are)
-                atomicMax(reinterpret_cast<int*>(&s_new[g]), __float_as_int(x));
-            }
+            const float x = __fdiv_rn(e4m3_value((uint8_t)top) * s_src[i], kE4m3Max);
+            const int g = (int)(((int64_t)ctx + i) / a.P - g0);
+            // (scales are >= 0: their bits are ordered as they are)
+            atomicMax(reinterpret_cast<int*>(&s_new[g]), __float_as_int(x));
         }
     }
     __syncthreads();
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kCThreads) compact_e4m3_kernel(const CompactAr
         const int64_t left = (int64_t)ctx + a.k - (g0 + g) * a.P;
         const int slots = (int)(left < a.P ? left : a.P);
         uint8_t* p = cache + ((int64_t)s_page[g] * a.Hkv + h) * a.P * a.D;
-        for (int e = tid * 4; e < slots * a.D; e += kCThreads * 4) {
+        for (int e = tid * 4; e < slots * a.D; e += kEThreads * 4) {
             uint32_t w = *reinterpret_cast<const uint32_t*>(p + e), o = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
@@ -520,25 +534,24 @@ __global__ void __launch_bounds__(kCThreads) compact_e4m3_kernel(const CompactAr
         if (tid == 0) scales[(int64_t)s_page[g] * a.Hkv + h] = s_new[g];
     }
     __syncthreads();
-    for (int i = tid >> 5; i < mv.n; i += kCThreads / 32) {
+    const int words = a.D / 4;
+    for (int e = tid; e < mv.n * words; e += kEThreads) {
+        const int i = e / words;
         if (mv.dst[i] < 0) continue;
         const int g = (int)(((int64_t)ctx + i) / a.P - g0);
         const bool same = mv.src[i] / a.P == mv.dst[i] / a.P && s_new[g] == s_old[g];
-        const float s = s_src[i], to_scale = s_new[g];
-        const int64_t to = at(mv.dst[i]);
-        for (int d = lane * 4; d < a.D; d += 128) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + i * a.D + d);
-            uint32_t o = w;
-            if (!same) {
-                o = 0;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + e * 4);
+        uint32_t o = w;
+        if (!same) {
+            const float s = s_src[i], to_scale = s_new[g];
+            o = 0;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float x = e4m3_value((w >> (8 * u)) & 0xff) * s;
-                    o |= (uint32_t)e4m3_of(to_scale > 0.f ? __fdiv_rn(x, to_scale) : 0.f) << (8 * u);
-                }
+            for (int u = 0; u < 4; ++u) {
+                const float x = e4m3_value((w >> (8 * u)) & 0xff) * s;
+                o |= (uint32_t)e4m3_of(to_scale > 0.f ? __fdiv_rn(x, to_scale) : 0.f) << (8 * u);
             }
-            *reinterpret_cast<uint32_t*>(cache + to + d) = o;
         }
+        *reinterpret_cast<uint32_t*>(cache + at(mv.dst[i]) + (e - i * words) * 4) = o;
     }
 }
 
@@ -572,8 +585,9 @@ cudaError_t launch_kv_release(const ReleaseArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream) {
     const dim3 grid((unsigned)(2 * a.Hkv), (unsigned)a.B);
-    return launch_dependent(a.cache_dtype == SPEC_DTYPE_E4M3 ? compact_e4m3_kernel : compact_kernel, grid,
-                            dim3(kCThreads), 0, stream, a);
+    return a.cache_dtype == SPEC_DTYPE_E4M3
+               ? launch_dependent(compact_e4m3_kernel, grid, dim3(kEThreads), 0, stream, a)
+               : launch_dependent(compact_kernel, grid, dim3(kCThreads), 0, stream, a);
 }
 
 }  // namespace specv
