@@ -373,47 +373,55 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) 
 constexpr int kCThreads = 128;
 constexpr int kChunks = 4;  // 16-byte pieces of a thread between two barriers
 
-// A sequence's moves: slot rows (page * P + slot) of the place i and of its
-// source, -1 where nothing moves.
+// A sequence's moves in one kv-head: rows of the cache ((page * Hkv + head) * P + slot) of
+// the place i and of its source, -1 where nothing moves, and their pages.
 struct Moves {
     int64_t dst[64], src[64];
+    int dst_page[64], src_page[64];
     int n;
 };
 
-__device__ __forceinline__ int64_t place_of(const CompactArgs& a, int b, int64_t pos, int* bad) {
-    if (pos < 0 || pos / a.P >= a.max_pages) {
+struct Place {
+    int page, slot;
+};
+__device__ __forceinline__ Place place_of(const CompactArgs& a, int b, uint32_t pos, int* bad) {
+    const uint32_t n = pos / (uint32_t)a.P;
+    if (n >= (uint32_t)a.max_pages) {
         *bad |= SPEC_DEVERR_CTX;
-        return -1;
+        return {-1, 0};
     }
-    const int page = a.block_table[(int64_t)b * a.max_pages + pos / a.P];
+    const int page = a.block_table[(int64_t)b * a.max_pages + n];
     if (page < 0 || page >= a.num_pages) {
         *bad |= SPEC_DEVERR_PAGE;
-        return -1;
+        return {-1, 0};
     }
-    return (int64_t)page * a.P + pos % a.P;
+    return {page, (int)(pos - n * a.P)};
 }
 
-__device__ __forceinline__ void find_moves(const CompactArgs& a, int b, Moves& mv) {
+__device__ __forceinline__ void find_moves(const CompactArgs& a, int b, int h, Moves& mv) {
     const int tid = threadIdx.x;
     if (tid < 64) {
+        const int from = tid < a.k ? a.path[(int64_t)b * a.k + tid] : -1;
         int n = a.accepted[b], bad = 0;
-        n = n < 0 ? 0 : n > a.k ? a.k : n;
         const int ctx = a.ctx_lens[b];
-        int64_t d = -1, s = -1;
+        n = n < 0 ? 0 : n > a.k ? a.k : n;
+        Place d = {-1, 0}, s = {-1, 0};
         if (tid < n) {
-            const int from = a.path[(int64_t)b * a.k + tid];
             if (from < tid || from >= a.k) {
                 bad = SPEC_DEVERR_TREE;
-            } else if (from != tid && ctx >= 0) {
-                d = place_of(a, b, (int64_t)ctx + tid, &bad);
-                s = place_of(a, b, (int64_t)ctx + from, &bad);
             } else if (ctx < 0) {
                 bad = SPEC_DEVERR_CTX;
+            } else if (from != tid) {
+                d = place_of(a, b, (uint32_t)ctx + tid, &bad);
+                s = place_of(a, b, (uint32_t)ctx + from, &bad);
             }
         }
         if (bad) raise_device_error(a.dev_err, bad);
-        mv.dst[tid] = d >= 0 && s >= 0 ? d : -1;
-        mv.src[tid] = s;
+        const bool go = d.page >= 0 && s.page >= 0;
+        mv.dst[tid] = go ? ((int64_t)d.page * a.Hkv + h) * a.P + d.slot : -1;
+        mv.src[tid] = ((int64_t)s.page * a.Hkv + h) * a.P + s.slot;
+        mv.dst_page[tid] = d.page;
+        mv.src_page[tid] = s.page;
         if (tid == 0) mv.n = n;
     }
     __syncthreads();
@@ -425,31 +433,29 @@ __global__ void __launch_bounds__(kCThreads) compact_kernel(const CompactArgs a)
     const int tid = threadIdx.x, t = blockIdx.x & 1, h = blockIdx.x >> 1, b = blockIdx.y;
     grid_dep_launch_dependents();
     grid_dep_wait();
-    find_moves(a, b, mv);
+    find_moves(a, b, h, mv);
     const int per = a.D * a.elem / 16;  // pieces of a row
     uint4* cache = reinterpret_cast<uint4*>(t ? a.v_cache : a.k_cache);
-    // slot row r of head h: ((page * Hkv + h) * P + slot), r = page * P + slot
-    auto row = [&](int64_t r) { return (r / a.P * a.Hkv + h) * a.P + r % a.P; };
     uint16_t* sc = static_cast<uint16_t*>(t ? a.v_scale : a.k_scale);
     uint16_t scale = 0;
     const bool with_scale = a.cache_dtype == SPEC_DTYPE_I8 && tid < mv.n && mv.dst[tid] >= 0;
-    if (with_scale) scale = sc[row(mv.src[tid])];
+    if (with_scale) scale = sc[mv.src[tid]];
     for (int e0 = 0; e0 < mv.n * per; e0 += kCThreads * kChunks) {
         uint4 x[kChunks];
 #pragma unroll
         for (int u = 0; u < kChunks; ++u) {
             const int e = e0 + u * kCThreads + tid, i = e / per;
-            if (i < mv.n && mv.dst[i] >= 0) x[u] = cache[row(mv.src[i]) * per + e % per];
+            if (i < mv.n && mv.dst[i] >= 0) x[u] = cache[mv.src[i] * per + e - i * per];
         }
         __syncthreads();  // places up to the last read are written only now
 #pragma unroll
         for (int u = 0; u < kChunks; ++u) {
             const int e = e0 + u * kCThreads + tid, i = e / per;
-            if (i < mv.n && mv.dst[i] >= 0) cache[row(mv.dst[i]) * per + e % per] = x[u];
+            if (i < mv.n && mv.dst[i] >= 0) cache[mv.dst[i] * per + e - i * per] = x[u];
         }
         __syncthreads();
     }
-    if (with_scale) sc[row(mv.dst[tid])] = scale;
+    if (with_scale) sc[mv.dst[tid]] = scale;
 }
 
 __device__ __forceinline__ uint8_t e4m3_of(float x) {
@@ -477,8 +483,8 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
     uint8_t* cache = static_cast<uint8_t*>(t ? a.v_cache : a.k_cache);
     float* scales = static_cast<float*>(t ? a.v_scale : a.k_scale);
     const int ctx = a.ctx_lens[b];
-    const int64_t g0 = ctx / a.P;
-    const int pages = ctx < 0 ? 0 : (int)(((int64_t)ctx + a.k - 1) / a.P - g0) + 1;  // 65 at most
+    const int g0 = ctx / a.P;
+    const int pages = ctx < 0 ? 0 : ((uint32_t)ctx + a.k - 1) / (uint32_t)a.P - g0 + 1;  // 65 at most
     // (the last threads, while the first 64 find the moves)
     for (int g = kEThreads - 1 - tid; g < pages; g += kEThreads) {
         int page = -1;
@@ -487,21 +493,20 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
         s_page[g] = page;
         s_old[g] = s_new[g] = page >= 0 ? scales[(int64_t)page * a.Hkv + h] : 0.f;
     }
-    find_moves(a, b, mv);
+    find_moves(a, b, h, mv);
     if (ctx < 0) return;
-    auto at = [&](int64_t r) { return ((r / a.P * a.Hkv + h) * a.P + r % a.P) * a.D; };
-    if (tid < mv.n && mv.dst[tid] >= 0) s_src[tid] = scales[mv.src[tid] / a.P * a.Hkv + h];
+    if (tid < mv.n && mv.dst[tid] >= 0) s_src[tid] = scales[(int64_t)mv.src_page[tid] * a.Hkv + h];
     const int per = a.D / 16;  // 16-byte pieces of a row
     for (int e = tid; e < mv.n * per; e += kEThreads) {
         const int i = e / per;
         if (mv.dst[i] >= 0)
             *reinterpret_cast<uint4*>(s_row + e * 16) =
-                *reinterpret_cast<const uint4*>(cache + at(mv.src[i]) + (e - i * per) * 16);
+                *reinterpret_cast<const uint4*>(cache + mv.src[i] * a.D + (e - i * per) * 16);
     }
     __syncthreads();
     // the scale that a row needs in another page (a warp per row)
     for (int i = tid >> 5; i < mv.n; i += kEThreads / 32) {
-        if (mv.dst[i] < 0 || mv.src[i] / a.P == mv.dst[i] / a.P) continue;
+        if (mv.dst[i] < 0 || mv.src_page[i] == mv.dst_page[i]) continue;
         int top = 0;  // largest code without its sign: codes are ordered as their values
         for (int d = lane * 4; d < a.D; d += 128) {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + i * a.D + d);
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) {
             const float x = __fdiv_rn(e4m3_value((uint8_t)top) * s_src[i], kE4m3Max);
-            const int g = (int)(((int64_t)ctx + i) / a.P - g0);
+            const int g = ((uint32_t)ctx + i) / (uint32_t)a.P - g0;
             // (scales are >= 0: their bits are ordered as they are)
             atomicMax(reinterpret_cast<int*>(&s_new[g]), __float_as_int(x));
         }
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
     // pages whose scale grew: every row of the sequence keeps its value
     for (int g = 0; g < pages; ++g) {
         if (s_page[g] < 0 || !(s_new[g] > s_old[g])) continue;
-        const int64_t left = (int64_t)ctx + a.k - (g0 + g) * a.P;
+        const int64_t left = (int64_t)ctx + a.k - (int64_t)(g0 + g) * a.P;
         const int slots = (int)(left < a.P ? left : a.P);
         uint8_t* p = cache + ((int64_t)s_page[g] * a.Hkv + h) * a.P * a.D;
         for (int e = tid * 4; e < slots * a.D; e += kEThreads * 4) {
@@ -538,8 +543,8 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
     for (int e = tid; e < mv.n * words; e += kEThreads) {
         const int i = e / words;
         if (mv.dst[i] < 0) continue;
-        const int g = (int)(((int64_t)ctx + i) / a.P - g0);
-        const bool same = mv.src[i] / a.P == mv.dst[i] / a.P && s_new[g] == s_old[g];
+        const int g = ((uint32_t)ctx + i) / (uint32_t)a.P - g0;
+        const bool same = mv.src_page[i] == mv.dst_page[i] && s_new[g] == s_old[g];
         const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + e * 4);
         uint32_t o = w;
         if (!same) {
@@ -551,7 +556,7 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
                 o |= (uint32_t)e4m3_of(to_scale > 0.f ? __fdiv_rn(x, to_scale) : 0.f) << (8 * u);
             }
         }
-        *reinterpret_cast<uint32_t*>(cache + at(mv.dst[i]) + (e - i * words) * 4) = o;
+        *reinterpret_cast<uint32_t*>(cache + mv.dst[i] * a.D + (e - i * words) * 4) = o;
     }
 }
 
