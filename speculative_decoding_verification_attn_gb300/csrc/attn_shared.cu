@@ -639,21 +639,27 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 }
                 return page;
             };
-            // e4m3: lane l < 8 the scale of K of keys [16 l, 16 l + 16), l + 8 that of V
-            auto fetch_scale = [&](int i) {
+            // e4m3: lane l < 8 the scale of K of keys [16 l, 16 l + 16) of tile i at cursor c,
+            // l + 8 that of V; and into the stage of the tile's use
+            auto fetch_scale = [&](const Cursor& c, int i) {
                 const int j = (lane & 7) * 16;
-                if (lane >= 16 || j >= cur.valid(L)) return 0.f;
+                if (lane >= 16 || j >= c.valid(L)) return 0.f;
                 const float* from = lane < 8 ? a.k_page_scale : a.v_page_scale;
-                return __ldg(from + (int64_t)page_of(i, j / CH) * Hkv + cur.kvh);
+                return __ldg(from + (int64_t)page_of(i, j / CH) * Hkv + c.kvh);
+            };
+            auto put_scale = [&](float x, int i) {
+                if (lane >= 16) return;
+                float* to = s_scale + (2 * s + (i & 1)) * 24 + lane;
+                to[0] = lane < 8 ? x * a.scale * kLog2e : x;
+                if (lane >= 8) to[8] = log2f(x);
             };
 #pragma unroll 1
             for (int i = 0; i < LOOKAHEAD; ++i) fetch_pids(i);
             bool ok = true;
-            float scale = 0.f;
             if (KV == KV_E4M3 && total > 0) {
                 cp_async_wait<LOOKAHEAD - 1>();
                 __syncwarp();
-                scale = fetch_scale(0);
+                put_scale(fetch_scale(cur, 0), 0);
             }
             int k_loads = 0, v_loads = 0;
 #pragma unroll 1
@@ -672,14 +678,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                                 (key & (P - 1));
                 }
                 const uint64_t pol = cur.v < L.B ? once : again;
+                Cursor nx = cur;
+                float scale = 0.f;  // the next tile's, stored when this one's V is on its way
+                if (i + 1 < total) {
+                    step(nx, i);
+                    if (KV == KV_E4M3) scale = fetch_scale(nx, i + 1);
+                }
                 if (i > 0) ok = warp_wait(&bars[Smem::B_KEMPTY + s], (i - 1) & 1, abort_flag, a.dev_err);
                 if (!ok) break;
                 const uint32_t bytes = (uint32_t)(nck * CH) * (CODES && !wide ? 128u : 256u);
-                if (KV == KV_E4M3 && lane < 16) {
-                    float* to = s_scale + (2 * s + (i & 1)) * 24 + lane;
-                    to[0] = lane < 8 ? scale * a.scale * kLog2e : scale;
-                    if (lane >= 8) to[8] = log2f(scale);
-                }
                 __syncwarp();
                 uint64_t* full = &bars[Smem::B_KFULL + s];
                 if (lane == 0)
@@ -716,10 +723,9 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 }
                 v_loads = i + 1;
                 __syncwarp();
-                if (i + 1 < total) {
-                    step(cur, i);
-                    if (KV == KV_E4M3) scale = fetch_scale(i + 1);
-                }
+                // (the stage's last tile, i - 1, is through: its P V freed the slot of V)
+                if (KV == KV_E4M3 && i + 1 < total) put_scale(scale, i + 1);
+                cur = nx;
             }
             cp_async_wait<0>();
             if (!ok && lane == 0) {
@@ -773,6 +779,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 const int len = uniform(min(cur.nt - cur.lt, (wide ? total : n) - t0));
                 const int keys = uniform(L.seg[cur.v].key1 - cur.key0(L));  // from its first tile on
                 const bool values = CODES && prm.k_prefix && uniform(cur.v >= L.B);
+                // (INT8's bounds of the scales come from the widening warps for every tile)
+                const bool widened = CODES && (KV == KV_I8 || !values);
                 ok = warp_wait(&bars[Smem::B_QFULL + s], (q_loads - 1) & 1, abort_flag, a.dev_err);
 #pragma unroll 1
                 for (int j = 0; j < len && ok; ++j) {
@@ -781,7 +789,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     const int slot = wide ? (t - n) & 1 : s;
                     const int use = wide ? (slot == s ? n : other) + ((t - n) >> 1) : t;
                     const int nvalid = min(TN, keys - j * TN), nvb = (nvalid + 15) / 16;
-                    ok = warp_wait(&bars[(CODES ? Smem::B_KREADY : Smem::B_KFULL) + slot], use & 1,
+                    ok = warp_wait(&bars[(widened ? Smem::B_KREADY : Smem::B_KFULL) + slot], use & 1,
                                    abort_flag, a.dev_err);
                     if (!ok) break;
                     tc_fence_after();
@@ -798,7 +806,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     umma_commit_w(&bars[Smem::B_SFULL + s]);
                     umma_commit_w(&bars[Smem::B_KEMPTY + slot]);
                     if (!wide) umma_commit_w(&bars[Smem::B_KEMPTY + slot]);  // for the other stream
-                    ok = warp_wait(&bars[(CODES ? Smem::B_VREADY : Smem::B_VFULL) + slot], use & 1,
+                    ok = warp_wait(&bars[(widened ? Smem::B_VREADY : Smem::B_VFULL) + slot], use & 1,
                                    abort_flag, a.dev_err);
                     if (!ok) break;
                     if (nvalid % 16 != 0 && (!CODES || values)) {
@@ -876,6 +884,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
             for (int i = 0; i < total; ++i) {
                 const int nvalid = c.valid(L);
                 const bool values = prm.k_prefix && c.v >= L.B;  // nothing to widen
+                if (KV == KV_E4M3 && values) break;  // nor in any tile from here on
 #pragma unroll 1
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     if (ok)
@@ -1317,11 +1326,11 @@ __global__ void __launch_bounds__(256) widen_kernel(const Params prm) {
     const uint2* vc = static_cast<const uint2*>(a.v_cache);
     uint4* ko = reinterpret_cast<uint4*>(prm.k_prefix);
     uint4* vo = reinterpret_cast<uint4*>(prm.v_prefix);
-    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < all; i0 += 2 * step) {
-        uint2 k[2], v[2];
-        int64_t to[2];
+    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < all; i0 += 4 * step) {
+        uint2 k[4], v[4];
+        int64_t to[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 4; ++u) {
             const int64_t i = i0 + u * step;
             if (i >= all) continue;
             const int piece = (int)(i & (per - 1));
@@ -1335,7 +1344,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const Params prm) {
             v[u] = __ldg(vc + from);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 4; ++u) {
             if (i0 + u * step >= all) continue;
             ko[to[u]] = widen8<KV>(k[u]);
             vo[to[u]] = widen8<KV>(v[u]);
