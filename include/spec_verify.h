@@ -302,15 +302,21 @@ SPEC_API int spec_verify_attn_window(const void *q, const void *k_cache, const v
  *                rows may be read for them
  * Groups are a promise about the tables, not a mask: every query sees what it
  * sees in spec_verify_attn.  A start outside [the one before it, batch] (the
- * group is taken as empty) sets SPEC_DEVERR_GROUP; so does a shared length below 0
- * or above the shortest context of the group, and it is clamped.  A part of a
- * shared length that does not fill a page is read sequence by sequence.
- * Limits: num_groups >= 0; else as spec_verify_attn.  A BF16 query with head_dim
- * 128 and a BF16, I8 or E4M3 cache of power-of-two pages in [16, 256], up to 128
- * query rows per kv-head and about 1000 sequences and blocks of 256 query rows
- * runs on a tensor-core kernel of its own, which rounds as the BF16 one of
- * spec_verify_attn does (codes are exact in its MMAs, scales fp32); every other
- * accepted shape runs as spec_verify_attn.
+ * group is taken as empty) sets SPEC_DEVERR_GROUP where the groups are read; so does
+ * a shared length below 0 or above the shortest context of the group, and it is
+ * clamped.  A part of a shared length that does not fill a page is read sequence by
+ * sequence, and so is one below 128 keys.
+ * A BF16 query with head_dim 128 and a BF16, I8 or E4M3 cache of power-of-two
+ * pages in [16, 256], up to 128 query rows per kv-head and about 1000 sequences and
+ * blocks of 256 query rows may run on a tensor-core kernel of its own, which reads
+ * the groups.  It rounds as the BF16 one of spec_verify_attn does (codes are exact
+ * in its MMAs, scales fp32), and its workspace holds two fp32 rows for each query
+ * and head and, where prefixes of codes serve 512 rows or more of a kv-head, their
+ * bf16 values (up to 1 GiB, by the tables' width).  It is taken where the sequences
+ * that a group saves, times the block table's width, outweigh its fixed cost (10-20
+ * us), and with SPEC_OPT_ATTN_PATH 5 wherever it fits; every other call runs as
+ * spec_verify_attn and does not read the groups.
+ * Limits: num_groups >= 0; else as spec_verify_attn.
  */
 SPEC_API int spec_verify_attn_shared(const void *q, const void *k_cache, const void *v_cache,
                                      const void *k_scale, const void *v_scale,

@@ -68,8 +68,17 @@ constexpr uint32_t TM_S = 0, TM_O = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 40.0f;  // log2 units
-constexpr int kSplitAlpha = 3;  // narrow tiles' time that a piece's fixed work takes
-constexpr int kWideCost = 2;    // narrow tiles' time that a wide tile takes
+// What the split over the CTAs charges, in quarters of a narrow tile's time: a tile
+// of a wide block (two Q tiles), and a piece's fixed work.  A narrow piece's end lies
+// under the other stream's tiles; a wide one holds both streams.  Measured from
+// (8, 12, 12), one charge for all pieces: 144 sequences of 10-150 own keys behind 208
+// shared 283 -> 175 us, 39 sequences of one group 69 -> 50 us, the e4m3 prompts of 32
+// rollouts 266 -> 259 us.
+constexpr int kTileCost = 4;
+struct Cost {
+    int wide, piece, wide_piece;
+};
+constexpr int kSnap = 1;  // tiles by which the two streams' parts may differ to save a cut
 // Keys below which a prefix is read sequence by sequence: one tile
 constexpr int kMinShared = TN;
 // Rows of K (and of V) that widened prefixes may take: 1 GiB together
@@ -204,9 +213,9 @@ struct Cursor {
 // registers that it takes for different in each lane cost several times the issue).
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// First tile of CTA c's range: equal parts of the cost (alpha a segment, 1 or
-// kWideCost a tile).
-__device__ __forceinline__ int range_begin(const List& L, const int* cpre, int alpha, uint32_t c,
+// First tile of CTA c's range: equal parts of the cost (a charge a segment and
+// one a tile).
+__device__ __forceinline__ int range_begin(const List& L, const int* cpre, Cost cost, uint32_t c,
                                            uint32_t C) {
     const uint32_t W = (uint32_t)(cpre[L.V] * L.Hkv), each_c = W / C;
     const int x = (int)(c * each_c + c * (W - each_c * C) / C);  // c W / C; C < 2^16
@@ -217,10 +226,12 @@ __device__ __forceinline__ int range_begin(const List& L, const int* cpre, int a
         const int mid = (lo + hi + 1) >> 1;
         if (cpre[mid] * L.Hkv <= x) lo = mid; else hi = mid - 1;
     }
-    const int nt = L.tpre[lo + 1] - L.tpre[lo], each = L.seg[lo].ntok > L.NT ? kWideCost : 1;
+    const bool wide = L.seg[lo].ntok > L.NT;
+    const int nt = L.tpre[lo + 1] - L.tpre[lo], each = wide ? cost.wide : kTileCost;
+    const int fixed = wide ? cost.wide_piece : cost.piece;
     const uint32_t off = (uint32_t)(x - cpre[lo] * L.Hkv), one = (uint32_t)(cpre[lo + 1] - cpre[lo]);
     const int h = (int)(off / one), r = (int)(off - h * one);
-    const int lt = r > alpha ? (r - alpha + each - 1) / each : 0;
+    const int lt = r > fixed ? (r - fixed + each - 1) / each : 0;
     return L.tpre[lo] * L.Hkv + h * nt + lt;
 }
 
@@ -252,7 +263,7 @@ __device__ __forceinline__ void warp_scan(int* s, int n) {
 // waits for it.
 template <int NTHREADS>
 __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre, int* cpre,
-                                          int* s_narrow, int alpha, int NT) {
+                                          int* s_narrow, Cost charge, int NT) {
     const AttnArgs& a = prm.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, k = a.k, groups = prm.groups;
     const bool one = blockIdx.x == 0;
@@ -338,7 +349,7 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
         auto cost = [&](int v) {
             const Seg q = seg[v];
             const int nt = (q.key1 - q.key0 + TN - 1) / TN;
-            return warp ? alpha + nt * (q.ntok > NT ? kWideCost : 1) : nt;
+            return !warp ? nt : q.ntok > NT ? charge.wide_piece + nt * charge.wide : charge.piece + nt * kTileCost;
         };
         int sum = 0;
 #pragma unroll 1
@@ -530,13 +541,15 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     }
     // (rows of a Q tile that no copy of q writes hold anything: a row of S, P or O
     // depends on its own row of Q alone, and those are not stored)
-    const int alpha = a.split_alpha >= 0 ? a.split_alpha : kSplitAlpha;
-    const int V = build_list<NTH>(prm, s_seg, s_tpre, s_cpre, s_narrow, alpha, NT);
+    const int opt = kTileCost * a.split_alpha;
+    const Cost cost = {KV == KV_BF16 ? 8 : KV == KV_E4M3 ? 7 : 6,
+                       opt >= 0 ? opt : KV == KV_I8 ? 5 : 4, opt >= 0 ? opt : 24};
+    const int V = build_list<NTH>(prm, s_seg, s_tpre, s_cpre, s_narrow, cost, NT);
     const List L = {s_seg, s_tpre, a.B, Hkv, NT, V};
     if (warp == 0) {
         // the CTA's range [t0, t1); its narrow part in two, at a segment's end where
         // one is near (a cut costs more than the imbalance), and where they begin
-        const int edge = range_begin(L, s_cpre, alpha, blockIdx.x + (lane & 1), gridDim.x);
+        const int edge = range_begin(L, s_cpre, cost, blockIdx.x + (lane & 1), gridDim.x);
         const int t0 = __shfl_sync(0xffffffffu, edge, 0), t1 = __shfl_sync(0xffffffffu, edge, 1);
         const int border = s_tpre[*s_narrow] * Hkv, last = s_tpre[V] * Hkv - 1;
         const int n0 = min(t0, border), n2 = min(t1, border), w0 = max(t0, border);
@@ -545,8 +558,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
         c.init(min(lane == 0 ? n0 : lane == 1 ? mid : w0, last), L);
         if (lane == 1) {
             const int back = c.lt, on = c.nt - c.lt;
-            if (2 * back <= alpha && mid - back > n0) mid -= back;
-            else if (2 * on <= alpha && mid + on < n2) mid += on;
+            if (back <= kSnap && mid - back > n0) mid -= back;
+            else if (on <= kSnap && mid + on < n2) mid += on;
             if (mid != c.start + c.lt) c.init(min(mid, last), L);
         }
         mid = __shfl_sync(0xffffffffu, mid, 1);
@@ -1407,9 +1420,30 @@ bool shared_supported(const AttnArgs& a, int groups) {
     if (segs > MAX_SEGS) return false;
     // tile and cost counts are 32-bit (a charge of up to 256 tiles a segment)
     const int64_t tiles = ((int64_t)a.max_pages * a.P + TN - 1) / TN + 1;
-    return tiles < (1LL << 31) && segs * (256 + kWideCost * tiles) < (1LL << 31) / a.Hkv &&
+    return tiles < (1LL << 31) && segs * (kTileCost * 256 + 2 * kTileCost * tiles) < (1LL << 31) / a.Hkv &&
            (int64_t)a.num_pages * a.Hkv * a.P < (1LL << 31) && tokens * a.Hq < (1LL << 28) &&
            a.Hkv < 65536;
+}
+
+// What this kernel saves over reading each sequence by itself is the tiles that a
+// group's blocks stand for, (B - blocks) Hkv T of a table of T tiles (a wide block's
+// tile takes the time of 7/4 narrow ones); what it costs is every CTA's list and the
+// second launch (10-20 us), and fp32 pieces of every row, written and read (2 KB, a
+// tile a CTA for some 8000 rows).  The table's width stands for lengths that the host
+// does not know, equal groups for the groups: the rule is for tables that the contexts
+// fill.  The kernels that read each sequence by itself differ by type.  Measured on 75
+// calls (this kernel / each sequence by itself, us, at saved tiles a CTA):
+//   bf16  4.8 57 / 41   10.7 29 / 28   19 34 / 52   29 29 / 59   114 74 / 170
+//   e4m3  8 79 / 52   25 37 / 37   28 45 / 39   363 257 / 262   973 240 / 639
+//   i8    1.5 108 / 56   3.5 38 / 41   6.2 31 / 40   23 60 / 135   682 196 / 1752
+// The worst left: bf16 12 77 / 61 (not taken), e4m3 363 (own keys are half of it).
+bool shared_pays(const AttnArgs& a, int groups, int sms) {
+    const int64_t T = ((int64_t)a.max_pages * a.P + TN - 1) / TN, NT = ROWS / (a.Hq / a.Hkv);
+    const int64_t tok = ((int64_t)a.B * a.k + groups - 1) / groups, left = tok % (2 * NT);  // of a group
+    const int64_t blocks = tok / (2 * NT) * 7 + (left > NT ? 7 : left > 0 ? 4 : 0);
+    const int64_t saved = (4 * a.B - groups * blocks) * a.Hkv * T;  // quarters of a tile
+    const int fixed = a.kv_dtype == SPEC_DTYPE_BF16 ? 14 : a.kv_dtype == SPEC_DTYPE_E4M3 ? 48 : 3;
+    return T >= 2 && saved >= 4 * (fixed + (int64_t)a.B * a.k * a.Hq / 8000) * sms;
 }
 
 size_t shared_workspace_bytes(const AttnArgs& a, int groups, int num_ctas) {

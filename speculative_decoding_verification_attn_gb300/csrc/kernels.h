@@ -169,6 +169,7 @@ cudaError_t launch_attn_f8(const AttnArgs& a, int num_ctas, void* workspace, cud
 // ---- tensor-core kernel for groups of sequences that share a prefix (bf16, i8
 // or e4m3 cache), and the launch that joins its pieces ----
 bool shared_supported(const AttnArgs& a, int groups);
+bool shared_pays(const AttnArgs& a, int groups, int sms);
 size_t shared_workspace_bytes(const AttnArgs& a, int groups, int num_ctas);
 cudaError_t launch_attn_shared(const AttnArgs& a, const int32_t* group_starts,
                                const int32_t* shared_lens, int groups, int num_ctas, void* workspace,

@@ -303,9 +303,11 @@ int verify_attn_impl(const void* q, const void* k_cache, const void* v_cache, co
     const bool f8_ok = specv::f8_supported(a);
     const bool tc2_ok = f8_ok || specv::tc2_supported(a);
     const bool small_ok = !win && specv::small_attn_max_keys(a) > 0;
-    // groups with shared prefixes: a tensor-core kernel of its own (any other
-    // forced kernel reads each sequence by itself)
-    const bool groups = (path == 0 || path == 5) && specv::shared_supported(a, num_groups);
+    // groups with shared prefixes: a tensor-core kernel of its own, where it saves
+    // more than it costs or path 5 asks for it (any other forced kernel reads each
+    // sequence by itself)
+    const bool groups = (path == 0 || path == 5) && specv::shared_supported(a, num_groups) &&
+                        (path == 5 || specv::shared_pays(a, num_groups, ws->sms));
     int kernel;
     if (path == 1 || groups) kernel = 1;
     else if (path >= 2) {

@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture()
 def binding():
     from speculative_decoding_verification_attn_gb300 import binding as m
-    m.spec_set_option(m.SPEC_OPT_ATTN_PATH, 0)
+    m.spec_set_option(m.SPEC_OPT_ATTN_PATH, 5)  # the groups' kernel, whatever it saves
     m.spec_device_error()
     yield m
     for opt in (m.SPEC_OPT_ATTN_PATH, m.SPEC_OPT_NUM_CTAS, m.SPEC_OPT_SPLIT_WEIGHT,
@@ -146,6 +146,7 @@ def test_shared_scores_over_the_exponent_range(binding):
     ("i8", 96, 5, torch.bfloat16), ("e4m3", 256, 16, torch.float32), ("f32", 128, 16, torch.bfloat16)])
 def test_shared_other_shapes(binding, kind, D, P, qdt):
     """Shapes that each sequence reads by itself."""
+    binding.spec_set_option(binding.SPEC_OPT_ATTN_PATH, 0)
     c = case(7, kind, [3, 2], [140, 50], [4, 30], 3, 4, 2, P, D=D, qdt=qdt, tail=1)
     check(c, *call(binding, c), f32=True if qdt == torch.float32 else False)
 
@@ -162,6 +163,18 @@ def test_shared_forced_paths_and_no_groups(binding):
     check(c, *call(binding, c), ref=ref)
     c["starts"], c["shared"] = torch.zeros(1, dtype=torch.int32), torch.zeros(0, dtype=torch.int32)
     check(c, *call(binding, c), ref=ref)
+
+
+@pytest.mark.parametrize("n,P,taken", [(40, 16, True), (40, 8, False), (4, 16, False)])
+def test_shared_rule(binding, n, P, taken):
+    """Automatic: the groups are read (and a bad one is seen) where that saves enough."""
+    binding.spec_set_option(binding.SPEC_OPT_ATTN_PATH, 0)
+    c = case(12, "i8", [n], [256], [0, 30, 110], 1, 8, 4, P)
+    check(c, *call(binding, c))
+    assert binding.spec_device_error() == 0
+    c["shared"] = torch.tensor([-1]).int()
+    check(c, *call(binding, c))
+    assert binding.spec_device_error() == (GROUP if taken else 0)
 
 
 @pytest.mark.parametrize("starts,shared", [
