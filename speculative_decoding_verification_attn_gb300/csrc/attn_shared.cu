@@ -47,7 +47,6 @@
 #include <cuda.h>
 #include <math.h>
 
-#include "attn_tile.cuh"
 #include "common.cuh"
 
 namespace specv {
@@ -208,6 +207,18 @@ struct Cursor {
     __device__ int key0(const List& L) const { return L.seg[v].key0 + lt * TN; }
     __device__ int valid(const List& L) const { return min(TN, L.seg[v].key1 - key0(L)); }
 };
+
+// Visible columns [c0, c0 + 64) of a 128-key tile for a query row: the context keys,
+// then the drafts of the row's bits, limited to the tile's keys.
+__device__ __forceinline__ uint64_t visible64(int key0, int c0, int nvalid, int ctx, uint64_t mrow) {
+    const int nctx = ctx - key0 - c0;
+    auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+    const uint64_t dbits = nctx >= 64    ? 0ull
+                           : nctx >= 0   ? mrow << nctx
+                           : nctx > -64  ? mrow >> -nctx
+                                         : 0ull;
+    return (below(nctx) | dbits) & below(nvalid - c0);
+}
 
 // A value that every lane holds, where the compiler knows it (tcgen05 operands from
 // registers that it takes for different in each lane cost several times the issue).
@@ -1007,7 +1018,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 const Scales<KV> sc = {s_scale + stage * 24 + half * 4,
                                        s_half + stage * 2 * TN + half * 64};
                 const uint64_t vis =
-                    visible64<false>(cur.key0(L), half * 64, cur.valid(L), ctx, mrow, 0, 0);
+                    visible64(cur.key0(L), half * 64, cur.valid(L), ctx, mrow);
                 // the row's maximum: with the loads where all keys are visible (INT8: within
                 // the bounds that the scales of 16 keys give, when those lie close enough)
                 float mx = -INFINITY;
@@ -1378,6 +1389,24 @@ size_t prefix_bytes(const AttnArgs& a, int groups) {
 struct Maps {
     CUtensorMap own, block, k, v, kwide, vwide;
 };
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    }
+    return fn;
+}
 
 template <int KV>
 cudaError_t launch_typed(const Maps& m, const Params& prm, int num_ctas, cudaStream_t stream) {
