@@ -613,7 +613,7 @@ SPEC_API int spec_commit(int32_t *ctx_lens, const int32_t *accepted_len, int32_t
  *     IEEE division, to nearest even, saturating) e4m3((c * s_from) / s'), with
  *     s' = max(s, |c * s_from| / 448 of the rows that come into the page), and
  *     where s' > s every row of the page below ctx_b + num_draft becomes
- *     e4m3((c * s) / s').
+ *     e4m3((c * s) / s').  (A NaN code counts as 0 in s' and stays a NaN.)
  * A position outside the block table or a page id outside [0, num_pages) moves
  * nothing and sets SPEC_DEVERR_CTX / SPEC_DEVERR_PAGE.  The pages that hold
  * drafts belong to one sequence.  Caches, scales and tables as in

@@ -19,7 +19,7 @@
 // All of it is launch latency, a few dependent round trips and the atomics on the counts:
 // a table row of 2048 entries is 8 KB, a copy at most a page.  240 rows of 1024 to 2048
 // pages released and forked again: 37 us with one entry of a thread at a time and an
-// exchange for each, see the table of figures for this form.
+// exchange for each, 25 us so.  56 beams of 64 to 512 pages: 11 us.
 //
 // Compaction, one launch: a block per (sequence, kv-head, tensor).  Row path[i]
 // goes to place i <= path[i], so blocks of rows in ascending order may be read
@@ -227,14 +227,17 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkArgs a) 
     grid_dep_wait();
     const int need = a.need[j];
     if (need < 0) return;
-    int before = 0, free = 0;
+    // (a sum of needs may pass 32 bits: in two halves)
+    int64_t before = 0;
     for (int i = tid; i < j; i += kThreads) before += max(0, a.need[i]);
-    before = block_sum(before, s_warp);
+    const int low = block_sum((int)(before & 0xfffff), s_warp);
+    before = ((int64_t)block_sum((int)min(before >> 20, (int64_t)1 << 22), s_warp) << 20) + low;
+    int free = 0;
     const int blocks = (int)(((int64_t)a.num_pages + kScan - 1) / kScan);
     for (int i = tid; i < blocks; i += kThreads) free += a.free_count[i];
     free = block_sum(free, s_warp);
     const int p = a.parents[j], c = a.children[j];
-    if (need > 0 && (int64_t)before + need > free) {  // out of pages
+    if (need > 0 && before + need > free) {  // out of pages
         if (tid == 0 && blockIdx.y == 0) raise_device_error(a.dev_err, SPEC_DEVERR_POOL);
         return;
     }
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads) fork_apply_kernel(const ForkArgs a) 
             rank += want[w];
         }
         if (mine >= 0) {
-            const int page = fresh_page(a, (int64_t)before + mine);
+            const int page = fresh_page(a, before + mine);
             if (lane == 0 && page >= 0) {
                 const int i = i0 + warp, old = c == p ? to[i] : -1;
                 to[i] = page;
@@ -511,7 +514,10 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
         for (int d = lane * 4; d < a.D; d += 128) {
             const uint32_t w = *reinterpret_cast<const uint32_t*>(s_row + i * a.D + d);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) top = max(top, (int)((w >> (8 * u)) & 0x7f));
+            for (int u = 0; u < 4; ++u) {
+                const int c = (w >> (8 * u)) & 0x7f;
+                top = max(top, c == 0x7f ? 0 : c);  // a NaN asks for no scale
+            }
         }
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) {

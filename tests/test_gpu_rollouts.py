@@ -123,6 +123,21 @@ def test_fork_large_pool(binding):
     binding.spec_kv_release(g["table"], g["ctx"], g["refs"], ints(list(range(300))), P)
     same_state(g, s)
 
+def test_fork_needs_past_32_bits(binding):
+    """Pairs that together ask for more than 2^31 pages: the first has them, no other."""
+    n, room = 4099, 1 << 19
+    NP = room + 5
+    cache = [torch.zeros(NP, 1, 1, 32, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    table = torch.full((n + 1, room), -1, dtype=torch.int32, device="cuda")
+    ctx, refs = torch.zeros(n + 1).int().cuda(), torch.zeros(NP).int().cuda()
+    binding.spec_kv_fork(*cache, table, ctx, refs, torch.zeros(n).int().cuda(),
+                         torch.arange(1, n + 1).int().cuda(), room)
+    assert binding.spec_device_error() == POOL
+    assert torch.equal(table[1], torch.arange(room).int().cuda())
+    assert bool((refs[:room] == 1).all()) and not bool(refs[room:].any())
+    table[1] = -1
+    assert bool((table == -1).all())
+
 
 # ------------------------------------------------------------------ release
 
@@ -192,6 +207,27 @@ def test_compact_e4m3_zero_scales_and_extremes(binding):
     binding.spec_kv_compact(g["kc"], g["vc"], g["table"], g["ctx"], path.cuda(), n.cuda(), g["ks"],
                             g["vs"])
     same_state(g, s)
+
+
+def test_compact_e4m3_nan_row(binding):
+    """A NaN in a row that comes into a page costs the page's other rows nothing."""
+    s = pool_state(5, "e4m3", [13], 2, 64, 8, hold_more=8)
+    path, n = torch.tensor([[4, 5, 6, 7, -1, -1, -1, -1]], dtype=torch.int32), torch.tensor([3]).int()
+    clean = clone(s)
+    page = int(s["table"][0, 18 // 8])
+    rollouts.raw(s["kc"])[page, :, 18 % 8, 3] = 0x7f  # node 5, behind the page's end
+    rollouts.raw(clean["kc"])[page, :, 18 % 8, 3] = 0
+    g = to_gpu(s)
+    rollouts.compact(clean, path, n)
+    binding.spec_kv_compact(g["kc"], g["vc"], g["table"], g["ctx"], path.cuda(), n.cuda(), g["ks"],
+                            g["vs"])
+    to = int(clean["table"][0, 14 // 8])
+    assert to != page and torch.equal(g["ks"].cpu(), clean["ks"])
+    got, want = rollouts.raw(g["kc"]).cpu(), rollouts.raw(clean["kc"])
+    assert bool((got[to, :, 14 % 8, 3] & 0x7f == 0x7f).all())
+    got[to, :, 14 % 8, 3] = want[to, :, 14 % 8, 3]
+    got[page, :, 18 % 8, 3] = want[page, :, 18 % 8, 3]
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
