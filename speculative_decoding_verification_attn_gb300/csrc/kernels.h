@@ -280,6 +280,7 @@ struct LogprobArgs {
     int32_t* top_ids;     // [B, n, K] or null
     float* top_logprobs;  // [B, n, K] or null
     int32_t parts = 1;    // CTAs of a row (logprob_parts)
+    int32_t part_rounds;  // rounds of loads of each
     int32_t* tickets;     // [B * n] zeroed when parts > 1 (self-resetting)
     float* part_stats;    // workspace
     float* part_v;

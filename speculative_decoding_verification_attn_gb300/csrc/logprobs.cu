@@ -21,14 +21,22 @@
 // Top alternatives, K <= 32.  In a part's first round the K-th largest of the maxima of
 // 64 groups of threads is a bound that K elements reach: only those at or above it go to
 // a list in shared memory, about K + a few for values in no order, and later rounds append
-// what exceeds it.  Every kCheck rounds the threads meet; a list past 128 entries is
-// ranked (each entry counts the better ones) and cut to K, whose last is the bound from
-// then on.  Where the list overflowed meanwhile (many equal or rising values) the rounds
-// since are read once more, each with a bound over the 256 threads' maxima by value and
-// index, which at most (K - 1) * 32 + 1 elements of a round reach, whatever they are.
-// Meeting in every round made rows of 152064 take 1.5 times as long.
+// what exceeds it.  After 1, 2, 4 rounds and then every kCheck the threads meet; a list past
+// K + kSlack entries is ranked (each entry counts the better ones) and cut to K, whose last
+// is the bound from then on: a thread that appends costs its warp half a round.  Where the
+// list overflowed meanwhile (many equal or rising values) the rounds since are read once
+// more, each with a bound over the 256 threads' maxima by value and index, which at most
+// (K - 1) * 32 + 1 elements of a round reach, whatever they are.
 // The rare parts are rolled loops, in line: unrolled, the kernel had 78 KB of code; as
 // function calls they made the compiler wait for the next round's loads at every call.
+//
+// Measured, bf16: 2048 rows of 152064 with 5 alternatives 133 us (4.7 TB/s; the bytes' floor
+// 92), without any 104; 32 sequences of up to 5 rows of 128256 with 20 alternatives 20.7,
+// without 11; 5 fp32 rows of 1000 5.5.  What is left of the alternatives is the appends (12
+// of 133 us, 4 of 20.7), the meetings and, in parts, the merge.  Alternatives: meeting in
+// every round 1.5 times as long (rows of 152064), no cut before the end 155 us, cuts at
+// 2 K + 16 entries 3 us more, the round's maximum over widened values 2.
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
@@ -40,8 +48,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVecs = 4;          // 16-byte loads of a thread per round
 constexpr int kCap = 2048;        // list entries
-constexpr int kSoft = 128;        // list length that is cut to K
-constexpr int kCheck = 4;         // rounds between two looks at the list
+constexpr int kSlack = 8;         // entries beyond K that cut the list to K
+constexpr int kCheck = 4;         // most rounds between two looks at the list
 constexpr int kMaxParts = 32;
 constexpr float kFarBelow = -1000.f;  // 2^y is +0 there; keeps -inf out of products
 
@@ -98,15 +106,20 @@ template <> __device__ __forceinline__ void widen<__nv_bfloat16>(const uint4& r,
     }
 }
 
-// Largest element of a vector.
-template <typename T> __device__ __forceinline__ float max_of(const uint4& r) {
-    constexpr int EPV = per_vec<T>();
-    float e[EPV];
-    widen<T>(r, e);
-    float m = fmaxf(e[0], e[1]);
+// Largest element of N vectors.  (bf16: in pairs as they lie, so that the values need not be
+// widened for it)
+template <typename T, int N> __device__ __forceinline__ float max_of(const uint4 (&r)[N]) {
+    auto two = [](uint32_t a, uint32_t b) {
+        uint32_t m;
+        if constexpr (sizeof(T) == 4) m = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+        else asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+        return m;
+    };
+    uint32_t m = two(two(r[0].x, r[0].y), two(r[0].z, r[0].w));
 #pragma unroll
-    for (int j = 2; j < EPV; j += 2) m = fmax3(m, e[j], e[j + 1]);
-    return m;
+    for (int u = 1; u < N; ++u) m = two(m, two(two(r[u].x, r[u].y), two(r[u].z, r[u].w)));
+    return sizeof(T) == 4 ? __uint_as_float(m)
+                          : fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
 // Vector v of a row: elements v * EPV - off .. of [0, V), -inf outside and for v >= end.
@@ -173,37 +186,42 @@ __device__ __forceinline__ int cut(Shared& s, int count, int K) {
     return kept;
 }
 
-// Appends the elements of a thread's round (vectors cur with maxima vm, elements from
-// `first` on, `stride` apart) that lie above `above` and reach the bound (bv at index bx at
-// the latest, or at any index: INT_MAX); returns the last place taken, -1 for none.  Most
-// calls find one element: a vector whose maximum is too small is not looked into.
-template <typename T>
-__device__ __forceinline__ int append(Shared& s, const uint4 (&cur)[kVecs], const float (&vm)[kVecs],
-                                      int first, float above, float bv, int bx) {
+// Appends the elements of a thread's round (vectors cur, elements from `first` on) that
+// exceed `above` (ABOVE), reach bv (REACH), or both, an equal of bv at index bx at the
+// latest (BOTH).  Most calls find one element: a vector whose maximum is too small is not
+// looked into.
+enum { ABOVE, REACH, BOTH };
+template <typename T, int HOW>
+__device__ __forceinline__ void append(Shared& s, const uint4 (&cur)[kVecs], int first, float above,
+                                       float bv, int bx) {
     constexpr int EPV = per_vec<T>(), EPW = EPV / 4;  // elements of a vector, of a word
-    int place = -1;
+    const float least = HOW == ABOVE ? above : bv;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-        if (!(vm[u] > above && vm[u] >= bv)) continue;
+        const uint4 one[1] = {cur[u]};
+        const float vm = max_of<T>(one);
+        if (HOW == ABOVE ? !(vm > least) : !(vm >= least)) continue;
         float e[EPV];
         widen<T>(cur[u], e);
         const int at = first + u * kThreads * EPV;
         uint32_t bits = 0;
 #pragma unroll
         for (int j = 0; j < EPV; ++j)
-            bits |= (uint32_t)(e[j] > above && !better(bv, bx, e[j], at + j)) << j;
+            bits |= (uint32_t)(HOW == ABOVE   ? e[j] > above
+                               : HOW == REACH ? e[j] >= bv
+                                              : e[j] > above && !better(bv, bx, e[j], at + j))
+                    << j;
 #pragma unroll 1
         for (; bits; bits &= bits - 1) {
             const int j = __ffs(bits) - 1, q = j / EPW;
             const uint32_t w = q == 0 ? cur[u].x : q == 1 ? cur[u].y : q == 2 ? cur[u].z : cur[u].w;
-            place = atomicAdd(&s.count, 1);
+            const int place = atomicAdd(&s.count, 1);
             if (place < kCap) {
                 s.v[place] = __uint_as_float(EPW == 1 ? w : j & 1 ? w & 0xffff0000u : w << 16);
                 s.i[place] = at + j;
             }
         }
     }
-    return place;
 }
 
 // Index of the first element of a thread's round that equals v.
@@ -267,8 +285,8 @@ __device__ __forceinline__ float bound_of_groups(Shared& s, float bm, int K) {
     return s.bound_v;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logprob_kernel(const LogprobArgs a) {
+template <typename T, bool TOP, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobArgs a) {
     constexpr int EPV = per_vec<T>();
     __shared__ Shared s;
     const int tid = threadIdx.x, S = a.parts, K = a.K;
@@ -287,8 +305,10 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
     const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.V;
     // vectors of 16 bytes on memory's grid (indexes inside a row are 32-bit)
     const int V = (int)a.V, off = (int)(((uint64_t)row * (uint64_t)a.V) % EPV);
-    const int vecs = (int)(((int64_t)V + off + EPV - 1) / EPV), per = (vecs + S - 1) / S;
-    const int v0 = part * per, v1 = min(v0 + per, vecs);
+    constexpr int kRound = kVecs * kThreads;
+    const int vecs = (int)(((int64_t)V + off + EPV - 1) / EPV);
+    const int per = S == 1 ? vecs : a.part_rounds * kRound;
+    const int v0 = part * per, v1 = part == S - 1 ? vecs : v0 + per;
     const float c = a.c;
     uint64_t l2 = f2(0.f, 0.f), a2 = l2;
     float m = -INFINITY;
@@ -319,10 +339,7 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
 #pragma unroll 1
     for (int v = v0; v < v1; v += kVecs * kThreads) {
         if (v + kVecs * kThreads < v1) fetch(nxt, v + kVecs * kThreads);
-        float vm[kVecs];
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) vm[u] = max_of<T>(cur[u]);
-        const float bm = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
+        const float bm = max_of<T>(cur);
         if (bm > m) {
             float p, q;
             Stats old;
@@ -360,23 +377,23 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
             else if (part == 0) raise_device_error(a.dev_err, SPEC_DEVERR_TOKEN);
         }
         if (TOP) {
-            constexpr int kRound = kVecs * kThreads;
             const int at = (v + tid) * EPV - off;
             if (v == v0) {
                 const float bv = bound_of_groups(s, bm, K);
-                if (bm >= bv) append<T>(s, cur, vm, at, -INFINITY, bv, INT_MAX);
+                // (-inf is no alternative)
+                if (bm >= bv) append<T, REACH>(s, cur, at, -INFINITY, fmaxf(bv, -FLT_MAX), INT_MAX);
                 tau = bv;
             } else if (bm > tau) {
-                append<T>(s, cur, vm, at, tau, -INFINITY, INT_MAX);
+                append<T, ABOVE>(s, cur, at, tau, -INFINITY, INT_MAX);
             }
             const bool end = v + kRound >= v1;
-            if (end || v == v0 || (v - checked) >= (kCheck - 1) * kRound) {
+            if (end || v == v0 || v + kRound - checked >= min(kCheck * kRound, checked - v0)) {
                 __syncthreads();
                 int count = s.count;
                 if (count > kCap) {
-                    // entries from before (at most kSoft) stand in front
+                    // entries from before (at most K + kSlack) stand in front
                     const int before =
-                        v == v0 ? 0 : __syncthreads_count(tid < kSoft && s.i[tid] < checked * EPV - off);
+                        v == v0 ? 0 : __syncthreads_count(tid < K + kSlack && s.i[tid] < checked * EPV - off);
                     if (v == v0) tau = -INFINITY;
                     __syncthreads();
                     if (tid == 0) s.count = before;
@@ -384,9 +401,7 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
                     for (int w = checked; w <= v; w += kRound) {
                         fetch(cur, w);
                         const int first = (w + tid) * EPV - off;
-#pragma unroll
-                        for (int u = 0; u < kVecs; ++u) vm[u] = max_of<T>(cur[u]);
-                        const float top = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
+                        const float top = max_of<T>(cur);
                         const int bi = index_of<T>(cur[0], cur[1], cur[2], cur[3], first, top);
                         s.tv[tid] = top;
                         s.ti[tid] = bi;
@@ -403,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
                             s.bound_i = bi;
                         }
                         __syncthreads();
-                        append<T>(s, cur, vm, first, tau, s.bound_v, s.bound_i);
+                        append<T, BOTH>(s, cur, first, tau, s.bound_v, s.bound_i);
                         __syncthreads();
                         count = s.count;
                         cut(s, count, K);
                         if (count >= K) tau = s.v[K - 1];
                         __syncthreads();
                     }
-                } else if (count > kSoft && !end) {
+                } else if (count > K + kSlack && !end) {
                     cut(s, count, K);
                     tau = s.v[K - 1];
                     __syncthreads();  // before the next round appends
@@ -508,15 +523,22 @@ __global__ void __launch_bounds__(kThreads, TOP && sizeof(T) == 2 ? 3 : 4) logpr
 
 }  // namespace
 
-// Parts of a row: four CTAs an SM where the rows alone are fewer, a round of
-// loads at least for each part.
-int logprob_parts(const LogprobArgs& a, int num_sms, int max_tickets) {
-    const int64_t rows = (int64_t)a.B * a.n;
+// Rounds that a row takes at least (one more where it begins inside a vector).
+static int64_t rounds_of(const LogprobArgs& a) {
     const int64_t round = kThreads * kVecs * (a.dtype == SPEC_DTYPE_F32 ? 4 : 8);
-    const int64_t most = (a.V + round - 1) / round, want = (4 * (int64_t)num_sms + rows - 1) / rows;
+    return (a.V + round - 1) / round;
+}
+
+// Parts of a row: four CTAs an SM where the rows alone are fewer, each of whole rounds and
+// as many as the others but for the last.
+int logprob_parts(const LogprobArgs& a, int num_sms, int max_tickets) {
+    const int64_t rows = (int64_t)a.B * a.n, most = rounds_of(a);
+    const int64_t want = (4 * (int64_t)num_sms + rows - 1) / rows;
+    if (rows > max_tickets) return 1;
     int64_t s = want < most ? want : most;
     if (s > kMaxParts) s = kMaxParts;
-    return rows > max_tickets ? 1 : (int)s;
+    const int64_t rounds = (most + s - 1) / s;
+    return (int)((most + rounds - 1) / rounds);
 }
 
 size_t logprob_workspace_bytes(const LogprobArgs& a) {
@@ -525,15 +547,22 @@ size_t logprob_workspace_bytes(const LogprobArgs& a) {
 
 cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.n;
+    // (parts - 1) part_rounds < rounds_of(a): no part is empty
+    a.part_rounds = (int)((rounds_of(a) + a.parts - 1) / a.parts);
     a.part_stats = static_cast<float*>(workspace);
     a.part_v = a.part_stats + rows * a.parts * 4;
     a.part_i = reinterpret_cast<int32_t*>(a.part_v + rows * a.parts * a.K);
     const dim3 grid((unsigned)(rows * a.parts)), block(kThreads);
-    if (a.dtype == SPEC_DTYPE_F32)
-        return a.K ? launch_dependent(logprob_kernel<float, true>, grid, block, 0, stream, a)
-                   : launch_dependent(logprob_kernel<float, false>, grid, block, 0, stream, a);
-    return a.K ? launch_dependent(logprob_kernel<__nv_bfloat16, true>, grid, block, 0, stream, a)
-               : launch_dependent(logprob_kernel<__nv_bfloat16, false>, grid, block, 0, stream, a);
+    // CTAs of an SM: four (64 registers) hide more of the loads.  Rows in parts with
+    // alternatives are faster with three: fewer of the given rows may be in use, and four
+    // of those on one SM are what the others wait for.  2048 rows of 152064, 5 alternatives:
+    // 132 us with four, 143 with three; 32 x up to 5 rows of 128256, 20 alternatives: 23.2, 20.4.
+    const bool f32 = a.dtype == SPEC_DTYPE_F32, three = a.K && !f32 && a.parts > 1;
+    auto* kern = f32 ? (a.K ? logprob_kernel<float, true, 4> : logprob_kernel<float, false, 4>)
+                 : three ? logprob_kernel<__nv_bfloat16, true, 3>
+                 : a.K   ? logprob_kernel<__nv_bfloat16, true, 4>
+                         : logprob_kernel<__nv_bfloat16, false, 4>;
+    return launch_dependent(kern, grid, block, 0, stream, a);
 }
 
 }  // namespace specv
