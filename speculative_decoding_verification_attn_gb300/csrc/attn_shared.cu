@@ -41,6 +41,22 @@
 //    and an abort flag, after which every role skips its remaining work, drains
 //    its copies and tensor-core operations, and returns.
 //
+// What bounds it (cycles of an SM): a narrow bf16 tile ~2700, which is its share of HBM
+// (7.0 TB/s); a wide one ~4500 (1000 TFLOP/s), the chain S, softmax, P V of a stream with one
+// S buffer, of which the tensor core is busy 1024; e4m3 ~3600 and ~6000, INT8 ~4150 and ~7300,
+// the scales in the softmax and the widening of narrow tiles.  And ~17 us of a call: the
+// list ~4, first loads, the last pieces, the join ~5 and 2 KB of fp32 for every row.
+// Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 48 us
+// (117 each by itself; the bytes' floor 13.7); 128 in four groups, 2-8K shared, 100-1500
+// own, 64/8 heads, e4m3 264 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
+// heads, INT8 225 (484; 62).
+// Measured and not kept: S in two buffers of 64 keys a stream, Q K^T a buffer ahead of the
+// softmax: wide blocks 13 % faster (16 trees behind 8K, bf16, 61 -> 53 us), narrow tiles 8 %
+// (bf16) to 25 % (codes) slower, since a tile's softmax then takes twice the meetings and
+// waits, and a K slot is free only after the second; own keys of e4m3 by the kernel that
+// feeds codes to 8-bit MMAs, in a launch of its own: 252 against 258 us on the 128
+// sequences, 50 against 45 and 65 against 52 on smaller calls.
+//
 // Every query's pieces meet in a second launch: rows of whole segments wait in
 // two fp32 arrays (own keys, prefix), those of segments that a range cuts in two
 // slots per range.
@@ -69,10 +85,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 40.0f;  // log2 units
 // What the split over the CTAs charges, in quarters of a narrow tile's time: a tile
 // of a wide block (two Q tiles), and a piece's fixed work.  A narrow piece's end lies
-// under the other stream's tiles; a wide one holds both streams.  Measured from
-// (8, 12, 12), one charge for all pieces: 144 sequences of 10-150 own keys behind 208
-// shared 283 -> 175 us, 39 sequences of one group 69 -> 50 us, the e4m3 prompts of 32
-// rollouts 266 -> 259 us.
+// under the other stream's tiles and goes with its rows (3 or 4 for 32 of them, which are
+// 16 KB of fp32 to write); a wide one holds both streams.  Measured: one charge of 12 for
+// all pieces left 144 sequences of 10-150 own keys behind 208 shared at 283 us against 138,
+// 39 sequences of one group 69 against 51; one of 4 for narrow pieces of any rows left 16
+// sequences of 112 rows behind 32K shared keys at 239 against 149.
 constexpr int kTileCost = 4;
 struct Cost {
     int wide, piece, wide_piece;
@@ -553,8 +570,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     // (rows of a Q tile that no copy of q writes hold anything: a row of S, P or O
     // depends on its own row of Q alone, and those are not stored)
     const int opt = kTileCost * a.split_alpha;
-    const Cost cost = {KV == KV_BF16 ? 8 : KV == KV_E4M3 ? 7 : 6,
-                       opt >= 0 ? opt : KV == KV_I8 ? 5 : 4, opt >= 0 ? opt : 24};
+    const Cost cost = {KV == KV_E4M3 ? 7 : 8,
+                       opt >= 0 ? opt : (k * G + 31) / 32 * (KV == KV_I8 ? 4 : 3), opt >= 0 ? opt : 24};
     const int V = build_list<NTH>(prm, s_seg, s_tpre, s_cpre, s_narrow, cost, NT);
     const List L = {s_seg, s_tpre, a.B, Hkv, NT, V};
     if (warp == 0) {
