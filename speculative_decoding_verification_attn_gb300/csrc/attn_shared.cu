@@ -43,13 +43,13 @@
 //
 // What bounds it (cycles of an SM): a narrow bf16 tile ~2700, which is its share of HBM
 // (7.0 TB/s); a wide one ~4500 (1000 TFLOP/s), the chain S, softmax, P V of a stream with one
-// S buffer, of which the tensor core is busy 1024; e4m3 ~3600 and ~6000, INT8 ~4150 and ~7300,
+// S buffer, of which the tensor core is busy 1024; e4m3 ~3550 and ~6000, INT8 ~4100 and ~7000,
 // the scales in the softmax and the widening of narrow tiles.  And ~17 us of a call: the
 // list ~4, first loads, the last pieces, the join ~5 and 2 KB of fp32 for every row.
 // Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 48 us
 // (117 each by itself; the bytes' floor 13.7); 128 in four groups, 2-8K shared, 100-1500
-// own, 64/8 heads, e4m3 264 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
-// heads, INT8 225 (484; 62).
+// own, 64/8 heads, e4m3 260 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
+// heads, INT8 216 (484; 62).
 // Measured and not kept: S in two buffers of 64 keys a stream, Q K^T a buffer ahead of the
 // softmax: wide blocks 13 % faster (16 trees behind 8K, bf16, 61 -> 53 us), narrow tiles 8 %
 // (bf16) to 25 % (codes) slower, since a tile's softmax then takes twice the meetings and
@@ -120,11 +120,12 @@ struct Smem {
     static constexpr int PIDS = STAT + 3 * 2 * 2 * ROWS * 4;  // [2 producers][LOOKAHEAD+1][8] int
     // scales of a slot's use u at stage u % 2 of the slot, K then V.  Two stages: a
     // tile's softmax may still read its scales when its K slot is refilled.
-    // e4m3: fp32 for every 16 keys, K's (with the softmax scale), V's and V's logarithm;
+    // e4m3: fp32 for every 16 keys, K's (with the softmax scale), V's, V's logarithm and
+    // reciprocal;
     // INT8: the fp16 words as they are stored, and the least and largest of K's for
     // every 16 keys
     static constexpr int SCALE = (PIDS + 2 * (LOOKAHEAD + 1) * NVB * 4 + 15) / 16 * 16;
-    static constexpr int SCRAW = SCALE + 4 * 24 * 4;
+    static constexpr int SCRAW = SCALE + 4 * 32 * 4;
     static constexpr int SEG = SCRAW + 4 * 2 * TN * 2;    // int4 [MAX_SEGS]
     static constexpr int TPRE = SEG + MAX_SEGS * 16;
     static constexpr int CPRE = TPRE + (MAX_SEGS + 4) * 4;
@@ -436,7 +437,7 @@ __device__ __forceinline__ void widen16(const uint4 r, uint4& lo, uint4& hi) {
 
 // The keys' scales of a tile as its softmax reads them.
 template <int KV> struct Scales {
-    const float* e4m3;    // of 16 keys: K's; 8 words on V's; 16 words on log2 of V's
+    const float* e4m3;    // of 16 keys: K's; 8 words on V's; 16 on log2 of V's; 24 on 1 / V's
     const __half* i8;     // K, and 128 on V
 };
 
@@ -511,7 +512,7 @@ __device__ __forceinline__ void weights(const uint32_t (&v)[N], const Scales<KV>
             pk[c / 2 + u] = pack_bf16x2(e0, e1);
         }
         // (the sums of 16 keys that share a scale, without it)
-        if (LOGV && c % 16 == 8) l = fmaf(total(), __frcp_rn(sc.e4m3[8 + (c0 + c) / 16]), l);
+        if (LOGV && c % 16 == 8) l = fmaf(total(), sc.e4m3[24 + (c0 + c) / 16], l);
     }
     if (!LOGV) l += total();
 }
@@ -539,7 +540,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     Seg* s_seg = reinterpret_cast<Seg*>(sm + Smem::SEG);
     int* s_tpre = reinterpret_cast<int*>(sm + Smem::TPRE);
     int* s_cpre = reinterpret_cast<int*>(sm + Smem::CPRE);
-    float* s_scale = reinterpret_cast<float*>(sm + Smem::SCALE);  // [slot][stage][24]
+    float* s_scale = reinterpret_cast<float*>(sm + Smem::SCALE);  // [slot][stage][32]
     __half* s_half = reinterpret_cast<__half*>(sm + Smem::SCRAW);  // [slot][stage][2][TN]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -624,8 +625,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     auto narrow_tiles = [&](int s) { return uniform(s_rng->n[s + 1] - s_rng->n[s]); };
 
     // Registers (a thread, per warpgroup; the launch gives 96, with codes 72): softmax
-    // 104 / 80, MMAs and copies 64 / 56, widening 64 (4 x 104 + 64 = 5 x 96, 4 x 80 + 56 +
-    // 2 x 64 = 7 x 72)
+    // 104 / 88, MMAs and copies 64 / 56, widening 48 (4 x 104 + 64 = 5 x 96, 4 x 88 + 56 +
+    // 2 x 48 = 7 x 72; with 80 and 64 INT8 was 3 % slower)
     if (warp >= 16 && warp < 20) {
         regs_dec<CODES ? 56 : 64>();
         if (warp == 17 || warp == 18) {
@@ -690,9 +691,12 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
             };
             auto put_scale = [&](float x, int i) {
                 if (lane >= 16) return;
-                float* to = s_scale + (2 * s + (i & 1)) * 24 + lane;
+                float* to = s_scale + (2 * s + (i & 1)) * 32 + lane;
                 to[0] = lane < 8 ? x * a.scale * kLog2e : x;
-                if (lane >= 8) to[8] = log2f(x);
+                if (lane >= 8) {
+                    to[8] = log2f(x);
+                    to[16] = __frcp_rn(x);
+                }
             };
 #pragma unroll 1
             for (int i = 0; i < LOOKAHEAD; ++i) fetch_pids(i);
@@ -908,7 +912,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
         }
     } else if (CODES && warp >= 20) {
         if constexpr (CODES) {
-            regs_dec<64>();
+            regs_dec<48>();
             // ================= widening of slot s (warps 20-23, 24-27) =================
             // Each code exactly to bf16, in place, in the layout the MMAs read.  The raw tile
             // sits in the upper half of its slot, row r at 16 KB + 128 r; its bf16 row
@@ -936,7 +940,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                         // bounds of K's scales over 16 keys, and no V scale past the end (a
                         // weight of 0 times whatever is stored there)
                         __half* raw = s_half + (2 * s + (i & 1)) * 2 * TN;
-                        float* to = s_scale + (2 * s + (i & 1)) * 24;
+                        float* to = s_scale + (2 * s + (i & 1)) * 32;
                         const int j = ct;
                         const float x = __half2float(raw[j]);
                         float lo = j < nvalid ? x : INFINITY, hi = j < nvalid ? x : 0.f;
@@ -994,7 +998,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
             }
         }
     } else {
-        regs_inc<CODES ? 80 : 104>();
+        regs_inc<CODES ? 88 : 104>();
         // ================= softmax of stream s =================
         // Two warps for the 32 rows of a TMEM quadrant, each on 64 of the tile's keys and
         // 64 of O's columns; they meet at the row's maximum.
@@ -1032,7 +1036,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 const int use = wide ? (slot == s ? n : other) + ((t - n) >> 1) : t;
                 const int stage = 2 * slot + (use & 1);
                 // scales of this half: e4m3 (and INT8's bounds) 4 of 8, INT8 64 of 128
-                const Scales<KV> sc = {s_scale + stage * 24 + half * 4,
+                const Scales<KV> sc = {s_scale + stage * 32 + half * 4,
                                        s_half + stage * 2 * TN + half * 64};
                 const uint64_t vis =
                     visible64(cur.key0(L), half * 64, cur.valid(L), ctx, mrow);
@@ -1109,7 +1113,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                 // compiler no longer runs the exponents under the products.)
                 constexpr bool LOGV = KV == KV_E4M3;
                 if (!slow) {
-#pragma unroll(KV == KV_I8 ? 2 : 1)
+#pragma unroll(KV == KV_E4M3 ? 2 : 1)
                     for (int c = 0; c < 64; c += 32) {
                         uint32_t v[32], pk[16];
                         tmem_ld32(s_mine + c, v);
