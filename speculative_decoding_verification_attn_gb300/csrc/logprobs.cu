@@ -30,12 +30,15 @@
 // The rare parts are rolled loops, in line: unrolled, the kernel had 78 KB of code; as
 // function calls they made the compiler wait for the next round's loads at every call.
 //
-// Measured, bf16: 2048 rows of 152064 with 5 alternatives 133 us (4.7 TB/s; the bytes' floor
-// 92), without any 104; 32 sequences of up to 5 rows of 128256 with 20 alternatives 20.7,
-// without 11; 5 fp32 rows of 1000 5.5.  What is left of the alternatives is the appends (12
-// of 133 us, 4 of 20.7), the meetings and, in parts, the merge.  Alternatives: meeting in
-// every round 1.5 times as long (rows of 152064), no cut before the end 155 us, cuts at
-// 2 K + 16 entries 3 us more, the round's maximum over widened values 2.
+// Rows that a warp can hold (1024 elements) go to a kernel of their own, a warp each; many
+// rows of up to 8192 to CTAs of 64 threads.
+//
+// Measured, bf16: 2048 rows of 152064 with 5 alternatives 124 us (5.0 TB/s; the bytes' floor
+// 92), without any 103; 32 sequences of up to 5 rows of 128256 with 20 alternatives 19.5,
+// without 11; 5 fp32 rows of 1000 4.0.  What is left of the alternatives is the appends (12
+// and 4 us of those), the meetings and, in parts, the merge.  Alternatives: meeting in
+// every round 1.5 times as long (rows of 152064), no cut before the end 22 us more, cuts at
+// 2 K + 16 entries 3, the round's maximum over widened values 2.
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -45,9 +48,7 @@
 namespace specv {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kVecs = 4;          // 16-byte loads of a thread per round
-constexpr int kCap = 2048;        // list entries
 constexpr int kSlack = 8;         // entries beyond K that cut the list to K
 constexpr int kCheck = 4;         // most rounds between two looks at the list
 constexpr int kMaxParts = 32;
@@ -122,38 +123,58 @@ template <typename T, int N> __device__ __forceinline__ float max_of(const uint4
                           : fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
-// Vector v of a row: elements v * EPV - off .. of [0, V), -inf outside and for v >= end.
-// The vectors lie on the 16-byte grid of memory; one that is not whole is read element by
-// element, so nothing outside the row is.
-template <typename T>
-__device__ __forceinline__ uint4 load_edge(const T* row, int V, int off, int v, int end) {
+// Vectors v0 + u step of a row: elements v EPV - off .. of [0, V), -inf outside and for
+// v >= end.  The vectors lie on the 16-byte grid of memory; one at a row's edge is read whole
+// and then masked, but for the tensor's last, of which the tensor has `left` elements from
+// the row's first on.
+template <typename T, int N>
+__device__ __forceinline__ void load_edge(uint4 (&r)[N], const T* row, int V, int64_t left, int off,
+                                          int v0, int step, int end) {
     constexpr int EPV = per_vec<T>(), EPW = EPV / 4;
-    const int64_t e = (int64_t)v * EPV - off;
-    if (v < end && e >= 0 && e + EPV <= V) return __ldg(reinterpret_cast<const uint4*>(row + e));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll 1
-    for (int i = 0; i < EPV; ++i) {
-        const T x = v < end && e + i >= 0 && e + i < V ? row[e + i] : Elem<T>::from_f32(-INFINITY);
-        uint32_t bits;
-        if constexpr (sizeof(T) == 4) bits = __float_as_uint(x);
-        else bits = (uint32_t)__bfloat16_as_ushort(x) << (16 * (i & 1));
-        const int j = i / EPW;
-        w[0] |= j == 0 ? bits : 0;
-        w[1] |= j == 1 ? bits : 0;
-        w[2] |= j == 2 ? bits : 0;
-        w[3] |= j == 3 ? bits : 0;
+    constexpr uint32_t kNone = EPW == 1 ? 0xff800000u : 0xff80ff80u;  // -inf
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int v = v0 + u * step;
+        const int64_t e = (int64_t)v * EPV - off;
+        r[u] = make_uint4(kNone, kNone, kNone, kNone);
+        if (v < end && e + EPV <= left) r[u] = __ldg(reinterpret_cast<const uint4*>(row + e));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const int v = v0 + u * step;
+        const int64_t e = (int64_t)v * EPV - off;
+        if (v >= end || (e >= 0 && e + EPV <= V)) continue;
+        uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
+        const bool last = e + EPV > left;  // nothing was read
+#pragma unroll 1
+        for (int i = 0; i < EPV; ++i) {
+            const bool in = e + i >= 0 && e + i < V;
+            if (in && !last) continue;
+            uint32_t bits = EPW == 1 ? 0xff800000u : 0xff80u;
+            if (in) {
+                if constexpr (EPW == 1) bits = __float_as_uint(row[e + i]);
+                else bits = __bfloat16_as_ushort(row[e + i]);
+            }
+            const uint32_t keep = EPW == 1 ? 0u : 0xffff0000u >> (16 * (i & 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j == i / EPW) w[j] = (w[j] & keep) | bits << (EPW == 1 ? 0 : 16 * (i & 1));
+        }
+        r[u] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
-struct Shared {
+template <int TH> struct Shared {
+    // list entries: a round's second look leaves (K - 1) kVecs EPV + 1 at most, after K +
+    // kSlack from before
+    static constexpr int kCap = TH == 256 ? 2048 : 1056;
     float v[kCap];
     int i[kCap];
-    alignas(16) float tv[kThreads];  // maxima of the groups or threads
-    int ti[kThreads];
+    alignas(16) float tv[TH];  // maxima of the groups or threads
+    int ti[TH];
     float best_v[32];
     int best_i[32];
-    float4 stats[kThreads / 32];
+    float4 stats[TH / 32];
     float bound_v;
     int bound_i;
     int count, last;
@@ -161,10 +182,10 @@ struct Shared {
 
 // Ranks the first `count` entries of the list and leaves its K best, sorted, at
 // the front (every thread calls it; the list is complete and visible).
-__device__ __forceinline__ int cut(Shared& s, int count, int K) {
+template <int TH> __device__ __forceinline__ int cut(Shared<TH>& s, int count, int K) {
     const int tid = threadIdx.x;
 #pragma unroll 1
-    for (int e = tid; e < count; e += kThreads) {
+    for (int e = tid; e < count; e += TH) {
         const float v = s.v[e];
         const int i = s.i[e];
         int rank = 0;
@@ -191,8 +212,8 @@ __device__ __forceinline__ int cut(Shared& s, int count, int K) {
 // latest (BOTH).  Most calls find one element: a vector whose maximum is too small is not
 // looked into.
 enum { ABOVE, REACH, BOTH };
-template <typename T, int HOW>
-__device__ __forceinline__ void append(Shared& s, const uint4 (&cur)[kVecs], int first, float above,
+template <typename T, int HOW, int TH>
+__device__ __forceinline__ void append(Shared<TH>& s, const uint4 (&cur)[kVecs], int first, float above,
                                        float bv, int bx) {
     constexpr int EPV = per_vec<T>(), EPW = EPV / 4;  // elements of a vector, of a word
     const float least = HOW == ABOVE ? above : bv;
@@ -203,7 +224,7 @@ __device__ __forceinline__ void append(Shared& s, const uint4 (&cur)[kVecs], int
         if (HOW == ABOVE ? !(vm > least) : !(vm >= least)) continue;
         float e[EPV];
         widen<T>(cur[u], e);
-        const int at = first + u * kThreads * EPV;
+        const int at = first + u * TH * EPV;
         uint32_t bits = 0;
 #pragma unroll
         for (int j = 0; j < EPV; ++j)
@@ -216,7 +237,7 @@ __device__ __forceinline__ void append(Shared& s, const uint4 (&cur)[kVecs], int
             const int j = __ffs(bits) - 1, q = j / EPW;
             const uint32_t w = q == 0 ? cur[u].x : q == 1 ? cur[u].y : q == 2 ? cur[u].z : cur[u].w;
             const int place = atomicAdd(&s.count, 1);
-            if (place < kCap) {
+            if (place < s.kCap) {
                 s.v[place] = __uint_as_float(EPW == 1 ? w : j & 1 ? w & 0xffff0000u : w << 16);
                 s.i[place] = at + j;
             }
@@ -225,7 +246,7 @@ __device__ __forceinline__ void append(Shared& s, const uint4 (&cur)[kVecs], int
 }
 
 // Index of the first element of a thread's round that equals v.
-template <typename T>
+template <typename T, int TH>
 __device__ __forceinline__ int index_of(uint4 c0, uint4 c1, uint4 c2, uint4 c3, int first, float v) {
     constexpr int EPV = per_vec<T>(), EPW = EPV / 4;
 #pragma unroll 1
@@ -234,40 +255,228 @@ __device__ __forceinline__ int index_of(uint4 c0, uint4 c1, uint4 c2, uint4 c3, 
         const uint4 r = u == 0 ? c0 : u == 1 ? c1 : u == 2 ? c2 : c3;
         const uint32_t w = j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
         if (__uint_as_float(EPW == 1 ? w : h ? w & 0xffff0000u : w << 16) == v)
-            return first + u * kThreads * EPV + e % EPV;
+            return first + u * TH * EPV + e % EPV;
     }
     return INT_MAX;
 }
 
-// What is written for a row: stats complete, the sorted alternatives in s.  (fp32: on this
-// GPU a 64-bit logarithm by every warp took longer than the row.)
-template <typename T>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, Shared& s, const Stats& st, int64_t row,
-                                          float token, int found) {
-    const int tid = threadIdx.x;
-    if (tid >= 32) return;
+// What is written for a row, by a warp: stats complete, the sorted alternatives in v, id.
+// (fp32: on this GPU a 64-bit logarithm by every warp took longer than the row.)
+__device__ __forceinline__ void write_row(const LogprobArgs& a, const float* v, const int* id,
+                                          const Stats& st, int64_t row, float token, int found) {
+    const int lane = threadIdx.x & 31;
     const bool none = st.l == 0.f;  // every logit is -inf
     const float lnl = logf(st.l);
     // z - lse = (x - m) / T - ln l, from the difference on
     auto lp = [&](float x) { return none ? -INFINITY : (x - st.m) * a.inv_t - lnl; };
-    if (tid == 0) {
+    if (lane == 0) {
         a.logprob[row] = lp(token);
         if (a.entropy) a.entropy[row] = none ? 0.f : lnl - 0.69314718055994530942f * (st.a / st.l);
     }
-    if (tid < a.K) {
-        const bool have = tid < found;
-        if (a.top_ids) a.top_ids[row * a.K + tid] = have ? s.i[tid] : -1;
-        if (a.top_logprobs) a.top_logprobs[row * a.K + tid] = have ? lp(s.v[tid]) : -INFINITY;
+    if (lane < a.K) {
+        const bool have = lane < found;
+        if (a.top_ids) a.top_ids[row * a.K + lane] = have ? id[lane] : -1;
+        if (a.top_logprobs) a.top_logprobs[row * a.K + lane] = have ? lp(v[lane]) : -INFINITY;
     }
 }
 
-// The K-th largest of the maxima of 64 groups of four threads (bm: a thread's), which K
+// The given token's logit (lane 0), -inf and a flag for one that is none.
+template <typename T> __device__ __forceinline__ float token_logit(const LogprobArgs& a, const T* x, int tok) {
+    if (tok >= 0 && tok < (int)a.V) return Elem<T>::to_f32(x[tok]);
+    raise_device_error(a.dev_err, SPEC_DEVERR_TOKEN);
+    return -INFINITY;
+}
+
+// Adds a vector's weights to the sums l2 and a2 (in halves), relative to m.
+template <typename T>
+__device__ __forceinline__ void add_weights(const uint4& r, float m, float c, uint64_t& l2, uint64_t& a2) {
+    constexpr int EPV = per_vec<T>();
+    const uint64_t neg = f2(-m, -m), cc = f2(c, c);
+    float e[EPV];
+    widen<T>(r, e);
+#pragma unroll
+    for (int j = 0; j < EPV; j += 2) {
+        float y0, y1;
+        f2_split(f2_mul(f2_add(f2(e[j], e[j + 1]), neg), cc), y0, y1);
+        y0 = max_nan(y0, kFarBelow);
+        y1 = max_nan(y1, kFarBelow);
+        const uint64_t w = f2(fast_exp2(y0), fast_exp2(y1));
+        l2 = f2_add(l2, w);
+        a2 = f2_fma(w, f2(y0, y1), a2);
+    }
+}
+
+// Short rows (kSmall elements, those before it in its first vector among them): a warp
+// holds a row in registers.  The bound is the K-th largest of 64 maxima (each lane's first
+// and second halves of its vectors); what reaches it goes to the warp's list by a running
+// sum of the lanes' counts and is ranked there.  Against a CTA per row: 51480 rows of 466 with
+// 32 alternatives 85 us, 2172; 32768 of 1000 with 5 57, 479, without 16, 425; 5 of them 4.0, 5.3.
+constexpr int kSmall = 1024;
+constexpr int kSmallWarps = 4;
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kSmallWarps * 32) logprob_small_kernel(const LogprobArgs a) {
+    constexpr int EPV = per_vec<T>(), U = kSmall / 32 / EPV;
+    __shared__ float s_list[TOP ? kSmallWarps : 1][TOP ? kSmall : 1];
+    __shared__ int s_id[TOP ? kSmallWarps : 1][TOP ? kSmall : 1];
+    __shared__ __align__(16) float s_max[kSmallWarps][64];
+    __shared__ float s_best[kSmallWarps][33];  // and the bound
+    __shared__ int s_best_id[kSmallWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, K = a.K;
+    grid_dep_launch_dependents();
+    grid_dep_wait();
+    const int row = blockIdx.x * kSmallWarps + warp;
+    if (row >= a.B * a.n) return;
+    if (a.lens) {
+        const int b = (uint32_t)row / (uint32_t)a.n;
+        if (row - b * a.n >= __ldg(a.lens + b)) return;
+    }
+    const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.V;
+    const int V = (int)a.V, off = (int)(((uint64_t)row * (uint64_t)a.V) % EPV);
+    const int64_t left = ((int64_t)a.B * a.n - row) * a.V;
+    const int vecs = (V + off + EPV - 1) / EPV;
+    const int tok = lane == 0 ? __ldg(a.tokens + row) : 0;
+    uint4 r[U];
+    load_edge<T>(r, x, V, left, off, lane, 32, vecs);
+    const float token = lane == 0 ? token_logit<T>(a, x, tok) : 0.f;
+    Stats st;
+    st.m = warp_max(max_of<T>(r));
+    uint64_t l2 = f2(0.f, 0.f), a2 = l2;
+#pragma unroll
+    for (int u = 0; u < U; ++u) add_weights<T>(r[u], st.m == -INFINITY ? 0.f : st.m, a.c, l2, a2);
+    float p, q;
+    f2_split(l2, p, q);
+    st.l = warp_sum(p + q);
+    f2_split(a2, p, q);
+    st.a = warp_sum(p + q);
+    int found = 0;
+    if constexpr (TOP) {
+        float* list = s_list[warp];
+        int* id = s_id[warp];
+        float* most = s_max[warp];
+        float half[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float e[EPV];
+            widen<T>(r[u], e);
+#pragma unroll
+            for (int j = 0; j < EPV; ++j) half[j * 2 / EPV] = fmaxf(half[j * 2 / EPV], e[j]);
+        }
+        most[lane] = half[0];
+        most[32 + lane] = half[1];
+        if (lane == 0) s_best[warp][32] = -INFINITY;
+        __syncwarp();
+        int rank[2] = {0, 0};
+#pragma unroll 4
+        for (int o = 0; o < 64; ++o) {
+            const float w = most[o];
+            rank[0] += better(w, o, half[0], lane);
+            rank[1] += better(w, o, half[1], 32 + lane);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (rank[h] == K - 1) s_best[warp][32] = half[h];
+        __syncwarp();
+        const float bound = fmaxf(s_best[warp][32], -FLT_MAX);  // (-inf is no alternative)
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float e[EPV];
+            widen<T>(r[u], e);
+#pragma unroll
+            for (int j = 0; j < EPV; ++j) mine += e[j] >= bound;
+        }
+        int at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += w;
+        }
+        int n = __shfl_sync(0xffffffffu, at, 31);
+        at -= mine;
+        if (n <= 128) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float e[EPV];
+                widen<T>(r[u], e);
+#pragma unroll
+                for (int j = 0; j < EPV; ++j)
+                    if (e[j] >= bound) {
+                        list[at] = e[j];
+                        id[at++] = (u * 32 + lane) * EPV - off + j;
+                    }
+            }
+        } else {
+            // many equal values: of those at the bound the K of lowest index will do.  The
+            // vectors in turn, so that running counts are in the order of the indexes; what
+            // lies above the bound is (K - 1) * 16 elements at most.
+            int equal = 0;
+            n = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float e[EPV];
+                widen<T>(r[u], e);
+                int counts = 0;
+#pragma unroll
+                for (int j = 0; j < EPV; ++j) counts += e[j] > bound ? 1 : e[j] == bound ? 1 << 16 : 0;
+                int upto = counts;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int w = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += w;
+                }
+                int above = n + ((upto - counts) & 0xffff), level = equal + ((upto - counts) >> 16);
+#pragma unroll
+                for (int j = 0; j < EPV; ++j) {
+                    const int i = (u * 32 + lane) * EPV - off + j;
+                    if (e[j] > bound) {
+                        list[above] = e[j];
+                        id[above++] = i;
+                    } else if (e[j] == bound) {
+                        if (level < K) s_best_id[warp][level] = i;
+                        ++level;
+                    }
+                }
+                const int total = __shfl_sync(0xffffffffu, upto, 31);
+                n += total & 0xffff;
+                equal += total >> 16;
+            }
+            __syncwarp();
+            equal = min(equal, K);
+            if (lane < equal) {
+                list[n + lane] = bound;
+                id[n + lane] = s_best_id[warp][lane];
+            }
+            n += equal;
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int e = lane; e < n; e += 32) {
+            const float v = list[e];
+            const int i = id[e];
+            int place = 0;
+#pragma unroll 4
+            for (int o = 0; o < n; ++o) place += better(list[o], id[o], v, i);
+            if (place < K) {
+                s_best[warp][place] = v;
+                s_best_id[warp][place] = i;
+            }
+        }
+        __syncwarp();
+        found = min(n, K);
+    }
+    write_row(a, s_best[warp], s_best_id[warp], st, row, token, found);
+}
+
+// The K-th largest of the maxima of 64 groups of threads (bm: a thread's), which K
 // elements reach; -inf if there are fewer.
-__device__ __forceinline__ float bound_of_groups(Shared& s, float bm, int K) {
+template <int TH> __device__ __forceinline__ float bound_of_groups(Shared<TH>& s, float bm, int K) {
     const int tid = threadIdx.x;
-    float g = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((tid & 3) == 0) s.tv[tid >> 2] = g;
+    constexpr int EACH = TH / 64;  // threads of a group
+    float g = bm;
+#pragma unroll
+    for (int o = 1; o < EACH; o <<= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (tid % EACH == 0) s.tv[tid / EACH] = g;
     __syncthreads();
     if (tid < 64) {
         const float mine = s.tv[tid];
@@ -285,10 +494,10 @@ __device__ __forceinline__ float bound_of_groups(Shared& s, float bm, int K) {
     return s.bound_v;
 }
 
-template <typename T, bool TOP, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobArgs a) {
+template <typename T, bool TOP, int CTAS, int TH>
+__global__ void __launch_bounds__(TH, CTAS) logprob_kernel(const LogprobArgs a) {
     constexpr int EPV = per_vec<T>();
-    __shared__ Shared s;
+    __shared__ Shared<TH> s;
     const int tid = threadIdx.x, S = a.parts, K = a.K;
     const int row = blockIdx.x / (uint32_t)S, part = blockIdx.x - row * S;
     if (tid == 0) {
@@ -305,7 +514,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
     const T* x = static_cast<const T*>(a.logits) + (int64_t)row * a.V;
     // vectors of 16 bytes on memory's grid (indexes inside a row are 32-bit)
     const int V = (int)a.V, off = (int)(((uint64_t)row * (uint64_t)a.V) % EPV);
-    constexpr int kRound = kVecs * kThreads;
+    const int64_t left = ((int64_t)a.B * a.n - row) * a.V;
+    constexpr int kRound = kVecs * TH;
     const int vecs = (int)(((int64_t)V + off + EPV - 1) / EPV);
     const int per = S == 1 ? vecs : a.part_rounds * kRound;
     const int v0 = part * per, v1 = part == S - 1 ? vecs : v0 + per;
@@ -319,17 +529,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
     uint4 cur[kVecs], nxt[kVecs];
     // (of a round that lies whole inside the row no vector is looked at singly)
     auto fetch = [&](uint4 (&r)[kVecs], int v) {
-        if (v + kVecs * kThreads <= v1 && (v > 0 || off == 0) && (int64_t)(v + kVecs * kThreads) * EPV - off <= V) {
+        if (v + kVecs * TH <= v1 && (v > 0 || off == 0) && (int64_t)(v + kVecs * TH) * EPV - off <= V) {
             const uint4* p = reinterpret_cast<const uint4*>(x - off) + v + tid;
 #pragma unroll
             for (int u = 0; u < kVecs; ++u)
                 asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(r[u].x), "=r"(r[u].y), "=r"(r[u].z), "=r"(r[u].w)
-                             : "l"(p + u * kThreads));
+                             : "l"(p + u * TH));
         } else {
-#pragma unroll
-            for (int u = 0; u < kVecs; ++u)
-                r[u] = load_edge<T>(x, V, off, v + u * kThreads + tid, v1);
+            load_edge<T>(r, x, V, left, off, v + tid, TH, v1);
         }
     };
     // the given token and, once it is known, its logit (thread 0)
@@ -337,8 +545,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
     float token = -INFINITY;
     fetch(cur, v0);
 #pragma unroll 1
-    for (int v = v0; v < v1; v += kVecs * kThreads) {
-        if (v + kVecs * kThreads < v1) fetch(nxt, v + kVecs * kThreads);
+    for (int v = v0; v < v1; v += kVecs * TH) {
+        if (v + kVecs * TH < v1) fetch(nxt, v + kVecs * TH);
         const float bm = max_of<T>(cur);
         if (bm > m) {
             float p, q;
@@ -353,29 +561,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
             l2 = f2(old.l, 0.f);
             a2 = f2(old.a, 0.f);
         }
-        {
-            const float mm = m == -INFINITY ? 0.f : m;
-            const uint64_t neg = f2(-mm, -mm), cc = f2(c, c);
 #pragma unroll
-            for (int u = 0; u < kVecs; ++u) {
-                float e[EPV];
-                widen<T>(cur[u], e);
-#pragma unroll
-                for (int j = 0; j < EPV; j += 2) {
-                    float y0, y1;
-                    f2_split(f2_mul(f2_add(f2(e[j], e[j + 1]), neg), cc), y0, y1);
-                    y0 = max_nan(y0, kFarBelow);
-                    y1 = max_nan(y1, kFarBelow);
-                    const uint64_t w = f2(fast_exp2(y0), fast_exp2(y1));
-                    l2 = f2_add(l2, w);
-                    a2 = f2_fma(w, f2(y0, y1), a2);
-                }
-            }
-        }
-        if (v == v0 && tid == 0) {
-            if (tok >= 0 && tok < V) token = Elem<T>::to_f32(x[tok]);
-            else if (part == 0) raise_device_error(a.dev_err, SPEC_DEVERR_TOKEN);
-        }
+        for (int u = 0; u < kVecs; ++u) add_weights<T>(cur[u], m == -INFINITY ? 0.f : m, c, l2, a2);
+        if (v == v0 && tid == 0) token = token_logit<T>(a, x, tok);
         if (TOP) {
             const int at = (v + tid) * EPV - off;
             if (v == v0) {
@@ -390,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
             if (end || v == v0 || v + kRound - checked >= min(kCheck * kRound, checked - v0)) {
                 __syncthreads();
                 int count = s.count;
-                if (count > kCap) {
+                if (count > s.kCap) {
                     // entries from before (at most K + kSlack) stand in front
                     const int before =
                         v == v0 ? 0 : __syncthreads_count(tid < K + kSlack && s.i[tid] < checked * EPV - off);
@@ -402,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
                         fetch(cur, w);
                         const int first = (w + tid) * EPV - off;
                         const float top = max_of<T>(cur);
-                        const int bi = index_of<T>(cur[0], cur[1], cur[2], cur[3], first, top);
+                        const int bi = index_of<T, TH>(cur[0], cur[1], cur[2], cur[3], first, top);
                         s.tv[tid] = top;
                         s.ti[tid] = bi;
                         if (tid == 0) {
@@ -412,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
                         __syncthreads();
                         int rank = 0;
 #pragma unroll 1
-                        for (int o = 0; o < kThreads; ++o) rank += better(s.tv[o], s.ti[o], top, bi);
+                        for (int o = 0; o < TH; ++o) rank += better(s.tv[o], s.ti[o], top, bi);
                         if (rank == K - 1 && top > -INFINITY) {
                             s.bound_v = top;
                             s.bound_i = bi;
@@ -461,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
         return warp_total(sum, c);
     };
     if (tid < 32) {
-        const float4 r = tid < kThreads / 32 ? s.stats[tid] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        const float4 r = tid < TH / 32 ? s.stats[tid] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         st.m = r.x;
         st.l = r.y;
         st.a = r.z;
@@ -469,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
     }
     int found = 0;
     if (TOP) found = cut(s, s.count, K);
-    if (S > 1) {
+    if (TH == 256 && S > 1) {
         // ---- parts: leave this one's record; the last CTA of the row merges them
         const int64_t rec = (int64_t)row * S + part;
         if (TOP && tid < K) {
@@ -488,13 +676,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
         __threadfence();
         if (tid == 0) a.tickets[row] = 0;
         // the parts' alternatives, up to four a thread, through a bound of their own
-        constexpr int kMine = kMaxParts * 32 / kThreads;
+        constexpr int kMine = kMaxParts * 32 / TH;
         float w[kMine], bm = -INFINITY;
         int id[kMine];
         if (TOP) {
 #pragma unroll
             for (int u = 0; u < kMine; ++u) {
-                const int e = u * kThreads + tid;
+                const int e = u * TH + tid;
                 w[u] = -INFINITY;
                 if (e < S * K) {
                     w[u] = __ldcg(a.part_v + (int64_t)row * S * K + e);
@@ -518,14 +706,18 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprob_kernel(const LogprobAr
             found = cut(s, s.count, K);
         }
     }
-    write_row<T>(a, s, st, row, token, found);
+    if (tid < 32) write_row(a, s.v, s.i, st, row, token, found);
 }
 
 }  // namespace
 
+static bool small_rows(const LogprobArgs& a) {
+    return a.V <= kSmall - (a.dtype == SPEC_DTYPE_F32 ? 3 : 7);
+}
+
 // Rounds that a row takes at least (one more where it begins inside a vector).
 static int64_t rounds_of(const LogprobArgs& a) {
-    const int64_t round = kThreads * kVecs * (a.dtype == SPEC_DTYPE_F32 ? 4 : 8);
+    const int64_t round = 256 * kVecs * (a.dtype == SPEC_DTYPE_F32 ? 4 : 8);
     return (a.V + round - 1) / round;
 }
 
@@ -547,21 +739,36 @@ size_t logprob_workspace_bytes(const LogprobArgs& a) {
 
 cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.n;
+    if (small_rows(a)) {
+        auto* kern = a.dtype == SPEC_DTYPE_F32 ? (a.K ? logprob_small_kernel<float, true>
+                                                      : logprob_small_kernel<float, false>)
+                     : a.K                     ? logprob_small_kernel<__nv_bfloat16, true>
+                                               : logprob_small_kernel<__nv_bfloat16, false>;
+        return launch_dependent(kern, dim3((unsigned)((rows + kSmallWarps - 1) / kSmallWarps)),
+                                dim3(kSmallWarps * 32), 0, stream, a);
+    }
+    // CTAs of 64 threads, 16 an SM, where rows are many and of a few rounds: 32768 rows of
+    // 1500, 4000 with 20 alternatives 113, 181 us against 277, 293 with 256 threads; 1200 rows of
+    // 4000 12.6, 13.7; 600 10.2, 7.9; 8192 rows of 8000 75, 85, 2048 of them 26, 23.
+    const bool mid = a.parts == 1 && (a.V <= 4096 ? rows >= 1024 : a.V <= 8192 && rows >= 4096);
     // (parts - 1) part_rounds < rounds_of(a): no part is empty
     a.part_rounds = (int)((rounds_of(a) + a.parts - 1) / a.parts);
     a.part_stats = static_cast<float*>(workspace);
     a.part_v = a.part_stats + rows * a.parts * 4;
     a.part_i = reinterpret_cast<int32_t*>(a.part_v + rows * a.parts * a.K);
-    const dim3 grid((unsigned)(rows * a.parts)), block(kThreads);
+    const dim3 grid((unsigned)(rows * a.parts)), block(mid ? 64 : 256);
     // CTAs of an SM: four (64 registers) hide more of the loads.  Rows in parts with
     // alternatives are faster with three: fewer of the given rows may be in use, and four
     // of those on one SM are what the others wait for.  2048 rows of 152064, 5 alternatives:
     // 132 us with four, 143 with three; 32 x up to 5 rows of 128256, 20 alternatives: 23.2, 20.4.
     const bool f32 = a.dtype == SPEC_DTYPE_F32, three = a.K && !f32 && a.parts > 1;
-    auto* kern = f32 ? (a.K ? logprob_kernel<float, true, 4> : logprob_kernel<float, false, 4>)
-                 : three ? logprob_kernel<__nv_bfloat16, true, 3>
-                 : a.K   ? logprob_kernel<__nv_bfloat16, true, 4>
-                         : logprob_kernel<__nv_bfloat16, false, 4>;
+    using B16 = __nv_bfloat16;
+    auto* kern = mid ? (f32 ? (a.K ? logprob_kernel<float, true, 16, 64> : logprob_kernel<float, false, 16, 64>)
+                            : (a.K ? logprob_kernel<B16, true, 16, 64> : logprob_kernel<B16, false, 16, 64>))
+                 : f32 ? (a.K ? logprob_kernel<float, true, 4, 256> : logprob_kernel<float, false, 4, 256>)
+                 : three ? logprob_kernel<B16, true, 3, 256>
+                 : a.K   ? logprob_kernel<B16, true, 4, 256>
+                         : logprob_kernel<B16, false, 4, 256>;
     return launch_dependent(kern, grid, block, 0, stream, a);
 }
 
