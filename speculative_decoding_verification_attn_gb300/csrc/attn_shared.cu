@@ -45,10 +45,10 @@
 // (7.0 TB/s); a wide one ~4500 (1000 TFLOP/s), the chain S, softmax, P V of a stream with one
 // S buffer, of which the tensor core is busy 1024; e4m3 ~3550 and ~6000, INT8 ~4100 and ~7000,
 // the scales in the softmax and the widening of narrow tiles.  And ~17 us of a call: the
-// list ~4, first loads, the last pieces, the join ~5 and 2 KB of fp32 for every row.
+// list ~4, first loads, the last pieces, the join ~4 and 2 KB of fp32 for every row.
 // Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 48 us
 // (117 each by itself; the bytes' floor 13.7); 128 in four groups, 2-8K shared, 100-1500
-// own, 64/8 heads, e4m3 260 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
+// own, 64/8 heads, e4m3 257 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
 // heads, INT8 216 (484; 62).
 // Measured and not kept: S in two buffers of 64 keys a stream, Q K^T a buffer ahead of the
 // softmax: wide blocks 13 % faster (16 trees behind 8K, bf16, 61 -> 53 us), narrow tiles 8 %
@@ -1228,7 +1228,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
 
 // ------------------------------------------------------------------ the pieces' sum
 
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 4;  // three look segments up
 
 // A segment's pieces for one kv-head: ranges first .. first + count - 1; one alone is
 // whole.  (Ranges without a tile among them have left sums of -inf.)
@@ -1253,10 +1253,11 @@ __device__ __forceinline__ void find_ranges(const int* begin, int n, int t0, int
 // x / y for 0 <= x < 2^20, given 1 / y
 __device__ __forceinline__ int quotient(int x, float inverse) { return (int)((x + 0.5f) * inverse); }
 
-// A block per (sequence, kv-head): its own keys' pieces and those of the (up to two)
-// blocks that hold its tokens are looked up once, by a warp each; then a warp per query
-// row, its pieces' sums and values in one round trip.  The launch runs once through its
-// code: short code counts more here than few instructions.
+// A block per (sequence, kv-head) and 8 rows: its own keys' pieces and those of the (up to two)
+// blocks that hold its tokens are looked up once, by a warp each; then half a
+// warp per query row, its pieces' sums and values in one round trip.  The launch runs once
+// through its code: short code counts more here than few instructions.  32768 rows: 16 us
+// cold, 24 with a warp per row in blocks of eight.
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm, int C) {
     __shared__ Pieces s_seg[3];
     grid_dep_launch_dependents();
@@ -1282,15 +1283,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
         if (lane == 0) s_seg[warp] = p;
     }
     __syncthreads();
-    const int row = blockIdx.z * kJoinWarps + warp;
+    // two rows per warp, 16 lanes with eight columns each
+    const int l = lane & 15, R = a.k * G;
+    const int row0 = (blockIdx.z * kJoinWarps + warp) * 2, row = min(row0 + (lane >> 4), R - 1);
     const Pieces own = s_seg[0];
-    if ((!shared && own.count == 1) || row >= a.k * G) return;  // written already
+    if ((!shared && own.count == 1) || row0 >= R) return;  // written already
     const int tok = quotient(row, inv_g), dt = dt0 + tok;
     const int nth = shared ? quotient(dt, 0.5f * inv_nt) : 0, off = dt - nth * 2 * NT;
     const int orow = (b * a.k + tok) * a.Hq + kvh * G + row - tok * G;
     const Pieces pre = shared ? s_seg[1 + nth - nth0] : Pieces{0, 0, 0};
     const int row1 = (off >= NT ? ROWS + (off - NT) * G : off * G) + row - tok * G;
     const int rows = a.B * a.k * a.Hq, slots = 8 * C * ROWS, n = own.count + pre.count;
+    const int most = max(n, __shfl_xor_sync(0xffffffffu, n, 16));
     // piece i: its row among the slots, or past them among the whole rows
     auto place = [&](int i) {
         const bool p = i >= own.count;
@@ -1302,49 +1306,64 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
     };
     // (the arrays of whole segments lie behind the slots': one base for both)
     float m = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 32) {  // (one round but for very long segments)
-        int mine = -1;
+    for (int i0 = 0; i0 < most; i0 += 16) {  // (one round but for very long segments)
+        int mine = 0;
         float z = -INFINITY;
-        if (i0 + lane < n) {
-            mine = place(i0 + lane);
+        if (i0 + l < n) {
+            mine = place(i0 + l);
             z = __ldg(prm.slot_lse + mine);
         }
-        const float top = fmaxf(m, warp_max(z));
+        float top = z;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = fmaxf(top, m);
         const float back = m == -INFINITY ? 0.f : fast_exp2(m - top);
         const float w_mine = z == -INFINITY ? 0.f : fast_exp2(z - top);
         m = top;
-        sum = sum * back + warp_sum(w_mine);
-        acc.x *= back, acc.y *= back, acc.z *= back, acc.w *= back;
-        const int left = min(32, n - i0);
+        float part = w_mine;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        sum = sum * back + part;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = f2_mul(acc[e], f2(back, back));
+        const int left = min(16, most - i0);
 #pragma unroll 4
         for (int i = 0; i < left; ++i) {
-            const int p = __shfl_sync(0xffffffffu, mine, i);
-            const float w = __shfl_sync(0xffffffffu, w_mine, i);
-            const float4 x =
-                __ldg(reinterpret_cast<const float4*>(prm.slot_o + (int64_t)p * D) + lane);
+            const int p = __shfl_sync(0xffffffffu, mine, i, 16);
+            const float w = __shfl_sync(0xffffffffu, w_mine, i, 16);
+            const float4* from = reinterpret_cast<const float4*>(prm.slot_o + (int64_t)p * D);
+            const float4 x = __ldg(from + l), y = __ldg(from + 16 + l);
             if (w > 0.f) {  // a place that nobody wrote holds anything
-                acc.x = fmaf(w, x.x, acc.x);
-                acc.y = fmaf(w, x.y, acc.y);
-                acc.z = fmaf(w, x.z, acc.z);
-                acc.w = fmaf(w, x.w, acc.w);
+                const uint64_t ww = f2(w, w);
+                acc[0] = f2_fma(ww, f2(x.x, x.y), acc[0]);
+                acc[1] = f2_fma(ww, f2(x.z, x.w), acc[1]);
+                acc[2] = f2_fma(ww, f2(y.x, y.y), acc[2]);
+                acc[3] = f2_fma(ww, f2(y.z, y.w), acc[3]);
             }
         }
     }
+    if (row0 + (lane >> 4) >= R) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint2 o;
-    o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-    o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)orow * D)[lane] = o;
-    if (lane == 0 && a.lse) a.lse[orow] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)orow * D);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float x0, x1, x2, x3;
+        f2_split(acc[2 * h], x0, x1);
+        f2_split(acc[2 * h + 1], x2, x3);
+        out[16 * h + l] = make_uint2(pack_bf16x2(x0 * inv, x1 * inv), pack_bf16x2(x2 * inv, x3 * inv));
+    }
+    if (l == 0 && a.lse) a.lse[orow] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ prefixes of codes
 
 // The codes of every group's prefix as bf16 values: a prefix of several blocks is read by
 // each of them.  grid (blocks, groups); a thread takes 8 codes of K and of V at a time, so
-// that a warp's loads and stores are whole lines.
+// that a warp's loads and stores are whole lines.  (A warp per page and kv-head found its
+// place less often, and was slower, 26 us against 24 for 20000 keys of 8 kv-heads: fewer
+// loads under way, and a page's id before every 16 KB.)
 template <int KV>
 __global__ void __launch_bounds__(256) widen_kernel(const Params prm) {
     grid_dep_launch_dependents();
@@ -1581,7 +1600,7 @@ cudaError_t launch_attn_shared(const AttnArgs& a, const int32_t* group_starts,
                           : a.kv_dtype == SPEC_DTYPE_E4M3 ? launch_typed<KV_E4M3>(m, prm, num_ctas, stream)
                                                           : launch_typed<KV_BF16>(m, prm, num_ctas, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)a.B, (unsigned)a.Hkv, (unsigned)((a.k * G + kJoinWarps - 1) / kJoinWarps));
+    const dim3 grid((unsigned)a.B, (unsigned)a.Hkv, (unsigned)((a.k * G + 2 * kJoinWarps - 1) / (2 * kJoinWarps)));
     return launch_dependent(join_kernel, grid, dim3(kJoinWarps * 32), 0, stream, prm, num_ctas);
 }
 
