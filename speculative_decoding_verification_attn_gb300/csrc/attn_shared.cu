@@ -1196,10 +1196,14 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                             dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                             dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         } else {
-                            uint4* dst = reinterpret_cast<uint4*>(po + c);
+                            // (whole sectors: a lane's row is 512 bytes from the next one's)
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                dst[u] = make_uint4(ov[4 * u], ov[4 * u + 1], ov[4 * u + 2], ov[4 * u + 3]);
+                            for (int u = 0; u < 16; u += 8)
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                                 po + c + u),
+                                             "r"(ov[u]), "r"(ov[u + 1]), "r"(ov[u + 2]), "r"(ov[u + 3]),
+                                             "r"(ov[u + 4]), "r"(ov[u + 5]), "r"(ov[u + 6]), "r"(ov[u + 7])
+                                             : "memory");
                         }
                         __syncwarp();
                     }
