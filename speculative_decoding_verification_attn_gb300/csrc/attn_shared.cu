@@ -46,10 +46,10 @@
 // S buffer, of which the tensor core is busy 1024; e4m3 ~3550 and ~6000, INT8 ~4100 and ~7000,
 // the scales in the softmax and the widening of narrow tiles.  And ~17 us of a call: the
 // list ~4, first loads, the last pieces, the join ~4 and 2 KB of fp32 for every row.
-// Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 48 us
+// Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 46 us
 // (117 each by itself; the bytes' floor 13.7); 128 in four groups, 2-8K shared, 100-1500
-// own, 64/8 heads, e4m3 257 (262; the products' floor 50); 16 trees of 16, 32K shared, 28/4
-// heads, INT8 216 (484; 62).
+// own, 64/8 heads, e4m3 250 (264; the products' floor 50); 16 trees of 16, 32K shared, 28/4
+// heads, INT8 211 (485; 62).
 // Measured and not kept: S in two buffers of 64 keys a stream, Q K^T a buffer ahead of the
 // softmax: wide blocks 13 % faster (16 trees behind 8K, bf16, 61 -> 53 us), narrow tiles 8 %
 // (bf16) to 25 % (codes) slower, since a tile's softmax then takes twice the meetings and
@@ -85,9 +85,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 40.0f;  // log2 units
 // What the split over the CTAs charges, in quarters of a narrow tile's time: a tile
 // of a wide block (two Q tiles), and a piece's fixed work.  A narrow piece's end lies
-// under the other stream's tiles and goes with its rows (3 or 4 for 32 of them, which are
+// under the other stream's tiles and goes with its rows (3 for 32 of them, which are
 // 16 KB of fp32 to write); a wide one holds both streams.  Measured: one charge of 12 for
-// all pieces left 144 sequences of 10-150 own keys behind 208 shared at 283 us against 138,
+// all pieces left 144 sequences of 10-150 own keys behind 208 shared at 283 us against 138 then,
 // 39 sequences of one group 69 against 51; one of 4 for narrow pieces of any rows left 16
 // sequences of 112 rows behind 32K shared keys at 239 against 149.
 constexpr int kTileCost = 4;
@@ -572,7 +572,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
     // depends on its own row of Q alone, and those are not stored)
     const int opt = kTileCost * a.split_alpha;
     const Cost cost = {KV == KV_E4M3 ? 7 : 8,
-                       opt >= 0 ? opt : (k * G + 31) / 32 * (KV == KV_I8 ? 4 : 3), opt >= 0 ? opt : 24};
+                       opt >= 0 ? opt : (k * G + 31) / 32 * 3, opt >= 0 ? opt : 20};
     const int V = build_list<NTH>(prm, s_seg, s_tpre, s_cpre, s_narrow, cost, NT);
     const List L = {s_seg, s_tpre, a.B, Hkv, NT, V};
     if (warp == 0) {
@@ -1502,21 +1502,21 @@ bool shared_supported(const AttnArgs& a, int groups) {
 // group's blocks stand for, (B - blocks) Hkv T of a table of T tiles (a wide block's
 // tile takes the time of 7/4 narrow ones); what it costs is every CTA's list and the
 // second launch (10-20 us), and fp32 pieces of every row, written and read (2 KB, a
-// tile a CTA for some 8000 rows).  The table's width stands for lengths that the host
-// does not know, equal groups for the groups: the rule is for tables that the contexts
+// tile a CTA for some 12000 rows).  The table's width stands for lengths that the host does
+// not know, equal groups for the groups: the rule is for tables that the contexts
 // fill.  The kernels that read each sequence by itself differ by type.  Measured on 75
 // calls (this kernel / each sequence by itself, us, at saved tiles a CTA):
-//   bf16  4.8 57 / 41   10.7 29 / 28   19 34 / 52   29 29 / 59   114 74 / 170
-//   e4m3  8 79 / 52   25 37 / 37   28 45 / 39   363 257 / 262   973 240 / 639
-//   i8    1.5 108 / 56   3.5 38 / 41   6.2 31 / 40   23 60 / 135   682 196 / 1752
-// The worst left: bf16 12 77 / 61 (not taken), e4m3 363 (own keys are half of it).
+//   bf16  4.8 47 / 42   10.7 30 / 28   19 33 / 52   32 29 / 59   112 68 / 169
+//   e4m3  8 66 / 52   25 35 / 37   28 43 / 39   363 249 / 266   973 229 / 651
+//   i8    1.7 71 / 55   3.5 37 / 41   9.1 48 / 71   22 54 / 132   682 163 / 1768
+// The worst left: bf16 12 62 / 61 and 7.6 24.5 / 28.9, e4m3 25 35 / 37 (not taken).
 bool shared_pays(const AttnArgs& a, int groups, int sms) {
     const int64_t T = ((int64_t)a.max_pages * a.P + TN - 1) / TN, NT = ROWS / (a.Hq / a.Hkv);
     const int64_t tok = ((int64_t)a.B * a.k + groups - 1) / groups, left = tok % (2 * NT);  // of a group
     const int64_t blocks = tok / (2 * NT) * 7 + (left > NT ? 7 : left > 0 ? 4 : 0);
     const int64_t saved = (4 * a.B - groups * blocks) * a.Hkv * T;  // quarters of a tile
-    const int fixed = a.kv_dtype == SPEC_DTYPE_BF16 ? 14 : a.kv_dtype == SPEC_DTYPE_E4M3 ? 48 : 3;
-    return T >= 2 && saved >= 4 * (fixed + (int64_t)a.B * a.k * a.Hq / 8000) * sms;
+    const int fixed = a.kv_dtype == SPEC_DTYPE_BF16 ? 13 : a.kv_dtype == SPEC_DTYPE_E4M3 ? 48 : 3;
+    return T >= 2 && saved >= 4 * (fixed + (int64_t)a.B * a.k * a.Hq / 12000) * sms;
 }
 
 size_t shared_workspace_bytes(const AttnArgs& a, int groups, int num_ctas) {
