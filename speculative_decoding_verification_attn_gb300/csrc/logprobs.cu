@@ -14,7 +14,7 @@
 // while the memory delivers its bf16 elements.
 //
 // A row goes to S CTAs (one where there are rows enough), each over a
-// contiguous part in rounds of 256 threads x 64 bytes, the next round's loads
+// contiguous part in rounds of its threads x 64 bytes, the next round's loads
 // in flight.  With S > 1 the CTA that takes the row's last ticket merges the
 // parts; no CTA waits on another.
 //
@@ -31,9 +31,9 @@
 // function calls they made the compiler wait for the next round's loads at every call.
 //
 // Rows that a warp can hold (1024 elements) go to a kernel of their own, a warp each; many
-// rows of up to 8192 to CTAs of 64 threads.
+// rows to CTAs of 128 or, of up to 8192 elements, 64 threads.
 //
-// Measured, bf16: 2048 rows of 152064 with 5 alternatives 124 us (5.0 TB/s; the bytes' floor
+// Measured, bf16: 2048 rows of 152064 with 5 alternatives 121 us (5.1 TB/s; the bytes' floor
 // 92), without any 103; 32 sequences of up to 5 rows of 128256 with 20 alternatives 19.5,
 // without 11; 5 fp32 rows of 1000 4.0.  What is left of the alternatives is the appends (12
 // and 4 us of those), the meetings and, in parts, the merge.  Alternatives: meeting in
@@ -747,27 +747,35 @@ cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream)
         return launch_dependent(kern, dim3((unsigned)((rows + kSmallWarps - 1) / kSmallWarps)),
                                 dim3(kSmallWarps * 32), 0, stream, a);
     }
-    // CTAs of 64 threads, 16 an SM, where rows are many and of a few rounds: 32768 rows of
-    // 1500, 4000 with 20 alternatives 113, 181 us against 277, 293 with 256 threads; 1200 rows of
-    // 4000 12.6, 13.7; 600 10.2, 7.9; 8192 rows of 8000 75, 85, 2048 of them 26, 23.
-    const bool mid = a.parts == 1 && (a.V <= 4096 ? rows >= 1024 : a.V <= 8192 && rows >= 4096);
+    // Smaller CTAs, more of an SM, where rows are many: a row's start and end hide behind
+    // more others, and fewer warps meet.  64 threads / 256: 32768 rows of 1500, 4000 with 20
+    // alternatives 113, 181 us / 277, 293; 8192 of 8000 75 / 85, 2048 26 / 23.  128 / 256: 8192
+    // rows of 32000 with 0, 5, 20 80, 130, 175 / 91, 153, 198; 2048 rows of 152064 106, 121, 144 /
+    // 102, 124, 149; 1200 58, 74, 88 / 58, 75, 90; 700 55, 71, 84 / 47, 55, 66.
+    const int threads = a.parts > 1 || rows < 1216                    ? 256
+                        : a.V <= 4096 || (a.V <= 8192 && rows >= 4096) ? 64
+                                                                       : 128;
     // (parts - 1) part_rounds < rounds_of(a): no part is empty
     a.part_rounds = (int)((rounds_of(a) + a.parts - 1) / a.parts);
     a.part_stats = static_cast<float*>(workspace);
     a.part_v = a.part_stats + rows * a.parts * 4;
     a.part_i = reinterpret_cast<int32_t*>(a.part_v + rows * a.parts * a.K);
-    const dim3 grid((unsigned)(rows * a.parts)), block(mid ? 64 : 256);
-    // CTAs of an SM: four (64 registers) hide more of the loads.  Rows in parts with
-    // alternatives are faster with three: fewer of the given rows may be in use, and four
-    // of those on one SM are what the others wait for.  2048 rows of 152064, 5 alternatives:
-    // 132 us with four, 143 with three; 32 x up to 5 rows of 128256, 20 alternatives: 23.2, 20.4.
+    const dim3 grid((unsigned)(rows * a.parts)), block(threads);
+    // CTAs of an SM: 1024 threads of 64 registers hide more of the loads.  Rows in parts
+    // with alternatives are faster with three CTAs of 256: fewer of the given rows may be in
+    // use, and four of those on one SM are what the others wait for.  2048 rows of 152064, 5
+    // alternatives, 256 threads: 132 us with four, 143 with three; 32 x up to 5 rows of 128256,
+    // 20 alternatives: 23.2, 20.4.
     const bool f32 = a.dtype == SPEC_DTYPE_F32, three = a.K && !f32 && a.parts > 1;
     using B16 = __nv_bfloat16;
-    auto* kern = mid ? (f32 ? (a.K ? logprob_kernel<float, true, 16, 64> : logprob_kernel<float, false, 16, 64>)
-                            : (a.K ? logprob_kernel<B16, true, 16, 64> : logprob_kernel<B16, false, 16, 64>))
-                 : f32 ? (a.K ? logprob_kernel<float, true, 4, 256> : logprob_kernel<float, false, 4, 256>)
-                 : three ? logprob_kernel<B16, true, 3, 256>
-                 : a.K   ? logprob_kernel<B16, true, 4, 256>
+    auto* kern =
+        threads == 64    ? (f32 ? (a.K ? logprob_kernel<float, true, 16, 64> : logprob_kernel<float, false, 16, 64>)
+                                : (a.K ? logprob_kernel<B16, true, 16, 64> : logprob_kernel<B16, false, 16, 64>))
+        : threads == 128 ? (f32 ? (a.K ? logprob_kernel<float, true, 8, 128> : logprob_kernel<float, false, 8, 128>)
+                                : (a.K ? logprob_kernel<B16, true, 8, 128> : logprob_kernel<B16, false, 8, 128>))
+        : f32            ? (a.K ? logprob_kernel<float, true, 4, 256> : logprob_kernel<float, false, 4, 256>)
+        : three          ? logprob_kernel<B16, true, 3, 256>
+        : a.K            ? logprob_kernel<B16, true, 4, 256>
                          : logprob_kernel<B16, false, 4, 256>;
     return launch_dependent(kern, grid, block, 0, stream, a);
 }

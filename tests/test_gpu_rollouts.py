@@ -308,7 +308,7 @@ def logits(seed, B, n, V, dtype, how="normal"):
     (3, 5, 1000, 20, 0.7), (1, 1, 8191, 32, 1.0), (1, 2, 8193, 3, 1.3), (2, 3, 32000, 0, 1.0),
     (1, 1, 128257, 32, 0.9), (2, 2, 152064, 1, 1.0), (40, 5, 20001, 20, 1.0), (700, 1, 5000, 5, 1.0),
     (7, 5, 1017, 32, 1.0), (5, 3, 1021, 20, 1.0), (3, 3, 1022, 5, 1.0), (9, 4, 250, 32, 1.0),
-    (11, 3, 466, 0, 0.5), (60, 35, 4096, 7, 1.0), (65, 65, 4099, 20, 1.0)])
+    (11, 3, 466, 0, 0.5), (60, 35, 4096, 7, 1.0), (65, 65, 4099, 20, 1.0), (5, 250, 8193, 32, 1.0)])
 def test_logprobs(binding, dtype, B, n, V, K, T):
     x = logits(V + K, B, n, V, dtype)
     tokens = torch.randint(0, V, (B, n), generator=torch.Generator().manual_seed(V)).int().cuda()
@@ -318,7 +318,7 @@ def test_logprobs(binding, dtype, B, n, V, K, T):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("how", ["coarse", "constant", "rising", "falling", "peaked", "masked", "far"])
 @pytest.mark.parametrize("B,V,K", [(1, 40000, 32), (700, 33001, 20), (71, 1013, 32), (71, 130, 20),
-                                   (1050, 3001, 32), (4130, 6001, 5)])
+                                   (1050, 3001, 32), (4130, 6001, 5), (1230, 3001, 20), (1250, 9001, 32)])
 def test_logprobs_shapes_of_rows(binding, dtype, how, B, V, K):
     """Values that fill the list of candidates, tie, or leave few of them: rows
     split over CTAs and whole rows."""
