@@ -617,6 +617,11 @@ __global__ void __launch_bounds__(TH, CTAS) logprob_kernel(const LogprobArgs a) 
                     cut(s, count, K);
                     tau = s.v[K - 1];
                     __syncthreads();  // before the next round appends
+                } else if (!end) {
+                    // every thread has read the count before the next round appends: else a
+                    // slower warp could read another one and take another branch, and its
+                    // barriers, than the rest
+                    __syncthreads();
                 }
                 checked = v + kRound;
             }

@@ -1,0 +1,48 @@
+"""GPU parity at the edges of the operators of several continuations, against
+plain implementations in 64 bits."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import rollouts
+from test_gpu_rollouts import binding, check_logprobs, run_logprobs  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ log probabilities
+
+def staircase(seed, B, V, dtype, step, per):
+    """Rows of noise far down in which every `step` elements hold `per` that beat all
+    before them: each round of loads adds a few candidates, so that the list crosses the
+    length that cuts it between any two looks at it."""
+    gen = torch.Generator().manual_seed(seed)
+    x = torch.randn(B, 1, V, generator=gen) - 200.0
+    at = 0
+    for r in range(-(-V // step)):
+        for u in range(per[r % len(per)]):
+            where = r * step + torch.randint(0, step, (B,), generator=gen)
+            ok = where < V
+            x[torch.arange(B)[ok], 0, where[ok]] = at * 0.5 - 100.0
+            at += 1
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("per", [[1], [3, 0, 5], [0, 2, 0, 13, 1]])
+@pytest.mark.parametrize("B,V,K", [(1300, 4001, 1), (1300, 4090, 5), (1300, 30001, 5), (1300, 20003, 20),
+                                   (700, 40001, 2), (700, 60007, 20), (3, 152064, 5), (1, 300007, 32)])
+def test_logprobs_list_across_looks(binding, dtype, per, B, V, K):
+    """CTAs of 64, 128 and 256 threads, rows whole and in parts: the list grows in every
+    round, is looked at every few, and is cut at some of the looks."""
+    threads = 64 if B >= 1216 and V <= 4096 else 128 if B >= 1216 else 256
+    step = threads * 64 // (4 if dtype == torch.float32 else 2)
+    x = staircase(V + K, B, V, dtype, step, per)
+    tokens = torch.randint(0, V, (B, 1), generator=torch.Generator().manual_seed(K)).int().cuda()
+    g = run_logprobs(binding, x, tokens, K, 1.0)
+    some = torch.arange(0, B, 60)
+    check_logprobs({k: v[some] for k, v in g.items()}, x[some.cuda()], tokens[some.cuda()], K, 1.0)
+    for _ in range(3):  # the other rows too: a call repeats itself
+        again = run_logprobs(binding, x, tokens, K, 1.0)
+        assert all(torch.equal(again[n], g[n]) for n in g)
