@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include "common.cuh"
+#include "places.h"
 
 namespace specv {
 namespace {
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
     // (the last threads, while the first 64 find the moves)
     for (int g = kEThreads - 1 - tid; g < pages; g += kEThreads) {
         int page = -1;
-        if (g0 + g < a.max_pages) page = a.block_table[(int64_t)b * a.max_pages + g0 + g];
+        if (in_table(g0, g, a.max_pages)) page = a.block_table[(int64_t)b * a.max_pages + g0 + g];
         if (page >= a.num_pages) page = -1;
         s_page[g] = page;
         s_old[g] = s_new[g] = page >= 0 ? scales[(int64_t)page * a.Hkv + h] : 0.f;

@@ -1,0 +1,20 @@
+// Index arithmetic of paged rows at the ends of its types (host and device, no CUDA).
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define SPECV_HD __host__ __device__ __forceinline__
+#else
+#define SPECV_HD inline
+#endif
+
+namespace specv {
+
+// Whether a block table row of `width` entries has entry first + g (first, g >= 0; with pages
+// of one token their sum may pass 31 bits).
+SPECV_HD bool in_table(int32_t first, int32_t g, int32_t width) {
+    return (uint32_t)first + (uint32_t)g < (uint32_t)width;
+}
+
+}  // namespace specv

@@ -46,3 +46,23 @@ def test_logprobs_list_across_looks(binding, dtype, per, B, V, K):
     for _ in range(3):  # the other rows too: a call repeats itself
         again = run_logprobs(binding, x, tokens, K, 1.0)
         assert all(torch.equal(again[n], g[n]) for n in g)
+
+
+# ------------------------------------------------------------------ pages
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 60, 2 ** 31 - 65])
+def test_compact_context_at_the_end_of_its_type(binding, kind, ctx):
+    """Pages of one token and a context far past the table: flagged, nothing moves, and
+    the other sequence's rows do."""
+    s = rollouts.pool_state(13, kind, [9, 70], 2, 64, 1, hold_more=64)
+    s["ctx"][0] = ctx
+    path = torch.full((2, 64), -1, dtype=torch.int32)
+    path[:, :8] = torch.arange(1, 16, 2)
+    n = torch.tensor([8, 8], dtype=torch.int32)
+    g = rollouts.to_gpu(s)
+    assert rollouts.compact(s, path, n) == rollouts.CTX
+    binding.spec_kv_compact(g["kc"], g["vc"], g["table"], g["ctx"], path.cuda(), n.cuda(), g["ks"],
+                            g["vs"])
+    rollouts.same_state(g, s)
+    assert binding.spec_device_error() == rollouts.CTX

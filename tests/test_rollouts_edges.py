@@ -1,0 +1,45 @@
+"""Index arithmetic of the paged calls of several continuations at the ends of its types,
+compiled for the host, and their refusals.  Runs without a GPU."""
+from __future__ import annotations
+
+import subprocess
+
+import pytest
+
+PLACES = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include "places.h"
+int main(int argc, char** argv) {
+    auto n = [&](int i) { return (int32_t)strtoll(argv[i], 0, 10); };
+    if (!strcmp(argv[1], "in_table")) printf("%d", (int)specv::in_table(n(2), n(3), n(4)));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def places(tmp_path_factory):
+    from speculative_decoding_verification_attn_gb300 import build
+    d = tmp_path_factory.mktemp("places")
+    (d / "main.cpp").write_text(PLACES)
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-fsanitize=signed-integer-overflow",
+                    "-fno-sanitize-recover", "-I" + build.CSRC, "-o", str(d / "main"),
+                    str(d / "main.cpp")], check=True)
+
+    def run(*args):
+        out = subprocess.run([str(d / "main"), *map(str, args)], check=True, capture_output=True)
+        return int(out.stdout)
+    return run
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("first,g,width", [
+    (0, 0, 1), (0, 1, 1), (3, 4, 8), (3, 4, 7), (BIG, 0, BIG), (BIG - 5, 63, 4), (BIG, 64, BIG),
+    (BIG - 1, 0, BIG), (BIG - 63, 62, BIG)])
+def test_entries_of_a_table(places, first, g, width):
+    """Contexts at the end of 31 bits over pages of one token: no entry is taken for one
+    of the table that is not."""
+    assert places("in_table", first, g, width) == (first + g < width)
