@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseArgs a) 
     }
     int32_t* row = a.block_table + (int64_t)r * a.max_pages;
     if (tid == 0) a.ctx_lens[r] = min(a.ctx_lens[r], keep);
-    const int first = (int)(((int64_t)keep + a.P - 1) / a.P);
+    // (no more than the table has: what follows adds to it)
+    const int first = entries_kept(keep, a.P, a.max_pages);
     int bad = 0;
     for (int i0 = first + tid; i0 < a.max_pages; i0 += kThreads * kBatch) {
         int page[kBatch], old[kBatch];

@@ -17,4 +17,10 @@ SPECV_HD bool in_table(int32_t first, int32_t g, int32_t width) {
     return (uint32_t)first + (uint32_t)g < (uint32_t)width;
 }
 
+// First entry, of a table row of `width`, behind the pages of `keep` >= 0 tokens.
+SPECV_HD int32_t entries_kept(int32_t keep, int32_t page_size, int32_t width) {
+    const int64_t n = ((int64_t)keep + page_size - 1) / page_size;
+    return n < width ? (int32_t)n : width;
+}
+
 }  // namespace specv

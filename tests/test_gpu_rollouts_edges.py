@@ -66,3 +66,17 @@ def test_compact_context_at_the_end_of_its_type(binding, kind, ctx):
                             g["vs"])
     rollouts.same_state(g, s)
     assert binding.spec_device_error() == rollouts.CTX
+
+
+@pytest.mark.parametrize("P", [1, 2, 16])
+@pytest.mark.parametrize("keep", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 300, 70, 1])
+def test_release_that_keeps_all(binding, P, keep):
+    """As many tokens kept as a number holds: the row stays as it is."""
+    s = rollouts.pool_state(17, "bf16", [60, 33, 0], 1, 32, P, MP=300, hold_more=9)
+    s["ctx"][1] = 60  # behind its pages
+    g = rollouts.to_gpu(s)
+    for rows, keeps in (([0, 1], [keep, keep]), ([1, 2, 1], [2 ** 31 - 1, keep, keep])):
+        assert rollouts.release(s, rows, keeps) == 0
+        binding.spec_kv_release(g["table"], g["ctx"], g["refs"], torch.tensor(rows).int().cuda(), P,
+                                torch.tensor(keeps).int().cuda())
+        rollouts.same_state(g, s)

@@ -14,6 +14,7 @@ PLACES = r"""
 int main(int argc, char** argv) {
     auto n = [&](int i) { return (int32_t)strtoll(argv[i], 0, 10); };
     if (!strcmp(argv[1], "in_table")) printf("%d", (int)specv::in_table(n(2), n(3), n(4)));
+    if (!strcmp(argv[1], "entries_kept")) printf("%d", specv::entries_kept(n(2), n(3), n(4)));
 }
 """
 
@@ -43,3 +44,12 @@ def test_entries_of_a_table(places, first, g, width):
     """Contexts at the end of 31 bits over pages of one token: no entry is taken for one
     of the table that is not."""
     assert places("in_table", first, g, width) == (first + g < width)
+
+
+@pytest.mark.parametrize("keep,P,width", [
+    (0, 16, 4), (1, 16, 4), (16, 16, 4), (17, 16, 4), (64, 16, 4), (65, 16, 4), (BIG, 1, 4),
+    (BIG, 16, 4), (BIG - 254, 1, 100), (BIG, 1, BIG), (BIG, BIG, 4), (5, BIG, 4)])
+def test_entries_that_a_release_keeps(places, keep, P, width):
+    """Every token kept, as the largest number: no entry behind the table is counted, so a
+    thread's place behind the first one stays within its type."""
+    assert places("entries_kept", keep, P, width) == min(-(-keep // P), width)
