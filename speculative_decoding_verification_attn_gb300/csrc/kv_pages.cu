@@ -196,7 +196,7 @@ __device__ __forceinline__ bool bit_of(const uint32_t* bits, int page) {
 
 // Copies the first `part` rows of heads [h0, h1) of page `src` to page `dst`.
 __device__ __forceinline__ void copy_rows(const ForkArgs& a, int src, int dst, int part, int h0, int h1) {
-    const int chunks = part * a.D * a.elem / 16;  // 16-byte pieces of a head's rows
+    const int chunks = row_pieces(part, a.D, a.elem);  // of a head
     const int64_t head = (int64_t)a.P * a.D * a.elem / 16;
     const int all = chunks * (h1 - h0) * 2;
     for (int e = threadIdx.x; e < all; e += kThreads) {

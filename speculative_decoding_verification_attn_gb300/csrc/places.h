@@ -23,4 +23,8 @@ SPECV_HD int32_t entries_kept(int32_t keep, int32_t page_size, int32_t width) {
     return n < width ? (int32_t)n : width;
 }
 
+// 16-byte pieces of `rows` cached rows of `dim` elements (a multiple of 32) of `elem` bytes: whole
+// ones in a row.  (A page may have 2^32 bytes, 2^28 pieces.)
+SPECV_HD int32_t row_pieces(int32_t rows, int32_t dim, int32_t elem) { return rows * (dim * elem / 16); }
+
 }  // namespace specv

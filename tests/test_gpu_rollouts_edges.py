@@ -80,3 +80,24 @@ def test_release_that_keeps_all(binding, P, keep):
         binding.spec_kv_release(g["table"], g["ctx"], g["refs"], torch.tensor(rows).int().cuda(), P,
                                 torch.tensor(keeps).int().cuda())
         rollouts.same_state(g, s)
+
+
+def test_fork_copies_a_page_past_31_bits_of_bytes(binding):
+    """The page in use of an fp32 cache holds more than 2^31 bytes a head."""
+    P, D = 2 ** 22 + 64, 128
+    part = P - 3
+    assert part * D * 4 > 2 ** 31
+    cache = [torch.empty(2, 1, P, D, device="cuda") for _ in range(2)]
+    for i, c in enumerate(cache):
+        c[1].zero_()
+        c[0] = (torch.arange(P, device="cuda") * (i + 1)).float()[:, None]
+        c[0, 0, :, 1:].add_(torch.arange(1, D, device="cuda"))
+    table = torch.tensor([[0, -1], [-1, -1]]).int().cuda()
+    ctx, refs = torch.tensor([part, 0]).int().cuda(), torch.tensor([1, 0]).int().cuda()
+    binding.spec_kv_fork(*cache, table, ctx, refs, torch.tensor([0]).int().cuda(),
+                         torch.tensor([1]).int().cuda())
+    assert table.tolist() == [[0, -1], [1, -1]] and refs.tolist() == [1, 1]
+    assert ctx.tolist() == [part, part]
+    for c in cache:
+        assert torch.equal(c[1, 0, :part], c[0, 0, :part])
+        assert not bool(c[1, 0, part:].any())

@@ -14,6 +14,7 @@ PLACES = r"""
 int main(int argc, char** argv) {
     auto n = [&](int i) { return (int32_t)strtoll(argv[i], 0, 10); };
     if (!strcmp(argv[1], "in_table")) printf("%d", (int)specv::in_table(n(2), n(3), n(4)));
+    if (!strcmp(argv[1], "row_pieces")) printf("%d", specv::row_pieces(n(2), n(3), n(4)));
     if (!strcmp(argv[1], "entries_kept")) printf("%d", specv::entries_kept(n(2), n(3), n(4)));
 }
 """
@@ -53,3 +54,12 @@ def test_entries_that_a_release_keeps(places, keep, P, width):
     """Every token kept, as the largest number: no entry behind the table is counted, so a
     thread's place behind the first one stays within its type."""
     assert places("entries_kept", keep, P, width) == min(-(-keep // P), width)
+
+
+@pytest.mark.parametrize("rows,dim,elem", [
+    (0, 32, 4), (3, 32, 1), (15, 128, 2), (2 ** 22 + 15, 128, 4), (2 ** 23 - 1, 128, 4),
+    (2 ** 25 - 1, 32, 4), (2 ** 22 - 1, 256, 4), (2 ** 25 - 1, 32, 1)])
+def test_pieces_of_a_copied_page(places, rows, dim, elem):
+    """Pages of up to 2^30 elements, 2^32 bytes."""
+    assert rows * dim < 2 ** 30
+    assert places("row_pieces", rows, dim, elem) == rows * dim * elem // 16
