@@ -1491,9 +1491,11 @@ bool shared_supported(const AttnArgs& a, int groups) {
     const int64_t tokens = (int64_t)a.B * a.k, NT = ROWS / G;
     const int64_t segs = a.B + tokens / (2 * NT) + groups;
     if (segs > MAX_SEGS) return false;
-    // tile and cost counts are 32-bit (a charge of up to 256 tiles a segment)
-    const int64_t tiles = ((int64_t)a.max_pages * a.P + TN - 1) / TN + 1;
-    return tiles < (1LL << 31) && segs * (kTileCost * 256 + 2 * kTileCost * tiles) < (1LL << 31) / a.Hkv &&
+    // keys, rounded up to tiles, and tile and cost counts are 32-bit (a charge of up to 256
+    // tiles a segment)
+    const int64_t keys = (int64_t)a.max_pages * a.P, tiles = (keys + TN - 1) / TN + 1;
+    return keys < (1LL << 31) - 2 * TN &&
+           segs * (kTileCost * 256 + 2 * kTileCost * tiles) < (1LL << 31) / a.Hkv &&
            (int64_t)a.num_pages * a.Hkv * a.P < (1LL << 31) && tokens * a.Hq < (1LL << 28) &&
            a.Hkv < 65536;
 }

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import rollouts
+from test_gpu_paged8 import cuda
 from test_gpu_rollouts import binding, check_logprobs, run_logprobs  # noqa: F401
+from test_gpu_shared import call, case, check
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +103,27 @@ def test_fork_copies_a_page_past_31_bits_of_bytes(binding):
     for c in cache:
         assert torch.equal(c[1, 0, :part], c[0, 0, :part])
         assert not bool(c[1, 0, part:].any())
+
+
+# ------------------------------------------------------------------ shared prefixes
+
+@pytest.fixture()
+def grouped(binding):  # noqa: F811
+    binding.spec_set_option(binding.SPEC_OPT_ATTN_PATH, 5)  # the groups' kernel, whatever it saves
+    yield binding
+    binding.spec_set_option(binding.SPEC_OPT_ATTN_PATH, 0)
+
+
+@pytest.mark.parametrize("entries,taken", [(64, True), (2 ** 27 - 32, True), (2 ** 27, False)])
+def test_shared_tables_of_2_31_keys(grouped, entries, taken):
+    """Keys are counted in 32 bits: a table of more goes to the kernels that read each
+    sequence by itself (the groups are not read, and a bad one is not seen)."""
+    c = case(41, "bf16", [2], [256], [30, 45], 3, 8, 2, 16)
+    table = torch.full((2, entries), -1, dtype=torch.int32, device="cuda")
+    table[:, :c["table"].shape[1]] = c["table"].cuda()
+    g = {n: cuda(v) if isinstance(v, torch.Tensor) else v for n, v in c.items()}
+    g["table"] = table
+    check(c, *call(grouped, c, g))
+    g["shared"] = torch.tensor([-1]).int().cuda()
+    check(c, *call(grouped, c, g))
+    assert grouped.spec_device_error() == (rollouts.GROUP if taken else 0)
