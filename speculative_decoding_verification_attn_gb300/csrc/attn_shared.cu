@@ -1167,8 +1167,9 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     const int te = wide ? s_rng->w[1] : s_rng->n[s + 1];
                     const bool complete = cur.start >= tb && cur.start + cur.nt <= te;
                     const bool final = complete && cur.v < L.B && q.key0 == 0;
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const float lse = l > 0.f ? m_ref + log2f(l) : -INFINITY;
+                    // (a NaN among the keys stays one, in the row's sum too)
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    const float lse = l == 0.f ? -INFINITY : m_ref + log2f(l);
                     // this row's place: out, the arrays of whole segments, or a slot
                     const int64_t orow =
                         (int64_t)(q.tok0 + (wide && s ? NT : 0) + r / G) * a.Hq + cur.kvh * G + r % G;
@@ -1339,7 +1340,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
             const float w = __shfl_sync(0xffffffffu, w_mine, i, 16);
             const float4* from = reinterpret_cast<const float4*>(prm.slot_o + (int64_t)p * D);
             const float4 x = __ldg(from + l), y = __ldg(from + 16 + l);
-            if (w > 0.f) {  // a place that nobody wrote holds anything
+            if (w != 0.f) {  // a place that nobody wrote holds anything; a NaN counts
                 const uint64_t ww = f2(w, w);
                 acc[0] = f2_fma(ww, f2(x.x, x.y), acc[0]);
                 acc[1] = f2_fma(ww, f2(x.z, x.w), acc[1]);
@@ -1349,7 +1350,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
         }
     }
     if (row0 + (lane >> 4) >= R) return;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)orow * D);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1358,7 +1359,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
         f2_split(acc[2 * h + 1], x2, x3);
         out[16 * h + l] = make_uint2(pack_bf16x2(x0 * inv, x1 * inv), pack_bf16x2(x2 * inv, x3 * inv));
     }
-    if (l == 0 && a.lse) a.lse[orow] = sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+    if (l == 0 && a.lse) a.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ prefixes of codes

@@ -2,13 +2,16 @@
 plain implementations in 64 bits."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
 import rollouts
+from paged8 import E4M3
 from test_gpu_paged8 import cuda
 from test_gpu_rollouts import binding, check_logprobs, run_logprobs  # noqa: F401
-from test_gpu_shared import call, case, check
+from test_gpu_shared import call, case, check, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +130,45 @@ def test_shared_tables_of_2_31_keys(grouped, entries, taken):
     g["shared"] = torch.tensor([-1]).int().cuda()
     check(c, *call(grouped, c, g))
     assert grouped.spec_device_error() == (rollouts.GROUP if taken else 0)
+
+
+def spoil(c, what, b, key):
+    """A NaN in the K or V row of a key of sequence b, in every head."""
+    P = c["kc"].shape[2]
+    page, slot = int(c["table"][b, key // P]), key % P
+    if c["kc"].dtype == torch.int8:
+        c[what + "s"][page, :, slot] = math.nan
+    else:
+        rollouts.raw(c[what + "c"])[page, :, slot, 7] = 0x7f if c["kc"].dtype == E4M3 else math.nan
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 7, 61])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("where", ["prefix", "own"])
+@pytest.mark.parametrize("kind", ["bf16", "i8"])
+@pytest.mark.parametrize("sizes", [[3], [40]])
+def test_shared_nan_rows(grouped, kind, sizes, what, where, ctas):
+    """A NaN in a cached row that a query sees is one in its output (of K: in its log-sum
+    too), whichever of its pieces holds the row; other queries have their answers."""
+    k, Hq, Hkv = (4, 8, 2) if sizes == [3] else (8, 16, 1)
+    c = case(43, kind, sizes, [300], [20, 150], k, Hq, Hkv, 16, tail=2)
+    ref = reference(c)
+    n, B = sizes[0], sizes[0] + 2
+    hit = torch.zeros(B, dtype=torch.bool)
+    if where == "prefix":
+        spoil(c, what, 0, 70)
+        hit[:n] = True
+    else:
+        spoil(c, what, 1, int(c["ctx"][1]) - 3)
+        hit[1] = True
+    grouped.spec_set_option(grouped.SPEC_OPT_NUM_CTAS, ctas)
+    out, lse = call(grouped, c)
+    grouped.spec_set_option(grouped.SPEC_OPT_NUM_CTAS, 0)
+    some = dict(c, q=c["q"][~hit])
+    check(some, out[~hit.cuda()], lse[~hit.cuda()], ref=[r[~hit] for r in ref])
+    nan = torch.isnan(out[hit.cuda()]).reshape(-1, 128)
+    if what == "k":
+        assert bool(nan.all()) and bool(torch.isnan(lse[hit.cuda()]).all())
+    else:  # the spoiled column (an int8 row's scale: all of them)
+        assert bool((nan if kind == "i8" else nan[:, 7]).all())
+        assert not bool(torch.isnan(lse[hit.cuda()]).any())
