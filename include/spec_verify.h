@@ -310,9 +310,8 @@ SPEC_API int spec_verify_attn_window(const void *q, const void *k_cache, const v
  * pages in [16, 256], up to 128 query rows per kv-head and about 1000 sequences and
  * blocks of 256 query rows may run on a tensor-core kernel of its own, which reads
  * the groups.  It rounds as the BF16 one of spec_verify_attn does (codes are exact
- * in its MMAs, scales fp32).  K and V are finite there as everywhere: a NaN of a BF16
- * cache or of an I8 scale gives NaN, but an E4M3 code 0x7f or 0xff counts as 480 or
- * -480 times its scale.  Its workspace holds two fp32 rows for each query
+ * in its MMAs, scales fp32; a NaN that a query sees is one in its output, though K and V
+ * are finite by contract).  Its workspace holds two fp32 rows for each query
  * and head and, where prefixes of codes serve 512 rows or more of a kv-head, their
  * bf16 values (up to 1 GiB, by the tables' width).  It is taken where the sequences
  * that a group saves, times the block table's width, outweigh its fixed cost (10-20

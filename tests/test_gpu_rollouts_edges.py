@@ -7,7 +7,6 @@ import math
 import pytest
 import torch
 
-import paged8
 import rollouts
 from paged8 import E4M3
 from test_gpu_paged8 import cuda
@@ -146,7 +145,7 @@ def spoil(c, what, b, key):
 @pytest.mark.parametrize("ctas", [0, 1, 7, 61])
 @pytest.mark.parametrize("what", ["k", "v"])
 @pytest.mark.parametrize("where", ["prefix", "own"])
-@pytest.mark.parametrize("kind", ["bf16", "i8"])
+@pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
 @pytest.mark.parametrize("sizes", [[3], [40]])
 def test_shared_nan_rows(grouped, kind, sizes, what, where, ctas):
     """A NaN in a cached row that a query sees is one in its output (of K: in its log-sum
@@ -173,19 +172,3 @@ def test_shared_nan_rows(grouped, kind, sizes, what, where, ctas):
     else:  # the spoiled column (an int8 row's scale: all of them)
         assert bool((nan if kind == "i8" else nan[:, 7]).all())
         assert not bool(torch.isnan(lse[hit.cuda()]).any())
-
-
-@pytest.mark.parametrize("sizes", [[3], [40]])
-def test_shared_e4m3_codes_past_the_finite_ones(grouped, sizes):
-    """0x7f and 0xff count as +-480 times the scale, in prefixes widened tile by tile and
-    ahead and in own keys."""
-    k, Hq, Hkv = (4, 8, 2) if sizes == [3] else (8, 16, 1)
-    c = case(44, "e4m3", sizes, [300], [20, 150], k, Hq, Hkv, 16, tail=2)
-    wide = dict(c, ks=None, vs=None)
-    for w in ("k", "v"):
-        wide[w + "c"] = paged8.value64(c[w + "c"], c[w + "s"])
-        for b, key, d, sign in ((0, 70, 7, 0), (1, int(c["ctx"][1]) - 3, 90, 0x80), (sizes[0], 3, 5, 0)):
-            page, slot = int(c["table"][b, key // 16]), key % 16
-            rollouts.raw(c[w + "c"])[page, :, slot, d] = 0x7f | sign
-            wide[w + "c"][page, :, slot, d] = (-480.0 if sign else 480.0) * c[w + "s"][page].double()
-    check(c, *call(grouped, c), ref=reference(wide))
