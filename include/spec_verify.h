@@ -309,11 +309,14 @@ SPEC_API int spec_verify_attn_window(const void *q, const void *k_cache, const v
  * A BF16 query with head_dim 128 and a BF16, I8 or E4M3 cache of power-of-two
  * pages in [16, 256], up to 128 query rows per kv-head and about 1000 sequences and
  * blocks of 256 query rows may run on a tensor-core kernel of its own, which reads
- * the groups.  It rounds as the BF16 one of spec_verify_attn does (codes are exact
- * in its MMAs, scales fp32; a NaN that a query sees is one in its output, though K and V
- * are finite by contract).  Its workspace holds two fp32 rows for each query
- * and head and, where prefixes of codes serve 512 rows or more of a kv-head, their
- * bf16 values (up to 1 GiB, by the tables' width).  It is taken where the sequences
+ * the groups.  It rounds as the kernels of spec_verify_attn do over a BF16 and an I8
+ * cache (of an E4M3 one as of BF16; codes are exact in its MMAs, scales fp32): a
+ * weight to 8 significant bits, over I8 times its key's scale to fp16, of which the
+ * largest product with the largest scale among 16 keys is 2^-1 or more.  A NaN that a
+ * query sees is one in its output, though K and V are finite by contract.  Its
+ * workspace holds two fp32 rows for each query and head and, where prefixes of codes
+ * serve 512 rows or more of a kv-head, their values in 16 bits (up to 1 GiB, by the
+ * tables' width).  It is taken where the sequences
  * that a group saves, times the block table's width, outweigh its fixed cost (10-20
  * us), and with SPEC_OPT_ATTN_PATH 5 wherever it fits; every other call runs as
  * spec_verify_attn and does not read the groups.

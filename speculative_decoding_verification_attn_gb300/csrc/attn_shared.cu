@@ -28,15 +28,16 @@
 //    each with a Q of its own, read it: 64 KB of L2 traffic for 16.8 MFLOP, half of
 //    what narrow tiles would ask of L2.
 //  * TMEM (512 columns): S of the streams [0,128), [128,256), their O [256,384),
-//    [384,512); P (bf16) over the S columns it came from.
+//    [384,512); P (bf16; INT8: fp16) over the S columns it came from.
 //  * Warps: 0-7 and 8-15 softmax (two for the 32 rows of a TMEM quadrant, half of the keys
 //    each); 16 and 19 MMAs; 17 and 18 producers; with codes, 20-23 and 24-27 widen
 //    what lands in slot 0 and slot 1.
-//  * INT8 and e4m3 codes become bf16 exactly: a sequence's own keys in place (raw bytes
-//    land in the upper half of their operand slot), and so a prefix that one block
-//    reads; prefixes of several blocks by a launch before this one, once (widen_kernel).
-//    Scales enter the scores and, before its rounding to bf16, P, in fp32.  So the MMAs
-//    see the stored values and the only roundings are P's (8 bits) and the output's.
+//  * INT8 and e4m3 codes become bf16 exactly, INT8's of V fp16: a sequence's own keys in
+//    place (raw bytes land in the upper half of their operand slot), and so a prefix that one
+//    block reads; prefixes of several blocks by a launch before this one, once (widen_kernel).
+//    Scales enter the scores and, before its rounding, P, in fp32.  So the MMAs see the stored
+//    values and the only roundings are the output's and P's: to 8 bits over bf16 and e4m3
+//    caches, to fp16's 11 over INT8, each as the kernels of single sequences do.
 //  * Every mbarrier wait is bounded (1 s); a timeout sets the device error word
 //    and an abort flag, after which every role skips its remaining work, drains
 //    its copies and tensor-core operations, and returns.
@@ -82,7 +83,14 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0, TM_O = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 40.0f;  // log2 units
+enum { KV_BF16, KV_I8, KV_E4M3 };
+// A tile's maximum (log2 units) that passes the reference of a row's weights by more moves it.
+// bf16 weights have fp32's exponents.  INT8's, times V's scales, are fp16: the scores count with
+// the power of two next above V's scales (the largest of 16 keys), and a reference is set to the
+// greatest lower bound of their maximum, at most kFollow below the upper one.  So the largest
+// product of a weight and such a scale lies in [2^-1, 2^15]; those of 2^-13 of it and more have
+// all of fp16's 11 bits, the others half a step of 2^-24 of it or less.
+template <int KV> constexpr float kFollow = KV == KV_I8 ? 15.f : 40.f;
 // What the split over the CTAs charges, in quarters of a narrow tile's time: a tile
 // of a wide block (two Q tiles), and a piece's fixed work.  A narrow piece's end lies
 // under the other stream's tiles and goes with its rows (3 for 32 of them, which are
@@ -100,11 +108,12 @@ constexpr int kMinShared = TN;
 // Rows of K (and of V) that widened prefixes may take: 1 GiB together
 constexpr int64_t kMaxPrefixRows = (int64_t)1 << 21;
 
-enum { KV_BF16, KV_I8, KV_E4M3 };
 template <int KV> constexpr int threads() { return KV == KV_BF16 ? 20 * 32 : 28 * 32; }
 
 constexpr uint32_t IDESC_QK = umma_idesc_bf16(ROWS, TN, 0, 0);
-constexpr uint32_t IDESC_PV = umma_idesc_bf16(ROWS, D, 0, 1);  // B (V) MN-major
+// B (V) MN-major.  INT8: P in fp16's 11 bits (as over an INT8 cache elsewhere), V's codes too
+template <int KV>
+constexpr uint32_t IDESC_PV = KV == KV_I8 ? umma_idesc_f16(ROWS, D, 0, 1) : umma_idesc_bf16(ROWS, D, 0, 1);
 
 struct Smem {
     static constexpr int Q = 0;                         // 2 tiles
@@ -140,7 +149,7 @@ struct Params {
     const int32_t* group_starts;
     const int32_t* shared_lens;
     int groups;
-    // codes: [groups][max_pages][Hkv][P][D] bf16 values of the prefixes' codes, K and V,
+    // codes: [groups][max_pages][Hkv][P][D] values of the prefixes' codes as the MMAs take them,
     // or null (they are widened tile by tile)
     __nv_bfloat16* k_prefix;
     __nv_bfloat16* v_prefix;
@@ -401,44 +410,43 @@ __device__ __forceinline__ int build_list(const Params& prm, Seg* seg, int* tpre
     return V;
 }
 
-// Codes to bf16, exactly.
-// INT8: the low seven bits under the exponent of 128, less 128 (or 256 for a
-// negative code, whose low seven bits are its value + 128).
-__device__ __forceinline__ uint32_t i8x2_to_bf16(uint32_t t) {  // bytes 0 and 2
-    const uint32_t m = (t & 0x007f007fu) | 0x43004300u, s = (t & 0x00800080u) | 0x43004300u;
-    uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(s));
-    return r;
+// Eight codes to fp16, which holds every one exactly (and a NaN as one).
+template <int KV> __device__ __forceinline__ uint4 codes_to_f16(const uint2 r) {
+    uint4 o;
+    if constexpr (KV == KV_I8) {
+        uint4 none;
+        i8x16_to_f16(make_uint4(r.x, r.y, 0, 0), o, none);
+    } else {
+        auto two = [](uint32_t w) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
+            return h;
+        };
+        o = make_uint4(two(r.x), two(r.x >> 16), two(r.y), two(r.y >> 16));
+    }
+    return o;
 }
-// e4m3: by way of fp16 and fp32, which hold every code, and a NaN as one.  (Moving exponent and
-// fraction to bf16's places and scaling by 2^120 is five operations a pair as this is four,
-// and makes 480 of a NaN: 128 sequences, e4m3, 250 us against 245; with a look at every word
-// for NaN codes 286.)
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16(uint16_t t) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(t));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    return pack_bf16x2(f.x, f.y);
+// The same values in bf16, exactly for codes.  (e4m3 by bits, exponent and fraction moved to
+// bf16's places and scaled by 2^120, is five operations a pair as this is four, and makes 480
+// of a NaN: 128 sequences 250 us against 245, with a look at every word for NaN codes 286.)
+__device__ __forceinline__ uint4 f16_to_bf16(const uint4 r) {
+    auto two = [](uint32_t h) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        return pack_bf16x2(f.x, f.y);
+    };
+    return make_uint4(two(r.x), two(r.y), two(r.z), two(r.w));
 }
-template <int KV> __device__ __forceinline__ uint2 widen4(uint32_t w) {
-    if (KV == KV_I8)
-        return make_uint2(i8x2_to_bf16(__byte_perm(w, 0, 0x4140)),
-                          i8x2_to_bf16(__byte_perm(w, 0, 0x4342)));
-    return make_uint2(e4m3x2_to_bf16((uint16_t)w), e4m3x2_to_bf16((uint16_t)(w >> 16)));
-}
-template <int KV> __device__ __forceinline__ uint4 widen8(const uint2 r) {
-    const uint2 a = widen4<KV>(r.x), b = widen4<KV>(r.y);
-    return make_uint4(a.x, a.y, b.x, b.y);
-}
-template <int KV>
-__device__ __forceinline__ void widen16(const uint4 r, uint4& lo, uint4& hi) {
-    lo = widen8<KV>(make_uint2(r.x, r.y));
-    hi = widen8<KV>(make_uint2(r.z, r.w));
+// Eight codes as the MMAs take them: bf16, INT8's of V fp16.
+template <int KV> __device__ __forceinline__ uint4 widen8(const uint2 r, bool is_v) {
+    const uint4 h = codes_to_f16<KV>(r);
+    return KV == KV_I8 && is_v ? h : f16_to_bf16(h);
 }
 
 // The keys' scales of a tile as its softmax reads them.
 template <int KV> struct Scales {
-    const float* e4m3;    // of 16 keys: K's; 8 words on V's; 16 on log2 of V's; 24 on 1 / V's
+    // of 16 keys: e4m3: K's; 8 words on V's; 16 on log2 of V's; 24 on 1 / V's
+    // INT8: K's least; 8 on their largest; 16 on log2 of the power of two above V's
+    const float* e4m3;
     const __half* i8;     // K, and 128 on V
 };
 
@@ -478,7 +486,7 @@ __device__ __forceinline__ void exponents(uint32_t (&r)[N], float sl2, const Sca
 }
 
 // p = 2^v of N columns from c0 on, for codes times the keys' scales of V (LOGV: they are in
-// v), packed to bf16 pairs; adds the sum of p to l.
+// v), packed to bf16 (INT8: fp16) pairs; adds the sum of p to l.
 template <int KV, bool LOGV, int N>
 __device__ __forceinline__ void weights(const uint32_t (&v)[N], const Scales<KV>& sc, int c0, float& l,
                                         uint32_t (&pk)[N / 2]) {
@@ -510,7 +518,7 @@ __device__ __forceinline__ void weights(const uint32_t (&v)[N], const Scales<KV>
                 s = f2(x.x, x.y);
             }
             if (KV != KV_BF16 && !LOGV) f2_split(f2_mul(e, s), e0, e1);
-            pk[c / 2 + u] = pack_bf16x2(e0, e1);
+            pk[c / 2 + u] = KV == KV_I8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
         }
         // (the sums of 16 keys that share a scale, without it)
         if (LOGV && c % 16 == 8) l = fmaf(total(), sc.e4m3[24 + (c0 + c) / 16], l);
@@ -890,7 +898,7 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                         for (int i = 0; i < NVB; ++i)
                             if (i < nvb)
                                 umma_ts(od, sbuf + (i < 4 ? 8 * i : 64 + 8 * (i - 4)),
-                                        vd + ((uint32_t)(i * 4096) >> 4), IDESC_PV,
+                                        vd + ((uint32_t)(i * 4096) >> 4), IDESC_PV<KV>,
                                         (j > 0 || i > 0) ? 1u : 0u);
                     }
                     __syncwarp();
@@ -938,21 +946,26 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                                        abort_flag, a.dev_err);
                     uint8_t* slot = sm + (is_v ? Smem::VS : Smem::KS) + s * SLOT_BYTES;
                     if (KV == KV_I8 && !is_v && ok) {
-                        // bounds of K's scales over 16 keys, and no V scale past the end (a
-                        // weight of 0 times whatever is stored there)
+                        // bounds of K's scales over 16 keys, the power of two above V's (of
+                        // 2^-24, fp16's least, where all are zero), and no V scale past the
+                        // end (a weight of 0 times whatever is stored there)
                         __half* raw = s_half + (2 * s + (i & 1)) * 2 * TN;
                         float* to = s_scale + (2 * s + (i & 1)) * 32;
                         const int j = ct;
                         const float x = __half2float(raw[j]);
                         float lo = j < nvalid ? x : INFINITY, hi = j < nvalid ? x : 0.f;
+                        float v = j < nvalid ? fabsf(__half2float(raw[TN + j])) : 0.f;
 #pragma unroll
                         for (int o = 8; o > 0; o >>= 1) {
                             lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
                             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
                         }
                         if (j % 16 == 0) {
-                            to[j / 16] = lo;
-                            to[8 + j / 16] = hi;
+                            // (with a negative scale of K they are no bounds: the slow way)
+                            to[j / 16] = lo < 0.f ? -INFINITY : lo;
+                            to[8 + j / 16] = lo < 0.f ? INFINITY : hi;
+                            to[16 + j / 16] = (float)((__float_as_int(fmaxf(v, 0x1p-24f)) >> 23) - 126);
                         }
                         if (j >= nvalid) raw[TN + j] = __float2half(0.f);
                     }
@@ -977,8 +990,13 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             uint4 lo, hi;
-                            widen16<KV>(raw[u], lo, hi);
-                            if (pass * 32 + u * 16 + j0 >= nvalid) lo = hi = make_uint4(0, 0, 0, 0);
+                            if (pass * 32 + u * 16 + j0 >= nvalid) raw[u] = make_uint4(0, 0, 0, 0);
+                            lo = codes_to_f16<KV>(make_uint2(raw[u].x, raw[u].y));
+                            hi = codes_to_f16<KV>(make_uint2(raw[u].z, raw[u].w));
+                            if (KV != KV_I8 || !is_v) {
+                                lo = f16_to_bf16(lo);
+                                hi = f16_to_bf16(hi);
+                            }
                             uint8_t* row = to + pass * 8192 + u * 4096;
                             *reinterpret_cast<uint4*>(row + o0) = h ? hi : lo;
                             *reinterpret_cast<uint4*>(row + o1) = h ? lo : hi;
@@ -1041,12 +1059,12 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                                        s_half + stage * 2 * TN + half * 64};
                 const uint64_t vis =
                     visible64(cur.key0(L), half * 64, cur.valid(L), ctx, mrow);
-                // the row's maximum: with the loads where all keys are visible (INT8: within
-                // the bounds that the scales of 16 keys give, when those lie close enough)
-                float mx = -INFINITY;
+                // the row's maximum: with the loads where all keys are visible (INT8: bounds
+                // of it, by the scales of 16 keys, which do unless a reference has to follow
+                // and they lie too far apart)
+                float mx = -INFINITY, least = -INFINITY;
                 bool slow = vis != ~0ull || a.scale < 0.f;
                 if (!__any_sync(0xffffffffu, slow && r < rows)) {
-                    float least = -INFINITY;
 #pragma unroll 1
                     for (int h = 0; h < 2; ++h) {
                         uint32_t d[2][16];
@@ -1058,8 +1076,10 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                         for (int j = 0; j < 2; ++j) {
                             if (KV == KV_I8) {
                                 const float lo = sc.e4m3[h * 2 + j], hi = sc.e4m3[8 + h * 2 + j];
-                                mx = fmaxf(mx, x[j] * sl2 * (x[j] > 0.f ? hi : lo));
-                                least = fmaxf(least, x[j] * sl2 * (x[j] > 0.f ? lo : hi));
+                                const float v = sc.e4m3[16 + h * 2 + j], y = x[j] * sl2;
+                                // (0 times an infinite bound: a NaN, and the slow way)
+                                asm("max.NaN.f32 %0, %0, %1;" : "+f"(mx) : "f"(fmaf(y, x[j] > 0.f ? hi : lo, v)));
+                                least = fmaxf(least, fmaf(y, x[j] > 0.f ? lo : hi, v));
                             } else {
                                 mx = fmaxf(mx, x[j] * (KV == KV_E4M3 ? sc.e4m3[h * 2 + j] : sl2));
                                 // a scale of V whose logarithm would cost weights
@@ -1067,7 +1087,8 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                             }
                         }
                     }
-                    if (KV == KV_I8) slow = !(mx - fmaxf(least, m_ref) <= kRescaleThreshold);
+                    if (KV == KV_I8)
+                        slow = !(mx <= m_ref + kFollow<KV> || mx - least <= kFollow<KV>);
                 }
                 // (rows past the piece's hold anything: they decide nothing)
                 slow = __any_sync(0xffffffffu, slow && r < rows);
@@ -1087,22 +1108,32 @@ attn_shared_kernel(const __grid_constant__ CUtensorMap own_map,  // q: boxes of 
                     for (int c = 0; c < 64; c += 16) {
                         uint32_t v[16];
                         some(c, 0.f, v);
+                        float most = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < 16; e += 2)
-                            mx = fmax3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                            most = fmax3(most, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                        if (KV == KV_I8) most += sc.e4m3[16 + c / 16];
+                        mx = fmaxf(mx, most);
                     }
+                    least = mx;
                 }
                 {
                     float* mine = stat + (t & 1) * 4 * ROWS;
-                    if (r >= rows) mx = 0.f;
+                    if (r >= rows) mx = least = 0.f;
                     mine[half * ROWS] = mx;
                     named_bar_sync(meet, 64);
                     mx = fmaxf(mx, mine[(1 - half) * ROWS]);
                 }
-                // the reference follows only a maximum 2^40 above it (weights and
+                // the reference follows only a maximum far above it (weights and
                 // sums have the exponents for that), so O is almost never rescaled
                 float al = 1.f;
-                const bool move = mx > m_ref + kRescaleThreshold;  // also -inf -> finite
+                const bool move = mx > m_ref + kFollow<KV>;  // also -inf -> finite
+                if (KV == KV_I8 && __any_sync(0xffffffffu, move)) {  // both warps of the pair
+                    float* mine = stat + 2 * 4 * ROWS;
+                    mine[half * ROWS] = least;
+                    named_bar_sync(meet, 64);
+                    mx = fmaxf(least, mine[(1 - half) * ROWS]);
+                }
                 if (move) {
                     al = (m_ref == -INFINITY) ? 0.f : fast_exp2(m_ref - mx);
                     m_ref = mx;
@@ -1365,7 +1396,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Params prm,
 
 // ------------------------------------------------------------------ prefixes of codes
 
-// The codes of every group's prefix as bf16 values: a prefix of several blocks is read by
+// The codes of every group's prefix as the MMAs take them: a prefix of several blocks is read by
 // each of them.  grid (blocks, groups); a thread takes 8 codes of K and of V at a time, so
 // that a warp's loads and stores are whole lines.  (A warp per page and kv-head found its
 // place less often, and was slower, 26 us against 24 for 20000 keys of 8 kv-heads: fewer
@@ -1416,8 +1447,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const Params prm) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             if (i0 + u * step >= all) continue;
-            ko[to[u]] = widen8<KV>(k[u]);
-            vo[to[u]] = widen8<KV>(v[u]);
+            ko[to[u]] = widen8<KV>(k[u], false);
+            vo[to[u]] = widen8<KV>(v[u], true);
         }
     }
 }

@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import paged8
 import rollouts
 from paged8 import E4M3
 from test_gpu_paged8 import cuda
@@ -172,3 +173,61 @@ def test_shared_nan_rows(grouped, kind, sizes, what, where, ctas):
     else:  # the spoiled column (an int8 row's scale: all of them)
         assert bool((nan if kind == "i8" else nan[:, 7]).all())
         assert not bool(torch.isnan(lse[hit.cuda()]).any())
+
+
+def int8_bounds(c, ref):
+    """Largest error of an output over an INT8 cache: weights times V's scales in fp16 (half a
+    step: 2^-11, at least 2^-25), codes exact, scores and sums in fp32, one rounding to bf16.
+
+    The weights' common factor puts the largest product of a weight and the largest V scale of
+    its 64 keys at 2^-1 or more, so that 2^-25 is at most 2^-24 max(v_scale) of a weight's sum:
+    each key adds up to 2^-24 max(v_scale) |code| beside 2^-11 p |v|.  q is bf16 and exact; a
+    score's error z is that of attn_bounds (128 products and sums of 2^-24, and the scales')."""
+    o64, l64, _, kn = ref
+    q, k, P = c["q"], c["k"], c["kc"].shape[2]
+    Hq, Hkv = q.shape[2], c["kc"].shape[1]
+    z = (256 * 2.0 ** -24 * q.double().abs().amax(-1)) * kn * abs(c["scale"])
+    bound = torch.zeros_like(o64)
+    mag = paged8.attn64(q, c["kc"], c["vc"].abs(), c["ks"], c["vs"].abs(), c["table"], c["ctx"],
+                        c["scale"], c["mask"])[0]
+    for b in range(q.shape[0]):
+        n = int(c["ctx"][b]) + k
+        at = [(int(c["table"][b, j // P]), j % P) for j in range(n)]
+        pages, slots = torch.tensor(at).T
+        codes = c["vc"][pages, :, slots].double().abs().sum(0)          # [Hkv, D]
+        top = c["vs"][pages, :, slots].double().abs().amax(0)           # [Hkv]
+        bound[b] = (2.0 ** -24 * top[:, None] * codes).repeat_interleave(Hq // Hkv, 0)
+    half_step = torch.exp2(torch.floor(torch.log2(o64.abs().clamp(min=2.0 ** -120))) - 8)
+    return half_step * 1.01 + bound + (2.0 ** -11 * 1.01 + 2 * z[..., None] + 1e-5) * mag + 1e-9
+
+
+def check_int8(c, out, lse):
+    ref = reference(c)
+    bound = int8_bounds(c, ref)
+    err = (out.double().cpu() - ref[0]).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    check(c, out, lse, ref=ref)
+
+
+@pytest.mark.parametrize("sizes,k,Hq,Hkv", [([3], 4, 8, 2), ([40], 8, 16, 1), ([2, 30], 3, 24, 4)])
+@pytest.mark.parametrize("how", ["uniform", "spread", "peaked", "signs", "long"])
+def test_shared_int8_weights_in_11_bits(grouped, sizes, k, Hq, Hkv, how):
+    """Weights over an INT8 cache have fp16's bits, as in the kernels of single sequences."""
+    shared, own_keys = [300, 270][:len(sizes)], [20, 150]
+    if how == "long":
+        shared, own_keys = [1800, 1500][:len(sizes)], [3, 700]
+    c = case(45, "i8", sizes, shared, own_keys, k, Hq, Hkv, 16, tail=1,
+             qscale={"uniform": 0.0, "peaked": 6.0}.get(how, 1.5))
+    gen = torch.Generator().manual_seed(45)
+    if how == "uniform":  # every weight rounds alike: nothing cancels
+        c["vs"] = (0.01 + torch.rand(1, Hkv, 1, generator=gen)).half().expand_as(c["vs"]).contiguous()
+        c["vc"] = torch.randint(-127, 128, (1, Hkv, 1, 128), generator=gen).to(torch.int8).expand_as(
+            c["vc"]).contiguous()
+    if how == "spread":  # V's scales 2^-20 .. 2^4, zeros among them; K's a factor of 16 apart
+        c["vs"] = torch.exp2(torch.randint(-20, 5, c["vs"].shape, generator=gen).float()).half()
+        c["vs"][torch.rand(c["vs"].shape, generator=gen) < 0.1] = 0
+        c["ks"] = (c["ks"].float() * torch.exp2(-4 * torch.rand(c["ks"].shape, generator=gen))).half()
+    if how == "signs":
+        c["ks"] *= torch.where(torch.rand(c["ks"].shape, generator=gen) < 0.5, 1, -1).half()
+        c["vs"] *= torch.where(torch.rand(c["vs"].shape, generator=gen) < 0.5, 1, -1).half()
+    check_int8(c, *call(grouped, c))
