@@ -289,7 +289,7 @@ struct LogprobArgs {
 };
 int logprob_parts(const LogprobArgs& a, int num_sms, int max_tickets);
 size_t logprob_workspace_bytes(const LogprobArgs& a);
-cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream);
+cudaError_t launch_logprobs(LogprobArgs a, int num_sms, void* workspace, cudaStream_t stream);
 
 // ---- pages held by several rows, and the accepted path of a tree (kv_pages.cu) ----
 struct ForkArgs {

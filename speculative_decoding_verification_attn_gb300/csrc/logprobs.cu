@@ -742,7 +742,7 @@ size_t logprob_workspace_bytes(const LogprobArgs& a) {
     return a.parts > 1 ? (size_t)a.B * a.n * a.parts * (16 + 8 * (size_t)a.K) : 0;
 }
 
-cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream) {
+cudaError_t launch_logprobs(LogprobArgs a, int num_sms, void* workspace, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.n;
     if (small_rows(a)) {
         auto* kern = a.dtype == SPEC_DTYPE_F32 ? (a.K ? logprob_small_kernel<float, true>
@@ -752,12 +752,13 @@ cudaError_t launch_logprobs(LogprobArgs a, void* workspace, cudaStream_t stream)
         return launch_dependent(kern, dim3((unsigned)((rows + kSmallWarps - 1) / kSmallWarps)),
                                 dim3(kSmallWarps * 32), 0, stream, a);
     }
-    // Smaller CTAs, more of an SM, where rows are many: a row's start and end hide behind
-    // more others, and fewer warps meet.  64 threads / 256: 32768 rows of 1500, 4000 with 20
-    // alternatives 113, 181 us / 277, 293; 8192 of 8000 75 / 85, 2048 26 / 23.  128 / 256: 8192
-    // rows of 32000 with 0, 5, 20 80, 130, 175 / 91, 153, 198; 2048 rows of 152064 106, 121, 144 /
-    // 102, 124, 149; 1200 58, 74, 88 / 58, 75, 90; 700 55, 71, 84 / 47, 55, 66.
-    const int threads = a.parts > 1 || rows < 1216                    ? 256
+    // Smaller CTAs, more of an SM, where rows are many (eight an SM): a row's start and end hide
+    // behind more others, and fewer warps meet.  64 threads / 256, on 152 SMs: 32768 rows of
+    // 1500, 4000 with 20 alternatives 113, 181 us / 277, 293; 8192 of 8000 75 / 85, 2048 26 / 23.
+    // 128 / 256: 8192 rows of 32000 with 0, 5, 20 80, 130, 175 / 91, 153, 198; 2048 rows of
+    // 152064 106, 121, 144 / 102, 124, 149; 1200 58, 74, 88 / 58, 75, 90; 700 55, 71, 84 / 47,
+    // 55, 66.
+    const int threads = a.parts > 1 || rows < 8 * (int64_t)num_sms     ? 256
                         : a.V <= 4096 || (a.V <= 8192 && rows >= 4096) ? 64
                                                                        : 128;
     // (parts - 1) part_rounds < rounds_of(a): no part is empty

@@ -894,7 +894,7 @@ int spec_token_logprobs(const void* logits, int32_t logits_dtype, const int32_t*
     if (rc) return rc;
     a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws->base) + kTicketsOff);
     a.dev_err = static_cast<int*>(ws->base);
-    cudaError_t e = specv::launch_logprobs(a, static_cast<char*>(ws->base) + kHeader, st);
+    cudaError_t e = specv::launch_logprobs(a, ws->sms, static_cast<char*>(ws->base) + kHeader, st);
     if (e != cudaSuccess) return cuda_fail(e, "token_logprobs launch");
     return SPEC_OK;
 }

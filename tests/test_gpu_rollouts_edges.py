@@ -11,7 +11,7 @@ import paged8
 import rollouts
 from paged8 import E4M3
 from test_gpu_paged8 import cuda
-from test_gpu_rollouts import binding, check_logprobs, run_logprobs  # noqa: F401
+from test_gpu_rollouts import binding, check_logprobs, logits, run_logprobs  # noqa: F401
 from test_gpu_shared import call, case, check, reference
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +52,52 @@ def test_logprobs_list_across_looks(binding, dtype, per, B, V, K):
     for _ in range(3):  # the other rows too: a call repeats itself
         again = run_logprobs(binding, x, tokens, K, 1.0)
         assert all(torch.equal(again[n], g[n]) for n in g)
+
+
+def logprob_errors(x, T, threads, rounds):
+    """What fp32 sums allow a row x [rows, V] in the form that runs: CTAs of `threads` (a warp
+    where rounds is 0) in `rounds` rounds, each of 64 bytes a thread in two accumulators.
+
+    A weight carries 2^-22 (2^y by the unit) and the rounding of its exponent, three half
+    steps, 3 * 2^-24 d with d = m / T - z.  An accumulator takes rounds * 32 / size terms (16
+    in a warp's registers), each a rounding of 2^-24 of the sum; halves, lanes, warps and parts
+    are merged over 1 + 5 + 3 + 5 levels.  A sum is moved to a new maximum once a round at
+    most, and at two of the merges: each time a factor 2^d with 2^-22, its exponent's two half
+    steps (2^d |d| <= 0.54) and two roundings, 2^-21 together.  The logarithm, z's two
+    roundings and the last difference are within 2^-22 of ln V and of the result."""
+    x = x.double()
+    z = x / T
+    p = torch.softmax(z, -1)
+    d = z.amax(-1, keepdim=True) - z
+    d = torch.where(p > 0, d, torch.zeros((), dtype=torch.float64))
+    pd, pd2 = (p * d).sum(-1), (p * d * d).sum(-1)
+    terms = max(16, rounds * 16)
+    r = 2.0 ** -22 + (terms + 14) * 2.0 ** -24 + (rounds + 2) * 2.0 ** -21 + 3 * 2.0 ** -24 * pd
+    last = 2.0 ** -22 * math.log(x.shape[-1] + 1)
+    return (lambda v: r + last + 2.0 ** -22 * v.abs(),
+            lambda v: r + 2 * r * pd + 3 * 2.0 ** -24 * pd2 + last + 2.0 ** -22 * v.abs())
+
+
+@pytest.mark.parametrize("how", ["normal", "rising", "falling", "peaked", "far"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V,threads", [(70, 1013, 0), (1300, 4001, 64), (1300, 30001, 128),
+                                         (700, 33001, 256), (2, 152064, 256)])
+def test_logprobs_within_the_form_s_own_errors(binding, how, dtype, B, V, threads):
+    T, K = 0.9, 3
+    x = logits(V + B, B, 1, V, dtype, how)
+    tokens = torch.randint(0, V, (B, 1), generator=torch.Generator().manual_seed(K)).int().cuda()
+    g = run_logprobs(binding, x, tokens, K, T)
+    some = torch.arange(0, B, 70)
+    rows = x[some.cuda(), 0].cpu().float()
+    size = x.element_size()
+    rounds = -(-(V + 8) * size // (64 * threads)) if threads else 0
+    lp, ent, ids, top = rollouts.logprob64(rows, tokens[some.cuda(), 0].cpu(), K, T)[:4]
+    lt, et = logprob_errors(rows, T, threads, rounds)
+    got = {n: v[some.cuda(), 0].double().cpu() for n, v in g.items()}
+    assert torch.equal(got["ids"].long(), ids)
+    assert bool(((got["lp"] - lp).abs() <= lt(lp)).all())
+    assert bool(((got["ent"] - ent).abs() <= et(ent)).all())
+    assert bool(((got["top"] - top).abs().T <= torch.stack([lt(t) for t in top.T])).all())
 
 
 # ------------------------------------------------------------------ pages
