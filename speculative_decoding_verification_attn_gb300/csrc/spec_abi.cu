@@ -742,6 +742,9 @@ int spec_kv_gather(const void* k_cache, const void* v_cache, const void* k_scale
     return SPEC_OK;
 }
 
+// Entries of a table row that a block walks, a few thousand further at a time, in 32 bits.
+constexpr int32_t kMaxTableWidth = 1 << 30;
+
 // Sizes, types and pointers of a paged cache that a call writes.
 static int check_cache(const void* k_cache, const void* v_cache, const void* k_scale,
                        const void* v_scale, int32_t cache_dtype, int32_t num_kv_heads,
@@ -815,6 +818,8 @@ int spec_kv_fork(void* k_cache, void* v_cache, void* k_scale, void* v_scale, int
     if (!block_table || !ctx_lens || !page_refs || !parents || !children)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
     if (num_pairs >= 1 << 24) return fail(SPEC_ERR_UNSUPPORTED, "num_pairs must be < 2^24");
+    if (max_pages_per_seq > kMaxTableWidth)
+        return fail(SPEC_ERR_UNSUPPORTED, "max_pages_per_seq must be <= 2^30");
     Workspace* ws = nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = get_workspace(specv::fork_workspace_bytes(num_pages, num_pairs), st, &ws);
@@ -844,6 +849,8 @@ int spec_kv_release(int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs,
     if (num == 0) return SPEC_OK;
     if (!block_table || !ctx_lens || !page_refs || !rows)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    if (max_pages_per_seq > kMaxTableWidth)
+        return fail(SPEC_ERR_UNSUPPORTED, "max_pages_per_seq must be <= 2^30");
     Workspace* ws = nullptr;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int rc = get_workspace(0, st, &ws);

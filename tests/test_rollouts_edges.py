@@ -2,6 +2,7 @@
 compiled for the host, and their refusals.  Runs without a GPU."""
 from __future__ import annotations
 
+import ctypes
 import subprocess
 
 import pytest
@@ -63,3 +64,23 @@ def test_pieces_of_a_copied_page(places, rows, dim, elem):
     """Pages of up to 2^30 elements, 2^32 bytes."""
     assert rows * dim < 2 ** 30
     assert places("row_pieces", rows, dim, elem) == rows * dim * elem // 16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from speculative_decoding_verification_attn_gb300 import binding, build
+    build.build()
+    return binding.load()
+
+
+@pytest.mark.parametrize("call", ["fork", "release"])
+@pytest.mark.parametrize("n,width,needle", [(1, 2 ** 30 + 1, "max_pages"), (1, BIG, "max_pages")])
+def test_widest_tables(lib, call, n, width, needle):
+    """What a block's 32-bit walk over a row would not end for is refused."""
+    p = ctypes.c_void_p(16)
+    if call == "fork":
+        rc = lib.spec_kv_fork(p, p, None, None, 1, p, p, p, p, p, n, 4, 2, 2, 128, 16, 8, width, None)
+    else:
+        rc = lib.spec_kv_release(p, p, p, p, None, n, 2, 16, 8, width, None)
+    assert rc == -2
+    assert needle in lib.spec_last_error().decode()
