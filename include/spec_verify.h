@@ -665,7 +665,7 @@ SPEC_API int spec_kv_compact(void *k_cache, void *v_cache, void *k_scale, void *
  * SPEC_DEVERR_POOL; a page id >= num_pages SPEC_DEVERR_PAGE.
  *
  * Limits: num_pairs, num >= 0; room >= 0; num_rows >= 1; else as spec_kv_append,
- * caches 16-byte aligned; num_pairs < 2^24; max_pages_per_seq <= 2^30.
+ * caches 16-byte aligned; num_pairs, num < 2^24; max_pages_per_seq <= 2^30.
  */
 SPEC_API int spec_kv_fork(void *k_cache, void *v_cache, void *k_scale, void *v_scale,
                           int32_t cache_dtype, int32_t *block_table, int32_t *ctx_lens,

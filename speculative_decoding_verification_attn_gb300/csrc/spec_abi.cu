@@ -849,6 +849,8 @@ int spec_kv_release(int32_t* block_table, int32_t* ctx_lens, int32_t* page_refs,
     if (num == 0) return SPEC_OK;
     if (!block_table || !ctx_lens || !page_refs || !rows)
         return fail(SPEC_ERR_INVALID, "null tensor pointer");
+    // (each row looks for itself among the others)
+    if (num >= 1 << 24) return fail(SPEC_ERR_UNSUPPORTED, "num must be < 2^24");
     if (max_pages_per_seq > kMaxTableWidth)
         return fail(SPEC_ERR_UNSUPPORTED, "max_pages_per_seq must be <= 2^30");
     Workspace* ws = nullptr;

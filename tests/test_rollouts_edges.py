@@ -74,9 +74,11 @@ def lib():
 
 
 @pytest.mark.parametrize("call", ["fork", "release"])
-@pytest.mark.parametrize("n,width,needle", [(1, 2 ** 30 + 1, "max_pages"), (1, BIG, "max_pages")])
-def test_widest_tables(lib, call, n, width, needle):
-    """What a block's 32-bit walk over a row would not end for is refused."""
+@pytest.mark.parametrize("n,width,needle", [(1, 2 ** 30 + 1, "max_pages"), (1, BIG, "max_pages"),
+                                            (1 << 24, 4, "2^24"), (BIG, 4, "2^24")])
+def test_widest_tables_and_most_rows(lib, call, n, width, needle):
+    """What a block's 32-bit walk over a row, and every row's look at all others, would not end
+    for is refused; nothing was launched."""
     p = ctypes.c_void_p(16)
     if call == "fork":
         rc = lib.spec_kv_fork(p, p, None, None, 1, p, p, p, p, p, n, 4, 2, 2, 128, 16, 8, width, None)
