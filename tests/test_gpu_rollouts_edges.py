@@ -277,3 +277,33 @@ def test_shared_int8_weights_in_11_bits(grouped, sizes, k, Hq, Hkv, how):
         c["ks"] *= torch.where(torch.rand(c["ks"].shape, generator=gen) < 0.5, 1, -1).half()
         c["vs"] *= torch.where(torch.rand(c["vs"].shape, generator=gen) < 0.5, 1, -1).half()
     check_int8(c, *call(grouped, c))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
+@pytest.mark.parametrize("sizes,shared", [([40], [300]), ([30, 9], [1300, 150]), ([3], [260])])
+def test_shared_tables_wider_than_the_contexts(grouped, kind, sizes, shared):
+    """A captured step has one table width for all its lengths: the same bits behind a wide
+    table, and where it is too wide for prefixes to be widened ahead."""
+    c = case(46, kind, sizes, shared, [20, 150, 0], 8, 16, 1, 16, tail=1)
+    g = {n: cuda(v) if isinstance(v, torch.Tensor) else v for n, v in c.items()}
+    first = call(grouped, c, g)
+    check(c, *first)
+    width = c["table"].shape[1]
+    for wide in (width + 1, 4 * width, 40000, 140000):
+        g["table"] = torch.full((c["q"].shape[0], wide), -1, dtype=torch.int32, device="cuda")
+        g["table"][:, :width] = c["table"].cuda()
+        again = call(grouped, c, g)
+        assert all(torch.equal(a, b) for a, b in zip(again, first))
+    grouped.spec_set_option(grouped.SPEC_OPT_ATTN_PATH, 0)  # by the rule
+    check(c, *call(grouped, c, g))
+
+
+def test_calls_repeat_themselves(grouped):
+    """The same call over the same inputs, other calls between them: the same bits."""
+    cases = [case(s, kind, [20, 3], [700, 200], [90, 0, 31], 4, 8, 2, 16, tree=s == 51)
+             for s, kind in ((50, "bf16"), (51, "i8"), (52, "e4m3"))]
+    gs = [{n: cuda(v) if isinstance(v, torch.Tensor) else v for n, v in c.items()} for c in cases]
+    first = [call(grouped, c, g) for c, g in zip(cases, gs)]
+    for _ in range(20):
+        for c, g, f in zip(cases, gs, first):
+            assert all(torch.equal(a, b) for a, b in zip(call(grouped, c, g), f))
