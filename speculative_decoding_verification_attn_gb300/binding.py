@@ -687,7 +687,7 @@ def spec_kv_release(block_table, ctx_lens, page_refs, rows, page_size: int, keep
     dev = _device_of(block_table)
     tp, cp, rp, wp, lp = _ptrs(dev, block_table, ctx_lens, page_refs, rows, keep_lens)
     _check(load().spec_kv_release(tp, cp, rp, wp, lp, rows.shape[0], block_table.shape[0],
-                                  int(page_size), page_refs.shape[0], block_table.shape[1],
+                                  _span(page_size), page_refs.shape[0], block_table.shape[1],
                                   _stream_on(stream, dev)))
 
 

@@ -6,6 +6,7 @@ import ctypes
 import subprocess
 
 import pytest
+import torch
 
 PLACES = r"""
 #include <cstdio>
@@ -86,3 +87,22 @@ def test_widest_tables_and_most_rows(lib, call, n, width, needle):
         rc = lib.spec_kv_release(p, p, p, p, None, n, 2, 16, 8, width, None)
     assert rc == -2
     assert needle in lib.spec_last_error().decode()
+
+
+@pytest.mark.parametrize("page_size,seen", [(16, 16), (2 ** 32 + 16, BIG), (-(2 ** 32) + 16, -1), (2 ** 31, BIG)])
+def test_binding_release_page_size(monkeypatch, page_size, seen):
+    """A page size past 32 bits keeps its sign and its size: none of its bits are dropped."""
+    from speculative_decoding_verification_attn_gb300 import binding
+    got = []
+
+    class Library:
+        def spec_kv_release(self, *args):
+            got.append(args)
+            return 0
+
+    monkeypatch.setattr(binding, "load", lambda: Library())
+    monkeypatch.setattr(binding, "_device_of", lambda t: -1)
+    monkeypatch.setattr(binding, "_stream_on", lambda stream, dev: 0)
+    row = torch.zeros(2, dtype=torch.int32)
+    binding.spec_kv_release(torch.zeros(2, 3, dtype=torch.int32), row, row, row, page_size)
+    assert got[0][7] == seen
