@@ -561,7 +561,9 @@ __global__ void __launch_bounds__(kEThreads) compact_e4m3_kernel(const CompactAr
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float x = e4m3_value((w >> (8 * u)) & 0xff) * s;
-                o |= (uint32_t)e4m3_of(to_scale > 0.f ? __fdiv_rn(x, to_scale) : 0.f) << (8 * u);
+                // (a page of zeros has scale 0; a NaN stays one there too)
+                const float y = to_scale > 0.f || x != x ? __fdiv_rn(x, to_scale) : 0.f;
+                o |= (uint32_t)e4m3_of(y) << (8 * u);
             }
         }
         *reinterpret_cast<uint32_t*>(cache + mv.dst[i] * a.D + (e - i * words) * 4) = o;

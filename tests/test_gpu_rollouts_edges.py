@@ -134,6 +134,31 @@ def test_release_that_keeps_all(binding, P, keep):
         rollouts.same_state(g, s)
 
 
+def test_compact_e4m3_nan_row_into_a_page_of_zeros(binding):
+    """A NaN code stays one where the page that it comes into has scale 0."""
+    P, D = 8, 64
+    s = rollouts.pool_state(19, "e4m3", [13], 2, D, P, hold_more=8)
+    for t in (s["ks"], s["vs"]):
+        t.zero_()
+    for t in (s["kc"], s["vc"]):
+        rollouts.raw(t).zero_()
+    page, to = int(s["table"][0, 18 // P]), int(s["table"][0, 14 // P])
+    assert page != to
+    rollouts.raw(s["kc"])[page, 0, 18 % P, 3] = 0x7f  # node 5, which becomes node 1
+    rollouts.raw(s["vc"])[page, 1, 18 % P, 60] = 0xff
+    s["vs"][page] = 2.0
+    path, n = torch.tensor([[0, 5] + [-1] * 6], dtype=torch.int32), torch.tensor([2]).int()
+    g = rollouts.to_gpu(s)
+    binding.spec_kv_compact(g["kc"], g["vc"], g["table"], g["ctx"], path.cuda(), n.cuda(), g["ks"],
+                            g["vs"])
+    assert torch.equal(g["ks"].cpu(), s["ks"]) and torch.equal(g["vs"].cpu(), s["vs"])
+    for name, h, d in (("kc", 0, 3), ("vc", 1, 60)):
+        got, want = rollouts.raw(g[name]).cpu(), rollouts.raw(s[name]).clone()
+        assert int(got[to, h, 14 % P, d]) & 0x7f == 0x7f
+        want[to, h, 14 % P, d] = got[to, h, 14 % P, d]
+        assert torch.equal(got, want)
+
+
 def test_fork_copies_a_page_past_31_bits_of_bytes(binding):
     """The page in use of an fp32 cache holds more than 2^31 bytes a head."""
     P, D = 2 ** 22 + 64, 128
