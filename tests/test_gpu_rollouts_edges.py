@@ -100,6 +100,31 @@ def test_logprobs_within_the_form_s_own_errors(binding, how, dtype, B, V, thread
     assert bool(((got["top"] - top).abs().T <= torch.stack([lt(t) for t in top.T])).all())
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1.0, 2.0])
+@pytest.mark.parametrize("B,V,K", [(3, 900, 20), (3, 152064, 20), (1300, 4001, 5), (700, 20011, 32)])
+def test_logprobs_masked_with_the_lowest_value(binding, dtype, T, B, V, K):
+    """Masks of the type's lowest value, which is finite: such tokens have a probability of 0,
+    are alternatives where no others are left, and rows of them alone are uniform.  (The 64-bit
+    form takes rows less their maximum: a log-sum of -3e38 + ln V has no ln V left in 64 bits.)"""
+    x = logits(V, B, 1, V, dtype)
+    gen = torch.Generator().manual_seed(V)
+    x[(torch.rand(B, 1, V, generator=gen) < 0.999).cuda()] = torch.finfo(dtype).min
+    x[0] = torch.finfo(dtype).min
+    tokens = torch.randint(0, V, (B, 1), generator=gen).int().cuda()
+    g = run_logprobs(binding, x, tokens, K, T)
+    some = torch.arange(0, B, 70).cuda()
+    rows = x[some, 0].double().cpu()
+    rows -= rows.amax(-1, keepdim=True)
+    lp, ent, ids, top, lt, et, tt = rollouts.logprob64(rows, tokens[some, 0].cpu(), K, T)
+    got = {n: v[some, 0].cpu() for n, v in g.items()}
+    assert torch.equal(got["ids"].long(), ids)
+    for name, want, tol in (("lp", lp, lt), ("ent", ent, et), ("top", top, tt)):
+        far = want < -torch.finfo(torch.float32).max  # (past fp32: -inf)
+        assert bool((got[name][far] == -math.inf).all())
+        assert bool(((got[name].double() - want).abs() <= tol)[~far].all())
+
+
 # ------------------------------------------------------------------ pages
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
@@ -332,3 +357,20 @@ def test_calls_repeat_themselves(grouped):
     for _ in range(20):
         for c, g, f in zip(cases, gs, first):
             assert all(torch.equal(a, b) for a, b in zip(call(grouped, c, g), f))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "i8", "e4m3"])
+def test_shared_rows_that_see_nothing(grouped, kind):
+    """Rows whose mask is empty: behind a prefix they see it alone, without a context
+    nothing (0 and -inf)."""
+    c = case(47, kind, [4], [300], [0, 40, 0, 9], 5, 8, 2, 16, tree=True, lead=2, tail=1)
+    c["mask"][:, 1] = 0
+    c["mask"][0] = 0
+    out, lse = call(grouped, c)
+    o64, l64, mag, kn = ref = reference(c)
+    none = torch.isinf(l64)
+    assert bool(none[0].all()) and not bool(none[2:6].any())
+    assert not bool(out.cpu()[none].any()) and torch.equal(lse.cpu()[none].double(), l64[none])
+    ob, lb = paged8.attn_bounds(c["q"], *ref[:1], mag, kn, c["scale"])
+    assert bool(((out.double().cpu() - o64).abs() <= ob).all())
+    assert bool(((lse.double().cpu() - l64).abs() <= lb)[~none].all())
