@@ -687,7 +687,8 @@ SPEC_API int spec_kv_release(int32_t *block_table, int32_t *ctx_lens, int32_t *p
  *   top_ids / top_logprobs = the num_top tokens of largest logit, largest
  *   first, the lower id first among equals (values compare as stored, -0 == +0).
  *
- *   logits        [batch, num_rows, vocab]  logits_dtype (F32 | BF16), finite or
+ *   logits        [batch, num_rows, vocab]  logits_dtype (F32 | BF16), finite, with
+ *                 differences inside fp32's range (others count as infinite), or
  *                 -inf (a masked token: p = 0, never an alternative).  A row with a NaN
  *                 or +inf gives NaN and undefined alternatives; a row of -inf
  *                 alone gives logprob -inf and entropy 0

@@ -43,14 +43,19 @@
 //    its copies and tensor-core operations, and returns.
 //
 // What bounds it (cycles of an SM): a narrow bf16 tile ~2700, which is its share of HBM
-// (7.0 TB/s); a wide one ~4500 (1000 TFLOP/s), the chain S, softmax, P V of a stream with one
-// S buffer, of which the tensor core is busy 1024; e4m3 ~3550 and ~6000, INT8 ~4100 and ~7000,
-// the scales in the softmax and the widening of narrow tiles.  And ~17 us of a call: the
-// list ~4, first loads, the last pieces, the join ~4 and 2 KB of fp32 for every row.
-// Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 46 us
+// (7.0 TB/s); a wide one ~4500 (1000 TFLOP/s), of which the tensor core is busy 1024: with the
+// tensor pipe at 30 %, issue at 23 to 47 and the exponentials at 10 to 15, no unit but the latency
+// of the chain S, maximum, exponents, P V of a stream; which link of it has not been timed.
+// e4m3 ~3450 and ~6000, INT8 ~4000 and ~7000, with the scales in the softmax and the widening
+// of narrow tiles.  And ~17 us of a call: the list ~4, first loads, the last pieces, the join
+// ~4 and 2 KB of fp32 for every row.
+// Measured: 32 sequences, 6000 shared and 100-900 own keys, 32/8 heads, 4 drafts, bf16 47 us
 // (117 each by itself; the bytes' floor 13.7); 128 in four groups, 2-8K shared, 100-1500
-// own, 64/8 heads, e4m3 250 (264; the products' floor 50); 16 trees of 16, 32K shared, 28/4
-// heads, INT8 211 (485; 62).
+// own, 64/8 heads, e4m3 242 (264; the products' floor 50); 16 trees of 16, 32K shared, 28/4
+// heads, INT8 215 (485; 62).
+// INT8 weights of fp16 for bf16's 8 bits: those trees 215 us for 211, 128 sequences of 1000 to
+// 2500 own keys 266 for 272.  Of the references tried, the upper bound of a tile's maximum (the
+// slow way for bounds 8 apart) took 224 on the trees, this one 215.
 // Measured and not kept: S in two buffers of 64 keys a stream, Q K^T a buffer ahead of the
 // softmax: wide blocks 13 % faster (16 trees behind 8K, bf16, 61 -> 53 us), narrow tiles 8 %
 // (bf16) to 25 % (codes) slower, since a tile's softmax then takes twice the meetings and

@@ -19,7 +19,7 @@
 // All of it is launch latency, a few dependent round trips and the atomics on the counts:
 // a table row of 2048 entries is 8 KB, a copy at most a page.  240 rows of 1024 to 2048
 // pages released and forked again: 37 us with one entry of a thread at a time and an
-// exchange for each, 25 us so.  56 beams of 64 to 512 pages: 11 us.
+// exchange for each, 25 us so.  56 beams of 64 to 512 pages: 10 us.
 //
 // Compaction, one launch: a block per (sequence, kv-head, tensor).  Row path[i]
 // goes to place i <= path[i], so blocks of rows in ascending order may be read

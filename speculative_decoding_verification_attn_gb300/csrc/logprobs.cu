@@ -34,8 +34,8 @@
 // rows to CTAs of 128 or, of up to 8192 elements, 64 threads.
 //
 // Measured, bf16: 2048 rows of 152064 with 5 alternatives 121 us (5.1 TB/s; the bytes' floor
-// 92), without any 103; 32 sequences of up to 5 rows of 128256 with 20 alternatives 19.5,
-// without 11; 5 fp32 rows of 1000 4.0.  What is left of the alternatives is the appends (12
+// 92), without any 103; 32 sequences of up to 5 rows of 128256 with 20 alternatives 18.5,
+// without 9.7; 5 fp32 rows of 1000 3.5.  What is left of the alternatives is the appends (12
 // and 4 us of those), the meetings and, in parts, the merge.  Alternatives: meeting in
 // every round 1.5 times as long (rows of 152064), no cut before the end 22 us more, cuts at
 // 2 K + 16 entries 3, the round's maximum over widened values 2.
